@@ -23,6 +23,8 @@ EID_DEAD = ROW_DEAD = -1
 LOOKUP_AUTO, LOOKUP_GATHER, LOOKUP_BULK = 0, 1, 2
 PROJECTION_AUTO, PROJECTION_SINGLE, PROJECTION_PAIR = 0, 1, 2
 MAX_HEADS, MAX_D = 32, 4096
+DTYPE_BF16, DTYPE_F32 = 0, 1
+MAX_EMBED_D = 16384
 
 
 class EngramError(RuntimeError):
@@ -143,6 +145,14 @@ def _load():
     L.engram_gate_add.restype = i32
     L.engram_pack_e8m0_rows.argtypes = [vp, vp, i64, i32, vp, vp]
     L.engram_pack_e8m0_rows.restype = i32
+    L.engram_embed.argtypes = [vp, i64, i32, i64, vp, i32, i64, i32, i64, C.c_float, i32, vp, i32,
+                               i64, i64, vp, vp]
+    L.engram_embed.restype = i32
+    L.engram_gate_add_grad_workspace_bytes.argtypes = []
+    L.engram_gate_add_grad_workspace_bytes.restype = sz
+    L.engram_gate_add_grad.argtypes = [vp, vp, i64, i32, vp, vp, C.c_float, vp, vp, vp, i32, vp,
+                                       vp, sz, vp]
+    L.engram_gate_add_grad.restype = i32
     return L
 
 
@@ -612,3 +622,126 @@ def engram_forward_static(token_ids, tid2eid, n_eids: int, n_heads: int, tables:
                                      _ptr(status), _stream(stream)),
            "engram_forward_static")
     return streams_out
+
+
+def _dtype(t, name):
+    """The DTYPE_* of a bf16 (or bf16 bits) or fp32 CUDA tensor of any strides."""
+    import torch
+    _need(t, (torch.bfloat16, torch.int16, torch.float32), name, contiguous=False)
+    return DTYPE_F32 if t.dtype == torch.float32 else DTYPE_BF16
+
+
+def _unit(t, name):
+    """Refuses a tensor whose last dimension is not dense."""
+    if t.dim() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise EngramError(ERR_INVALID_ARG, f"the last dimension of {name} must be contiguous")
+
+
+def _ids_view(ids):
+    """ids [..., R] as (tokens, R, stride between tokens)."""
+    import torch
+    _need(ids, (torch.int32,), "ids", contiguous=False)
+    if ids.dim() == 0:
+        raise EngramError(ERR_INVALID_ARG, "ids must have a dimension")
+    _unit(ids, "ids")
+    if ids.dim() == 2:
+        return ids.shape[0], ids.shape[1], max(ids.stride(0), ids.shape[1])
+    if not ids.is_contiguous():
+        raise EngramError(ERR_INVALID_ARG, "ids must be contiguous (or [tokens, ids] rows)")
+    R = ids.shape[-1] if ids.dim() > 1 else 1
+    return (ids.numel() // R if R else 0), R, R
+
+
+def _rows_view(t, lead, D, name):
+    """t [*lead, D] as the strides (between tokens, between ids) of its rows; lead has
+    one or two dimensions once the leading ones are flattened."""
+    if tuple(t.shape) != (*lead, D):
+        raise EngramError(ERR_INVALID_ARG, f"{name} must be {[*lead, D]}")
+    _unit(t, name)
+    if len(lead) == 1:
+        return t.stride(0), 0
+    if len(lead) == 2:
+        return t.stride(0), t.stride(1)
+    if not t.is_contiguous():
+        raise EngramError(ERR_INVALID_ARG, f"{name} must be contiguous beyond three dimensions")
+    return lead[-1] * D, D
+
+
+def _embed_rows(ids, t, D, pooled, name):
+    """The row strides of an output or gradient tensor that goes with ids: [*ids.shape,
+    D], or [*ids.shape[:-1], D] when pooled."""
+    lead = tuple(ids.shape[:-1]) if pooled else tuple(ids.shape)
+    if pooled and len(lead) > 1:
+        if tuple(t.shape) != (*lead, D) or not t.is_contiguous():
+            raise EngramError(ERR_INVALID_ARG, f"{name} must be contiguous {[*lead, D]}")
+        return D, 0
+    tok, per = _rows_view(t, lead, D, name)
+    return (tok, 0) if pooled else (tok, per if ids.dim() > 1 else D)
+
+
+def engram_embed(ids, table, scale: float = 1.0, pooled: bool = False, out=None, out_dtype=None,
+                 status=None, stream=None):
+    """out[..., :] = scale * table[ids]: ids int32 [T] or [T, R] (any leading dimensions when
+    contiguous; rows of a wider id tensor when 2-D), table bf16 or fp32 [rows, D].  pooled
+    sums over the last dimension of ids: [*ids.shape[:-1], D].  -1 reads as zeros."""
+    import torch
+    td = _dtype(table, "table")
+    if table.dim() != 2:
+        raise EngramError(ERR_INVALID_ARG, "table must be [rows, D]")
+    _unit(table, "table")
+    if pooled and ids.dim() < 2:
+        raise EngramError(ERR_INVALID_ARG, "pooled ids must be [..., ids]")
+    T, R, ids_stride = _ids_view(ids)
+    rows, D = table.shape
+    if out is None:
+        out = torch.empty((*(ids.shape[:-1] if pooled else ids.shape), D),
+                          dtype=out_dtype or table.dtype, device=table.device)
+    od = _dtype(out, "out")
+    tok, per = _embed_rows(ids, out, D, pooled, "out")
+    _check(lib.engram_embed(_ptr(ids), T, R, ids_stride, _ptr(table), td, rows, D,
+                            max(table.stride(0), D), float(scale), int(pooled), _ptr(out), od, tok,
+                            per, _ptr(status), _stream(stream)), "engram_embed")
+    return out
+
+
+def engram_gate_add_grad_workspace_bytes() -> int:
+    return int(lib.engram_gate_add_grad_workspace_bytes())
+
+
+def engram_gate_add_grad(k, state, streams_in, alpha, dy, eps: float = 1e-6, dx=None, dk=None,
+                         dalpha=None, dk_dtype=None, workspace=None, stream=None):
+    """The backward pass of engram_gate_add: k fp32 [..., D], state uint8 [tokens] or None
+    (every token live), streams_in and dy bf16 [..., 4, D].  Returns (dx, dk, dalpha); dx may
+    be dy itself."""
+    import torch
+    bf = (torch.bfloat16, torch.int16)
+    _need(k, (torch.float32,), "k")
+    _need(state, (torch.uint8,), "state")
+    _need(streams_in, bf, "streams_in")
+    _need(dy, bf, "dy")
+    _need(alpha, (torch.float32,), "alpha")
+    D = streams_in.shape[-1]
+    if streams_in.dim() < 2 or streams_in.shape[-2] != 4 or dy.shape != streams_in.shape:
+        raise EngramError(ERR_INVALID_ARG, "streams_in and dy must be [..., 4, D]")
+    T = streams_in.numel() // (4 * D) if D else 0
+    if k.numel() != T * D or (state is not None and state.numel() != T) or alpha.numel() != 4:
+        raise EngramError(ERR_INVALID_ARG, "k / state / alpha sizes disagree with the streams")
+    if dx is None:
+        dx = torch.empty_like(dy)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=dk_dtype or torch.float32, device=k.device)
+    if dalpha is None:
+        dalpha = torch.empty(4, dtype=torch.float32, device=k.device)
+    _need(dx, bf, "dx")
+    _need(dk, (torch.float32, *bf), "dk")
+    _need(dalpha, (torch.float32,), "dalpha")
+    if dx.numel() != dy.numel() or dk.numel() != k.numel() or dalpha.numel() != 4:
+        raise EngramError(ERR_INVALID_ARG, "dx / dk / dalpha sizes")
+    if workspace is None:
+        workspace = torch.empty(engram_gate_add_grad_workspace_bytes(), dtype=torch.uint8,
+                                device=k.device)
+    _check(lib.engram_gate_add_grad(_ptr(k), _ptr(state), T, D, _ptr(streams_in), _ptr(alpha),
+                                    float(eps), _ptr(dy), _ptr(dx), _ptr(dk), _dtype(dk, "dk"),
+                                    _ptr(dalpha), _ptr(workspace), workspace.numel(),
+                                    _stream(stream)), "engram_gate_add_grad")
+    return dx, dk, dalpha

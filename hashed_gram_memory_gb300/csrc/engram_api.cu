@@ -83,6 +83,8 @@ engram_status engram::set_error(engram_status code, const char *fmt, ...) {
   return code;
 }
 
+engram_status engram::check_sm103() { return check_device(); }
+
 extern "C" {
 
 ENGRAM_API int32_t engram_abi_version(void) { return ENGRAM_ABI_VERSION; }

@@ -145,6 +145,9 @@ bool forward_is_decode_step(int32_t batch, int32_t seq, int32_t n_heads,
 // Records the message engram_last_error() returns on this thread; returns code.
 engram_status set_error(engram_status code, const char *fmt, ...);
 
+// ENGRAM_OK, or the error of a current device that is not sm_103.
+engram_status check_sm103();
+
 // splitmix64 first output for state x (S. Vigna, public domain), used for the
 // per-(order, head) hash seeds on the host.
 uint64_t splitmix64(uint64_t x);

@@ -1,0 +1,172 @@
+// train_api.cu -- the extern "C" entry points of the training calls: argument
+// validation on the host, the device check and the launches.
+#include <math.h>
+
+#include "train_internal.cuh"
+
+namespace {
+
+using engram::dtype_bytes;
+using engram::set_error;
+
+engram_status ok() { return set_error(ENGRAM_OK, "%s", ""); }
+
+engram_status launched(const char *what, cudaError_t e) {
+  if (e != cudaSuccess)
+    return set_error(ENGRAM_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
+  return ok();
+}
+
+bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && na && nb && x < y + nb && y < x + na;
+}
+
+bool dtype_ok(int32_t d) { return d == ENGRAM_DTYPE_BF16 || d == ENGRAM_DTYPE_F32; }
+
+// Elements from the first to one past the last of an [n, m, width] view.
+int64_t extent(int64_t n, int64_t stride_n, int64_t m, int64_t stride_m, int64_t width) {
+  return n > 0 && m > 0 ? (n - 1) * stride_n + (m - 1) * stride_m + width : 0;
+}
+
+// The checks of ids [n_tokens, n_ids] shared by the embedding calls.
+engram_status check_ids(const char *fn, const int32_t *ids, int64_t n_tokens, int32_t n_ids,
+                        int64_t ids_stride, int64_t rows, int32_t D, const int32_t *status) {
+  if (n_tokens < 0 || n_ids < 1 || n_tokens > INT32_MAX / n_ids)
+    return set_error(ENGRAM_ERR_INVALID_ARG,
+                     "%s: n_tokens >= 0, n_ids >= 1 and n_tokens * n_ids <= 2^31-1", fn);
+  if (rows < 1 || rows > INT32_MAX)
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: rows must be in [1, 2^31-1]", fn);
+  if (D < 1 || D > ENGRAM_MAX_EMBED_D)
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: D must be in [1, %d]", fn, ENGRAM_MAX_EMBED_D);
+  if (n_tokens > 0 && !ids) return set_error(ENGRAM_ERR_INVALID_ARG, "%s: ids is NULL", fn);
+  if (!aligned(ids, 4) || !aligned(status, 4))
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: int32 pointers must be 4-byte aligned", fn);
+  if (n_tokens > 1 && ids_stride < n_ids)
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: ids_stride is under n_ids", fn);
+  return ENGRAM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ENGRAM_API engram_status engram_embed(const int32_t *ids, int64_t n_tokens, int32_t n_ids,
+                                      int64_t ids_stride, const void *table, int32_t table_dtype,
+                                      int64_t rows, int32_t D, int64_t table_stride, float scale,
+                                      int32_t pooled, void *out, int32_t out_dtype,
+                                      int64_t out_token_stride, int64_t out_id_stride,
+                                      int32_t *status, void *stream) {
+  ENGRAM_NVTX_RANGE("engram_embed");
+  const char *fn = "engram_embed";
+  engram_status st = check_ids(fn, ids, n_tokens, n_ids, ids_stride, rows, D, status);
+  if (st != ENGRAM_OK) return st;
+  if (!dtype_ok(table_dtype) || !dtype_ok(out_dtype))
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: unknown dtype", fn);
+  if (!table || !aligned(table, dtype_bytes(table_dtype)) || (rows > 1 && table_stride < D))
+    return set_error(ENGRAM_ERR_INVALID_ARG,
+                     "%s: table NULL or misaligned, or its stride under D", fn);
+  const int64_t per = pooled ? 1 : n_ids;
+  // The output rows must not share elements: either ids inside tokens or the other way round.
+  const bool inner = out_id_stride >= D && out_token_stride >= (per - 1) * out_id_stride + D;
+  const bool outer = out_token_stride >= D && out_id_stride >= (n_tokens - 1) * out_token_stride + D;
+  if (per > 1 ? !(inner || (n_tokens <= 1 && out_id_stride >= D) || outer)
+              : (n_tokens > 1 && out_token_stride < D))
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: output rows overlap (strides)", fn);
+  if (n_tokens == 0) return ok();
+  if (!out || !aligned(out, dtype_bytes(out_dtype)))
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: out NULL or misaligned", fn);
+  const size_t ob = extent(n_tokens, out_token_stride, per, out_id_stride, D) * dtype_bytes(out_dtype);
+  if (overlap(out, ob, ids, extent(n_tokens, ids_stride, 1, 0, n_ids) * 4) ||
+      overlap(out, ob, table, extent(rows, table_stride, 1, 0, D) * dtype_bytes(table_dtype)) ||
+      overlap(out, ob, status, 4))
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: out overlaps an input", fn);
+  if ((st = engram::check_sm103()) != ENGRAM_OK) return st;
+  engram::EmbedParams p{};
+  p.ids = ids;
+  p.table = table;
+  p.out = out;
+  p.status = status;
+  p.n_tokens = n_tokens;
+  p.ids_stride = ids_stride;
+  p.rows = rows;
+  p.table_stride = table_stride;
+  p.out_token_stride = out_token_stride;
+  p.out_id_stride = out_id_stride;
+  p.n_ids = n_ids;
+  p.D = D;
+  p.scale = scale;
+  return launched("engram_embed launch", engram::launch_embed(p, table_dtype, out_dtype, pooled != 0,
+                                                              (cudaStream_t)stream));
+}
+
+ENGRAM_API size_t engram_gate_add_grad_workspace_bytes(void) {
+  return engram::kGateGradMaxBlocks * sizeof(float4);
+}
+
+ENGRAM_API engram_status engram_gate_add_grad(const float *k, const uint8_t *state,
+                                              int64_t n_tokens, int32_t D,
+                                              const uint16_t *streams_in, const float *alpha,
+                                              float eps, const uint16_t *dy, uint16_t *dx,
+                                              void *dk, int32_t dk_dtype, float *dalpha,
+                                              void *workspace, size_t workspace_bytes,
+                                              void *stream) {
+  ENGRAM_NVTX_RANGE("engram_gate_add_grad");
+  const char *fn = "engram_gate_add_grad";
+  if (n_tokens < 0 || n_tokens > INT32_MAX)
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: n_tokens out of range", fn);
+  if (D < 16 || D % 16 != 0 || D > 8192)
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: D must be a multiple of 16 in [16, 8192]", fn);
+  if (!dtype_ok(dk_dtype)) return set_error(ENGRAM_ERR_INVALID_ARG, "%s: unknown dk dtype", fn);
+  if (!alpha || !dalpha || !aligned(alpha, 4) || !aligned(dalpha, 4))
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: alpha or dalpha NULL or misaligned", fn);
+  if (!(eps >= 0.f) || !isfinite(eps))
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", fn);
+  const size_t need = engram_gate_add_grad_workspace_bytes();
+  if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
+    return set_error(ENGRAM_ERR_INVALID_ARG,
+                     "%s: workspace NULL, not 16-byte aligned or under %zu bytes", fn, need);
+  const size_t sb = (size_t)n_tokens * 4 * D * 2, kb = (size_t)n_tokens * D * 4;
+  const size_t db = (size_t)n_tokens * D * dtype_bytes(dk_dtype);
+  if (n_tokens > 0) {
+    if (!k || !streams_in || !dy || !dx || !dk)
+      return set_error(ENGRAM_ERR_INVALID_ARG, "%s: NULL buffer", fn);
+    if (!aligned(k, 16) || !aligned(streams_in, 16) || !aligned(dy, 16) || !aligned(dx, 16) ||
+        !aligned(dk, 16))
+      return set_error(ENGRAM_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned", fn);
+  }
+  const struct {
+    const void *p;
+    size_t n;
+  } outs[4] = {{dx, sb}, {dk, db}, {dalpha, 16}, {workspace, need}},
+    ins[5] = {{k, kb}, {state, state ? (size_t)n_tokens : 0}, {streams_in, sb}, {alpha, 16}, {dy, sb}};
+  for (int o = 0; o < 4; ++o) {
+    for (int i = 0; i < 5; ++i)
+      if (!(o == 0 && i == 4 && dx == dy) && overlap(outs[o].p, outs[o].n, ins[i].p, ins[i].n))
+        return set_error(ENGRAM_ERR_INVALID_ARG, "%s: an output overlaps an input", fn);
+    for (int i = 0; i < o; ++i)
+      if (overlap(outs[o].p, outs[o].n, outs[i].p, outs[i].n))
+        return set_error(ENGRAM_ERR_INVALID_ARG, "%s: output buffers overlap", fn);
+  }
+  engram_status st = engram::check_sm103();
+  if (st != ENGRAM_OK) return st;
+  engram::GateGradParams p{};
+  p.k = k;
+  p.state = state;
+  p.x = streams_in;
+  p.dy = dy;
+  p.dx = dx;
+  p.dk = dk;
+  p.alpha = alpha;
+  p.partial = static_cast<float4 *>(workspace);
+  p.dalpha = dalpha;
+  p.T = n_tokens;
+  p.D = D;
+  p.eps = eps;
+  return launched("engram_gate_add_grad launch",
+                  engram::launch_gate_grad(p, dk_dtype, (cudaStream_t)stream));
+}
+
+}  // extern "C"

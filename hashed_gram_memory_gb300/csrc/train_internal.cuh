@@ -1,0 +1,40 @@
+// train_internal.cuh -- launch parameters and launchers of the training kernels
+// (embedding lookup and gradient, FP8 quantisation and product, the gate's
+// backward pass), shared with their C ABI layer (train_api.cu).
+#pragma once
+
+#include "engram_internal.cuh"
+
+namespace engram {
+
+inline size_t dtype_bytes(int dtype) { return dtype == ENGRAM_DTYPE_F32 ? 4 : 2; }
+
+struct EmbedParams {
+  const int32_t *ids;
+  const void *table;
+  void *out;
+  int32_t *status;
+  int64_t n_tokens, ids_stride, rows, table_stride, out_token_stride, out_id_stride;
+  int32_t n_ids, D;
+  float scale;
+};
+cudaError_t launch_embed(const EmbedParams &p, int table_dtype, int out_dtype, bool pooled,
+                         cudaStream_t stream);
+
+struct GateGradParams {
+  const float *k;
+  const uint8_t *state;  // NULL: every token live
+  const uint16_t *x, *dy;
+  uint16_t *dx;
+  void *dk;
+  const float *alpha;
+  float4 *partial;  // [kGateGradMaxBlocks]: each block's sums of g <dy_s, k>
+  float *dalpha;
+  int64_t T;
+  int32_t D, group;  // group: lanes per token of the warp kernel (a power of two)
+  float eps;
+};
+constexpr int kGateGradMaxBlocks = 4096;
+cudaError_t launch_gate_grad(const GateGradParams &p, int dk_dtype, cudaStream_t stream);
+
+}  // namespace engram

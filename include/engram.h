@@ -523,6 +523,75 @@ ENGRAM_API engram_status engram_pack_e8m0_rows(const uint8_t *table, const uint8
                                                void *stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Training the memory and its connection.  The pages describe no training
+ * kernels; these calls are this library's own: the lookup of scaled rows and its
+ * gradient, the 8-bit product with a scale for each block of 128 that the
+ * projection's weights and gradients run on, and the gate's backward pass.  The
+ * conventions above hold: device pointers, caller-owned memory and workspaces,
+ * asynchronous on `stream`, argument errors before any launch, data errors as
+ * bits of *status.  Results do not depend on timing: the same call on the same
+ * inputs gives the same bits.
+ */
+#define ENGRAM_DTYPE_BF16 0
+#define ENGRAM_DTYPE_F32 1
+#define ENGRAM_MAX_EMBED_D 16384  /* row width of the embedding calls, any value from 1 */
+#define ENGRAM_FP8_BLOCK 128      /* values along K (and rows, where asked) sharing a scale */
+
+/*
+ * engram_embed -- rows of one table looked up by id and scaled:
+ *   pooled == 0:  out[t, j] = scale * table[ids[t, j]]
+ *   pooled != 0:  out[t]    = scale * sum_j table[ids[t, j]]   (fp32, j ascending)
+ *   ids         int32 [n_tokens, n_ids], ids_stride elements between tokens (a
+ *               slice of the hash's [tokens, 3*n_heads] ids is such a view)
+ *   table       ENGRAM_DTYPE_* [rows, D], table_stride elements between rows
+ *   out         ENGRAM_DTYPE_*; row (t, j) starts at t*out_token_stride +
+ *               j*out_id_stride elements (out_id_stride unused when pooled);
+ *               rounded once
+ * An id ENGRAM_ROW_DEAD reads as a row of zeros.  Any other id outside [0, rows)
+ * sets ENGRAM_FLAG_BAD_ROW and leaves that output row (the token, when pooled)
+ * unwritten.  1 <= D <= ENGRAM_MAX_EMBED_D, n_tokens * n_ids <= 2^31 - 1.  Any
+ * strides and element alignment; rows of 8 values on 16-byte boundaries take the
+ * vector path.  out must not overlap ids or the table.
+ */
+ENGRAM_API engram_status engram_embed(const int32_t *ids, int64_t n_tokens, int32_t n_ids,
+                                      int64_t ids_stride, const void *table, int32_t table_dtype,
+                                      int64_t rows, int32_t D, int64_t table_stride, float scale,
+                                      int32_t pooled, void *out, int32_t out_dtype,
+                                      int64_t out_token_stride, int64_t out_id_stride,
+                                      int32_t *status, void *stream);
+
+/*
+ * engram_gate_add_grad -- the backward pass of engram_gate_add (and, with k the
+ * memory of mem_out, of engram_lookup_fused's gate and add).  Per token, with
+ * a = stream 0, ra = (|a|^2/D + eps)^-1/2, rk likewise for k, z = ra rk <a, k> /
+ * sqrt(D), g = sigmoid(z), c = sum_s alpha_s dy_s and dz = <c, k> g (1 - g):
+ *   dk       = g c + dz (ra rk / sqrt(D) a - z rk^2 / D k)
+ *   dx_0     = dy_0 + dz (ra rk / sqrt(D) k - z ra^2 / D a);  dx_s = dy_s, s > 0
+ *   dalpha_s = sum over live tokens of g <dy_s, k>
+ *   k           fp32 [n_tokens, D];  state uint8 [n_tokens] as engram_gate_add,
+ *               or NULL when every token is live
+ *   streams_in  bf16 bits [n_tokens, 4, D], the forward call's input (stream 0
+ *               of each token is read)
+ *   dy, dx      bf16 bits [n_tokens, 4, D]; dx may be dy (in place: then only
+ *               stream 0 is written) or must not overlap any input
+ *   dk          ENGRAM_DTYPE_* [n_tokens, D];  dalpha fp32 [4], overwritten
+ *   workspace   device, 16-byte aligned, engram_gate_add_grad_workspace_bytes()
+ * A dead token (state 1) passes dy through (dk = 0); a bad one (state 2) has dk = 0
+ * and its dx left unwritten; neither adds to dalpha.  D a multiple of 16 in [16,
+ * 8192]; all but state, alpha and dalpha 16-byte aligned.  n_tokens == 0 zeroes
+ * dalpha.
+ */
+ENGRAM_API size_t engram_gate_add_grad_workspace_bytes(void);
+ENGRAM_API engram_status engram_gate_add_grad(const float *k, const uint8_t *state,
+                                              int64_t n_tokens, int32_t D,
+                                              const uint16_t *streams_in, const float *alpha,
+                                              float eps, const uint16_t *dy, uint16_t *dx,
+                                              void *dk, int32_t dk_dtype, float *dalpha,
+                                              void *workspace, size_t workspace_bytes,
+                                              void *stream);
+
+/*
  * engram_read_status -- waits for `stream`, copies the device status word into
  * *flags_host and returns ENGRAM_OK (no flag), ENGRAM_ERR_TIMEOUT
  * (ENGRAM_FLAG_TIMEOUT set) or ENGRAM_ERR_OUT_OF_RANGE (a range flag set).  The
