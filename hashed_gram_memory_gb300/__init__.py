@@ -25,6 +25,7 @@ PROJECTION_AUTO, PROJECTION_SINGLE, PROJECTION_PAIR = 0, 1, 2
 MAX_HEADS, MAX_D = 32, 4096
 DTYPE_BF16, DTYPE_F32 = 0, 1
 MAX_EMBED_D = 16384
+FP8_BLOCK = 128
 
 
 class EngramError(RuntimeError):
@@ -148,6 +149,11 @@ def _load():
     L.engram_embed.argtypes = [vp, i64, i32, i64, vp, i32, i64, i32, i64, C.c_float, i32, vp, i32,
                                i64, i64, vp, vp]
     L.engram_embed.restype = i32
+    L.engram_fp8_quantise.argtypes = [vp, i32, i64, i64, i64, i32, vp, i64, vp, vp, i64, vp, vp]
+    L.engram_fp8_quantise.restype = i32
+    L.engram_fp8_matmul.argtypes = [vp, i64, vp, i32, vp, i64, vp, i32, i64, i64, i64, vp, i32,
+                                    i64, vp, vp]
+    L.engram_fp8_matmul.restype = i32
     L.engram_gate_add_grad_workspace_bytes.argtypes = []
     L.engram_gate_add_grad_workspace_bytes.restype = sz
     L.engram_gate_add_grad.argtypes = [vp, vp, i64, i32, vp, vp, C.c_float, vp, vp, vp, i32, vp,
@@ -701,6 +707,94 @@ def engram_embed(ids, table, scale: float = 1.0, pooled: bool = False, out=None,
     _check(lib.engram_embed(_ptr(ids), T, R, ids_stride, _ptr(table), td, rows, D,
                             max(table.stride(0), D), float(scale), int(pooled), _ptr(out), od, tok,
                             per, _ptr(status), _stream(stream)), "engram_embed")
+    return out
+
+
+def fp8_empty(rows: int, cols: int, device):
+    """An uninitialised uint8 [rows, cols] operand: rows a multiple of 16 bytes apart."""
+    import torch
+    return torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.uint8, device=device)[:, :cols]
+
+
+def _fp8_operand(t, name):
+    import torch
+    _need(t, (torch.uint8,), name, contiguous=False)
+    if t.dim() != 2:
+        raise EngramError(ERR_INVALID_ARG, f"{name} must be two-dimensional")
+    _unit(t, name)
+    return t.stride(0)
+
+
+def _fp8_scales(t, rows, cols, block, name):
+    import torch
+    _need(t, (torch.uint8,), name)
+    want = (-(-rows // block), -(-cols // FP8_BLOCK))
+    if tuple(t.shape) != want:
+        raise EngramError(ERR_INVALID_ARG, f"{name} must be {list(want)}")
+
+
+def engram_fp8_quantise(x, block_rows: int = 1, rows: bool = True, cols: bool = False, out=None,
+                        stream=None):
+    """x bf16 or fp32 [M, K] as e4m3fn bytes with a power-of-two scale byte per block of 128.
+    rows: (q [M, K], s [M, ceil(K/128)]), blocks along K.  cols: (qt [K, M], st [K,
+    ceil(M/128)]), the transposed copy with blocks along M.  block_rows FP8_BLOCK: 128 x 128
+    tiles share a scale.  Returns the copies asked for, in that order; out gives their
+    buffers (rows a multiple of 16 bytes apart: fp8_empty)."""
+    import torch
+    xd = _dtype(x, "x")
+    if x.dim() != 2:
+        raise EngramError(ERR_INVALID_ARG, "x must be [M, K]")
+    _unit(x, "x")
+    if block_rows not in (1, FP8_BLOCK):
+        raise EngramError(ERR_INVALID_ARG, f"block_rows must be 1 or {FP8_BLOCK}")
+    M, K = x.shape
+    dims = ([(M, K)] if rows else []) + ([(K, M)] if cols else [])
+    if out is None:
+        out = []
+        for r, c in dims:
+            out += [fp8_empty(r, c, x.device),
+                    torch.empty((-(-r // block_rows), -(-c // FP8_BLOCK)), dtype=torch.uint8,
+                                device=x.device)]
+    if len(out) != 2 * len(dims):
+        raise EngramError(ERR_INVALID_ARG, "out must hold a value and a scale buffer per copy")
+    args = []
+    for i, (r, c) in enumerate(dims):
+        stride = _fp8_operand(out[2 * i], "q")
+        if tuple(out[2 * i].shape) != (r, c):
+            raise EngramError(ERR_INVALID_ARG, f"q must be {[r, c]}")
+        _fp8_scales(out[2 * i + 1], r, c, block_rows, "scales")
+        args.append((_ptr(out[2 * i]), stride, _ptr(out[2 * i + 1])))
+    none = (None, 0, None)
+    q = args[0] if rows else none
+    qt = args[-1] if cols else none
+    _check(lib.engram_fp8_quantise(_ptr(x), xd, M, K, max(x.stride(0), K), block_rows, *q, *qt,
+                                   _stream(stream)), "engram_fp8_quantise")
+    return tuple(out)
+
+
+def engram_fp8_matmul(a, a_scale, b, b_scale, a_block: int = 1, b_block: int = 1, out=None,
+                      out_dtype=None, status=None, stream=None):
+    """out[m, n] = sum_k a[m, k] b[n, k]: a uint8 [M, K] and b uint8 [N, K] with their scale
+    bytes, as engram_fp8_quantise returns them (a_block / b_block: FP8_BLOCK where 128 x 128
+    tiles share a scale).  out: fp32 (default) or bf16 [M, N]."""
+    import torch
+    sa, sb = _fp8_operand(a, "a"), _fp8_operand(b, "b")
+    (M, K), N = a.shape, b.shape[0]
+    if b.shape[1] != K:
+        raise EngramError(ERR_INVALID_ARG, "a and b disagree on K")
+    if a_block not in (1, FP8_BLOCK) or b_block not in (1, FP8_BLOCK):
+        raise EngramError(ERR_INVALID_ARG, f"a_block and b_block must be 1 or {FP8_BLOCK}")
+    _fp8_scales(a_scale, M, K, a_block, "a_scale")
+    _fp8_scales(b_scale, N, K, b_block, "b_scale")
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or torch.float32, device=a.device)
+    od = _dtype(out, "out")
+    if tuple(out.shape) != (M, N):
+        raise EngramError(ERR_INVALID_ARG, f"out must be {[M, N]}")
+    _unit(out, "out")
+    _check(lib.engram_fp8_matmul(_ptr(a), sa, _ptr(a_scale), a_block, _ptr(b), sb, _ptr(b_scale),
+                                 b_block, M, N, K, _ptr(out), od, max(out.stride(0), N),
+                                 _ptr(status), _stream(stream)), "engram_fp8_matmul")
     return out
 
 

@@ -85,6 +85,8 @@ engram_status engram::set_error(engram_status code, const char *fmt, ...) {
 
 engram_status engram::check_sm103() { return check_device(); }
 
+int64_t engram::wait_limit_ns() { return g_wait_limit_ns.load(std::memory_order_relaxed); }
+
 extern "C" {
 
 ENGRAM_API int32_t engram_abi_version(void) { return ENGRAM_ABI_VERSION; }

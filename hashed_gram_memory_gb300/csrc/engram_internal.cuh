@@ -148,6 +148,9 @@ engram_status set_error(engram_status code, const char *fmt, ...);
 // ENGRAM_OK, or the error of a current device that is not sm_103.
 engram_status check_sm103();
 
+// The limit of every bounded wait inside a kernel (engram_set_wait_limit_ns).
+int64_t wait_limit_ns();
+
 // splitmix64 first output for state x (S. Vigna, public domain), used for the
 // per-(order, head) hash seeds on the host.
 uint64_t splitmix64(uint64_t x);

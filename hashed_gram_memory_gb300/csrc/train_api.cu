@@ -102,6 +102,117 @@ ENGRAM_API engram_status engram_embed(const int32_t *ids, int64_t n_tokens, int3
                                                               (cudaStream_t)stream));
 }
 
+ENGRAM_API engram_status engram_fp8_quantise(const void *x, int32_t x_dtype, int64_t M, int64_t K,
+                                             int64_t x_stride, int32_t block_rows, uint8_t *q,
+                                             int64_t q_stride, uint8_t *s, uint8_t *qt,
+                                             int64_t qt_stride, uint8_t *st, void *stream) {
+  ENGRAM_NVTX_RANGE("engram_fp8_quantise");
+  const char *fn = "engram_fp8_quantise";
+  if (M < 0 || K < 1 || M > INT32_MAX || K > INT32_MAX)
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: M in [0, 2^31-1] and K in [1, 2^31-1]", fn);
+  const int64_t kb = (K + 127) / 128, mb = (M + 127) / 128;
+  if (mb * kb > INT32_MAX || M * kb / 16 > INT32_MAX)
+    return set_error(ENGRAM_ERR_UNSUPPORTED, "%s: over 2^31-1 tiles", fn);
+  if (!dtype_ok(x_dtype)) return set_error(ENGRAM_ERR_INVALID_ARG, "%s: unknown x dtype", fn);
+  if (block_rows != 1 && block_rows != ENGRAM_FP8_BLOCK)
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: block_rows must be 1 or %d", fn, ENGRAM_FP8_BLOCK);
+  if (M == 0) return ok();  // empty buffers have no address
+  if ((!q && !qt) || (q && !s) || (qt && !st))
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: q or qt must be given, each with its scales", fn);
+  if (!x || !aligned(x, dtype_bytes(x_dtype)) || (M > 1 && x_stride < K))
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: x NULL or misaligned, or its stride under K", fn);
+  if (!aligned(q, 16) || !aligned(qt, 16) || (q && M > 1 && (q_stride < K || q_stride % 16 != 0)) ||
+      (qt && K > 1 && (qt_stride < M || qt_stride % 16 != 0)))
+    return set_error(ENGRAM_ERR_INVALID_ARG,
+                     "%s: q and qt must be 16-byte aligned, their strides multiples of 16 that hold a row",
+                     fn);
+  const size_t xb = extent(M, x_stride, 1, 0, K) * dtype_bytes(x_dtype);
+  const size_t sn = (block_rows == 1 ? M : mb) * kb, tn = (block_rows == 1 ? K : kb) * mb;
+  const struct {
+    const void *p;
+    size_t n;
+  } outs[4] = {{q, q ? (size_t)extent(M, q_stride, 1, 0, K) : 0}, {q ? s : nullptr, sn},
+               {qt, qt ? (size_t)extent(K, qt_stride, 1, 0, M) : 0}, {qt ? st : nullptr, tn}};
+  for (int o = 0; o < 4; ++o) {
+    if (overlap(outs[o].p, outs[o].n, x, xb))
+      return set_error(ENGRAM_ERR_INVALID_ARG, "%s: an output overlaps x", fn);
+    for (int i = 0; i < o; ++i)
+      if (overlap(outs[o].p, outs[o].n, outs[i].p, outs[i].n))
+        return set_error(ENGRAM_ERR_INVALID_ARG, "%s: output buffers overlap", fn);
+  }
+  engram_status code = engram::check_sm103();
+  if (code != ENGRAM_OK) return code;
+  engram::QuantiseParams p{};
+  p.x = x;
+  p.q = q;
+  p.s = s;
+  p.qt = qt;
+  p.st = st;
+  p.M = M;
+  p.K = K;
+  p.x_stride = x_stride;
+  p.q_stride = q_stride;
+  p.qt_stride = qt_stride;
+  p.block_rows = block_rows;
+  return launched("engram_fp8_quantise launch",
+                  engram::launch_quantise(p, x_dtype, (cudaStream_t)stream));
+}
+
+ENGRAM_API engram_status engram_fp8_matmul(const uint8_t *a, int64_t a_stride, const uint8_t *a_scale,
+                                           int32_t a_block, const uint8_t *b, int64_t b_stride,
+                                           const uint8_t *b_scale, int32_t b_block, int64_t M,
+                                           int64_t N, int64_t K, void *out, int32_t out_dtype,
+                                           int64_t out_stride, int32_t *status, void *stream) {
+  ENGRAM_NVTX_RANGE("engram_fp8_matmul");
+  const char *fn = "engram_fp8_matmul";
+  const int64_t most = INT32_MAX - 256;  // tile origins stay in 32 bits
+  if (M < 0 || N < 0 || K < 1 || M > most || N > most || K > most)
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: M, N >= 0 and K >= 1, all under 2^31 - 256", fn);
+  if ((a_block != 1 && a_block != ENGRAM_FP8_BLOCK) || (b_block != 1 && b_block != ENGRAM_FP8_BLOCK))
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: a_block and b_block must be 1 or %d", fn,
+                     ENGRAM_FP8_BLOCK);
+  if (!dtype_ok(out_dtype)) return set_error(ENGRAM_ERR_INVALID_ARG, "%s: unknown out dtype", fn);
+  if (M == 0 || N == 0) return ok();
+  if (!a || !a_scale || !b || !b_scale || !out)
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: NULL buffer", fn);
+  // One row needs no stride, but the copies' descriptors take one all the same.
+  const int64_t one = (K + 15) / 16 * 16;
+  if (M == 1) a_stride = one;
+  if (N == 1) b_stride = one;
+  if (!aligned(a, 16) || !aligned(b, 16) || a_stride < K || b_stride < K || a_stride % 16 != 0 ||
+      b_stride % 16 != 0)
+    return set_error(ENGRAM_ERR_INVALID_ARG,
+                     "%s: a and b must be 16-byte aligned, their strides multiples of 16 from K on", fn);
+  if (!aligned(out, dtype_bytes(out_dtype)) || (M > 1 && out_stride < N) || !aligned(status, 4))
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: out misaligned or its stride under N", fn);
+  const int64_t kb = (K + 127) / 128;
+  const size_t ob = extent(M, out_stride, 1, 0, N) * dtype_bytes(out_dtype);
+  if (overlap(out, ob, a, extent(M, a_stride, 1, 0, K)) ||
+      overlap(out, ob, b, extent(N, b_stride, 1, 0, K)) ||
+      overlap(out, ob, a_scale, ((M - 1) / a_block + 1) * kb) ||
+      overlap(out, ob, b_scale, ((N - 1) / b_block + 1) * kb) || overlap(out, ob, status, 4))
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: out overlaps an input", fn);
+  engram_status st = engram::check_sm103();
+  if (st != ENGRAM_OK) return st;
+  engram::MatmulParams p{};
+  p.a = a;
+  p.a_scale = a_scale;
+  p.b = b;
+  p.b_scale = b_scale;
+  p.out = out;
+  p.status = status;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.a_stride = a_stride;
+  p.b_stride = b_stride;
+  p.out_stride = out_stride;
+  p.a_block = a_block;
+  p.b_block = b_block;
+  return launched("engram_fp8_matmul launch",
+                  engram::launch_fp8_matmul(p, out_dtype, (cudaStream_t)stream));
+}
+
 ENGRAM_API size_t engram_gate_add_grad_workspace_bytes(void) {
   return engram::kGateGradMaxBlocks * sizeof(float4);
 }

@@ -37,4 +37,22 @@ struct GateGradParams {
 constexpr int kGateGradMaxBlocks = 4096;
 cudaError_t launch_gate_grad(const GateGradParams &p, int dk_dtype, cudaStream_t stream);
 
+struct QuantiseParams {
+  const void *x;
+  uint8_t *q, *s;    // NULL q: no row copy
+  uint8_t *qt, *st;  // NULL qt: no transposed copy
+  int64_t M, K, x_stride, q_stride, qt_stride;
+  int32_t block_rows;  // 1 or ENGRAM_FP8_BLOCK
+};
+cudaError_t launch_quantise(const QuantiseParams &p, int dtype, cudaStream_t stream);
+
+struct MatmulParams {
+  const uint8_t *a, *a_scale, *b, *b_scale;
+  void *out;
+  int32_t *status;
+  int64_t M, N, K, a_stride, b_stride, out_stride;
+  int32_t a_block, b_block;  // rows sharing a scale: 1 or ENGRAM_FP8_BLOCK
+};
+cudaError_t launch_fp8_matmul(const MatmulParams &p, int out_dtype, cudaStream_t stream);
+
 }  // namespace engram

@@ -562,6 +562,49 @@ ENGRAM_API engram_status engram_embed(const int32_t *ids, int64_t n_tokens, int3
                                       int32_t *status, void *stream);
 
 /*
+ * engram_fp8_quantise -- x as e4m3fn bytes with one power-of-two scale per block of 128:
+ * for each block, the smallest exponent e >= -127 with max|x| <= 448 * 2^e is stored as
+ * the byte e + 127 (OCP E8M0, as the tables' exponents), and x becomes e4m3(x * 2^-e),
+ * rounded to nearest even; the only rounding.
+ *   x      ENGRAM_DTYPE_* [M, K], x_stride elements between rows (any)
+ *   q, s   uint8 [M, K], q_stride bytes between rows (a multiple of 16), and
+ *          [M, ceil(K/128)]: blocks of 128 along K (the last one may be short); NULL q:
+ *          not made
+ *   qt, st the transposed copy for products that sum over the rows of x: uint8 [K, M],
+ *          qt_stride bytes between rows (a multiple of 16), and [K, ceil(M/128)], blocks
+ *          of 128 along M; NULL qt: not made
+ *   block_rows  1, or ENGRAM_FP8_BLOCK: 128 x 128 tiles share a scale, s is
+ *          [ceil(M/128), ceil(K/128)] and st its transpose (weights)
+ * A block that holds a NaN or an infinity gets the scale 0xFF and the bytes 0x7F (both
+ * NaN).  q and qt are 16-byte aligned; bytes between rows are not written.  M == 0
+ * launches nothing.
+ */
+ENGRAM_API engram_status engram_fp8_quantise(const void *x, int32_t x_dtype, int64_t M, int64_t K,
+                                             int64_t x_stride, int32_t block_rows, uint8_t *q,
+                                             int64_t q_stride, uint8_t *s, uint8_t *qt,
+                                             int64_t qt_stride, uint8_t *st, void *stream);
+
+/*
+ * engram_fp8_matmul -- out[m, n] = sum_k a[m, k] b[n, k] of operands as
+ * engram_fp8_quantise writes them: tcgen05 tensor cores applying the scales, fp32
+ * accumulation, rounded once to the output's type.
+ *   a, a_scale  e4m3fn bytes [M, K], a_stride bytes between rows, and their scale bytes:
+ *               [M, ceil(K/128)] (a_block 1) or [ceil(M/128), ceil(K/128)] (a_block
+ *               ENGRAM_FP8_BLOCK), rows contiguous
+ *   b, b_scale  e4m3fn bytes [N, K], likewise
+ *   out         ENGRAM_DTYPE_* [M, N], out_stride elements between rows (any)
+ * a and b are 16-byte aligned with strides that are multiples of 16; M, N and K are any
+ * (values past K in a row are not read as part of it).  A NaN (byte 0x7F or 0xFF, or scale
+ * 0xFF) makes the outputs that it is summed into NaN.  A wait that runs out sets
+ * ENGRAM_FLAG_TIMEOUT and leaves outputs unwritten.  M == 0 or N == 0 launches nothing.
+ */
+ENGRAM_API engram_status engram_fp8_matmul(const uint8_t *a, int64_t a_stride, const uint8_t *a_scale,
+                                           int32_t a_block, const uint8_t *b, int64_t b_stride,
+                                           const uint8_t *b_scale, int32_t b_block, int64_t M,
+                                           int64_t N, int64_t K, void *out, int32_t out_dtype,
+                                           int64_t out_stride, int32_t *status, void *stream);
+
+/*
  * engram_gate_add_grad -- the backward pass of engram_gate_add (and, with k the
  * memory of mem_out, of engram_lookup_fused's gate and add).  Per token, with
  * a = stream 0, ra = (|a|^2/D + eps)^-1/2, rk likewise for k, z = ra rk <a, k> /
