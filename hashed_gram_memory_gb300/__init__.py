@@ -149,6 +149,14 @@ def _load():
     L.engram_embed.argtypes = [vp, i64, i32, i64, vp, i32, i64, i32, i64, C.c_float, i32, vp, i32,
                                i64, i64, vp, vp]
     L.engram_embed.restype = i32
+    L.engram_embed_grad_workspace_bytes.argtypes = [i64, i32, i32]
+    L.engram_embed_grad_workspace_bytes.restype = sz
+    L.engram_embed_grad.argtypes = [vp, i64, i32, i64, vp, i32, i64, i64, i64, i32, C.c_float, i32,
+                                    vp, i32, i64, vp, sz, vp, vp]
+    L.engram_embed_grad.restype = i32
+    L.engram_embed_grad_rows.argtypes = [vp, i64, i32, i64, vp, i32, i64, i64, i64, i32, C.c_float,
+                                         vp, vp, i32, i64, vp, vp, sz, vp, vp]
+    L.engram_embed_grad_rows.restype = i32
     L.engram_fp8_quantise.argtypes = [vp, i32, i64, i64, i64, i32, vp, i64, vp, vp, i64, vp, vp]
     L.engram_fp8_quantise.restype = i32
     L.engram_fp8_matmul.argtypes = [vp, i64, vp, i32, vp, i64, vp, i32, i64, i64, i64, vp, i32,
@@ -708,6 +716,74 @@ def engram_embed(ids, table, scale: float = 1.0, pooled: bool = False, out=None,
                             max(table.stride(0), D), float(scale), int(pooled), _ptr(out), od, tok,
                             per, _ptr(status), _stream(stream)), "engram_embed")
     return out
+
+
+def engram_embed_grad_workspace_bytes(n_tokens: int, n_ids: int, D: int) -> int:
+    return int(lib.engram_embed_grad_workspace_bytes(n_tokens, n_ids, D))
+
+
+def _grad_args(ids, dy, pooled, workspace):
+    """The arguments the two gradient calls share, from ids and dy ([*ids.shape, D], or
+    [*ids.shape[:-1], D] when pooled; expanded dimensions may have stride 0)."""
+    import torch
+    dd = _dtype(dy, "dy")
+    if pooled and ids.dim() < 2:
+        raise EngramError(ERR_INVALID_ARG, "pooled ids must be [..., ids]")
+    T, R, ids_stride = _ids_view(ids)
+    D = dy.shape[-1] if dy.dim() else 0
+    tok, per = _embed_rows(ids, dy, D, pooled, "dy")
+    if workspace is None:
+        workspace = torch.empty(max(engram_embed_grad_workspace_bytes(T, R, D), 16),
+                                dtype=torch.uint8, device=dy.device)
+    return D, T * R, (_ptr(ids), T, R, ids_stride, _ptr(dy), dd, tok, per), workspace
+
+
+def engram_embed_grad(ids, dy, rows: int, scale: float = 1.0, pooled: bool = False, grad=None,
+                      grad_dtype=None, accumulate: bool = False, workspace=None, status=None,
+                      stream=None):
+    """The gradient of engram_embed(ids, table [rows, D], scale, pooled)'s table for the output
+    gradient dy: [rows, D], every row written (accumulate: added to grad, fp32 or bf16)."""
+    import torch
+    D, n, args, workspace = _grad_args(ids, dy, pooled, workspace)
+    if grad is None:
+        if accumulate:
+            raise EngramError(ERR_INVALID_ARG, "accumulate needs a grad to add to")
+        grad = torch.empty((rows, D), dtype=grad_dtype or torch.float32, device=dy.device)
+    gd = _dtype(grad, "grad")
+    if tuple(grad.shape) != (rows, D):
+        raise EngramError(ERR_INVALID_ARG, f"grad must be {[rows, D]}")
+    _unit(grad, "grad")
+    _check(lib.engram_embed_grad(*args, rows, D, float(scale), int(accumulate), _ptr(grad), gd,
+                                 max(grad.stride(0), D), _ptr(workspace), workspace.numel(),
+                                 _ptr(status), _stream(stream)), "engram_embed_grad")
+    return grad
+
+
+def engram_embed_grad_rows(ids, dy, rows: int, scale: float = 1.0, pooled: bool = False,
+                           row_ids=None, grads=None, count=None, grad_dtype=None, workspace=None,
+                           status=None, stream=None):
+    """The same gradient as its distinct rows: (row_ids int32 [n], grads [n, D], count int32 [1])
+    for n = ids.numel(): the ascending distinct ids and then -1, their gradients (the rows past
+    count are not written), and their number."""
+    import torch
+    D, n, args, workspace = _grad_args(ids, dy, pooled, workspace)
+    if row_ids is None:
+        row_ids = torch.empty(n, dtype=torch.int32, device=dy.device)
+    if grads is None:
+        grads = torch.empty((n, D), dtype=grad_dtype or torch.float32, device=dy.device)
+    if count is None:
+        count = torch.empty(1, dtype=torch.int32, device=dy.device)
+    _need(row_ids, (torch.int32,), "row_ids")
+    _need(count, (torch.int32,), "count")
+    gd = _dtype(grads, "grads")
+    if row_ids.numel() != n or tuple(grads.shape) != (n, D) or count.numel() != 1:
+        raise EngramError(ERR_INVALID_ARG, "row_ids / grads / count sizes disagree with ids")
+    _unit(grads, "grads")
+    _check(lib.engram_embed_grad_rows(*args, rows, D, float(scale), _ptr(row_ids), _ptr(grads), gd,
+                                      max(grads.stride(0), D), _ptr(count), _ptr(workspace),
+                                      workspace.numel(), _ptr(status), _stream(stream)),
+           "engram_embed_grad_rows")
+    return row_ids, grads, count
 
 
 def fp8_empty(rows: int, cols: int, device):

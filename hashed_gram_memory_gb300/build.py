@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libengram.so")
 
 SOURCES = ["engram_api.cu", "compress_hash.cu", "lookup_fused.cu", "lookup_bulk.cu",
            "decode_step.cu", "forward.cu", "forward_static.cu", "wkv_gemm.cu", "connection.cu",
-           "table_pack.cu", "train_api.cu", "embed.cu", "gate_grad.cu",
+           "table_pack.cu", "train_api.cu", "embed.cu", "embed_grad.cu", "gate_grad.cu",
            "fp8_quantise.cu", "fp8_matmul.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

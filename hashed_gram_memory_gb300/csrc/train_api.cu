@@ -102,6 +102,110 @@ ENGRAM_API engram_status engram_embed(const int32_t *ids, int64_t n_tokens, int3
                                                               (cudaStream_t)stream));
 }
 
+ENGRAM_API size_t engram_embed_grad_workspace_bytes(int64_t n_tokens, int32_t n_ids, int32_t D) {
+  if (n_tokens < 0 || n_ids < 1 || n_tokens > INT32_MAX / n_ids || D < 1 || D > ENGRAM_MAX_EMBED_D)
+    return 0;
+  return engram::embed_grad_workspace_bytes(n_tokens * n_ids, D);
+}
+
+// The checks and the launch that the two gradient calls share; `out_rows` rows of grad.
+static engram_status embed_grad_common(const char *fn, const int32_t *ids, int64_t n_tokens,
+                                       int32_t n_ids, int64_t ids_stride, const void *dy,
+                                       int32_t dy_dtype, int64_t dy_token_stride,
+                                       int64_t dy_id_stride, int64_t rows, int32_t D, float scale,
+                                       bool accumulate, void *grad, int32_t grad_dtype,
+                                       int64_t grad_stride, bool sparse, int32_t *row_ids_out,
+                                       int32_t *count_out, void *workspace,
+                                       size_t workspace_bytes, int32_t *status, void *stream) {
+  engram_status st = check_ids(fn, ids, n_tokens, n_ids, ids_stride, rows, D, status);
+  if (st != ENGRAM_OK) return st;
+  if (!dtype_ok(dy_dtype) || !dtype_ok(grad_dtype))
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: unknown dtype", fn);
+  const int64_t n = n_tokens * n_ids, out_rows = sparse ? n : rows;
+  if (dy_id_stride < 0 || dy_token_stride < 0)
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: dy strides < 0", fn);
+  if (n > 0 && (!dy || !aligned(dy, dtype_bytes(dy_dtype))))
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: dy NULL or misaligned", fn);
+  if ((out_rows > 0 && (!grad || !aligned(grad, dtype_bytes(grad_dtype)))) ||
+      (out_rows > 1 && grad_stride < D))
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: gradient NULL or misaligned, or its stride under D", fn);
+  if (sparse && (!count_out || !aligned(count_out, 4) || (n > 0 && !row_ids_out) ||
+                 !aligned(row_ids_out, 4)))
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: row_ids_out or count_out NULL or misaligned", fn);
+  const size_t need = engram_embed_grad_workspace_bytes(n_tokens, n_ids, D);
+  if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
+    return set_error(ENGRAM_ERR_INVALID_ARG,
+                     "%s: workspace NULL, not 16-byte aligned or under %zu bytes", fn, need);
+  const struct {
+    const void *p;
+    size_t n;
+  } outs[4] = {{grad, extent(out_rows, grad_stride, 1, 0, D) * dtype_bytes(grad_dtype)},
+               {workspace, need},
+               {sparse ? row_ids_out : nullptr, (size_t)n * 4},
+               {sparse ? count_out : nullptr, 4}},
+    ins[3] = {{ids, (size_t)extent(n_tokens, ids_stride, 1, 0, n_ids) * 4},
+              {dy, extent(n_tokens, dy_token_stride, n_ids, dy_id_stride, D) * dtype_bytes(dy_dtype)},
+              {status, 4}};
+  for (int o = 0; o < 4; ++o) {
+    for (int i = 0; i < 3; ++i)
+      if (overlap(outs[o].p, outs[o].n, ins[i].p, ins[i].n))
+        return set_error(ENGRAM_ERR_INVALID_ARG, "%s: an output overlaps an input", fn);
+    for (int i = 0; i < o; ++i)
+      if (overlap(outs[o].p, outs[o].n, outs[i].p, outs[i].n))
+        return set_error(ENGRAM_ERR_INVALID_ARG, "%s: output buffers overlap", fn);
+  }
+  if ((st = engram::check_sm103()) != ENGRAM_OK) return st;
+  engram::EmbedGradParams p{};
+  p.ids = ids;
+  p.dy = dy;
+  p.grad = grad;
+  p.row_ids_out = row_ids_out;
+  p.count_out = count_out;
+  p.status = status;
+  p.n = n;
+  p.ids_stride = ids_stride;
+  p.rows = rows;
+  p.dy_token_stride = dy_token_stride;
+  p.dy_id_stride = dy_id_stride;
+  p.grad_stride = grad_stride;
+  p.n_ids = n_ids;
+  p.D = D;
+  p.scale = scale;
+  p.accumulate = accumulate;
+  return launched(fn, engram::launch_embed_grad(p, dy_dtype, grad_dtype, workspace, sparse,
+                                                (cudaStream_t)stream));
+}
+
+ENGRAM_API engram_status engram_embed_grad(const int32_t *ids, int64_t n_tokens, int32_t n_ids,
+                                           int64_t ids_stride, const void *dy, int32_t dy_dtype,
+                                           int64_t dy_token_stride, int64_t dy_id_stride,
+                                           int64_t rows, int32_t D, float scale,
+                                           int32_t accumulate, void *grad, int32_t grad_dtype,
+                                           int64_t grad_stride, void *workspace,
+                                           size_t workspace_bytes, int32_t *status, void *stream) {
+  ENGRAM_NVTX_RANGE("engram_embed_grad");
+  return embed_grad_common("engram_embed_grad", ids, n_tokens, n_ids, ids_stride, dy, dy_dtype,
+                           dy_token_stride, dy_id_stride, rows, D, scale, accumulate != 0, grad,
+                           grad_dtype, grad_stride, false, nullptr, nullptr, workspace,
+                           workspace_bytes, status, stream);
+}
+
+ENGRAM_API engram_status engram_embed_grad_rows(const int32_t *ids, int64_t n_tokens, int32_t n_ids,
+                                                int64_t ids_stride, const void *dy,
+                                                int32_t dy_dtype, int64_t dy_token_stride,
+                                                int64_t dy_id_stride, int64_t rows, int32_t D,
+                                                float scale, int32_t *row_ids_out, void *grads_out,
+                                                int32_t grads_dtype, int64_t grads_stride,
+                                                int32_t *count_out, void *workspace,
+                                                size_t workspace_bytes, int32_t *status,
+                                                void *stream) {
+  ENGRAM_NVTX_RANGE("engram_embed_grad_rows");
+  return embed_grad_common("engram_embed_grad_rows", ids, n_tokens, n_ids, ids_stride, dy, dy_dtype,
+                           dy_token_stride, dy_id_stride, rows, D, scale, false, grads_out,
+                           grads_dtype, grads_stride, true, row_ids_out, count_out, workspace,
+                           workspace_bytes, status, stream);
+}
+
 ENGRAM_API engram_status engram_fp8_quantise(const void *x, int32_t x_dtype, int64_t M, int64_t K,
                                              int64_t x_stride, int32_t block_rows, uint8_t *q,
                                              int64_t q_stride, uint8_t *s, uint8_t *qt,

@@ -21,6 +21,36 @@ struct EmbedParams {
 cudaError_t launch_embed(const EmbedParams &p, int table_dtype, int out_dtype, bool pooled,
                          cudaStream_t stream);
 
+struct FastDiv {  // x / d as x * mul >> shift
+  uint32_t mul, shift;
+};
+
+struct EmbedGradParams {
+  const int32_t *ids;
+  const void *dy;
+  void *grad;            // dense: [rows, D]; sparse: a row per distinct id
+  int32_t *row_ids_out;  // sparse: [n], the distinct ids, then ENGRAM_ROW_DEAD
+  int32_t *count_out;    // sparse: how many
+  int32_t *status;
+  int64_t n, ids_stride, rows, dy_token_stride, dy_id_stride, grad_stride;
+  int32_t n_ids, D;
+  float scale;
+  bool accumulate;
+  // set by the launcher
+  FastDiv by_ids;
+  bool dy_linear;              // dy rows are dy_id_stride apart throughout
+  int32_t passes, digit_bits;  // of the sort
+  int64_t tiles;
+  uint32_t *keys, *pos, *counts, *totals;
+  uint32_t *run_base;  // sparse: runs before each chunk, their number behind; else NULL
+  float *partial;      // [chunks][2][partial_stride]: a run open at the start, at the end
+  int64_t partial_stride, chunks, sum_blocks;
+  int32_t group, slabs, chunk;  // lanes a group, column slabs, sorted ids a chunk
+};
+size_t embed_grad_workspace_bytes(int64_t n, int32_t D);
+cudaError_t launch_embed_grad(EmbedGradParams p, int dy_dtype, int grad_dtype, void *workspace,
+                              bool sparse, cudaStream_t stream);
+
 struct GateGradParams {
   const float *k;
   const uint8_t *state;  // NULL: every token live

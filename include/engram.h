@@ -562,6 +562,48 @@ ENGRAM_API engram_status engram_embed(const int32_t *ids, int64_t n_tokens, int3
                                       int32_t *status, void *stream);
 
 /*
+ * engram_embed_grad -- the gradient of engram_embed's table, every row written:
+ *   grad[v] = scale * sum over (t, j) with ids[t, j] = v of dy[t, j]
+ * added up in fp32 in ascending (t, j), rounded once; accumulate != 0 adds to grad
+ * instead (rows that no id names stay as they are).
+ *   ids, n_tokens, n_ids, ids_stride, rows, D, scale as engram_embed
+ *   dy    ENGRAM_DTYPE_*; row (t, j) starts at t*dy_token_stride + j*dy_id_stride
+ *         elements.  dy_id_stride 0 is the gradient of a pooled lookup: every id of a
+ *         token has the token's row (any other broadcast likewise)
+ *   grad  ENGRAM_DTYPE_* [rows, D], grad_stride elements between rows
+ *   workspace  device, 16-byte aligned, at least
+ *         engram_embed_grad_workspace_bytes(n_tokens, n_ids, D) bytes
+ * Ids ENGRAM_ROW_DEAD take no part; any other id outside [0, rows) sets
+ * ENGRAM_FLAG_BAD_ROW and takes no part either.  n_tokens == 0 zeroes grad.
+ *
+ * engram_embed_grad_rows -- the same for tables whose dense gradient would not fit: the
+ * distinct ids and their rows.
+ *   row_ids_out  int32 [n_tokens * n_ids]: the distinct ids, ascending, then
+ *                ENGRAM_ROW_DEAD
+ *   grads_out    ENGRAM_DTYPE_* [n_tokens * n_ids, D], grads_stride elements between
+ *                rows: row i is the gradient of row_ids_out[i]; rows past the distinct
+ *                ids are not written
+ *   count_out    int32 [1]: the number of distinct ids
+ */
+ENGRAM_API size_t engram_embed_grad_workspace_bytes(int64_t n_tokens, int32_t n_ids, int32_t D);
+ENGRAM_API engram_status engram_embed_grad(const int32_t *ids, int64_t n_tokens, int32_t n_ids,
+                                           int64_t ids_stride, const void *dy, int32_t dy_dtype,
+                                           int64_t dy_token_stride, int64_t dy_id_stride,
+                                           int64_t rows, int32_t D, float scale,
+                                           int32_t accumulate, void *grad, int32_t grad_dtype,
+                                           int64_t grad_stride, void *workspace,
+                                           size_t workspace_bytes, int32_t *status, void *stream);
+ENGRAM_API engram_status engram_embed_grad_rows(const int32_t *ids, int64_t n_tokens, int32_t n_ids,
+                                                int64_t ids_stride, const void *dy,
+                                                int32_t dy_dtype, int64_t dy_token_stride,
+                                                int64_t dy_id_stride, int64_t rows, int32_t D,
+                                                float scale, int32_t *row_ids_out, void *grads_out,
+                                                int32_t grads_dtype, int64_t grads_stride,
+                                                int32_t *count_out, void *workspace,
+                                                size_t workspace_bytes, int32_t *status,
+                                                void *stream);
+
+/*
  * engram_fp8_quantise -- x as e4m3fn bytes with one power-of-two scale per block of 128:
  * for each block, the smallest exponent e >= -127 with max|x| <= 448 * 2^e is stored as
  * the byte e + 127 (OCP E8M0, as the tables' exponents), and x becomes e4m3(x * 2^-e),
