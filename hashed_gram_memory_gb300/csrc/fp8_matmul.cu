@@ -9,14 +9,26 @@
 // neighbouring outputs of one row of out in its lanes and stores whole lines for any
 // output stride and size.
 //
-// One persistent CTA per SM walks 128 (b) x up to 128 (a) tiles.  Warps:
+// The fp32 accumulator of the tensor cores does not round to nearest: its error grows with
+// the number of additions (2e-6 of the result at K = 16,411, against 2.5e-7 of an fp32 sum).
+// So K is cut into segments of at most 64 blocks (8192 values) that each start a new
+// accumulator, and the epilogue adds the segments in registers, rounding to nearest.
+//
+// Two persistent kernels walk tiles of out:
+//   fp8_matmul_pair_kernel: CTA pairs, tiles of 256 (b) x up to 240 (a) values with
+//     tcgen05.mma.cta_group::2 -- each CTA stages its 128 rows of b and half of the rows of
+//     a.  240, not 256: two whole accumulators and the scales then fit the 512 columns, and
+//     a tile's MMAs follow the last one's without waiting for the epilogue;
+//   fp8_matmul_kernel: one CTA per SM, 128 x up to 128 tiles, for products too small to
+//     fill the pairs.
+// Warps:
 //   0     TMA producer: a ring of stages, each a 128-byte slice along K of the tile's rows
 //         of a and b (128-byte swizzle);
-//   1     allocates TMEM; one thread copies the scales to TMEM (tcgen05.cp) and issues the
-//         MMAs into one of two accumulators;
-//   2..5  epilogue: TMEM lanes 32*(warp%4).., stores;
-//   6     scales: for every four blocks of K one 32-bit word per row, put into shared
-//         memory in the order tcgen05.cp wants (word (r%32)*4 + r/32 of each 128 rows).
+//   1     allocates TMEM; one thread (of the pair's even CTA) copies the scales to TMEM
+//         (tcgen05.cp) and issues the MMAs into one of two accumulators;
+//   2, 3  scales (the pairs' second warp shares the work): for every four blocks of K one 32-bit word per row, put into shared
+//         memory in the order tcgen05.cp wants (word (r%32)*4 + r/32 of each 128 rows);
+//   4..   epilogue: TMEM lanes 32*(warp%4).., stores.
 // Every wait is bounded as in wkv_gemm.cu: one that gives up sets ENGRAM_FLAG_TIMEOUT and
 // leaves the tiles not yet stored unwritten.
 #include <mutex>
@@ -30,9 +42,11 @@ namespace {
 
 constexpr int kP = 128;       // rows of b a tile
 constexpr int kQMax = 128;    // most rows of a a tile
-constexpr int kThreads = 224;
-constexpr int kScaleSlots = 4;
-constexpr uint32_t kSlotBytes = (kP + kQMax) * 4;
+constexpr int kThreads = 256;  // warp 3 idles: the epilogue's warps start at a multiple of 4
+constexpr int kSegmentBlocks = 64;
+constexpr int kScaleSlots = 2;                        // of 16 blocks of K: four groups of four
+constexpr uint32_t kGroupBytes = (kP + kQMax) * 4;
+constexpr uint32_t kSlotBytes = 4 * kGroupBytes;
 constexpr int kMaxStages = 8;
 constexpr uint32_t kStageBudget = 192 * 1024;
 constexpr uint32_t kTmemCols = 512;
@@ -46,7 +60,8 @@ struct MatmulDev {
   int64_t M, N, out_stride;
   int32_t kblocks, a_shift, b_shift;  // log2 of the rows sharing a scale (0 or 7)
   int32_t q_tile, stages;
-  int64_t tiles_q, tiles;
+  int32_t segments, seg_blocks;  // K in segments of seg_blocks blocks (a multiple of 4)
+  int64_t tiles_p, tiles_q, tiles;
   int64_t wait_limit_ns;
 };
 
@@ -78,18 +93,54 @@ __device__ __forceinline__ void umma_fp8(uint32_t d, uint64_t p_desc, uint64_t q
       : "memory");
 }
 
-// The scale bytes of four blocks of K (from block kb on) of one row, zero past either end.
-__device__ __forceinline__ uint32_t scale_word(const uint8_t *s, int64_t row, int64_t rows, int shift,
-                                               int kb, int kblocks) {
-  if (row >= rows) return 0;
-  const uint8_t *src = s + (row >> shift) * kblocks + kb;
-  if (kb + 4 <= kblocks && ((uintptr_t)src & 3) == 0) return __ldg(reinterpret_cast<const uint32_t *>(src));
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (kb + i < kblocks) w |= (uint32_t)__ldg(src + i) << (8 * i);
-  return w;
+// The whole warp waits; the same answer in every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                          const MatmulDev &p) {
+  return __all_sync(0xffffffffu, wait_phase(bar, parity, abort_flag, p.wait_limit_ns, p.status));
 }
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
+// The scale bytes of 16 blocks of K (from block kb on, a multiple of 16) of one row, as whole
+// aligned words and the shift to their first byte, so that they can be in flight while the
+// batch before them is written.  Bytes past the last block are whatever follows (no MMA reads
+// them), rows past the last one zero; single bytes are loaded only where a word would reach
+// outside the array.
+struct Scales {
+  uint32_t v[5], shift;
+
+  __device__ __forceinline__ void load(const uint8_t *s, int64_t row, int64_t rows, int row_shift, int kb,
+                                       int kblocks) {
+    shift = 0;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) v[i] = 0;
+    if (row >= rows) return;
+    const uint8_t *end = s + (((rows - 1) >> row_shift) + 1) * kblocks;
+    const uint8_t *src = s + (row >> row_shift) * kblocks + kb;
+    const uint32_t off = (uint32_t)((uintptr_t)src & 3);
+    const uint8_t *word = src - off;
+    if (word >= s && word + 20 <= end) {
+      shift = 8 * off;
+#pragma unroll
+      for (int i = 0; i < 5; ++i) v[i] = __ldg(reinterpret_cast<const uint32_t *>(word) + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (kb + i < kblocks) v[i >> 2] |= (uint32_t)__ldg(src + i) << (8 * (i & 3));
+    }
+  }
+  // The bytes of blocks kb + 4g .. kb + 4g + 3.
+  __device__ __forceinline__ uint32_t word(int g) const { return __funnelshift_r(v[g], v[g + 1], shift); }
+};
 
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&v)[16]) {
   asm volatile(
@@ -103,6 +154,15 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&v)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// Tiles in groups of up to 16 along b, a's tiles inside a group in order: what the resident
+// CTAs read at one time is a few slices of each operand.
+__device__ __forceinline__ void tile_at(const MatmulDev &p, int64_t tile, int64_t &tp, int64_t &tq) {
+  const int64_t per = 16 * p.tiles_q, g = tile / per, in = tile - g * per;
+  const int64_t wide = min((int64_t)16, p.tiles_p - g * 16);
+  tq = in / wide;
+  tp = g * 16 + in - tq * wide;
+}
+
 template <typename TO>
 __device__ __forceinline__ void store_out(TO *dst, uint32_t v) {
   if constexpr (sizeof(TO) == 4)
@@ -111,7 +171,57 @@ __device__ __forceinline__ void store_out(TO *dst, uint32_t v) {
     *dst = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v)));
 }
 
-template <typename TO>
+// A warp's part of an accumulator -- 32 lanes (outputs n, n + 1, ..), `chunks` times 16 columns
+// (outputs m0, m0 + 1, ..) -- goes to memory or (MULTI) into sums over the segments that the
+// last one stores.  `release` runs once the last column is in registers, before its stores.
+template <typename TO, int CHUNKS, bool MULTI>
+struct Drain {
+  float sum[MULTI ? CHUNKS * 16 : 1];
+
+  template <typename F>
+  __device__ __forceinline__ void run(uint32_t taddr, int chunks, bool first, bool last, TO *out, int64_t stride,
+                                      int64_t m0, int64_t M, bool mine, F release) {
+    const int rows = (int)min((int64_t)chunks * 16, M - m0);
+    if constexpr (MULTI) {
+#pragma unroll
+      for (int c = 0; c < CHUNKS; ++c) {
+        if (c < chunks) {
+          uint32_t v[16];
+          tmem_ld16(taddr + c * 16, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float f = __uint_as_float(v[i]);
+            sum[c * 16 + i] = first ? f : sum[c * 16 + i] + f;
+          }
+        }
+      }
+      release();
+      if (!last || !mine) return;
+      out += m0 * stride;
+#pragma unroll
+      for (int i = 0; i < CHUNKS * 16; ++i) {
+        if (i < rows) store_out(out, __float_as_uint(sum[i]));
+        out += stride;
+      }
+    } else {
+      out += m0 * stride;
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c) {
+        uint32_t v[16];
+        tmem_ld16(taddr + c * 16, v);
+        if (c == chunks - 1) release();
+        if (!mine) continue;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (c * 16 + i < rows) store_out(out, v[i]);
+          out += stride;
+        }
+      }
+    }
+  }
+};
+
+template <typename TO, bool MULTI>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                       const __grid_constant__ MatmulDev p) {
@@ -169,7 +279,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t ph = 0;
       bool ok = true;
       for (int64_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) {
-        const int p0 = (int)(tile / p.tiles_q) * kP, q0 = (int)(tile % p.tiles_q) * qt;
+        int64_t tp, tq;
+        tile_at(p, tile, tp, tq);
+        const int p0 = (int)(tp * kP), q0 = (int)(tq * qt);
         for (int kb = 0; kb < kblocks; ++kb, ++it) {
           if (!(ok = wait_phase(empty + s, ph ^ 1, abort_flag, p.wait_limit_ns, p.status))) break;
           uint8_t *st = sm + s * stage_bytes;
@@ -184,98 +296,124 @@ __global__ void __launch_bounds__(kThreads, 1)
         drain_phase(full + j % stages, (j / stages) & 1, p.wait_limit_ns);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------------------------------------------------- MMA issuer
-      uint32_t local = 0, group = 0;
-      int s = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (int64_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x, ++local) {
-        const uint32_t acc = local & 1, use = local >> 1;
-        if (!wait_phase(acc_empty + acc, (use & 1) ^ 1, abort_flag, p.wait_limit_ns, p.status)) break;
+    // ------------------------------------------------------------ MMA issuer
+    // The warp runs the loop together, so that what the instructions take (descriptors,
+    // columns) is computed once in its uniform registers; one lane issues.
+    uint32_t unit = 0, batch = 0;
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    const bool one = elect_one();
+    for (int64_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) {
+      for (int kb0 = 0; ok && kb0 < kblocks; kb0 += p.seg_blocks, ++unit) {
+        const int kb1 = min(kb0 + p.seg_blocks, kblocks);
+        const uint32_t acc = unit & 1, use = unit >> 1;
+        if (!(ok = warp_wait(acc_empty + acc, (use & 1) ^ 1, abort_flag, p))) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t d = tmem + acc * kQMax;
         uint32_t sp = 0, sq = 0;
-        for (int kb = 0; kb < kblocks; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if ((kb & 3) == 0) {  // the scales of the next four blocks
-            const int slot = group % kScaleSlots;
-            if (!(ok = wait_phase(sc_full + slot, (group / kScaleSlots) & 1, abort_flag,
-                                  p.wait_limit_ns, p.status)))
-              break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            sp = tmem + kScaleCol + (group & 1) * 8, sq = sp + 4;
-            const uint32_t src = smem_u32(slots + slot * kSlotBytes);
-            copy_scales(sp, smem_desc_scales(src));
-            copy_scales(sq, smem_desc_scales(src + kP * 4));
-            umma_commit(sc_empty + slot);
-            ++group;
+            const int slot = batch & 1;
+            if ((kb & 15) == 0) {
+              if (!(ok = warp_wait(sc_full + slot, (batch >> 1) & 1, abort_flag, p))) break;
+              asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            }
+            sp = tmem + kScaleCol + (kb >> 2 & 1) * 8, sq = sp + 4;
+            const uint64_t src =
+                smem_desc_scales(smem_u32(slots + slot * kSlotBytes + (kb >> 2 & 3) * kGroupBytes));
+            const bool done = (kb & 15) == 12 || kb + 4 >= kblocks;  // with this slot
+            if (one) {
+              copy_scales(sp, src);
+              copy_scales(sq, src + (kP * 4 >> 4));
+              if (done) umma_commit(sc_empty + slot);
+            }
+            batch += done;
           }
-          if (!(ok = wait_phase(full + s, ph, abort_flag, p.wait_limit_ns, p.status))) break;
+          if (!(ok = warp_wait(full + s, ph, abort_flag, p))) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t ps = smem_u32(sm + s * stage_bytes), qs = ps + kP * 128;
+          const uint32_t ps = smem_u32(sm + s * stage_bytes);
+          const uint64_t pd = smem_desc_sw128(ps), qd = smem_desc_sw128(ps + kP * 128);
           const uint32_t idesc = instr_desc(kP, qt, kb & 3);
+          if (one) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_fp8(d, smem_desc_sw128(ps + 32 * k), smem_desc_sw128(qs + 32 * k), idesc, sp, sq,
-                     (kb | k) != 0 ? 1u : 0u);
-          umma_commit(empty + s);
+            for (int k = 0; k < 4; ++k)  // 32 values along K: 32 bytes
+              umma_fp8(d, pd + 2 * k, qd + 2 * k, idesc, sp, sq, kb != kb0 || k != 0 ? 1u : 0u);
+            umma_commit(empty + s);
+          }
+          __syncwarp();
           if (++s == stages) s = 0, ph ^= 1;
         }
-        if (ok) umma_commit(acc_full + acc);
-      }
-      umma_commit(mma_done);
-    }
-  } else if (warp == 6) {
-    // --------------------------------------------------------------- scales
-    uint32_t group = 0;
-    bool ok = true;
-    for (int64_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) {
-      const int64_t p0 = tile / p.tiles_q * kP, q0 = tile % p.tiles_q * qt;
-      for (int kb = 0; kb < kblocks; kb += 4, ++group) {
-        const int slot = group % kScaleSlots;
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = scale_word(p.b_scale, p0 + 32 * i + lane, p.N, p.b_shift, kb, kblocks);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[4 + i] = 32 * i < qt ? scale_word(p.a_scale, q0 + 32 * i + lane, p.M, p.a_shift, kb, kblocks) : 0;
-        ok = __all_sync(0xffffffffu, wait_phase(sc_empty + slot, ((group / kScaleSlots) & 1) ^ 1,
-                                                abort_flag, p.wait_limit_ns, p.status));
-        if (!ok) break;
-        uint4 *dst = reinterpret_cast<uint4 *>(slots + slot * kSlotBytes);
-        dst[lane] = make_uint4(w[0], w[1], w[2], w[3]);
-        dst[32 + lane] = make_uint4(w[4], w[5], w[6], w[7]);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (ok && one) umma_commit(acc_full + acc);
         __syncwarp();
-        if (lane == 0) mbar_arrive(sc_full + slot);
       }
     }
-  } else {
+    if (one) umma_commit(mma_done);
+    __syncwarp();
+  } else if (warp == 2) {
+    // --------------------------------------------------------------- scales
+    // 16 blocks of K at a time, the next batch's loads in flight under this one's waits.
+    uint32_t batch = 0;
+    bool ok = true;
+    const auto load = [&](int64_t tile, int kb, Scales(&w)[8]) {
+      if (tile >= p.tiles) return;
+      int64_t p0, q0;
+      tile_at(p, tile, p0, q0);
+      p0 *= kP, q0 *= qt;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[i].load(p.b_scale, p0 + 32 * i + lane, p.N, p.b_shift, kb, kblocks);
+        w[4 + i].load(p.a_scale, q0 + 32 * i + lane, 32 * i < qt ? p.M : 0, p.a_shift, kb, kblocks);
+      }
+    };
+    Scales w[8];
+    int64_t tile = blockIdx.x;
+    int kb = 0;
+    load(tile, kb, w);
+    while (ok && tile < p.tiles) {
+      const int64_t next_tile = kb + 16 < kblocks ? tile : tile + gridDim.x;
+      const int next_kb = kb + 16 < kblocks ? kb + 16 : 0;
+      Scales next[8];
+      load(next_tile, next_kb, next);
+      const int slot = batch & 1;
+      if (!(ok = warp_wait(sc_empty + slot, ((batch >> 1) & 1) ^ 1, abort_flag, p))) break;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        uint4 *dst = reinterpret_cast<uint4 *>(slots + slot * kSlotBytes + g * kGroupBytes);
+        dst[lane] = make_uint4(w[0].word(g), w[1].word(g), w[2].word(g), w[3].word(g));
+        dst[32 + lane] = make_uint4(w[4].word(g), w[5].word(g), w[6].word(g), w[7].word(g));
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sc_full + slot);
+      ++batch;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = next[i];
+      tile = next_tile, kb = next_kb;
+    }
+  } else if (warp >= 4) {
     // ------------------------------------------------------------- epilogue
     const int quad = warp & 3;
-    uint32_t local = 0;
-    for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x, ++local) {
-      const uint32_t acc = local & 1, use = local >> 1;
-      const bool ok = wait_phase(acc_full + acc, use & 1, abort_flag, p.wait_limit_ns, p.status);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const int64_t n = tile / p.tiles_q * kP + quad * 32 + lane;
-      const int64_t m0 = tile % p.tiles_q * qt;
+    uint32_t unit = 0;
+    bool ok = true;
+    Drain<TO, kQMax / 16, MULTI> drain;
+    for (int64_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) {
+      int64_t tp, tq;
+      tile_at(p, tile, tp, tq);
+      const int64_t n = tp * kP + quad * 32 + lane, m0 = tq * qt;
       TO *out = static_cast<TO *>(p.out) + n;
-#pragma unroll 1
-      for (int c = 0; c < qt; c += 16) {
-        uint32_t v[16];
-        tmem_ld16(tmem + ((uint32_t)(quad * 32) << 16) + acc * kQMax + c, v);
-        if (n < p.N) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (m0 + c + i < p.M) store_out(out + (m0 + c + i) * p.out_stride, v[i]);
-        }
+      for (int seg = 0; seg < p.segments; ++seg, ++unit) {
+        const uint32_t acc = unit & 1, use = unit >> 1;
+        ok = warp_wait(acc_full + acc, use & 1, abort_flag, p);
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t base = tmem + ((uint32_t)(quad * 32) << 16) + acc * kQMax;
+        drain.run(base, qt / 16, seg == 0, seg == p.segments - 1, out, p.out_stride, m0, p.M, n < p.N, [&] {
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(acc_empty + acc);
+        });
       }
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty + acc);
     }
   }
 
@@ -290,6 +428,272 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
                  : "memory");
   }
+}
+
+// ---- CTA pairs ------------------------------------------------------------------------
+
+constexpr int kPairQMax = 240;
+constexpr int kPairThreads = 384;
+constexpr uint32_t kPairStageBudget = 213 * 1024;
+constexpr uint32_t kPairGroupBytes = (kP + 256) * 4;
+constexpr uint32_t kPairSlotBytes = 4 * kPairGroupBytes;
+constexpr uint32_t kPairScaleCol = 2 * kPairQMax;  // scale words: two buffers of 4 (b) + 8 (a) columns
+constexpr size_t kPairSmemBytes = 1024 + kPairStageBudget + kScaleSlots * kPairSlotBytes + 512;
+static_assert(kPairScaleCol + 2 * 12 <= kTmemCols && kPairSmemBytes <= 227 * 1024);
+
+__device__ __forceinline__ void copy_scales_pair(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+__device__ __forceinline__ void umma_fp8_pair(uint32_t d, uint64_t p_desc, uint64_t q_desc, uint32_t idesc,
+                                              uint32_t sp, uint32_t sq, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
+      "[%5], p;\n\t}" ::"r"(d),
+      "l"(p_desc), "l"(q_desc), "r"(idesc), "r"(sp), "r"(sq), "r"(accumulate)
+      : "memory");
+}
+
+// Barriers as in wkv_gemm_pair_kernel: full and sc_full live in the leader (the even CTA),
+// sc_full with one arrival per scale warp; empty, sc_empty, acc_full and mma_done exist
+// in both and take the leader's multicast commits; acc_empty lives in the leader and takes an
+// arrival from every epilogue warp of the pair.
+template <typename TO, bool MULTI>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    fp8_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_a,
+                           const __grid_constant__ CUtensorMap map_b, const __grid_constant__ MatmulDev p) {
+  extern __shared__ uint8_t sm_raw[];
+  uint8_t *sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kblocks = p.kblocks, stages = p.stages, qt = p.q_tile;
+  const uint32_t stage_bytes = (uint32_t)(kP + qt / 2) * 128;
+  uint8_t *slots = sm + kPairStageBudget;
+  uint64_t *full = reinterpret_cast<uint64_t *>(slots + kScaleSlots * kPairSlotBytes);
+  uint64_t *empty = full + kMaxStages;
+  uint64_t *sc_full = empty + kMaxStages;
+  uint64_t *sc_empty = sc_full + kScaleSlots;
+  uint64_t *acc_full = sc_empty + kScaleSlots;
+  uint64_t *acc_empty = acc_full + 2;
+  uint64_t *mma_done = acc_empty + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+  const uint32_t rank = cluster_rank();
+  const int64_t cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int s = 0; s < kScaleSlots; ++s) {
+      mbar_init(sc_full + s, 4);
+      mbar_init(sc_empty + s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(acc_full + a, 1);
+      mbar_init(acc_empty + a, 16);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  cluster_sync();  // both CTAs' barriers are initialised before either uses the other's
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ----------------------------------------------- TMA producer (both CTAs)
+      const uint32_t full_lead = map_to_rank(smem_u32(full), 0);
+      uint32_t it = 0;
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int64_t tile = cluster; ok && tile < p.tiles; tile += n_clusters) {
+        int64_t tp, tq;
+        tile_at(p, tile, tp, tq);
+        const int p0 = (int)(tp * 2 * kP) + (int)rank * kP, q0 = (int)(tq * qt) + (int)rank * (qt / 2);
+        for (int kb = 0; kb < kblocks; ++kb, ++it) {
+          if (!(ok = wait_phase(empty + s, ph ^ 1, abort_flag, p.wait_limit_ns, p.status))) break;
+          uint8_t *st = sm + s * stage_bytes;
+          const uint32_t bar = full_lead + 8u * s;
+          if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * stage_bytes);
+          tma_load_2d_pair(st, &map_b, kb * 128, p0, bar);
+          tma_load_2d_pair(st + kP * 128, &map_a, kb * 128, q0, bar);
+          if (++s == stages) s = 0, ph ^= 1;
+        }
+      }
+      // The leader's full barriers count both CTAs' bytes.
+      if (rank == 0)
+        for (uint32_t j = it > (uint32_t)stages ? it - stages : 0; j < it; ++j)
+          drain_phase(full + j % stages, (j / stages) & 1, p.wait_limit_ns);
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      // ------------------------------------------------- MMA issuer (leader)
+      uint32_t unit = 0, batch = 0;
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      const bool one = elect_one();
+      for (int64_t tile = cluster; ok && tile < p.tiles; tile += n_clusters) {
+        for (int kb0 = 0; ok && kb0 < kblocks; kb0 += p.seg_blocks, ++unit) {
+          const int kb1 = min(kb0 + p.seg_blocks, kblocks);
+          const uint32_t acc = unit & 1, use = unit >> 1;
+          if (!(ok = warp_wait(acc_empty + acc, (use & 1) ^ 1, abort_flag, p))) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint32_t d = tmem + acc * kPairQMax;
+          uint32_t sp = 0, sq = 0;
+          for (int kb = kb0; kb < kb1; ++kb) {
+            if ((kb & 3) == 0) {
+              const int slot = batch & 1;
+              // Both CTAs' words: their writers fenced them for the async proxy and released
+              // them to the cluster.  This thread does not read them (tcgen05.cp does), so a
+              // cluster-scope acquire is not needed.
+              if ((kb & 15) == 0) {
+                if (!(ok = warp_wait(sc_full + slot, (batch >> 1) & 1, abort_flag, p))) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+              }
+              sp = tmem + kPairScaleCol + (kb >> 2 & 1) * 12, sq = sp + 4;
+              const uint64_t src =
+                  smem_desc_scales(smem_u32(slots + slot * kPairSlotBytes + (kb >> 2 & 3) * kPairGroupBytes));
+              const bool done = (kb & 15) == 12 || kb + 4 >= kblocks;
+              if (one) {
+                copy_scales_pair(sp, src);
+                copy_scales_pair(sq, src + (kP * 4 >> 4));
+                if (qt > 128) copy_scales_pair(sq + 4, src + (2 * kP * 4 >> 4));
+                if (done) umma_commit_pair(sc_empty + slot);
+              }
+              batch += done;
+            }
+            if (!(ok = warp_wait(full + s, ph, abort_flag, p))) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t ps = smem_u32(sm + s * stage_bytes);
+            const uint64_t pd = smem_desc_sw128(ps), qd = smem_desc_sw128(ps + kP * 128);
+            const uint32_t idesc = instr_desc(2 * kP, qt, kb & 3);
+            if (one) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                umma_fp8_pair(d, pd + 2 * k, qd + 2 * k, idesc, sp, sq, kb != kb0 || k != 0 ? 1u : 0u);
+              umma_commit_pair(empty + s);
+            }
+            __syncwarp();
+            if (++s == stages) s = 0, ph ^= 1;
+          }
+          if (ok && one) umma_commit_pair(acc_full + acc);
+          __syncwarp();
+        }
+      }
+      if (one) umma_commit_pair(mma_done);
+      __syncwarp();
+    }
+  } else if (warp < 4) {
+    // --------------------------- scales (both CTAs: own rows of b, all rows of a)
+    // 12 rows a lane: warp 2 takes the four of b and two of a, warp 3 six of a; 16 blocks of
+    // K at a time, the next batch's loads in flight under this one's waits.
+    const uint32_t sc_full_lead = map_to_rank(smem_u32(sc_full), 0);
+    const bool first = warp == 2;
+    uint32_t batch = 0;
+    bool ok = true;
+    const auto load = [&](int64_t tile, int kb, Scales(&w)[6]) {
+      if (tile >= p.tiles) return;
+      int64_t p0, q0;
+      tile_at(p, tile, p0, q0);
+      p0 = p0 * 2 * kP + rank * kP, q0 *= qt;
+#pragma unroll
+      for (int i = 0; i < 6; ++i) {
+        const int r = first ? i : 6 + i;  // of the 12
+        if (r < 4)
+          w[i].load(p.b_scale, p0 + 32 * r + lane, p.N, p.b_shift, kb, kblocks);
+        else
+          w[i].load(p.a_scale, q0 + 32 * (r - 4) + lane, 32 * (r - 4) < qt ? p.M : 0, p.a_shift, kb, kblocks);
+      }
+    };
+    Scales w[6];
+    int64_t tile = cluster;
+    int kb = 0;
+    load(tile, kb, w);
+    while (ok && tile < p.tiles) {
+      const int64_t next_tile = kb + 16 < kblocks ? tile : tile + n_clusters;
+      const int next_kb = kb + 16 < kblocks ? kb + 16 : 0;
+      Scales next[6];
+      load(next_tile, next_kb, next);
+      const int slot = batch & 1;
+      if (!(ok = warp_wait(sc_empty + slot, ((batch >> 1) & 1) ^ 1, abort_flag, p))) break;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        uint32_t *dst =
+            reinterpret_cast<uint32_t *>(slots + slot * kPairSlotBytes + g * kPairGroupBytes) + lane * 4;
+        if (first) {
+          *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0].word(g), w[1].word(g), w[2].word(g), w[3].word(g));
+          *reinterpret_cast<uint2 *>(dst + 128) = make_uint2(w[4].word(g), w[5].word(g));
+        } else {
+          *reinterpret_cast<uint2 *>(dst + 130) = make_uint2(w[0].word(g), w[1].word(g));
+          *reinterpret_cast<uint4 *>(dst + 256) =
+              make_uint4(w[2].word(g), w[3].word(g), w[4].word(g), w[5].word(g));
+        }
+      }
+      // Once for 16 blocks: the fence and the cluster-wide release wait for everything this
+      // warp has in flight, and once for four blocks they took longer than the blocks.
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(sc_full_lead + 8u * slot);
+      ++batch;
+#pragma unroll
+      for (int i = 0; i < 6; ++i) w[i] = next[i];
+      tile = next_tile, kb = next_kb;
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------- epilogue (both CTAs)
+    const int quad = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t acc_empty_lead = map_to_rank(smem_u32(acc_empty), 0);
+    // This warp's 16-column chunks: the first or the second half of the tile's.
+    const int c0 = half ? (qt / 16 + 1) / 2 : 0, chunks = half ? qt / 16 - c0 : (qt / 16 + 1) / 2;
+    uint32_t unit = 0;
+    bool ok = true;
+    Drain<TO, 8, MULTI> drain;
+    for (int64_t tile = cluster; ok && tile < p.tiles; tile += n_clusters) {
+      int64_t tp, tq;
+      tile_at(p, tile, tp, tq);
+      const int64_t n = tp * 2 * kP + rank * kP + quad * 32 + lane, m0 = tq * qt + c0 * 16;
+      TO *out = static_cast<TO *>(p.out) + n;
+      for (int seg = 0; seg < p.segments; ++seg, ++unit) {
+        const uint32_t acc = unit & 1, use = unit >> 1;
+        ok = warp_wait(acc_full + acc, use & 1, abort_flag, p);
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t base = tmem + ((uint32_t)(quad * 32) << 16) + acc * kPairQMax + c0 * 16;
+        drain.run(base, chunks, seg == 0, seg == p.segments - 1, out, p.out_stride, m0, p.M, n < p.N, [&] {
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(acc_empty_lead + 8u * acc);
+        });
+      }
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  __syncwarp();
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == 1 && lane == 0) drain_phase(mma_done, 0, p.wait_limit_ns);  // the pair's MMAs ran
+  __syncwarp();
+  cluster_sync();  // no CTA leaves while the other may still signal it
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
+                 : "memory");
 }
 
 // A row-major byte matrix [rows, cols] with rows `stride` apart as a 2-D tiled map with
@@ -309,10 +713,35 @@ bool make_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, in
 
 struct DeviceInfo {
   bool ready = false;
-  int sms = 0;
+  int sms = 0, pairs = 0;  // pairs: CTA pairs that fit at once
 };
 DeviceInfo g_info[64];
 std::mutex g_info_mu;
+
+using Kernel = void (*)(CUtensorMap, CUtensorMap, MatmulDev);
+Kernel kernel_of(bool pair, bool f32, bool multi) {
+  static constexpr Kernel all[2][2][2] = {
+      {{fp8_matmul_kernel<uint16_t, false>, fp8_matmul_kernel<uint16_t, true>},
+       {fp8_matmul_kernel<float, false>, fp8_matmul_kernel<float, true>}},
+      {{fp8_matmul_pair_kernel<uint16_t, false>, fp8_matmul_pair_kernel<uint16_t, true>},
+       {fp8_matmul_pair_kernel<float, false>, fp8_matmul_pair_kernel<float, true>}}};
+  return all[pair][f32][multi];
+}
+
+cudaLaunchConfig_t pair_config(int pairs, cudaLaunchAttribute *attr, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = 2;
+  attr->val.clusterDim.y = 1;
+  attr->val.clusterDim.z = 1;
+  cfg.gridDim = dim3(2 * pairs, 1, 1);
+  cfg.blockDim = dim3(kPairThreads, 1, 1);
+  cfg.dynamicSmemBytes = kPairSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
 
 cudaError_t device_info(DeviceInfo &out) {
   int dev = 0;
@@ -322,15 +751,21 @@ cudaError_t device_info(DeviceInfo &out) {
   DeviceInfo &d = g_info[dev & 63];
   if (!d.ready) {
     e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-    for (auto *k : {fp8_matmul_kernel<float>, fp8_matmul_kernel<uint16_t>})
-      if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    for (int i = 0; i < 8 && e == cudaSuccess; ++i)
+      e = cudaFuncSetAttribute(kernel_of(i & 4, i & 2, i & 1), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)(i & 4 ? kPairSmemBytes : kSmemBytes));
     if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = pair_config(d.sms / 2, &attr, 0);
+    if ((e = cudaOccupancyMaxActiveClusters(&d.pairs, kernel_of(true, true, false), &cfg)) != cudaSuccess)
+      return e;
     d.ready = true;
   }
   out = d;
   return cudaSuccess;
 }
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
@@ -349,21 +784,43 @@ cudaError_t launch_fp8_matmul(const MatmulParams &p, int out_dtype, cudaStream_t
   d.kblocks = (int32_t)((p.K + 127) / 128);
   d.a_shift = p.a_block == 1 ? 0 : 7;
   d.b_shift = p.b_block == 1 ? 0 : 7;
-  d.q_tile = (int32_t)(p.M < kQMax ? (p.M + 15) / 16 * 16 : kQMax);
-  d.stages = (int32_t)(kStageBudget / ((kP + d.q_tile) * 128));
-  if (d.stages > kMaxStages) d.stages = kMaxStages;
-  d.tiles_q = (p.M + d.q_tile - 1) / d.q_tile;
-  d.tiles = d.tiles_q * ((p.N + kP - 1) / kP);
   d.wait_limit_ns = wait_limit_ns();
+  const int64_t segments = ceil_div(d.kblocks, kSegmentBlocks);
+  d.seg_blocks = (int32_t)(ceil_div(ceil_div(d.kblocks, segments), 4) * 4);
+  d.segments = (int32_t)ceil_div(d.kblocks, d.seg_blocks);
+  // Pairs where their tiles occupy most of the SMs.
+  const bool pair = info.pairs > 0 && p.M > 128 && p.N > 128 &&
+                    ceil_div(p.N, 2 * kP) * ceil_div(p.M, kPairQMax) * 2 >= info.pairs;
+  if (pair) {
+    // The width of a tile along a: the one whose whole waves over the pairs take least (a
+    // wave lasts as long as its tile is wide, and a little).
+    d.tiles_p = ceil_div(p.N, 2 * kP);
+    int64_t best = INT64_MAX;
+    for (int qt = kPairQMax; qt >= 128; qt -= 16) {
+      const int64_t cost = ceil_div(d.tiles_p * ceil_div(p.M, qt), info.pairs) * (qt + 16);
+      if (cost < best) best = cost, d.q_tile = qt;
+    }
+    d.stages = (int32_t)(kPairStageBudget / ((kP + d.q_tile / 2) * 128));
+  } else {
+    d.tiles_p = ceil_div(p.N, kP);
+    d.q_tile = (int32_t)(p.M < kQMax ? ceil_div(p.M, 16) * 16 : kQMax);
+    d.stages = (int32_t)(kStageBudget / ((kP + d.q_tile) * 128));
+  }
+  if (d.stages > kMaxStages) d.stages = kMaxStages;
+  d.tiles_q = ceil_div(p.M, d.q_tile);
+  d.tiles = d.tiles_p * d.tiles_q;
   CUtensorMap map_a, map_b;
-  if (!make_map(&map_a, p.a, p.M, p.K, p.a_stride, (uint32_t)d.q_tile) ||
+  if (!make_map(&map_a, p.a, p.M, p.K, p.a_stride, (uint32_t)(pair ? d.q_tile / 2 : d.q_tile)) ||
       !make_map(&map_b, p.b, p.N, p.K, p.b_stride, kP))
     return cudaErrorInvalidValue;
+  const Kernel kernel = kernel_of(pair, out_dtype == ENGRAM_DTYPE_F32, d.segments > 1);
+  if (pair) {
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = pair_config((int)(d.tiles < info.pairs ? d.tiles : info.pairs), &attr, stream);
+    return cudaLaunchKernelEx(&cfg, kernel, map_a, map_b, d);
+  }
   const unsigned grid = (unsigned)(d.tiles < info.sms ? d.tiles : info.sms);
-  if (out_dtype == ENGRAM_DTYPE_F32)
-    fp8_matmul_kernel<float><<<grid, kThreads, kSmemBytes, stream>>>(map_a, map_b, d);
-  else
-    fp8_matmul_kernel<uint16_t><<<grid, kThreads, kSmemBytes, stream>>>(map_a, map_b, d);
+  kernel<<<grid, kThreads, kSmemBytes, stream>>>(map_a, map_b, d);
   return cudaGetLastError();
 }
 

@@ -191,7 +191,8 @@ def check_product(got, av, bv, bf16):
 MCASES = [(1, 1, 1), (1, 128, 128), (16, 16, 16), (7, 100, 130), (16, 4096, 6144), (1, 640, 2048),
           (33, 257, 1000), (64, 512, 512), (128, 128, 512), (129, 129, 129), (200, 1000, 640),
           (256, 256, 384), (300, 70, 4096), (1000, 1030, 1100), (2500, 2300, 300), (5, 9000, 256),
-          (9000, 5, 256), (512, 4096, 6144), (257, 2048, 8200)]
+          (9000, 5, 256), (512, 4096, 6144), (257, 2048, 8200),
+          (1601, 1600, 640), (4100, 1100, 9000), (1900, 2049, 8320), (20000, 260, 1500), (16411, 256, 16)]
 
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])
