@@ -180,16 +180,19 @@ def _check(code: int, what: str):
 
 
 def _ptr(t):
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    import torch
     if stream is None:
-        return C.c_void_p(torch.cuda.current_stream().cuda_stream)
+        import torch
+        try:  # the raw handle: a stream object costs several microseconds a call
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:
+            return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
-        return C.c_void_p(stream)
-    return C.c_void_p(stream.cuda_stream)
+        return stream
+    return stream.cuda_stream
 
 
 def _need(t, dtypes, name, contiguous=True):
@@ -638,59 +641,59 @@ def engram_forward_static(token_ids, tid2eid, n_eids: int, n_heads: int, tables:
     return streams_out
 
 
+_dtype_codes: dict = {}
+
+
 def _dtype(t, name):
     """The DTYPE_* of a bf16 (or bf16 bits) or fp32 CUDA tensor of any strides."""
-    import torch
-    _need(t, (torch.bfloat16, torch.int16, torch.float32), name, contiguous=False)
-    return DTYPE_F32 if t.dtype == torch.float32 else DTYPE_BF16
+    if not _dtype_codes:
+        import torch
+        _dtype_codes.update({torch.bfloat16: DTYPE_BF16, torch.int16: DTYPE_BF16,
+                             torch.float32: DTYPE_F32})
+    code = _dtype_codes.get(t.dtype)
+    if code is None or not t.is_cuda:
+        _need(t, tuple(_dtype_codes), name, contiguous=False)
+    return code
 
 
-def _unit(t, name):
-    """Refuses a tensor whose last dimension is not dense."""
-    if t.dim() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
+def _strides(t, name):
+    """The strides of a tensor whose last dimension is dense."""
+    st = t.stride()
+    if st and st[-1] != 1 and t.shape[-1] > 1:
         raise EngramError(ERR_INVALID_ARG, f"the last dimension of {name} must be contiguous")
+    return st
 
 
 def _ids_view(ids):
-    """ids [..., R] as (tokens, R, stride between tokens)."""
+    """ids [..., R] as (shape, tokens, R, stride between tokens)."""
     import torch
-    _need(ids, (torch.int32,), "ids", contiguous=False)
-    if ids.dim() == 0:
+    if ids.dtype != torch.int32 or not ids.is_cuda:
+        _need(ids, (torch.int32,), "ids", contiguous=False)
+    shape, st = ids.shape, _strides(ids, "ids")
+    if len(shape) == 2:
+        return shape, shape[0], shape[1], max(st[0], shape[1])
+    if not shape:
         raise EngramError(ERR_INVALID_ARG, "ids must have a dimension")
-    _unit(ids, "ids")
-    if ids.dim() == 2:
-        return ids.shape[0], ids.shape[1], max(ids.stride(0), ids.shape[1])
     if not ids.is_contiguous():
         raise EngramError(ERR_INVALID_ARG, "ids must be contiguous (or [tokens, ids] rows)")
-    R = ids.shape[-1] if ids.dim() > 1 else 1
-    return (ids.numel() // R if R else 0), R, R
+    R = shape[-1] if len(shape) > 1 else 1
+    return shape, (ids.numel() // R if R else 0), R, R
 
 
-def _rows_view(t, lead, D, name):
-    """t [*lead, D] as the strides (between tokens, between ids) of its rows; lead has
-    one or two dimensions once the leading ones are flattened."""
-    if tuple(t.shape) != (*lead, D):
-        raise EngramError(ERR_INVALID_ARG, f"{name} must be {[*lead, D]}")
-    _unit(t, name)
-    if len(lead) == 1:
-        return t.stride(0), 0
-    if len(lead) == 2:
-        return t.stride(0), t.stride(1)
+def _embed_rows(lead, t, D, pooled, name):
+    """The strides (between tokens, between ids) of the rows of an output or gradient tensor
+    that goes with ids of shape lead: [*lead, D], or [*lead[:-1], D] when pooled."""
+    want = (*lead[:-1], D) if pooled else (*lead, D)
+    if t.shape != want:
+        raise EngramError(ERR_INVALID_ARG, f"{name} must be {list(want)}")
+    st = _strides(t, name)
+    if len(want) == 2:
+        return (st[0], 0) if pooled else (st[0], D)
+    if len(want) == 3 and not pooled:
+        return st[0], st[1]
     if not t.is_contiguous():
         raise EngramError(ERR_INVALID_ARG, f"{name} must be contiguous beyond three dimensions")
-    return lead[-1] * D, D
-
-
-def _embed_rows(ids, t, D, pooled, name):
-    """The row strides of an output or gradient tensor that goes with ids: [*ids.shape,
-    D], or [*ids.shape[:-1], D] when pooled."""
-    lead = tuple(ids.shape[:-1]) if pooled else tuple(ids.shape)
-    if pooled and len(lead) > 1:
-        if tuple(t.shape) != (*lead, D) or not t.is_contiguous():
-            raise EngramError(ERR_INVALID_ARG, f"{name} must be contiguous {[*lead, D]}")
-        return D, 0
-    tok, per = _rows_view(t, lead, D, name)
-    return (tok, 0) if pooled else (tok, per if ids.dim() > 1 else D)
+    return (D, 0) if pooled else (lead[-1] * D, D)
 
 
 def engram_embed(ids, table, scale: float = 1.0, pooled: bool = False, out=None, out_dtype=None,
@@ -698,23 +701,22 @@ def engram_embed(ids, table, scale: float = 1.0, pooled: bool = False, out=None,
     """out[..., :] = scale * table[ids]: ids int32 [T] or [T, R] (any leading dimensions when
     contiguous; rows of a wider id tensor when 2-D), table bf16 or fp32 [rows, D].  pooled
     sums over the last dimension of ids: [*ids.shape[:-1], D].  -1 reads as zeros."""
-    import torch
     td = _dtype(table, "table")
     if table.dim() != 2:
         raise EngramError(ERR_INVALID_ARG, "table must be [rows, D]")
-    _unit(table, "table")
-    if pooled and ids.dim() < 2:
+    lead, T, R, ids_stride = _ids_view(ids)
+    if pooled and len(lead) < 2:
         raise EngramError(ERR_INVALID_ARG, "pooled ids must be [..., ids]")
-    T, R, ids_stride = _ids_view(ids)
     rows, D = table.shape
     if out is None:
-        out = torch.empty((*(ids.shape[:-1] if pooled else ids.shape), D),
-                          dtype=out_dtype or table.dtype, device=table.device)
+        import torch
+        out = torch.empty((*(lead[:-1] if pooled else lead), D), dtype=out_dtype or table.dtype,
+                          device=table.device)
     od = _dtype(out, "out")
-    tok, per = _embed_rows(ids, out, D, pooled, "out")
-    _check(lib.engram_embed(_ptr(ids), T, R, ids_stride, _ptr(table), td, rows, D,
-                            max(table.stride(0), D), float(scale), int(pooled), _ptr(out), od, tok,
-                            per, _ptr(status), _stream(stream)), "engram_embed")
+    tok, per = _embed_rows(lead, out, D, pooled, "out")
+    _check(lib.engram_embed(ids.data_ptr(), T, R, ids_stride, table.data_ptr(), td, rows, D,
+                            max(_strides(table, "table")[0], D), scale, pooled, out.data_ptr(), od,
+                            tok, per, _ptr(status), _stream(stream)), "engram_embed")
     return out
 
 
@@ -725,17 +727,17 @@ def engram_embed_grad_workspace_bytes(n_tokens: int, n_ids: int, D: int) -> int:
 def _grad_args(ids, dy, pooled, workspace):
     """The arguments the two gradient calls share, from ids and dy ([*ids.shape, D], or
     [*ids.shape[:-1], D] when pooled; expanded dimensions may have stride 0)."""
-    import torch
     dd = _dtype(dy, "dy")
-    if pooled and ids.dim() < 2:
+    lead, T, R, ids_stride = _ids_view(ids)
+    if pooled and len(lead) < 2:
         raise EngramError(ERR_INVALID_ARG, "pooled ids must be [..., ids]")
-    T, R, ids_stride = _ids_view(ids)
     D = dy.shape[-1] if dy.dim() else 0
-    tok, per = _embed_rows(ids, dy, D, pooled, "dy")
+    tok, per = _embed_rows(lead, dy, D, pooled, "dy")
     if workspace is None:
+        import torch
         workspace = torch.empty(max(engram_embed_grad_workspace_bytes(T, R, D), 16),
                                 dtype=torch.uint8, device=dy.device)
-    return D, T * R, (_ptr(ids), T, R, ids_stride, _ptr(dy), dd, tok, per), workspace
+    return D, T * R, (ids.data_ptr(), T, R, ids_stride, dy.data_ptr(), dd, tok, per), workspace
 
 
 def engram_embed_grad(ids, dy, rows: int, scale: float = 1.0, pooled: bool = False, grad=None,
@@ -743,19 +745,19 @@ def engram_embed_grad(ids, dy, rows: int, scale: float = 1.0, pooled: bool = Fal
                       stream=None):
     """The gradient of engram_embed(ids, table [rows, D], scale, pooled)'s table for the output
     gradient dy: [rows, D], every row written (accumulate: added to grad, fp32 or bf16)."""
-    import torch
     D, n, args, workspace = _grad_args(ids, dy, pooled, workspace)
     if grad is None:
         if accumulate:
             raise EngramError(ERR_INVALID_ARG, "accumulate needs a grad to add to")
+        import torch
         grad = torch.empty((rows, D), dtype=grad_dtype or torch.float32, device=dy.device)
     gd = _dtype(grad, "grad")
-    if tuple(grad.shape) != (rows, D):
+    if grad.shape != (rows, D):
         raise EngramError(ERR_INVALID_ARG, f"grad must be {[rows, D]}")
-    _unit(grad, "grad")
-    _check(lib.engram_embed_grad(*args, rows, D, float(scale), int(accumulate), _ptr(grad), gd,
-                                 max(grad.stride(0), D), _ptr(workspace), workspace.numel(),
-                                 _ptr(status), _stream(stream)), "engram_embed_grad")
+    _check(lib.engram_embed_grad(*args, rows, D, scale, accumulate, grad.data_ptr(), gd,
+                                 max(_strides(grad, "grad")[0], D), workspace.data_ptr(),
+                                 workspace.numel(), _ptr(status), _stream(stream)),
+           "engram_embed_grad")
     return grad
 
 
@@ -776,36 +778,39 @@ def engram_embed_grad_rows(ids, dy, rows: int, scale: float = 1.0, pooled: bool 
     _need(row_ids, (torch.int32,), "row_ids")
     _need(count, (torch.int32,), "count")
     gd = _dtype(grads, "grads")
-    if row_ids.numel() != n or tuple(grads.shape) != (n, D) or count.numel() != 1:
+    if row_ids.numel() != n or grads.shape != (n, D) or count.numel() != 1:
         raise EngramError(ERR_INVALID_ARG, "row_ids / grads / count sizes disagree with ids")
-    _unit(grads, "grads")
-    _check(lib.engram_embed_grad_rows(*args, rows, D, float(scale), _ptr(row_ids), _ptr(grads), gd,
-                                      max(grads.stride(0), D), _ptr(count), _ptr(workspace),
-                                      workspace.numel(), _ptr(status), _stream(stream)),
-           "engram_embed_grad_rows")
+    _check(lib.engram_embed_grad_rows(*args, rows, D, scale, row_ids.data_ptr(), grads.data_ptr(),
+                                      gd, max(_strides(grads, "grads")[0], D), count.data_ptr(),
+                                      workspace.data_ptr(), workspace.numel(), _ptr(status),
+                                      _stream(stream)), "engram_embed_grad_rows")
     return row_ids, grads, count
 
 
 def fp8_empty(rows: int, cols: int, device):
-    """An uninitialised uint8 [rows, cols] operand: rows a multiple of 16 bytes apart."""
+    """An uninitialised uint8 [rows, cols] operand: rows a multiple of 16 bytes apart (of 128
+    where they are long: the product reads them in 128-byte pieces)."""
     import torch
-    return torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.uint8, device=device)[:, :cols]
+    step = 128 if cols > 512 else 16
+    return torch.empty((rows, (cols + step - 1) // step * step), dtype=torch.uint8,
+                       device=device)[:, :cols]
 
 
 def _fp8_operand(t, name):
+    """(rows, columns, stride) of a uint8 operand."""
     import torch
-    _need(t, (torch.uint8,), name, contiguous=False)
+    if t.dtype != torch.uint8 or not t.is_cuda:
+        _need(t, (torch.uint8,), name, contiguous=False)
     if t.dim() != 2:
         raise EngramError(ERR_INVALID_ARG, f"{name} must be two-dimensional")
-    _unit(t, name)
-    return t.stride(0)
+    return *t.shape, _strides(t, name)[0]
 
 
 def _fp8_scales(t, rows, cols, block, name):
     import torch
-    _need(t, (torch.uint8,), name)
     want = (-(-rows // block), -(-cols // FP8_BLOCK))
-    if tuple(t.shape) != want:
+    _need(t, (torch.uint8,), name)
+    if t.shape != want:
         raise EngramError(ERR_INVALID_ARG, f"{name} must be {list(want)}")
 
 
@@ -816,16 +821,15 @@ def engram_fp8_quantise(x, block_rows: int = 1, rows: bool = True, cols: bool = 
     ceil(M/128)]), the transposed copy with blocks along M.  block_rows FP8_BLOCK: 128 x 128
     tiles share a scale.  Returns the copies asked for, in that order; out gives their
     buffers (rows a multiple of 16 bytes apart: fp8_empty)."""
-    import torch
     xd = _dtype(x, "x")
     if x.dim() != 2:
         raise EngramError(ERR_INVALID_ARG, "x must be [M, K]")
-    _unit(x, "x")
     if block_rows not in (1, FP8_BLOCK):
         raise EngramError(ERR_INVALID_ARG, f"block_rows must be 1 or {FP8_BLOCK}")
     M, K = x.shape
     dims = ([(M, K)] if rows else []) + ([(K, M)] if cols else [])
     if out is None:
+        import torch
         out = []
         for r, c in dims:
             out += [fp8_empty(r, c, x.device),
@@ -835,16 +839,17 @@ def engram_fp8_quantise(x, block_rows: int = 1, rows: bool = True, cols: bool = 
         raise EngramError(ERR_INVALID_ARG, "out must hold a value and a scale buffer per copy")
     args = []
     for i, (r, c) in enumerate(dims):
-        stride = _fp8_operand(out[2 * i], "q")
-        if tuple(out[2 * i].shape) != (r, c):
+        q, s = out[2 * i], out[2 * i + 1]
+        qr, qc, stride = _fp8_operand(q, "q")
+        if qr != r or qc != c:
             raise EngramError(ERR_INVALID_ARG, f"q must be {[r, c]}")
-        _fp8_scales(out[2 * i + 1], r, c, block_rows, "scales")
-        args.append((_ptr(out[2 * i]), stride, _ptr(out[2 * i + 1])))
+        _fp8_scales(s, r, c, block_rows, "scales")
+        args.append((q.data_ptr(), stride, s.data_ptr()))
     none = (None, 0, None)
     q = args[0] if rows else none
     qt = args[-1] if cols else none
-    _check(lib.engram_fp8_quantise(_ptr(x), xd, M, K, max(x.stride(0), K), block_rows, *q, *qt,
-                                   _stream(stream)), "engram_fp8_quantise")
+    _check(lib.engram_fp8_quantise(x.data_ptr(), xd, M, K, max(_strides(x, "x")[0], K), block_rows,
+                                   *q, *qt, _stream(stream)), "engram_fp8_quantise")
     return tuple(out)
 
 
@@ -853,24 +858,23 @@ def engram_fp8_matmul(a, a_scale, b, b_scale, a_block: int = 1, b_block: int = 1
     """out[m, n] = sum_k a[m, k] b[n, k]: a uint8 [M, K] and b uint8 [N, K] with their scale
     bytes, as engram_fp8_quantise returns them (a_block / b_block: FP8_BLOCK where 128 x 128
     tiles share a scale).  out: fp32 (default) or bf16 [M, N]."""
-    import torch
-    sa, sb = _fp8_operand(a, "a"), _fp8_operand(b, "b")
-    (M, K), N = a.shape, b.shape[0]
-    if b.shape[1] != K:
+    (M, K, sa), (N, kb, sb) = _fp8_operand(a, "a"), _fp8_operand(b, "b")
+    if kb != K:
         raise EngramError(ERR_INVALID_ARG, "a and b disagree on K")
     if a_block not in (1, FP8_BLOCK) or b_block not in (1, FP8_BLOCK):
         raise EngramError(ERR_INVALID_ARG, f"a_block and b_block must be 1 or {FP8_BLOCK}")
     _fp8_scales(a_scale, M, K, a_block, "a_scale")
     _fp8_scales(b_scale, N, K, b_block, "b_scale")
     if out is None:
+        import torch
         out = torch.empty((M, N), dtype=out_dtype or torch.float32, device=a.device)
     od = _dtype(out, "out")
-    if tuple(out.shape) != (M, N):
+    if out.shape != (M, N):
         raise EngramError(ERR_INVALID_ARG, f"out must be {[M, N]}")
-    _unit(out, "out")
-    _check(lib.engram_fp8_matmul(_ptr(a), sa, _ptr(a_scale), a_block, _ptr(b), sb, _ptr(b_scale),
-                                 b_block, M, N, K, _ptr(out), od, max(out.stride(0), N),
-                                 _ptr(status), _stream(stream)), "engram_fp8_matmul")
+    _check(lib.engram_fp8_matmul(a.data_ptr(), sa, a_scale.data_ptr(), a_block, b.data_ptr(), sb,
+                                 b_scale.data_ptr(), b_block, M, N, K, out.data_ptr(), od,
+                                 max(_strides(out, "out")[0], N), _ptr(status), _stream(stream)),
+           "engram_fp8_matmul")
     return out
 
 

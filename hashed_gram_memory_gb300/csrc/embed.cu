@@ -6,6 +6,7 @@
 // alignments), four outputs at a time, their loads issued together so that a warp
 // keeps 2 KB in flight; neighbouring lanes read neighbouring columns.  A pooled
 // output loops over the token's ids in order, four rows in flight, in fp32.
+#include "launch.cuh"
 #include "lookup_common.cuh"
 #include "train_internal.cuh"
 
@@ -86,6 +87,7 @@ __device__ __forceinline__ void store_float(T *dst, const float (&f)[V]) {
 template <typename TI, typename TO, int V, int U, bool POOLED>
 __global__ void __launch_bounds__(kThreads)
     embed_kernel(const __grid_constant__ EmbedParams p, int32_t chunks, uint32_t magic) {
+  dependency_wait();
   const int64_t base = (int64_t)blockIdx.x * (kThreads * U);
   const int64_t row0 = base / chunks;
   const uint32_t rem0 = (uint32_t)(base - row0 * chunks);
@@ -178,15 +180,15 @@ cudaError_t launch_sized(const EmbedParams &p, cudaStream_t stream) {
   const int64_t items = n_rows * chunks;
   // Few items, or pooled ones (which loop over their ids): one a thread.
   if (POOLED || items <= 152 * 4 * kThreads) {
-    embed_kernel<TI, TO, V, 1, POOLED>
-        <<<(unsigned)((items + kThreads - 1) / kThreads), kThreads, 0, stream>>>(p, chunks, magic);
-  } else if constexpr (!POOLED) {
-    constexpr int U = 4;
-    embed_kernel<TI, TO, V, U, POOLED>
-        <<<(unsigned)((items + kThreads * U - 1) / (kThreads * U)), kThreads, 0, stream>>>(p, chunks,
-                                                                                        magic);
+    return launch(embed_kernel<TI, TO, V, 1, POOLED>, (items + kThreads - 1) / kThreads, kThreads, 0, stream, 1,
+                  p, chunks, magic);
   }
-  return cudaGetLastError();
+  if constexpr (!POOLED) {
+    constexpr int U = 4;
+    return launch(embed_kernel<TI, TO, V, U, POOLED>, (items + kThreads * U - 1) / (kThreads * U), kThreads, 0,
+                  stream, 1, p, chunks, magic);
+  }
+  return cudaErrorInvalidValue;  // not reached
 }
 
 template <typename TI, typename TO>

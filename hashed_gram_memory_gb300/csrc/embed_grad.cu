@@ -18,6 +18,7 @@
 //
 // HBM-bound: dy read once (scattered whole rows), each output row written once; the sort's
 // lists stay in L2.
+#include "launch.cuh"
 #include "lookup_common.cuh"
 #include "train_internal.cuh"
 
@@ -106,6 +107,7 @@ __global__ void __launch_bounds__(kSortThreads)
   __shared__ uint16_t s_pos[kTile];
   __shared__ uint32_t s_cnt[kSortWarps][256];
   __shared__ uint32_t s_start[256];
+  dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = (int)p.n;
   uint32_t key[kPer], pos[kPer], place[kPer];
@@ -176,6 +178,7 @@ __global__ void __launch_bounds__(kSortThreads)
     count_digits_kernel(const __grid_constant__ EmbedGradParams p, const uint32_t *__restrict__ keys,
                         int shift) {
   __shared__ uint32_t s_cnt[256];
+  dependency_wait();
   const int tid = threadIdx.x;
   const uint32_t mask = (1u << p.digit_bits) - 1;
   if (tid < 256) s_cnt[tid] = 0;
@@ -200,6 +203,7 @@ __global__ void __launch_bounds__(kSortThreads)
 __global__ void __launch_bounds__(256) scan_digits_kernel(uint32_t *counts, int64_t tiles,
                                                           uint32_t *totals) {
   __shared__ uint32_t s_sum[8];
+  dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t *c = counts + blockIdx.x * tiles;
   uint32_t carry = 0;
@@ -235,6 +239,7 @@ __global__ void __launch_bounds__(kSortThreads)
   __shared__ uint32_t s_cnt[kSortWarps][256];
   __shared__ uint32_t s_start[256];
   __shared__ uint32_t s_sum[8];
+  dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t mask = (1u << p.digit_bits) - 1;
   const int64_t base = (int64_t)blockIdx.x * kTile;
@@ -289,6 +294,7 @@ __global__ void __launch_bounds__(kSortThreads)
 
 // Runs that start in each chunk, a warp a chunk.
 __global__ void __launch_bounds__(256) count_runs_kernel(const __grid_constant__ EmbedGradParams p) {
+  dependency_wait();
   const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (c >= p.chunks) return;
@@ -305,6 +311,7 @@ __global__ void __launch_bounds__(256) count_runs_kernel(const __grid_constant__
 // run_base becomes its exclusive prefix sums; the number of runs goes behind it.
 __global__ void __launch_bounds__(1024) scan_runs_kernel(const __grid_constant__ EmbedGradParams p) {
   __shared__ uint32_t s_sum[32];
+  dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t carry = 0;
   for (int64_t i0 = 0; i0 < p.chunks; i0 += 1024 * 8) {
@@ -541,6 +548,7 @@ __device__ __forceinline__ void zero_rows(const EmbedGradParams &p, int64_t r0) 
 
 template <typename TY, typename TG, int V, int U>
 __global__ void __launch_bounds__(kSumThreads) sum_runs_kernel(const __grid_constant__ EmbedGradParams p) {
+  dependency_wait();
   if ((int64_t)blockIdx.x >= p.sum_blocks) {  // the zeroing blocks
     const int64_t w = (blockIdx.x - p.sum_blocks) * (kSumThreads / 32) + (threadIdx.x >> 5);
     if (w * 32 < p.rows) zero_rows<TG, V>(p, w * 32);
@@ -560,6 +568,7 @@ template <typename TG, int V>
 __global__ void __launch_bounds__(kJoinThreads) join_runs_kernel(const __grid_constant__ EmbedGradParams p) {
   extern __shared__ float s_part[];  // [groups a block][lanes a group * V]
   __shared__ int64_t s_parts[kJoinThreads];
+  dependency_wait();
   const int G = p.group, groups = kJoinThreads / G;
   const int slot = threadIdx.x / G, in = threadIdx.x & (G - 1);
   const Item it = item_of(p, (int64_t)blockIdx.x * groups + slot, in, V);
@@ -701,14 +710,13 @@ cudaError_t launch_sums(EmbedGradParams p, cudaStream_t stream) {
   const int64_t zero_blocks =
       p.run_base || p.accumulate ? 0 : (p.rows + kSumThreads - 1) / kSumThreads;  // a row a lane
   if (p.sum_blocks + zero_blocks > INT32_MAX) return cudaErrorInvalidValue;
+  cudaError_t e = cudaSuccess;
   if (p.sum_blocks + zero_blocks > 0)
-    sum_runs_kernel<TY, TG, V, U><<<(unsigned)(p.sum_blocks + zero_blocks), kSumThreads, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+    e = launch(sum_runs_kernel<TY, TG, V, U>, p.sum_blocks + zero_blocks, kSumThreads, 0, stream, 1, p);
   if (e != cudaSuccess || p.chunks < 2) return e;
   const int per = kJoinThreads / p.group;
-  join_runs_kernel<TG, V><<<(unsigned)((groups + per - 1) / per), kJoinThreads,
-                            kJoinThreads * V * sizeof(float), stream>>>(p);
-  return cudaGetLastError();
+  return launch(join_runs_kernel<TG, V>, (groups + per - 1) / per, kJoinThreads,
+                kJoinThreads * V * sizeof(float), stream, 1, p);
 }
 
 template <typename TY, typename TG>
@@ -758,29 +766,25 @@ cudaError_t launch_embed_grad(EmbedGradParams p, int dy_dtype, int grad_dtype, v
   if (p.n == 0) {
     if (sparse) return cudaMemsetAsync(p.count_out, 0, 4, stream);
   } else if (p.n <= kTile) {
-    sort_small_kernel<<<1, kSortThreads, 0, stream>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch(sort_small_kernel, 1, kSortThreads, 0, stream, 1, p)) != cudaSuccess) return e;
   } else {
-    const unsigned tiles = (unsigned)p.tiles;
-    for (int pass = 0; pass < p.passes; ++pass) {
+    for (int pass = 0; pass < p.passes && e == cudaSuccess; ++pass) {
       const int shift = pass * p.digit_bits, in = pass & 1 ^ 1, out = pass & 1;
-      if (pass == 0)
-        count_digits_kernel<true><<<tiles, kSortThreads, 0, stream>>>(p, nullptr, shift);
-      else
-        count_digits_kernel<false><<<tiles, kSortThreads, 0, stream>>>(p, keys[in], shift);
-      scan_digits_kernel<<<1u << p.digit_bits, 256, 0, stream>>>(p.counts, p.tiles, p.totals);
-      if (pass == 0)
-        scatter_kernel<true><<<tiles, kSortThreads, 0, stream>>>(p, nullptr, nullptr, keys[out], pos[out], shift);
-      else
-        scatter_kernel<false><<<tiles, kSortThreads, 0, stream>>>(p, keys[in], pos[in], keys[out], pos[out], shift);
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      e = launch(pass == 0 ? count_digits_kernel<true> : count_digits_kernel<false>, p.tiles, kSortThreads, 0,
+                 stream, 1, p, keys[in], shift);
+      if (e == cudaSuccess)
+        e = launch(scan_digits_kernel, 1 << p.digit_bits, 256, 0, stream, 1, p.counts, p.tiles, p.totals);
+      if (e == cudaSuccess)
+        e = launch(pass == 0 ? scatter_kernel<true> : scatter_kernel<false>, p.tiles, kSortThreads, 0, stream, 1,
+                   p, keys[in], pos[in], keys[out], pos[out], shift);
     }
+    if (e != cudaSuccess) return e;
     p.keys = keys[(p.passes - 1) & 1];
     p.pos = pos[(p.passes - 1) & 1];
     if (sparse) {
-      count_runs_kernel<<<(unsigned)((p.chunks + 7) / 8), 256, 0, stream>>>(p);
-      scan_runs_kernel<<<1, 1024, 0, stream>>>(p);
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      e = launch(count_runs_kernel, (p.chunks + 7) / 8, 256, 0, stream, 1, p);
+      if (e == cudaSuccess) e = launch(scan_runs_kernel, 1, 1024, 0, stream, 1, p);
+      if (e != cudaSuccess) return e;
     }
   }
   if (dy_dtype == ENGRAM_DTYPE_F32)

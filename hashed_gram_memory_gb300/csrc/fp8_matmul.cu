@@ -20,7 +20,9 @@
 //     a.  240, not 256: two whole accumulators and the scales then fit the 512 columns, and
 //     a tile's MMAs follow the last one's without waiting for the epilogue;
 //   fp8_matmul_kernel: one CTA per SM, 128 x up to 128 tiles, for products too small to
-//     fill the pairs.
+//     fill the pairs; where even those leave SMs idle (a few rows of a: reading b is the
+//     work), the CTAs of a cluster share a tile, each with a part of K, and add their
+//     parts through distributed shared memory in rank order.
 // Warps:
 //   0     TMA producer: a ring of stages, each a 128-byte slice along K of the tile's rows
 //         of a and b (128-byte swizzle);
@@ -33,6 +35,7 @@
 // leaves the tiles not yet stored unwritten.
 #include <mutex>
 
+#include "launch.cuh"
 #include "lookup_common.cuh"
 #include "tensor_core.cuh"
 #include "train_internal.cuh"
@@ -47,7 +50,7 @@ constexpr int kSegmentBlocks = 64;
 constexpr int kScaleSlots = 2;                        // of 16 blocks of K: four groups of four
 constexpr uint32_t kGroupBytes = (kP + kQMax) * 4;
 constexpr uint32_t kSlotBytes = 4 * kGroupBytes;
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 12;
 constexpr uint32_t kStageBudget = 192 * 1024;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kScaleCol = 2 * kQMax;  // scale words: two buffers of 4 (b) + 4 (a) columns
@@ -61,6 +64,7 @@ struct MatmulDev {
   int32_t kblocks, a_shift, b_shift;  // log2 of the rows sharing a scale (0 or 7)
   int32_t q_tile, stages;
   int32_t segments, seg_blocks;  // K in segments of seg_blocks blocks (a multiple of 4)
+  int32_t splits;                // CTAs that share a tile's K (a cluster)
   int64_t tiles_p, tiles_q, tiles;
   int64_t wait_limit_ns;
 };
@@ -91,6 +95,12 @@ __device__ __forceinline__ void umma_fp8(uint32_t d, uint64_t p_desc, uint64_t q
       "[%5], p;\n\t}" ::"r"(d),
       "l"(p_desc), "l"(q_desc), "r"(idesc), "r"(sp), "r"(sq), "r"(accumulate)
       : "memory");
+}
+
+__device__ __forceinline__ uint32_t load_cluster(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
 }
 
 // The whole warp waits; the same answer in every lane.
@@ -221,7 +231,7 @@ struct Drain {
   }
 };
 
-template <typename TO, bool MULTI>
+template <typename TO, bool MULTI, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                       const __grid_constant__ MatmulDev p) {
@@ -239,8 +249,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kblocks = p.kblocks, stages = p.stages, qt = p.q_tile;
+  const int stages = p.stages, qt = p.q_tile;
   const uint32_t stage_bytes = (uint32_t)(kP + qt) * 128;
+  // This CTA's blocks of K (from kb_first on) and its tiles.
+  const int rank = SPLIT ? (int)cluster_rank() : 0;
+  const int kb_first = SPLIT ? p.kblocks * rank / p.splits : 0;
+  const int kblocks = SPLIT ? p.kblocks * (rank + 1) / p.splits - kb_first : p.kblocks;
+  const int64_t first_tile = SPLIT ? blockIdx.x / p.splits : blockIdx.x;
+  const int64_t tile_step = SPLIT ? gridDim.x / p.splits : gridDim.x;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
@@ -270,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *tmem_slot;
+  dependency_wait();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -278,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int64_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) {
+      for (int64_t tile = first_tile; ok && tile < p.tiles; tile += tile_step) {
         int64_t tp, tq;
         tile_at(p, tile, tp, tq);
         const int p0 = (int)(tp * kP), q0 = (int)(tq * qt);
@@ -286,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = wait_phase(empty + s, ph ^ 1, abort_flag, p.wait_limit_ns, p.status))) break;
           uint8_t *st = sm + s * stage_bytes;
           mbar_arrive_expect_tx(full + s, stage_bytes);
-          tma_load_2d(st, &map_b, kb * 128, p0, full + s);
-          tma_load_2d(st + kP * 128, &map_a, kb * 128, q0, full + s);
+          tma_load_2d(st, &map_b, (kb_first + kb) * 128, p0, full + s);
+          tma_load_2d(st + kP * 128, &map_a, (kb_first + kb) * 128, q0, full + s);
           if (++s == stages) s = 0, ph ^= 1;
         }
       }
@@ -304,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ph = 0;
     bool ok = true;
     const bool one = elect_one();
-    for (int64_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) {
+    for (int64_t tile = first_tile; ok && tile < p.tiles; tile += tile_step) {
       for (int kb0 = 0; ok && kb0 < kblocks; kb0 += p.seg_blocks, ++unit) {
         const int kb1 = min(kb0 + p.seg_blocks, kblocks);
         const uint32_t acc = unit & 1, use = unit >> 1;
@@ -362,16 +379,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       p0 *= kP, q0 *= qt;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        w[i].load(p.b_scale, p0 + 32 * i + lane, p.N, p.b_shift, kb, kblocks);
-        w[4 + i].load(p.a_scale, q0 + 32 * i + lane, 32 * i < qt ? p.M : 0, p.a_shift, kb, kblocks);
+        w[i].load(p.b_scale, p0 + 32 * i + lane, p.N, p.b_shift, kb_first + kb, p.kblocks);
+        w[4 + i].load(p.a_scale, q0 + 32 * i + lane, 32 * i < qt ? p.M : 0, p.a_shift, kb_first + kb,
+                      p.kblocks);
       }
     };
     Scales w[8];
-    int64_t tile = blockIdx.x;
+    int64_t tile = first_tile;
     int kb = 0;
     load(tile, kb, w);
     while (ok && tile < p.tiles) {
-      const int64_t next_tile = kb + 16 < kblocks ? tile : tile + gridDim.x;
+      const int64_t next_tile = kb + 16 < kblocks ? tile : tile + tile_step;
       const int next_kb = kb + 16 < kblocks ? kb + 16 : 0;
       Scales next[8];
       load(next_tile, next_kb, next);
@@ -397,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t unit = 0;
     bool ok = true;
     Drain<TO, kQMax / 16, MULTI> drain;
-    for (int64_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) {
+    for (int64_t tile = first_tile; ok && tile < p.tiles; tile += tile_step) {
       int64_t tp, tq;
       tile_at(p, tile, tp, tq);
       const int64_t n = tp * kP + quad * 32 + lane, m0 = tq * qt;
@@ -408,6 +426,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t base = tmem + ((uint32_t)(quad * 32) << 16) + acc * kQMax;
+        if constexpr (SPLIT) {
+          // The partial tile into shared memory (the stages: every MMA has read them).
+          float *part = reinterpret_cast<float *>(sm) + quad * 32 + lane;
+          for (int c = 0; c < qt; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(base + c, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) part[(c + i) * kP] = __uint_as_float(v[i]);
+          }
+          break;
+        }
         drain.run(base, qt / 16, seg == 0, seg == p.segments - 1, out, p.out_stride, m0, p.M, n < p.N, [&] {
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
           __syncwarp();
@@ -415,6 +444,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         });
       }
     }
+  }
+
+  if constexpr (SPLIT) {
+    // Each CTA adds a share of the tile's columns over the cluster, in rank order.
+    __syncwarp();
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    cluster_sync();
+    bool ok = true;
+    for (int r = 0; r < p.splits; ++r)  // a CTA that gave up has no partial tile
+      ok &= load_cluster(map_to_rank(smem_u32(const_cast<int *>(abort_flag)), r)) == 0;
+    int64_t tp, tq;
+    tile_at(p, first_tile, tp, tq);
+    const int64_t n = tp * kP + (threadIdx.x & (kP - 1));
+    const int q_end = qt * (rank + 1) / p.splits;
+    for (int q = qt * rank / p.splits + threadIdx.x / kP; q < q_end; q += kThreads / kP) {
+      const int64_t m = tq * qt + q;
+      const uint32_t at = smem_u32(sm) + (q * kP + (threadIdx.x & (kP - 1))) * 4;
+      float sum = 0.f;
+      for (int r = 0; r < p.splits; ++r) sum += __uint_as_float(load_cluster(map_to_rank(at, r)));
+      if (ok && n < p.N && m < p.M)
+        store_out(static_cast<TO *>(p.out) + m * p.out_stride + n, __float_as_uint(sum));
+    }
+    cluster_sync();  // no CTA leaves while another may still read its part
   }
 
   // ---------------------------------------------------------------- teardown
@@ -511,6 +563,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   cluster_sync();  // both CTAs' barriers are initialised before either uses the other's
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *tmem_slot;
+  dependency_wait();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -719,28 +772,15 @@ DeviceInfo g_info[64];
 std::mutex g_info_mu;
 
 using Kernel = void (*)(CUtensorMap, CUtensorMap, MatmulDev);
-Kernel kernel_of(bool pair, bool f32, bool multi) {
-  static constexpr Kernel all[2][2][2] = {
-      {{fp8_matmul_kernel<uint16_t, false>, fp8_matmul_kernel<uint16_t, true>},
-       {fp8_matmul_kernel<float, false>, fp8_matmul_kernel<float, true>}},
-      {{fp8_matmul_pair_kernel<uint16_t, false>, fp8_matmul_pair_kernel<uint16_t, true>},
-       {fp8_matmul_pair_kernel<float, false>, fp8_matmul_pair_kernel<float, true>}}};
-  return all[pair][f32][multi];
-}
-
-cudaLaunchConfig_t pair_config(int pairs, cudaLaunchAttribute *attr, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  attr->id = cudaLaunchAttributeClusterDimension;
-  attr->val.clusterDim.x = 2;
-  attr->val.clusterDim.y = 1;
-  attr->val.clusterDim.z = 1;
-  cfg.gridDim = dim3(2 * pairs, 1, 1);
-  cfg.blockDim = dim3(kPairThreads, 1, 1);
-  cfg.dynamicSmemBytes = kPairSmemBytes;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cfg;
+enum Form { kSingle, kSingleMulti, kSplit, kPair, kPairMulti, kForms };
+Kernel kernel_of(int form, bool f32) {
+  static constexpr Kernel all[kForms][2] = {
+      {fp8_matmul_kernel<uint16_t, false, false>, fp8_matmul_kernel<float, false, false>},
+      {fp8_matmul_kernel<uint16_t, true, false>, fp8_matmul_kernel<float, true, false>},
+      {fp8_matmul_kernel<uint16_t, false, true>, fp8_matmul_kernel<float, false, true>},
+      {fp8_matmul_pair_kernel<uint16_t, false>, fp8_matmul_pair_kernel<float, false>},
+      {fp8_matmul_pair_kernel<uint16_t, true>, fp8_matmul_pair_kernel<float, true>}};
+  return all[form][f32];
 }
 
 cudaError_t device_info(DeviceInfo &out) {
@@ -751,14 +791,22 @@ cudaError_t device_info(DeviceInfo &out) {
   DeviceInfo &d = g_info[dev & 63];
   if (!d.ready) {
     e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-    for (int i = 0; i < 8 && e == cudaSuccess; ++i)
-      e = cudaFuncSetAttribute(kernel_of(i & 4, i & 2, i & 1), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)(i & 4 ? kPairSmemBytes : kSmemBytes));
+    for (int i = 0; i < 2 * kForms && e == cudaSuccess; ++i)
+      e = cudaFuncSetAttribute(kernel_of(i / 2, i & 1), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)(i / 2 >= kPair ? kPairSmemBytes : kSmemBytes));
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = pair_config(d.sms / 2, &attr, 0);
-    if ((e = cudaOccupancyMaxActiveClusters(&d.pairs, kernel_of(true, true, false), &cfg)) != cudaSuccess)
-      return e;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(d.sms / 2 * 2, 1, 1);
+    cfg.blockDim = dim3(kPairThreads, 1, 1);
+    cfg.dynamicSmemBytes = kPairSmemBytes;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaOccupancyMaxActiveClusters(&d.pairs, kernel_of(kPair, true), &cfg)) != cudaSuccess) return e;
     d.ready = true;
   }
   out = d;
@@ -791,6 +839,7 @@ cudaError_t launch_fp8_matmul(const MatmulParams &p, int out_dtype, cudaStream_t
   // Pairs where their tiles occupy most of the SMs.
   const bool pair = info.pairs > 0 && p.M > 128 && p.N > 128 &&
                     ceil_div(p.N, 2 * kP) * ceil_div(p.M, kPairQMax) * 2 >= info.pairs;
+  d.splits = 1;
   if (pair) {
     // The width of a tile along a: the one whose whole waves over the pairs take least (a
     // wave lasts as long as its tile is wide, and a little).
@@ -809,19 +858,29 @@ cudaError_t launch_fp8_matmul(const MatmulParams &p, int out_dtype, cudaStream_t
   if (d.stages > kMaxStages) d.stages = kMaxStages;
   d.tiles_q = ceil_div(p.M, d.q_tile);
   d.tiles = d.tiles_p * d.tiles_q;
+  int form = pair ? (d.segments > 1 ? kPairMulti : kPair) : (d.segments > 1 ? kSingleMulti : kSingle);
+  if (!pair) {
+    // Clusters that share K while there are SMs for them and each CTA keeps two blocks.
+    int64_t splits = info.sms / d.tiles;
+    splits = splits > 8 ? 8 : splits;
+    splits = splits > d.kblocks / 2 ? d.kblocks / 2 : splits;
+    if (splits > 1 && ceil_div(d.kblocks, splits) <= kSegmentBlocks) {
+      d.splits = (int32_t)splits;
+      form = kSplit;
+    }
+  }
   CUtensorMap map_a, map_b;
   if (!make_map(&map_a, p.a, p.M, p.K, p.a_stride, (uint32_t)(pair ? d.q_tile / 2 : d.q_tile)) ||
       !make_map(&map_b, p.b, p.N, p.K, p.b_stride, kP))
     return cudaErrorInvalidValue;
-  const Kernel kernel = kernel_of(pair, out_dtype == ENGRAM_DTYPE_F32, d.segments > 1);
-  if (pair) {
-    cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = pair_config((int)(d.tiles < info.pairs ? d.tiles : info.pairs), &attr, stream);
-    return cudaLaunchKernelEx(&cfg, kernel, map_a, map_b, d);
-  }
-  const unsigned grid = (unsigned)(d.tiles < info.sms ? d.tiles : info.sms);
-  kernel<<<grid, kThreads, kSmemBytes, stream>>>(map_a, map_b, d);
-  return cudaGetLastError();
+  const Kernel kernel = kernel_of(form, out_dtype == ENGRAM_DTYPE_F32);
+  if (pair)
+    return launch(kernel, 2 * (d.tiles < info.pairs ? d.tiles : info.pairs), kPairThreads, kPairSmemBytes,
+                  stream, 2, map_a, map_b, d);
+  if (form == kSplit)
+    return launch(kernel, d.tiles * d.splits, kThreads, kSmemBytes, stream, d.splits, map_a, map_b, d);
+  return launch(kernel, d.tiles < info.sms ? d.tiles : info.sms, kThreads, kSmemBytes, stream, 1, map_a,
+                map_b, d);
 }
 
 }  // namespace engram

@@ -19,6 +19,7 @@
 //     column) so that both copies leave as whole 128-byte lines.
 #include <cuda_fp8.h>
 
+#include "launch.cuh"
 #include "lookup_common.cuh"
 #include "train_internal.cuh"
 
@@ -87,6 +88,7 @@ constexpr int kRowsThreads = 256;
 template <typename T, bool VEC, int U>
 __global__ void __launch_bounds__(kRowsThreads)
     quantise_rows_kernel(const __grid_constant__ QuantiseParams p, int32_t kblocks) {
+  dependency_wait();
   const int64_t n = p.M * kblocks;
   const int in = threadIdx.x & 15;
   const int64_t first = (int64_t)blockIdx.x * (kRowsThreads / 16 * U) + (threadIdx.x >> 4);
@@ -130,6 +132,7 @@ __global__ void __launch_bounds__(256, 2)
     quantise_tile_kernel(const __grid_constant__ QuantiseParams p, int32_t kblocks, int32_t mblocks) {
   __shared__ uint4 s_turn[128 * 8];
   __shared__ uint4 s_max[8][32];  // [warp][lane]: the maxima of four columns
+  dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t mb = blockIdx.x / kblocks, kb = blockIdx.x - mb * kblocks;
   const int64_t m0 = mb * 128 + warp * 16, k0 = kb * 128 + lane * 4;
@@ -246,27 +249,26 @@ cudaError_t launch_typed(const QuantiseParams &p, cudaStream_t stream) {
     const int64_t n = p.M * kblocks;
     constexpr int kPer = kRowsThreads / 16;
     if (n <= 152 * 8 * kPer) {
-      const unsigned grid = (unsigned)((n + kPer - 1) / kPer);
+      const int64_t grid = (n + kPer - 1) / kPer;
       if (vec)
-        quantise_rows_kernel<T, true, 1><<<grid, kRowsThreads, 0, stream>>>(p, (int32_t)kblocks);
+        return launch(quantise_rows_kernel<T, true, 1>, grid, kRowsThreads, 0, stream, 1, p, (int32_t)kblocks);
       else
-        quantise_rows_kernel<T, false, 1><<<grid, kRowsThreads, 0, stream>>>(p, (int32_t)kblocks);
+        return launch(quantise_rows_kernel<T, false, 1>, grid, kRowsThreads, 0, stream, 1, p, (int32_t)kblocks);
     } else {
-      const unsigned grid = (unsigned)((n + kPer * 4 - 1) / (kPer * 4));
+      const int64_t grid = (n + kPer * 4 - 1) / (kPer * 4);
       if (vec)
-        quantise_rows_kernel<T, true, 4><<<grid, kRowsThreads, 0, stream>>>(p, (int32_t)kblocks);
+        return launch(quantise_rows_kernel<T, true, 4>, grid, kRowsThreads, 0, stream, 1, p, (int32_t)kblocks);
       else
-        quantise_rows_kernel<T, false, 4><<<grid, kRowsThreads, 0, stream>>>(p, (int32_t)kblocks);
+        return launch(quantise_rows_kernel<T, false, 4>, grid, kRowsThreads, 0, stream, 1, p, (int32_t)kblocks);
     }
   } else {
     const bool vec = (uintptr_t)p.x % (4 * sizeof(T)) == 0 && p.x_stride % 4 == 0;
-    const unsigned grid = (unsigned)(kblocks * mblocks);
+    const int64_t grid = kblocks * mblocks;
     if (vec)
-      quantise_tile_kernel<T, true><<<grid, 256, 0, stream>>>(p, (int32_t)kblocks, (int32_t)mblocks);
+      return launch(quantise_tile_kernel<T, true>, grid, 256, 0, stream, 1, p, (int32_t)kblocks, (int32_t)mblocks);
     else
-      quantise_tile_kernel<T, false><<<grid, 256, 0, stream>>>(p, (int32_t)kblocks, (int32_t)mblocks);
+      return launch(quantise_tile_kernel<T, false>, grid, 256, 0, stream, 1, p, (int32_t)kblocks, (int32_t)mblocks);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace

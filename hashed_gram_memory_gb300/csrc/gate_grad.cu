@@ -17,6 +17,9 @@
 // of two lanes of a warp.  dalpha crosses tokens: each block adds its tokens in
 // order and writes one partial; a second launch of one block adds the partials in
 // a fixed order in fp64, so the result does not depend on timing.
+#include <atomic>
+
+#include "launch.cuh"
 #include "lookup_common.cuh"
 #include "train_internal.cuh"
 
@@ -153,6 +156,7 @@ template <typename TK, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT <= 512 ? 1024 / MAXT : 1)
     gate_grad_block_kernel(const __grid_constant__ GateGradParams p) {
   __shared__ float4 s_red[2][MAXT / 32][2];  // two tokens in turn: one barrier a token
+  dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const int col = tid * 8;
   const bool mine = col < p.D;
@@ -201,6 +205,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 512 ? 1024 / MAXT : 1)
 template <typename TK>
 __global__ void __launch_bounds__(256) gate_grad_warp_kernel(const __grid_constant__ GateGradParams p) {
   __shared__ float4 s_da[128];
+  dependency_wait();
   const int tid = threadIdx.x, G = p.group;
   const int in = tid & (G - 1), slot = tid / G, slots = 256 / G;
   const int col = in * 8;
@@ -245,6 +250,7 @@ __global__ void __launch_bounds__(256) gate_grad_warp_kernel(const __grid_consta
 __global__ void __launch_bounds__(256) dalpha_kernel(const float4 *__restrict__ partial, int n,
                                                      float *__restrict__ dalpha) {
   __shared__ double s[8][4];
+  dependency_wait();
   double v[4] = {0, 0, 0, 0};
   for (int i = threadIdx.x; i < n; i += 256) {
     const float4 q = partial[i];
@@ -265,14 +271,23 @@ __global__ void __launch_bounds__(256) dalpha_kernel(const float4 *__restrict__ 
   }
 }
 
-template <typename K>
-cudaError_t resident_blocks(K kernel, int threads, int &blocks) {
-  int dev = 0, sms = 0, per = 0;
+// Blocks that fit on the device at once, asked once per kernel, block size and device.
+template <void (*kernel)(GateGradParams)>
+cudaError_t resident_blocks(int threads, int &blocks) {
+  static std::atomic<int> known[64][33];
+  int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  std::atomic<int> &slot = known[dev & 63][threads / 32];
+  blocks = slot.load(std::memory_order_relaxed);
+  if (blocks) return cudaSuccess;
+  int sms = 0, per = 0;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, 0);
+  if (e != cudaSuccess) return e;
   blocks = per * sms < kGateGradMaxBlocks ? per * sms : kGateGradMaxBlocks;
-  return e;
+  slot.store(blocks, std::memory_order_relaxed);
+  return cudaSuccess;
 }
 
 template <typename TK>
@@ -285,20 +300,21 @@ cudaError_t launch_typed(GateGradParams p, cudaStream_t stream) {
       p.group = 2;
       while (p.group < chunks) p.group *= 2;
       const int64_t need = (p.T + 256 / p.group - 1) / (256 / p.group);
-      if ((e = resident_blocks(gate_grad_warp_kernel<TK>, 256, n)) != cudaSuccess) return e;
+      if ((e = resident_blocks<gate_grad_warp_kernel<TK>>(256, n)) != cudaSuccess) return e;
       n = (int)(need < n ? need : n);
-      gate_grad_warp_kernel<TK><<<n, 256, 0, stream>>>(p);
+      e = launch(gate_grad_warp_kernel<TK>, n, 256, 0, stream, 1, p);
     } else {
       const int threads = (chunks + 31) / 32 * 32;
-      auto kernel = threads <= 512 ? gate_grad_block_kernel<TK, 512> : gate_grad_block_kernel<TK, 1024>;
-      if ((e = resident_blocks(kernel, threads, n)) != cudaSuccess) return e;
+      const bool wide = threads > 512;
+      e = wide ? resident_blocks<gate_grad_block_kernel<TK, 1024>>(threads, n)
+               : resident_blocks<gate_grad_block_kernel<TK, 512>>(threads, n);
+      if (e != cudaSuccess) return e;
       n = (int)(p.T < n ? p.T : n);
-      kernel<<<n, threads, 0, stream>>>(p);
+      e = launch(wide ? gate_grad_block_kernel<TK, 1024> : gate_grad_block_kernel<TK, 512>, n, threads, 0, stream, 1, p);
     }
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (e != cudaSuccess) return e;
   }
-  dalpha_kernel<<<1, 256, 0, stream>>>(p.partial, n, p.dalpha);
-  return cudaGetLastError();
+  return launch(dalpha_kernel, 1, 256, 0, stream, 1, p.partial, n, p.dalpha);
 }
 
 }  // namespace
