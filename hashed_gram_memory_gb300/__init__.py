@@ -157,7 +157,8 @@ def _load():
     L.engram_embed_grad_rows.argtypes = [vp, i64, i32, i64, vp, i32, i64, i64, i64, i32, C.c_float,
                                          vp, vp, i32, i64, vp, vp, sz, vp, vp]
     L.engram_embed_grad_rows.restype = i32
-    L.engram_fp8_quantise.argtypes = [vp, i32, i64, i64, i64, i32, vp, i64, vp, vp, i64, vp, vp]
+    L.engram_fp8_quantise.argtypes = [vp, i32, i64, i64, i64, i32, vp, i64, vp, vp, i64, vp, vp,
+                                      vp]
     L.engram_fp8_quantise.restype = i32
     L.engram_fp8_matmul.argtypes = [vp, i64, vp, i32, vp, i64, vp, i32, i64, i64, i64, vp, i32,
                                     i64, vp, vp]
@@ -165,7 +166,7 @@ def _load():
     L.engram_gate_add_grad_workspace_bytes.argtypes = []
     L.engram_gate_add_grad_workspace_bytes.restype = sz
     L.engram_gate_add_grad.argtypes = [vp, vp, i64, i32, vp, vp, C.c_float, vp, vp, vp, i32, vp,
-                                       vp, sz, vp]
+                                       vp, sz, vp, vp]
     L.engram_gate_add_grad.restype = i32
     return L
 
@@ -815,7 +816,7 @@ def _fp8_scales(t, rows, cols, block, name):
 
 
 def engram_fp8_quantise(x, block_rows: int = 1, rows: bool = True, cols: bool = False, out=None,
-                        stream=None):
+                        status=None, stream=None):
     """x bf16 or fp32 [M, K] as e4m3fn bytes with a power-of-two scale byte per block of 128.
     rows: (q [M, K], s [M, ceil(K/128)]), blocks along K.  cols: (qt [K, M], st [K,
     ceil(M/128)]), the transposed copy with blocks along M.  block_rows FP8_BLOCK: 128 x 128
@@ -849,7 +850,7 @@ def engram_fp8_quantise(x, block_rows: int = 1, rows: bool = True, cols: bool = 
     q = args[0] if rows else none
     qt = args[-1] if cols else none
     _check(lib.engram_fp8_quantise(x.data_ptr(), xd, M, K, max(_strides(x, "x")[0], K), block_rows,
-                                   *q, *qt, _stream(stream)), "engram_fp8_quantise")
+                                   *q, *qt, _ptr(status), _stream(stream)), "engram_fp8_quantise")
     return tuple(out)
 
 
@@ -883,7 +884,7 @@ def engram_gate_add_grad_workspace_bytes() -> int:
 
 
 def engram_gate_add_grad(k, state, streams_in, alpha, dy, eps: float = 1e-6, dx=None, dk=None,
-                         dalpha=None, dk_dtype=None, workspace=None, stream=None):
+                         dalpha=None, dk_dtype=None, workspace=None, status=None, stream=None):
     """The backward pass of engram_gate_add: k fp32 [..., D], state uint8 [tokens] or None
     (every token live), streams_in and dy bf16 [..., 4, D].  Returns (dx, dk, dalpha); dx may
     be dy itself."""
@@ -916,6 +917,6 @@ def engram_gate_add_grad(k, state, streams_in, alpha, dy, eps: float = 1e-6, dx=
                                 device=k.device)
     _check(lib.engram_gate_add_grad(_ptr(k), _ptr(state), T, D, _ptr(streams_in), _ptr(alpha),
                                     float(eps), _ptr(dy), _ptr(dx), _ptr(dk), _dtype(dk, "dk"),
-                                    _ptr(dalpha), _ptr(workspace), workspace.numel(),
+                                    _ptr(dalpha), _ptr(workspace), workspace.numel(), _ptr(status),
                                     _stream(stream)), "engram_gate_add_grad")
     return dx, dk, dalpha

@@ -1,11 +1,16 @@
 // embed.cu -- rows of one table looked up by id, scaled, and optionally summed
 // over a token's ids.
 //
-// HBM-bound: a row is read (4 or 2 bytes a value) and written once.  Each thread
-// handles 8 columns of an output row (one column on the path for odd widths and
-// alignments), four outputs at a time, their loads issued together so that a warp
-// keeps 2 KB in flight; neighbouring lanes read neighbouring columns.  A pooled
-// output loops over the token's ids in order, four rows in flight, in fp32.
+// HBM-bound: a row is read (4 or 2 bytes a value) and written once; a thread handles 8
+// columns of an output row, neighbouring lanes neighbouring columns.
+//   rows kernel (many rows of 2^i or 256 j columns): a warp takes 32 output rows, its
+//     lanes first their ids and places, one each; then the rows go through the warp, four
+//     loads in flight a lane, with two shuffles for what the flat kernel computes per
+//     thread.
+//   flat kernel (few rows, other widths; one column a thread where they are not on
+//     16-byte boundaries): a thread an output chunk.
+//   pooled outputs (flat): a thread loops over the token's ids in order, four rows in
+//     flight, in fp32.
 #include "launch.cuh"
 #include "lookup_common.cuh"
 #include "train_internal.cuh"
@@ -111,7 +116,7 @@ __global__ void __launch_bounds__(kThreads)
       id[u] = ENGRAM_ROW_DEAD - 1;
       if (row[u] < n_rows) {
         const uint32_t r32 = (uint32_t)row[u];  // n_tokens * n_ids < 2^31
-        const uint32_t t = r32 / (uint32_t)p.n_ids, j = r32 - t * (uint32_t)p.n_ids;
+        const uint32_t t = fast_div(r32, p.by_ids), j = r32 - t * (uint32_t)p.n_ids;
         id[u] = __ldg(p.ids + t * p.ids_stride + j);
         at[u] = t * p.out_token_stride + j * p.out_id_stride;
         if (id[u] < ENGRAM_ROW_DEAD || id[u] >= p.rows) {
@@ -172,19 +177,79 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// Output rows in batches of 32 a warp: G lanes a row (p.D = 8 G, or G = 32 and 256 columns
+// a slab), U rows in flight a lane.
+template <typename TI, typename TO, int U>
+__global__ void __launch_bounds__(kThreads)
+    embed_rows_kernel(const __grid_constant__ EmbedParams p, int32_t G, int32_t slabs) {
+  dependency_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
+  const int64_t batch = unit / slabs;
+  const int slab = (int)(unit - batch * slabs);
+  const int64_t n_rows = p.n_tokens * p.n_ids, row = batch * 32 + lane;
+  if (batch * 32 >= n_rows) return;
+  int32_t id = ENGRAM_ROW_DEAD - 1;
+  int64_t at = 0;
+  if (row < n_rows) {
+    const uint32_t t = fast_div((uint32_t)row, p.by_ids), j = (uint32_t)row - t * (uint32_t)p.n_ids;
+    id = __ldg(p.ids + t * p.ids_stride + j);
+    at = t * p.out_token_stride + j * p.out_id_stride;
+    if (id < ENGRAM_ROW_DEAD || id >= p.rows) {
+      if (slab == 0 && p.status) atomicOr(p.status, ENGRAM_FLAG_BAD_ROW);
+      id = ENGRAM_ROW_DEAD - 1;
+    }
+  }
+  const int per = 32 / G, mine = lane / G;  // rows side by side in a warp
+  const int col = (slab * 32 + (lane & (G - 1))) * 8;
+  const TI *table = static_cast<const TI *>(p.table) + col;
+  TO *out = static_cast<TO *>(p.out) + col;
+  for (int i = 0; i < G; i += U) {
+    Raw<TI, 8> raw[U];
+    int32_t ids[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      ids[u] = __shfl_sync(0xffffffffu, id, (i + u) * per + mine);
+      if (ids[u] >= 0) raw[u] = load_raw<TI, 8>(table + ids[u] * p.table_stride);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t to = __shfl_sync(0xffffffffu, at, (i + u) * per + mine);
+      if (ids[u] < ENGRAM_ROW_DEAD) continue;
+      float f[8] = {};
+      if (ids[u] >= 0) {
+        to_float<TI, 8>(raw[u], f);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) f[c] *= p.scale;
+      }
+      store_float<TO, 8>(out + to, f);
+    }
+  }
+}
+
 template <typename TI, typename TO, int V, bool POOLED>
 cudaError_t launch_sized(const EmbedParams &p, cudaStream_t stream) {
   const int32_t chunks = (p.D + V - 1) / V;
   const uint32_t magic = (uint32_t)(((1ull << 32) + chunks - 1) / chunks);
   const int64_t n_rows = POOLED ? p.n_tokens : p.n_tokens * p.n_ids;
   const int64_t items = n_rows * chunks;
+  if constexpr (!POOLED && V == 8) {
+    // Warps of 32 rows where there are several for every SM's schedulers.
+    const int G = chunks < 32 ? chunks : 32, slabs = chunks < 32 ? 1 : chunks / 32;
+    const int64_t units = (n_rows + 31) / 32 * slabs;
+    if (G >= 4 && (G & (G - 1)) == 0 && chunks % G == 0 && units >= kSms * 16) {
+      constexpr int U = sizeof(TI) == 4 ? 2 : 4;
+      return launch(embed_rows_kernel<TI, TO, U>, (units + kThreads / 32 - 1) / (kThreads / 32), kThreads, 0,
+                    stream, 1, p, G, slabs);
+    }
+  }
   // Few items, or pooled ones (which loop over their ids): one a thread.
-  if (POOLED || items <= 152 * 4 * kThreads) {
+  if (POOLED || items <= kSms * 4 * kThreads) {
     return launch(embed_kernel<TI, TO, V, 1, POOLED>, (items + kThreads - 1) / kThreads, kThreads, 0, stream, 1,
                   p, chunks, magic);
   }
   if constexpr (!POOLED) {
-    constexpr int U = 4;
+    constexpr int U = 2;
     return launch(embed_kernel<TI, TO, V, U, POOLED>, (items + kThreads * U - 1) / (kThreads * U), kThreads, 0,
                   stream, 1, p, chunks, magic);
   }
@@ -204,8 +269,10 @@ cudaError_t launch_typed(const EmbedParams &p, bool pooled, cudaStream_t stream)
 
 }  // namespace
 
-cudaError_t launch_embed(const EmbedParams &p, int table_dtype, int out_dtype, bool pooled,
+cudaError_t launch_embed(const EmbedParams &args, int table_dtype, int out_dtype, bool pooled,
                          cudaStream_t stream) {
+  EmbedParams p = args;
+  p.by_ids = fast_div_of((uint32_t)p.n_ids);
   if (table_dtype == ENGRAM_DTYPE_F32)
     return out_dtype == ENGRAM_DTYPE_F32 ? launch_typed<float, float>(p, pooled, stream)
                                          : launch_typed<float, uint16_t>(p, pooled, stream);

@@ -2,19 +2,23 @@
 //   grad[v] (+)= scale * sum over positions i with ids[i] = v, in ascending i, of dy[i]
 // as a dense [rows, D] gradient, or as the distinct ids and their rows.
 //
-// 1. Sort (id, position) pairs by id, stably: a radix sort, 8 bits a pass at most.  Up to
-//    4096 ids run all passes in one block's shared memory; more take three launches a
-//    pass (digit counts per tile of 4096, their prefix sums per digit, the scatter).  Dead
-//    and bad ids get the key `rows`, which sorts behind every row.
-// 2. Sum the runs of equal ids.  The sorted list is cut into chunks of equal length, a
+// 1. Sort (id, position) pairs by id, stably.  Up to 4096 ids: each id's place is the
+//    number of ids before it in that order, counted by comparing it with all of them in
+//    shared memory -- n^2 comparisons, but one launch over all SMs.  More: a radix sort, 9
+//    bits a pass at most, three launches a pass (digit counts per tile, their prefix sums
+//    per digit, the scatter).  Dead and bad ids get the key `rows`, which sorts behind
+//    every row.
+// 2. Sum the runs of equal ids.  The sorted list is cut into chunks of equal length; a
 //    group of lanes (8 columns a lane) walks a chunk with the rows of dy that come next
-//    in flight, adds in fp32 and writes each run that lies inside its chunk; a run that
-//    crosses a chunk's border leaves a partial sum there.  The chunks' equal length is what
-//    keeps a token that makes up a tenth of the text from running on one SM.
-// 3. Add the partial sums of each crossing run, in chunk order.
+//    in flight, adds in fp32 and writes each run that starts in its chunk, reading on into
+//    the next chunk where the run ends there.  A run that goes on beyond the next chunk
+//    leaves a partial sum for every chunk that it touches, and goes on a list: the chunks'
+//    equal length is what keeps a token that makes up a tenth of the text from running on
+//    one SM.
+// 3. Add the partial sums of each listed run, in an order that its chunks fix.
 // Every sum has one order, so results do not depend on timing; there are no atomics on
 // values.  A dense gradient's untouched rows are zeroed by further blocks of the second
-// step's launch, which look each row up in the sorted list.
+// step's launch, spread evenly among the others, which look each row up in the sorted list.
 //
 // HBM-bound: dy read once (scattered whole rows), each output row written once; the sort's
 // lists stay in L2.
@@ -25,14 +29,27 @@
 namespace engram {
 namespace {
 
-constexpr int kSortThreads = 512;
-constexpr int kTile = 4096;             // pairs a tile of the sort
-constexpr int kPer = kTile / kSortThreads;
-constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
+constexpr int kDigits = 512;       // most digits of a pass: one a thread
+constexpr int kCountSort = 4096;   // most pairs sorted by counting
 
-// x / d for x < 2^31: exact with m = ceil(2^(31 + l) / d), l = ceil(log2 d) (m < 2^32).
-__device__ __forceinline__ uint32_t fast_div(uint32_t x, const FastDiv &f) {
-  return (uint32_t)(((uint64_t)x * f.mul) >> f.shift);
+// Pairs a thread sorts of a tile: few where there are few tiles, so that they fill the SMs.
+constexpr int kPerLarge = 8, kPerSmall = 2;
+constexpr int64_t kLargeTiles = kSms * kSortThreads * kPerLarge;  // from here on
+
+// The sum of v over the threads before this one, of a block of kSortThreads.
+__device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t *s_sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t sum = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += u;
+  }
+  if (lane == 31) s_sum[warp] = sum;
+  __syncthreads();
+  const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? s_sum[lane] : 0);
+  return before + sum - v;
 }
 
 // The sort key of position i: its id, or `rows` where it takes no part.
@@ -44,149 +61,135 @@ __device__ __forceinline__ uint32_t key_of(const EmbedGradParams &p, uint32_t i,
   return (uint32_t)p.rows;
 }
 
-// Stable ranks of a tile's pairs by one digit.  Warp w holds pairs w*32*kPer .. in order,
-// pair (round r, lane l) at w*32*kPer + 32 r + l; slots at or past n are left out.  On
+// Stable ranks of a tile's pairs by one digit.  Warp w holds pairs w*32*PER .. in order,
+// pair (round r, lane l) at w*32*PER + 32 r + l; slots at or past n are left out.  On
 // return place[r] is the pair's position among the tile's pairs sorted by digit, and
 // s_start[d] the first position of digit d.
-__device__ __forceinline__ void rank_tile(const uint32_t (&key)[kPer], int n, int shift, uint32_t mask,
-                                          uint32_t (*s_cnt)[256], uint32_t *s_start,
-                                          uint32_t (&place)[kPer]) {
+template <int PER>
+__device__ __forceinline__ void rank_tile(const uint32_t (&key)[PER], int n, int shift, int bits,
+                                          uint16_t (*s_cnt)[kDigits], uint32_t *s_start, uint32_t *s_sum,
+                                          uint32_t (&place)[PER]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < kSortWarps * 256; i += kSortThreads) (&s_cnt[0][0])[i] = 0;
+  const uint32_t mask = (1u << bits) - 1;
+  uint4 *zero = reinterpret_cast<uint4 *>(&s_cnt[0][0]);
+  for (int i = tid; i < kSortWarps * kDigits / 8; i += kSortThreads) zero[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
 #pragma unroll
-  for (int r = 0; r < kPer; ++r) {
-    const bool have = warp * 32 * kPer + 32 * r + lane < n;
-    const uint32_t d = have ? (key[r] >> shift) & mask : 256;
-    const uint32_t same = __match_any_sync(0xffffffffu, d);
+  for (int r = 0; r < PER; ++r) {
+    const bool have = warp * 32 * PER + 32 * r + lane < n;
+    const uint32_t d = (key[r] >> shift) & mask;
+    uint32_t same = __ballot_sync(0xffffffffu, have);  // the lanes with this digit, bit by bit
+#pragma unroll
+    for (int b = 0; b < 9; ++b) {
+      const uint32_t set = __ballot_sync(0xffffffffu, d >> b & 1);
+      same &= d >> b & 1 ? set : ~set;
+    }
     const uint32_t before = __popc(same & ((1u << lane) - 1));
     if (have) {
       place[r] = s_cnt[warp][d] + before;
       __syncwarp(same);
-      if (before == 0) s_cnt[warp][d] += __popc(same);
+      if (before == 0) s_cnt[warp][d] += (uint16_t)__popc(same);
     }
     __syncwarp();
   }
   __syncthreads();
-  // Exclusive prefix over the warps of each digit, then over the digits (256 threads).
-  uint32_t total = 0, sum = 0;
-  if (tid < 256) {
-    for (int w = 0; w < kSortWarps; ++w) {
-      const uint32_t c = s_cnt[w][tid];
-      s_cnt[w][tid] = total;
-      total += c;
-    }
-    sum = total;
+  // Exclusive prefix over the warps of each digit (one a thread), then over the digits.
+  uint32_t total = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += v;
-    }
-    if (lane == 31) s_start[warp] = sum;
+  for (int w = 0; w < kSortWarps; ++w) {
+    const uint32_t c = s_cnt[w][tid];
+    s_cnt[w][tid] = (uint16_t)total;
+    total += c;
   }
-  __syncthreads();
-  uint32_t base = 0;
-  if (tid < 256)
-    for (int w = 0; w < warp; ++w) base += s_start[w];
-  __syncthreads();
-  if (tid < 256) s_start[tid] = base + sum - total;
+  s_start[tid] = block_exclusive(total, s_sum);
   __syncthreads();
 #pragma unroll
-  for (int r = 0; r < kPer; ++r)
-    if (warp * 32 * kPer + 32 * r + lane < n) {
+  for (int r = 0; r < PER; ++r)
+    if (warp * 32 * PER + 32 * r + lane < n) {
       const uint32_t d = (key[r] >> shift) & mask;
       place[r] += s_cnt[warp][d] + s_start[d];
     }
 }
 
-// All passes of at most kTile pairs, then (for the sparse form) the number of runs that
-// start before each chunk.
-__global__ void __launch_bounds__(kSortThreads)
-    sort_small_kernel(const __grid_constant__ EmbedGradParams p) {
-  __shared__ uint32_t s_key[kTile];
-  __shared__ uint16_t s_pos[kTile];
-  __shared__ uint32_t s_cnt[kSortWarps][256];
-  __shared__ uint32_t s_start[256];
+// The sort of up to kCountSort pairs: a pair's place is the number of pairs with a smaller
+// key, or an equal one and an earlier position.  Each warp places 8 pairs, its lanes
+// comparing them with 4 keys a load; positions are compared only inside the block's own 64
+// pairs (before them equal keys count, behind them they do not).
+constexpr int kCountThreads = 256, kCountPairs = 64;
+
+__global__ void __launch_bounds__(kCountThreads)
+    count_sort_kernel(const __grid_constant__ EmbedGradParams p) {
+  extern __shared__ uint4 s_key4[];
+  uint32_t *s_key = reinterpret_cast<uint32_t *>(s_key4);
   dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = (int)p.n;
-  uint32_t key[kPer], pos[kPer], place[kPer];
   bool bad = false;
+#pragma unroll 8
+  for (int i = tid; i < (n + 3) / 4 * 4; i += kCountThreads)
+    s_key[i] = i < n ? key_of(p, i, bad) : 0xFFFFFFFFu;  // the padding sorts behind everything
+  if (bad && p.status && blockIdx.x == 0) atomicOr(p.status, ENGRAM_FLAG_BAD_ROW);
+  if (blockIdx.x == 0 && tid == 0) *p.long_count = 0;
+  __syncthreads();
+  const int first = blockIdx.x * kCountPairs;  // a multiple of 4, as are all the bounds below
+  const int mine = first + warp * 8;
+  uint32_t key[8];
+  int count[8];
 #pragma unroll
-  for (int r = 0; r < kPer; ++r) {
-    pos[r] = warp * 32 * kPer + 32 * r + lane;
-    if (pos[r] < (uint32_t)n) key[r] = key_of(p, pos[r], bad);
+  for (int i = 0; i < 8; ++i) {
+    key[i] = mine + i < n ? s_key[mine + i] : 0;
+    count[i] = 0;
   }
-  if (bad && p.status) atomicOr(p.status, ENGRAM_FLAG_BAD_ROW);
-  for (int pass = 0; pass < p.passes; ++pass) {
-    rank_tile(key, n, pass * p.digit_bits, (1u << p.digit_bits) - 1, s_cnt, s_start, place);
-    __syncthreads();
+  const int end = (n + 3) / 4, own = first / 4, after = min(end, own + kCountPairs / 4);
+#pragma unroll 2
+  for (int j = lane; j < own; j += 32) {
+    const uint4 k = s_key4[j];
 #pragma unroll
-    for (int r = 0; r < kPer; ++r)
-      if (warp * 32 * kPer + 32 * r + lane < n) {
-        s_key[place[r]] = key[r];
-        s_pos[place[r]] = (uint16_t)pos[r];
-      }
-    __syncthreads();
+    for (int i = 0; i < 8; ++i)
+      count[i] += (k.x <= key[i]) + (k.y <= key[i]) + (k.z <= key[i]) + (k.w <= key[i]);
+  }
+  for (int j = own + lane; j < after; j += 32) {
+    const uint4 k = s_key4[j];
 #pragma unroll
-    for (int r = 0; r < kPer; ++r) {
-      const int i = warp * 32 * kPer + 32 * r + lane;
-      if (i < n) {
-        key[r] = s_key[i];
-        pos[r] = s_pos[i];
-      }
+    for (int i = 0; i < 8; ++i) {
+      const int at = mine + i - 4 * j;  // positions 4j .. 4j+3 against this pair's
+      count[i] += (k.x < key[i] || (k.x == key[i] && at > 0)) + (k.y < key[i] || (k.y == key[i] && at > 1)) +
+                  (k.z < key[i] || (k.z == key[i] && at > 2)) + (k.w < key[i] || (k.w == key[i] && at > 3));
     }
   }
-  for (int i = tid; i < n; i += kSortThreads) {
-    p.keys[i] = s_key[i];
-    p.pos[i] = s_pos[i];
-  }
-  if (!p.run_base) return;
-  // Runs starting in each of this thread's entries, then prefix sums over the entries.
-  uint32_t mine = 0;
+#pragma unroll 2
+  for (int j = after + lane; j < end; j += 32) {
+    const uint4 k = s_key4[j];
 #pragma unroll
-  for (int r = 0; r < kPer; ++r) {
-    const int i = tid * kPer + r;
-    mine += i < n && s_key[i] < (uint32_t)p.rows && (i == 0 || s_key[i - 1] != s_key[i]);
+    for (int i = 0; i < 8; ++i)
+      count[i] += (k.x < key[i]) + (k.y < key[i]) + (k.z < key[i]) + (k.w < key[i]);
   }
-  uint32_t sum = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t v = __shfl_up_sync(0xffffffffu, sum, o);
-    if (lane >= o) sum += v;
-  }
-  if (lane == 31) s_start[warp] = sum;
-  __syncthreads();
-  uint32_t at = sum - mine;
-  for (int w = 0; w < warp; ++w) at += s_start[w];
-#pragma unroll
-  for (int r = 0; r < kPer; ++r) {
-    const int i = tid * kPer + r;
-    if (i < n && i % p.chunk == 0) p.run_base[i / p.chunk] = at;
-    at += i < n && s_key[i] < (uint32_t)p.rows && (i == 0 || s_key[i - 1] != s_key[i]);
-  }
-  if (tid == kSortThreads - 1) {
-    p.run_base[p.chunks] = at;
-    *p.count_out = (int32_t)at;
+  for (int i = 0; i < 8; ++i) {
+    const int place = __reduce_add_sync(0xffffffffu, count[i]);
+    if (lane == i && mine + i < n) {
+      p.keys[place] = key[i];
+      p.pos[place] = mine + i;
+    }
   }
 }
 
 // ---- one pass of the sort of many pairs -----------------------------------------------
 
-template <bool FIRST>
+template <bool FIRST, int PER>
 __global__ void __launch_bounds__(kSortThreads)
     count_digits_kernel(const __grid_constant__ EmbedGradParams p, const uint32_t *__restrict__ keys,
                         int shift) {
-  __shared__ uint32_t s_cnt[256];
+  __shared__ uint32_t s_cnt[kDigits];
   dependency_wait();
   const int tid = threadIdx.x;
   const uint32_t mask = (1u << p.digit_bits) - 1;
-  if (tid < 256) s_cnt[tid] = 0;
+  s_cnt[tid] = 0;
   __syncthreads();
-  const int64_t base = (int64_t)blockIdx.x * kTile;
+  const int64_t base = (int64_t)blockIdx.x * (kSortThreads * PER);
   bool bad = false;
 #pragma unroll
-  for (int r = 0; r < kPer; ++r) {
+  for (int r = 0; r < PER; ++r) {
     const int64_t i = base + r * kSortThreads + tid;
     if (i < p.n) {
       const uint32_t k = FIRST ? key_of(p, (uint32_t)i, bad) : __ldg(keys + i);
@@ -201,7 +204,7 @@ __global__ void __launch_bounds__(kSortThreads)
 // Block d: the counts of digit d become their exclusive prefix sums over the tiles; the
 // digit's total goes behind the array.
 __global__ void __launch_bounds__(256) scan_digits_kernel(uint32_t *counts, int64_t tiles,
-                                                          uint32_t *totals) {
+                                                          uint32_t *totals, uint32_t *long_count) {
   __shared__ uint32_t s_sum[8];
   dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -227,68 +230,69 @@ __global__ void __launch_bounds__(256) scan_digits_kernel(uint32_t *counts, int6
     __syncthreads();
   }
   if (tid == 0) totals[blockIdx.x] = carry;
+  if (tid == 0 && blockIdx.x == 0) *long_count = 0;
 }
 
-template <bool FIRST>
-__global__ void __launch_bounds__(kSortThreads)
+template <bool FIRST, int PER>
+__global__ void __launch_bounds__(kSortThreads, 3)
     scatter_kernel(const __grid_constant__ EmbedGradParams p, const uint32_t *__restrict__ keys,
                    const uint32_t *__restrict__ poss, uint32_t *__restrict__ keys_out,
                    uint32_t *__restrict__ pos_out, int shift) {
+  constexpr int kTile = kSortThreads * PER;
+  __shared__ __align__(16) uint16_t s_cnt[kSortWarps][kDigits];
   __shared__ uint32_t s_key[kTile];
   __shared__ uint16_t s_from[kTile];
-  __shared__ uint32_t s_cnt[kSortWarps][256];
-  __shared__ uint32_t s_start[256];
-  __shared__ uint32_t s_sum[8];
+  __shared__ uint32_t s_start[kDigits];
+  __shared__ uint32_t s_sum[2][32];
   dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t mask = (1u << p.digit_bits) - 1;
   const int64_t base = (int64_t)blockIdx.x * kTile;
   const int n = (int)(p.n - base < kTile ? p.n - base : kTile);
-  uint32_t key[kPer], place[kPer];
+  // What every digit has before it over all tiles, and this digit in the tiles before this one.
+  const bool digit = tid <= (int)mask;
+  const uint32_t total = digit ? __ldg(p.totals + tid) : 0;
+  const uint32_t ahead = digit ? __ldg(p.counts + (int64_t)tid * p.tiles + blockIdx.x) : 0;
+  uint32_t key[PER], place[PER];
   bool bad = false;
 #pragma unroll
-  for (int r = 0; r < kPer; ++r) {
-    const int i = warp * 32 * kPer + 32 * r + lane;
+  for (int r = 0; r < PER; ++r) {
+    const int i = warp * 32 * PER + 32 * r + lane;
+    key[r] = 0;
     if (i < n) key[r] = FIRST ? key_of(p, (uint32_t)(base + i), bad) : __ldg(keys + base + i);
   }
-  rank_tile(key, n, shift, mask, s_cnt, s_start, place);
-  __syncthreads();
+  rank_tile<PER>(key, n, shift, p.digit_bits, s_cnt, s_start, s_sum[0], place);
 #pragma unroll
-  for (int r = 0; r < kPer; ++r) {
-    const int i = warp * 32 * kPer + 32 * r + lane;
+  for (int r = 0; r < PER; ++r) {
+    const int i = warp * 32 * PER + 32 * r + lane;
     if (i < n) {
       s_key[place[r]] = key[r];
       s_from[place[r]] = (uint16_t)i;
     }
   }
-  // Where each digit of this tile goes: the digits' totals before it, this digit in the
-  // tiles before this one, less its first position in the tile.
-  uint32_t *s_to = &s_cnt[0][0];
+  // Where a digit of this tile goes, less its first position in the tile.
+  const uint32_t to = block_exclusive(total, s_sum[1]) + ahead - s_start[tid];
   __syncthreads();
-  uint32_t t = 0, sum = 0;
-  if (tid < 256) {
-    t = tid <= (int)mask ? __ldg(p.totals + tid) : 0;
-    sum = t;
+  s_start[tid] = to;
+  __syncthreads();
+  uint32_t pos[PER];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += v;
+  for (int r = 0; r < PER; ++r) {
+    const int i = r * kSortThreads + tid;
+    if (i < n) {
+      const uint32_t from = (uint32_t)base + s_from[i];
+      pos[r] = FIRST ? from : __ldg(poss + from);
     }
-    if (lane == 31) s_sum[warp] = sum;
   }
-  __syncthreads();
-  if (tid <= (int)mask) {
-    uint32_t b = sum - t;
-    for (int w = 0; w < warp; ++w) b += s_sum[w];
-    s_to[tid] = b + __ldg(p.counts + (int64_t)tid * p.tiles + blockIdx.x) - s_start[tid];
-  }
-  __syncthreads();
-  for (int i = tid; i < n; i += kSortThreads) {
-    const uint32_t k = s_key[i];
-    const uint32_t to = s_to[(k >> shift) & mask] + i;
-    const uint32_t from = (uint32_t)base + s_from[i];
-    keys_out[to] = k;
-    pos_out[to] = FIRST ? from : __ldg(poss + from);
+#pragma unroll
+  for (int r = 0; r < PER; ++r) {
+    const int i = r * kSortThreads + tid;
+    if (i < n) {
+      const uint32_t k = s_key[i];
+      const uint32_t at = s_start[(k >> shift) & mask] + i;
+      keys_out[at] = k;
+      pos_out[at] = pos[r];
+    }
   }
 }
 
@@ -310,40 +314,47 @@ __global__ void __launch_bounds__(256) count_runs_kernel(const __grid_constant__
 
 // run_base becomes its exclusive prefix sums; the number of runs goes behind it.
 __global__ void __launch_bounds__(1024) scan_runs_kernel(const __grid_constant__ EmbedGradParams p) {
-  __shared__ uint32_t s_sum[32];
+  __shared__ uint32_t s_sum[2][32];
   dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint4 *base = reinterpret_cast<uint4 *>(p.run_base);  // padded to whole words of eight
   uint32_t carry = 0;
-  for (int64_t i0 = 0; i0 < p.chunks; i0 += 1024 * 8) {
-    uint32_t v[8], mine = 0;
+  int buf = 0;
+  for (int64_t i0 = 0; i0 < p.chunks; i0 += 1024 * 8, buf ^= 1) {
+    const int64_t c = i0 + tid * 8;
+    uint32_t v[8] = {};
+    if (c < p.chunks) {
+      const uint4 x = base[c / 4], y = base[c / 4 + 1];
+      const uint32_t all[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t c = i0 + tid * 8 + i;
-      v[i] = c < p.chunks ? p.run_base[c] : 0;
-      mine += v[i];
+      for (int i = 0; i < 8; ++i) v[i] = c + i < p.chunks ? all[i] : 0;
     }
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mine += v[i];
     uint32_t sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += u;
     }
-    if (lane == 31) s_sum[warp] = sum;
+    if (lane == 31) s_sum[buf][warp] = sum;
     __syncthreads();
-    uint32_t at = carry + sum - mine, all = carry;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) at += s_sum[w];
-      all += s_sum[w];
-    }
+    const uint32_t w = s_sum[buf][lane];  // every warp adds up the warps before it
+    uint32_t at = carry + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + sum - mine;
+    carry += __reduce_add_sync(0xffffffffu, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int64_t c = i0 + tid * 8 + i;
-      if (c < p.chunks) p.run_base[c] = at;
+      const uint32_t here = at;
       at += v[i];
+      v[i] = here;
     }
-    carry = all;
-    __syncthreads();
+    if (c < p.chunks) {
+      base[c / 4] = make_uint4(v[0], v[1], v[2], v[3]);
+      base[c / 4 + 1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
   }
+  __syncthreads();  // the words past the last chunk are written before the number goes there
   if (tid == 0) {
     p.run_base[p.chunks] = carry;
     *p.count_out = (int32_t)carry;
@@ -445,29 +456,40 @@ __device__ __forceinline__ Item item_of(const EmbedGradParams &p, int64_t group,
 
 template <typename TY, typename TG, int V, int U>
 __device__ __forceinline__ void sum_chunk(const EmbedGradParams &p, const Item &it) {
-  const int64_t e0 = it.chunk * p.chunk, e1 = min(e0 + p.chunk, p.n);
+  const int64_t C = p.chunk, e0 = it.chunk * C, e1 = min(e0 + C, p.n);
   const uint32_t rows = (uint32_t)p.rows;
   const bool mine = it.col < p.D;
   const bool lead = it.slab == 0 && it.in == 0;
+  const uint32_t first = __ldg(p.keys + e0), last = __ldg(p.keys + e1 - 1);
+  const bool comes = e0 > 0 && __ldg(p.keys + e0 - 1) == first;
+  const bool leaves = e1 < p.n && __ldg(p.keys + e1) == last;
+  const bool through = comes && leaves && first == last;
+  // A run that touches three chunks or more is summed in parts, one that touches two by the
+  // chunk that it starts in.
+  const bool long_in = comes && (through || (e0 - C >= 1 && __ldg(p.keys + e0 - C - 1) == first));
+  const bool long_out = leaves && (through || (e0 + 2 * C < p.n && __ldg(p.keys + e0 + 2 * C) == last));
   int64_t run = 0;
   if (p.run_base) {
-    run = __ldg(p.run_base + it.chunk);
+    run = (int64_t)__ldg(p.run_base + it.chunk) - comes;
     if (it.slab == 0) {  // ids beyond the distinct ones
       const int64_t count = __ldg(p.run_base + p.chunks);
       for (int64_t e = e0 + it.in; e < e1; e += p.group)
         if (e >= count) p.row_ids_out[e] = ENGRAM_ROW_DEAD;
     }
   }
-  uint32_t cur = __ldg(p.keys + e0);
-  if (cur >= rows) return;
-  bool open = e0 > 0 && __ldg(p.keys + e0 - 1) == cur;  // the run began in an earlier chunk
-  if (open) --run;
+  if (first >= rows) return;
+  if (long_out && !through && lead && last < rows) p.long_list[atomicAdd(p.long_count, 1u)] = (uint32_t)it.chunk;
+  const int64_t end = leaves && !long_out ? min(e0 + 2 * C, p.n) : e1;
+  const bool skip = comes && !long_in;  // the first run is the chunk before's
+  uint32_t cur = first;
+  bool open = comes;
   const TY *dy = static_cast<const TY *>(p.dy) + it.col;
   float acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
-  const auto flush = [&](bool more) {
-    if (open || more) {
+  const auto flush = [&](bool out_part) {
+    if (open && skip) return;
+    if (open || out_part) {
       if (mine) write_partial<V>(p.partial + (it.chunk * 2 + (open ? 0 : 1)) * p.partial_stride + it.col, acc);
     } else {
       const int64_t row = p.run_base ? run : cur;
@@ -476,7 +498,7 @@ __device__ __forceinline__ void sum_chunk(const EmbedGradParams &p, const Item &
       if (p.run_base && lead) p.row_ids_out[run] = (int32_t)cur;
     }
   };
-  for (int64_t e = e0; e < e1; e += U) {
+  for (int64_t e = e0; e < end; e += U) {
     uint32_t key[U];
     Slice<TY, V> s[U];
 #pragma unroll
@@ -486,8 +508,11 @@ __device__ __forceinline__ void sum_chunk(const EmbedGradParams &p, const Item &
       const uint32_t kk[4] = {k4.x, k4.y, k4.z, k4.w}, pp[4] = {p4.x, p4.y, p4.z, p4.w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        key[u + q] = e + u + q < e1 ? kk[q] : kNoKey;
-        if (mine && key[u + q] < rows) {
+        const int64_t at_e = e + u + q;
+        const uint32_t k = kk[q];
+        // past the chunk only its last run counts; kNoKey ends the walk
+        key[u + q] = at_e < e1 || (at_e < end && k == last) ? k : kNoKey;
+        if (mine && key[u + q] < rows && !(skip && k == first)) {
           int64_t at = (int64_t)pp[q] * p.dy_id_stride;
           if (!p.dy_linear) {
             const uint32_t t = fast_div(pp[q], p.by_ids);
@@ -509,19 +534,19 @@ __device__ __forceinline__ void sum_chunk(const EmbedGradParams &p, const Item &
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = 0.f;
       }
-      if (mine) s[u].add_to(acc);
+      if (mine && !(open && skip)) s[u].add_to(acc);
     }
   }
-  flush(e1 < p.n && __ldg(p.keys + e1) == cur);
+  flush(long_out);
 }
 
-// 32 rows of a dense gradient: those that no id names are zeroed.
+// p.zero_rows rows of a dense gradient (32 at most): those that no id names are zeroed.
 template <typename TG, int V>
 __device__ __forceinline__ void zero_rows(const EmbedGradParams &p, int64_t r0) {
   const int lane = threadIdx.x & 31;
   const int64_t row = r0 + lane;
   bool zero = false;
-  if (row < p.rows) {
+  if (lane < p.zero_rows && row < p.rows) {
     int64_t lo = 0, hi = p.n;  // the first key >= row
     while (lo < hi) {
       const int64_t mid = (lo + hi) >> 1;
@@ -532,15 +557,13 @@ __device__ __forceinline__ void zero_rows(const EmbedGradParams &p, int64_t r0) 
     }
     zero = lo >= p.n || __ldg(p.keys + lo) != (uint32_t)row;
   }
-  uint32_t todo = __ballot_sync(0xffffffffu, zero);
-  while (todo) {
-    const int r = __ffs(todo) - 1;
-    todo &= todo - 1;
-    TG *dst = static_cast<TG *>(p.grad) + (r0 + r) * p.grad_stride;
+  for (uint32_t todo = __ballot_sync(0xffffffffu, zero); todo; todo &= todo - 1) {
+    TG *dst = static_cast<TG *>(p.grad) + (r0 + __ffs(todo) - 1) * p.grad_stride;
     if constexpr (V == 1) {
       for (int c = lane; c < p.D; c += 32) dst[c] = TG(0);
     } else {
-      for (int c = lane * (16 / (int)sizeof(TG)); c < p.D; c += 32 * (16 / (int)sizeof(TG)))
+      constexpr int kWord = 16 / (int)sizeof(TG);
+      for (int c = lane * kWord; c < p.D; c += 32 * kWord)
         __stcs(reinterpret_cast<uint4 *>(dst + c), make_uint4(0, 0, 0, 0));
     }
   }
@@ -549,81 +572,54 @@ __device__ __forceinline__ void zero_rows(const EmbedGradParams &p, int64_t r0) 
 template <typename TY, typename TG, int V, int U>
 __global__ void __launch_bounds__(kSumThreads) sum_runs_kernel(const __grid_constant__ EmbedGradParams p) {
   dependency_wait();
-  if ((int64_t)blockIdx.x >= p.sum_blocks) {  // the zeroing blocks
-    const int64_t w = (blockIdx.x - p.sum_blocks) * (kSumThreads / 32) + (threadIdx.x >> 5);
-    if (w * 32 < p.rows) zero_rows<TG, V>(p, w * 32);
+  // Block b is zeroing block z if it is the z-th of them, spread evenly over the grid.
+  const uint64_t b = blockIdx.x, all = p.sum_blocks + p.zero_blocks;
+  const uint64_t z = b * p.zero_blocks / all;
+  if ((b + 1) * p.zero_blocks / all > z) {
+    const int64_t r0 = (z * (kSumThreads / 32) + (threadIdx.x >> 5)) * (int64_t)p.zero_rows;
+    if (r0 < p.rows) zero_rows<TG, V>(p, r0);
     return;
   }
-  const int64_t group = ((int64_t)blockIdx.x * kSumThreads + threadIdx.x) / p.group;
+  const int64_t group = ((int64_t)(b - z) * kSumThreads + threadIdx.x) / p.group;
   const Item it = item_of(p, group, threadIdx.x & (p.group - 1), V);
   if (it.chunk < p.chunks) sum_chunk<TY, TG, V, U>(p, it);
 }
 
-// ---- runs that cross chunks ----------------------------------------------------------------
+// ---- runs in parts ---------------------------------------------------------------------------
 
 constexpr int kJoinThreads = 256;
-constexpr int kAlone = 16;  // parts a group adds by itself
 
+// A block at a time takes a listed run and a slab of columns: each of its groups adds every
+// groups-th part (the keys that end the run are loaded along with the parts), then the first
+// group adds the groups' sums in order.
 template <typename TG, int V>
 __global__ void __launch_bounds__(kJoinThreads) join_runs_kernel(const __grid_constant__ EmbedGradParams p) {
-  extern __shared__ float s_part[];  // [groups a block][lanes a group * V]
-  __shared__ int64_t s_parts[kJoinThreads];
+  extern __shared__ float s_part[];  // [groups][lanes a group * V]
   dependency_wait();
   const int G = p.group, groups = kJoinThreads / G;
   const int slot = threadIdx.x / G, in = threadIdx.x & (G - 1);
-  const Item it = item_of(p, (int64_t)blockIdx.x * groups + slot, in, V);
-  // The partial sums of the run that starts in this chunk and goes on after it.
-  int64_t parts = 0;
-  uint32_t key = kNoKey;
-  if (it.chunk + 1 < p.chunks) {
-    const int64_t e0 = it.chunk * p.chunk, e1 = e0 + p.chunk;
-    key = __ldg(p.keys + e1 - 1);
-    if (key < (uint32_t)p.rows && __ldg(p.keys + e1) == key &&
-        !(e0 > 0 && __ldg(p.keys + e0 - 1) == key)) {
-      int64_t lo = it.chunk + 1, hi = p.chunks;  // the first chunk that starts with another key
-      while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (__ldg(p.keys + mid * p.chunk) == key)
-          lo = mid + 1;
-        else
-          hi = mid;
-      }
-      parts = lo - it.chunk;
-    }
-  }
-  const auto part = [&](int64_t chunk, int64_t i, int col) {
-    return p.partial + ((chunk + i) * 2 + (i == 0 ? 1 : 0)) * p.partial_stride + col;
-  };
-  const auto finish = [&](int64_t chunk, uint32_t k, int slab, int col, float (&acc)[V]) {
-    const int64_t row = p.run_base ? (int64_t)__ldg(p.run_base + chunk + 1) - 1 : k;
-    if (col < p.D) write_row<TG, V>(static_cast<TG *>(p.grad) + row * p.grad_stride + col, acc, p.scale, p.accumulate);
-    if (p.run_base && slab == 0 && in == 0) p.row_ids_out[row] = (int32_t)k;
-  };
-  if (parts > 0 && parts <= kAlone) {
+  const int64_t C = p.chunk, items = (int64_t)*p.long_count * p.slabs;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t listed = item / p.slabs;
+    const int slab = (int)(item - listed * p.slabs), col = (slab * G + in) * V;
+    const bool mine = col < p.D;
+    const int64_t chunk = __ldg(p.long_list + listed);
+    const uint32_t key = __ldg(p.keys + (chunk + 2) * C);
     float acc[V] = {};
-    if (it.col < p.D)
-      for (int64_t i = 0; i < parts; ++i) {
-        Slice<float, V> s;
-        s.load(part(it.chunk, i, it.col));
-        s.add_to(acc);
+    bool more = true;
+    for (int64_t i0 = slot; more; i0 += 4 * groups) {
+      uint32_t k[4];
+      Slice<float, V> s[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t i = i0 + u * groups, c = chunk + i;
+        k[u] = i == 0 ? key : (c < p.chunks ? __ldg(p.keys + c * C) : kNoKey);
+        if (mine && c < p.chunks) s[u].load(p.partial + (c * 2 + (i == 0 ? 1 : 0)) * p.partial_stride + col);
       }
-    finish(it.chunk, key, it.slab, it.col, acc);
-  }
-  if (in == 0) s_parts[slot] = parts;
-  __syncthreads();
-  // Longer runs take the whole block: each group adds every groups-th part, then the
-  // first one adds the groups' sums in order.
-  for (int o = 0; o < groups; ++o) {
-    const int64_t n = s_parts[o];  // block-uniform
-    if (n <= kAlone) continue;
-    const Item other = item_of(p, (int64_t)blockIdx.x * groups + o, in, V);
-    float acc[V] = {};
-    if (other.col < p.D) {
-#pragma unroll 4
-      for (int64_t i = slot; i < n; i += groups) {
-        Slice<float, V> s;
-        s.load(part(other.chunk, i, other.col));
-        s.add_to(acc);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        more = more && k[u] == key;
+        if (more && mine) s[u].add_to(acc);
       }
     }
 #pragma unroll
@@ -633,7 +629,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_runs_kernel(const __grid_co
       for (int g = 1; g < groups; ++g)
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] += s_part[(g * G + in) * V + i];
-      finish(other.chunk, __ldg(p.keys + (other.chunk + 1) * p.chunk), other.slab, other.col, acc);
+      const int64_t row = p.run_base ? (int64_t)__ldg(p.run_base + chunk + 1) - 1 : key;
+      if (mine)
+        write_row<TG, V>(static_cast<TG *>(p.grad) + row * p.grad_stride + col, acc, p.scale, p.accumulate);
+      if (p.run_base && slab == 0 && in == 0) p.row_ids_out[row] = (int32_t)key;
     }
     __syncthreads();
   }
@@ -641,13 +640,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_runs_kernel(const __grid_co
 
 // ---- host ---------------------------------------------------------------------------------
 
-FastDiv fast_div_of(uint32_t d) {
-  uint32_t l = 0;
-  while ((1ull << l) < d) ++l;
-  FastDiv f;
-  f.shift = 31 + l;
-  f.mul = (uint32_t)(((1ull << f.shift) + d - 1) / d);
-  return f;
+int64_t sort_tiles(int64_t n) {
+  const int64_t tile = kSortThreads * (n >= kLargeTiles ? kPerLarge : kPerSmall);
+  return (n + tile - 1) / tile;
 }
 
 size_t round16(size_t x) { return (x + 15) / 16 * 16; }
@@ -664,10 +659,10 @@ Cut cut_of(int64_t n, int D, bool vec) {
   c.group = 1;
   while (c.group < 32 && c.group < cols) c.group *= 2;
   c.slabs = (cols + c.group - 1) / c.group;
-  // Chunks long enough that partial sums are a small part of the traffic, short enough
-  // that there are several warps for every SM's schedulers.
-  c.chunk = 256;
-  const int64_t warps = 152 * 48;
+  // Chunks long enough that what starts one is a small part of it, short enough that there
+  // are several warps for every SM's schedulers.
+  c.chunk = 64;
+  const int64_t warps = kSms * 48;
   while (c.chunk > 16 && (n + c.chunk - 1) / c.chunk * c.slabs * c.group / 32 < warps) c.chunk /= 2;
   // Short lists: shorter chunks still, while their partial sums stay under 2 MB.
   while (c.chunk > 4 && (n + c.chunk - 1) / c.chunk * c.slabs * c.group / 32 < warps / 8 &&
@@ -679,7 +674,7 @@ Cut cut_of(int64_t n, int D, bool vec) {
 }
 
 struct Layout {
-  size_t keys[2], pos[2], counts, totals, run_base, partial, total;
+  size_t keys[2], pos[2], counts, totals, run_base, long_list, partial, total;
 };
 Layout layout_of(int64_t n, int D, const Cut &c) {
   Layout l;
@@ -694,9 +689,10 @@ Layout layout_of(int64_t n, int D, const Cut &c) {
     l.keys[i] = take(list);
     l.pos[i] = take(list);
   }
-  l.counts = take((size_t)((n + kTile - 1) / kTile) * 256 * 4);
-  l.totals = take(256 * 4);
-  l.run_base = take((size_t)(c.chunks + 1) * 4);
+  l.counts = take((size_t)sort_tiles(n) * kDigits * 4);
+  l.totals = take(kDigits * 4);
+  l.run_base = take((size_t)(c.chunks + 8) / 8 * 32 + 4);  // read and written eight at a time
+  l.long_list = take((size_t)(c.chunks + 1) * 4);
   l.partial = take((size_t)c.chunks * 2 * c.stride * 4);
   l.total = at;
   return l;
@@ -704,18 +700,21 @@ Layout layout_of(int64_t n, int D, const Cut &c) {
 
 template <typename TY, typename TG, int V>
 cudaError_t launch_sums(EmbedGradParams p, cudaStream_t stream) {
-  constexpr int U = V == 1 ? 8 : (sizeof(TY) == 4 ? 4 : 8);
+  constexpr int U = V == 1 ? 8 : 4;
   const int64_t groups = p.chunks * p.slabs;
   p.sum_blocks = (groups * p.group + kSumThreads - 1) / kSumThreads;
-  const int64_t zero_blocks =
-      p.run_base || p.accumulate ? 0 : (p.rows + kSumThreads - 1) / kSumThreads;  // a row a lane
-  if (p.sum_blocks + zero_blocks > INT32_MAX) return cudaErrorInvalidValue;
+  // Rows a warp of the zeroing blocks looks up: 32, or fewer wide ones, about 64 KB.
+  p.zero_rows = 32;
+  while (p.zero_rows > 1 && (int64_t)p.zero_rows * p.D * (int)sizeof(TG) > 65536) p.zero_rows /= 2;
+  const int64_t per = kSumThreads / 32 * p.zero_rows;
+  p.zero_blocks = p.run_base || p.accumulate ? 0 : (p.rows + per - 1) / per;
+  const int64_t blocks = p.sum_blocks + p.zero_blocks;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
-  if (p.sum_blocks + zero_blocks > 0)
-    e = launch(sum_runs_kernel<TY, TG, V, U>, p.sum_blocks + zero_blocks, kSumThreads, 0, stream, 1, p);
-  if (e != cudaSuccess || p.chunks < 2) return e;
-  const int per = kJoinThreads / p.group;
-  return launch(join_runs_kernel<TG, V>, (groups + per - 1) / per, kJoinThreads,
+  if (blocks > 0) e = launch(sum_runs_kernel<TY, TG, V, U>, blocks, kSumThreads, 0, stream, 1, p);
+  if (e != cudaSuccess || p.chunks < 3) return e;  // no run touches three chunks
+  const int64_t most = p.chunks / 2 * p.slabs;     // a listed run has two chunks' borders at least
+  return launch(join_runs_kernel<TG, V>, most < kSms * 3 ? most : kSms * 3, kJoinThreads,
                 kJoinThreads * V * sizeof(float), stream, 1, p);
 }
 
@@ -744,10 +743,12 @@ cudaError_t launch_embed_grad(EmbedGradParams p, int dy_dtype, int grad_dtype, v
   char *w = static_cast<char *>(workspace);
   p.by_ids = fast_div_of((uint32_t)p.n_ids);
   p.dy_linear = p.dy_token_stride == p.n_ids * p.dy_id_stride;
-  p.tiles = (p.n + kTile - 1) / kTile;
+  p.tiles = sort_tiles(p.n);
   p.counts = reinterpret_cast<uint32_t *>(w + l.counts);
   p.totals = reinterpret_cast<uint32_t *>(w + l.totals);
   p.run_base = sparse ? reinterpret_cast<uint32_t *>(w + l.run_base) : nullptr;
+  p.long_count = reinterpret_cast<uint32_t *>(w + l.long_list);
+  p.long_list = p.long_count + 1;
   p.partial = reinterpret_cast<float *>(w + l.partial);
   p.partial_stride = c.stride;
   p.group = c.group;
@@ -756,7 +757,7 @@ cudaError_t launch_embed_grad(EmbedGradParams p, int dy_dtype, int grad_dtype, v
   p.chunks = c.chunks;
   int bits = 1;
   while (bits < 32 && ((uint64_t)p.rows >> bits) != 0) ++bits;  // keys are 0 .. rows
-  p.passes = (bits + 7) / 8;
+  p.passes = (bits + 8) / 9;
   p.digit_bits = (bits + p.passes - 1) / p.passes;
   uint32_t *keys[2] = {reinterpret_cast<uint32_t *>(w + l.keys[0]), reinterpret_cast<uint32_t *>(w + l.keys[1])};
   uint32_t *pos[2] = {reinterpret_cast<uint32_t *>(w + l.pos[0]), reinterpret_cast<uint32_t *>(w + l.pos[1])};
@@ -765,27 +766,34 @@ cudaError_t launch_embed_grad(EmbedGradParams p, int dy_dtype, int grad_dtype, v
   p.pos = pos[0];
   if (p.n == 0) {
     if (sparse) return cudaMemsetAsync(p.count_out, 0, 4, stream);
-  } else if (p.n <= kTile) {
-    if ((e = launch(sort_small_kernel, 1, kSortThreads, 0, stream, 1, p)) != cudaSuccess) return e;
+  } else if (p.n <= kCountSort) {
+    e = launch(count_sort_kernel, (p.n + kCountPairs - 1) / kCountPairs, kCountThreads,
+               (size_t)(p.n + 3) / 4 * 16, stream, 1, p);
+    if (e != cudaSuccess) return e;
   } else {
+    const bool large = p.n >= kLargeTiles;
     for (int pass = 0; pass < p.passes && e == cudaSuccess; ++pass) {
       const int shift = pass * p.digit_bits, in = pass & 1 ^ 1, out = pass & 1;
-      e = launch(pass == 0 ? count_digits_kernel<true> : count_digits_kernel<false>, p.tiles, kSortThreads, 0,
-                 stream, 1, p, keys[in], shift);
+      const bool first = pass == 0;
+      e = launch(large ? (first ? count_digits_kernel<true, kPerLarge> : count_digits_kernel<false, kPerLarge>)
+                       : (first ? count_digits_kernel<true, kPerSmall> : count_digits_kernel<false, kPerSmall>),
+                 p.tiles, kSortThreads, 0, stream, 1, p, keys[in], shift);
       if (e == cudaSuccess)
-        e = launch(scan_digits_kernel, 1 << p.digit_bits, 256, 0, stream, 1, p.counts, p.tiles, p.totals);
+        e = launch(scan_digits_kernel, 1 << p.digit_bits, 256, 0, stream, 1, p.counts, p.tiles, p.totals,
+                   p.long_count);
       if (e == cudaSuccess)
-        e = launch(pass == 0 ? scatter_kernel<true> : scatter_kernel<false>, p.tiles, kSortThreads, 0, stream, 1,
-                   p, keys[in], pos[in], keys[out], pos[out], shift);
+        e = launch(large ? (first ? scatter_kernel<true, kPerLarge> : scatter_kernel<false, kPerLarge>)
+                         : (first ? scatter_kernel<true, kPerSmall> : scatter_kernel<false, kPerSmall>),
+                   p.tiles, kSortThreads, 0, stream, 1, p, keys[in], pos[in], keys[out], pos[out], shift);
     }
     if (e != cudaSuccess) return e;
     p.keys = keys[(p.passes - 1) & 1];
     p.pos = pos[(p.passes - 1) & 1];
-    if (sparse) {
-      e = launch(count_runs_kernel, (p.chunks + 7) / 8, 256, 0, stream, 1, p);
-      if (e == cudaSuccess) e = launch(scan_runs_kernel, 1, 1024, 0, stream, 1, p);
-      if (e != cudaSuccess) return e;
-    }
+  }
+  if (sparse && p.n > 0) {
+    e = launch(count_runs_kernel, (p.chunks + 7) / 8, 256, 0, stream, 1, p);
+    if (e == cudaSuccess) e = launch(scan_runs_kernel, 1, 1024, 0, stream, 1, p);
+    if (e != cudaSuccess) return e;
   }
   if (dy_dtype == ENGRAM_DTYPE_F32)
     return grad_dtype == ENGRAM_DTYPE_F32 ? launch_typed<float, float>(p, vec, stream)

@@ -16,11 +16,16 @@
 //     registers of 256 threads -- 16 rows x 4 columns each, so row maxima are warp
 //     reductions and column maxima one exchange through shared memory; the transposed
 //     bytes are turned in shared memory (16 KB, chunks of 16 bytes XOR-swizzled by the
-//     column) so that both copies leave as whole 128-byte lines.
+//     column) so that both copies leave as whole 128-byte lines.  Two persistent blocks an
+//     SM walk the tiles; a tile comes by one tensor copy into shared memory, and as soon as
+//     it is in registers the next one's copy starts, under its arithmetic.
 #include <cuda_fp8.h>
+
+#include <atomic>
 
 #include "launch.cuh"
 #include "lookup_common.cuh"
+#include "tensor_core.cuh"
 #include "train_internal.cuh"
 
 namespace engram {
@@ -127,24 +132,12 @@ __global__ void __launch_bounds__(kRowsThreads)
   }
 }
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(256, 2)
-    quantise_tile_kernel(const __grid_constant__ QuantiseParams p, int32_t kblocks, int32_t mblocks) {
-  __shared__ uint4 s_turn[128 * 8];
-  __shared__ uint4 s_max[8][32];  // [warp][lane]: the maxima of four columns
-  dependency_wait();
+// The tile (mb, kb), held as 16 rows x 4 columns a thread: its scales and bytes.
+__device__ __forceinline__ void quantise_tile(const QuantiseParams &p, const float (&v)[16][4], int64_t mb,
+                                              int64_t kb, int32_t kblocks, int32_t mblocks, uint4 *s_turn,
+                                              uint4 (*s_max)[32]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t mb = blockIdx.x / kblocks, kb = blockIdx.x - mb * kblocks;
   const int64_t m0 = mb * 128 + warp * 16, k0 = kb * 128 + lane * 4;
-  float v[16][4];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    if (m0 + i < p.M) {
-      load_vals<T, 4, VEC>(static_cast<const T *>(p.x) + (m0 + i) * p.x_stride, k0, p.K, v[i]);
-    } else {
-      v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
-    }
-  }
   // Column maxima: this thread's 16 rows, then the eight warps' through shared memory.
   uint32_t cm[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -241,6 +234,95 @@ __global__ void __launch_bounds__(256, 2)
   }
 }
 
+// A tile loaded into registers, for rows that are not on 16-byte boundaries.
+template <typename T>
+__global__ void __launch_bounds__(256, 2)
+    quantise_tile_kernel(const __grid_constant__ QuantiseParams p, int32_t kblocks, int32_t mblocks) {
+  __shared__ uint4 s_turn[128 * 8];
+  __shared__ uint4 s_max[8][32];  // [warp][lane]: the maxima of four columns
+  dependency_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t mb = blockIdx.x / kblocks, kb = blockIdx.x - mb * kblocks;
+  const int64_t m0 = mb * 128 + warp * 16, k0 = kb * 128 + lane * 4;
+  float v[16][4];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if (m0 + i < p.M) {
+      load_vals<T, 4, false>(static_cast<const T *>(p.x) + (m0 + i) * p.x_stride, k0, p.K, v[i]);
+    } else {
+      v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
+    }
+  }
+  quantise_tile(p, v, mb, kb, kblocks, mblocks, s_turn, s_max);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256, 2)
+    quantise_tma_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ QuantiseParams p,
+                        int32_t kblocks, int32_t mblocks) {
+  extern __shared__ __align__(128) uint8_t s_tile[];  // [128 rows][128 values], zero outside x
+  __shared__ uint4 s_turn[128 * 8];
+  __shared__ uint4 s_max[8][32];
+  __shared__ uint64_t s_full;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t tiles = kblocks * mblocks;  // under 2^31
+  constexpr uint32_t kRow = 128 * sizeof(T);
+  if (tid == 0) {
+    mbar_init(&s_full, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  dependency_wait();
+  __syncthreads();
+  int32_t mb = (int32_t)blockIdx.x / kblocks, kb = (int32_t)blockIdx.x - mb * kblocks;
+  const auto issue = [&](int32_t m, int32_t k) {
+    mbar_arrive_expect_tx(&s_full, 128 * kRow);
+    tma_load_2d(s_tile, &map, k * 128, m * 128, &s_full);
+  };
+  if (tid == 0 && (int32_t)blockIdx.x < tiles) issue(mb, kb);
+  uint32_t phase = 0;
+  for (int32_t tile = blockIdx.x; tile < tiles; phase ^= 1) {
+    const bool late = !drain_phase(&s_full, phase, p.wait_limit_ns);
+    float v[16][4];
+    const T *src = reinterpret_cast<const T *>(s_tile + warp * 16 * kRow) + lane * 4;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(src + i * 128);
+        v[i][0] = f.x, v[i][1] = f.y, v[i][2] = f.z, v[i][3] = f.w;
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2 *>(src + i * 128);
+        v[i][0] = bf16_lo(w.x), v[i][1] = bf16_hi(w.x), v[i][2] = bf16_lo(w.y), v[i][3] = bf16_hi(w.y);
+      }
+    }
+    if (__syncthreads_or(late)) {  // the copy did not arrive: the block stops together
+      if (tid == 0) {
+        if (p.status) atomicOr(p.status, ENGRAM_FLAG_TIMEOUT);
+        drain_phase(&s_full, phase, p.wait_limit_ns);  // it lands, or gives up likewise
+      }
+      break;
+    }
+    const int32_t this_mb = mb, this_kb = kb;
+    tile += gridDim.x;
+    mb = tile / kblocks, kb = tile - mb * kblocks;
+    if (tid == 0 && tile < tiles) issue(mb, kb);
+    quantise_tile(p, v, this_mb, this_kb, kblocks, mblocks, s_turn, s_max);
+  }
+}
+
+// x as a 2-D tiled map with box [128 values, 128 rows], zero fill outside.
+template <typename T>
+bool make_map(CUtensorMap *map, const QuantiseParams &p) {
+  EncodeTiled fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)p.K, (cuuint64_t)p.M};
+  const cuuint64_t strides[1] = {(cuuint64_t)(p.x_stride * sizeof(T))};
+  const cuuint32_t box[2] = {128, 128}, estr[2] = {1, 1};
+  return fn(map, sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+            const_cast<void *>(p.x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T>
 cudaError_t launch_typed(const QuantiseParams &p, cudaStream_t stream) {
   const int64_t kblocks = (p.K + 127) / 128, mblocks = (p.M + 127) / 128;
@@ -262,12 +344,27 @@ cudaError_t launch_typed(const QuantiseParams &p, cudaStream_t stream) {
         return launch(quantise_rows_kernel<T, false, 4>, grid, kRowsThreads, 0, stream, 1, p, (int32_t)kblocks);
     }
   } else {
-    const bool vec = (uintptr_t)p.x % (4 * sizeof(T)) == 0 && p.x_stride % 4 == 0;
-    const int64_t grid = kblocks * mblocks;
-    if (vec)
-      return launch(quantise_tile_kernel<T, true>, grid, 256, 0, stream, 1, p, (int32_t)kblocks, (int32_t)mblocks);
-    else
-      return launch(quantise_tile_kernel<T, false>, grid, 256, 0, stream, 1, p, (int32_t)kblocks, (int32_t)mblocks);
+    const int64_t tiles = kblocks * mblocks;
+    const int64_t stride = p.M > 1 ? p.x_stride : (p.K + 7) / 8 * 8;  // one row needs none
+    if ((uintptr_t)p.x % 16 != 0 || stride * sizeof(T) % 16 != 0)
+      return launch(quantise_tile_kernel<T>, tiles, 256, 0, stream, 1, p, (int32_t)kblocks, (int32_t)mblocks);
+    constexpr int kTileBytes = 128 * 128 * sizeof(T);
+    static std::atomic<uint64_t> configured{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (!(configured.load(std::memory_order_relaxed) & 1ull << (dev & 63))) {
+      e = cudaFuncSetAttribute(quantise_tma_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileBytes);
+      if (e != cudaSuccess) return e;
+      configured.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
+    }
+    QuantiseParams q = p;
+    q.x_stride = stride;
+    CUtensorMap map;
+    if (!make_map<T>(&map, q)) return cudaErrorInvalidValue;
+    const int64_t grid = tiles < 2 * kSms ? tiles : 2 * kSms;
+    return launch(quantise_tma_kernel<T>, grid, 256, kTileBytes, stream, 1, map, p, (int32_t)kblocks,
+                  (int32_t)mblocks);
   }
 }
 

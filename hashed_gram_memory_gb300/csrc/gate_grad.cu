@@ -13,12 +13,16 @@
 // read twice.  A token's k, stream 0 and four gradient streams stay in the
 // registers of its threads (8 columns each: 16-byte accesses, neighbouring lanes
 // adjacent) between the reduction of the seven sums (|a|^2, |k|^2, <a,k>, <dy_s,k>)
-// and the stores.  Wide tokens take a block each (D/8 threads), narrow ones a power
-// of two lanes of a warp.  dalpha crosses tokens: each block adds its tokens in
+// and the stores.  Wide tokens take a block at a time (D/8 threads), which walks
+// its tokens with the next ones' bytes on the way: bulk copies into a ring of
+// shared-memory stages, refilled as soon as a token is in registers.  (Loads into
+// registers instead, two blocks an SM: see the measurements at the launch.)  Narrow
+// tokens take a power of two lanes of a warp.  dalpha crosses tokens: each block adds its tokens in
 // order and writes one partial; a second launch of one block adds the partials in
 // a fixed order in fp64, so the result does not depend on timing.
 #include <atomic>
 
+#include "bulk_copy.cuh"
 #include "launch.cuh"
 #include "lookup_common.cuh"
 #include "train_internal.cuh"
@@ -78,21 +82,52 @@ struct Gate {
   float g, cross, wa, wk;  // dk = g c + cross a + wk k;  dx_0 = dy_0 + cross k + wa a
 };
 
-__device__ __forceinline__ Gate gate_of(const float (&r)[7], const float4 &alpha, float Df,
-                                        float eps) {
-  const float ra = 1.f / sqrtf(r[0] / Df + eps), rk = 1.f / sqrtf(r[1] / Df + eps);
-  const float u = ra * rk / sqrtf(Df);
+__device__ __forceinline__ Gate gate_of(const float (&r)[7], const float4 &alpha,
+                                        const GateGradParams &p) {
+  const float ra = rsqrtf(fmaf(r[0], p.inv_D, p.eps)), rk = rsqrtf(fmaf(r[1], p.inv_D, p.eps));
+  const float u = ra * rk * p.inv_sqrt_D;
   const float z = r[2] * u;
   // sigmoid and its slope from exp(-|z|), which neither overflows nor cancels
-  const float e = expf(-fabsf(z)), d = 1.f / (1.f + e);
+  const float e = expf(-fabsf(z)), d = __fdividef(1.f, 1.f + e);
   const float dc = alpha.x * r[3] + alpha.y * r[4] + alpha.z * r[5] + alpha.w * r[6];
   const float dz = dc * (e * d * d);
   Gate o;
   o.g = z >= 0.f ? d : e * d;
   o.cross = dz * u;
-  o.wa = -dz * z * ra * ra / Df;
-  o.wk = -dz * z * rk * rk / Df;
+  o.wa = -dz * z * ra * ra * p.inv_D;
+  o.wk = -dz * z * rk * rk * p.inv_D;
   return o;
+}
+
+// The seven sums over a block.  A warp halves the number of values a lane holds at each of
+// three exchanges, so 9 shuffles do for 35; lane 4i then has value i.  s_red: [7][warps].
+__device__ __forceinline__ void warp_sums(const float (&r)[7], float *s_red, int warp, int warps, int lane) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = i < 7 ? r[i] : 0.f;
+#pragma unroll
+  for (int half = 4; half > 0; half >>= 1) {
+    const bool up = lane & (4 * half);
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float give = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * half);
+    }
+  }
+  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+  if ((lane & 3) == 0 && lane < 28) s_red[(lane >> 2) * warps + warp] = v[0];
+}
+
+// .. and, behind a barrier, over its warps: a lane a warp, then a butterfly.
+__device__ __forceinline__ void block_sums(float (&r)[7], const float *s_red, int warps, int lane) {
+#pragma unroll
+  for (int i = 0; i < 7; ++i) {
+    float v = lane < warps ? s_red[i * warps + lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    r[i] = v;
+  }
 }
 
 template <typename TK>
@@ -151,11 +186,11 @@ __device__ __forceinline__ void store_dead(const GateGradParams &p, uint8_t stat
   }
 }
 
-// Wide tokens: one token a block at a time, threads = D/8 rounded up to warps.
-template <typename TK, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT <= 512 ? 1024 / MAXT : 1)
-    gate_grad_block_kernel(const __grid_constant__ GateGradParams p) {
-  __shared__ float4 s_red[2][MAXT / 32][2];  // two tokens in turn: one barrier a token
+// The widest tokens (D > 4096, of which no three fit shared memory): one token a block at a
+// time, loaded into registers, threads = D/8 rounded up to warps.
+template <typename TK>
+__global__ void __launch_bounds__(1024) gate_grad_block_kernel(const __grid_constant__ GateGradParams p) {
+  __shared__ float s_red[2][7 * 32];  // two tokens in turn: one barrier a token
   dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const int col = tid * 8;
@@ -176,24 +211,118 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 512 ? 1024 / MAXT : 1)
       load_cols(c, p, t, col);
       partial_sums(c, r);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-      for (int i = 0; i < 7; ++i) r[i] += __shfl_xor_sync(0xffffffffu, r[i], o);
-    if (lane == 0) {
-      s_red[buf][warp][0] = make_float4(r[0], r[1], r[2], r[3]);
-      s_red[buf][warp][1] = make_float4(r[4], r[5], r[6], 0.f);
-    }
+    warp_sums(r, s_red[buf], warp, warps, lane);
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 7; ++i) r[i] = 0.f;
-    for (int w = 0; w < warps; ++w) {
-      const float4 u = s_red[buf][w][0], v = s_red[buf][w][1];
-      r[0] += u.x, r[1] += u.y, r[2] += u.z, r[3] += u.w;
-      r[4] += v.x, r[5] += v.y, r[6] += v.z;
-    }
+    block_sums(r, s_red[buf], warps, lane);
     buf ^= 1;
-    const Gate o = gate_of(r, alpha, (float)p.D, p.eps);
+    const Gate o = gate_of(r, alpha, p);
+    da.x = fmaf(o.g, r[3], da.x), da.y = fmaf(o.g, r[4], da.y);
+    da.z = fmaf(o.g, r[5], da.z), da.w = fmaf(o.g, r[6], da.w);
+    if (mine) store_cols<TK>(c, o, alpha, p, t, col);
+  }
+  if (tid == 0) p.partial[blockIdx.x] = da;
+}
+
+// The same with the tokens' bytes brought by bulk copies: a ring of p.stages stages of
+// 14 D bytes (k, stream 0, dy), the next tokens' copies in flight while one is worked on.
+__device__ __forceinline__ void issue_token(const GateGradParams &p, int64_t t, uint8_t *stage,
+                                            uint64_t *full, uint8_t *state_slot) {
+  const uint32_t D = p.D;
+  const uint8_t state = p.state ? p.state[t] : 0;
+  *state_slot = state;
+  if (state == kBad) {
+    mbar_arrive(full);
+    return;
+  }
+  mbar_arrive_expect_tx(full, state == kDead ? 8 * D : 14 * D);
+  if (state != kDead) {
+    bulk_g2s(stage, p.k + t * D, 4 * D, full);
+    bulk_g2s(stage + 4 * D, p.x + t * 4 * D, 2 * D, full);
+  }
+  bulk_g2s(stage + 6 * D, p.dy + t * 4 * D, 8 * D, full);
+}
+
+template <typename TK>
+__global__ void __launch_bounds__(512, 2) gate_grad_bulk_kernel(const __grid_constant__ GateGradParams p) {
+  extern __shared__ __align__(128) uint8_t s_stage[];
+  __shared__ float s_red[2][7 * 16];  // two tokens in turn: one barrier a token
+  __shared__ uint64_t s_full[kGateGradMaxStages];
+  __shared__ uint8_t s_state[kGateGradMaxStages];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  const int col = tid * 8;
+  const bool mine = col < p.D;
+  const uint32_t D = p.D, stage_bytes = 14 * D;
+  if (tid == 0) {
+    for (int s = 0; s < p.stages; ++s) mbar_init(s_full + s, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  dependency_wait();
+  __syncthreads();
+  int64_t ahead = blockIdx.x;  // thread 0: the next token to issue
+  if (tid == 0)
+    for (int s = 0; s < p.stages && ahead < p.T; ++s, ahead += gridDim.x)
+      issue_token(p, ahead, s_stage + s * stage_bytes, s_full + s, s_state + s);
+  const float4 alpha = make_float4(__ldg(p.alpha), __ldg(p.alpha + 1), __ldg(p.alpha + 2),
+                                   __ldg(p.alpha + 3));
+  float4 da = make_float4(0.f, 0.f, 0.f, 0.f);
+  int buf = 0, s = 0;
+  uint32_t phase = 0;
+  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+    const bool late = !wait_bounded(s_full + s, p.wait_limit_ns, phase);
+    uint8_t state = kBad;
+    Cols c;
+    float r[7] = {};
+    if (!late) {
+      state = s_state[s];
+      const uint8_t *stage = s_stage + s * stage_bytes;
+      if (state != kBad && mine) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          c.dy[q] = *reinterpret_cast<const uint4 *>(stage + 6 * D + (q * D + col) * 2);
+        if (state != kDead) {
+          const float4 *kr = reinterpret_cast<const float4 *>(stage + col * 4);
+          const float4 k0 = kr[0], k1 = kr[1];
+          c.a = *reinterpret_cast<const uint4 *>(stage + 4 * D + col * 2);
+          c.k[0] = k0.x, c.k[1] = k0.y, c.k[2] = k0.z, c.k[3] = k0.w;
+          c.k[4] = k1.x, c.k[5] = k1.y, c.k[6] = k1.z, c.k[7] = k1.w;
+          partial_sums(c, r);
+        }
+      }
+    }
+    warp_sums(r, s_red[buf], warp, warps, lane);
+    if (__syncthreads_or(late)) {  // a copy did not arrive: the block stops together
+      if (tid == 0) {
+        if (p.status) atomicOr(p.status, ENGRAM_FLAG_TIMEOUT);
+        // the copies in flight land, or give up likewise, before the block's memory goes
+        for (int64_t u = t; u < ahead; u += gridDim.x) {
+          wait_bounded(s_full + s, p.wait_limit_ns, phase);
+          if (++s == p.stages) s = 0, phase ^= 1;
+        }
+      }
+      break;
+    }
+    // Every thread has its columns: the stage takes the next token.
+    if (tid == 0 && ahead < p.T) {
+      issue_token(p, ahead, s_stage + s * stage_bytes, s_full + s, s_state + s);
+      ahead += gridDim.x;
+    }
+    if (++s == p.stages) s = 0, phase ^= 1;
+    if (state == kBad || state == kDead) {
+      if (mine) {
+        const float zero[8] = {};
+        store_dk(static_cast<TK *>(p.dk) + t * D + col, zero);
+        if (state == kDead && p.dx != p.dy) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            __stcs(reinterpret_cast<uint4 *>(p.dx + (t * 4 + q) * (int64_t)D + col), c.dy[q]);
+        }
+      }
+      buf ^= 1;
+      continue;
+    }
+    block_sums(r, s_red[buf], warps, lane);
+    buf ^= 1;
+    const Gate o = gate_of(r, alpha, p);
     da.x = fmaf(o.g, r[3], da.x), da.y = fmaf(o.g, r[4], da.y);
     da.z = fmaf(o.g, r[5], da.z), da.w = fmaf(o.g, r[6], da.w);
     if (mine) store_cols<TK>(c, o, alpha, p, t, col);
@@ -228,7 +357,7 @@ __global__ void __launch_bounds__(256) gate_grad_warp_kernel(const __grid_consta
 #pragma unroll
       for (int i = 0; i < 7; ++i) r[i] += __shfl_xor_sync(0xffffffffu, r[i], o);
     if (live) {
-      const Gate o = gate_of(r, alpha, (float)p.D, p.eps);
+      const Gate o = gate_of(r, alpha, p);
       da.x = fmaf(o.g, r[3], da.x), da.y = fmaf(o.g, r[4], da.y);
       da.z = fmaf(o.g, r[5], da.z), da.w = fmaf(o.g, r[6], da.w);
       if (mine) store_cols<TK>(c, o, alpha, p, t, col);
@@ -271,9 +400,11 @@ __global__ void __launch_bounds__(256) dalpha_kernel(const float4 *__restrict__ 
   }
 }
 
+constexpr int kMaxRing = 225 * 1024;  // the most shared memory of one block's stages
+
 // Blocks that fit on the device at once, asked once per kernel, block size and device.
 template <void (*kernel)(GateGradParams)>
-cudaError_t resident_blocks(int threads, int &blocks) {
+cudaError_t resident_blocks(int threads, int &blocks, size_t smem = 0) {
   static std::atomic<int> known[64][33];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -283,7 +414,9 @@ cudaError_t resident_blocks(int threads, int &blocks) {
   if (blocks) return cudaSuccess;
   int sms = 0, per = 0;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, 0);
+  if (e == cudaSuccess && smem)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRing);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem);
   if (e != cudaSuccess) return e;
   blocks = per * sms < kGateGradMaxBlocks ? per * sms : kGateGradMaxBlocks;
   slot.store(blocks, std::memory_order_relaxed);
@@ -293,6 +426,8 @@ cudaError_t resident_blocks(int threads, int &blocks) {
 template <typename TK>
 cudaError_t launch_typed(GateGradParams p, cudaStream_t stream) {
   int n = 0;
+  p.inv_D = 1.f / (float)p.D;
+  p.inv_sqrt_D = 1.f / sqrtf((float)p.D);
   if (p.T > 0) {
     const int chunks = p.D / 8;
     cudaError_t e;
@@ -303,14 +438,26 @@ cudaError_t launch_typed(GateGradParams p, cudaStream_t stream) {
       if ((e = resident_blocks<gate_grad_warp_kernel<TK>>(256, n)) != cudaSuccess) return e;
       n = (int)(need < n ? need : n);
       e = launch(gate_grad_warp_kernel<TK>, n, 256, 0, stream, 1, p);
+    } else if (chunks <= 512) {
+      // Two blocks an SM at D = 4096 (more where the tokens are narrow, up to 1024 threads), so
+      // that one's sums and stores run under the other's, with two stages each at least:
+      // one block of four stages took XXX us for 65,536 x 4096, two of two YYY us.
+      const int threads = (chunks + 31) / 32 * 32;
+      const size_t stage = (size_t)14 * p.D;
+      constexpr size_t kSm = 228 * 1024, kBlock = 2048;  // an SM's; static and reserved a block
+      size_t per = kSm / (2 * stage + kBlock);
+      per = per > (size_t)(1024 / threads) ? 1024 / threads : per;
+      p.stages = (int)((kSm / per - kBlock) / stage);
+      if (p.stages > kGateGradMaxStages) p.stages = kGateGradMaxStages;
+      const size_t ring = p.stages * stage;
+      if ((e = resident_blocks<gate_grad_bulk_kernel<TK>>(threads, n, ring)) != cudaSuccess) return e;
+      n = (int)(p.T < n ? p.T : n);
+      e = launch(gate_grad_bulk_kernel<TK>, n, threads, ring, stream, 1, p);
     } else {
       const int threads = (chunks + 31) / 32 * 32;
-      const bool wide = threads > 512;
-      e = wide ? resident_blocks<gate_grad_block_kernel<TK, 1024>>(threads, n)
-               : resident_blocks<gate_grad_block_kernel<TK, 512>>(threads, n);
-      if (e != cudaSuccess) return e;
+      if ((e = resident_blocks<gate_grad_block_kernel<TK>>(threads, n)) != cudaSuccess) return e;
       n = (int)(p.T < n ? p.T : n);
-      e = launch(wide ? gate_grad_block_kernel<TK, 1024> : gate_grad_block_kernel<TK, 512>, n, threads, 0, stream, 1, p);
+      e = launch(gate_grad_block_kernel<TK>, n, threads, 0, stream, 1, p);
     }
     if (e != cudaSuccess) return e;
   }

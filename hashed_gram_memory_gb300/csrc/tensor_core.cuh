@@ -63,12 +63,13 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volat
   }
 }
 
-// Bounded wait that ignores the abort flag (draining work already issued).
-__device__ __forceinline__ void drain_phase(uint64_t *bar, uint32_t parity, int64_t limit_ns) {
+// Bounded wait that ignores the abort flag (draining work already issued); false if it gave up.
+__device__ __forceinline__ bool drain_phase(uint64_t *bar, uint32_t parity, int64_t limit_ns) {
   const long long limit = limit_ns * 21 / 10;
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity))
-    if (clock64() - t0 > limit) return;
+    if (clock64() - t0 > limit) return false;
+  return true;
 }
 
 // 2-D TMA tile load (coordinates: x = K offset, y = row) completing on `bar`.

@@ -209,13 +209,14 @@ ENGRAM_API engram_status engram_embed_grad_rows(const int32_t *ids, int64_t n_to
 ENGRAM_API engram_status engram_fp8_quantise(const void *x, int32_t x_dtype, int64_t M, int64_t K,
                                              int64_t x_stride, int32_t block_rows, uint8_t *q,
                                              int64_t q_stride, uint8_t *s, uint8_t *qt,
-                                             int64_t qt_stride, uint8_t *st, void *stream) {
+                                             int64_t qt_stride, uint8_t *st, int32_t *status,
+                                             void *stream) {
   ENGRAM_NVTX_RANGE("engram_fp8_quantise");
   const char *fn = "engram_fp8_quantise";
   if (M < 0 || K < 1 || M > INT32_MAX || K > INT32_MAX)
     return set_error(ENGRAM_ERR_INVALID_ARG, "%s: M in [0, 2^31-1] and K in [1, 2^31-1]", fn);
   const int64_t kb = (K + 127) / 128, mb = (M + 127) / 128;
-  if (mb * kb > INT32_MAX || M * kb / 16 > INT32_MAX)
+  if (mb * kb > INT32_MAX - 4096 || M * kb / 16 > INT32_MAX)
     return set_error(ENGRAM_ERR_UNSUPPORTED, "%s: over 2^31-1 tiles", fn);
   if (!dtype_ok(x_dtype)) return set_error(ENGRAM_ERR_INVALID_ARG, "%s: unknown x dtype", fn);
   if (block_rows != 1 && block_rows != ENGRAM_FP8_BLOCK)
@@ -223,6 +224,7 @@ ENGRAM_API engram_status engram_fp8_quantise(const void *x, int32_t x_dtype, int
   if (M == 0) return ok();  // empty buffers have no address
   if ((!q && !qt) || (q && !s) || (qt && !st))
     return set_error(ENGRAM_ERR_INVALID_ARG, "%s: q or qt must be given, each with its scales", fn);
+  if (!aligned(status, 4)) return set_error(ENGRAM_ERR_INVALID_ARG, "%s: status misaligned", fn);
   if (!x || !aligned(x, dtype_bytes(x_dtype)) || (M > 1 && x_stride < K))
     return set_error(ENGRAM_ERR_INVALID_ARG, "%s: x NULL or misaligned, or its stride under K", fn);
   if (!aligned(q, 16) || !aligned(qt, 16) || (q && M > 1 && (q_stride < K || q_stride % 16 != 0)) ||
@@ -238,8 +240,8 @@ ENGRAM_API engram_status engram_fp8_quantise(const void *x, int32_t x_dtype, int
   } outs[4] = {{q, q ? (size_t)extent(M, q_stride, 1, 0, K) : 0}, {q ? s : nullptr, sn},
                {qt, qt ? (size_t)extent(K, qt_stride, 1, 0, M) : 0}, {qt ? st : nullptr, tn}};
   for (int o = 0; o < 4; ++o) {
-    if (overlap(outs[o].p, outs[o].n, x, xb))
-      return set_error(ENGRAM_ERR_INVALID_ARG, "%s: an output overlaps x", fn);
+    if (overlap(outs[o].p, outs[o].n, x, xb) || overlap(outs[o].p, outs[o].n, status, 4))
+      return set_error(ENGRAM_ERR_INVALID_ARG, "%s: an output overlaps x or status", fn);
     for (int i = 0; i < o; ++i)
       if (overlap(outs[o].p, outs[o].n, outs[i].p, outs[i].n))
         return set_error(ENGRAM_ERR_INVALID_ARG, "%s: output buffers overlap", fn);
@@ -252,6 +254,8 @@ ENGRAM_API engram_status engram_fp8_quantise(const void *x, int32_t x_dtype, int
   p.s = s;
   p.qt = qt;
   p.st = st;
+  p.status = status;
+  p.wait_limit_ns = engram::wait_limit_ns();
   p.M = M;
   p.K = K;
   p.x_stride = x_stride;
@@ -327,7 +331,7 @@ ENGRAM_API engram_status engram_gate_add_grad(const float *k, const uint8_t *sta
                                               float eps, const uint16_t *dy, uint16_t *dx,
                                               void *dk, int32_t dk_dtype, float *dalpha,
                                               void *workspace, size_t workspace_bytes,
-                                              void *stream) {
+                                              int32_t *status, void *stream) {
   ENGRAM_NVTX_RANGE("engram_gate_add_grad");
   const char *fn = "engram_gate_add_grad";
   if (n_tokens < 0 || n_tokens > INT32_MAX)
@@ -335,8 +339,8 @@ ENGRAM_API engram_status engram_gate_add_grad(const float *k, const uint8_t *sta
   if (D < 16 || D % 16 != 0 || D > 8192)
     return set_error(ENGRAM_ERR_INVALID_ARG, "%s: D must be a multiple of 16 in [16, 8192]", fn);
   if (!dtype_ok(dk_dtype)) return set_error(ENGRAM_ERR_INVALID_ARG, "%s: unknown dk dtype", fn);
-  if (!alpha || !dalpha || !aligned(alpha, 4) || !aligned(dalpha, 4))
-    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: alpha or dalpha NULL or misaligned", fn);
+  if (!alpha || !dalpha || !aligned(alpha, 4) || !aligned(dalpha, 4) || !aligned(status, 4))
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: alpha or dalpha NULL, or they or status misaligned", fn);
   if (!(eps >= 0.f) || !isfinite(eps))
     return set_error(ENGRAM_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", fn);
   const size_t need = engram_gate_add_grad_workspace_bytes();
@@ -356,9 +360,10 @@ ENGRAM_API engram_status engram_gate_add_grad(const float *k, const uint8_t *sta
     const void *p;
     size_t n;
   } outs[4] = {{dx, sb}, {dk, db}, {dalpha, 16}, {workspace, need}},
-    ins[5] = {{k, kb}, {state, state ? (size_t)n_tokens : 0}, {streams_in, sb}, {alpha, 16}, {dy, sb}};
+    ins[6] = {{k, kb}, {state, state ? (size_t)n_tokens : 0}, {streams_in, sb}, {alpha, 16}, {dy, sb},
+              {status, 4}};
   for (int o = 0; o < 4; ++o) {
-    for (int i = 0; i < 5; ++i)
+    for (int i = 0; i < 6; ++i)
       if (!(o == 0 && i == 4 && dx == dy) && overlap(outs[o].p, outs[o].n, ins[i].p, ins[i].n))
         return set_error(ENGRAM_ERR_INVALID_ARG, "%s: an output overlaps an input", fn);
     for (int i = 0; i < o; ++i)
@@ -377,6 +382,8 @@ ENGRAM_API engram_status engram_gate_add_grad(const float *k, const uint8_t *sta
   p.alpha = alpha;
   p.partial = static_cast<float4 *>(workspace);
   p.dalpha = dalpha;
+  p.status = status;
+  p.wait_limit_ns = engram::wait_limit_ns();
   p.T = n_tokens;
   p.D = D;
   p.eps = eps;

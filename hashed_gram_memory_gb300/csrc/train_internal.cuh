@@ -7,7 +7,25 @@
 
 namespace engram {
 
+constexpr int kSms = 152;  // of a GB300; grids are sized by it
+
 inline size_t dtype_bytes(int dtype) { return dtype == ENGRAM_DTYPE_F32 ? 4 : 2; }
+
+struct FastDiv {  // x / d as x * mul >> shift, for x < 2^31
+  uint32_t mul, shift;
+};
+// Exact with m = ceil(2^(31 + l) / d), l = ceil(log2 d) (m < 2^32).
+inline FastDiv fast_div_of(uint32_t d) {
+  uint32_t l = 0;
+  while ((1ull << l) < d) ++l;
+  FastDiv f;
+  f.shift = 31 + l;
+  f.mul = (uint32_t)(((1ull << f.shift) + d - 1) / d);
+  return f;
+}
+__device__ __forceinline__ uint32_t fast_div(uint32_t x, const FastDiv &f) {
+  return (uint32_t)(((uint64_t)x * f.mul) >> f.shift);
+}
 
 struct EmbedParams {
   const int32_t *ids;
@@ -17,13 +35,10 @@ struct EmbedParams {
   int64_t n_tokens, ids_stride, rows, table_stride, out_token_stride, out_id_stride;
   int32_t n_ids, D;
   float scale;
+  FastDiv by_ids;  // set by the launcher
 };
 cudaError_t launch_embed(const EmbedParams &p, int table_dtype, int out_dtype, bool pooled,
                          cudaStream_t stream);
-
-struct FastDiv {  // x / d as x * mul >> shift
-  uint32_t mul, shift;
-};
 
 struct EmbedGradParams {
   const int32_t *ids;
@@ -44,7 +59,9 @@ struct EmbedGradParams {
   uint32_t *keys, *pos, *counts, *totals;
   uint32_t *run_base;  // sparse: runs before each chunk, their number behind; else NULL
   float *partial;      // [chunks][2][partial_stride]: a run open at the start, at the end
-  int64_t partial_stride, chunks, sum_blocks;
+  uint32_t *long_count, *long_list;  // chunks in which a run of more than two chunks starts
+  int64_t partial_stride, chunks, sum_blocks, zero_blocks;
+  int32_t zero_rows;  // rows a warp of the zeroing blocks looks at
   int32_t group, slabs, chunk;  // lanes a group, column slabs, sorted ids a chunk
 };
 size_t embed_grad_workspace_bytes(int64_t n, int32_t D);
@@ -61,16 +78,23 @@ struct GateGradParams {
   float4 *partial;  // [kGateGradMaxBlocks]: each block's sums of g <dy_s, k>
   float *dalpha;
   int64_t T;
-  int32_t D, group;  // group: lanes per token of the warp kernel (a power of two)
+  int32_t *status;
+  int64_t wait_limit_ns;
+  int32_t D;
   float eps;
+  float inv_D, inv_sqrt_D;  // set by the launcher, as are the rest
+  int32_t group, stages;    // lanes per narrow token, stages of the ring
 };
 constexpr int kGateGradMaxBlocks = 4096;
+constexpr int kGateGradMaxStages = 8;
 cudaError_t launch_gate_grad(const GateGradParams &p, int dk_dtype, cudaStream_t stream);
 
 struct QuantiseParams {
   const void *x;
   uint8_t *q, *s;    // NULL q: no row copy
   uint8_t *qt, *st;  // NULL qt: no transposed copy
+  int32_t *status;
+  int64_t wait_limit_ns;
   int64_t M, K, x_stride, q_stride, qt_stride;
   int32_t block_rows;  // 1 or ENGRAM_FP8_BLOCK
 };

@@ -618,13 +618,15 @@ ENGRAM_API engram_status engram_embed_grad_rows(const int32_t *ids, int64_t n_to
  *   block_rows  1, or ENGRAM_FP8_BLOCK: 128 x 128 tiles share a scale, s is
  *          [ceil(M/128), ceil(K/128)] and st its transpose (weights)
  * A block that holds a NaN or an infinity gets the scale 0xFF and the bytes 0x7F (both
- * NaN).  q and qt are 16-byte aligned; bytes between rows are not written.  M == 0
- * launches nothing.
+ * NaN).  q and qt are 16-byte aligned; bytes between rows are not written.  A copy that
+ * does not arrive within the wait limit sets ENGRAM_FLAG_TIMEOUT and leaves that block's
+ * later tiles unwritten.  M == 0 launches nothing.
  */
 ENGRAM_API engram_status engram_fp8_quantise(const void *x, int32_t x_dtype, int64_t M, int64_t K,
                                              int64_t x_stride, int32_t block_rows, uint8_t *q,
                                              int64_t q_stride, uint8_t *s, uint8_t *qt,
-                                             int64_t qt_stride, uint8_t *st, void *stream);
+                                             int64_t qt_stride, uint8_t *st, int32_t *status,
+                                             void *stream);
 
 /*
  * engram_fp8_matmul -- out[m, n] = sum_k a[m, k] b[n, k] of operands as
@@ -665,7 +667,8 @@ ENGRAM_API engram_status engram_fp8_matmul(const uint8_t *a, int64_t a_stride, c
  * A dead token (state 1) passes dy through (dk = 0); a bad one (state 2) has dk = 0
  * and its dx left unwritten; neither adds to dalpha.  D a multiple of 16 in [16,
  * 8192]; all but state, alpha and dalpha 16-byte aligned.  n_tokens == 0 zeroes
- * dalpha.
+ * dalpha.  A copy that does not arrive within the wait limit sets ENGRAM_FLAG_TIMEOUT and
+ * leaves that block's later tokens unwritten.
  */
 ENGRAM_API size_t engram_gate_add_grad_workspace_bytes(void);
 ENGRAM_API engram_status engram_gate_add_grad(const float *k, const uint8_t *state,
@@ -674,7 +677,7 @@ ENGRAM_API engram_status engram_gate_add_grad(const float *k, const uint8_t *sta
                                               float eps, const uint16_t *dy, uint16_t *dx,
                                               void *dk, int32_t dk_dtype, float *dalpha,
                                               void *workspace, size_t workspace_bytes,
-                                              void *stream);
+                                              int32_t *status, void *stream);
 
 /*
  * engram_read_status -- waits for `stream`, copies the device status word into
