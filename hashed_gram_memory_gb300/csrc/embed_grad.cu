@@ -4,7 +4,7 @@
 //
 // 1. Sort (id, position) pairs by id, stably.  Up to 4096 ids: each id's place is the
 //    number of ids before it in that order, counted by comparing it with all of them in
-//    shared memory -- n^2 comparisons, but one launch over all SMs.  More: a radix sort, 9
+//    shared memory -- n^2 comparisons, but one launch over all SMs.  More: a radix sort, 10
 //    bits a pass at most, three launches a pass (digit counts per tile, their prefix sums
 //    per digit, the scatter).  Dead and bad ids get the key `rows`, which sorts behind
 //    every row.
@@ -22,6 +22,7 @@
 //
 // HBM-bound: dy read once (scattered whole rows), each output row written once; the sort's
 // lists stay in L2.
+#include "bulk_copy.cuh"
 #include "launch.cuh"
 #include "lookup_common.cuh"
 #include "train_internal.cuh"
@@ -30,7 +31,7 @@ namespace engram {
 namespace {
 
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
-constexpr int kDigits = 512;       // most digits of a pass: one a thread
+constexpr int kDigits = 1024;      // most digits of a pass: two a thread
 constexpr int kCountSort = 4096;   // most pairs sorted by counting
 
 // Pairs a thread sorts of a tile: few where there are few tiles, so that they fill the SMs.
@@ -80,7 +81,7 @@ __device__ __forceinline__ void rank_tile(const uint32_t (&key)[PER], int n, int
     const uint32_t d = (key[r] >> shift) & mask;
     uint32_t same = __ballot_sync(0xffffffffu, have);  // the lanes with this digit, bit by bit
 #pragma unroll
-    for (int b = 0; b < 9; ++b) {
+    for (int b = 0; b < 10; ++b) {
       const uint32_t set = __ballot_sync(0xffffffffu, d >> b & 1);
       same &= d >> b & 1 ? set : ~set;
     }
@@ -93,15 +94,19 @@ __device__ __forceinline__ void rank_tile(const uint32_t (&key)[PER], int n, int
     __syncwarp();
   }
   __syncthreads();
-  // Exclusive prefix over the warps of each digit (one a thread), then over the digits.
+  // Exclusive prefix over the warps of each digit (two a thread, added side by side: a
+  // tile's counts fit 16 bits), then over the digits.
   uint32_t total = 0;
 #pragma unroll
   for (int w = 0; w < kSortWarps; ++w) {
-    const uint32_t c = s_cnt[w][tid];
-    s_cnt[w][tid] = (uint16_t)total;
+    uint32_t *both = reinterpret_cast<uint32_t *>(s_cnt[w]) + tid;
+    const uint32_t c = *both;
+    *both = total;
     total += c;
   }
-  s_start[tid] = block_exclusive(total, s_sum);
+  const uint32_t base = block_exclusive((total & 0xFFFF) + (total >> 16), s_sum);
+  s_start[2 * tid] = base;
+  s_start[2 * tid + 1] = base + (total & 0xFFFF);
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < PER; ++r)
@@ -184,7 +189,7 @@ __global__ void __launch_bounds__(kSortThreads)
   dependency_wait();
   const int tid = threadIdx.x;
   const uint32_t mask = (1u << p.digit_bits) - 1;
-  s_cnt[tid] = 0;
+  for (int d = tid; d < kDigits; d += kSortThreads) s_cnt[d] = 0;
   __syncthreads();
   const int64_t base = (int64_t)blockIdx.x * (kSortThreads * PER);
   bool bad = false;
@@ -198,7 +203,7 @@ __global__ void __launch_bounds__(kSortThreads)
   }
   if (FIRST && bad && p.status) atomicOr(p.status, ENGRAM_FLAG_BAD_ROW);
   __syncthreads();
-  if (tid <= (int)mask) p.counts[(int64_t)tid * p.tiles + blockIdx.x] = s_cnt[tid];
+  for (int d = tid; d <= (int)mask; d += kSortThreads) p.counts[(int64_t)d * p.tiles + blockIdx.x] = s_cnt[d];
 }
 
 // Block d: the counts of digit d become their exclusive prefix sums over the tiles; the
@@ -239,10 +244,11 @@ __global__ void __launch_bounds__(kSortThreads, 3)
                    const uint32_t *__restrict__ poss, uint32_t *__restrict__ keys_out,
                    uint32_t *__restrict__ pos_out, int shift) {
   constexpr int kTile = kSortThreads * PER;
-  __shared__ __align__(16) uint16_t s_cnt[kSortWarps][kDigits];
-  __shared__ uint32_t s_key[kTile];
-  __shared__ uint16_t s_from[kTile];
-  __shared__ uint32_t s_start[kDigits];
+  extern __shared__ __align__(16) uint8_t s_all[];  // scatter_smem(PER)
+  auto s_cnt = reinterpret_cast<uint16_t (*)[kDigits]>(s_all);
+  uint32_t *s_start = reinterpret_cast<uint32_t *>(s_cnt + kSortWarps);
+  uint32_t *s_key = s_start + kDigits;
+  uint16_t *s_from = reinterpret_cast<uint16_t *>(s_key + kTile);
   __shared__ uint32_t s_sum[2][32];
   dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -250,9 +256,13 @@ __global__ void __launch_bounds__(kSortThreads, 3)
   const int64_t base = (int64_t)blockIdx.x * kTile;
   const int n = (int)(p.n - base < kTile ? p.n - base : kTile);
   // What every digit has before it over all tiles, and this digit in the tiles before this one.
-  const bool digit = tid <= (int)mask;
-  const uint32_t total = digit ? __ldg(p.totals + tid) : 0;
-  const uint32_t ahead = digit ? __ldg(p.counts + (int64_t)tid * p.tiles + blockIdx.x) : 0;
+  uint32_t total[2], ahead[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int d = 2 * tid + h;
+    total[h] = d <= (int)mask ? __ldg(p.totals + d) : 0;
+    ahead[h] = d <= (int)mask ? __ldg(p.counts + (int64_t)d * p.tiles + blockIdx.x) : 0;
+  }
   uint32_t key[PER], place[PER];
   bool bad = false;
 #pragma unroll
@@ -271,9 +281,9 @@ __global__ void __launch_bounds__(kSortThreads, 3)
     }
   }
   // Where a digit of this tile goes, less its first position in the tile.
-  const uint32_t to = block_exclusive(total, s_sum[1]) + ahead - s_start[tid];
-  __syncthreads();
-  s_start[tid] = to;
+  const uint32_t to = block_exclusive(total[0] + total[1], s_sum[1]);
+  s_start[2 * tid] = to + ahead[0] - s_start[2 * tid];
+  s_start[2 * tid + 1] = to + total[0] + ahead[1] - s_start[2 * tid + 1];
   __syncthreads();
   uint32_t pos[PER];
 #pragma unroll
@@ -294,6 +304,10 @@ __global__ void __launch_bounds__(kSortThreads, 3)
       pos_out[at] = pos[r];
     }
   }
+}
+
+constexpr size_t scatter_smem(int per) {
+  return kSortWarps * kDigits * 2 + kDigits * 4 + (size_t)kSortThreads * per * 6;
 }
 
 // Runs that start in each chunk, a warp a chunk.
@@ -498,30 +512,40 @@ __device__ __forceinline__ void sum_chunk(const EmbedGradParams &p, const Item &
       if (p.run_base && lead) p.row_ids_out[run] = (int32_t)cur;
     }
   };
+  // U entries at a time, the next ones' keys and positions on their way meanwhile.
+  uint4 next_key[U / 4], next_pos[U / 4];
+  const auto fetch = [&](int64_t e) {
+#pragma unroll
+    for (int i = 0; i < U / 4; ++i) {
+      next_key[i] = __ldg(reinterpret_cast<const uint4 *>(p.keys + e) + i);
+      next_pos[i] = __ldg(reinterpret_cast<const uint4 *>(p.pos + e) + i);
+    }
+  };
+  fetch(e0);
   for (int64_t e = e0; e < end; e += U) {
     uint32_t key[U];
     Slice<TY, V> s[U];
+    // past the chunk only its last run counts; kNoKey ends the walk
+    const int in_chunk = (int)min(e1 - e, (int64_t)U), in_walk = (int)min(end - e, (int64_t)U);
 #pragma unroll
-    for (int u = 0; u < U; u += 4) {
-      const uint4 k4 = __ldg(reinterpret_cast<const uint4 *>(p.keys + e + u));
-      const uint4 p4 = __ldg(reinterpret_cast<const uint4 *>(p.pos + e + u));
-      const uint32_t kk[4] = {k4.x, k4.y, k4.z, k4.w}, pp[4] = {p4.x, p4.y, p4.z, p4.w};
+    for (int i = 0; i < U / 4; ++i) {
+      const uint32_t kk[4] = {next_key[i].x, next_key[i].y, next_key[i].z, next_key[i].w};
+      const uint32_t pp[4] = {next_pos[i].x, next_pos[i].y, next_pos[i].z, next_pos[i].w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int64_t at_e = e + u + q;
-        const uint32_t k = kk[q];
-        // past the chunk only its last run counts; kNoKey ends the walk
-        key[u + q] = at_e < e1 || (at_e < end && k == last) ? k : kNoKey;
-        if (mine && key[u + q] < rows && !(skip && k == first)) {
+        const int u = 4 * i + q;
+        key[u] = u < in_chunk || (u < in_walk && kk[q] == last) ? kk[q] : kNoKey;
+        if (mine && key[u] < rows && !(skip && key[u] == first)) {
           int64_t at = (int64_t)pp[q] * p.dy_id_stride;
           if (!p.dy_linear) {
             const uint32_t t = fast_div(pp[q], p.by_ids);
             at = t * p.dy_token_stride + (int64_t)(pp[q] - t * (uint32_t)p.n_ids) * p.dy_id_stride;
           }
-          s[u + q].load(dy + at);
+          s[u].load(dy + at);
         }
       }
     }
+    if (e + U < end) fetch(e + U);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (key[u] == kNoKey) break;
@@ -544,19 +568,38 @@ __device__ __forceinline__ void sum_chunk(const EmbedGradParams &p, const Item &
 template <typename TG, int V>
 __device__ __forceinline__ void zero_rows(const EmbedGradParams &p, int64_t r0) {
   const int lane = threadIdx.x & 31;
-  const int64_t row = r0 + lane;
-  bool zero = false;
-  if (lane < p.zero_rows && row < p.rows) {
-    int64_t lo = 0, hi = p.n;  // the first key >= row
-    while (lo < hi) {
-      const int64_t mid = (lo + hi) >> 1;
-      if (__ldg(p.keys + mid) < (uint32_t)row)
-        lo = mid + 1;
-      else
-        hi = mid;
-    }
-    zero = lo >= p.n || __ldg(p.keys + lo) != (uint32_t)row;
+  // The first key >= r0: 32 probes at a time.
+  int64_t lo = 0, hi = p.n;
+  while (lo < hi) {
+    const int64_t step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const int less = __popc(__ballot_sync(0xffffffffu, at < hi && __ldg(p.keys + at) < (uint32_t)r0));
+    if (less == 0) break;
+    hi = min(lo + less * step, hi);
+    lo += (less - 1) * step + 1;
   }
+  // Which of the rows the keys from there on name, 32 keys at a time; behind a long run of
+  // one row, a search of its own per row.
+  const int64_t end = min(r0 + p.zero_rows, p.rows);
+  uint32_t named = 0;
+  bool done = false;
+  for (int i = 0; i < 4 && !done; ++i, lo += 32) {
+    const uint32_t k = lo + lane < p.n ? __ldg(p.keys + lo + lane) : kNoKey;
+    named |= __reduce_or_sync(0xffffffffu, k < (uint32_t)end ? 1u << (k - (uint32_t)r0) : 0);
+    done = __any_sync(0xffffffffu, k >= (uint32_t)end);
+  }
+  const int64_t row = r0 + lane;
+  if (!done && row < end && !(named >> lane & 1)) {
+    int64_t a = lo, b = p.n;  // the first key >= row
+    while (a < b) {
+      const int64_t mid = (a + b) >> 1;
+      if (__ldg(p.keys + mid) < (uint32_t)row)
+        a = mid + 1;
+      else
+        b = mid;
+    }
+    if (a < p.n && __ldg(p.keys + a) == (uint32_t)row) named |= 1u << lane;
+  }
+  const bool zero = row < end && !(named >> lane & 1);
   for (uint32_t todo = __ballot_sync(0xffffffffu, zero); todo; todo &= todo - 1) {
     TG *dst = static_cast<TG *>(p.grad) + (r0 + __ffs(todo) - 1) * p.grad_stride;
     if constexpr (V == 1) {
@@ -757,7 +800,7 @@ cudaError_t launch_embed_grad(EmbedGradParams p, int dy_dtype, int grad_dtype, v
   p.chunks = c.chunks;
   int bits = 1;
   while (bits < 32 && ((uint64_t)p.rows >> bits) != 0) ++bits;  // keys are 0 .. rows
-  p.passes = (bits + 8) / 9;
+  p.passes = (bits + 9) / 10;
   p.digit_bits = (bits + p.passes - 1) / p.passes;
   uint32_t *keys[2] = {reinterpret_cast<uint32_t *>(w + l.keys[0]), reinterpret_cast<uint32_t *>(w + l.keys[1])};
   uint32_t *pos[2] = {reinterpret_cast<uint32_t *>(w + l.pos[0]), reinterpret_cast<uint32_t *>(w + l.pos[1])};
@@ -772,6 +815,12 @@ cudaError_t launch_embed_grad(EmbedGradParams p, int dy_dtype, int grad_dtype, v
     if (e != cudaSuccess) return e;
   } else {
     const bool large = p.n >= kLargeTiles;
+    if (large) {  // the only kernels over 48 KB
+      static std::atomic<uint64_t> configured{0};
+      if ((e = raise_smem_ceiling(scatter_kernel<true, kPerLarge>, configured)) != cudaSuccess) return e;
+      static std::atomic<uint64_t> configured_next{0};
+      if ((e = raise_smem_ceiling(scatter_kernel<false, kPerLarge>, configured_next)) != cudaSuccess) return e;
+    }
     for (int pass = 0; pass < p.passes && e == cudaSuccess; ++pass) {
       const int shift = pass * p.digit_bits, in = pass & 1 ^ 1, out = pass & 1;
       const bool first = pass == 0;
@@ -784,7 +833,8 @@ cudaError_t launch_embed_grad(EmbedGradParams p, int dy_dtype, int grad_dtype, v
       if (e == cudaSuccess)
         e = launch(large ? (first ? scatter_kernel<true, kPerLarge> : scatter_kernel<false, kPerLarge>)
                          : (first ? scatter_kernel<true, kPerSmall> : scatter_kernel<false, kPerSmall>),
-                   p.tiles, kSortThreads, 0, stream, 1, p, keys[in], pos[in], keys[out], pos[out], shift);
+                   p.tiles, kSortThreads, scatter_smem(large ? kPerLarge : kPerSmall), stream, 1, p, keys[in],
+                   pos[in], keys[out], pos[out], shift);
     }
     if (e != cudaSuccess) return e;
     p.keys = keys[(p.passes - 1) & 1];

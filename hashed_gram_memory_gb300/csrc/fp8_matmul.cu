@@ -22,7 +22,8 @@
 //   fp8_matmul_kernel: one CTA per SM, 128 x up to 128 tiles, for products too small to
 //     fill the pairs; where even those leave SMs idle (a few rows of a: reading b is the
 //     work), the CTAs of a cluster share a tile, each with a part of K, and add their
-//     parts through distributed shared memory in rank order.
+//     parts through distributed shared memory in rank order; two such CTAs an SM, whose
+//     stages together have most of a decode step's weights on the way at once.
 // Warps:
 //   0     TMA producer: a ring of stages, each a 128-byte slice along K of the tile's rows
 //         of a and b (128-byte swizzle);
@@ -55,6 +56,11 @@ constexpr uint32_t kStageBudget = 192 * 1024;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kScaleCol = 2 * kQMax;  // scale words: two buffers of 4 (b) + 4 (a) columns
 constexpr size_t kSmemBytes = 1024 + kStageBudget + kScaleSlots * kSlotBytes + 512;
+// The CTAs that share a tile's K have one accumulator, half the TMEM and half the shared memory.
+constexpr uint32_t kSplitStageBudget = 102 * 1024;
+constexpr uint32_t kSplitTmemCols = 256, kSplitScaleCol = kQMax;
+constexpr size_t kSplitSmemBytes = 1024 + kSplitStageBudget + kScaleSlots * kSlotBytes + 512;
+static_assert(2 * (kSplitSmemBytes + 1024 + 64) <= 228 * 1024);
 
 struct MatmulDev {
   const uint8_t *a_scale, *b_scale;
@@ -232,12 +238,14 @@ struct Drain {
 };
 
 template <typename TO, bool MULTI, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
     fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                       const __grid_constant__ MatmulDev p) {
   extern __shared__ uint8_t sm_raw[];
   uint8_t *sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
-  uint8_t *slots = sm + kStageBudget;
+  uint8_t *slots = sm + (SPLIT ? kSplitStageBudget : kStageBudget);
+  constexpr uint32_t kCols = SPLIT ? kSplitTmemCols : kTmemCols;
+  constexpr uint32_t kScales = SPLIT ? kSplitScaleCol : kScaleCol;
   uint64_t *full = reinterpret_cast<uint64_t *>(slots + kScaleSlots * kSlotBytes);
   uint64_t *empty = full + kMaxStages;
   uint64_t *sc_full = empty + kMaxStages;
@@ -278,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(tmem_slot)),
-                 "r"(kTmemCols)
+                 "r"(kCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -336,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!(ok = warp_wait(sc_full + slot, (batch >> 1) & 1, abort_flag, p))) break;
               asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             }
-            sp = tmem + kScaleCol + (kb >> 2 & 1) * 8, sq = sp + 4;
+            sp = tmem + kScales + (kb >> 2 & 1) * 8, sq = sp + 4;
             const uint64_t src =
                 smem_desc_scales(smem_u32(slots + slot * kSlotBytes + (kb >> 2 & 3) * kGroupBytes));
             const bool done = (kb & 15) == 12 || kb + 4 >= kblocks;  // with this slot
@@ -477,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) drain_phase(mma_done, 0, p.wait_limit_ns);
     __syncwarp();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols)
                  : "memory");
   }
 }
@@ -793,7 +801,7 @@ cudaError_t device_info(DeviceInfo &out) {
     e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
     for (int i = 0; i < 2 * kForms && e == cudaSuccess; ++i)
       e = cudaFuncSetAttribute(kernel_of(i / 2, i & 1), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)(i / 2 >= kPair ? kPairSmemBytes : kSmemBytes));
+                               (int)(i / 2 >= kPair ? kPairSmemBytes : i / 2 == kSplit ? kSplitSmemBytes : kSmemBytes));
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -860,12 +868,13 @@ cudaError_t launch_fp8_matmul(const MatmulParams &p, int out_dtype, cudaStream_t
   d.tiles = d.tiles_p * d.tiles_q;
   int form = pair ? (d.segments > 1 ? kPairMulti : kPair) : (d.segments > 1 ? kSingleMulti : kSingle);
   if (!pair) {
-    // Clusters that share K while there are SMs for them and each CTA keeps two blocks.
-    int64_t splits = info.sms / d.tiles;
+    // Clusters that share K while there is room for them and each CTA keeps two blocks.
+    int64_t splits = 2 * info.sms / d.tiles;
     splits = splits > 8 ? 8 : splits;
     splits = splits > d.kblocks / 2 ? d.kblocks / 2 : splits;
     if (splits > 1 && ceil_div(d.kblocks, splits) <= kSegmentBlocks) {
       d.splits = (int32_t)splits;
+      d.stages = (int32_t)(kSplitStageBudget / ((kP + d.q_tile) * 128));
       form = kSplit;
     }
   }
@@ -878,7 +887,7 @@ cudaError_t launch_fp8_matmul(const MatmulParams &p, int out_dtype, cudaStream_t
     return launch(kernel, 2 * (d.tiles < info.pairs ? d.tiles : info.pairs), kPairThreads, kPairSmemBytes,
                   stream, 2, map_a, map_b, d);
   if (form == kSplit)
-    return launch(kernel, d.tiles * d.splits, kThreads, kSmemBytes, stream, d.splits, map_a, map_b, d);
+    return launch(kernel, d.tiles * d.splits, kThreads, kSplitSmemBytes, stream, d.splits, map_a, map_b, d);
   return launch(kernel, d.tiles < info.sms ? d.tiles : info.sms, kThreads, kSmemBytes, stream, 1, map_a,
                 map_b, d);
 }

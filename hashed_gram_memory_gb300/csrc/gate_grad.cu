@@ -18,8 +18,8 @@
 // shared-memory stages, refilled as soon as a token is in registers.  (Loads into
 // registers instead, two blocks an SM: see the measurements at the launch.)  Narrow
 // tokens take a power of two lanes of a warp.  dalpha crosses tokens: each block adds its tokens in
-// order and writes one partial; a second launch of one block adds the partials in
-// a fixed order in fp64, so the result does not depend on timing.
+// order and writes one partial; a second launch of one block adds the partials as
+// a tree in a fixed order, so the result does not depend on timing.
 #include <atomic>
 
 #include "bulk_copy.cuh"
@@ -225,10 +225,9 @@ __global__ void __launch_bounds__(1024) gate_grad_block_kernel(const __grid_cons
 
 // The same with the tokens' bytes brought by bulk copies: a ring of p.stages stages of
 // 14 D bytes (k, stream 0, dy), the next tokens' copies in flight while one is worked on.
-__device__ __forceinline__ void issue_token(const GateGradParams &p, int64_t t, uint8_t *stage,
-                                            uint64_t *full, uint8_t *state_slot) {
+__device__ __forceinline__ void issue_token(const GateGradParams &p, int64_t t, uint8_t state,
+                                            uint8_t *stage, uint64_t *full, uint8_t *state_slot) {
   const uint32_t D = p.D;
-  const uint8_t state = p.state ? p.state[t] : 0;
   *state_slot = state;
   if (state == kBad) {
     mbar_arrive(full);
@@ -258,10 +257,14 @@ __global__ void __launch_bounds__(512, 2) gate_grad_bulk_kernel(const __grid_con
   }
   dependency_wait();
   __syncthreads();
-  int64_t ahead = blockIdx.x;  // thread 0: the next token to issue
-  if (tid == 0)
-    for (int s = 0; s < p.stages && ahead < p.T; ++s, ahead += gridDim.x)
-      issue_token(p, ahead, s_stage + s * stage_bytes, s_full + s, s_state + s);
+  // The first tokens: a lane each.
+  if (tid < p.stages && blockIdx.x + (int64_t)tid * gridDim.x < p.T) {
+    const int64_t t = blockIdx.x + (int64_t)tid * gridDim.x;
+    issue_token(p, t, p.state ? p.state[t] : 0, s_stage + tid * stage_bytes, s_full + tid, s_state + tid);
+  }
+  // Thread 0: the next token to issue, and its state ahead of time.
+  int64_t ahead = blockIdx.x + (int64_t)p.stages * gridDim.x;
+  uint8_t ahead_state = tid == 0 && p.state && ahead < p.T ? p.state[ahead] : 0;
   const float4 alpha = make_float4(__ldg(p.alpha), __ldg(p.alpha + 1), __ldg(p.alpha + 2),
                                    __ldg(p.alpha + 3));
   float4 da = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -294,7 +297,7 @@ __global__ void __launch_bounds__(512, 2) gate_grad_bulk_kernel(const __grid_con
       if (tid == 0) {
         if (p.status) atomicOr(p.status, ENGRAM_FLAG_TIMEOUT);
         // the copies in flight land, or give up likewise, before the block's memory goes
-        for (int64_t u = t; u < ahead; u += gridDim.x) {
+        for (int64_t u = t; u < ahead && u < p.T; u += gridDim.x) {
           wait_bounded(s_full + s, p.wait_limit_ns, phase);
           if (++s == p.stages) s = 0, phase ^= 1;
         }
@@ -303,8 +306,9 @@ __global__ void __launch_bounds__(512, 2) gate_grad_bulk_kernel(const __grid_con
     }
     // Every thread has its columns: the stage takes the next token.
     if (tid == 0 && ahead < p.T) {
-      issue_token(p, ahead, s_stage + s * stage_bytes, s_full + s, s_state + s);
+      issue_token(p, ahead, ahead_state, s_stage + s * stage_bytes, s_full + s, s_state + s);
       ahead += gridDim.x;
+      if (p.state && ahead < p.T) ahead_state = p.state[ahead];
     }
     if (++s == p.stages) s = 0, phase ^= 1;
     if (state == kBad || state == kDead) {
@@ -378,9 +382,9 @@ __global__ void __launch_bounds__(256) gate_grad_warp_kernel(const __grid_consta
 
 __global__ void __launch_bounds__(256) dalpha_kernel(const float4 *__restrict__ partial, int n,
                                                      float *__restrict__ dalpha) {
-  __shared__ double s[8][4];
+  __shared__ float s[8][4];
   dependency_wait();
-  double v[4] = {0, 0, 0, 0};
+  float v[4] = {0, 0, 0, 0};
   for (int i = threadIdx.x; i < n; i += 256) {
     const float4 q = partial[i];
     v[0] += q.x, v[1] += q.y, v[2] += q.z, v[3] += q.w;
@@ -394,9 +398,9 @@ __global__ void __launch_bounds__(256) dalpha_kernel(const float4 *__restrict__ 
     for (int i = 0; i < 4; ++i) s[threadIdx.x >> 5][i] = v[i];
   __syncthreads();
   if (threadIdx.x < 4) {
-    double t = 0;
+    float t = 0;
     for (int w = 0; w < 8; ++w) t += s[w][threadIdx.x];
-    dalpha[threadIdx.x] = (float)t;
+    dalpha[threadIdx.x] = t;
   }
 }
 
