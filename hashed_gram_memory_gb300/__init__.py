@@ -802,17 +802,28 @@ def _fp8_operand(t, name):
     import torch
     if t.dtype != torch.uint8 or not t.is_cuda:
         _need(t, (torch.uint8,), name, contiguous=False)
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise EngramError(ERR_INVALID_ARG, f"{name} must be two-dimensional")
-    return *t.shape, _strides(t, name)[0]
+    return shape[0], shape[1], _strides(t, name)[0]
 
 
 def _fp8_scales(t, rows, cols, block, name):
     import torch
-    want = (-(-rows // block), -(-cols // FP8_BLOCK))
-    _need(t, (torch.uint8,), name)
+    want = ((rows + block - 1) // block, (cols + FP8_BLOCK - 1) // FP8_BLOCK)
+    if t.dtype != torch.uint8 or not t.is_cuda or not t.is_contiguous():
+        _need(t, (torch.uint8,), name)
     if t.shape != want:
         raise EngramError(ERR_INVALID_ARG, f"{name} must be {list(want)}")
+    return t.data_ptr()
+
+
+def _fp8_copy(out, at, rows, cols, block):
+    """The pointers and stride of one of the quantiser's copies, out[at] and out[at + 1]."""
+    r, c, stride = _fp8_operand(out[at], "q")
+    if r != rows or c != cols:
+        raise EngramError(ERR_INVALID_ARG, f"q must be {[rows, cols]}")
+    return out[at].data_ptr(), stride, _fp8_scales(out[at + 1], rows, cols, block, "scales")
 
 
 def engram_fp8_quantise(x, block_rows: int = 1, rows: bool = True, cols: bool = False, out=None,
@@ -825,30 +836,20 @@ def engram_fp8_quantise(x, block_rows: int = 1, rows: bool = True, cols: bool = 
     xd = _dtype(x, "x")
     if x.dim() != 2:
         raise EngramError(ERR_INVALID_ARG, "x must be [M, K]")
-    if block_rows not in (1, FP8_BLOCK):
+    if block_rows != 1 and block_rows != FP8_BLOCK:
         raise EngramError(ERR_INVALID_ARG, f"block_rows must be 1 or {FP8_BLOCK}")
     M, K = x.shape
-    dims = ([(M, K)] if rows else []) + ([(K, M)] if cols else [])
     if out is None:
         import torch
         out = []
-        for r, c in dims:
+        for r, c in ([(M, K)] if rows else []) + ([(K, M)] if cols else []):
             out += [fp8_empty(r, c, x.device),
                     torch.empty((-(-r // block_rows), -(-c // FP8_BLOCK)), dtype=torch.uint8,
                                 device=x.device)]
-    if len(out) != 2 * len(dims):
+    if len(out) != 2 * (bool(rows) + bool(cols)):
         raise EngramError(ERR_INVALID_ARG, "out must hold a value and a scale buffer per copy")
-    args = []
-    for i, (r, c) in enumerate(dims):
-        q, s = out[2 * i], out[2 * i + 1]
-        qr, qc, stride = _fp8_operand(q, "q")
-        if qr != r or qc != c:
-            raise EngramError(ERR_INVALID_ARG, f"q must be {[r, c]}")
-        _fp8_scales(s, r, c, block_rows, "scales")
-        args.append((q.data_ptr(), stride, s.data_ptr()))
-    none = (None, 0, None)
-    q = args[0] if rows else none
-    qt = args[-1] if cols else none
+    q = _fp8_copy(out, 0, M, K, block_rows) if rows else (None, 0, None)
+    qt = _fp8_copy(out, 2 if rows else 0, K, M, block_rows) if cols else (None, 0, None)
     _check(lib.engram_fp8_quantise(x.data_ptr(), xd, M, K, max(_strides(x, "x")[0], K), block_rows,
                                    *q, *qt, _ptr(status), _stream(stream)), "engram_fp8_quantise")
     return tuple(out)
@@ -864,16 +865,16 @@ def engram_fp8_matmul(a, a_scale, b, b_scale, a_block: int = 1, b_block: int = 1
         raise EngramError(ERR_INVALID_ARG, "a and b disagree on K")
     if a_block not in (1, FP8_BLOCK) or b_block not in (1, FP8_BLOCK):
         raise EngramError(ERR_INVALID_ARG, f"a_block and b_block must be 1 or {FP8_BLOCK}")
-    _fp8_scales(a_scale, M, K, a_block, "a_scale")
-    _fp8_scales(b_scale, N, K, b_block, "b_scale")
+    pa = _fp8_scales(a_scale, M, K, a_block, "a_scale")
+    pb = _fp8_scales(b_scale, N, K, b_block, "b_scale")
     if out is None:
         import torch
         out = torch.empty((M, N), dtype=out_dtype or torch.float32, device=a.device)
     od = _dtype(out, "out")
     if out.shape != (M, N):
         raise EngramError(ERR_INVALID_ARG, f"out must be {[M, N]}")
-    _check(lib.engram_fp8_matmul(a.data_ptr(), sa, a_scale.data_ptr(), a_block, b.data_ptr(), sb,
-                                 b_scale.data_ptr(), b_block, M, N, K, out.data_ptr(), od,
+    _check(lib.engram_fp8_matmul(a.data_ptr(), sa, pa, a_block, b.data_ptr(), sb, pb, b_block, M,
+                                 N, K, out.data_ptr(), od,
                                  max(_strides(out, "out")[0], N), _ptr(status), _stream(stream)),
            "engram_fp8_matmul")
     return out
