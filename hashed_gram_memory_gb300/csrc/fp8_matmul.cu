@@ -34,6 +34,8 @@
 //   4..   epilogue: TMEM lanes 32*(warp%4).., stores.
 // Every wait is bounded as in wkv_gemm.cu: one that gives up sets ENGRAM_FLAG_TIMEOUT and
 // leaves the tiles not yet stored unwritten.
+#include <math.h>
+
 #include <mutex>
 
 #include "launch.cuh"
@@ -106,6 +108,15 @@ __device__ __forceinline__ void umma_fp8(uint32_t d, uint64_t p_desc, uint64_t q
 __device__ __forceinline__ uint32_t load_cluster(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float4 load4_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
@@ -464,15 +475,24 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
       ok &= load_cluster(map_to_rank(smem_u32(const_cast<int *>(abort_flag)), r)) == 0;
     int64_t tp, tq;
     tile_at(p, first_tile, tp, tq);
-    const int64_t n = tp * kP + (threadIdx.x & (kP - 1));
+    // A warp a column (128 outputs of one row of out), four outputs a lane.
+    const int64_t n = tp * kP + lane * 4;
     const int q_end = qt * (rank + 1) / p.splits;
-    for (int q = qt * rank / p.splits + threadIdx.x / kP; q < q_end; q += kThreads / kP) {
+    for (int q = qt * rank / p.splits + warp; q < q_end; q += kThreads / 32) {
       const int64_t m = tq * qt + q;
-      const uint32_t at = smem_u32(sm) + (q * kP + (threadIdx.x & (kP - 1))) * 4;
-      float sum = 0.f;
-      for (int r = 0; r < p.splits; ++r) sum += __uint_as_float(load_cluster(map_to_rank(at, r)));
-      if (ok && n < p.N && m < p.M)
-        store_out(static_cast<TO *>(p.out) + m * p.out_stride + n, __float_as_uint(sum));
+      const uint32_t at = smem_u32(sm) + (q * kP + lane * 4) * 4;
+      float4 v[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        v[r] = r < p.splits ? load4_cluster(map_to_rank(at, r)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int r = 1; r < 8; ++r)
+        v[0].x += v[r].x, v[0].y += v[r].y, v[0].z += v[r].z, v[0].w += v[r].w;
+      const float sum[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+      TO *out = static_cast<TO *>(p.out) + m * p.out_stride + n;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (ok && n + i < p.N && m < p.M) store_out(out + i, __float_as_uint(sum[i]));
     }
     cluster_sync();  // no CTA leaves while another may still read its part
   }
@@ -844,40 +864,52 @@ cudaError_t launch_fp8_matmul(const MatmulParams &p, int out_dtype, cudaStream_t
   const int64_t segments = ceil_div(d.kblocks, kSegmentBlocks);
   d.seg_blocks = (int32_t)(ceil_div(ceil_div(d.kblocks, segments), 4) * 4);
   d.segments = (int32_t)ceil_div(d.kblocks, d.seg_blocks);
-  // Pairs where their tiles occupy most of the SMs.
-  const bool pair = info.pairs > 0 && p.M > 128 && p.N > 128 &&
-                    ceil_div(p.N, 2 * kP) * ceil_div(p.M, kPairQMax) * 2 >= info.pairs;
-  d.splits = 1;
-  if (pair) {
-    // The width of a tile along a: the one whose whole waves over the pairs take least (a
-    // wave lasts as long as its tile is wide, and a little).
-    d.tiles_p = ceil_div(p.N, 2 * kP);
-    int64_t best = INT64_MAX;
+  // The form and the width of a tile along a go by an estimate of their time in microseconds,
+  // fitted to both forms over M 1 .. 16,384, N 1024 and 4096, K 256 .. 8192 (it picks the
+  // faster one there, or one within 5 %):
+  //   single: 1.3 + 0.23 a block of K, for each wave of tiles over the SMs;
+  //   pairs:  2.1 + max(0.2, 0.00118 (width + 16)) a block, but at least what draining the
+  //           tile takes, 4.6 at 240 columns; for each wave over the pairs, and 1.5 once.
+  const double kb = d.kblocks;
+  const int q_single = (int)(p.M < kQMax ? ceil_div(p.M, 16) * 16 : kQMax);
+  const int64_t single_tiles = ceil_div(p.N, kP) * ceil_div(p.M, q_single);
+  const double single_us = ceil_div(single_tiles, info.sms) * (1.3 + 0.23 * kb);
+  double pair_us = HUGE_VAL;
+  if (info.pairs > 0 && p.M > 128 && p.N > 128) {
     for (int qt = kPairQMax; qt >= 128; qt -= 16) {
-      const int64_t cost = ceil_div(d.tiles_p * ceil_div(p.M, qt), info.pairs) * (qt + 16);
-      if (cost < best) best = cost, d.q_tile = qt;
+      const int64_t waves = ceil_div(ceil_div(p.N, 2 * kP) * ceil_div(p.M, qt), info.pairs);
+      const double block = fmax(0.2, 0.00118 * (qt + 16));
+      const double us = 1.5 + waves * fmax(4.6 * qt / kPairQMax, 2.1 + block * kb);
+      if (us < pair_us) pair_us = us, d.q_tile = qt;
     }
+  }
+  const bool pair = pair_us < single_us;
+  d.splits = 1;
+  int form;
+  if (pair) {
+    form = d.segments > 1 ? kPairMulti : kPair;
+    d.tiles_p = ceil_div(p.N, 2 * kP);
     d.stages = (int32_t)(kPairStageBudget / ((kP + d.q_tile / 2) * 128));
   } else {
+    form = d.segments > 1 ? kSingleMulti : kSingle;
     d.tiles_p = ceil_div(p.N, kP);
-    d.q_tile = (int32_t)(p.M < kQMax ? ceil_div(p.M, 16) * 16 : kQMax);
+    d.q_tile = q_single;
     d.stages = (int32_t)(kStageBudget / ((kP + d.q_tile) * 128));
+    // Eight CTAs share K where there is room for them and seven eighths of the blocks' time
+    // (0.2 each) is more than the joining takes: measured 1 + 0.02 a column of the tile and
+    // 0.06 a tile (16 x 4096 x 6144: 9.0 us against 14.2; 16 x 4096 x 1024: 6.4 against 5.4).
+    if (8 * single_tiles <= 2 * info.sms && ceil_div(d.kblocks, 8) <= kSegmentBlocks &&
+        0.175 * kb > 1 + 0.02 * d.q_tile + 0.06 * single_tiles) {
+      form = kSplit;
+      d.splits = 8;
+      d.segments = 1;  // a CTA's part of K is one
+      d.seg_blocks = kSegmentBlocks;
+      d.stages = (int32_t)(kSplitStageBudget / ((kP + d.q_tile) * 128));
+    }
   }
   if (d.stages > kMaxStages) d.stages = kMaxStages;
   d.tiles_q = ceil_div(p.M, d.q_tile);
   d.tiles = d.tiles_p * d.tiles_q;
-  int form = pair ? (d.segments > 1 ? kPairMulti : kPair) : (d.segments > 1 ? kSingleMulti : kSingle);
-  if (!pair) {
-    // Clusters that share K while there is room for them and each CTA keeps two blocks.
-    int64_t splits = 2 * info.sms / d.tiles;
-    splits = splits > 8 ? 8 : splits;
-    splits = splits > d.kblocks / 2 ? d.kblocks / 2 : splits;
-    if (splits > 1 && ceil_div(d.kblocks, splits) <= kSegmentBlocks) {
-      d.splits = (int32_t)splits;
-      d.stages = (int32_t)(kSplitStageBudget / ((kP + d.q_tile) * 128));
-      form = kSplit;
-    }
-  }
   CUtensorMap map_a, map_b;
   if (!make_map(&map_a, p.a, p.M, p.K, p.a_stride, (uint32_t)(pair ? d.q_tile / 2 : d.q_tile)) ||
       !make_map(&map_b, p.b, p.N, p.K, p.b_stride, kP))
