@@ -33,6 +33,7 @@ namespace {
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
 constexpr int kDigits = 1024;      // most digits of a pass: two a thread
 constexpr int kCountSort = 4096;   // most pairs sorted by counting
+constexpr uint32_t kNoKey = 0xFFFFFFFFu;
 
 // Pairs a thread sorts of a tile: few where there are few tiles, so that they fill the SMs.
 constexpr int kPerLarge = 8, kPerSmall = 2;
@@ -117,10 +118,10 @@ __device__ __forceinline__ void rank_tile(const uint32_t (&key)[PER], int n, int
 }
 
 // The sort of up to kCountSort pairs: a pair's place is the number of pairs with a smaller
-// key, or an equal one and an earlier position.  Each warp places 8 pairs, its lanes
-// comparing them with 4 keys a load; positions are compared only inside the block's own 64
+// key, or an equal one and an earlier position.  Each warp places 4 pairs, its lanes
+// comparing them with 4 keys a load; positions are compared only inside the block's own 32
 // pairs (before them equal keys count, behind them they do not).
-constexpr int kCountThreads = 256, kCountPairs = 64;
+constexpr int kCountThreads = 256, kCountOwn = 4, kCountPairs = kCountThreads / 32 * kCountOwn;
 
 __global__ void __launch_bounds__(kCountThreads)
     count_sort_kernel(const __grid_constant__ EmbedGradParams p) {
@@ -137,40 +138,40 @@ __global__ void __launch_bounds__(kCountThreads)
   if (blockIdx.x == 0 && tid == 0) *p.long_count = 0;
   __syncthreads();
   const int first = blockIdx.x * kCountPairs;  // a multiple of 4, as are all the bounds below
-  const int mine = first + warp * 8;
-  uint32_t key[8];
-  int count[8];
+  const int mine = first + warp * kCountOwn;
+  uint32_t key[kCountOwn];
+  int count[kCountOwn];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < kCountOwn; ++i) {
     key[i] = mine + i < n ? s_key[mine + i] : 0;
     count[i] = 0;
   }
   const int end = (n + 3) / 4, own = first / 4, after = min(end, own + kCountPairs / 4);
-#pragma unroll 2
+#pragma unroll 4
   for (int j = lane; j < own; j += 32) {
     const uint4 k = s_key4[j];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < kCountOwn; ++i)
       count[i] += (k.x <= key[i]) + (k.y <= key[i]) + (k.z <= key[i]) + (k.w <= key[i]);
   }
   for (int j = own + lane; j < after; j += 32) {
     const uint4 k = s_key4[j];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kCountOwn; ++i) {
       const int at = mine + i - 4 * j;  // positions 4j .. 4j+3 against this pair's
       count[i] += (k.x < key[i] || (k.x == key[i] && at > 0)) + (k.y < key[i] || (k.y == key[i] && at > 1)) +
                   (k.z < key[i] || (k.z == key[i] && at > 2)) + (k.w < key[i] || (k.w == key[i] && at > 3));
     }
   }
-#pragma unroll 2
+#pragma unroll 4
   for (int j = after + lane; j < end; j += 32) {
     const uint4 k = s_key4[j];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < kCountOwn; ++i)
       count[i] += (k.x < key[i]) + (k.y < key[i]) + (k.z < key[i]) + (k.w < key[i]);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < kCountOwn; ++i) {
     const int place = __reduce_add_sync(0xffffffffu, count[i]);
     if (lane == i && mine + i < n) {
       p.keys[place] = key[i];
@@ -308,6 +309,37 @@ __global__ void __launch_bounds__(kSortThreads, 3)
 
 constexpr size_t scatter_smem(int per) {
   return kSortWarps * kDigits * 2 + kDigits * 4 + (size_t)kSortThreads * per * 6;
+}
+
+// Both of the next two kernels' work for lists that one block reads quickly.
+constexpr int kRunsSmall = 16384;
+__global__ void __launch_bounds__(kSortThreads) runs_small_kernel(const __grid_constant__ EmbedGradParams p) {
+  __shared__ uint32_t s_sum[32];
+  dependency_wait();
+  constexpr int kEach = kRunsSmall / kSortThreads;  // at most, a multiple of 4
+  const int n = (int)p.n, per = ((n + kSortThreads - 1) / kSortThreads + 3) / 4 * 4;
+  const int e0 = threadIdx.x * per;
+  uint32_t starts = 0;  // a bit an entry
+  uint32_t before = e0 > 0 && e0 < n ? __ldg(p.keys + e0 - 1) : kNoKey;
+#pragma unroll
+  for (int i = 0; i < kEach; i += 4) {
+    if (i < per && e0 + i < n) {
+      const uint4 k4 = __ldg(reinterpret_cast<const uint4 *>(p.keys + e0 + i));
+      const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (e0 + i + q < n && k[q] < (uint32_t)p.rows && k[q] != before) starts |= 1u << (i + q);
+        before = k[q];
+      }
+    }
+  }
+  const uint32_t base = block_exclusive(__popc(starts), s_sum);
+  for (int i = 0; i < per && e0 + i < n; ++i)  // chunks that start here (their length is 4 at least)
+    if ((e0 + i) % p.chunk == 0) p.run_base[(e0 + i) / p.chunk] = base + __popc(starts & ((1u << i) - 1));
+  if (threadIdx.x == kSortThreads - 1) {
+    p.run_base[p.chunks] = base + __popc(starts);
+    *p.count_out = (int32_t)(base + __popc(starts));
+  }
 }
 
 // Runs that start in each chunk, a warp a chunk.
@@ -451,7 +483,6 @@ __device__ __forceinline__ void write_partial(float *dst, const float (&acc)[V])
   }
 }
 
-constexpr uint32_t kNoKey = 0xFFFFFFFFu;
 constexpr int kSumThreads = 128;
 
 // A group's place: the chunk and the columns it works on.
@@ -600,14 +631,26 @@ __device__ __forceinline__ void zero_rows(const EmbedGradParams &p, int64_t r0) 
     if (a < p.n && __ldg(p.keys + a) == (uint32_t)row) named |= 1u << lane;
   }
   const bool zero = row < end && !(named >> lane & 1);
-  for (uint32_t todo = __ballot_sync(0xffffffffu, zero); todo; todo &= todo - 1) {
-    TG *dst = static_cast<TG *>(p.grad) + (r0 + __ffs(todo) - 1) * p.grad_stride;
-    if constexpr (V == 1) {
-      for (int c = lane; c < p.D; c += 32) dst[c] = TG(0);
-    } else {
-      constexpr int kWord = 16 / (int)sizeof(TG);
-      for (int c = lane * kWord; c < p.D; c += 32 * kWord)
-        __stcs(reinterpret_cast<uint4 *>(dst + c), make_uint4(0, 0, 0, 0));
+  const uint32_t todo = __ballot_sync(0xffffffffu, zero);
+  constexpr int kWord = V == 1 ? 1 : 16 / (int)sizeof(TG);  // values stored at once
+  const uint32_t words = (uint32_t)p.D / kWord;
+  TG *base = static_cast<TG *>(p.grad) + r0 * p.grad_stride;
+  const auto clear = [](TG *dst) {
+    if constexpr (V == 1)
+      *dst = TG(0);
+    else
+      __stcs(reinterpret_cast<uint4 *>(dst), make_uint4(0, 0, 0, 0));
+  };
+  if (words >= 64) {  // wide rows: one after the other
+    for (uint32_t left = todo; left; left &= left - 1) {
+      TG *dst = base + (__ffs(left) - 1) * p.grad_stride;
+      for (uint32_t c = lane; c < words; c += 32) clear(dst + c * kWord);
+    }
+  } else {  // narrow ones: their words through the lanes, whichever row they are in
+#pragma unroll 4
+    for (uint32_t i = lane; i < words * (uint32_t)p.zero_rows; i += 32) {
+      const uint32_t r = words == 1 ? i : __umulhi(i, p.zero_magic);
+      if (todo >> r & 1) clear(base + r * p.grad_stride + (i - r * words) * kWord);
     }
   }
 }
@@ -749,6 +792,8 @@ cudaError_t launch_sums(EmbedGradParams p, cudaStream_t stream) {
   // Rows a warp of the zeroing blocks looks up: 32, or fewer wide ones, about 64 KB.
   p.zero_rows = 32;
   while (p.zero_rows > 1 && (int64_t)p.zero_rows * p.D * (int)sizeof(TG) > 65536) p.zero_rows /= 2;
+  const uint32_t words = p.D / (V == 1 ? 1 : 16 / (int)sizeof(TG));
+  p.zero_magic = (uint32_t)(((1ull << 32) + words - 1) / words);  // exact below 2^32 / words words
   const int64_t per = kSumThreads / 32 * p.zero_rows;
   p.zero_blocks = p.run_base || p.accumulate ? 0 : (p.rows + per - 1) / per;
   const int64_t blocks = p.sum_blocks + p.zero_blocks;
@@ -840,7 +885,9 @@ cudaError_t launch_embed_grad(EmbedGradParams p, int dy_dtype, int grad_dtype, v
     p.keys = keys[(p.passes - 1) & 1];
     p.pos = pos[(p.passes - 1) & 1];
   }
-  if (sparse && p.n > 0) {
+  if (sparse && p.n > 0 && p.n <= kRunsSmall) {
+    if ((e = launch(runs_small_kernel, 1, kSortThreads, 0, stream, 1, p)) != cudaSuccess) return e;
+  } else if (sparse && p.n > 0) {
     e = launch(count_runs_kernel, (p.chunks + 7) / 8, 256, 0, stream, 1, p);
     if (e == cudaSuccess) e = launch(scan_runs_kernel, 1, 1024, 0, stream, 1, p);
     if (e != cudaSuccess) return e;

@@ -6,12 +6,13 @@
 // x 2^-e is exact in fp32: the only rounding is the one to e4m3, and the matrix product
 // can hand the byte to the tensor cores as it is.  With max|B| = m 2^x, 1 <= m < 2, and
 // 448 = 1.75 * 2^8, e = x - 8, or x - 7 when m > 1.75: integer arithmetic on the bits of
-// the maximum.  Magnitudes are compared as integers, so a NaN or infinity wins; such a
-// block gets the NaN scale 0xFF and NaN bytes 0x7F.
+// the maximum.  The maximum keeps NaN, and a NaN or infinity gives its block the NaN
+// scale 0xFF and NaN bytes 0x7F.
 //
 // HBM-bound: x read once, a byte a value written (two with the transposed copy).
-//   rows kernel: 16 lanes a block of 128 values (8 each), four blocks of loads in
-//     flight a thread;
+//   linear kernel (x and q without gaps, K a multiple of 128: block b is values 128 b ..):
+//     8 lanes a block, 16 values each in two runs of 8, two blocks in flight a thread;
+//   rows kernel (any strides and widths): 16 lanes a block, 8 values each;
 //   tile kernel (a transposed copy, or 128 x 128 blocks): a 128 x 128 tile in the
 //     registers of 256 threads -- 16 rows x 4 columns each, so row maxima are warp
 //     reductions and column maxima one exchange through shared memory; the transposed
@@ -31,8 +32,6 @@
 namespace engram {
 namespace {
 
-constexpr uint32_t kNaN4 = 0x7F7F7F7Fu;
-
 // The scale byte of a block whose largest magnitude has these bits.
 __device__ __forceinline__ uint32_t scale_byte(uint32_t bits) {
   const int32_t x = (int32_t)(bits >> 23);
@@ -44,15 +43,34 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t bits) {
 // 2^(127 - s): what a block's values are multiplied by (s in [0, 247]: a normal number).
 __device__ __forceinline__ float inverse_scale(uint32_t s) { return __uint_as_float((254u - s) << 23); }
 
-__device__ __forceinline__ uint32_t quantise4(float a, float b, float c, float d, uint32_t s) {
-  if (s == 255) return kNaN4;
-  const float m = inverse_scale(s);
+// What a block's values are multiplied by: NaN for the NaN scale, so that they become NaN.
+__device__ __forceinline__ float multiplier(uint32_t s) {
+  return s == 255 ? __uint_as_float(0x7FFFFFFFu) : inverse_scale(s);
+}
+
+__device__ __forceinline__ uint32_t quantise4(float a, float b, float c, float d, float m) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a * m, b * m), __NV_SATFINITE, __NV_E4M3);
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c * m, d * m), __NV_SATFINITE, __NV_E4M3);
   return lo | hi << 16;
 }
 
-__device__ __forceinline__ uint32_t mag(float f) { return __float_as_uint(f) & 0x7FFFFFFFu; }
+// The larger magnitude; NaN if either is NaN (its exponent then marks the block).
+__device__ __forceinline__ float max_mag(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return m;
+}
+__device__ __forceinline__ uint32_t scale_byte(float largest) {
+  return scale_byte(__float_as_uint(largest) & 0x7FFFFFFFu);
+}
+
+template <int N>
+__device__ __forceinline__ float max_of(const float (&f)[N]) {
+  float m = fabsf(f[0]);
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = max_mag(m, f[i]);
+  return m;
+}
 
 // N values of a row from column `col` on, zero beyond K.
 template <typename T, int N, bool VEC>
@@ -66,12 +84,11 @@ __device__ __forceinline__ void load_vals(const T *row, int64_t col, int64_t K, 
           f[4 * i] = v.x, f[4 * i + 1] = v.y, f[4 * i + 2] = v.z, f[4 * i + 3] = v.w;
         }
       } else {
+        static_assert(sizeof(T) == 4 || N == 8);
+        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(row + col));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < N / 4; ++i) {
-          const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(row + col) + i);
-          f[4 * i] = bf16_lo(v.x), f[4 * i + 1] = bf16_hi(v.x);
-          f[4 * i + 2] = bf16_lo(v.y), f[4 * i + 3] = bf16_hi(v.y);
-        }
+        for (int i = 0; i < 4; ++i) f[2 * i] = bf16_lo(w[i]), f[2 * i + 1] = bf16_hi(w[i]);
       }
       return;
     }
@@ -90,73 +107,148 @@ __device__ __forceinline__ void load_vals(const T *row, int64_t col, int64_t K, 
 
 constexpr int kRowsThreads = 256;
 
-template <typename T, bool VEC, int U>
-__global__ void __launch_bounds__(kRowsThreads)
-    quantise_rows_kernel(const __grid_constant__ QuantiseParams p, int32_t kblocks) {
+template <typename T, int U>
+__global__ void __launch_bounds__(kRowsThreads) quantise_linear_kernel(const __grid_constant__ QuantiseParams p,
+                                                                       int64_t n) {
   dependency_wait();
-  const int64_t n = p.M * kblocks;
-  const int in = threadIdx.x & 15;
-  const int64_t first = (int64_t)blockIdx.x * (kRowsThreads / 16 * U) + (threadIdx.x >> 4);
-  float f[U][8];
-  int64_t row[U], col[U];
+  const int in = threadIdx.x & 7;
+  const int64_t first = (int64_t)blockIdx.x * (kRowsThreads / 8 * U) + (threadIdx.x >> 3);
+  float f[U][16];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t b = first + u * (kRowsThreads / 16);
-    row[u] = b < n ? b / kblocks : -1;
-    col[u] = b < n ? (b - row[u] * kblocks) * 128 + in * 8 : 0;
-    if (row[u] >= 0)
-      load_vals<T, 8, VEC>(static_cast<const T *>(p.x) + row[u] * p.x_stride, col[u], p.K, f[u]);
+    const int64_t at = (first + u * (kRowsThreads / 8)) * 128 + in * 8;
+    if (at < n * 128) {
+      float lo[8], hi[8];
+      load_vals<T, 8, true>(static_cast<const T *>(p.x), at, n * 128, lo);
+      load_vals<T, 8, true>(static_cast<const T *>(p.x), at + 64, n * 128, hi);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[u][i] = lo[i], f[u][8 + i] = hi[i];
+    }
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    uint32_t m = 0;
-    if (row[u] >= 0) {
+    const int64_t b = first + u * (kRowsThreads / 8);
+    float m = b < n ? max_of<16>(f[u]) : 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, mag(f[u][i]));
+    for (int o = 4; o > 0; o >>= 1) m = max_mag(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (b >= n) continue;
+    const uint32_t s = scale_byte(m);
+    if (in == 0) p.s[b] = (uint8_t)s;
+    const float by = multiplier(s);
+    uint8_t *q = p.q + b * 128 + in * 8;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<uint2 *>(q + 64 * h) =
+          make_uint2(quantise4(f[u][8 * h], f[u][8 * h + 1], f[u][8 * h + 2], f[u][8 * h + 3], by),
+                     quantise4(f[u][8 * h + 4], f[u][8 * h + 5], f[u][8 * h + 6], f[u][8 * h + 7], by));
+  }
+}
+
+// Blocks of 128 values numbered along the rows, 16 lanes each, U of them a thread.  `magic`
+// is ceil(2^32 / kblocks): a thread block's local numbers are below kblocks + 16 U, where the
+// multiplication is exact (kblocks < 2^24).
+template <typename T, bool VEC, int U>
+__global__ void __launch_bounds__(kRowsThreads)
+    quantise_rows_kernel(const __grid_constant__ QuantiseParams p, int32_t kblocks, uint32_t magic) {
+  dependency_wait();
+  constexpr int kPer = kRowsThreads / 16;
+  const int in = threadIdx.x & 15, slot = threadIdx.x >> 4;
+  const int64_t base = (int64_t)blockIdx.x * (kPer * U);
+  const int64_t row0 = base / kblocks;
+  const uint32_t rem0 = (uint32_t)(base - row0 * kblocks);
+  float f[U][8];
+  int64_t row[U];
+  int32_t kb[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t x = rem0 + u * kPer + slot;
+    const uint32_t q = kblocks == 1 ? x : __umulhi(x, magic);
+    row[u] = row0 + q;
+    kb[u] = (int32_t)(x - q * kblocks);
+    if (row[u] < p.M)
+      load_vals<T, 8, VEC>(static_cast<const T *>(p.x) + row[u] * p.x_stride, (int64_t)kb[u] * 128 + in * 8, p.K,
+                           f[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float m = 0.f;
+    if (row[u] < p.M) {
+      m = max_of<8>(f[u]);
     }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (row[u] < 0) continue;
+    for (int o = 8; o > 0; o >>= 1) m = max_mag(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (row[u] >= p.M) continue;
     const uint32_t s = scale_byte(m);
-    if (in == 0) p.s[row[u] * kblocks + (col[u] >> 7)] = (uint8_t)s;
-    const uint2 w = make_uint2(quantise4(f[u][0], f[u][1], f[u][2], f[u][3], s),
-                               quantise4(f[u][4], f[u][5], f[u][6], f[u][7], s));
-    uint8_t *q = p.q + row[u] * p.q_stride + col[u];
-    if (col[u] + 8 <= p.K) {
+    if (in == 0) p.s[row[u] * kblocks + kb[u]] = (uint8_t)s;
+    const float by = multiplier(s);
+    const uint2 w = make_uint2(quantise4(f[u][0], f[u][1], f[u][2], f[u][3], by),
+                               quantise4(f[u][4], f[u][5], f[u][6], f[u][7], by));
+    const int64_t col = (int64_t)kb[u] * 128 + in * 8;
+    uint8_t *q = p.q + row[u] * p.q_stride + col;
+    if (col + 8 <= p.K) {
       *reinterpret_cast<uint2 *>(q) = w;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (col[u] + i < p.K) q[i] = (uint8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+        if (col + i < p.K) q[i] = (uint8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
     }
   }
 }
 
+// The tile kernel's arithmetic in two forms that give the same bytes.  LEAN: maxima by
+// max.NaN on the values, the NaN scale as a multiplier, edges looked up once a tile.  The
+// other one, with integer maxima and a branch per word, issues about a third more
+// instructions.  bf16 tiles, which the arithmetic binds, take LEAN (24,935 x 1664 with 128 x
+// 128 blocks, both copies: 31 us against 44); fp32 tiles, which HBM binds, the other
+// (65,536 x 4096, both copies: 265 us against 284; why the longer form's pace suits HBM
+// better is not established).
+template <bool LEAN>
+struct Form {
+  static __device__ __forceinline__ uint32_t larger(uint32_t bits, float f) {
+    if constexpr (LEAN) return __float_as_uint(max_mag(__uint_as_float(bits), f));
+    return max(bits, __float_as_uint(f) & 0x7FFFFFFFu);
+  }
+  // What quantise() takes for a block of scale byte s.
+  static __device__ __forceinline__ uint32_t code(uint32_t s) {
+    if constexpr (LEAN) return __float_as_uint(multiplier(s));
+    return s;
+  }
+  static __device__ __forceinline__ uint32_t quantise(float a, float b, float c, float d, uint32_t code) {
+    if constexpr (LEAN) return quantise4(a, b, c, d, __uint_as_float(code));
+    if (code == 255) return 0x7F7F7F7Fu;
+    return quantise4(a, b, c, d, inverse_scale(code));
+  }
+};
+
 // The tile (mb, kb), held as 16 rows x 4 columns a thread: its scales and bytes.
+template <bool LEAN>
 __device__ __forceinline__ void quantise_tile(const QuantiseParams &p, const float (&v)[16][4], int64_t mb,
                                               int64_t kb, int32_t kblocks, int32_t mblocks, uint4 *s_turn,
                                               uint4 (*s_max)[32]) {
+  using F = Form<LEAN>;
+  const auto join = [](uint32_t x, uint32_t y) { return F::larger(x, __uint_as_float(y)); };
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t m0 = mb * 128 + warp * 16, k0 = kb * 128 + lane * 4;
+  const bool whole = LEAN && (mb + 1) * 128 <= p.M && (kb + 1) * 128 <= p.K;  // no edge to look out for
   // Column maxima: this thread's 16 rows, then the eight warps' through shared memory.
   uint32_t cm[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < 16; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) cm[j] = max(cm[j], mag(v[i][j]));
+    for (int j = 0; j < 4; ++j) cm[j] = F::larger(cm[j], v[i][j]);
   s_max[warp][lane] = make_uint4(cm[0], cm[1], cm[2], cm[3]);
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < 8; ++w) {
     const uint4 o = s_max[w][lane];
-    cm[0] = max(cm[0], o.x), cm[1] = max(cm[1], o.y);
-    cm[2] = max(cm[2], o.z), cm[3] = max(cm[3], o.w);
+    cm[0] = join(cm[0], o.x), cm[1] = join(cm[1], o.y);
+    cm[2] = join(cm[2], o.z), cm[3] = join(cm[3], o.w);
   }
   uint32_t tile = 0;
   if (p.block_rows != 1) {
-    tile = max(max(cm[0], cm[1]), max(cm[2], cm[3]));
+    tile = join(join(cm[0], cm[1]), join(cm[2], cm[3]));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) tile = max(tile, __shfl_xor_sync(0xffffffffu, tile, o));
+    for (int o = 16; o > 0; o >>= 1) tile = join(tile, __shfl_xor_sync(0xffffffffu, tile, o));
     tile = scale_byte(tile);
     if (threadIdx.x == 0) {
       if (p.s) p.s[mb * kblocks + kb] = (uint8_t)tile;
@@ -164,34 +256,37 @@ __device__ __forceinline__ void quantise_tile(const QuantiseParams &p, const flo
     }
   }
   if (p.q) {
-    uint32_t rs = tile;  // lanes 2i and 2i + 1: row i's scale
+    uint32_t by = F::code(tile);  // lanes 2i and 2i + 1: row i's
     if (p.block_rows == 1) {
       // Row maxima: 16 values a lane, halved in number at each of four exchanges.
       uint32_t r[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        r[i] = max(max(mag(v[i][0]), mag(v[i][1])), max(mag(v[i][2]), mag(v[i][3])));
+      for (int i = 0; i < 16; ++i) {
+        r[i] = F::larger(F::larger(0, v[i][0]), v[i][1]);
+        r[i] = join(r[i], F::larger(F::larger(0, v[i][2]), v[i][3]));
+      }
 #pragma unroll
       for (int half = 8; half > 0; half >>= 1) {
         const bool up = lane & (2 * half);
 #pragma unroll
         for (int i = 0; i < half; ++i) {
           const uint32_t give = up ? r[i] : r[i + half], keep = up ? r[i + half] : r[i];
-          r[i] = max(keep, __shfl_xor_sync(0xffffffffu, give, 2 * half));
+          r[i] = join(keep, __shfl_xor_sync(0xffffffffu, give, 2 * half));
         }
       }
-      r[0] = max(r[0], __shfl_xor_sync(0xffffffffu, r[0], 1));
-      rs = scale_byte(r[0]);
+      r[0] = join(r[0], __shfl_xor_sync(0xffffffffu, r[0], 1));
+      const uint32_t rs = scale_byte(r[0]);
+      by = F::code(rs);
       const int64_t row = m0 + (lane >> 1);
       if (!(lane & 1) && row < p.M) p.s[row * kblocks + kb] = (uint8_t)rs;
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const uint32_t s = __shfl_sync(0xffffffffu, rs, 2 * i);
-      if (m0 + i < p.M) {
-        const uint32_t w = quantise4(v[i][0], v[i][1], v[i][2], v[i][3], s);
+      const uint32_t row_by = __shfl_sync(0xffffffffu, by, 2 * i);
+      if (whole || m0 + i < p.M) {
+        const uint32_t w = F::quantise(v[i][0], v[i][1], v[i][2], v[i][3], row_by);
         uint8_t *q = p.q + (m0 + i) * p.q_stride + k0;
-        if (k0 + 4 <= p.K) {
+        if (whole || k0 + 4 <= p.K) {
           *reinterpret_cast<uint32_t *>(q) = w;
         } else {
 #pragma unroll
@@ -206,11 +301,12 @@ __device__ __forceinline__ void quantise_tile(const QuantiseParams &p, const flo
     for (int j = 0; j < 4; ++j) {
       const uint32_t s = p.block_rows == 1 ? scale_byte(cm[j]) : tile;
       if (p.block_rows == 1 && warp == 0 && k0 + j < p.K) p.st[(k0 + j) * mblocks + mb] = (uint8_t)s;
+      const uint32_t by = F::code(s);
       uint4 w;
-      w.x = quantise4(v[0][j], v[1][j], v[2][j], v[3][j], s);
-      w.y = quantise4(v[4][j], v[5][j], v[6][j], v[7][j], s);
-      w.z = quantise4(v[8][j], v[9][j], v[10][j], v[11][j], s);
-      w.w = quantise4(v[12][j], v[13][j], v[14][j], v[15][j], s);
+      w.x = F::quantise(v[0][j], v[1][j], v[2][j], v[3][j], by);
+      w.y = F::quantise(v[4][j], v[5][j], v[6][j], v[7][j], by);
+      w.z = F::quantise(v[8][j], v[9][j], v[10][j], v[11][j], by);
+      w.w = F::quantise(v[12][j], v[13][j], v[14][j], v[15][j], by);
       s_turn[(lane * 4 + j) * 8 + (warp ^ (lane & 7))] = w;
     }
     __syncthreads();
@@ -219,10 +315,10 @@ __device__ __forceinline__ void quantise_tile(const QuantiseParams &p, const flo
       const int idx = i * 256 + threadIdx.x;
       const int c = idx >> 3, chunk = idx & 7;
       const int64_t k = kb * 128 + c, m = mb * 128 + chunk * 16;
-      if (k >= p.K || m >= p.M) continue;
+      if (!whole && (k >= p.K || m >= p.M)) continue;
       const uint4 w = s_turn[c * 8 + (chunk ^ ((c >> 2) & 7))];
       uint8_t *q = p.qt + k * p.qt_stride + m;
-      if (m + 16 <= p.M) {
+      if (whole || m + 16 <= p.M) {
         *reinterpret_cast<uint4 *>(q) = w;
       } else {
         const uint32_t b[4] = {w.x, w.y, w.z, w.w};
@@ -253,7 +349,7 @@ __global__ void __launch_bounds__(256, 2)
       v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
     }
   }
-  quantise_tile(p, v, mb, kb, kblocks, mblocks, s_turn, s_max);
+  quantise_tile<true>(p, v, mb, kb, kblocks, mblocks, s_turn, s_max);
 }
 
 template <typename T>
@@ -305,7 +401,7 @@ __global__ void __launch_bounds__(256, 2)
     tile += gridDim.x;
     mb = tile / kblocks, kb = tile - mb * kblocks;
     if (tid == 0 && tile < tiles) issue(mb, kb);
-    quantise_tile(p, v, this_mb, this_kb, kblocks, mblocks, s_turn, s_max);
+    quantise_tile<sizeof(T) == 2>(p, v, this_mb, this_kb, kblocks, mblocks, s_turn, s_max);
   }
 }
 
@@ -330,18 +426,26 @@ cudaError_t launch_typed(const QuantiseParams &p, cudaStream_t stream) {
     const bool vec = (uintptr_t)p.x % 16 == 0 && p.x_stride * sizeof(T) % 16 == 0;
     const int64_t n = p.M * kblocks;
     constexpr int kPer = kRowsThreads / 16;
-    if (n <= 152 * 8 * kPer) {
+    if (vec && p.K % 128 == 0 && (p.M == 1 || (p.x_stride == p.K && p.q_stride == p.K))) {
+      if (n <= kSms * 4 * (kRowsThreads / 8))
+        return launch(quantise_linear_kernel<T, 1>, (n * 8 + kRowsThreads - 1) / kRowsThreads, kRowsThreads, 0, stream,
+                      1, p, n);
+      return launch(quantise_linear_kernel<T, 2>, (n * 4 + kRowsThreads - 1) / kRowsThreads, kRowsThreads, 0, stream,
+                    1, p, n);
+    }
+    const uint32_t magic = (uint32_t)(((1ull << 32) + kblocks - 1) / kblocks);
+    if (n <= kSms * 8 * kPer) {
       const int64_t grid = (n + kPer - 1) / kPer;
       if (vec)
-        return launch(quantise_rows_kernel<T, true, 1>, grid, kRowsThreads, 0, stream, 1, p, (int32_t)kblocks);
+        return launch(quantise_rows_kernel<T, true, 1>, grid, kRowsThreads, 0, stream, 1, p, (int32_t)kblocks, magic);
       else
-        return launch(quantise_rows_kernel<T, false, 1>, grid, kRowsThreads, 0, stream, 1, p, (int32_t)kblocks);
+        return launch(quantise_rows_kernel<T, false, 1>, grid, kRowsThreads, 0, stream, 1, p, (int32_t)kblocks, magic);
     } else {
       const int64_t grid = (n + kPer * 4 - 1) / (kPer * 4);
       if (vec)
-        return launch(quantise_rows_kernel<T, true, 4>, grid, kRowsThreads, 0, stream, 1, p, (int32_t)kblocks);
+        return launch(quantise_rows_kernel<T, true, 4>, grid, kRowsThreads, 0, stream, 1, p, (int32_t)kblocks, magic);
       else
-        return launch(quantise_rows_kernel<T, false, 4>, grid, kRowsThreads, 0, stream, 1, p, (int32_t)kblocks);
+        return launch(quantise_rows_kernel<T, false, 4>, grid, kRowsThreads, 0, stream, 1, p, (int32_t)kblocks, magic);
     }
   } else {
     const int64_t tiles = kblocks * mblocks;

@@ -61,7 +61,8 @@ struct EmbedGradParams {
   float *partial;      // [chunks][2][partial_stride]: a run open at the start, at the end
   uint32_t *long_count, *long_list;  // chunks in which a run of more than two chunks starts
   int64_t partial_stride, chunks, sum_blocks, zero_blocks;
-  int32_t zero_rows;  // rows a warp of the zeroing blocks looks at
+  int32_t zero_rows;    // rows a warp of the zeroing blocks looks at
+  uint32_t zero_magic;  // ceil(2^32 / words a row)
   int32_t group, slabs, chunk;  // lanes a group, column slabs, sorted ids a chunk
 };
 size_t embed_grad_workspace_bytes(int64_t n, int32_t D);
