@@ -34,6 +34,7 @@ constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
 constexpr int kDigits = 1024;      // most digits of a pass: two a thread
 constexpr int kCountSort = 4096;   // most pairs sorted by counting
 constexpr uint32_t kNoKey = 0xFFFFFFFFu;
+constexpr int kRunGroup = 16;      // chunks whose runs are counted together
 
 // Pairs a thread sorts of a tile: few where there are few tiles, so that they fill the SMs.
 constexpr int kPerLarge = 8, kPerSmall = 2;
@@ -204,39 +205,52 @@ __global__ void __launch_bounds__(kSortThreads)
   }
   if (FIRST && bad && p.status) atomicOr(p.status, ENGRAM_FLAG_BAD_ROW);
   __syncthreads();
-  for (int d = tid; d <= (int)mask; d += kSortThreads) p.counts[(int64_t)d * p.tiles + blockIdx.x] = s_cnt[d];
+  for (int d = tid; d <= (int)mask; d += kSortThreads)
+    p.counts[(int64_t)blockIdx.x << p.digit_bits | d] = s_cnt[d];
 }
 
-// Block d: the counts of digit d become their exclusive prefix sums over the tiles; the
-// digit's total goes behind the array.
-__global__ void __launch_bounds__(256) scan_digits_kernel(uint32_t *counts, int64_t tiles,
-                                                          uint32_t *totals, uint32_t *long_count) {
-  __shared__ uint32_t s_sum[8];
+// counts[tile][digit] becomes its exclusive prefix sums over the tiles; the digits' totals go
+// to `totals`.  A block takes 32 digits, a lane each; its warps take the tiles in as many
+// contiguous parts: their sums first, then, from what comes before a part, its prefix.
+constexpr int kScanThreads = 1024, kScanAhead = 8;
+__global__ void __launch_bounds__(kScanThreads) scan_digits_kernel(uint32_t *counts, int64_t tiles, int32_t bits,
+                                                                   uint32_t *totals, uint32_t *long_count) {
+  __shared__ uint32_t s_sum[kScanThreads / 32][32];
   dependency_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint32_t *c = counts + blockIdx.x * tiles;
-  uint32_t carry = 0;
-  for (int64_t i0 = 0; i0 < tiles; i0 += 256) {
-    const uint32_t v = i0 + tid < tiles ? c[i0 + tid] : 0;
-    uint32_t sum = v;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int d = blockIdx.x * 32 + lane;
+  const bool mine = d < 1 << bits;
+  const int64_t per = (tiles + kScanThreads / 32 - 1) / (kScanThreads / 32);
+  const int64_t first = warp * per, last = min(first + per, tiles);
+  uint32_t *c = counts + d;
+  uint32_t sum = 0;
+  for (int64_t t = first; mine && t < last; t += kScanAhead) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += u;
-    }
-    if (lane == 31) s_sum[warp] = sum;
-    __syncthreads();
-    uint32_t before = carry, all = carry;
-    for (int w = 0; w < 8; ++w) {
-      if (w < warp) before += s_sum[w];
-      all += s_sum[w];
-    }
-    if (i0 + tid < tiles) c[i0 + tid] = before + sum - v;
-    carry = all;
-    __syncthreads();
+    for (int i = 0; i < kScanAhead; ++i)
+      if (t + i < last) sum += c[(t + i) << bits];
   }
-  if (tid == 0) totals[blockIdx.x] = carry;
-  if (tid == 0 && blockIdx.x == 0) *long_count = 0;
+  s_sum[warp][lane] = sum;
+  __syncthreads();
+  uint32_t before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kScanThreads / 32; ++w) {
+    const uint32_t v = s_sum[w][lane];
+    before += w < warp ? v : 0;
+    all += v;
+  }
+  for (int64_t t = first; mine && t < last; t += kScanAhead) {
+    uint32_t v[kScanAhead];
+#pragma unroll
+    for (int i = 0; i < kScanAhead; ++i) v[i] = t + i < last ? c[(t + i) << bits] : 0;
+#pragma unroll
+    for (int i = 0; i < kScanAhead; ++i)
+      if (t + i < last) {
+        c[(t + i) << bits] = before;
+        before += v[i];
+      }
+  }
+  if (mine && warp == 0) totals[d] = all;
+  if (threadIdx.x == 0 && blockIdx.x == 0) *long_count = 0;
 }
 
 template <bool FIRST, int PER>
@@ -262,7 +276,7 @@ __global__ void __launch_bounds__(kSortThreads, 3)
   for (int h = 0; h < 2; ++h) {
     const int d = 2 * tid + h;
     total[h] = d <= (int)mask ? __ldg(p.totals + d) : 0;
-    ahead[h] = d <= (int)mask ? __ldg(p.counts + (int64_t)d * p.tiles + blockIdx.x) : 0;
+    ahead[h] = d <= (int)mask ? __ldg(p.counts + ((int64_t)blockIdx.x << p.digit_bits | d)) : 0;
   }
   uint32_t key[PER], place[PER];
   bool bad = false;
@@ -335,50 +349,57 @@ __global__ void __launch_bounds__(kSortThreads) runs_small_kernel(const __grid_c
   }
   const uint32_t base = block_exclusive(__popc(starts), s_sum);
   for (int i = 0; i < per && e0 + i < n; ++i)  // chunks that start here (their length is 4 at least)
-    if ((e0 + i) % p.chunk == 0) p.run_base[(e0 + i) / p.chunk] = base + __popc(starts & ((1u << i) - 1));
+    if ((e0 + i) % p.chunk == 0) {
+      const int c = (e0 + i) / p.chunk;
+      p.run_base[c] = base + __popc(starts & ((1u << i) - 1));
+      if (c % kRunGroup == 0) p.run_group[c / kRunGroup] = 0;
+    }
   if (threadIdx.x == kSortThreads - 1) {
-    p.run_base[p.chunks] = base + __popc(starts);
+    *p.run_total = base + __popc(starts);
     *p.count_out = (int32_t)(base + __popc(starts));
   }
 }
 
-// Runs that start in each chunk, a warp a chunk.
-__global__ void __launch_bounds__(256) count_runs_kernel(const __grid_constant__ EmbedGradParams p) {
+// Runs that start in a group of kRunGroup chunks, and before each of them in the group: a block
+// a group, a warp a chunk.
+__global__ void __launch_bounds__(kRunGroup * 32) count_runs_kernel(const __grid_constant__ EmbedGradParams p) {
+  __shared__ uint32_t s_count[kRunGroup];
   dependency_wait();
-  const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (c >= p.chunks) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * kRunGroup + warp;
   const int64_t e0 = c * p.chunk, e1 = min(e0 + p.chunk, p.n);
   uint32_t mine = 0;
+#pragma unroll 4
   for (int64_t e = e0 + lane; e < e1; e += 32) {
     const uint32_t k = __ldg(p.keys + e);
     mine += k < (uint32_t)p.rows && (e == 0 || __ldg(p.keys + e - 1) != k);
   }
   mine = __reduce_add_sync(0xffffffffu, mine);
-  if (lane == 0) p.run_base[c] = mine;
+  if (lane == 0) s_count[warp] = mine;
+  __syncthreads();
+  if (warp != 0) return;
+  const uint32_t v = lane < kRunGroup ? s_count[lane] : 0;
+  uint32_t sum = v;
+#pragma unroll
+  for (int o = 1; o < kRunGroup; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += u;
+  }
+  if (lane < kRunGroup && c + lane < p.chunks) p.run_base[c + lane] = sum - v;
+  if (lane == kRunGroup - 1) p.run_group[blockIdx.x] = sum;
 }
 
-// run_base becomes its exclusive prefix sums; the number of runs goes behind it.
+// run_group becomes its exclusive prefix sums; the number of runs goes to run_total.
 __global__ void __launch_bounds__(1024) scan_runs_kernel(const __grid_constant__ EmbedGradParams p) {
   __shared__ uint32_t s_sum[2][32];
   dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint4 *base = reinterpret_cast<uint4 *>(p.run_base);  // padded to whole words of eight
+  const int64_t groups = (p.chunks + kRunGroup - 1) / kRunGroup;
   uint32_t carry = 0;
   int buf = 0;
-  for (int64_t i0 = 0; i0 < p.chunks; i0 += 1024 * 8, buf ^= 1) {
-    const int64_t c = i0 + tid * 8;
-    uint32_t v[8] = {};
-    if (c < p.chunks) {
-      const uint4 x = base[c / 4], y = base[c / 4 + 1];
-      const uint32_t all[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = c + i < p.chunks ? all[i] : 0;
-    }
-    uint32_t mine = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) mine += v[i];
-    uint32_t sum = mine;
+  for (int64_t i0 = 0; i0 < groups; i0 += 1024, buf ^= 1) {
+    const uint32_t v = i0 + tid < groups ? p.run_group[i0 + tid] : 0;
+    uint32_t sum = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
@@ -387,24 +408,19 @@ __global__ void __launch_bounds__(1024) scan_runs_kernel(const __grid_constant__
     if (lane == 31) s_sum[buf][warp] = sum;
     __syncthreads();
     const uint32_t w = s_sum[buf][lane];  // every warp adds up the warps before it
-    uint32_t at = carry + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + sum - mine;
+    const uint32_t at = carry + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + sum - v;
     carry += __reduce_add_sync(0xffffffffu, w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t here = at;
-      at += v[i];
-      v[i] = here;
-    }
-    if (c < p.chunks) {
-      base[c / 4] = make_uint4(v[0], v[1], v[2], v[3]);
-      base[c / 4 + 1] = make_uint4(v[4], v[5], v[6], v[7]);
-    }
+    if (i0 + tid < groups) p.run_group[i0 + tid] = at;
   }
-  __syncthreads();  // the words past the last chunk are written before the number goes there
   if (tid == 0) {
-    p.run_base[p.chunks] = carry;
+    *p.run_total = carry;
     *p.count_out = (int32_t)carry;
   }
+}
+
+// Runs that start before chunk c.
+__device__ __forceinline__ int64_t runs_before(const EmbedGradParams &p, int64_t c) {
+  return (int64_t)__ldg(p.run_base + c) + __ldg(p.run_group + c / kRunGroup);
 }
 
 // ---- sums of runs ------------------------------------------------------------------------
@@ -515,9 +531,9 @@ __device__ __forceinline__ void sum_chunk(const EmbedGradParams &p, const Item &
   const bool long_out = leaves && (through || (e0 + 2 * C < p.n && __ldg(p.keys + e0 + 2 * C) == last));
   int64_t run = 0;
   if (p.run_base) {
-    run = (int64_t)__ldg(p.run_base + it.chunk) - comes;
+    run = runs_before(p, it.chunk) - comes;
     if (it.slab == 0) {  // ids beyond the distinct ones
-      const int64_t count = __ldg(p.run_base + p.chunks);
+      const int64_t count = __ldg(p.run_total);
       for (int64_t e = e0 + it.in; e < e1; e += p.group)
         if (e >= count) p.row_ids_out[e] = ENGRAM_ROW_DEAD;
     }
@@ -715,7 +731,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_runs_kernel(const __grid_co
       for (int g = 1; g < groups; ++g)
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] += s_part[(g * G + in) * V + i];
-      const int64_t row = p.run_base ? (int64_t)__ldg(p.run_base + chunk + 1) - 1 : key;
+      const int64_t row = p.run_base ? runs_before(p, chunk + 1) - 1 : key;
       if (mine)
         write_row<TG, V>(static_cast<TG *>(p.grad) + row * p.grad_stride + col, acc, p.scale, p.accumulate);
       if (p.run_base && slab == 0 && in == 0) p.row_ids_out[row] = (int32_t)key;
@@ -760,7 +776,7 @@ Cut cut_of(int64_t n, int D, bool vec) {
 }
 
 struct Layout {
-  size_t keys[2], pos[2], counts, totals, run_base, long_list, partial, total;
+  size_t keys[2], pos[2], counts, totals, run_base, run_group, long_list, partial, total;
 };
 Layout layout_of(int64_t n, int D, const Cut &c) {
   Layout l;
@@ -777,7 +793,8 @@ Layout layout_of(int64_t n, int D, const Cut &c) {
   }
   l.counts = take((size_t)sort_tiles(n) * kDigits * 4);
   l.totals = take(kDigits * 4);
-  l.run_base = take((size_t)(c.chunks + 8) / 8 * 32 + 4);  // read and written eight at a time
+  l.run_base = take((size_t)c.chunks * 4);
+  l.run_group = take((size_t)(c.chunks / kRunGroup + 2) * 4);  // their number in front
   l.long_list = take((size_t)(c.chunks + 1) * 4);
   l.partial = take((size_t)c.chunks * 2 * c.stride * 4);
   l.total = at;
@@ -835,6 +852,8 @@ cudaError_t launch_embed_grad(EmbedGradParams p, int dy_dtype, int grad_dtype, v
   p.counts = reinterpret_cast<uint32_t *>(w + l.counts);
   p.totals = reinterpret_cast<uint32_t *>(w + l.totals);
   p.run_base = sparse ? reinterpret_cast<uint32_t *>(w + l.run_base) : nullptr;
+  p.run_total = reinterpret_cast<uint32_t *>(w + l.run_group);
+  p.run_group = p.run_total + 1;
   p.long_count = reinterpret_cast<uint32_t *>(w + l.long_list);
   p.long_list = p.long_count + 1;
   p.partial = reinterpret_cast<float *>(w + l.partial);
@@ -873,8 +892,8 @@ cudaError_t launch_embed_grad(EmbedGradParams p, int dy_dtype, int grad_dtype, v
                        : (first ? count_digits_kernel<true, kPerSmall> : count_digits_kernel<false, kPerSmall>),
                  p.tiles, kSortThreads, 0, stream, 1, p, keys[in], shift);
       if (e == cudaSuccess)
-        e = launch(scan_digits_kernel, 1 << p.digit_bits, 256, 0, stream, 1, p.counts, p.tiles, p.totals,
-                   p.long_count);
+        e = launch(scan_digits_kernel, ((1 << p.digit_bits) + 31) / 32, kScanThreads, 0, stream, 1, p.counts,
+                   p.tiles, p.digit_bits, p.totals, p.long_count);
       if (e == cudaSuccess)
         e = launch(large ? (first ? scatter_kernel<true, kPerLarge> : scatter_kernel<false, kPerLarge>)
                          : (first ? scatter_kernel<true, kPerSmall> : scatter_kernel<false, kPerSmall>),
@@ -888,7 +907,7 @@ cudaError_t launch_embed_grad(EmbedGradParams p, int dy_dtype, int grad_dtype, v
   if (sparse && p.n > 0 && p.n <= kRunsSmall) {
     if ((e = launch(runs_small_kernel, 1, kSortThreads, 0, stream, 1, p)) != cudaSuccess) return e;
   } else if (sparse && p.n > 0) {
-    e = launch(count_runs_kernel, (p.chunks + 7) / 8, 256, 0, stream, 1, p);
+    e = launch(count_runs_kernel, (p.chunks + kRunGroup - 1) / kRunGroup, kRunGroup * 32, 0, stream, 1, p);
     if (e == cudaSuccess) e = launch(scan_runs_kernel, 1, 1024, 0, stream, 1, p);
     if (e != cudaSuccess) return e;
   }

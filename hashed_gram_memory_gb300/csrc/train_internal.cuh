@@ -57,7 +57,9 @@ struct EmbedGradParams {
   int32_t passes, digit_bits;  // of the sort
   int64_t tiles;
   uint32_t *keys, *pos, *counts, *totals;
-  uint32_t *run_base;  // sparse: runs before each chunk, their number behind; else NULL
+  uint32_t *run_base;   // sparse: runs before each chunk in its group of chunks; else NULL
+  uint32_t *run_group;  // runs before each group
+  uint32_t *run_total;
   float *partial;      // [chunks][2][partial_stride]: a run open at the start, at the end
   uint32_t *long_count, *long_list;  // chunks in which a run of more than two chunks starts
   int64_t partial_stride, chunks, sum_blocks, zero_blocks;
