@@ -61,7 +61,7 @@ class Connection:
         """dx, dalpha, dwkv, and the table's gradient as (row ids, rows, count)."""
         ids, x, k, state, (qt, st), w = saved
         T = ids.shape[0]
-        dx, dk, dalpha = eg.engram_gate_add_grad(k, state, x, self.alpha, dy, status=self.status)
+        dx, dk, dalpha = eg.engram_gate_add_grad(k, state, x, self.alpha, dy)
         q, s, kt, ks = eg.engram_fp8_quantise(dk, cols=True, status=self.status)
         de = eg.engram_fp8_matmul(q, s, w[2], w[3], b_block=eg.FP8_BLOCK, out_dtype=torch.bfloat16,
                                   status=self.status)

@@ -166,7 +166,7 @@ def _load():
     L.engram_gate_add_grad_workspace_bytes.argtypes = []
     L.engram_gate_add_grad_workspace_bytes.restype = sz
     L.engram_gate_add_grad.argtypes = [vp, vp, i64, i32, vp, vp, C.c_float, vp, vp, vp, i32, vp,
-                                       vp, sz, vp, vp]
+                                       vp, sz, vp]
     L.engram_gate_add_grad.restype = i32
     return L
 
@@ -885,7 +885,7 @@ def engram_gate_add_grad_workspace_bytes() -> int:
 
 
 def engram_gate_add_grad(k, state, streams_in, alpha, dy, eps: float = 1e-6, dx=None, dk=None,
-                         dalpha=None, dk_dtype=None, workspace=None, status=None, stream=None):
+                         dalpha=None, dk_dtype=None, workspace=None, stream=None):
     """The backward pass of engram_gate_add: k fp32 [..., D], state uint8 [tokens] or None
     (every token live), streams_in and dy bf16 [..., 4, D].  Returns (dx, dk, dalpha); dx may
     be dy itself."""
@@ -918,6 +918,5 @@ def engram_gate_add_grad(k, state, streams_in, alpha, dy, eps: float = 1e-6, dx=
                                 device=k.device)
     _check(lib.engram_gate_add_grad(_ptr(k), _ptr(state), T, D, _ptr(streams_in), _ptr(alpha),
                                     float(eps), _ptr(dy), _ptr(dx), _ptr(dk), _dtype(dk, "dk"),
-                                    _ptr(dalpha), _ptr(workspace), workspace.numel(), _ptr(status),
-                                    _stream(stream)), "engram_gate_add_grad")
+                                    _ptr(dalpha), _ptr(workspace), workspace.numel(), _stream(stream)), "engram_gate_add_grad")
     return dx, dk, dalpha

@@ -13,16 +13,19 @@
 // read twice.  A token's k, stream 0 and four gradient streams stay in the
 // registers of its threads (8 columns each: 16-byte accesses, neighbouring lanes
 // adjacent) between the reduction of the seven sums (|a|^2, |k|^2, <a,k>, <dy_s,k>)
-// and the stores.  Wide tokens take a block at a time (D/8 threads), which walks
-// its tokens with the next ones' bytes on the way: bulk copies into a ring of
-// shared-memory stages, refilled as soon as a token is in registers.  (Loads into
-// registers instead, two blocks an SM: see the measurements at the launch.)  Narrow
-// tokens take a power of two lanes of a warp.  dalpha crosses tokens: each block adds its tokens in
-// order and writes one partial; a second launch of one block adds the partials as
-// a tree in a fixed order, so the result does not depend on timing.
+// and the stores.  Tokens wider than 256 take a block at a time (D/8 threads), two such
+// blocks an SM at D = 4096, so that one's sums and stores run under the other's loads.
+// (Bulk copies into a ring of shared-memory stages under the same arithmetic were
+// slower everywhere: 1104 us against 1054 at 65,536 x 4096, 17.1 against 13.0 at 512 x
+// 4096, 7.7 against 6.5 at 1024 x 1024.)  Narrower tokens take a power of two lanes of
+// a warp (262,144 x 128: 141 us, 163 a block at a time; x 256: 278 and 285).  dalpha crosses tokens: each
+// block adds its tokens in order and writes one partial; a second launch of one block adds
+// the partials as a tree in a fixed order, so the result does not depend on timing.
+// Measured: 65,536 x 4096 1054 us (26 D bytes a token: 6.6 TB/s), 512 x 4096 13 us
+// (the load, sums and stores of two tokens, one after the other, and the second launch).
+// At D = 8192 one block fits an SM and nothing overlaps: 32,768 tokens take 1530 us.
 #include <atomic>
 
-#include "bulk_copy.cuh"
 #include "launch.cuh"
 #include "lookup_common.cuh"
 #include "train_internal.cuh"
@@ -186,8 +189,7 @@ __device__ __forceinline__ void store_dead(const GateGradParams &p, uint8_t stat
   }
 }
 
-// The widest tokens (D > 4096, of which no three fit shared memory): one token a block at a
-// time, loaded into registers, threads = D/8 rounded up to warps.
+// One token a block at a time, threads = D/8 rounded up to warps.
 template <typename TK>
 __global__ void __launch_bounds__(1024) gate_grad_block_kernel(const __grid_constant__ GateGradParams p) {
   __shared__ float s_red[2][7 * 32];  // two tokens in turn: one barrier a token
@@ -213,117 +215,6 @@ __global__ void __launch_bounds__(1024) gate_grad_block_kernel(const __grid_cons
     }
     warp_sums(r, s_red[buf], warp, warps, lane);
     __syncthreads();
-    block_sums(r, s_red[buf], warps, lane);
-    buf ^= 1;
-    const Gate o = gate_of(r, alpha, p);
-    da.x = fmaf(o.g, r[3], da.x), da.y = fmaf(o.g, r[4], da.y);
-    da.z = fmaf(o.g, r[5], da.z), da.w = fmaf(o.g, r[6], da.w);
-    if (mine) store_cols<TK>(c, o, alpha, p, t, col);
-  }
-  if (tid == 0) p.partial[blockIdx.x] = da;
-}
-
-// The same with the tokens' bytes brought by bulk copies: a ring of p.stages stages of
-// 14 D bytes (k, stream 0, dy), the next tokens' copies in flight while one is worked on.
-__device__ __forceinline__ void issue_token(const GateGradParams &p, int64_t t, uint8_t state,
-                                            uint8_t *stage, uint64_t *full, uint8_t *state_slot) {
-  const uint32_t D = p.D;
-  *state_slot = state;
-  if (state == kBad) {
-    mbar_arrive(full);
-    return;
-  }
-  mbar_arrive_expect_tx(full, state == kDead ? 8 * D : 14 * D);
-  if (state != kDead) {
-    bulk_g2s(stage, p.k + t * D, 4 * D, full);
-    bulk_g2s(stage + 4 * D, p.x + t * 4 * D, 2 * D, full);
-  }
-  bulk_g2s(stage + 6 * D, p.dy + t * 4 * D, 8 * D, full);
-}
-
-template <typename TK>
-__global__ void __launch_bounds__(512, 2) gate_grad_bulk_kernel(const __grid_constant__ GateGradParams p) {
-  extern __shared__ __align__(128) uint8_t s_stage[];
-  __shared__ float s_red[2][7 * 16];  // two tokens in turn: one barrier a token
-  __shared__ uint64_t s_full[kGateGradMaxStages];
-  __shared__ uint8_t s_state[kGateGradMaxStages];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  const int col = tid * 8;
-  const bool mine = col < p.D;
-  const uint32_t D = p.D, stage_bytes = 14 * D;
-  if (tid == 0) {
-    for (int s = 0; s < p.stages; ++s) mbar_init(s_full + s, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  dependency_wait();
-  __syncthreads();
-  // The first tokens: a lane each.
-  if (tid < p.stages && blockIdx.x + (int64_t)tid * gridDim.x < p.T) {
-    const int64_t t = blockIdx.x + (int64_t)tid * gridDim.x;
-    issue_token(p, t, p.state ? p.state[t] : 0, s_stage + tid * stage_bytes, s_full + tid, s_state + tid);
-  }
-  // Thread 0: the next token to issue, and its state ahead of time.
-  int64_t ahead = blockIdx.x + (int64_t)p.stages * gridDim.x;
-  uint8_t ahead_state = tid == 0 && p.state && ahead < p.T ? p.state[ahead] : 0;
-  const float4 alpha = make_float4(__ldg(p.alpha), __ldg(p.alpha + 1), __ldg(p.alpha + 2),
-                                   __ldg(p.alpha + 3));
-  float4 da = make_float4(0.f, 0.f, 0.f, 0.f);
-  int buf = 0, s = 0;
-  uint32_t phase = 0;
-  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-    const bool late = !wait_bounded(s_full + s, p.wait_limit_ns, phase);
-    uint8_t state = kBad;
-    Cols c;
-    float r[7] = {};
-    if (!late) {
-      state = s_state[s];
-      const uint8_t *stage = s_stage + s * stage_bytes;
-      if (state != kBad && mine) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          c.dy[q] = *reinterpret_cast<const uint4 *>(stage + 6 * D + (q * D + col) * 2);
-        if (state != kDead) {
-          const float4 *kr = reinterpret_cast<const float4 *>(stage + col * 4);
-          const float4 k0 = kr[0], k1 = kr[1];
-          c.a = *reinterpret_cast<const uint4 *>(stage + 4 * D + col * 2);
-          c.k[0] = k0.x, c.k[1] = k0.y, c.k[2] = k0.z, c.k[3] = k0.w;
-          c.k[4] = k1.x, c.k[5] = k1.y, c.k[6] = k1.z, c.k[7] = k1.w;
-          partial_sums(c, r);
-        }
-      }
-    }
-    warp_sums(r, s_red[buf], warp, warps, lane);
-    if (__syncthreads_or(late)) {  // a copy did not arrive: the block stops together
-      if (tid == 0) {
-        if (p.status) atomicOr(p.status, ENGRAM_FLAG_TIMEOUT);
-        // the copies in flight land, or give up likewise, before the block's memory goes
-        for (int64_t u = t; u < ahead && u < p.T; u += gridDim.x) {
-          wait_bounded(s_full + s, p.wait_limit_ns, phase);
-          if (++s == p.stages) s = 0, phase ^= 1;
-        }
-      }
-      break;
-    }
-    // Every thread has its columns: the stage takes the next token.
-    if (tid == 0 && ahead < p.T) {
-      issue_token(p, ahead, ahead_state, s_stage + s * stage_bytes, s_full + s, s_state + s);
-      ahead += gridDim.x;
-      if (p.state && ahead < p.T) ahead_state = p.state[ahead];
-    }
-    if (++s == p.stages) s = 0, phase ^= 1;
-    if (state == kBad || state == kDead) {
-      if (mine) {
-        const float zero[8] = {};
-        store_dk(static_cast<TK *>(p.dk) + t * D + col, zero);
-        if (state == kDead && p.dx != p.dy) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            __stcs(reinterpret_cast<uint4 *>(p.dx + (t * 4 + q) * (int64_t)D + col), c.dy[q]);
-        }
-      }
-      buf ^= 1;
-      continue;
-    }
     block_sums(r, s_red[buf], warps, lane);
     buf ^= 1;
     const Gate o = gate_of(r, alpha, p);
@@ -404,11 +295,9 @@ __global__ void __launch_bounds__(256) dalpha_kernel(const float4 *__restrict__ 
   }
 }
 
-constexpr int kMaxRing = 225 * 1024;  // the most shared memory of one block's stages
-
 // Blocks that fit on the device at once, asked once per kernel, block size and device.
 template <void (*kernel)(GateGradParams)>
-cudaError_t resident_blocks(int threads, int &blocks, size_t smem = 0) {
+cudaError_t resident_blocks(int threads, int &blocks) {
   static std::atomic<int> known[64][33];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -418,9 +307,7 @@ cudaError_t resident_blocks(int threads, int &blocks, size_t smem = 0) {
   if (blocks) return cudaSuccess;
   int sms = 0, per = 0;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess && smem)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRing);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, 0);
   if (e != cudaSuccess) return e;
   blocks = per * sms < kGateGradMaxBlocks ? per * sms : kGateGradMaxBlocks;
   slot.store(blocks, std::memory_order_relaxed);
@@ -442,21 +329,6 @@ cudaError_t launch_typed(GateGradParams p, cudaStream_t stream) {
       if ((e = resident_blocks<gate_grad_warp_kernel<TK>>(256, n)) != cudaSuccess) return e;
       n = (int)(need < n ? need : n);
       e = launch(gate_grad_warp_kernel<TK>, n, 256, 0, stream, 1, p);
-    } else if (chunks <= 512) {
-      // Two blocks an SM at D = 4096 (more where the tokens are narrow, up to 1024 threads), so
-      // that one's sums and stores run under the other's, with two stages each at least:
-      // one block of four stages took XXX us for 65,536 x 4096, two of two YYY us.
-      const int threads = (chunks + 31) / 32 * 32;
-      const size_t stage = (size_t)14 * p.D;
-      constexpr size_t kSm = 228 * 1024, kBlock = 2048;  // an SM's; static and reserved a block
-      size_t per = kSm / (2 * stage + kBlock);
-      per = per > (size_t)(1024 / threads) ? 1024 / threads : per;
-      p.stages = (int)((kSm / per - kBlock) / stage);
-      if (p.stages > kGateGradMaxStages) p.stages = kGateGradMaxStages;
-      const size_t ring = p.stages * stage;
-      if ((e = resident_blocks<gate_grad_bulk_kernel<TK>>(threads, n, ring)) != cudaSuccess) return e;
-      n = (int)(p.T < n ? p.T : n);
-      e = launch(gate_grad_bulk_kernel<TK>, n, threads, ring, stream, 1, p);
     } else {
       const int threads = (chunks + 31) / 32 * 32;
       if ((e = resident_blocks<gate_grad_block_kernel<TK>>(threads, n)) != cudaSuccess) return e;

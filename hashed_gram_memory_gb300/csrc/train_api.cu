@@ -331,7 +331,7 @@ ENGRAM_API engram_status engram_gate_add_grad(const float *k, const uint8_t *sta
                                               float eps, const uint16_t *dy, uint16_t *dx,
                                               void *dk, int32_t dk_dtype, float *dalpha,
                                               void *workspace, size_t workspace_bytes,
-                                              int32_t *status, void *stream) {
+                                              void *stream) {
   ENGRAM_NVTX_RANGE("engram_gate_add_grad");
   const char *fn = "engram_gate_add_grad";
   if (n_tokens < 0 || n_tokens > INT32_MAX)
@@ -339,8 +339,8 @@ ENGRAM_API engram_status engram_gate_add_grad(const float *k, const uint8_t *sta
   if (D < 16 || D % 16 != 0 || D > 8192)
     return set_error(ENGRAM_ERR_INVALID_ARG, "%s: D must be a multiple of 16 in [16, 8192]", fn);
   if (!dtype_ok(dk_dtype)) return set_error(ENGRAM_ERR_INVALID_ARG, "%s: unknown dk dtype", fn);
-  if (!alpha || !dalpha || !aligned(alpha, 4) || !aligned(dalpha, 4) || !aligned(status, 4))
-    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: alpha or dalpha NULL, or they or status misaligned", fn);
+  if (!alpha || !dalpha || !aligned(alpha, 4) || !aligned(dalpha, 4))
+    return set_error(ENGRAM_ERR_INVALID_ARG, "%s: alpha or dalpha NULL or misaligned", fn);
   if (!(eps >= 0.f) || !isfinite(eps))
     return set_error(ENGRAM_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", fn);
   const size_t need = engram_gate_add_grad_workspace_bytes();
@@ -360,10 +360,9 @@ ENGRAM_API engram_status engram_gate_add_grad(const float *k, const uint8_t *sta
     const void *p;
     size_t n;
   } outs[4] = {{dx, sb}, {dk, db}, {dalpha, 16}, {workspace, need}},
-    ins[6] = {{k, kb}, {state, state ? (size_t)n_tokens : 0}, {streams_in, sb}, {alpha, 16}, {dy, sb},
-              {status, 4}};
+    ins[5] = {{k, kb}, {state, state ? (size_t)n_tokens : 0}, {streams_in, sb}, {alpha, 16}, {dy, sb}};
   for (int o = 0; o < 4; ++o) {
-    for (int i = 0; i < 6; ++i)
+    for (int i = 0; i < 5; ++i)
       if (!(o == 0 && i == 4 && dx == dy) && overlap(outs[o].p, outs[o].n, ins[i].p, ins[i].n))
         return set_error(ENGRAM_ERR_INVALID_ARG, "%s: an output overlaps an input", fn);
     for (int i = 0; i < o; ++i)
@@ -382,8 +381,6 @@ ENGRAM_API engram_status engram_gate_add_grad(const float *k, const uint8_t *sta
   p.alpha = alpha;
   p.partial = static_cast<float4 *>(workspace);
   p.dalpha = dalpha;
-  p.status = status;
-  p.wait_limit_ns = engram::wait_limit_ns();
   p.T = n_tokens;
   p.D = D;
   p.eps = eps;

@@ -81,15 +81,12 @@ struct GateGradParams {
   float4 *partial;  // [kGateGradMaxBlocks]: each block's sums of g <dy_s, k>
   float *dalpha;
   int64_t T;
-  int32_t *status;
-  int64_t wait_limit_ns;
   int32_t D;
   float eps;
   float inv_D, inv_sqrt_D;  // set by the launcher, as are the rest
-  int32_t group, stages;    // lanes per narrow token, stages of the ring
+  int32_t group;            // lanes per narrow token
 };
 constexpr int kGateGradMaxBlocks = 4096;
-constexpr int kGateGradMaxStages = 8;
 cudaError_t launch_gate_grad(const GateGradParams &p, int dk_dtype, cudaStream_t stream);
 
 struct QuantiseParams {

@@ -667,8 +667,7 @@ ENGRAM_API engram_status engram_fp8_matmul(const uint8_t *a, int64_t a_stride, c
  * A dead token (state 1) passes dy through (dk = 0); a bad one (state 2) has dk = 0
  * and its dx left unwritten; neither adds to dalpha.  D a multiple of 16 in [16,
  * 8192]; all but state, alpha and dalpha 16-byte aligned.  n_tokens == 0 zeroes
- * dalpha.  A copy that does not arrive within the wait limit sets ENGRAM_FLAG_TIMEOUT and
- * leaves that block's later tokens unwritten.
+ * dalpha.
  */
 ENGRAM_API size_t engram_gate_add_grad_workspace_bytes(void);
 ENGRAM_API engram_status engram_gate_add_grad(const float *k, const uint8_t *state,
@@ -677,7 +676,7 @@ ENGRAM_API engram_status engram_gate_add_grad(const float *k, const uint8_t *sta
                                               float eps, const uint16_t *dy, uint16_t *dx,
                                               void *dk, int32_t dk_dtype, float *dalpha,
                                               void *workspace, size_t workspace_bytes,
-                                              int32_t *status, void *stream);
+                                              void *stream);
 
 /*
  * engram_read_status -- waits for `stream`, copies the device status word into

@@ -94,13 +94,13 @@ def test_matmul_argument_errors(eg):
 def test_gate_grad_argument_errors(eg):
     need = eg.engram_gate_add_grad_workspace_bytes()
     base = dict(k=P, state=None, n=10, D=64, x=Q, alpha=W, eps=1e-6, dy=S, dx=O, dk=O + (1 << 20), kd=F32,
-                dalpha=W + 64, ws=W + 4096, wb=need, status=None, stream=None)
+                dalpha=W + 64, ws=W + 4096, wb=need, stream=None)
     refuses(eg, "engram_gate_add_grad", base, [
         dict(k=None), dict(k=P + 4), dict(n=-1), dict(n=2 ** 31), dict(D=8), dict(D=24), dict(D=8208), dict(x=None),
         dict(x=Q + 2), dict(alpha=None), dict(alpha=W + 1), dict(eps=-1.0), dict(eps=NAN), dict(eps=INF),
         dict(dy=None), dict(dx=None), dict(dk=None), dict(dk=O + (1 << 20) + 8), dict(kd=4), dict(dalpha=None),
         dict(dalpha=W + 65), dict(ws=None), dict(ws=W + 4104), dict(wb=need - 1), dict(dx=Q), dict(dx=S + 512),
-        dict(dk=P), dict(dalpha=W + 8), dict(dk=O), dict(ws=W + 64), dict(status=W + 2), dict(status=O)])
+        dict(dk=P), dict(dalpha=W + 8), dict(dk=O), dict(ws=W + 64)])
 
 
 def test_binding_rejects_cpu_tensors(eg):
