@@ -2,7 +2,7 @@
 //   grad[v] (+)= scale * sum over positions i with ids[i] = v, in ascending i, of dy[i]
 // as a dense [rows, D] gradient, or as the distinct ids and their rows.
 //
-// 1. Sort (id, position) pairs by id, stably.  Up to 4096 ids: each id's place is the
+// 1. Sort (id, position) pairs by id, stably.  Up to 6144 ids: each id's place is the
 //    number of ids before it in that order, counted by comparing it with all of them in
 //    shared memory -- n^2 comparisons, but one launch over all SMs.  More: a radix sort, 10
 //    bits a pass at most, three launches a pass (digit counts per tile, their prefix sums
@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
 constexpr int kDigits = 1024;      // most digits of a pass: two a thread
-constexpr int kCountSort = 4096;   // most pairs sorted by counting
+constexpr int kCountSort = 6144;   // most pairs sorted by counting
 constexpr uint32_t kNoKey = 0xFFFFFFFFu;
 constexpr int kRunGroup = 16;      // chunks whose runs are counted together
 
@@ -326,7 +326,7 @@ constexpr size_t scatter_smem(int per) {
 }
 
 // Both of the next two kernels' work for lists that one block reads quickly.
-constexpr int kRunsSmall = 16384;
+constexpr int kRunsSmall = kCountSort;
 __global__ void __launch_bounds__(kSortThreads) runs_small_kernel(const __grid_constant__ EmbedGradParams p) {
   __shared__ uint32_t s_sum[32];
   dependency_wait();

@@ -107,41 +107,25 @@ __device__ __forceinline__ void load_vals(const T *row, int64_t col, int64_t K, 
 
 constexpr int kRowsThreads = 256;
 
-template <typename T, int U>
+template <typename T>
 __global__ void __launch_bounds__(kRowsThreads) quantise_linear_kernel(const __grid_constant__ QuantiseParams p,
                                                                        int64_t n) {
   dependency_wait();
   const int in = threadIdx.x & 7;
-  const int64_t first = (int64_t)blockIdx.x * (kRowsThreads / 8 * U) + (threadIdx.x >> 3);
-  float f[U][16];
+  const int64_t b = (int64_t)blockIdx.x * (kRowsThreads / 8) + (threadIdx.x >> 3), at = b * 128 + in * 8;
+  float lo[8], hi[8];  // zero past the last block
+  load_vals<T, 8, true>(static_cast<const T *>(p.x), at, n * 128, lo);
+  load_vals<T, 8, true>(static_cast<const T *>(p.x), at + 64, n * 128, hi);
+  float m = max_mag(max_of<8>(lo), max_of<8>(hi));
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t at = (first + u * (kRowsThreads / 8)) * 128 + in * 8;
-    if (at < n * 128) {
-      float lo[8], hi[8];
-      load_vals<T, 8, true>(static_cast<const T *>(p.x), at, n * 128, lo);
-      load_vals<T, 8, true>(static_cast<const T *>(p.x), at + 64, n * 128, hi);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[u][i] = lo[i], f[u][8 + i] = hi[i];
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t b = first + u * (kRowsThreads / 8);
-    float m = b < n ? max_of<16>(f[u]) : 0.f;
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) m = max_mag(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (b >= n) continue;
-    const uint32_t s = scale_byte(m);
-    if (in == 0) p.s[b] = (uint8_t)s;
-    const float by = multiplier(s);
-    uint8_t *q = p.q + b * 128 + in * 8;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      *reinterpret_cast<uint2 *>(q + 64 * h) =
-          make_uint2(quantise4(f[u][8 * h], f[u][8 * h + 1], f[u][8 * h + 2], f[u][8 * h + 3], by),
-                     quantise4(f[u][8 * h + 4], f[u][8 * h + 5], f[u][8 * h + 6], f[u][8 * h + 7], by));
-  }
+  for (int o = 4; o > 0; o >>= 1) m = max_mag(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (b >= n) return;
+  const uint32_t s = scale_byte(m);
+  if (in == 0) p.s[b] = (uint8_t)s;
+  const float by = multiplier(s);
+  uint2 *q = reinterpret_cast<uint2 *>(p.q + at);
+  q[0] = make_uint2(quantise4(lo[0], lo[1], lo[2], lo[3], by), quantise4(lo[4], lo[5], lo[6], lo[7], by));
+  q[8] = make_uint2(quantise4(hi[0], hi[1], hi[2], hi[3], by), quantise4(hi[4], hi[5], hi[6], hi[7], by));
 }
 
 // Blocks of 128 values numbered along the rows, 16 lanes each, U of them a thread.  `magic`
@@ -427,11 +411,8 @@ cudaError_t launch_typed(const QuantiseParams &p, cudaStream_t stream) {
     const int64_t n = p.M * kblocks;
     constexpr int kPer = kRowsThreads / 16;
     if (vec && p.K % 128 == 0 && (p.M == 1 || (p.x_stride == p.K && p.q_stride == p.K))) {
-      if (n <= kSms * 4 * (kRowsThreads / 8))
-        return launch(quantise_linear_kernel<T, 1>, (n * 8 + kRowsThreads - 1) / kRowsThreads, kRowsThreads, 0, stream,
-                      1, p, n);
-      return launch(quantise_linear_kernel<T, 2>, (n * 4 + kRowsThreads - 1) / kRowsThreads, kRowsThreads, 0, stream,
-                    1, p, n);
+      return launch(quantise_linear_kernel<T>, (n * 8 + kRowsThreads - 1) / kRowsThreads, kRowsThreads, 0, stream, 1,
+                    p, n);
     }
     const uint32_t magic = (uint32_t)(((1ull << 32) + kblocks - 1) / kblocks);
     if (n <= kSms * 8 * kPer) {

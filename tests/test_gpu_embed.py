@@ -161,3 +161,29 @@ def test_embed_runs_on_the_given_stream(eg):
     eg.engram_embed(ic, late, out=out, stream=s)
     s.synchronize()
     assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("table,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("T,R,D,pad", [(9801, 24, 256, 0), (6601, 24, 64, 8), (79001, 2, 32, 0), (2503, 24, 1024, 16)])
+def test_embed_many_rows(eg, T, R, D, pad, table, out):
+    """Lists long enough for the form that takes 32 rows a warp, compared on the device."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(T)
+    rows, scale = 1001, 0.37
+    t = torch.randn(rows, D + pad, device="cuda", generator=g).to(_dt(table))[:, :D]
+    ids = torch.randint(-1, rows, (T, R), device="cuda", generator=g, dtype=torch.int32)
+    ids[T - 1] = -1
+    ids[:, 1] = torch.where(ids[:, 1] % 7 == 3, rows + ids[:, 1], ids[:, 1])  # bad ones
+    got = torch.full((T, R, D + pad), 9.0, dtype=_dt(out), device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    eg.engram_embed(ids, t, scale=scale, out=got[..., :D], status=status)
+    assert eg.engram_read_status(status)[1] == eg.FLAG_BAD_ROW
+    assert (got[..., D:] == 9.0).all()
+    for a in range(0, T, 2000):  # in slices: fp64
+        i, y = ids[a:a + 2000].long(), got[a:a + 2000, :, :D].double()
+        ref = t.double()[i.clamp(0, rows - 1)] * float(np.float32(scale)) * (i >= 0).unsqueeze(-1)
+        tol = 2.0 ** -24 * ref.abs() + 2.0 ** -133
+        if out == "bf16":
+            tol = tol + 2.0 ** -8 * 1.001 * ref.abs()
+        bad = (i >= rows).unsqueeze(-1).expand_as(y)
+        assert (torch.where(bad, y == 9.0, (y - ref).abs() <= tol)).all()

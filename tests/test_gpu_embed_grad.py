@@ -264,3 +264,22 @@ def test_runs_on_the_given_stream(eg):
     eg.engram_embed_grad(ids, late, 700, grad=grad, workspace=ws, stream=s)
     s.synchronize()
     assert torch.equal(grad, want)
+
+
+@pytest.mark.parametrize("T,R", [(6143, 1), (1536, 4), (6145, 1), (1229, 5), (622591, 1), (207532, 3)])
+@pytest.mark.parametrize("kind", ["skewed", "uniform"])
+def test_list_lengths_where_the_sort_changes(eg, T, R, kind):
+    import torch
+    D, rows = 8, 200003
+    ids, dy = make_ids(T, R, rows, kind, seed=T), make_dy(T, R, D, "f32", False, seed=T)
+    uniq, ref, bound = reference(ids, dy, rows, 0.37, False)
+    ci, cd = torch.from_numpy(ids).cuda(), dy.cuda()
+    grad = eg.engram_embed_grad(ci, cd, rows, scale=0.37)
+    row_ids, grads, count = eg.engram_embed_grad_rows(ci, cd, rows, scale=0.37)
+    n = int(count)
+    got_ids = row_ids.cpu().numpy()
+    assert n == len(uniq) and (got_ids[:n] == uniq).all() and (got_ids[n:] == -1).all()
+    close(grads[:n].double().cpu().numpy(), ref, bound, "f32")
+    assert torch.equal(grads[:n], grad[torch.from_numpy(uniq).cuda()])
+    grad[torch.from_numpy(uniq).cuda()] = 0
+    assert not grad.any()
