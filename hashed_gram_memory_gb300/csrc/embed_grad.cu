@@ -74,9 +74,9 @@ __device__ __forceinline__ void rank_tile(const uint32_t (&key)[PER], int n, int
                                           uint32_t (&place)[PER]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t mask = (1u << bits) - 1;
-  uint4 *zero = reinterpret_cast<uint4 *>(&s_cnt[0][0]);
-  for (int i = tid; i < kSortWarps * kDigits / 8; i += kSortThreads) zero[i] = make_uint4(0, 0, 0, 0);
-  __syncthreads();
+  uint4 *zero = reinterpret_cast<uint4 *>(s_cnt[warp]);
+  for (int i = lane; i <= (int)mask / 8; i += 32) zero[i] = make_uint4(0, 0, 0, 0);
+  __syncwarp();
 #pragma unroll
   for (int r = 0; r < PER; ++r) {
     const bool have = warp * 32 * PER + 32 * r + lane < n;
@@ -84,6 +84,7 @@ __device__ __forceinline__ void rank_tile(const uint32_t (&key)[PER], int n, int
     uint32_t same = __ballot_sync(0xffffffffu, have);  // the lanes with this digit, bit by bit
 #pragma unroll
     for (int b = 0; b < 10; ++b) {
+      if (b == bits) break;
       const uint32_t set = __ballot_sync(0xffffffffu, d >> b & 1);
       same &= d >> b & 1 ? set : ~set;
     }
@@ -99,12 +100,14 @@ __device__ __forceinline__ void rank_tile(const uint32_t (&key)[PER], int n, int
   // Exclusive prefix over the warps of each digit (two a thread, added side by side: a
   // tile's counts fit 16 bits), then over the digits.
   uint32_t total = 0;
+  if (2 * tid <= (int)mask) {
 #pragma unroll
-  for (int w = 0; w < kSortWarps; ++w) {
-    uint32_t *both = reinterpret_cast<uint32_t *>(s_cnt[w]) + tid;
-    const uint32_t c = *both;
-    *both = total;
-    total += c;
+    for (int w = 0; w < kSortWarps; ++w) {
+      uint32_t *both = reinterpret_cast<uint32_t *>(s_cnt[w]) + tid;
+      const uint32_t c = *both;
+      *both = total;
+      total += c;
+    }
   }
   const uint32_t base = block_exclusive((total & 0xFFFF) + (total >> 16), s_sum);
   s_start[2 * tid] = base;
