@@ -201,6 +201,9 @@ __device__ __forceinline__ void store_out(TO *dst, uint32_t v) {
 // A warp's part of an accumulator -- 32 lanes (outputs n, n + 1, ..), `chunks` times 16 columns
 // (outputs m0, m0 + 1, ..) -- goes to memory or (MULTI) into sums over the segments that the
 // last one stores.  `release` runs once the last column is in registers, before its stores.
+// The sums move through the registers so that one chunk's code serves all: written out per
+// chunk it was fetched once a tile, from beyond the instruction cache, and that took 13 us of
+// 47 for one tile of 92 blocks (151 x 5888 x 11,776).
 template <typename TO, int CHUNKS, bool MULTI>
 struct Drain {
   float sum[MULTI ? CHUNKS * 16 : 1];
@@ -210,25 +213,23 @@ struct Drain {
                                       int64_t m0, int64_t M, bool mine, F release) {
     const int rows = (int)min((int64_t)chunks * 16, M - m0);
     if constexpr (MULTI) {
-#pragma unroll
-      for (int c = 0; c < CHUNKS; ++c) {
-        if (c < chunks) {
-          uint32_t v[16];
-          tmem_ld16(taddr + c * 16, v);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float f = __uint_as_float(v[i]);
-            sum[c * 16 + i] = first ? f : sum[c * 16 + i] + f;
-          }
-        }
-      }
-      release();
-      if (!last || !mine) return;
       out += m0 * stride;
+#pragma unroll 1
+      for (int c = 0; c < CHUNKS; ++c) {
+        uint32_t v[16];
+        if (c < chunks) tmem_ld16(taddr + c * 16, v);
+        if (c == chunks - 1) release();
 #pragma unroll
-      for (int i = 0; i < CHUNKS * 16; ++i) {
-        if (i < rows) store_out(out, __float_as_uint(sum[i]));
-        out += stride;
+        for (int i = 0; i < 16; ++i) {
+          if (!first) v[i] = __float_as_uint(sum[i] + __uint_as_float(v[i]));
+          if (last && mine && c * 16 + i < rows) store_out(out, v[i]);
+          out += stride;
+        }
+        // The chunk's sums go to the back: after CHUNKS turns each is in its place again.
+#pragma unroll
+        for (int i = 0; i < CHUNKS * 16 - 16; ++i) sum[i] = sum[i + 16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[CHUNKS * 16 - 16 + i] = __uint_as_float(v[i]);
       }
     } else {
       out += m0 * stride;
@@ -513,7 +514,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
 // ---- CTA pairs ------------------------------------------------------------------------
 
 constexpr int kPairQMax = 240;
-constexpr int kPairThreads = 384;
+constexpr int kPairThreads = 512;
+constexpr int kPairParts = 3;  // of a tile's columns, a warp of each quarter of the lanes each
 constexpr uint32_t kPairStageBudget = 213 * 1024;
 constexpr uint32_t kPairGroupBytes = (kP + 256) * 4;
 constexpr uint32_t kPairSlotBytes = 4 * kPairGroupBytes;
@@ -574,7 +576,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(acc_full + a, 1);
-      mbar_init(acc_empty + a, 16);
+      mbar_init(acc_empty + a, 2 * 4 * kPairParts);
     }
     mbar_init(mma_done, 1);
     *abort_flag = 0;
@@ -737,13 +739,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   } else if (warp >= 4) {
     // ------------------------------------------------- epilogue (both CTAs)
-    const int quad = warp & 3, half = (warp - 4) >> 2;
+    const int quad = warp & 3, part = (warp - 4) >> 2;
     const uint32_t acc_empty_lead = map_to_rank(smem_u32(acc_empty), 0);
-    // This warp's 16-column chunks: the first or the second half of the tile's.
-    const int c0 = half ? (qt / 16 + 1) / 2 : 0, chunks = half ? qt / 16 - c0 : (qt / 16 + 1) / 2;
+    // This warp's 16-column chunks: a part of the tile's.
+    const int c0 = qt / 16 * part / kPairParts, chunks = qt / 16 * (part + 1) / kPairParts - c0;
     uint32_t unit = 0;
     bool ok = true;
-    Drain<TO, 8, MULTI> drain;
+    Drain<TO, (kPairQMax / 16 + kPairParts - 1) / kPairParts, MULTI> drain;
     for (int64_t tile = cluster; ok && tile < p.tiles; tile += n_clusters) {
       int64_t tp, tq;
       tile_at(p, tile, tp, tq);
@@ -865,11 +867,15 @@ cudaError_t launch_fp8_matmul(const MatmulParams &p, int out_dtype, cudaStream_t
   d.seg_blocks = (int32_t)(ceil_div(ceil_div(d.kblocks, segments), 4) * 4);
   d.segments = (int32_t)ceil_div(d.kblocks, d.seg_blocks);
   // The form and the width of a tile along a go by an estimate of their time in microseconds,
-  // fitted to both forms over M 1 .. 16,384, N 1024 and 4096, K 256 .. 8192 (it picks the
-  // faster one there, or one within 5 %):
+  // less the launch's, fitted to all forms over M 1 .. 16,384, N 128 .. 8192, K 256 .. 16,384:
   //   single: 1.3 + 0.23 a block of K, for each wave of tiles over the SMs;
   //   pairs:  2.1 + max(0.2, 0.00118 (width + 16)) a block, but at least what draining the
-  //           tile takes, 4.6 at 240 columns; for each wave over the pairs, and 1.5 once.
+  //           tile takes, 4.6 at 240 columns; for each wave over the pairs, and 1.5 once;
+  //   split:  4 or 8 CTAs share a tile's K where there is room for them, two an SM: 0.25 a
+  //           block of a CTA's part, and the joining, 2.4 + 0.02 a column of the tile and
+  //           0.00014 a column of each CTA.
+  // (16 x 4096 x 6144: split in 8 9.0 us, single 14.2; 512 x 1024 x 8192: in 4 13.3, in 8 14.5,
+  // single 18.5, pairs 19.1; 16 x 4096 x 1024: in 8 6.4, single 5.4.)
   const double kb = d.kblocks;
   const int q_single = (int)(p.M < kQMax ? ceil_div(p.M, 16) * 16 : kQMax);
   const int64_t single_tiles = ceil_div(p.N, kP) * ceil_div(p.M, q_single);
@@ -883,28 +889,26 @@ cudaError_t launch_fp8_matmul(const MatmulParams &p, int out_dtype, cudaStream_t
       if (us < pair_us) pair_us = us, d.q_tile = qt;
     }
   }
-  const bool pair = pair_us < single_us;
-  d.splits = 1;
+  double split_us = HUGE_VAL;
+  for (int n = 4; n <= 8; n *= 2) {
+    if (n * single_tiles > 2 * info.sms || d.kblocks < n || ceil_div(d.kblocks, n) > kSegmentBlocks) continue;
+    const double us = 0.25 * kb / n + 2.4 + 0.02 * q_single + 0.00014 * q_single * n * single_tiles;
+    if (us < split_us) split_us = us, d.splits = n;
+  }
+  const bool split = split_us < single_us && split_us < pair_us, pair = !split && pair_us < single_us;
   int form;
   if (pair) {
     form = d.segments > 1 ? kPairMulti : kPair;
     d.tiles_p = ceil_div(p.N, 2 * kP);
     d.stages = (int32_t)(kPairStageBudget / ((kP + d.q_tile / 2) * 128));
   } else {
-    form = d.segments > 1 ? kSingleMulti : kSingle;
+    form = split ? kSplit : d.segments > 1 ? kSingleMulti : kSingle;
     d.tiles_p = ceil_div(p.N, kP);
     d.q_tile = q_single;
-    d.stages = (int32_t)(kStageBudget / ((kP + d.q_tile) * 128));
-    // Eight CTAs share K where there is room for them and seven eighths of the blocks' time
-    // (0.2 each) is more than the joining takes: measured 1 + 0.02 a column of the tile and
-    // 0.06 a tile (16 x 4096 x 6144: 9.0 us against 14.2; 16 x 4096 x 1024: 6.4 against 5.4).
-    if (8 * single_tiles <= 2 * info.sms && ceil_div(d.kblocks, 8) <= kSegmentBlocks &&
-        0.175 * kb > 1 + 0.02 * d.q_tile + 0.06 * single_tiles) {
-      form = kSplit;
-      d.splits = 8;
-      d.segments = 1;  // a CTA's part of K is one
+    d.stages = (int32_t)((split ? kSplitStageBudget : kStageBudget) / ((kP + d.q_tile) * 128));
+    if (split) {  // a CTA's part of K is one segment
+      d.segments = 1;
       d.seg_blocks = kSegmentBlocks;
-      d.stages = (int32_t)(kSplitStageBudget / ((kP + d.q_tile) * 128));
     }
   }
   if (d.stages > kMaxStages) d.stages = kMaxStages;
