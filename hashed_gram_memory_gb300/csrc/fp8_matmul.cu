@@ -21,16 +21,22 @@
 //     a tile's MMAs follow the last one's without waiting for the epilogue;
 //   fp8_matmul_kernel: one CTA per SM, 128 x up to 128 tiles, for products too small to
 //     fill the pairs; where even those leave SMs idle (a few rows of a: reading b is the
-//     work), the CTAs of a cluster share a tile, each with a part of K, and add their
+//     work), 4 or 8 CTAs of a cluster share a tile, each with a part of K, and add their
 //     parts through distributed shared memory in rank order; two such CTAs an SM, whose
 //     stages together have most of a decode step's weights on the way at once.
+// Measured: 65,536 x 4096 x 6144 893 us (3.7 PFLOP/s; bound by the tensor cores, and in a
+// long loop by the power limit: 1120 us near 1.6 GHz); 4096 x 6144 x 16,411 with rows 16,416
+// bytes apart 262 us (3.2 PFLOP/s; every 128-byte slice of a row straddles two lines);
+// 16 x 4096 x 6144 8.9 us (25 MB of weights, 3.8 us at the copy bandwidth; the rest is the
+// launch, the first bytes' latency and the join).
 // Warps:
 //   0     TMA producer: a ring of stages, each a 128-byte slice along K of the tile's rows
 //         of a and b (128-byte swizzle);
 //   1     allocates TMEM; one thread (of the pair's even CTA) copies the scales to TMEM
 //         (tcgen05.cp) and issues the MMAs into one of two accumulators;
-//   2, 3  scales (the pairs' second warp shares the work): for every four blocks of K one 32-bit word per row, put into shared
-//         memory in the order tcgen05.cp wants (word (r%32)*4 + r/32 of each 128 rows);
+//   2, 3  scales (the pairs' two warps share the work): for every four blocks of K one 32-bit
+//         word per row, put into shared memory in the order tcgen05.cp wants (word (r%32)*4 +
+//         r/32 of each 128 rows);
 //   4..   epilogue: TMEM lanes 32*(warp%4).., stores.
 // Every wait is bounded as in wkv_gemm.cu: one that gives up sets ENGRAM_FLAG_TIMEOUT and
 // leaves the tiles not yet stored unwritten.
@@ -704,38 +710,40 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
     };
     Scales w[6];
-    int64_t tile = cluster;
-    int kb = 0;
-    load(tile, kb, w);
-    while (ok && tile < p.tiles) {
-      const int64_t next_tile = kb + 16 < kblocks ? tile : tile + n_clusters;
-      const int next_kb = kb + 16 < kblocks ? kb + 16 : 0;
+    int64_t tile = cluster, next_tile = cluster;
+    int kb = kblocks, next_kb = 0;
+    while (ok) {
       Scales next[6];
       load(next_tile, next_kb, next);
-      const int slot = batch & 1;
-      if (!(ok = warp_wait(sc_empty + slot, ((batch >> 1) & 1) ^ 1, abort_flag, p))) break;
+      if (kb < kblocks) {  // not the first time
+        const int slot = batch & 1;
+        if (!(ok = warp_wait(sc_empty + slot, ((batch >> 1) & 1) ^ 1, abort_flag, p))) break;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        uint32_t *dst =
-            reinterpret_cast<uint32_t *>(slots + slot * kPairSlotBytes + g * kPairGroupBytes) + lane * 4;
-        if (first) {
-          *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0].word(g), w[1].word(g), w[2].word(g), w[3].word(g));
-          *reinterpret_cast<uint2 *>(dst + 128) = make_uint2(w[4].word(g), w[5].word(g));
-        } else {
-          *reinterpret_cast<uint2 *>(dst + 130) = make_uint2(w[0].word(g), w[1].word(g));
-          *reinterpret_cast<uint4 *>(dst + 256) =
-              make_uint4(w[2].word(g), w[3].word(g), w[4].word(g), w[5].word(g));
+        for (int g = 0; g < 4; ++g) {
+          uint32_t *dst =
+              reinterpret_cast<uint32_t *>(slots + slot * kPairSlotBytes + g * kPairGroupBytes) + lane * 4;
+          if (first) {
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0].word(g), w[1].word(g), w[2].word(g), w[3].word(g));
+            *reinterpret_cast<uint2 *>(dst + 128) = make_uint2(w[4].word(g), w[5].word(g));
+          } else {
+            *reinterpret_cast<uint2 *>(dst + 130) = make_uint2(w[0].word(g), w[1].word(g));
+            *reinterpret_cast<uint4 *>(dst + 256) =
+                make_uint4(w[2].word(g), w[3].word(g), w[4].word(g), w[5].word(g));
+          }
         }
+        // Once for 16 blocks: the fence and the cluster-wide release wait for everything this
+        // warp has in flight, and once for four blocks they took longer than the blocks.
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(sc_full_lead + 8u * slot);
+        ++batch;
       }
-      // Once for 16 blocks: the fence and the cluster-wide release wait for everything this
-      // warp has in flight, and once for four blocks they took longer than the blocks.
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(sc_full_lead + 8u * slot);
-      ++batch;
+      if ((tile = next_tile) >= p.tiles) break;
 #pragma unroll
       for (int i = 0; i < 6; ++i) w[i] = next[i];
-      tile = next_tile, kb = next_kb;
+      kb = next_kb;
+      next_kb = kb + 16 < kblocks ? kb + 16 : 0;
+      next_tile = next_kb ? tile : tile + n_clusters;
     }
   } else if (warp >= 4) {
     // ------------------------------------------------- epilogue (both CTAs)

@@ -287,3 +287,11 @@ def test_product_empty(eg):
     assert eg.engram_fp8_matmul(a, sa, e, se).shape == (5, 0)
     assert [tuple(t.shape) for t in eg.engram_fp8_quantise(torch.empty(0, 64, device="cuda"), cols=True)] == \
         [(0, 64), (0, 1), (64, 0), (64, 0)]
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(512, 1024, 8192), (16, 6144, 4096), (371, 260, 12052), (151, 5888, 8320),
+                                   (53, 1283, 12462), (2100, 1500, 8320), (405, 128, 5120), (241, 2300, 16400)])
+def test_product_long_sums_and_few_tiles(eg, M, N, K, out):
+    """K shared by the CTAs of a cluster, and K in several accumulators, at every kind of tile."""
+    test_product_matches_fp64(eg, M, N, K, (1, 128), out)
