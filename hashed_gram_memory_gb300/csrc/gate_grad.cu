@@ -23,11 +23,14 @@
 // the partials as a tree in a fixed order, so the result does not depend on timing.
 // Measured: 65,536 x 4096 1054 us (26 D bytes a token: 6.6 TB/s), 512 x 4096 13 us
 // (the load, sums and stores of two tokens, one after the other, and the second launch).
-// At D = 8192 one block fits an SM and nothing overlaps: 32,768 tokens take 1530 us.
+// A block of more than 512 threads would have an SM to itself and overlap nothing, so wider
+// tokens take a pair of CTAs (a cluster), half of the columns each, whose sums meet through
+// distributed shared memory: 32,768 x 8192 1291 us, a block a token 1531.
 #include <atomic>
 
 #include "launch.cuh"
 #include "lookup_common.cuh"
+#include "tensor_core.cuh"
 #include "train_internal.cuh"
 
 namespace engram {
@@ -122,11 +125,21 @@ __device__ __forceinline__ void warp_sums(const float (&r)[7], float *s_red, int
   if ((lane & 3) == 0 && lane < 28) s_red[(lane >> 2) * warps + warp] = v[0];
 }
 
-// .. and, behind a barrier, over its warps: a lane a warp, then a butterfly.
+// .. and, behind a barrier, over its warps: a lane a warp, then a butterfly.  PAIR: over the
+// warps of both CTAs, in the order of their ranks.
+template <bool PAIR>
 __device__ __forceinline__ void block_sums(float (&r)[7], const float *s_red, int warps, int lane) {
+  const int rank = PAIR && lane >= warps;
+  const uint32_t from = PAIR ? map_to_rank(smem_u32(s_red), rank) + (lane - rank * warps) * 4 : 0;
 #pragma unroll
   for (int i = 0; i < 7; ++i) {
-    float v = lane < warps ? s_red[i * warps + lane] : 0.f;
+    float v = 0.f;
+    if constexpr (PAIR) {
+      if (lane < 2 * warps)
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(from + i * warps * 4) : "memory");
+    } else {
+      if (lane < warps) v = s_red[i * warps + lane];
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     r[i] = v;
@@ -189,20 +202,23 @@ __device__ __forceinline__ void store_dead(const GateGradParams &p, uint8_t stat
   }
 }
 
-// One token a block at a time, threads = D/8 rounded up to warps.
-template <typename TK>
-__global__ void __launch_bounds__(1024) gate_grad_block_kernel(const __grid_constant__ GateGradParams p) {
-  __shared__ float s_red[2][7 * 32];  // two tokens in turn: one barrier a token
+// One token a block at a time, threads = D/8 rounded up to warps; PAIR: a token a pair of
+// CTAs (a cluster), half of its columns each.
+template <typename TK, bool PAIR>
+__global__ void __launch_bounds__(512, 2) gate_grad_block_kernel(const __grid_constant__ GateGradParams p) {
+  __shared__ float s_red[2][7 * 16];  // two tokens in turn: one barrier a token
   dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  const int col = tid * 8;
-  const bool mine = col < p.D;
+  const int width = PAIR ? p.D / 2 : p.D;
+  const bool mine = tid * 8 < width;
+  const int col = PAIR ? (int)cluster_rank() * width + tid * 8 : tid * 8;
+  const int64_t first = PAIR ? blockIdx.x / 2 : blockIdx.x, step = PAIR ? gridDim.x / 2 : gridDim.x;
   const float4 alpha = make_float4(__ldg(p.alpha), __ldg(p.alpha + 1), __ldg(p.alpha + 2),
                                    __ldg(p.alpha + 3));
   float4 da = make_float4(0.f, 0.f, 0.f, 0.f);
   int buf = 0;
-  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-    const uint8_t state = p.state ? p.state[t] : 0;  // block-uniform
+  for (int64_t t = first; t < p.T; t += step) {
+    const uint8_t state = p.state ? p.state[t] : 0;  // the same in the whole block or pair
     if (state == kDead || state == kBad) {
       if (mine) store_dead<TK>(p, state, t, col);
       continue;
@@ -214,15 +230,19 @@ __global__ void __launch_bounds__(1024) gate_grad_block_kernel(const __grid_cons
       partial_sums(c, r);
     }
     warp_sums(r, s_red[buf], warp, warps, lane);
-    __syncthreads();
-    block_sums(r, s_red[buf], warps, lane);
+    if constexpr (PAIR)
+      cluster_sync();
+    else
+      __syncthreads();
+    block_sums<PAIR>(r, s_red[buf], warps, lane);
     buf ^= 1;
     const Gate o = gate_of(r, alpha, p);
     da.x = fmaf(o.g, r[3], da.x), da.y = fmaf(o.g, r[4], da.y);
     da.z = fmaf(o.g, r[5], da.z), da.w = fmaf(o.g, r[6], da.w);
     if (mine) store_cols<TK>(c, o, alpha, p, t, col);
   }
-  if (tid == 0) p.partial[blockIdx.x] = da;
+  if constexpr (PAIR) cluster_sync();  // no CTA leaves while the other may still read its sums
+  if (tid == 0 && (!PAIR || cluster_rank() == 0)) p.partial[first] = da;
 }
 
 // Narrow tokens (D <= 256): p.group lanes a token, 256 / group tokens a block.
@@ -329,11 +349,16 @@ cudaError_t launch_typed(GateGradParams p, cudaStream_t stream) {
       if ((e = resident_blocks<gate_grad_warp_kernel<TK>>(256, n)) != cudaSuccess) return e;
       n = (int)(need < n ? need : n);
       e = launch(gate_grad_warp_kernel<TK>, n, 256, 0, stream, 1, p);
-    } else {
+    } else if (chunks <= 512) {
       const int threads = (chunks + 31) / 32 * 32;
-      if ((e = resident_blocks<gate_grad_block_kernel<TK>>(threads, n)) != cudaSuccess) return e;
+      if ((e = resident_blocks<gate_grad_block_kernel<TK, false>>(threads, n)) != cudaSuccess) return e;
       n = (int)(p.T < n ? p.T : n);
-      e = launch(gate_grad_block_kernel<TK>, n, threads, 0, stream, 1, p);
+      e = launch(gate_grad_block_kernel<TK, false>, n, threads, 0, stream, 1, p);
+    } else {
+      const int threads = (chunks / 2 + 31) / 32 * 32;
+      if ((e = resident_blocks<gate_grad_block_kernel<TK, true>>(threads, n)) != cudaSuccess) return e;
+      n = (int)(p.T < n / 2 ? p.T : n / 2);
+      e = launch(gate_grad_block_kernel<TK, true>, 2 * (int64_t)n, threads, 0, stream, 2, p);
     }
     if (e != cudaSuccess) return e;
   }
