@@ -187,3 +187,12 @@ def test_embed_many_rows(eg, T, R, D, pad, table, out):
             tol = tol + 2.0 ** -8 * 1.001 * ref.abs()
         bad = (i >= rows).unsqueeze(-1).expand_as(y)
         assert (torch.where(bad, y == 9.0, (y - ref).abs() <= tol)).all()
+
+
+@pytest.mark.parametrize("table,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("T,R,D,pad", [(5003, 1, 17, 0), (2600, 2, 33, 1), (811, 6, 109, 0), (5001, 1, 66, 3),
+                                       (1700, 3, 250, 0), (2503, 2, 475, 2), (204, 24, 1278, 0), (4865, 1, 256, 1)])
+def test_embed_many_unaligned_rows(eg, T, R, D, pad, table, out):
+    if R == 1:  # the check below writes bad ids into the second column
+        T, R = T // 2 + 1, 2
+    test_embed_many_rows(eg, T, R, D, pad, table, out)
