@@ -24,8 +24,8 @@
 // lists stay in L2.  Measured: 1,572,864 pairs of 256 bf16 columns into 1.30 M distinct rows
 // 448 us, of which the sums 340 (2.1 GB of random 512-byte and 1 KB rows: 6.2 TB/s) and the
 // sort, three passes of 10 bits, about 95; 16,384 x 4096 into a dense 129,280-row gradient
-// 371 us (2.25 GB moved: 6.1 TB/s); 1536 pairs of 256 into 4096 rows 9.4 us (three launches, each waiting for the one
-// before it).
+// 371 us (2.25 GB moved: 6.1 TB/s); 1536 pairs of 256 into 4096 rows 9.4 us (three launches,
+// each waiting for the one before it).
 #include "bulk_copy.cuh"
 #include "launch.cuh"
 #include "lookup_common.cuh"
