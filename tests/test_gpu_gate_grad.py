@@ -199,3 +199,28 @@ def test_matches_differences(eg):
             up[which], down[which] = P + h * v, P - h * v
             diff = (loss(up["x"], up["k"], up["a"]) - loss(down["x"], down["k"], down["a"])) / (2 * h)
             assert abs((G * v).sum() - diff) <= slack * np.linalg.norm(G) * np.linalg.norm(v)
+
+
+@pytest.mark.parametrize("dk_dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,D", [(700, 4112), (500, 8192), (1300, 512), (900, 6000)])
+def test_several_tokens_a_block(eg, T, D, dk_dtype):
+    test_matches_the_formula(eg, T, D, dk_dtype)
+
+
+@pytest.mark.parametrize("D", [4096, 4112, 8192])
+def test_dead_bad_and_in_place_wide(eg, D):
+    test_dead_bad_and_in_place(eg, D)
+
+
+def test_wide_dead_tokens_among_many(eg):
+    import torch
+    T, D = 1000, 4224
+    x, k, dy, alpha = make(T, D, seed=4)
+    state = (torch.arange(T) % 3 == 1).to(torch.uint8)
+    live = state == 0
+    dx, dk, da = eg.engram_gate_add_grad(k.cuda(), state.cuda(), x.cuda(), alpha.cuda(), dy.cuda(), eps=EPS)
+    ox, ok, oa = eg.engram_gate_add_grad(k[live].cuda(), None, x[live].cuda(), alpha.cuda(), dy[live].cuda(),
+                                         eps=EPS)
+    assert torch.equal(dx.cpu()[live], ox.cpu()) and torch.equal(dk.cpu()[live], ok.cpu())
+    assert torch.equal(dx.cpu()[~live], dy[~live]) and not dk.cpu()[~live].any()
+    assert torch.allclose(da, oa, rtol=1e-4, atol=1e-3 * float(da.abs().max()))
