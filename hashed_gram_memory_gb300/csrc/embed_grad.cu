@@ -742,8 +742,8 @@ __global__ void __launch_bounds__(kSumThreads) sum_runs_kernel(const __grid_cons
 constexpr int kJoinThreads = 256;
 
 // A block at a time takes a listed run and a slab of columns: each of its groups adds every
-// groups-th part (the keys that end the run are loaded along with the parts), then the first
-// group adds the groups' sums in order.
+// groups-th part (the keys that end the run are loaded along with the parts), then the groups'
+// sums are added up.
 template <typename TG, bool VEC>
 __global__ void __launch_bounds__(kJoinThreads) join_runs_kernel(const __grid_constant__ EmbedGradParams p) {
   constexpr int V = kCols<VEC>;
@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_runs_kernel(const __grid_co
     const int64_t chunk = __ldg(p.long_list + listed);
     const uint32_t key = __ldg(p.keys + (chunk + 2) * C);
     float acc[V] = {};
-    bool more = true;
+    bool more = true, any = false;
     for (int64_t i0 = slot; more; i0 += 4 * groups) {
       uint32_t k[4];
       Slice<float, VEC> s[4];
@@ -775,16 +775,26 @@ __global__ void __launch_bounds__(kJoinThreads) join_runs_kernel(const __grid_co
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         more = more && k[u] == key;
+        any |= more;
         if (more && mine) s[u].add_to(acc);
       }
     }
+    // The groups that had a part are the first ones; their sums meet as a tree.
+    int active = __syncthreads_count(in == 0 && any);
+    int half = 1;
+    while (2 * half < active) half *= 2;
+    for (; active > 1; active = half, half /= 2) {
+      if (slot >= half && slot < active) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) s_part[(slot * G + in) * V + i] = acc[i];
-    __syncthreads();
+        for (int i = 0; i < V; ++i) s_part[(slot * G + in) * V + i] = acc[i];
+      }
+      __syncthreads();
+      if (slot + half < active) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] += s_part[((slot + half) * G + in) * V + i];
+      }
+    }
     if (slot == 0) {
-      for (int g = 1; g < groups; ++g)
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] += s_part[(g * G + in) * V + i];
       const int64_t row = p.run_base ? runs_before(p, chunk + 1) - 1 : key;
       if (mine)
         write_row<TG, VEC>(static_cast<TG *>(p.grad) + row * p.grad_stride + col, acc, G, n, p.scale, p.accumulate);
@@ -821,8 +831,12 @@ Cut cut_of(int64_t n, int D, bool vec) {
   c.chunk = 64;
   const int64_t warps = kSms * 48;
   while (c.chunk > 16 && (n + c.chunk - 1) / c.chunk * c.slabs * c.group / 32 < warps) c.chunk /= 2;
-  // Short lists: shorter chunks still, while their partial sums stay under 2 MB.
-  while (c.chunk > 4 && (n + c.chunk - 1) / c.chunk * c.slabs * c.group / 32 < warps / 8 &&
+  // Short lists: shorter chunks still, while their partial sums stay under 2 MB; narrow rows not
+  // so short, as a warp has many of their chunks and the runs that need joining slow it down
+  // (3861 pairs of 16 columns, 574 rows: 35 us with chunks of 4, 23 with 8; 1024 distinct ones of
+  // 256: 9.1 and 10.4).
+  const int least = c.group < 16 ? 8 : 4;
+  while (c.chunk > least && (n + c.chunk - 1) / c.chunk * c.slabs * c.group / 32 < warps / 8 &&
          (n / (c.chunk / 2) + 1) * 2 * (D + 8) * 4 <= (2 << 20))
     c.chunk /= 2;
   c.chunks = (n + c.chunk - 1) / c.chunk;
