@@ -665,14 +665,21 @@ def _strides(t, name):
     return st
 
 
+def _row_stride(t, name):
+    """Elements between the rows of a two-dimensional tensor.  Under a row's width (broadcast or
+    overlapping rows) the library refuses it; one row alone has no stride, whatever torch says."""
+    stride = _strides(t, name)[0]
+    return stride if t.shape[0] > 1 else max(stride, t.shape[1])
+
+
 def _ids_view(ids):
     """ids [..., R] as (shape, tokens, R, stride between tokens)."""
     import torch
     if ids.dtype != torch.int32 or not ids.is_cuda:
         _need(ids, (torch.int32,), "ids", contiguous=False)
-    shape, st = ids.shape, _strides(ids, "ids")
+    shape = ids.shape
     if len(shape) == 2:
-        return shape, shape[0], shape[1], max(st[0], shape[1])
+        return shape, shape[0], shape[1], _row_stride(ids, "ids")
     if not shape:
         raise EngramError(ERR_INVALID_ARG, "ids must have a dimension")
     if not ids.is_contiguous():
@@ -716,7 +723,7 @@ def engram_embed(ids, table, scale: float = 1.0, pooled: bool = False, out=None,
     od = _dtype(out, "out")
     tok, per = _embed_rows(lead, out, D, pooled, "out")
     _check(lib.engram_embed(ids.data_ptr(), T, R, ids_stride, table.data_ptr(), td, rows, D,
-                            max(_strides(table, "table")[0], D), scale, pooled, out.data_ptr(), od,
+                            _row_stride(table, "table"), scale, pooled, out.data_ptr(), od,
                             tok, per, _ptr(status), _stream(stream)), "engram_embed")
     return out
 
@@ -756,7 +763,7 @@ def engram_embed_grad(ids, dy, rows: int, scale: float = 1.0, pooled: bool = Fal
     if grad.shape != (rows, D):
         raise EngramError(ERR_INVALID_ARG, f"grad must be {[rows, D]}")
     _check(lib.engram_embed_grad(*args, rows, D, scale, accumulate, grad.data_ptr(), gd,
-                                 max(_strides(grad, "grad")[0], D), workspace.data_ptr(),
+                                 _row_stride(grad, "grad"), workspace.data_ptr(),
                                  workspace.numel(), _ptr(status), _stream(stream)),
            "engram_embed_grad")
     return grad
@@ -782,7 +789,7 @@ def engram_embed_grad_rows(ids, dy, rows: int, scale: float = 1.0, pooled: bool 
     if row_ids.numel() != n or grads.shape != (n, D) or count.numel() != 1:
         raise EngramError(ERR_INVALID_ARG, "row_ids / grads / count sizes disagree with ids")
     _check(lib.engram_embed_grad_rows(*args, rows, D, scale, row_ids.data_ptr(), grads.data_ptr(),
-                                      gd, max(_strides(grads, "grads")[0], D), count.data_ptr(),
+                                      gd, _row_stride(grads, "grads"), count.data_ptr(),
                                       workspace.data_ptr(), workspace.numel(), _ptr(status),
                                       _stream(stream)), "engram_embed_grad_rows")
     return row_ids, grads, count
@@ -850,7 +857,7 @@ def engram_fp8_quantise(x, block_rows: int = 1, rows: bool = True, cols: bool = 
         raise EngramError(ERR_INVALID_ARG, "out must hold a value and a scale buffer per copy")
     q = _fp8_copy(out, 0, M, K, block_rows) if rows else (None, 0, None)
     qt = _fp8_copy(out, 2 if rows else 0, K, M, block_rows) if cols else (None, 0, None)
-    _check(lib.engram_fp8_quantise(x.data_ptr(), xd, M, K, max(_strides(x, "x")[0], K), block_rows,
+    _check(lib.engram_fp8_quantise(x.data_ptr(), xd, M, K, _row_stride(x, "x"), block_rows,
                                    *q, *qt, _ptr(status), _stream(stream)), "engram_fp8_quantise")
     return tuple(out)
 
@@ -874,9 +881,8 @@ def engram_fp8_matmul(a, a_scale, b, b_scale, a_block: int = 1, b_block: int = 1
     if out.shape != (M, N):
         raise EngramError(ERR_INVALID_ARG, f"out must be {[M, N]}")
     _check(lib.engram_fp8_matmul(a.data_ptr(), sa, pa, a_block, b.data_ptr(), sb, pb, b_block, M,
-                                 N, K, out.data_ptr(), od,
-                                 max(_strides(out, "out")[0], N), _ptr(status), _stream(stream)),
-           "engram_fp8_matmul")
+                                 N, K, out.data_ptr(), od, _row_stride(out, "out"), _ptr(status),
+                                 _stream(stream)), "engram_fp8_matmul")
     return out
 
 

@@ -551,8 +551,9 @@ ENGRAM_API engram_status engram_pack_e8m0_rows(const uint8_t *table, const uint8
  * An id ENGRAM_ROW_DEAD reads as a row of zeros.  Any other id outside [0, rows)
  * sets ENGRAM_FLAG_BAD_ROW and leaves that output row (the token, when pooled)
  * unwritten.  1 <= D <= ENGRAM_MAX_EMBED_D, n_tokens * n_ids <= 2^31 - 1.  Any
- * strides and element alignment; rows of 8 values on 16-byte boundaries take the
- * vector path.  out must not overlap ids or the table.
+ * element alignment and any strides of a row's width or more (rows that share
+ * elements are refused); rows of 8 values on 16-byte boundaries take the vector
+ * path.  out must not overlap ids or the table.
  */
 ENGRAM_API engram_status engram_embed(const int32_t *ids, int64_t n_tokens, int32_t n_ids,
                                       int64_t ids_stride, const void *table, int32_t table_dtype,
@@ -608,7 +609,7 @@ ENGRAM_API engram_status engram_embed_grad_rows(const int32_t *ids, int64_t n_to
  * for each block, the smallest exponent e >= -127 with max|x| <= 448 * 2^e is stored as
  * the byte e + 127 (OCP E8M0, as the tables' exponents), and x becomes e4m3(x * 2^-e),
  * rounded to nearest even; the only rounding.
- *   x      ENGRAM_DTYPE_* [M, K], x_stride elements between rows (any)
+ *   x      ENGRAM_DTYPE_* [M, K], x_stride elements between rows (any from K on)
  *   q, s   uint8 [M, K], q_stride bytes between rows (a multiple of 16), and
  *          [M, ceil(K/128)]: blocks of 128 along K (the last one may be short); NULL q:
  *          not made
@@ -636,7 +637,7 @@ ENGRAM_API engram_status engram_fp8_quantise(const void *x, int32_t x_dtype, int
  *               [M, ceil(K/128)] (a_block 1) or [ceil(M/128), ceil(K/128)] (a_block
  *               ENGRAM_FP8_BLOCK), rows contiguous
  *   b, b_scale  e4m3fn bytes [N, K], likewise
- *   out         ENGRAM_DTYPE_* [M, N], out_stride elements between rows (any)
+ *   out         ENGRAM_DTYPE_* [M, N], out_stride elements between rows (any from N on)
  * a and b are 16-byte aligned with strides that are multiples of 16; M, N and K are any
  * (values past K in a row are not read as part of it).  A NaN (byte 0x7F or 0xFF, or scale
  * 0xFF) makes the outputs that it is summed into NaN.  A wait that runs out sets
