@@ -128,9 +128,11 @@ __global__ void __launch_bounds__(kRowsThreads) quantise_linear_kernel(const __g
   q[8] = make_uint2(quantise4(hi[0], hi[1], hi[2], hi[3], by), quantise4(hi[4], hi[5], hi[6], hi[7], by));
 }
 
-// Blocks of 128 values numbered along the rows, 16 lanes each, U of them a thread.  `magic`
-// is ceil(2^32 / kblocks): a thread block's local numbers are below kblocks + 16 U, where the
-// multiplication is exact (kblocks < 2^24).
+// Blocks of 128 values numbered along the rows, 16 lanes each, U of them a thread.  A thread
+// block's local numbers x are below kblocks + 16 U.  Short rows take x / kblocks by `magic` =
+// ceil(2^32 / kblocks), exact while x (magic kblocks - 2^32) < x kblocks < 2^32, so far beyond
+// kblocks = 16 U; from there on a thread block meets one row's end at most, and a comparison
+// does for rows of any length.
 template <typename T, bool VEC, int U>
 __global__ void __launch_bounds__(kRowsThreads)
     quantise_rows_kernel(const __grid_constant__ QuantiseParams p, int32_t kblocks, uint32_t magic) {
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(kRowsThreads)
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const uint32_t x = rem0 + u * kPer + slot;
-    const uint32_t q = kblocks == 1 ? x : __umulhi(x, magic);
+    const uint32_t q = kblocks >= kPer * U ? x >= (uint32_t)kblocks : kblocks == 1 ? x : __umulhi(x, magic);
     row[u] = row0 + q;
     kb[u] = (int32_t)(x - q * kblocks);
     if (row[u] < p.M)
