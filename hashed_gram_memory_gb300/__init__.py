@@ -2,7 +2,8 @@
 
 A thin Python binding over libengram.so, whose C ABI is include/engram.h.  The
 functions carry the C names and only marshal arguments: torch tensors become
-device pointers, the current torch CUDA stream becomes the cudaStream_t, and a
+device pointers, the current torch CUDA stream becomes the cudaStream_t (or the one
+that `stream` names, to which what a call allocates then belongs too), and a
 non-zero status becomes an EngramError.  Every step of the path runs in the
 library's CUDA kernels; there is no CPU or PyTorch fallback, and importing this
 package fails if the library has not been built.
@@ -196,6 +197,23 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _made(stream, make, *args, scratch=False, **kw):
+    """make(*args, **kw), a tensor that a call makes for itself, in the pool of the stream that the
+    call launches on: its memory is free for use there at once, and not handed out again before
+    the launch is done with it.  Results (not scratch) also stay while the current stream reads
+    them."""
+    if stream is None or _stream(stream) == _stream(None):
+        return make(*args, **kw)
+    import torch
+    if isinstance(stream, int):  # 0 and 1 name the default stream, which is not an external one
+        stream = torch.cuda.ExternalStream(stream) if stream > 1 else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        t = make(*args, **kw)
+    if not scratch:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def _need(t, dtypes, name, contiguous=True):
     if t is None:
         return
@@ -264,7 +282,8 @@ def engram_pack_e8m0_rows(table, exps, packed=None, stream=None):
     if tuple(exps.shape) != (rows, D // 32):
         raise EngramError(ERR_INVALID_ARG, "exps must be [rows, D/32]")
     if packed is None:
-        packed = torch.empty((rows, e8m0_row_bytes(D)), dtype=torch.uint8, device=table.device)
+        packed = _made(stream, torch.empty, (rows, e8m0_row_bytes(D)), dtype=torch.uint8,
+                       device=table.device)
     _need(packed, (torch.uint8,), "packed")
     _check(lib.engram_pack_e8m0_rows(_ptr(table), _ptr(exps), rows, D, _ptr(packed),
                                      _stream(stream)), "engram_pack_e8m0_rows")
@@ -280,7 +299,7 @@ def engram_compress(token_ids, tid2eid, n_eids: int, eids_out=None, status=None,
     _need(tid2eid, (torch.int32,), "tid2eid")
     _need(dead, (torch.uint8, torch.bool), "dead")
     if eids_out is None:
-        eids_out = torch.empty_like(token_ids)
+        eids_out = _made(stream, torch.empty_like, token_ids)
     _need(eids_out, (torch.int32,), "eids_out")
     _check(lib.engram_compress_masked(_ptr(token_ids), token_ids.numel(), _ptr(tid2eid),
                                       tid2eid.numel(), n_eids, _ptr(dead), _ptr(eids_out),
@@ -313,7 +332,8 @@ def engram_hash(eids, n_heads: int, rows, history=None, history_out=None, row_id
         raise EngramError(ERR_INVALID_ARG, "eids must be [batch, seq]")
     B, S = eids.shape
     if row_ids_out is None:
-        row_ids_out = torch.empty((B, S, 3, n_heads), dtype=torch.int32, device=eids.device)
+        row_ids_out = _made(stream, torch.empty, (B, S, 3, n_heads), dtype=torch.int32,
+                            device=eids.device)
     _need(row_ids_out, (torch.int32,), "row_ids_out")
     _need(history, (torch.int32,), "history")
     _need(history_out, (torch.int32,), "history_out")
@@ -345,7 +365,8 @@ def engram_compress_hash(token_ids, tid2eid, n_eids: int, n_heads: int, rows, hi
         raise EngramError(ERR_INVALID_ARG, "token_ids must be [batch, seq]")
     B, S = token_ids.shape
     if row_ids_out is None:
-        row_ids_out = torch.empty((B, S, 3, n_heads), dtype=torch.int32, device=token_ids.device)
+        row_ids_out = _made(stream, torch.empty, (B, S, 3, n_heads), dtype=torch.int32,
+                            device=token_ids.device)
     _need(row_ids_out, (torch.int32,), "row_ids_out")
     _need(eids_out, (torch.int32,), "eids_out")
     _need(history, (torch.int32,), "history")
@@ -375,7 +396,7 @@ def engram_lookup_fused(row_ids, n_heads: int, tables: Tables, streams_in, alpha
     if row_ids.numel() != T * 3 * n_heads:
         raise EngramError(ERR_INVALID_ARG, "row_ids and streams disagree on the token count")
     if streams_out is None:
-        streams_out = torch.empty_like(streams_in)
+        streams_out = _made(stream, torch.empty_like, streams_in)
     _need(streams_out, bf, "streams_out")
     _need(gate_out, (torch.float32,), "gate_out")
     _need(mem_out, (torch.float32,), "mem_out")
@@ -411,13 +432,14 @@ def engram_connection(row_ids, n_heads: int, tables: Tables, wkv, streams_in, al
     if tuple(wkv.shape) != (D, 3 * n_heads * tables.D):
         raise EngramError(ERR_INVALID_ARG, f"wkv must be [{D}, {3 * n_heads * tables.D}]")
     if streams_out is None:
-        streams_out = torch.empty_like(streams_in)
+        streams_out = _made(stream, torch.empty_like, streams_in)
     _need(streams_out, bf, "streams_out")
     _need(gate_out, (torch.float32,), "gate_out")
     _need(k_out, (torch.float32,), "k_out")
     need = engram_connection_workspace_bytes(T, n_heads, tables.D, D)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=streams_in.device)
+        workspace = _made(stream, torch.empty, max(need, 1), dtype=torch.uint8,
+                          device=streams_in.device, scratch=True)
     s = tables.struct()
     _check(lib.engram_connection(_ptr(row_ids), T, n_heads, C.byref(s), _ptr(wkv), D,
                                  _ptr(streams_in), _ptr(streams_out), _ptr(alpha), float(eps),
@@ -437,9 +459,9 @@ def engram_concat_rows(row_ids, n_heads: int, tables: Tables, e_out=None, state_
     K = 3 * n_heads * tables.D
     dev = row_ids.device
     if e_out is None:
-        e_out = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
+        e_out = _made(stream, torch.empty, (T, K), dtype=torch.bfloat16, device=dev)
     if state_out is None:
-        state_out = torch.empty((T,), dtype=torch.uint8, device=dev)
+        state_out = _made(stream, torch.empty, (T,), dtype=torch.uint8, device=dev)
     _need(e_out, (torch.bfloat16, torch.int16), "e_out")
     _need(state_out, (torch.uint8,), "state_out")
     if e_out.numel() != T * K or state_out.numel() != T:
@@ -462,7 +484,7 @@ def engram_wkv_project(e, wkv, k_out=None, status=None, stream=None):
     if wkv.shape[1] != K:
         raise EngramError(ERR_INVALID_ARG, "e and wkv disagree on K")
     if k_out is None:
-        k_out = torch.empty((T, D), dtype=torch.float32, device=e.device)
+        k_out = _made(stream, torch.empty, (T, D), dtype=torch.float32, device=e.device)
     _need(k_out, (torch.float32,), "k_out")
     if k_out.numel() != T * D:
         raise EngramError(ERR_INVALID_ARG, "k_out must be [T, D]")
@@ -485,7 +507,7 @@ def engram_gate_add(k, state, streams_in, alpha, eps: float = 1e-6, streams_out=
     if k.numel() != T * D or state.numel() != T:
         raise EngramError(ERR_INVALID_ARG, "k / state sizes disagree with the streams")
     if streams_out is None:
-        streams_out = torch.empty_like(streams_in)
+        streams_out = _made(stream, torch.empty_like, streams_in)
     _need(streams_out, bf, "streams_out")
     _need(gate_out, (torch.float32,), "gate_out")
     _check(lib.engram_gate_add(_ptr(k), _ptr(state), T, D, _ptr(streams_in), _ptr(streams_out),
@@ -551,10 +573,11 @@ def engram_forward(token_ids, tid2eid, n_eids: int, n_heads: int, tables: Tables
     _need(token_ids, (torch.int32,), "token_ids")
     B, S = token_ids.shape
     if streams_out is None:
-        streams_out = torch.empty_like(streams_in)
+        streams_out = _made(stream, torch.empty_like, streams_in)
     need = engram_forward_workspace_bytes(B, S, n_heads)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=token_ids.device)
+        workspace = _made(stream, torch.empty, max(need, 16), dtype=torch.uint8,
+                          device=token_ids.device, scratch=True)
     s = tables.struct()
     lay = _layout(positions, dead, primes, host=False)
     _check(lib.engram_forward(_ptr(token_ids), B, S, _ptr(tid2eid), tid2eid.numel(), n_eids,
@@ -631,7 +654,7 @@ def engram_forward_static(token_ids, tid2eid, n_eids: int, n_heads: int, tables:
     _need(token_ids, (torch.int32,), "token_ids")
     B, S = token_ids.shape
     if streams_out is None:
-        streams_out = torch.empty_like(streams_in)
+        streams_out = _made(stream, torch.empty_like, streams_in)
     s = tables.struct()
     lay = _layout(positions, dead, primes, host=False)
     _check(lib.engram_forward_static(_ptr(token_ids), B, S, _ptr(tid2eid), tid2eid.numel(), n_eids,
@@ -718,8 +741,8 @@ def engram_embed(ids, table, scale: float = 1.0, pooled: bool = False, out=None,
     rows, D = table.shape
     if out is None:
         import torch
-        out = torch.empty((*(lead[:-1] if pooled else lead), D), dtype=out_dtype or table.dtype,
-                          device=table.device)
+        out = _made(stream, torch.empty, (*(lead[:-1] if pooled else lead), D),
+                    dtype=out_dtype or table.dtype, device=table.device)
     od = _dtype(out, "out")
     tok, per = _embed_rows(lead, out, D, pooled, "out")
     _check(lib.engram_embed(ids.data_ptr(), T, R, ids_stride, table.data_ptr(), td, rows, D,
@@ -732,7 +755,7 @@ def engram_embed_grad_workspace_bytes(n_tokens: int, n_ids: int, D: int) -> int:
     return int(lib.engram_embed_grad_workspace_bytes(n_tokens, n_ids, D))
 
 
-def _grad_args(ids, dy, pooled, workspace):
+def _grad_args(ids, dy, pooled, workspace, stream):
     """The arguments the two gradient calls share, from ids and dy ([*ids.shape, D], or
     [*ids.shape[:-1], D] when pooled; expanded dimensions may have stride 0)."""
     dd = _dtype(dy, "dy")
@@ -743,8 +766,8 @@ def _grad_args(ids, dy, pooled, workspace):
     tok, per = _embed_rows(lead, dy, D, pooled, "dy")
     if workspace is None:
         import torch
-        workspace = torch.empty(max(engram_embed_grad_workspace_bytes(T, R, D), 16),
-                                dtype=torch.uint8, device=dy.device)
+        workspace = _made(stream, torch.empty, max(engram_embed_grad_workspace_bytes(T, R, D), 16),
+                          dtype=torch.uint8, device=dy.device, scratch=True)
     return D, T * R, (ids.data_ptr(), T, R, ids_stride, dy.data_ptr(), dd, tok, per), workspace
 
 
@@ -753,12 +776,13 @@ def engram_embed_grad(ids, dy, rows: int, scale: float = 1.0, pooled: bool = Fal
                       stream=None):
     """The gradient of engram_embed(ids, table [rows, D], scale, pooled)'s table for the output
     gradient dy: [rows, D], every row written (accumulate: added to grad, fp32 or bf16)."""
-    D, n, args, workspace = _grad_args(ids, dy, pooled, workspace)
+    D, n, args, workspace = _grad_args(ids, dy, pooled, workspace, stream)
     if grad is None:
         if accumulate:
             raise EngramError(ERR_INVALID_ARG, "accumulate needs a grad to add to")
         import torch
-        grad = torch.empty((rows, D), dtype=grad_dtype or torch.float32, device=dy.device)
+        grad = _made(stream, torch.empty, (rows, D), dtype=grad_dtype or torch.float32,
+                     device=dy.device)
     gd = _dtype(grad, "grad")
     if grad.shape != (rows, D):
         raise EngramError(ERR_INVALID_ARG, f"grad must be {[rows, D]}")
@@ -776,13 +800,14 @@ def engram_embed_grad_rows(ids, dy, rows: int, scale: float = 1.0, pooled: bool 
     for n = ids.numel(): the ascending distinct ids and then -1, their gradients (the rows past
     count are not written), and their number."""
     import torch
-    D, n, args, workspace = _grad_args(ids, dy, pooled, workspace)
+    D, n, args, workspace = _grad_args(ids, dy, pooled, workspace, stream)
     if row_ids is None:
-        row_ids = torch.empty(n, dtype=torch.int32, device=dy.device)
+        row_ids = _made(stream, torch.empty, n, dtype=torch.int32, device=dy.device)
     if grads is None:
-        grads = torch.empty((n, D), dtype=grad_dtype or torch.float32, device=dy.device)
+        grads = _made(stream, torch.empty, (n, D), dtype=grad_dtype or torch.float32,
+                      device=dy.device)
     if count is None:
-        count = torch.empty(1, dtype=torch.int32, device=dy.device)
+        count = _made(stream, torch.empty, 1, dtype=torch.int32, device=dy.device)
     _need(row_ids, (torch.int32,), "row_ids")
     _need(count, (torch.int32,), "count")
     gd = _dtype(grads, "grads")
@@ -850,9 +875,9 @@ def engram_fp8_quantise(x, block_rows: int = 1, rows: bool = True, cols: bool = 
         import torch
         out = []
         for r, c in ([(M, K)] if rows else []) + ([(K, M)] if cols else []):
-            out += [fp8_empty(r, c, x.device),
-                    torch.empty((-(-r // block_rows), -(-c // FP8_BLOCK)), dtype=torch.uint8,
-                                device=x.device)]
+            out += [_made(stream, fp8_empty, r, c, x.device),
+                    _made(stream, torch.empty, (-(-r // block_rows), -(-c // FP8_BLOCK)),
+                          dtype=torch.uint8, device=x.device)]
     if len(out) != 2 * (bool(rows) + bool(cols)):
         raise EngramError(ERR_INVALID_ARG, "out must hold a value and a scale buffer per copy")
     q = _fp8_copy(out, 0, M, K, block_rows) if rows else (None, 0, None)
@@ -876,7 +901,8 @@ def engram_fp8_matmul(a, a_scale, b, b_scale, a_block: int = 1, b_block: int = 1
     pb = _fp8_scales(b_scale, N, K, b_block, "b_scale")
     if out is None:
         import torch
-        out = torch.empty((M, N), dtype=out_dtype or torch.float32, device=a.device)
+        out = _made(stream, torch.empty, (M, N), dtype=out_dtype or torch.float32,
+                    device=a.device)
     od = _dtype(out, "out")
     if out.shape != (M, N):
         raise EngramError(ERR_INVALID_ARG, f"out must be {[M, N]}")
@@ -909,19 +935,20 @@ def engram_gate_add_grad(k, state, streams_in, alpha, dy, eps: float = 1e-6, dx=
     if k.numel() != T * D or (state is not None and state.numel() != T) or alpha.numel() != 4:
         raise EngramError(ERR_INVALID_ARG, "k / state / alpha sizes disagree with the streams")
     if dx is None:
-        dx = torch.empty_like(dy)
+        dx = _made(stream, torch.empty_like, dy)
     if dk is None:
-        dk = torch.empty(k.shape, dtype=dk_dtype or torch.float32, device=k.device)
+        dk = _made(stream, torch.empty, k.shape, dtype=dk_dtype or torch.float32,
+                   device=k.device)
     if dalpha is None:
-        dalpha = torch.empty(4, dtype=torch.float32, device=k.device)
+        dalpha = _made(stream, torch.empty, 4, dtype=torch.float32, device=k.device)
     _need(dx, bf, "dx")
     _need(dk, (torch.float32, *bf), "dk")
     _need(dalpha, (torch.float32,), "dalpha")
     if dx.numel() != dy.numel() or dk.numel() != k.numel() or dalpha.numel() != 4:
         raise EngramError(ERR_INVALID_ARG, "dx / dk / dalpha sizes")
     if workspace is None:
-        workspace = torch.empty(engram_gate_add_grad_workspace_bytes(), dtype=torch.uint8,
-                                device=k.device)
+        workspace = _made(stream, torch.empty, engram_gate_add_grad_workspace_bytes(),
+                          dtype=torch.uint8, device=k.device, scratch=True)
     _check(lib.engram_gate_add_grad(_ptr(k), _ptr(state), T, D, _ptr(streams_in), _ptr(alpha),
                                     float(eps), _ptr(dy), _ptr(dx), _ptr(dk), _dtype(dk, "dk"),
                                     _ptr(dalpha), _ptr(workspace), workspace.numel(), _stream(stream)), "engram_gate_add_grad")
