@@ -768,6 +768,7 @@ def _grad_args(ids, dy, pooled, workspace, stream):
         import torch
         workspace = _made(stream, torch.empty, max(engram_embed_grad_workspace_bytes(T, R, D), 16),
                           dtype=torch.uint8, device=dy.device, scratch=True)
+    _need(workspace, (workspace.dtype,), "workspace")
     return D, T * R, (ids.data_ptr(), T, R, ids_stride, dy.data_ptr(), dd, tok, per), workspace
 
 
@@ -949,7 +950,9 @@ def engram_gate_add_grad(k, state, streams_in, alpha, dy, eps: float = 1e-6, dx=
     if workspace is None:
         workspace = _made(stream, torch.empty, engram_gate_add_grad_workspace_bytes(),
                           dtype=torch.uint8, device=k.device, scratch=True)
+    _need(workspace, (workspace.dtype,), "workspace")
     _check(lib.engram_gate_add_grad(_ptr(k), _ptr(state), T, D, _ptr(streams_in), _ptr(alpha),
                                     float(eps), _ptr(dy), _ptr(dx), _ptr(dk), _dtype(dk, "dk"),
-                                    _ptr(dalpha), _ptr(workspace), workspace.numel(), _stream(stream)), "engram_gate_add_grad")
+                                    _ptr(dalpha), _ptr(workspace), workspace.numel(),
+                                    _stream(stream)), "engram_gate_add_grad")
     return dx, dk, dalpha

@@ -119,3 +119,27 @@ def test_strides_of_rows_go_through(eg, recorder):
         assert recorder.calls.pop()[1][13] == stride
     eg.engram_embed_grad(ids(5), zeros(5, 8), 9, grad=zeros(9, 12)[:, :8], workspace=workspace(eg, 5, 1, 8), stream=1)
     assert recorder.calls.pop()[1][14] == 12
+
+
+# Scratch that is not a run of device bytes: host memory, and views that hold less than they say.
+SCRATCH = {"host memory": lambda n: torch.zeros(n, dtype=torch.uint8), "a broadcast byte": lambda n: u8(1).expand(n),
+           "every other byte": lambda n: u8(2 * n)[::2]}
+
+
+@pytest.mark.parametrize("kind", SCRATCH)
+def test_scratch_must_be_device_memory_in_one_piece(eg, recorder, kind):
+    def scratch(n):
+        return SCRATCH[kind](n)
+    n = eg.engram_embed_grad_workspace_bytes(5, 1, 8)
+    for call in (lambda: eg.engram_embed_grad(ids(5), zeros(5, 8), 9, grad=zeros(9, 8), workspace=scratch(n), stream=1),
+                 lambda: eg.engram_embed_grad_rows(ids(5), zeros(5, 8), 9, row_ids=ids(5), grads=zeros(5, 8),
+                                                   count=ids(1), workspace=scratch(n), stream=1),
+                 lambda: eg.engram_gate_add_grad(zeros(3, 16), None, zeros(3, 4, 16, dtype=torch.bfloat16), zeros(4),
+                                                 zeros(3, 4, 16, dtype=torch.bfloat16),
+                                                 dx=zeros(3, 4, 16, dtype=torch.bfloat16), dk=zeros(3, 16),
+                                                 dalpha=zeros(4), stream=1,
+                                                 workspace=scratch(eg.engram_gate_add_grad_workspace_bytes()))):
+        with pytest.raises(eg.EngramError) as e:
+            call()
+        assert e.value.code == eg.ERR_INVALID_ARG and "workspace" in str(e.value)
+    assert recorder.calls == []
