@@ -223,6 +223,7 @@ struct Drain {
 #pragma unroll 1
       for (int c = 0; c < CHUNKS; ++c) {
         uint32_t v[16];
+        __syncwarp();  // together again after the stores, as tcgen05.ld wants the warp
         if (c < chunks) tmem_ld16(taddr + c * 16, v);
         if (c == chunks - 1) release();
 #pragma unroll
@@ -242,12 +243,12 @@ struct Drain {
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
         uint32_t v[16];
+        __syncwarp();  // as above
         tmem_ld16(taddr + c * 16, v);
         if (c == chunks - 1) release();
-        if (!mine) continue;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          if (c * 16 + i < rows) store_out(out, v[i]);
+          if (mine && c * 16 + i < rows) store_out(out, v[i]);
           out += stride;
         }
       }
