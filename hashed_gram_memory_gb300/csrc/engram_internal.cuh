@@ -136,7 +136,7 @@ engram_status prepare_lookup(const char *fn, const int32_t *row_ids, bool need_r
                              LookupParams &p);
 int lookup_kernel_choice();
 // The test hook of engram_debug_withhold_copies: true (and one launch fewer left)
-// while launches are to withhold a row copy.
+// while launches are to withhold a copy.
 bool take_withheld_launch();
 // engram_forward runs this call as the fused decode launch (no workspace used).
 bool forward_is_decode_step(int32_t batch, int32_t seq, int32_t n_heads,

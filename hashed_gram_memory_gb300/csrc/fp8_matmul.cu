@@ -81,6 +81,7 @@ struct MatmulDev {
   int32_t splits;                // CTAs that share a tile's K (a cluster)
   int64_t tiles_p, tiles_q, tiles;
   int64_t wait_limit_ns;
+  bool withhold;  // test hook: the first stage waits for bytes that never come
 };
 
 // Shared-memory descriptor of the scale words: 32 rows of 16 bytes, no swizzle, 8-row
@@ -109,6 +110,12 @@ __device__ __forceinline__ void umma_fp8(uint32_t d, uint64_t p_desc, uint64_t q
       "[%5], p;\n\t}" ::"r"(d),
       "l"(p_desc), "l"(q_desc), "r"(idesc), "r"(sp), "r"(sq), "r"(accumulate)
       : "memory");
+}
+
+// Bytes that the current phase of a barrier waits for, without an arrival.
+__device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
+               : "memory");
 }
 
 __device__ __forceinline__ uint32_t load_cluster(uint32_t addr) {
@@ -299,6 +306,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1)
       mbar_init(acc_empty + a, 4);
     }
     mbar_init(mma_done, 1);
+    if (p.withhold) mbar_expect_tx(full, 16);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -586,6 +594,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_init(acc_empty + a, 2 * 4 * kPairParts);
     }
     mbar_init(mma_done, 1);
+    if (p.withhold) mbar_expect_tx(full, 16);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -872,6 +881,7 @@ cudaError_t launch_fp8_matmul(const MatmulParams &p, int out_dtype, cudaStream_t
   d.a_shift = p.a_block == 1 ? 0 : 7;
   d.b_shift = p.b_block == 1 ? 0 : 7;
   d.wait_limit_ns = wait_limit_ns();
+  d.withhold = take_withheld_launch();
   const int64_t segments = ceil_div(d.kblocks, kSegmentBlocks);
   d.seg_blocks = (int32_t)(ceil_div(ceil_div(d.kblocks, segments), 4) * 4);
   d.segments = (int32_t)ceil_div(d.kblocks, d.seg_blocks);

@@ -360,7 +360,12 @@ __global__ void __launch_bounds__(256, 2)
     mbar_arrive_expect_tx(&s_full, 128 * kRow);
     tma_load_2d(s_tile, &map, k * 128, m * 128, &s_full);
   };
-  if (tid == 0 && (int32_t)blockIdx.x < tiles) issue(mb, kb);
+  if (tid == 0 && (int32_t)blockIdx.x < tiles) {
+    if (p.withhold)
+      mbar_arrive_expect_tx(&s_full, 128 * kRow);
+    else
+      issue(mb, kb);
+  }
   uint32_t phase = 0;
   for (int32_t tile = blockIdx.x; tile < tiles; phase ^= 1) {
     const bool late = !drain_phase(&s_full, phase, p.wait_limit_ns);
@@ -449,8 +454,9 @@ cudaError_t launch_typed(const QuantiseParams &p, cudaStream_t stream) {
     q.x_stride = stride;
     CUtensorMap map;
     if (!make_map<T>(&map, q)) return cudaErrorInvalidValue;
+    q.withhold = take_withheld_launch();
     const int64_t grid = tiles < 2 * kSms ? tiles : 2 * kSms;
-    return launch(quantise_tma_kernel<T>, grid, 256, kTileBytes, stream, 1, map, p, (int32_t)kblocks,
+    return launch(quantise_tma_kernel<T>, grid, 256, kTileBytes, stream, 1, map, q, (int32_t)kblocks,
                   (int32_t)mblocks);
   }
 }

@@ -97,6 +97,7 @@ struct QuantiseParams {
   int64_t wait_limit_ns;
   int64_t M, K, x_stride, q_stride, qt_stride;
   int32_t block_rows;  // 1 or ENGRAM_FP8_BLOCK
+  bool withhold;       // test hook, set by the launcher: a block's first copy is never issued
 };
 cudaError_t launch_quantise(const QuantiseParams &p, int dtype, cudaStream_t stream);
 

@@ -741,7 +741,9 @@ ENGRAM_API int64_t engram_set_wait_limit_ns(int64_t ns);
  * lookup kernels or of the fused decode step (engram_forward with seq = 1)
  * withhold one row copy in every block (the mbarrier still expects its bytes),
  * so the block's bounded wait runs out, the block skips its token or slot, and
- * the launch reports ENGRAM_FLAG_TIMEOUT.  For tests only; 0 turns it off.
+ * the launch reports ENGRAM_FLAG_TIMEOUT.  Launches of engram_fp8_matmul and of
+ * engram_fp8_quantise's tiles count too: the mbarrier of each block's first tile
+ * waits for bytes that never come.  For tests only; 0 turns it off.
  */
 ENGRAM_API void engram_debug_withhold_copies(int32_t launches);
 

@@ -28,10 +28,11 @@ def operand(eg, rows, K, seed):
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("N", [1, 31, 33, 63, 97, 127, 129, 255, 257, 300])
-@pytest.mark.parametrize("M,K", [(5, 200), (130, 640),        # single CTAs
-                                 (16, 2048),                   # K shared by a cluster
-                                 (9000, 512),                  # CTA pairs
-                                 (700, 8320), (5000, 8320)])   # several accumulators
+@pytest.mark.parametrize("M,K", [(5, 200), (130, 640), (9000, 512),  # single CTAs
+                                 (5000, 8320),                        # with several accumulators
+                                 (16, 2048), (700, 8320),             # K shared by a cluster
+                                 (20000, 4096),                       # CTA pairs, from 129 columns on
+                                 (20000, 8320)])                      # with several accumulators
 def test_columns_past_the_last(eg, M, N, K, out):
     import torch
     a, sa, av = operand(eg, M, K, M)
