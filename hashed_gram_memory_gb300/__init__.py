@@ -4,9 +4,9 @@ A thin Python binding over libengram.so, whose C ABI is include/engram.h.  The
 functions carry the C names and only marshal arguments: torch tensors become
 device pointers, the current torch CUDA stream becomes the cudaStream_t (or the one
 that `stream` names, to which what a call allocates then belongs too), and a
-non-zero status becomes an EngramError.  Every step of the path runs in the
-library's CUDA kernels; there is no CPU or PyTorch fallback, and importing this
-package fails if the library has not been built.
+non-zero status becomes an EngramError.  No call builds an autograd graph.  Every
+step of the path runs in the library's CUDA kernels; there is no CPU or PyTorch
+fallback, and importing this package fails if the library has not been built.
 """
 from __future__ import annotations
 

@@ -11,7 +11,8 @@
 //     fewer rows a warp and a column a lane;
 //   flat kernel (few rows, other widths): a thread an output chunk (one row of 4096: 1.4 us);
 //   pooled outputs (flat): a thread loops over the token's ids in order, four rows in
-//     flight, in fp32.
+//     flight, in fp32 (65,536 x 24 ids of 256 bf16: 133 us, its bytes take 115 at the copy
+//     bandwidth; 4096 x 6 of 256: 3.4 of 2.2; 20,000 x 6 of 475, a column a thread: 84 of 13).
 #include "launch.cuh"
 #include "lookup_common.cuh"
 #include "train_internal.cuh"

@@ -565,8 +565,9 @@ ENGRAM_API engram_status engram_embed(const int32_t *ids, int64_t n_tokens, int3
 /*
  * engram_embed_grad -- the gradient of engram_embed's table, every row written:
  *   grad[v] = scale * sum over (t, j) with ids[t, j] = v of dy[t, j]
- * added up in fp32 in ascending (t, j), rounded once; accumulate != 0 adds to grad
- * instead (rows that no id names stay as they are).
+ * added up in fp32 in an order that the ids fix (ascending (t, j); the terms of a
+ * frequent id in parts, each ascending, whose sums are added), rounded once; accumulate
+ * != 0 adds to grad instead (rows that no id names stay as they are).
  *   ids, n_tokens, n_ids, ids_stride, rows, D, scale as engram_embed
  *   dy    ENGRAM_DTYPE_*; row (t, j) starts at t*dy_token_stride + j*dy_id_stride
  *         elements.  dy_id_stride 0 is the gradient of a pooled lookup: every id of a

@@ -1,5 +1,6 @@
-"""The training example: its gradients against torch's in fp32 on the same quantised operands,
-and its loss, which has to fall."""
+"""The training example as a whole: its gradients against torch's in fp32 on the same chain
+without quantisation, loosely, and its loss, which has to fall.  Each link on its own operands
+is in test_gpu_train_connection_operands.py."""
 import importlib.util
 import os
 
@@ -22,10 +23,12 @@ def example():
 
 
 def test_gradients_follow_the_unquantised_chain(example):
-    """Every e4m3 value is within 2^-4 of what it stands for (3 stored bits, to nearest), so each
-    product of two such factors is within 2^-3 + 2^-8 of the plain one, term by term, and over
-    many terms of either sign the errors average out: the norm of a gradient's error stays well
-    inside 2^-3 of its own norm, and its direction within a cosine of 0.99."""
+    """An e4m3 value is within 2^-4 of what it stands for (3 stored bits, to nearest) while that is
+    at least 2^-13 of the block's largest magnitude, and within 2^-17 of that magnitude below
+    (e4m3's subnormals), so each product of two such factors is about within 2^-3 + 2^-8 of
+    the plain one, term by term, and over many terms of either sign the errors average out: the
+    norm of a gradient's error stays well inside 2^-3 of its own norm, and its direction within a
+    cosine of 0.99."""
     import torch
     net = example.Connection(seed=3)
     T = 700
