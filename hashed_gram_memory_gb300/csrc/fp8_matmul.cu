@@ -24,13 +24,13 @@
 //     work), 4 or 8 CTAs of a cluster share a tile, each with a part of K, and add their
 //     parts through distributed shared memory in rank order; two such CTAs an SM, whose
 //     stages together have most of a decode step's weights on the way at once.
-// Measured: 65,536 x 4096 x 6144 893 to 937 us by the box (3.5 to 3.7 PFLOP/s; bound by the
+// Measured: 65,536 x 4096 x 6144 893 to 937 us by the card (3.5 to 3.7 PFLOP/s; bound by the
 // tensor cores, and in a long loop by the power limit: 1100 us near 1.6 GHz); 4096 x 6144 x
 // 16,411 with rows 16,416 bytes apart 262 to 277 us (3.0 to 3.2 PFLOP/s; every 128-byte slice of
 // a row straddles two lines); few tiles and a long K leave SMs idle: 151 x 5888 x 11,776 27 us
-// (its bytes take 11; 92 CTAs walk all of K, as 4 to a tile would not all be resident, and M =
-// 151 makes two tiles of 128 rows), 379 x 2944 x 15,104 25 us (its products take 8.6; 276 CTAs,
-// 4 to a tile);
+// (its bytes take 11; 46 CTA pairs walk all of K, with 144 and 7 rows of a to a tile, as 4 CTAs
+// to a tile would not all be resident), 379 x 2944 x 15,104 25 us (its products take 8.6; 276
+// CTAs, 4 to a tile);
 // 16 x 4096 x 6144 8.9 us (25 MB of weights, 3.8 us at the copy bandwidth; the rest is the
 // launch, the first bytes' latency and the join).
 // Warps:
