@@ -27,6 +27,7 @@ MAX_HEADS, MAX_D = 32, 4096
 DTYPE_BF16, DTYPE_F32 = 0, 1
 MAX_EMBED_D = 16384
 FP8_BLOCK = 128
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU = range(4)
 
 
 class EngramError(RuntimeError):
@@ -169,6 +170,22 @@ def _load():
     L.engram_gate_add_grad.argtypes = [vp, vp, i64, i32, vp, vp, C.c_float, vp, vp, vp, i32, vp,
                                        vp, sz, vp]
     L.engram_gate_add_grad.restype = i32
+    f32, operands = C.c_float, [vp, i64, i32, vp, i64, i32, i64, i64, i64]
+    L.engram_matmul_workspace_bytes.argtypes = operands
+    L.engram_matmul_workspace_bytes.restype = sz
+    L.engram_matmul.argtypes = operands + [f32, vp, i32, i32, vp, i32, i64, vp, i32, i64, vp, i32,
+                                           i64, vp, sz, vp, vp]
+    L.engram_matmul.restype = i32
+    L.engram_matmul_grad_workspace_bytes.argtypes = [vp, i32, i64] + operands + [i32, i32, i32, i32]
+    L.engram_matmul_grad_workspace_bytes.restype = sz
+    L.engram_matmul_grad.argtypes = [vp, i32, i64] + operands + [
+        f32, vp, i32, i64, i32, i32, vp, i32, i64, vp, i32, i64, vp, vp, sz, vp, vp]
+    L.engram_matmul_grad.restype = i32
+    L.engram_orthogonalise_workspace_bytes.argtypes = [i64, i64, i64]
+    L.engram_orthogonalise_workspace_bytes.restype = sz
+    L.engram_orthogonalise.argtypes = [vp, i32, i64, i64, i64, i64, i64, vp, i64, i64, f32, i32, i32,
+                                       f32, f32, f32, f32, f32, vp, i64, i64, vp, sz, vp, vp]
+    L.engram_orthogonalise.restype = i32
     return L
 
 
@@ -956,3 +973,188 @@ def engram_gate_add_grad(k, state, streams_in, alpha, dy, eps: float = 1e-6, dx=
                                     _ptr(dalpha), _ptr(workspace), workspace.numel(),
                                     _stream(stream)), "engram_gate_add_grad")
     return dx, dk, dalpha
+
+
+def _bf16_operand(t, name):
+    """(rows, columns, pointer, stride, transposed) of a bf16 matrix of which either dimension
+    is dense."""
+    if _dtype(t, name) != DTYPE_BF16:
+        import torch
+        _need(t, (torch.bfloat16, torch.int16), name, contiguous=False)
+    if t.dim() != 2:
+        raise EngramError(ERR_INVALID_ARG, f"{name} must be two-dimensional")
+    rows, cols = t.shape
+    st = t.stride()
+    if st[1] == 1 or cols == 1:
+        return rows, cols, t.data_ptr(), st[0] if rows > 1 else cols, 0
+    if st[0] == 1 or rows == 1:
+        return rows, cols, t.data_ptr(), st[1], 1
+    raise EngramError(ERR_INVALID_ARG, f"a dimension of {name} must be contiguous")
+
+
+def _plane(t, shape, name):
+    """(pointer, dtype, row stride) of a bf16 or fp32 [M, N] tensor, (None, 0, 0) for none."""
+    if t is None:
+        return None, 0, 0
+    code = _dtype(t, name)
+    if t.shape != shape:
+        raise EngramError(ERR_INVALID_ARG, f"{name} must be {list(shape)}")
+    return t.data_ptr(), code, _strides(t, name)[0]
+
+
+def _one_device(stream, first, *others):
+    """Every tensor of a call is on one device: the current one, where no stream says another."""
+    dev = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise EngramError(ERR_INVALID_ARG, "the tensors of a call must be on one device")
+    if stream is None:
+        import torch
+        if dev != torch._C._cuda_getDevice():
+            raise EngramError(ERR_INVALID_ARG, "the tensors must be on the current device")
+
+
+def _activation(activation):
+    if activation not in (ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU):
+        raise EngramError(ERR_INVALID_ARG, f"unknown activation {activation}")
+    return activation
+
+
+def _scratch(workspace, need, like, stream):
+    """(pointer, bytes) of the caller's workspace, or of one that the call makes, and its tensor."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        import torch
+        workspace = _made(stream, torch.empty, need, dtype=torch.uint8, device=like.device,
+                          scratch=True)
+    _need(workspace, (workspace.dtype,), "workspace")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def engram_matmul_workspace_bytes(a, b) -> int:
+    """0 unless the rows of a or b are off 16-byte boundaries."""
+    M, K, *a = _bf16_operand(a, "a")
+    N, _, *b = _bf16_operand(b, "b")
+    return int(lib.engram_matmul_workspace_bytes(*a, *b, M, N, K))
+
+
+def engram_matmul(a, b, bias=None, activation: int = ACT_NONE, residual=None, scale: float = 1.0,
+                  pre=None, out=None, out_dtype=None, workspace=None, status=None, stream=None):
+    """out[m, n] = act(z) + residual[m, n] with z = scale * sum_k a[m, k] b[n, k] + bias[n]: a bf16
+    [M, K] and b bf16 [N, K], each row-major or a transposed view.  bias [N], residual [M, N] (it
+    may be out itself) and out (fp32 by default) are bf16 or fp32; pre, a [M, N] buffer, receives z
+    for engram_matmul_grad."""
+    M, K, *pa = _bf16_operand(a, "a")
+    N, kb, *pb = _bf16_operand(b, "b")
+    if kb != K:
+        raise EngramError(ERR_INVALID_ARG, "a and b disagree on K")
+    shape = (M, N)
+    if out is None:
+        import torch
+        out = _made(stream, torch.empty, shape, dtype=out_dtype or torch.float32, device=a.device)
+    bias_ptr, bias_dtype = None, 0
+    if bias is not None:
+        bias_ptr, bias_dtype = bias.data_ptr(), _dtype(bias, "bias")
+        if bias.shape != (N,) or not bias.is_contiguous():
+            raise EngramError(ERR_INVALID_ARG, f"bias must be contiguous {[N]}")
+    _one_device(stream, a, b, out, bias, residual, pre, workspace, status)
+    ws, ws_bytes, workspace = _scratch(
+        workspace, lib.engram_matmul_workspace_bytes(*pa, *pb, M, N, K), a, stream)
+    _check(lib.engram_matmul(*pa, *pb, M, N, K, scale, bias_ptr, bias_dtype, _activation(activation),
+                             *_plane(residual, shape, "residual"), *_plane(pre, shape, "pre"),
+                             *_plane(out, shape, "out"), ws, ws_bytes, _ptr(status),
+                             _stream(stream)), "engram_matmul")
+    return out
+
+
+def engram_matmul_grad(dy, a, b, pre=None, activation: int = ACT_NONE, scale: float = 1.0,
+                       grad_a: bool = True, grad_b: bool = True, grad_bias: bool = False,
+                       accumulate: bool = False, da=None, db=None, dbias=None, da_dtype=None,
+                       db_dtype=None, workspace=None, status=None, stream=None):
+    """The backward pass of engram_matmul(a, b, bias, activation, scale=scale, pre=pre) for the
+    output gradient dy (bf16 or fp32 [M, N]; rows may repeat): (da [M, K], db [N, K], dbias fp32
+    [N]), None for those not asked for.  da and db are bf16 by default; accumulate adds to the db
+    and dbias given.  What the two products read of dy act'(pre) has been rounded to bf16."""
+    import torch
+    dd = _dtype(dy, "dy")
+    if dy.dim() != 2:
+        raise EngramError(ERR_INVALID_ARG, "dy must be [M, N]")
+    M, N = shape = dy.shape
+    rows, K, *pa = _bf16_operand(a, "a")
+    cols, kb, *pb = _bf16_operand(b, "b")
+    if rows != M or cols != N or kb != K:
+        raise EngramError(ERR_INVALID_ARG, "a must be [M, K] and b [N, K] for dy [M, N]")
+    if accumulate and ((grad_b and db is None) or (grad_bias and dbias is None)):
+        raise EngramError(ERR_INVALID_ARG, "accumulate needs gradients to add to")
+    if _activation(activation) != ACT_NONE and pre is None:
+        raise EngramError(ERR_INVALID_ARG, "the gradient of an activation needs pre")
+    dev = dy.device
+    if not grad_a:
+        da = None
+    elif da is None:
+        da = _made(stream, torch.empty, (M, K), dtype=da_dtype or torch.bfloat16, device=dev)
+    if not grad_b:
+        db = None
+    elif db is None:
+        db = _made(stream, torch.empty, (N, K), dtype=db_dtype or torch.bfloat16, device=dev)
+    if not grad_bias:
+        dbias = None
+    elif dbias is None:
+        dbias = _made(stream, torch.empty, N, dtype=torch.float32, device=dev)
+    _need(dbias, (torch.float32,), "dbias")
+    if dbias is not None and dbias.shape != (N,):
+        raise EngramError(ERR_INVALID_ARG, f"dbias must be {[N]}")
+    _one_device(stream, dy, a, b, pre, da, db, dbias, workspace, status)
+    args = (dy.data_ptr(), dd, _strides(dy, "dy")[0], *pa, *pb, M, N, K)
+    ws, ws_bytes, workspace = _scratch(
+        workspace, lib.engram_matmul_grad_workspace_bytes(*args, activation, grad_a, grad_b, grad_bias),
+        dy, stream)
+    _check(lib.engram_matmul_grad(*args, scale, *_plane(pre, shape, "pre"), activation, accumulate,
+                                  *_plane(da, (M, K), "da"), *_plane(db, (N, K), "db"), _ptr(dbias),
+                                  ws, ws_bytes, _ptr(status), _stream(stream)), "engram_matmul_grad")
+    return da, db, dbias
+
+
+def _matrices(t, shape, name):
+    """(pointer, strides between matrices and rows) of a tensor of `shape`, [M, N] or [L, M, N]."""
+    if t is None:
+        return None, 0, 0
+    if t.shape != shape:
+        raise EngramError(ERR_INVALID_ARG, f"{name} must be {list(shape)}")
+    st = _strides(t, name)
+    return (t.data_ptr(), st[0], st[1]) if len(st) == 3 else (t.data_ptr(), 0, st[0])
+
+
+def engram_orthogonalise_workspace_bytes(count: int, M: int, N: int) -> int:
+    return int(lib.engram_orthogonalise_workspace_bytes(count, M, N))
+
+
+def engram_orthogonalise(g, momentum=None, beta: float = 0.95, nesterov: bool = True, steps: int = 5,
+                         coefficients=(3.4445, -4.7750, 2.0315), scale: float = 1.0,
+                         eps: float = 1e-7, out=None, workspace=None, status=None, stream=None):
+    """The orthogonalised update of a weight matrix, or of several of one shape at once: g bf16 or
+    fp32 [M, N] or [L, M, N], momentum fp32 (updated in place: beta * momentum + g) or None.
+    Returns out, bf16: scale times the Newton-Schulz iterate (`steps` times a X + (b A + c A^2) X,
+    A = X X^T) of the momentum, or with nesterov of g + beta * momentum, over its Frobenius norm."""
+    import torch
+    gd, shape = _dtype(g, "g"), g.shape
+    if len(shape) not in (2, 3):
+        raise EngramError(ERR_INVALID_ARG, "g must be [M, N] or [L, M, N]")
+    L, M, N = shape if len(shape) == 3 else (1, *shape)
+    if len(coefficients) != 3:
+        raise EngramError(ERR_INVALID_ARG, "coefficients must be three numbers")
+    if momentum is not None:
+        _need(momentum, (torch.float32,), "momentum", contiguous=False)
+    if out is None:
+        out = _made(stream, torch.empty, shape, dtype=torch.bfloat16, device=g.device)
+    _need(out, (torch.bfloat16, torch.int16), "out", contiguous=False)
+    _one_device(stream, g, momentum, out, workspace, status)
+    gp, *gs = _matrices(g, shape, "g")
+    ws, ws_bytes, workspace = _scratch(workspace, engram_orthogonalise_workspace_bytes(L, M, N), g,
+                                       stream)
+    _check(lib.engram_orthogonalise(gp, gd, L, M, N, *gs, *_matrices(momentum, shape, "momentum"),
+                                    beta, nesterov, steps, *coefficients, scale, eps,
+                                    *_matrices(out, shape, "out"), ws, ws_bytes, _ptr(status),
+                                    _stream(stream)), "engram_orthogonalise")
+    return out

@@ -1,0 +1,77 @@
+// product_internal.cuh -- launch parameters and launchers of the 16-bit product and of what is
+// built on it (its gradient, the orthogonalised update), shared with their C ABI layer
+// (product_api.cu).
+#pragma once
+
+#include "train_internal.cuh"
+
+namespace engram {
+
+constexpr int kTypeF16 = 2;  // beside ENGRAM_DTYPE_*: values inside the library
+
+// A 16-bit operand [rows, K]: element (r, k) at r * stride + k, or with `t` at k * stride + r.
+// 16-byte aligned, stride and batch a multiple of 8 elements.
+struct Operand {
+  const void *p;
+  int64_t stride, batch;  // batch: elements between matrices
+  bool t;
+};
+
+// A value [M, N] per matrix, element (m, n) at m * stride + n; NULL: not there.
+struct Plane {
+  void *p;
+  int64_t stride, batch;
+  int32_t type;  // ENGRAM_DTYPE_* or kTypeF16
+};
+
+// out = act(scale * a b^T + bias) + residual_scale * residual, pre = what act is taken of; for
+// `count` matrices.
+struct ProductParams {
+  Operand a, b;
+  bool f16;  // operands: f16, else bf16
+  int64_t M, N, K, count;
+  float scale, residual_scale;
+  Plane out, residual, pre;
+  const void *bias;
+  int32_t bias_type, act;
+  // a and b are one matrix and so out is symmetric (as must be residual): the products on one
+  // side of the diagonal are computed, and written on both
+  bool symmetric;
+  int32_t *status;
+};
+cudaError_t launch_product(const ProductParams &p, cudaStream_t stream);
+
+// [rows, cols] 16-bit values from rows src_stride apart to rows dst_stride apart (a multiple of
+// 8, dst 16-byte aligned).
+cudaError_t launch_pack(const void *src, int64_t src_stride, void *dst, int64_t dst_stride, int64_t rows,
+                        int64_t cols, cudaStream_t stream);
+
+// dz = dy * act'(pre), rounded to bf16, and its column sums before the rounding.
+struct ActGradParams {
+  const void *dy, *pre;  // pre NULL without an activation
+  void *dz;              // bf16 [M, N], dz_stride a multiple of 8, or NULL
+  float *dbias;          // [N] or NULL
+  float *partial;        // act_grad_partial_bytes()
+  int64_t M, N, dy_stride, pre_stride, dz_stride;
+  int32_t dy_type, pre_type, act;
+  bool accumulate;  // dbias is added to
+  // set by the launcher
+  int32_t slabs, col_blocks;
+  int64_t slab_rows;
+};
+size_t act_grad_partial_bytes(int64_t M, int64_t N);
+cudaError_t launch_act_grad(ActGradParams p, cudaStream_t stream);
+
+// Newton-Schulz on `count` matrices [M, N].
+struct OrthogonaliseParams {
+  Plane g, momentum, out;  // momentum.p NULL: none
+  int64_t M, N, count;
+  float beta, eps, scale, a, b, c;
+  int32_t steps;
+  bool nesterov;
+  int32_t *status;
+};
+size_t orthogonalise_workspace_bytes(int64_t M, int64_t N, int64_t count);
+cudaError_t launch_orthogonalise(const OrthogonaliseParams &p, void *workspace, cudaStream_t stream);
+
+}  // namespace engram

@@ -681,6 +681,119 @@ ENGRAM_API engram_status engram_gate_add_grad(const float *k, const uint8_t *sta
                                               void *stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The bf16 product with an epilogue, its gradient, and the orthogonalised update of a
+ * weight matrix.  The conventions of the training calls hold, as do their dtypes.
+ */
+#define ENGRAM_ACT_NONE 0
+#define ENGRAM_ACT_RELU 1 /* max(z, 0) */
+#define ENGRAM_ACT_SILU 2 /* z / (1 + e^-z) */
+#define ENGRAM_ACT_GELU 3 /* z Phi(z), Phi the normal distribution function (no tanh form) */
+
+/*
+ * engram_matmul -- a matrix product with bias, activation and residual:
+ *   z = scale * a b^T + bias;   out = act(z) + residual;   pre = z where pre is given
+ * tcgen05 tensor cores, fp32 accumulation, each output rounded once to its type.
+ *   a     bf16 bits [M, K]: element (m, k) at m*a_stride + k, or, with a_trans, at
+ *         k*a_stride + m (the transposed view of a [K, M] matrix)
+ *   b     bf16 bits [N, K], likewise
+ *   bias  ENGRAM_DTYPE_* [N], or NULL
+ *   residual  ENGRAM_DTYPE_* [M, N], residual_stride elements between rows (0: one row for
+ *         all), or NULL; it may be out itself
+ *   pre   ENGRAM_DTYPE_* [M, N], pre_stride elements between rows, or NULL: what
+ *         engram_matmul_grad needs of the forward pass
+ *   out   ENGRAM_DTYPE_* [M, N], out_stride elements between rows
+ * Any sizes, strides of a row's width or more, and element alignment.  An operand whose rows
+ * do not all start on 16-byte boundaries is copied first, into the workspace:
+ *   workspace  device, 16-byte aligned, engram_matmul_workspace_bytes(...) bytes for these
+ *         operands; 0 (and workspace unused) when both start on 16-byte boundaries with
+ *         strides that are multiples of 8 elements
+ * The fp32 sums of long products (fp32 out, K > 8192) are added up in parts of at most 8192,
+ * except with an activation or pre and out as its own residual.  A wait that runs out
+ * sets ENGRAM_FLAG_TIMEOUT and leaves outputs unwritten.  M == 0 launches nothing.
+ */
+ENGRAM_API size_t engram_matmul_workspace_bytes(const uint16_t *a, int64_t a_stride, int32_t a_trans,
+                                                const uint16_t *b, int64_t b_stride, int32_t b_trans,
+                                                int64_t M, int64_t N, int64_t K);
+ENGRAM_API engram_status engram_matmul(const uint16_t *a, int64_t a_stride, int32_t a_trans,
+                                       const uint16_t *b, int64_t b_stride, int32_t b_trans,
+                                       int64_t M, int64_t N, int64_t K, float scale,
+                                       const void *bias, int32_t bias_dtype, int32_t activation,
+                                       const void *residual, int32_t residual_dtype,
+                                       int64_t residual_stride, void *pre, int32_t pre_dtype,
+                                       int64_t pre_stride, void *out, int32_t out_dtype,
+                                       int64_t out_stride, void *workspace, size_t workspace_bytes,
+                                       int32_t *status, void *stream);
+
+/*
+ * engram_matmul_grad -- the backward pass of engram_matmul for the output gradient dy (the
+ * residual's gradient is dy itself):
+ *   dz = dy act'(pre);  da = scale dz b;  db = scale dz^T a;  dbias = sum over m of dz
+ * dz is rounded once to bf16 as the operand of the two products (nothing is rounded where dy
+ * is bf16 and there is no activation) and summed for dbias before that, in fp32 in an order
+ * that M and N fix.
+ *   dy    ENGRAM_DTYPE_* [M, N], dy_stride elements between rows (0: one row for all)
+ *   a, b  as engram_matmul (a is read for db, b for da; the other may be NULL)
+ *   pre   ENGRAM_DTYPE_* [M, N], the forward pass's; not read without an activation
+ *   da    ENGRAM_DTYPE_* [M, K], db ENGRAM_DTYPE_* [N, K] with strides between their rows,
+ *         dbias fp32 [N]; NULL: not made
+ *   accumulate  != 0: db and dbias are added to what is there
+ *   workspace  device, 16-byte aligned, engram_matmul_grad_workspace_bytes(...) bytes for
+ *         these operands and for the gradients that are asked for
+ * M == 0 zeroes db and dbias (unless they accumulate).
+ */
+ENGRAM_API size_t engram_matmul_grad_workspace_bytes(const void *dy, int32_t dy_dtype,
+                                                     int64_t dy_stride, const uint16_t *a,
+                                                     int64_t a_stride, int32_t a_trans,
+                                                     const uint16_t *b, int64_t b_stride,
+                                                     int32_t b_trans, int64_t M, int64_t N,
+                                                     int64_t K, int32_t activation, int32_t grad_a,
+                                                     int32_t grad_b, int32_t grad_bias);
+ENGRAM_API engram_status engram_matmul_grad(const void *dy, int32_t dy_dtype, int64_t dy_stride,
+                                            const uint16_t *a, int64_t a_stride, int32_t a_trans,
+                                            const uint16_t *b, int64_t b_stride, int32_t b_trans,
+                                            int64_t M, int64_t N, int64_t K, float scale,
+                                            const void *pre, int32_t pre_dtype, int64_t pre_stride,
+                                            int32_t activation, int32_t accumulate, void *da,
+                                            int32_t da_dtype, int64_t da_stride, void *db,
+                                            int32_t db_dtype, int64_t db_stride, float *dbias,
+                                            void *workspace, size_t workspace_bytes,
+                                            int32_t *status, void *stream);
+
+/*
+ * engram_orthogonalise -- the update of a weight matrix from its gradient by momentum and the
+ * Newton-Schulz iteration, which brings the singular values near one (as the Muon optimiser
+ * does), for `count` matrices [M, N] at once:
+ *   m = beta m + g;   u = g + beta m (nesterov) or m   (without momentum u = g)
+ *   X = u / (|u|_F + eps);   `steps` times, with A = X X^T:
+ *   X = coeff_a X + (coeff_b A + coeff_c A^2) X;   out = scale X
+ *   g         ENGRAM_DTYPE_* [count, M, N], g_batch and g_stride elements between matrices
+ *             and rows
+ *   momentum  fp32 [count, M, N], updated in place, or NULL
+ *   out       bf16 bits [count, M, N]
+ *   workspace device, 16-byte aligned, engram_orthogonalise_workspace_bytes(...) bytes
+ * fp32 momentum, norm and sums; the iterate and the square matrices are held in fp16 times
+ * 2^8 between the products: the result is about 4e-3 off at most (of its Frobenius norm;
+ * its own rounding to bf16 is 1.7e-3) with the usual coefficients 3.4445, -4.7750, 2.0315
+ * and 5 steps.  Singular values over 255 on the way overflow.  The squares of the norm are
+ * fp32: values of u under 1e-19 count as zero in it.  A matrix of zeros stays zero; a NaN or
+ * an infinity makes its matrix NaN.  steps in [1, 64], coefficients in [-16, 16].  A wait
+ * that runs out sets ENGRAM_FLAG_TIMEOUT: then the outputs are not valid.  count == 0
+ * launches nothing.
+ */
+ENGRAM_API size_t engram_orthogonalise_workspace_bytes(int64_t count, int64_t M, int64_t N);
+ENGRAM_API engram_status engram_orthogonalise(const void *g, int32_t g_dtype, int64_t count,
+                                              int64_t M, int64_t N, int64_t g_batch,
+                                              int64_t g_stride, float *momentum,
+                                              int64_t momentum_batch, int64_t momentum_stride,
+                                              float beta, int32_t nesterov, int32_t steps,
+                                              float coeff_a, float coeff_b, float coeff_c,
+                                              float scale, float eps, uint16_t *out,
+                                              int64_t out_batch, int64_t out_stride,
+                                              void *workspace, size_t workspace_bytes,
+                                              int32_t *status, void *stream);
+
+/*
  * engram_read_status -- waits for `stream`, copies the device status word into
  * *flags_host and returns ENGRAM_OK (no flag), ENGRAM_ERR_TIMEOUT
  * (ENGRAM_FLAG_TIMEOUT set) or ENGRAM_ERR_OUT_OF_RANGE (a range flag set).  The
