@@ -41,41 +41,53 @@
 namespace engram {
 namespace {
 
-constexpr int kP = 128;         // rows of b a CTA stages
+constexpr int kP = 128;         // rows of the P operand a CTA stages
 constexpr int kBK = 64;         // of K a stage: 128 bytes
-constexpr int kQMax = 128;      // most rows of a a tile of one CTA
+constexpr int kQMax = 128;      // most rows of the Q operand a tile of one CTA
 constexpr int kPairQMax = 256;  // and of a pair
-constexpr int kThreads = 256;   // warps 2 and 3 idle: the epilogue's start at a multiple of 4
-constexpr int kPairThreads = 512;
-constexpr int kPairParts = 3;  // of a tile's columns, a warp of each quarter of the lanes each
+// Epilogue warps: one of each quarter of the lanes for each part of a tile's columns; warps 2 and
+// 3 idle, as the epilogue's start at a multiple of 4.
+constexpr int kParts = 2, kPairParts = 3;
+constexpr int kThreads = 128 * (1 + kParts), kPairThreads = 128 * (1 + kPairParts);
 constexpr int kSegmentBlocks = 128;
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 12, kMaxAhead = 4;
 constexpr uint32_t kPBytes = kP * kBK * 2;
-constexpr uint32_t kBarBytes = 512;
-constexpr uint32_t kStageBudget = 192 * 1024;
-constexpr uint32_t kSplitStageBudget = 104 * 1024;
-constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSplitTmemCols = 128;
-constexpr size_t kSmemBytes = 1024 + kStageBudget + kBarBytes;
-constexpr size_t kSplitSmemBytes = 1024 + kSplitStageBudget + kBarBytes;
-constexpr uint32_t kPairStageBudget = 224 * 1024;
-constexpr size_t kPairSmemBytes = 1024 + kPairStageBudget + kBarBytes;
-static_assert(2 * (kSplitSmemBytes + 1024 + 64) <= 228 * 1024 && kPairSmemBytes <= 227 * 1024);
-static_assert((2 * kMaxStages + 6) * 8 + 8 <= kBarBytes);
+constexpr uint32_t kBarBytes = 1024;
+constexpr int kUnit = 32;   // columns a warp of the tiles' epilogue moves at a time
+constexpr int kPitch = 36;  // floats between the rows of a warp's transposing buffer: no bank conflicts
+constexpr uint32_t kBufferBytes = 16 * kPitch * 4;
+// Shared memory for stages and epilogue buffers.
+constexpr uint32_t kBudget = 224 * 1024;
+constexpr uint32_t kSplitBudget = 104 * 1024;
+constexpr uint32_t kTmemCols = 512, kSplitTmemCols = 128;
+constexpr size_t kSmemBytes = 1024 + kBarBytes + kBudget;
+constexpr size_t kSplitSmemBytes = 1024 + kBarBytes + kSplitBudget;
+static_assert(2 * (kSplitSmemBytes + 1024) <= 228 * 1024 && kSmemBytes <= 227 * 1024);
+static_assert((2 * kMaxStages + 6 + 4 * kPairParts * kMaxAhead) * 8 + 8 <= kBarBytes);
+
+struct PlaneDev {
+  void *p;
+  int64_t stride, batch;
+  int32_t type;
+  bool vec;  // rows start on 16-byte boundaries
+};
 
 struct ProductDev {
-  Plane out, residual, pre;
-  const void *bias;
+  PlaneDev out, residual, pre, bias;
   int32_t *status;
   int64_t wait_limit_ns;
   int32_t M, N;
   float scale, residual_scale;
-  int32_t bias_type, act;
-  int32_t kblocks, q_tile, q_rows, stages;  // q_rows: rows of a that a CTA stages
+  int32_t act;
+  int32_t kblocks, q_tile, q_rows, stages;  // q_rows: rows of Q that a CTA stages
   int32_t segments, seg_blocks, splits;
   int32_t tiles_p, tiles_q, tiles, matrix_tiles;
   uint32_t idesc;
-  bool p_t, q_t, symmetric, many;
+  // the tiles' epilogue: of each warp, buffers for units of the residual ahead (ahead of them,
+  // ahead_bytes each) and for units on their way out (slots of them, slot_bytes each)
+  int32_t ahead, slots;
+  uint32_t ahead_bytes, slot_bytes;
+  bool p_t, q_t, many;
   bool fold;      // the residual goes into the first segment's sum (it lies where out does)
   bool withhold;  // test hook: the first stage waits for bytes that never come
 };
@@ -156,10 +168,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
 struct Tile {
   int p0, q0, z;
 };
-// Tiles in groups of up to 16 along b, a's tiles inside a group in order: what the resident
+// Tiles in groups of up to 16 along P, Q's tiles inside a group in order: what the resident
 // CTAs read at one time is a few slices of each operand.  Of a symmetric product those that
 // hold any output (m, n) with n <= m.
-template <int WIDTH>
+template <int WIDTH, bool SYMMETRIC>
 __device__ __forceinline__ Tile tile_at(const ProductDev &p, int tile) {
   Tile r{0, 0, 0};
   uint32_t t = tile;
@@ -168,7 +180,7 @@ __device__ __forceinline__ Tile tile_at(const ProductDev &p, int tile) {
     t -= r.z * (uint32_t)p.matrix_tiles;
   }
   uint32_t tp, tq;
-  if (p.symmetric) {
+  if constexpr (SYMMETRIC) {
     for (tq = 0;; ++tq) {
       const uint32_t wide = min(p.tiles_p, (min(p.M, (int)(tq + 1) * p.q_tile) - 1) / WIDTH + 1);
       if (t < wide) break;
@@ -187,6 +199,17 @@ __device__ __forceinline__ Tile tile_at(const ProductDev &p, int tile) {
 
 // ---- epilogue ---------------------------------------------------------------------------
 
+// How a kernel's epilogue moves its values.
+//   kTiles: the lanes of TMEM are rows of out.  A lane turns 32 values of its row into words that it
+//     puts into shared memory, from where tensor copies take 32 x 32 values at a time to out (and
+//     pre); the residual comes in the same way, asked for ahead.  Where out, pre and residual have
+//     rows on 16-byte boundaries.
+//   kSingles: the lanes of TMEM are columns of out.  A warp moves 32 neighbouring values of a row at
+//     a time: any strides, few rows, sums in segments.
+//   kSymmetric: as kSingles, for a symmetric product.
+// One of them to a kernel: code of all would not stay in the instruction cache.
+enum Epilogue { kTiles, kSingles, kSymmetric };
+
 // f(a null pointer of the C++ type of `type`).
 template <typename F>
 __device__ __forceinline__ void by_type(int type, F f) {
@@ -196,6 +219,46 @@ __device__ __forceinline__ void by_type(int type, F f) {
     f(static_cast<__nv_bfloat16 *>(nullptr));
   else
     f(static_cast<__half *>(nullptr));
+}
+
+__device__ __forceinline__ uint8_t *element(const PlaneDev &s, int64_t z, int64_t m, int64_t n) {
+  return static_cast<uint8_t *>(s.p) + ((z * s.batch + m * s.stride + n) << (s.type == ENGRAM_DTYPE_F32 ? 2 : 1));
+}
+__device__ __forceinline__ float load_one(const PlaneDev &s, int64_t z, int64_t m, int64_t n) {
+  const uint8_t *at = element(s, z, m, n);
+  if (s.type == ENGRAM_DTYPE_F32) return *reinterpret_cast<const float *>(at);
+  const uint16_t v = *reinterpret_cast<const uint16_t *>(at);
+  return s.type == ENGRAM_DTYPE_BF16 ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
+}
+__device__ __forceinline__ void store_one(const PlaneDev &d, int64_t z, int64_t m, int64_t n, float v) {
+  by_type(d.type, [&](auto *type) { from_float(*reinterpret_cast<decltype(type)>(element(d, z, m, n)), v); });
+}
+
+__device__ __forceinline__ void decode2(uint32_t w, int type, float &lo, float &hi) {
+  if (type == ENGRAM_DTYPE_BF16) {
+    lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
+  } else {
+    lo = __half2float(__ushort_as_half((uint16_t)w)), hi = __half2float(__ushort_as_half((uint16_t)(w >> 16)));
+  }
+}
+// Two neighbouring 16-bit values, rounded to nearest even.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, int type) {
+  if (type == ENGRAM_DTYPE_BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ void store8(const PlaneDev &d, int64_t z, int64_t m, int64_t n, const float (&x)[8]) {
+  uint4 *at = reinterpret_cast<uint4 *>(element(d, z, m, n));
+  if (d.type == ENGRAM_DTYPE_F32) {
+    reinterpret_cast<float4 *>(at)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4 *>(at)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+    at[0] = make_uint4(pack2(x[0], x[1], d.type), pack2(x[2], x[3], d.type), pack2(x[4], x[5], d.type),
+                       pack2(x[6], x[7], d.type));
+  }
 }
 
 template <int N>
@@ -212,128 +275,418 @@ __device__ __forceinline__ void activate(float (&x)[N], int act) {
   }
 }
 
-// N values of one column of out (x[i] is output (m0 + i, n)), or of one row (ROW: (m, n0 + i)),
-// of which the first `count` count.
-template <bool ROW, int N>
-__device__ __forceinline__ void load_values(const Plane &s, int64_t z, int64_t m, int64_t n, int count,
-                                            float (&x)[N]) {
-  by_type(s.type, [&](auto *type) {
-    auto *src = static_cast<decltype(type)>(s.p) + z * s.batch + m * s.stride + n;
-    const int64_t step = ROW ? 1 : s.stride;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      x[i] = i < count ? to_float(*src) : 0.f;
-      src += step;
-    }
-  });
-}
-template <bool ROW, int N>
-__device__ __forceinline__ void store_values(const Plane &d, int64_t z, int64_t m, int64_t n, int count,
-                                             const float (&x)[N]) {
-  by_type(d.type, [&](auto *type) {
-    auto *dst = static_cast<decltype(type)>(d.p) + z * d.batch + m * d.stride + n;
-    const int64_t step = ROW ? 1 : d.stride;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (i < count) from_float(*dst, x[i]);
-      dst += step;
-    }
-  });
+// 8 values (four columns of each of two chunks' rows, say) of the buffer from `at` on.
+__device__ __forceinline__ void load8(const float *at, float (&x)[8]) {
+  const float4 a = reinterpret_cast<const float4 *>(at)[0], b = reinterpret_cast<const float4 *>(at)[1];
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
 
-// Sums of products become outputs: (m + i, n), or with ROW (m, n + i), for i < count.
-// `loaded`: the residual's values, already on their way.
-template <bool ROW, int N>
-__device__ __forceinline__ void finish(const ProductDev &p, int64_t z, int64_t m, int64_t n, int count, bool first,
-                                       bool last, float (&x)[N], const float (&residual)[N]) {
+// ---- kTiles
+
+// Where 16-byte piece j of row r of a unit lies: rows of 64 or 128 bytes (F32), swizzled as the
+// tensor copies do.
+template <bool F32>
+__device__ __forceinline__ uint32_t piece(uint32_t unit, int r, int j) {
+  return F32 ? unit + r * 128 + ((j ^ (r & 7)) << 4) : unit + r * 64 + ((j ^ (r >> 1 & 3)) << 4);
+}
+__device__ __forceinline__ void st_shared(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+// A lane's 32 values of row r of a unit, rounded to `type`.
+__device__ __forceinline__ void put_row(uint32_t unit, int r, int type, const float (&x)[kUnit]) {
+  if (type == ENGRAM_DTYPE_F32) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] *= p.scale;
-  if (!first) {
-    float sum[N];
-    load_values<ROW>(p.out, z, m, n, count, sum);
+    for (int j = 0; j < 8; ++j)
+      st_shared(piece<true>(unit, r, j), __float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]),
+                __float_as_uint(x[4 * j + 2]), __float_as_uint(x[4 * j + 3]));
+  } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] += sum[i];
+    for (int j = 0; j < 4; ++j)
+      st_shared(piece<false>(unit, r, j), pack2(x[8 * j], x[8 * j + 1], type), pack2(x[8 * j + 2], x[8 * j + 3], type),
+                pack2(x[8 * j + 4], x[8 * j + 5], type), pack2(x[8 * j + 6], x[8 * j + 7], type));
   }
-  if (last && p.bias) {
-    if constexpr (ROW) {
-      float b[N];
-      load_values<true>(Plane{const_cast<void *>(p.bias), 0, 0, p.bias_type}, 0, 0, n, count, b);
+}
+// x += by * the row's values.
+__device__ __forceinline__ void add_row(uint32_t unit, int r, int type, float by, float (&x)[kUnit]) {
+  if (type == ENGRAM_DTYPE_F32) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[i] += b[i];
-    } else if (count > 0) {
-      float b = 0.f;
-      by_type(p.bias_type, [&](auto *type) {
-        b = to_float(static_cast<const std::remove_pointer_t<decltype(type)> *>(p.bias)[n]);
-      });
+    for (int j = 0; j < 8; ++j) {
+      const uint4 v = ld_shared(piece<true>(unit, r, j));
+      x[4 * j] = fmaf(by, __uint_as_float(v.x), x[4 * j]);
+      x[4 * j + 1] = fmaf(by, __uint_as_float(v.y), x[4 * j + 1]);
+      x[4 * j + 2] = fmaf(by, __uint_as_float(v.z), x[4 * j + 2]);
+      x[4 * j + 3] = fmaf(by, __uint_as_float(v.w), x[4 * j + 3]);
+    }
+  } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[i] += b;
+    for (int j = 0; j < 4; ++j) {
+      const uint4 v = ld_shared(piece<false>(unit, r, j));
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        decode2(w[i], type, lo, hi);
+        x[8 * j + 2 * i] = fmaf(by, lo, x[8 * j + 2 * i]);
+        x[8 * j + 2 * i + 1] = fmaf(by, hi, x[8 * j + 2 * i + 1]);
+      }
     }
   }
-  if (last && p.pre.p) store_values<ROW>(p.pre, z, m, n, count, x);
-  if (last) activate(x, p.act);
-  if (p.residual.p && (p.fold ? first : last)) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] += p.residual_scale * residual[i];
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]),
+        "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]),
+        "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]),
+        "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(addr)
+      : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// What a warp moves of its CTA's tiles, unit by unit (32 rows x 32 columns): units [first, end) of
+// each tile, `row0` rows into it.  Units that lie outside out are passed over.
+struct Units {
+  int tile, step, unit, first, end, row0;
+  Tile at;
+
+  template <int WIDTH>
+  __device__ __forceinline__ void start(const ProductDev &p, int tile_, int step_, int first_, int end_, int row0_) {
+    tile = tile_, step = step_, first = unit = first_, end = end_, row0 = row0_;
+    if (first == end) tile = p.tiles;
+    if (tile < p.tiles) at = tile_at<WIDTH, false>(p, tile);
   }
-  if (p.symmetric) {
-    // This side of the diagonal, and its mirror image.
-    by_type(p.out.type, [&](auto *type) {
-      using T = std::remove_pointer_t<decltype(type)>;
-      T *out = static_cast<T *>(p.out.p) + z * p.out.batch;
-      if constexpr (ROW) {
+  __device__ __forceinline__ bool done(const ProductDev &p) const { return tile >= p.tiles; }
+  __device__ __forceinline__ int n() const { return at.q0 + unit * kUnit; }
+  __device__ __forceinline__ int m() const { return at.p0 + row0; }
+  __device__ __forceinline__ bool inside(const ProductDev &p) const { return n() < p.N && m() < p.M; }
+  template <int WIDTH>
+  __device__ __forceinline__ void next(const ProductDev &p) {
+    if (++unit < end) return;
+    unit = first;
+    tile += step;
+    if (tile < p.tiles) at = tile_at<WIDTH, false>(p, tile);
+  }
+};
+
+// A warp's share of the epilogue of all of its CTA's tiles.  `buffers`: its shared memory; `arrived`:
+// its barriers, one a residual buffer.
+template <bool PAIR, typename F>
+__device__ __forceinline__ void move_tiles(const ProductDev &p, const CUtensorMap *map_out, const CUtensorMap *map_pre,
+                                           const CUtensorMap *map_residual, uint32_t buffers, uint64_t *arrived,
+                                           uint64_t *acc_full, uint32_t quad_tmem, int first_tile, int tile_step,
+                                           int first, int end, int row0, int lane, volatile int *abort_flag,
+                                           F release) {
+  constexpr int kWidth = PAIR ? 2 * kP : kP, kAccCols = PAIR ? kPairQMax : kQMax;
+  const uint32_t slots = buffers + p.ahead * p.ahead_bytes;
+  Units ahead, now;
+  ahead.start<kWidth>(p, first_tile, tile_step, first, end, row0);
+  uint32_t asked = 0, used = 0, slot = 0;
+  // The residual of the next unit that has not been asked for.
+  const auto ask = [&] {
+    while (!ahead.done(p) && !ahead.inside(p)) ahead.next<kWidth>(p);
+    if (ahead.done(p)) return;
+    const uint32_t b = asked % (uint32_t)p.ahead;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(arrived + b, p.ahead_bytes);
+      tma_load_3d<false>(buffers + b * p.ahead_bytes, map_residual, ahead.n(), ahead.m(), ahead.at.z,
+                         smem_u32(arrived + b));
+    }
+    ++asked;
+    ahead.next<kWidth>(p);
+  };
+  // A free buffer: of the stores before, all but slots - 1 have been read.
+  const auto free_slot = [&] {
+    if (lane == 0) {
+      if (p.slots == 1)
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      else
+        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    }
+    __syncwarp();
+    const uint32_t at = slots + slot * p.slot_bytes;
+    slot = slot + 1 == (uint32_t)p.slots ? 0 : slot + 1;
+    return at;
+  };
+  const auto send = [&](const CUtensorMap *map, uint32_t from) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) tma_store_3d(map, from, now.n(), now.m(), now.at.z);
+  };
+  if (p.ahead)
+    for (int i = 0; i < p.ahead; ++i) ask();
+  bool ok = true;
+  uint32_t local = 0;
+  now.start<kWidth>(p, first_tile, tile_step, first, end, row0);
+  for (; ok && !now.done(p); now.next<kWidth>(p)) {
+    const uint32_t acc = local & 1;
+    if (now.unit == first) {
+      if (!(ok = warp_wait(acc_full + acc, (local >> 1) & 1, abort_flag, p))) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    }
+    uint32_t v[kUnit];
+    __syncwarp();
+    tmem_ld32(quad_tmem + acc * kAccCols + now.unit * kUnit, v);
+    if (now.unit == end - 1) {
+      release(acc);
+      ++local;
+    }
+    if (!now.inside(p)) continue;
+    float x[kUnit];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          if (i < count && n + i <= m) from_float(out[m * p.out.stride + n + i], x[i]);
-          if (i < count && n + i < m) from_float(out[(n + i) * p.out.stride + m], x[i]);
+    for (int i = 0; i < kUnit; ++i) x[i] = p.scale * __uint_as_float(v[i]);
+    if (p.bias.p) {
+      const int n = now.n();
+      if (n + kUnit <= p.N && p.bias.vec) {  // the same 32 values in every lane
+        if (p.bias.type == ENGRAM_DTYPE_F32) {
+          const float4 *at = reinterpret_cast<const float4 *>(static_cast<const float *>(p.bias.p) + n);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float4 b = __ldg(at + j);
+            x[4 * j] += b.x, x[4 * j + 1] += b.y, x[4 * j + 2] += b.z, x[4 * j + 3] += b.w;
+          }
+        } else {
+          const uint4 *at = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias.p) + n);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 b = __ldg(at + j);
+            const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[8 * j + 2 * i] += __uint_as_float(w[i] << 16);
+              x[8 * j + 2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
+            }
+          }
         }
       } else {
-        T *dst = out + m * p.out.stride + n;
+        // A lane a value; past the edge nothing is kept.
+        const float mine = n + lane < p.N ? load_one(p.bias, 0, 0, n + lane) : 0.f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          if (i < count && n <= m + i) from_float(*dst, x[i]);
-          dst += p.out.stride;
-        }
-        dst = out + n * p.out.stride + m;
-        if (sizeof(T) == 2 && count == N && n < m) {  // rows of 8 values on 16 bytes, as the operands'
-          alignas(16) T v[N];
-#pragma unroll
-          for (int i = 0; i < N; ++i) from_float(v[i], x[i]);
-#pragma unroll
-          for (int i = 0; i < N; i += 8)
-            *reinterpret_cast<uint4 *>(dst + i) = *reinterpret_cast<const uint4 *>(v + i);
-        } else {
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (i < count && n < m + i) from_float(dst[i], x[i]);
-        }
+        for (int i = 0; i < kUnit; ++i) x[i] += __shfl_sync(0xffffffffu, mine, i);
       }
-    });
-  } else {
-    store_values<ROW>(p.out, z, m, n, count, x);
+    }
+    if (p.pre.p) {
+      const uint32_t at = free_slot();
+      put_row(at, lane, p.pre.type, x);
+      send(map_pre, at);
+    }
+    activate(x, p.act);
+    if (p.ahead) {
+      const uint32_t b = used % (uint32_t)p.ahead;
+      if (!(ok = warp_wait(arrived + b, (used / (uint32_t)p.ahead) & 1, abort_flag, p))) break;
+      ++used;
+      add_row(buffers + b * p.ahead_bytes, lane, p.residual.type, p.residual_scale, x);
+      __syncwarp();
+      ask();
+    }
+    const uint32_t at = free_slot();
+    put_row(at, lane, p.out.type, x);
+    send(map_out, at);
   }
+  // What is on its way has arrived before the block exits.
+  if (lane == 0) {
+    for (; used < asked; ++used)
+      drain_phase(arrived + used % (uint32_t)p.ahead, (used / (uint32_t)p.ahead) & 1, p.wait_limit_ns);
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+  __syncwarp();
 }
 
-// A warp's part of an accumulator: 32 lanes (columns n, n + 1, .. of out), `chunks` times 16 of
-// its rows from m0 on.  `release` runs once the last column is in registers, before its stores.
-template <typename F>
-__device__ __forceinline__ void drain(const ProductDev &p, uint32_t taddr, int chunks, int z, int m0, int n,
-                                      bool first, bool last, F release) {
-  const int rows = n < p.N ? min(chunks * 16, p.M - m0) : 0;
-  const bool residual = p.residual.p && (p.fold ? first : last);
-#pragma unroll 1
-  for (int c = 0; c < chunks; ++c) {
-    const int count = min(16, rows - c * 16);
-    float r[16];
-    if (residual) load_values<false>(p.residual, z, m0 + c * 16, n, count, r);
-    uint32_t v[16];
-    __syncwarp();  // together again after the stores, as tcgen05.ld wants the warp
-    tmem_ld16(taddr + c * 16, v);
-    if (c == chunks - 1) release();
-    float x[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[i]);
-    finish<false>(p, z, m0 + c * 16, n, count, first, last, x, r);
+// A warp's part of an accumulator: 32 lanes (columns n0, n0 + 1, .. of out), `chunks` times 16 of
+// its rows from m0 on.  begin() asks for what the first rows need, before the accumulator is
+// waited for; run() drains it, and calls `release` once the last column is in registers.
+template <int KIND>
+struct Drain;
+
+// A lane a column: a warp moves 32 neighbouring values of a row at a time.
+template <>
+struct Drain<kSingles> {
+  int z, m0, n;
+  float bias;
+
+  __device__ __forceinline__ void begin(const ProductDev &p, int z_, int m0_, int, int n0, int lane, bool, bool last) {
+    z = z_, m0 = m0_, n = n0 + lane;
+    bias = last && p.bias.p && n < p.N ? load_one(p.bias, 0, 0, n) : 0.f;
   }
+
+  static __device__ __forceinline__ void load(const PlaneDev &s, int z, int m, int n, int count, float (&x)[16]) {
+    by_type(s.type, [&](auto *type) {
+      auto *src = reinterpret_cast<decltype(type)>(element(s, z, m, n));
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        x[i] = i < count ? to_float(*src) : 0.f;
+        src += s.stride;
+      }
+    });
+  }
+  static __device__ __forceinline__ void store(const PlaneDev &d, int z, int m, int n, int count,
+                                               const float (&x)[16]) {
+    by_type(d.type, [&](auto *type) {
+      auto *dst = reinterpret_cast<decltype(type)>(element(d, z, m, n));
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (i < count) from_float(*dst, x[i]);
+        dst += d.stride;
+      }
+    });
+  }
+
+  template <typename F>
+  __device__ __forceinline__ void run(const ProductDev &p, uint32_t taddr, int chunks, float *, int, bool first,
+                                      bool last, F release) {
+    const bool add = p.residual.p && (p.fold ? first : last);
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+      const int m = m0 + c * 16, count = n < p.N ? min(16, p.M - m) : 0;
+      float y[16];
+      if (add) load(p.residual, z, m, n, count, y);
+      uint32_t v[16];
+      __syncwarp();
+      tmem_ld16(taddr + c * 16, v);
+      if (c == chunks - 1) release();
+      float x[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = p.scale * __uint_as_float(v[i]);
+      if (!first) {
+        float sum[16];
+        load(p.out, z, m, n, count, sum);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] += sum[i];
+      }
+      if (last) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] += bias;
+        if (p.pre.p) store(p.pre, z, m, n, count, x);
+        activate(x, p.act);
+      }
+      if (add) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = fmaf(p.residual_scale, y[i], x[i]);
+      }
+      store(p.out, z, m, n, count, x);
+    }
+  }
+};
+
+// A lane's 16 values of a chunk are neighbours in the mirror image's row n, where the residual
+// (fp16 and symmetric itself) is read and one image is stored; the other one is turned around.
+// Both are fp16 with rows on 16-byte boundaries.
+template <>
+struct Drain<kSymmetric> {
+  uint4 next[2];
+  int z, m0, row;  // row: this lane's n
+
+  __device__ __forceinline__ bool needs(const ProductDev &p, int m) const {
+    return p.residual.p && row < p.N && row < m + 16 && m < p.M;
+  }
+  // Rows are padded to multiples of 64, so a whole chunk can be read.
+  __device__ __forceinline__ void load_residual(const ProductDev &p, int m) {
+    const uint4 *at = reinterpret_cast<const uint4 *>(element(p.residual, z, row, m));
+    next[0] = at[0], next[1] = at[1];
+  }
+  __device__ __forceinline__ void begin(const ProductDev &p, int z_, int m0_, int, int n0, int lane, bool, bool) {
+    z = z_, m0 = m0_;
+    row = n0 + lane;
+    if (needs(p, m0)) load_residual(p, m0);
+  }
+
+  template <typename F>
+  __device__ __forceinline__ void run(const ProductDev &p, uint32_t taddr, int chunks, float *buffer, int lane, bool,
+                                      bool, F release) {
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+      const int m = m0 + c * 16;
+      uint32_t v[16];
+      __syncwarp();
+      tmem_ld16(taddr + c * 16, v);
+      if (c == chunks - 1) release();
+      float x[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = p.scale * __uint_as_float(v[i]);
+      if (needs(p, m)) {
+        const uint32_t w[8] = {next[0].x, next[0].y, next[0].z, next[0].w, next[1].x, next[1].y, next[1].z, next[1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float lo, hi;
+          decode2(w[i], kTypeF16, lo, hi);
+          x[2 * i] = fmaf(p.residual_scale, lo, x[2 * i]);
+          x[2 * i + 1] = fmaf(p.residual_scale, hi, x[2 * i + 1]);
+        }
+      }
+      if (c + 1 < chunks && needs(p, m + 16)) load_residual(p, m + 16);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) buffer[i * kPitch + lane] = x[i];
+      if (row < p.N && m < p.M) {
+        __half *dst = reinterpret_cast<__half *>(element(p.out, z, row, m));
+        if (row < m && m + 16 <= p.M) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            reinterpret_cast<uint4 *>(dst)[i] =
+                make_uint4(pack2(x[8 * i], x[8 * i + 1], kTypeF16), pack2(x[8 * i + 2], x[8 * i + 3], kTypeF16),
+                           pack2(x[8 * i + 4], x[8 * i + 5], kTypeF16), pack2(x[8 * i + 6], x[8 * i + 7], kTypeF16));
+        } else {  // on the diagonal the values after it, at the edge those before it
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (row < m + i && m + i < p.M) dst[i] = __float2half_rn(x[i]);
+        }
+      }
+      __syncwarp();
+      const int n = row - lane + (lane & 3) * 8;
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        const int q = 8 * h + (lane >> 2), side = min(p.N - 1, m + q) - n + 1;  // values up to the diagonal
+        if (m + q >= p.M || side <= 0) continue;
+        float y[8];
+        load8(buffer + q * kPitch + (lane & 3) * 8, y);
+        if (side >= 8) {
+          store8(p.out, z, m + q, n, y);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i < side) store_one(p.out, z, m + q, n + i, y[i]);
+        }
+      }
+    }
+  }
+};
+
+// One sum of products of a tile that several CTAs share becomes outputs; of a symmetric product,
+// on the side n <= m, both images.
+template <bool SYMMETRIC>
+__device__ __forceinline__ void finish_one(const ProductDev &p, int64_t z, int64_t m, int64_t n, float x, float bias,
+                                           float residual) {
+  if constexpr (SYMMETRIC) {
+    if (n > m) return;
+    x += residual;
+    store_one(p.out, z, m, n, x);
+    if (n < m) store_one(p.out, z, n, m, x);
+    return;
+  }
+  float v[1] = {x + bias};
+  if (p.pre.p) store_one(p.pre, z, m, n, v[0]);
+  activate(v, p.act);
+  store_one(p.out, z, m, n, v[0] + residual);
 }
 
 // ---- the kernels ------------------------------------------------------------------------
@@ -342,24 +695,27 @@ __device__ __forceinline__ void drain(const ProductDev &p, uint32_t taddr, int c
 // arrival that expects both CTAs' bytes; empty, acc_full and mma_done exist in both and take the
 // leader's multicast commits; acc_empty lives in the leader and takes an arrival from every
 // epilogue warp of the pair.
-template <bool PAIR, bool SPLIT>
+template <bool PAIR, bool SPLIT, int KIND>
 __global__ void __launch_bounds__(PAIR ? kPairThreads : kThreads, SPLIT ? 2 : 1)
     product_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
-                   const __grid_constant__ ProductDev p) {
-  static_assert(!(PAIR && SPLIT));
-  constexpr uint32_t kBudget = PAIR ? kPairStageBudget : SPLIT ? kSplitStageBudget : kStageBudget;
+                   const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_pre,
+                   const __grid_constant__ CUtensorMap map_residual, const __grid_constant__ ProductDev p) {
+  static_assert(!(PAIR && SPLIT) && !(SPLIT && KIND == kTiles));
   constexpr uint32_t kCols = SPLIT ? kSplitTmemCols : kTmemCols;
   constexpr int kAccCols = PAIR ? kPairQMax : kQMax;
   constexpr int kTileP = PAIR ? 2 * kP : kP;
-  constexpr int kParts = PAIR ? kPairParts : 1;
+  constexpr int kPartsHere = PAIR ? kPairParts : kParts;
+  constexpr bool kSym = KIND == kSymmetric;
   extern __shared__ uint8_t sm_raw[];
-  uint8_t *sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
-  uint64_t *full = reinterpret_cast<uint64_t *>(sm + kBudget);
+  // Barriers, stages, the epilogue's buffers.
+  uint8_t *base = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023), *sm = base + kBarBytes;
+  uint64_t *full = reinterpret_cast<uint64_t *>(base);
   uint64_t *empty = full + kMaxStages;
   uint64_t *acc_full = empty + kMaxStages;
   uint64_t *acc_empty = acc_full + 2;
   uint64_t *mma_done = acc_empty + 2;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
+  uint64_t *arrived = mma_done + 1;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(arrived + 4 * kPairParts * kMaxAhead);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -379,12 +735,23 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : kThreads, SPLIT ? 2 : 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(acc_full + a, 1);
-      mbar_init(acc_empty + a, (PAIR ? 2 : 1) * 4 * kParts);
+      mbar_init(acc_empty + a, (PAIR ? 2 : 1) * 4 * kPartsHere);
     }
     mbar_init(mma_done, 1);
+    if (KIND == kTiles)
+      for (int i = 0; i < 4 * kPartsHere * kMaxAhead; ++i) mbar_init(arrived + i, 1);
     if (p.withhold) mbar_expect_tx(full, 16);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (threadIdx.x == 64) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_p)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_q)) : "memory");
+    if (KIND == kTiles) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_out)) : "memory");
+      if (p.ahead)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_residual)) : "memory");
+    }
   }
   if (warp == 1) {
     if constexpr (PAIR) {
@@ -419,7 +786,7 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : kThreads, SPLIT ? 2 : 1)
       uint32_t ph = 0;
       bool ok = true;
       for (int tile = first_tile; ok && tile < p.tiles; tile += tile_step) {
-        Tile t = tile_at<kTileP>(p, tile);
+        Tile t = tile_at<kTileP, kSym>(p, tile);
         if constexpr (PAIR) t.p0 += rank * kP, t.q0 += rank * (qt / 2);
         for (int kb = 0; kb < kblocks; ++kb, ++it) {
           if (!(ok = wait_phase(empty + s, ph ^ 1, abort_flag, p.wait_limit_ns, p.status))) break;
@@ -480,41 +847,67 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : kThreads, SPLIT ? 2 : 1)
     // ------------------------------------------------------------- epilogue
     const int quad = warp & 3, part = (warp - 4) >> 2;
     const uint32_t acc_empty_at = PAIR ? map_to_rank(smem_u32(acc_empty), 0) : smem_u32(acc_empty);
-    // This warp's 16-column chunks: a part of the tile's.
-    const int c0 = qt / 16 * part / kParts, chunks = qt / 16 * (part + 1) / kParts - c0;
     const uint32_t quad_tmem = tmem + ((uint32_t)(quad * 32) << 16);
-    uint32_t unit = 0;
-    bool ok = true;
-    for (int tile = first_tile; ok && tile < p.tiles; tile += tile_step) {
-      const Tile t = tile_at<kTileP>(p, tile);
-      const int n = t.p0 + (PAIR ? rank * kP : 0) + quad * 32 + lane;
-      for (int seg = 0; seg < p.segments; ++seg, ++unit) {
-        const uint32_t acc = SPLIT ? 0 : unit & 1, use = unit >> 1;
-        ok = warp_wait(acc_full + acc, use & 1, abort_flag, p);
-        if (!ok) break;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if constexpr (SPLIT) {
-          // The partial tile into shared memory (the stages: every MMA has read them).
-          float *mine = reinterpret_cast<float *>(sm) + quad * 32 + lane;
-          for (int c = 0; c < qt; c += 16) {
-            uint32_t v[16];
-            tmem_ld16(quad_tmem + c, v);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) mine[(c + i) * kP] = __uint_as_float(v[i]);
-          }
-          break;
+    const int lanes0 = (PAIR ? rank * kP : 0) + quad * 32;  // of P, of the tile
+    uint8_t *buffers = sm + stages * stage_bytes;
+    const auto release = [&](uint32_t acc) {
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR)
+          mbar_arrive_cluster(acc_empty_at + 8u * acc);
+        else
+          mbar_arrive(acc_empty + acc);
+      }
+    };
+    if constexpr (KIND == kTiles) {
+      const int units = qt / kUnit, u0 = units * part / kPartsHere, u1 = units * (part + 1) / kPartsHere;
+      if (u0 == u1) {  // a narrow tile has nothing for this part
+        uint32_t local = 0;
+        for (int tile = first_tile; tile < p.tiles; tile += tile_step, ++local) {
+          if (!warp_wait(acc_full + (local & 1), (local >> 1) & 1, abort_flag, p)) break;
+          release(local & 1);
         }
-        drain(p, quad_tmem + acc * kAccCols + c0 * 16, chunks, t.z, t.q0 + c0 * 16, n, seg == 0,
-              seg == p.segments - 1, [&] {
-                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) {
-                  if constexpr (PAIR)
-                    mbar_arrive_cluster(acc_empty_at + 8u * acc);
-                  else
-                    mbar_arrive(acc_empty + acc);
-                }
-              });
+      } else {
+        move_tiles<PAIR>(p, &map_out, &map_pre, &map_residual,
+                         smem_u32(buffers) + (warp - 4) * (p.ahead * p.ahead_bytes + p.slots * p.slot_bytes),
+                         arrived + (warp - 4) * kMaxAhead, acc_full, quad_tmem, first_tile, tile_step, u0, u1, lanes0,
+                         lane, abort_flag, release);
+      }
+    } else {
+      // This warp's 16-column chunks: a part of the tile's.
+      const int c0 = qt / 16 * part / kPartsHere, chunks = qt / 16 * (part + 1) / kPartsHere - c0;
+      float *buffer = reinterpret_cast<float *>(buffers + (warp - 4) * kBufferBytes);
+      uint32_t unit = 0;
+      bool ok = true;
+      for (int tile = first_tile; ok && tile < p.tiles; tile += tile_step) {
+        const Tile t = tile_at<kTileP, kSym>(p, tile);
+        const int n0 = t.p0 + lanes0, m0 = t.q0 + c0 * 16;
+        for (int seg = 0; seg < p.segments; ++seg, ++unit) {
+          const uint32_t acc = SPLIT ? 0 : unit & 1, use = unit >> 1;
+          const bool first = seg == 0, last = seg == p.segments - 1;
+          Drain<KIND> drain;
+          if constexpr (!SPLIT) drain.begin(p, t.z, m0, chunks, n0, lane, first, last);
+          ok = warp_wait(acc_full + acc, use & 1, abort_flag, p);
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint32_t taddr = quad_tmem + acc * kAccCols + c0 * 16;
+          if constexpr (SPLIT) {
+            // The partial tile into shared memory (the stages: every MMA has read them).
+            float *mine = reinterpret_cast<float *>(sm) + c0 * 16 * kP + quad * 32 + lane;
+            for (int c = 0; c < chunks; ++c) {
+              uint32_t v[16];
+              tmem_ld16(taddr + c * 16, v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) mine[(c * 16 + i) * kP] = __uint_as_float(v[i]);
+            }
+            break;
+          }
+          if (chunks == 0)  // a tile of 16 columns has nothing for the second part
+            release(acc);
+          else
+            drain.run(p, taddr, chunks, buffer, lane, first, last, [&] { release(acc); });
+        }
       }
     }
   }
@@ -527,15 +920,20 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : kThreads, SPLIT ? 2 : 1)
     bool ok = true;
     for (int r = 0; r < p.splits; ++r)  // a CTA that gave up has no partial tile
       ok &= load_cluster(map_to_rank(smem_u32(const_cast<int *>(abort_flag)), r)) == 0;
-    const Tile t = tile_at<kTileP>(p, first_tile);
+    const Tile t = tile_at<kTileP, kSym>(p, first_tile);
     // A warp a column (128 outputs of one row of out), four outputs a lane.
     const int n = t.p0 + lane * 4;
     const int q_end = qt * (rank + 1) / p.splits;
     for (int q = qt * rank / p.splits + warp; q < q_end; q += kThreads / 32) {
-      const int m = t.q0 + q, count = ok && m < p.M ? min(4, p.N - n) : 0;
+      const int m = t.q0 + q;
+      if (!ok || m >= p.M) break;
       const uint32_t at = smem_u32(sm) + (q * kP + lane * 4) * 4;
-      float residual[4];
-      if (p.residual.p) load_values<true>(p.residual, t.z, m, n, count, residual);
+      float residual[4], bias[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        residual[i] = p.residual.p && n + i < p.N ? p.residual_scale * load_one(p.residual, t.z, m, n + i) : 0.f;
+        bias[i] = p.bias.p && n + i < p.N ? load_one(p.bias, 0, 0, n + i) : 0.f;
+      }
       float4 v[8];
 #pragma unroll
       for (int r = 0; r < 8; ++r)
@@ -543,8 +941,10 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : kThreads, SPLIT ? 2 : 1)
 #pragma unroll
       for (int r = 1; r < 8; ++r)
         v[0].x += v[r].x, v[0].y += v[r].y, v[0].z += v[r].z, v[0].w += v[r].w;
-      float x[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-      finish<true>(p, t.z, m, n, count, true, true, x, residual);
+      const float x[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < p.N) finish_one<kSym>(p, t.z, m, n + i, p.scale * x[i], bias[i], residual[i]);
     }
     cluster_sync();  // no CTA leaves while another may still read its part
   }
@@ -585,12 +985,41 @@ bool make_map(CUtensorMap *map, const Operand &o, int64_t rows, int64_t K, int64
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A plane as a 3-D tiled map: boxes of 32 x 32 values.
+bool make_plane_map(CUtensorMap *map, const PlaneDev &d, int64_t M, int64_t N, int64_t count) {
+  EncodeTiled fn = encode_fn();
+  if (!fn) return false;
+  const bool f32 = d.type == ENGRAM_DTYPE_F32;
+  const int64_t bytes = f32 ? 4 : 2, stride = M > 1 ? d.stride * bytes : (N * bytes + 15) / 16 * 16;
+  const cuuint64_t dims[3] = {(cuuint64_t)N, (cuuint64_t)M, (cuuint64_t)count};
+  const cuuint64_t strides[2] = {(cuuint64_t)stride, (cuuint64_t)(count > 1 ? d.batch * bytes : stride * M)};
+  const cuuint32_t box[3] = {kUnit, 32, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, d.p, dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct DeviceInfo {
   bool ready = false;
   int sms = 0, pairs = 0;  // pairs: CTA pairs that fit at once
 };
 DeviceInfo g_info[64];
 std::mutex g_info_mu;
+
+using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, ProductDev);
+enum Form { kSingle, kSplit, kPair, kForms };
+Kernel kernel_of(int form, int kind) {
+  static constexpr Kernel all[kForms][3] = {
+      {product_kernel<false, false, kTiles>, product_kernel<false, false, kSingles>,
+       product_kernel<false, false, kSymmetric>},
+      // the join moves values one by one in any case
+      {product_kernel<false, true, kSingles>, product_kernel<false, true, kSingles>,
+       product_kernel<false, true, kSymmetric>},
+      {product_kernel<true, false, kTiles>, product_kernel<true, false, kSingles>,
+       product_kernel<true, false, kSymmetric>}};
+  return all[form][kind];
+}
 
 cudaError_t device_info(DeviceInfo &out) {
   int dev = 0;
@@ -599,11 +1028,10 @@ cudaError_t device_info(DeviceInfo &out) {
   std::lock_guard<std::mutex> lock(g_info_mu);
   DeviceInfo &d = g_info[dev & 63];
   if (!d.ready) {
-    constexpr auto attribute = cudaFuncAttributeMaxDynamicSharedMemorySize;
     e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(product_kernel<false, false>, attribute, (int)kSmemBytes);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(product_kernel<false, true>, attribute, (int)kSplitSmemBytes);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(product_kernel<true, false>, attribute, (int)kPairSmemBytes);
+    for (int i = 0; i < 3 * kForms && e == cudaSuccess; ++i)
+      e = cudaFuncSetAttribute(kernel_of(i / 3, i % 3), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)(i / 3 == kSplit ? kSplitSmemBytes : kSmemBytes));
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -613,10 +1041,10 @@ cudaError_t device_info(DeviceInfo &out) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(d.sms / 2 * 2, 1, 1);
     cfg.blockDim = dim3(kPairThreads, 1, 1);
-    cfg.dynamicSmemBytes = kPairSmemBytes;
+    cfg.dynamicSmemBytes = kSmemBytes;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if ((e = cudaOccupancyMaxActiveClusters(&d.pairs, product_kernel<true, false>, &cfg)) != cudaSuccess) return e;
+    if ((e = cudaOccupancyMaxActiveClusters(&d.pairs, kernel_of(kPair, kTiles), &cfg)) != cudaSuccess) return e;
     d.ready = true;
   }
   out = d;
@@ -625,16 +1053,23 @@ cudaError_t device_info(DeviceInfo &out) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tiles of one matrix, `width` (along b) by qt (along a).
-int64_t tiles_of(const ProductParams &p, int width, int qt) {
-  const int64_t tp = ceil_div(p.N, width), tq = ceil_div(p.M, qt);
-  if (!p.symmetric) return tp * tq;
+// Tiles of one matrix, `width` along P by qt along Q.
+int64_t tiles_of(int64_t P, int64_t Q, int width, int qt, bool symmetric) {
+  const int64_t tp = ceil_div(P, width), tq = ceil_div(Q, qt);
+  if (!symmetric) return tp * tq;
   int64_t n = 0;
   for (int64_t q = 0; q < tq; ++q) {
-    const int64_t end = p.M < (q + 1) * qt ? p.M : (q + 1) * qt, wide = (end - 1) / width + 1;
+    const int64_t end = Q < (q + 1) * qt ? Q : (q + 1) * qt, wide = (end - 1) / width + 1;
     n += tp < wide ? tp : wide;
   }
   return n;
+}
+
+PlaneDev plane_of(const ProductParams &p, const Plane &x) {
+  const int64_t step = x.type == ENGRAM_DTYPE_F32 ? 4 : 8;
+  PlaneDev d{x.p, p.M > 1 ? x.stride : 0, p.count > 1 ? x.batch : 0, x.type, false};
+  d.vec = ((uintptr_t)x.p & 15) == 0 && d.stride % step == 0 && d.batch % step == 0;
+  return d;
 }
 
 bool overlaps(const Plane &a, const Plane &b, int64_t M, int64_t N) {
@@ -645,6 +1080,76 @@ bool overlaps(const Plane &a, const Plane &b, int64_t M, int64_t N) {
   return x && y && x < y + bytes(b) && y < x + bytes(a);
 }
 
+// Bytes of a tiles' epilogue unit.
+uint32_t unit_bytes(const PlaneDev &d) { return d.p ? 32 * kUnit * (d.type == ENGRAM_DTYPE_F32 ? 4 : 2) : 0; }
+
+// Fills in what a form needs and launches it: rows of a (`rows`) or of b in the lanes.
+cudaError_t launch_form(const ProductParams &p, ProductDev &d, int form, bool rows, int q_tile, const DeviceInfo &info,
+                        cudaStream_t stream) {
+  const Operand &op = rows ? p.a : p.b, &oq = rows ? p.b : p.a;
+  const int64_t P = rows ? p.M : p.N, Q = rows ? p.N : p.M;
+  const int kind = p.symmetric ? kSymmetric : rows ? kTiles : kSingles;
+  d.p_t = op.t;
+  d.q_t = oq.t;
+  d.q_tile = q_tile;
+  const int q_staged = form == kPair ? q_tile / 2 : q_tile;
+  d.q_rows = d.q_t ? (q_staged + 63) / 64 * 64 : q_staged;
+  const int64_t stage = kPBytes + d.q_rows * 128;
+  uint32_t budget = form == kSplit ? kSplitBudget : kBudget;
+  const int warps = 4 * (form == kPair ? kPairParts : kParts);
+  if (kind == kTiles) {
+    // One buffer of each sort beside the stages; more of them, and fewer stages, where K is short
+    // and moving out's values is the work.
+    d.ahead_bytes = unit_bytes(d.residual);
+    d.slot_bytes = unit_bytes(d.out) > unit_bytes(d.pre) ? unit_bytes(d.out) : unit_bytes(d.pre);
+    d.ahead = d.ahead_bytes ? 1 : 0;
+    d.slots = 1;
+    const auto stages = [&](int ahead, int slots) {
+      const int64_t left = (int64_t)budget - (int64_t)warps * (ahead * d.ahead_bytes + slots * d.slot_bytes);
+      return (int)(left / stage);
+    };
+    const int least = d.kblocks <= 16 ? 2 : 5;
+    if (stages(d.ahead, 2) >= least) d.slots = 2;
+    while (d.ahead && d.ahead < kMaxAhead && stages(d.ahead + 1, d.slots) >= least) ++d.ahead;
+    budget -= warps * (d.ahead * d.ahead_bytes + d.slots * d.slot_bytes);
+  } else if (kind == kSymmetric && form != kSplit) {
+    budget -= warps * kBufferBytes;
+  }
+  d.stages = (int32_t)(budget / stage);
+  if (d.stages > kMaxStages) d.stages = kMaxStages;
+  if (form == kSplit) {  // a CTA's part of K is one segment
+    d.segments = 1;
+    d.seg_blocks = d.kblocks;
+    d.fold = false;
+  }
+  const int width = form == kPair ? 2 * kP : kP;
+  const int64_t matrix_tiles = tiles_of(P, Q, width, q_tile, p.symmetric), tiles = matrix_tiles * p.count;
+  if (tiles > INT32_MAX / 16) return cudaErrorInvalidConfiguration;
+  d.tiles_p = (int32_t)ceil_div(P, width);
+  d.tiles_q = (int32_t)ceil_div(Q, q_tile);
+  d.matrix_tiles = (int32_t)matrix_tiles;
+  d.tiles = (int32_t)tiles;
+  // kind::f16: fp32 accumulator, the operands' type (0: f16, 1: bf16), which of them are MN-major.
+  d.idesc = 1u << 4 | (p.f16 ? 0u : 1u << 7 | 1u << 10) | (uint32_t)d.p_t << 15 | (uint32_t)d.q_t << 16 |
+            (uint32_t)(q_tile >> 3) << 17 | (uint32_t)(width >> 4) << 24;
+  CUtensorMap map_p, map_q, map_out{}, map_pre{}, map_residual{};
+  if (!make_map(&map_p, op, P, p.K, p.count, kP) || !make_map(&map_q, oq, Q, p.K, p.count, (uint32_t)q_staged))
+    return cudaErrorInvalidValue;
+  if (kind == kTiles && (!make_plane_map(&map_out, d.out, p.M, p.N, p.count) ||
+                         (d.pre.p && !make_plane_map(&map_pre, d.pre, p.M, p.N, p.count)) ||
+                         (d.residual.p && !make_plane_map(&map_residual, d.residual, p.M, p.N, p.count))))
+    return cudaErrorInvalidValue;
+  const Kernel kernel = kernel_of(form, kind);
+  if (form == kPair)
+    return launch(kernel, 2 * (tiles < info.pairs ? tiles : info.pairs), kPairThreads, kSmemBytes, stream, 2, map_p,
+                  map_q, map_out, map_pre, map_residual, d);
+  if (form == kSplit)
+    return launch(kernel, tiles * d.splits, kThreads, kSplitSmemBytes, stream, d.splits, map_p, map_q, map_out, map_pre,
+                  map_residual, d);
+  return launch(kernel, tiles < info.sms ? tiles : info.sms, kThreads, kSmemBytes, stream, 1, map_p, map_q, map_out,
+                map_pre, map_residual, d);
+}
+
 }  // namespace
 
 cudaError_t launch_product(const ProductParams &p, cudaStream_t stream) {
@@ -652,11 +1157,10 @@ cudaError_t launch_product(const ProductParams &p, cudaStream_t stream) {
   cudaError_t e = device_info(info);
   if (e != cudaSuccess) return e;
   ProductDev d{};
-  d.out = p.out;
-  d.residual = p.residual;
-  d.pre = p.pre;
-  d.bias = p.bias;
-  d.bias_type = p.bias_type;
+  d.out = plane_of(p, p.out);
+  d.residual = plane_of(p, p.residual);
+  d.pre = plane_of(p, p.pre);
+  d.bias = plane_of(p, Plane{const_cast<void *>(p.bias), 0, 0, p.bias_type});
   d.act = p.act;
   d.scale = p.scale;
   d.residual_scale = p.residual_scale;
@@ -665,9 +1169,6 @@ cudaError_t launch_product(const ProductParams &p, cudaStream_t stream) {
   d.withhold = take_withheld_launch();
   d.M = (int32_t)p.M;
   d.N = (int32_t)p.N;
-  d.p_t = p.b.t;
-  d.q_t = p.a.t;
-  d.symmetric = p.symmetric;
   d.many = p.count > 1;
   d.kblocks = (int32_t)ceil_div(p.K, kBK);
   // Segments only where the output has the bits to show them, and nothing of it is needed later.
@@ -679,58 +1180,34 @@ cudaError_t launch_product(const ProductParams &p, cudaStream_t stream) {
     d.segments = (int32_t)ceil_div(d.kblocks, d.seg_blocks);
     d.fold = in_place && d.segments > 1;
   }
+  // The tiles' epilogue wants rows on 16-byte boundaries (a row that repeats has none apart).
+  const auto moves = [&](const PlaneDev &x) { return !x.p || (x.vec && (p.M == 1 || x.stride >= p.N)); };
+  const bool rows = !p.symmetric && d.segments == 1 && p.M > 64 && moves(d.out) && moves(d.pre) && moves(d.residual);
+  const int64_t P = rows ? p.M : p.N, Q = rows ? p.N : p.M;
+  const int step = rows ? kUnit : 16;
   const double kb = d.kblocks;
-  const int q_single = (int)(p.M < kQMax ? ceil_div(p.M, 16) * 16 : kQMax);
-  const int64_t single_tiles = p.count * tiles_of(p, kP, q_single);
+  const int q_single = (int)(Q < kQMax ? ceil_div(Q, step) * step : kQMax);
+  const int64_t single_tiles = p.count * tiles_of(P, Q, kP, q_single, p.symmetric);
   const double single_us = ceil_div(single_tiles, info.sms) * (1.3 + 0.23 * kb);
   double pair_us = HUGE_VAL;
-  if (info.pairs > 0 && p.M > 128 && p.N > 128) {
-    for (int qt = kPairQMax; qt >= 128; qt -= 16) {
-      const int64_t waves = ceil_div(p.count * tiles_of(p, 2 * kP, qt), info.pairs);
+  if (info.pairs > 0 && P > 128) {
+    for (int qt = kPairQMax; qt >= 32; qt -= 32) {
+      const int64_t waves = ceil_div(p.count * tiles_of(P, Q, 2 * kP, qt, p.symmetric), info.pairs);
       const double us = 1.5 + waves * fmax(4.6 * qt / kPairQMax, 2.1 + fmax(0.2, 0.0013 * qt) * kb);
       if (us < pair_us) pair_us = us, d.q_tile = qt;
     }
   }
   double split_us = HUGE_VAL;
+  const int q_split = (int)(p.M < kQMax ? ceil_div(p.M, 16) * 16 : kQMax);
+  const int64_t split_tiles = p.count * tiles_of(p.N, p.M, kP, q_split, p.symmetric);
   for (int n = 4; n <= 8; n *= 2) {
-    if (n * single_tiles > 2 * info.sms || d.kblocks < n || ceil_div(d.kblocks, n) > kSegmentBlocks) continue;
-    const double us = 0.25 * kb / n + 2.4 + 0.02 * q_single + 0.00014 * q_single * n * single_tiles;
+    if (n * split_tiles > 2 * info.sms || d.kblocks < n || ceil_div(d.kblocks, n) > kSegmentBlocks) continue;
+    const double us = 0.25 * kb / n + 2.4 + 0.02 * q_split + 0.00014 * q_split * n * split_tiles;
     if (us < split_us) split_us = us, d.splits = n;
   }
-  const bool split = split_us < single_us && split_us < pair_us, pair = !split && pair_us < single_us;
-  if (!pair) d.q_tile = q_single;
-  const int q_staged = pair ? d.q_tile / 2 : d.q_tile;
-  d.q_rows = d.q_t ? (q_staged + 63) / 64 * 64 : q_staged;
-  const uint32_t budget = pair ? kPairStageBudget : split ? kSplitStageBudget : kStageBudget;
-  d.stages = (int32_t)(budget / (kPBytes + d.q_rows * 128));
-  if (d.stages > kMaxStages) d.stages = kMaxStages;
-  if (split) {  // a CTA's part of K is one segment
-    d.segments = 1;
-    d.seg_blocks = d.kblocks;
-    d.fold = false;
-  }
-  const int width = pair ? 2 * kP : kP;
-  const int64_t matrix_tiles = tiles_of(p, width, d.q_tile), tiles = matrix_tiles * p.count;
-  if (tiles > INT32_MAX / 16) return cudaErrorInvalidConfiguration;
-  d.tiles_p = (int32_t)ceil_div(p.N, width);
-  d.tiles_q = (int32_t)ceil_div(p.M, d.q_tile);
-  d.matrix_tiles = (int32_t)matrix_tiles;
-  d.tiles = (int32_t)tiles;
-  // kind::f16: fp32 accumulator, the operands' type (0: f16, 1: bf16), which of them are MN-major.
-  d.idesc = 1u << 4 | (p.f16 ? 0u : 1u << 7 | 1u << 10) | (uint32_t)d.p_t << 15 | (uint32_t)d.q_t << 16 |
-            (uint32_t)(d.q_tile >> 3) << 17 | (uint32_t)(width >> 4) << 24;
-  CUtensorMap map_p, map_q;
-  if (!make_map(&map_p, p.b, p.N, p.K, p.count, kP) ||
-      !make_map(&map_q, p.a, p.M, p.K, p.count, (uint32_t)q_staged))
-    return cudaErrorInvalidValue;
-  if (pair)
-    return launch(product_kernel<true, false>, 2 * (tiles < info.pairs ? tiles : info.pairs), kPairThreads,
-                  kPairSmemBytes, stream, 2, map_p, map_q, d);
-  if (split)
-    return launch(product_kernel<false, true>, tiles * d.splits, kThreads, kSplitSmemBytes, stream, d.splits,
-                  map_p, map_q, d);
-  return launch(product_kernel<false, false>, tiles < info.sms ? tiles : info.sms, kThreads, kSmemBytes, stream, 1,
-                map_p, map_q, d);
+  const int form = split_us < single_us && split_us < pair_us ? kSplit : pair_us < single_us ? kPair : kSingle;
+  return launch_form(p, d, form, form != kSplit && rows, form == kSplit ? q_split : form == kPair ? d.q_tile : q_single,
+                     info, stream);
 }
 
 }  // namespace engram
