@@ -996,16 +996,15 @@ def _plane(t, shape, name):
     """(pointer, dtype, row stride) of a bf16 or fp32 [M, N] tensor, (None, 0, 0) for none."""
     if t is None:
         return None, 0, 0
-    code = _dtype(t, name)
     if t.shape != shape:
         raise EngramError(ERR_INVALID_ARG, f"{name} must be {list(shape)}")
-    return t.data_ptr(), code, _strides(t, name)[0]
+    return t.data_ptr(), _dtype(t, name), _strides(t, name)[0]
 
 
 def _one_device(stream, first, *others):
     """Every tensor of a call is on one device: the current one, where no stream says another."""
     dev = first.get_device()
-    for t in others:
+    for t in others:  # those that the call has
         if t is not None and t.get_device() != dev:
             raise EngramError(ERR_INVALID_ARG, "the tensors of a call must be on one device")
     if stream is None:
@@ -1015,8 +1014,8 @@ def _one_device(stream, first, *others):
 
 
 def _activation(activation):
-    if activation not in (ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU):
-        raise EngramError(ERR_INVALID_ARG, f"unknown activation {activation}")
+    if activation.__class__ is not int:
+        raise EngramError(ERR_INVALID_ARG, "activation must be one of the ACT_* numbers")
     return activation
 
 
@@ -1059,12 +1058,16 @@ def engram_matmul(a, b, bias=None, activation: int = ACT_NONE, residual=None, sc
         if bias.shape != (N,) or not bias.is_contiguous():
             raise EngramError(ERR_INVALID_ARG, f"bias must be contiguous {[N]}")
     _one_device(stream, a, b, out, bias, residual, pre, workspace, status)
-    ws, ws_bytes, workspace = _scratch(
-        workspace, lib.engram_matmul_workspace_bytes(*pa, *pb, M, N, K), a, stream)
-    _check(lib.engram_matmul(*pa, *pb, M, N, K, scale, bias_ptr, bias_dtype, _activation(activation),
+    ws, ws_bytes = None, 0
+    if workspace is not None or (pa[0] | pb[0]) & 15 or (pa[1] | pb[1]) & 7:  # else it needs none
+        ws, ws_bytes, workspace = _scratch(
+            workspace, lib.engram_matmul_workspace_bytes(*pa, *pb, M, N, K), a, stream)
+    code = lib.engram_matmul(*pa, *pb, M, N, K, scale, bias_ptr, bias_dtype, _activation(activation),
                              *_plane(residual, shape, "residual"), *_plane(pre, shape, "pre"),
                              *_plane(out, shape, "out"), ws, ws_bytes, _ptr(status),
-                             _stream(stream)), "engram_matmul")
+                             _stream(stream))
+    if code:
+        _check(code, "engram_matmul")
     return out
 
 
@@ -1087,7 +1090,7 @@ def engram_matmul_grad(dy, a, b, pre=None, activation: int = ACT_NONE, scale: fl
         raise EngramError(ERR_INVALID_ARG, "a must be [M, K] and b [N, K] for dy [M, N]")
     if accumulate and ((grad_b and db is None) or (grad_bias and dbias is None)):
         raise EngramError(ERR_INVALID_ARG, "accumulate needs gradients to add to")
-    if _activation(activation) != ACT_NONE and pre is None:
+    if activation != ACT_NONE and pre is None:
         raise EngramError(ERR_INVALID_ARG, "the gradient of an activation needs pre")
     dev = dy.device
     if not grad_a:
@@ -1108,9 +1111,9 @@ def engram_matmul_grad(dy, a, b, pre=None, activation: int = ACT_NONE, scale: fl
     _one_device(stream, dy, a, b, pre, da, db, dbias, workspace, status)
     args = (dy.data_ptr(), dd, _strides(dy, "dy")[0], *pa, *pb, M, N, K)
     ws, ws_bytes, workspace = _scratch(
-        workspace, lib.engram_matmul_grad_workspace_bytes(*args, activation, grad_a, grad_b, grad_bias),
+        workspace, lib.engram_matmul_grad_workspace_bytes(*args, _activation(activation), grad_a, grad_b, grad_bias),
         dy, stream)
-    _check(lib.engram_matmul_grad(*args, scale, *_plane(pre, shape, "pre"), activation, accumulate,
+    _check(lib.engram_matmul_grad(*args, scale, *_plane(pre, shape, "pre"), _activation(activation), accumulate,
                                   *_plane(da, (M, K), "da"), *_plane(db, (N, K), "db"), _ptr(dbias),
                                   ws, ws_bytes, _ptr(status), _stream(stream)), "engram_matmul_grad")
     return da, db, dbias

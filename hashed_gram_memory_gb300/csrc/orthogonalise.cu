@@ -18,7 +18,7 @@ namespace engram {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxParts = 512;  // blocks a matrix
+constexpr int kMaxParts = 8 * kSms;  // blocks a matrix
 constexpr float kHeld = 256.f;  // what fp16 values are held times
 
 struct StartDev {
@@ -26,20 +26,56 @@ struct StartDev {
   __half *x;
   int64_t x_stride, x_batch;
   float *partial;  // [count][parts]: sums of squares
-  int32_t M, N, parts;
+  int32_t M, N, parts, lanes;  // lanes: threads a row, a power of two
   float beta, eps;
   bool nesterov;
 };
 
-// u of one element; with `first` the momentum moves.
-template <typename T>
-__device__ __forceinline__ float update_of(const StartDev &p, int64_t z, int64_t m, int64_t n, bool first) {
-  const float g = to_float(static_cast<const T *>(p.g.p)[z * p.g.batch + m * p.g.stride + n]);
-  if (!p.momentum.p) return g;
+// VEC values of a row; with VEC 4 they are one word of 8 or 16 bytes.
+template <int VEC, typename T>
+__device__ __forceinline__ void load_values(const T *at, float (&x)[VEC]) {
+  if constexpr (VEC == 1) {
+    x[0] = to_float(*at);
+  } else if constexpr (sizeof(T) == 4) {
+    const float4 v = *reinterpret_cast<const float4 *>(at);
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2 *>(at);
+    x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xffff0000u);
+    x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xffff0000u);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void store_values(float *at, const float (&x)[VEC]) {
+  if constexpr (VEC == 1)
+    *at = x[0];
+  else
+    *reinterpret_cast<float4 *>(at) = make_float4(x[0], x[1], x[2], x[3]);
+}
+
+// u of VEC elements; with FIRST the momentum moves.
+template <int VEC, typename T, bool FIRST>
+__device__ __forceinline__ void update_of(const StartDev &p, int64_t z, int64_t m, int64_t n, float (&u)[VEC]) {
+  load_values<VEC>(static_cast<const T *>(p.g.p) + z * p.g.batch + m * p.g.stride + n, u);
+  if (!p.momentum.p) return;
   float *at = static_cast<float *>(p.momentum.p) + z * p.momentum.batch + m * p.momentum.stride + n;
-  float v = *at;
-  if (first) *at = v = fmaf(p.beta, v, g);
-  return p.nesterov ? fmaf(p.beta, v, g) : v;
+  float v[VEC];
+  load_values<VEC>(at, v);
+  if (FIRST) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = fmaf(p.beta, v[i], u[i]);
+    store_values<VEC>(at, v);
+  }
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) u[i] = p.nesterov ? fmaf(p.beta, v[i], u[i]) : v[i];
+}
+
+// f(row, column) for a block's share of a matrix in steps of VEC columns: `lanes` threads a row.
+template <int VEC, typename F>
+__device__ __forceinline__ void over_share(const StartDev &p, int part, F f) {
+  const int lanes = p.lanes, rows = kThreads / lanes;
+  for (int m = part * rows + threadIdx.x / lanes; m < p.M; m += p.parts * rows)
+    for (int n = (threadIdx.x & (lanes - 1)) * VEC; n < p.N; n += lanes * VEC) f(m, n);
 }
 
 __device__ __forceinline__ float block_sum(float v) {
@@ -54,23 +90,24 @@ __device__ __forceinline__ float block_sum(float v) {
 }
 
 // The momentum step and each block's sum of squares of u.
-template <typename T>
+template <int VEC, typename T>
 __global__ void __launch_bounds__(kThreads) momentum_kernel(const StartDev p) {
   dependency_wait();
   const int64_t z = blockIdx.x / p.parts;
   const int part = blockIdx.x - (int)z * p.parts;
   float sum = 0.f;
-  for (int m = part; m < p.M; m += p.parts)
-    for (int n = threadIdx.x; n < p.N; n += kThreads) {
-      const float u = update_of<T>(p, z, m, n, true);
-      sum = fmaf(u, u, sum);
-    }
+  over_share<VEC>(p, part, [&](int m, int n) {
+    float u[VEC];
+    update_of<VEC, T, true>(p, z, m, n, u);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) sum = fmaf(u[i], u[i], sum);
+  });
   sum = block_sum(sum);
   if (threadIdx.x == 0) p.partial[blockIdx.x] = sum;
 }
 
 // X = u / (|u| + eps), held in fp16.
-template <typename T>
+template <int VEC, typename T>
 __global__ void __launch_bounds__(kThreads) normalise_kernel(const StartDev p) {
   dependency_wait();
   const int64_t z = blockIdx.x / p.parts;
@@ -78,9 +115,23 @@ __global__ void __launch_bounds__(kThreads) normalise_kernel(const StartDev p) {
   float sum = 0.f;
   for (int i = threadIdx.x; i < p.parts; i += kThreads) sum += p.partial[z * p.parts + i];
   const float by = kHeld / (sqrtf(block_sum(sum)) + p.eps);
-  for (int m = part; m < p.M; m += p.parts)
-    for (int n = threadIdx.x; n < p.N; n += kThreads)
-      p.x[z * p.x_batch + m * p.x_stride + n] = __float2half_rn(update_of<T>(p, z, m, n, false) * by);
+  over_share<VEC>(p, part, [&](int m, int n) {
+    float u[VEC];
+    update_of<VEC, T, false>(p, z, m, n, u);
+    __half *at = p.x + z * p.x_batch + (int64_t)m * p.x_stride + n;
+    if constexpr (VEC == 1) {
+      *at = __float2half_rn(u[0] * by);
+    } else {
+      __half2 v[2] = {__floats2half2_rn(u[0] * by, u[1] * by), __floats2half2_rn(u[2] * by, u[3] * by)};
+      *reinterpret_cast<uint2 *>(at) = make_uint2(*reinterpret_cast<uint32_t *>(v), *reinterpret_cast<uint32_t *>(v + 1));
+    }
+  });
+}
+
+// Rows of words of four values.
+bool words(const Plane &x, int64_t count) {
+  const uintptr_t bytes = x.type == ENGRAM_DTYPE_F32 ? 16 : 8;
+  return !x.p || (((uintptr_t)x.p & (bytes - 1)) == 0 && x.stride % 4 == 0 && (count == 1 || x.batch % 4 == 0));
 }
 
 int64_t padded(int64_t n) { return (n + 63) / 64 * 64; }
@@ -128,16 +179,23 @@ cudaError_t launch_orthogonalise(const OrthogonaliseParams &p, void *workspace, 
   s.beta = p.beta;
   s.eps = p.eps;
   s.nesterov = p.nesterov;
+  const bool wide = p.N % 4 == 0 && words(p.g, p.count) && words(p.momentum, p.count);
+  s.lanes = 1;
+  while (s.lanes < kThreads && s.lanes * (wide ? 4 : 1) < p.N) s.lanes *= 2;
+  // About eight blocks an SM.
+  const int64_t rows = kThreads / s.lanes, most = (p.M + rows - 1) / rows;
   int64_t parts = (8 * kSms + p.count - 1) / p.count;
-  if (parts > p.M) parts = p.M;
+  if (parts > most) parts = most;
   if (parts > kMaxParts) parts = kMaxParts;
   s.parts = (int32_t)parts;
-  const bool f32 = p.g.type == ENGRAM_DTYPE_F32;
-  cudaError_t e = launch(f32 ? momentum_kernel<float> : momentum_kernel<__nv_bfloat16>, parts * p.count, kThreads, 0,
-                         stream, 1, s);
-  if (e == cudaSuccess)
-    e = launch(f32 ? normalise_kernel<float> : normalise_kernel<__nv_bfloat16>, parts * p.count, kThreads, 0, stream,
-               1, s);
+  using Start = void (*)(StartDev);
+  static constexpr Start first[4] = {momentum_kernel<1, __nv_bfloat16>, momentum_kernel<1, float>,
+                                     momentum_kernel<4, __nv_bfloat16>, momentum_kernel<4, float>};
+  static constexpr Start second[4] = {normalise_kernel<1, __nv_bfloat16>, normalise_kernel<1, float>,
+                                      normalise_kernel<4, __nv_bfloat16>, normalise_kernel<4, float>};
+  const int which = 2 * wide + (p.g.type == ENGRAM_DTYPE_F32);
+  cudaError_t e = launch(first[which], parts * p.count, kThreads, 0, stream, 1, s);
+  if (e == cudaSuccess) e = launch(second[which], parts * p.count, kThreads, 0, stream, 1, s);
   const bool tall = p.M > p.N;
   const int64_t r = tall ? p.N : p.M, w = tall ? p.M : p.N;
   const Plane none{nullptr, 0, 0, ENGRAM_DTYPE_BF16};

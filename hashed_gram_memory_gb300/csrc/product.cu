@@ -504,11 +504,12 @@ __device__ __forceinline__ void move_tiles(const ProductDev &p, const CUtensorMa
     put_row(at, lane, p.out.type, x);
     send(map_out, at);
   }
-  // What is on its way has arrived before the block exits.
+  // What is on its way into shared memory has arrived, and what leaves it has been read, before
+  // the block exits.
   if (lane == 0) {
     for (; used < asked; ++used)
       drain_phase(arrived + used % (uint32_t)p.ahead, (used / (uint32_t)p.ahead) & 1, p.wait_limit_ns);
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   }
   __syncwarp();
 }
