@@ -15,8 +15,9 @@
 //     those leave SMs idle (a few rows of a: reading b is the work), 4 or 8 CTAs of a cluster
 //     share a tile, each with a part of K, and add their parts through distributed shared memory
 //     in rank order, two such CTAs an SM.
-// Warps: 0 TMA producer (a ring of stages of 64 of K, 128-byte swizzle); 1 allocates TMEM, one
-// thread (of the pair's even CTA) issues the MMAs into one of two accumulators; 4.. epilogue.
+// Warps: 0 and 2 TMA producers, of P and of Q (a ring of stages of 64 of K, 128-byte swizzle); 1
+// allocates TMEM, one thread (of the pair's even CTA) issues the MMAs into one of two accumulators;
+// 4.. epilogue.
 //
 // The fp32 accumulator of the tensor cores does not round to nearest: its error grows with the
 // number of additions.  For fp32 outputs K is cut into segments of at most 8192 that each start
@@ -45,8 +46,8 @@ constexpr int kP = 128;         // rows of the P operand a CTA stages
 constexpr int kBK = 64;         // of K a stage: 128 bytes
 constexpr int kQMax = 128;      // most rows of the Q operand a tile of one CTA
 constexpr int kPairQMax = 256;  // and of a pair
-// Epilogue warps: one of each quarter of the lanes for each part of a tile's columns; warps 2 and
-// 3 idle, as the epilogue's start at a multiple of 4.
+// Epilogue warps: one of each quarter of the lanes for each part of a tile's columns; warp 3 idles,
+// as the epilogue's start at a multiple of 4.
 constexpr int kParts = 2, kPairParts = 3;
 constexpr int kThreads = 128 * (1 + kParts), kPairThreads = 128 * (1 + kPairParts);
 constexpr int kSegmentBlocks = 128;
@@ -80,16 +81,30 @@ struct ProductDev {
   float scale, residual_scale;
   int32_t act;
   int32_t kblocks, q_tile, q_rows, stages;  // q_rows: rows of Q that a CTA stages
-  int32_t segments, seg_blocks, splits;
+  int32_t segments, seg_blocks;
   int32_t tiles_p, tiles_q, tiles, matrix_tiles;
   uint32_t idesc;
   // the tiles' epilogue: of each warp, buffers for units of the residual ahead (ahead of them,
   // ahead_bytes each) and for units on their way out (slots of them, slot_bytes each)
   int32_t ahead, slots;
   uint32_t ahead_bytes, slot_bytes;
+  // which CTAs (or pairs) take which tiles: see Walk
+  int32_t shift, extra;
   bool p_t, q_t, many;
+  bool rows;      // rows of out in the lanes (kTiles); else its columns
   bool fold;      // the residual goes into the first segment's sum (it lies where out does)
   bool withhold;  // test hook: the first stage waits for bytes that never come
+};
+
+// One product, or two that share a launch.
+struct Job {
+  CUtensorMap p, q, out, pre, residual;
+  ProductDev d;
+};
+struct Jobs {
+  Job job[2];
+  int32_t count, stages, splits;
+  uint32_t stage_bytes;
 };
 
 // Shared-memory descriptor of an operand tile, 128-byte swizzle.  K-major: rows of 64 of K,
@@ -148,17 +163,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
-// The rows from r0 on of one operand, 64 of K from k on, into a stage.
-template <bool PAIR>
-__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap *map, bool t, int r0, int rows,
-                                             int k, int z, uint32_t bar) {
-  if (t) {
-    for (int r = 0; r < rows; r += 64) tma_load_3d<PAIR>(dst + r * 128, map, r0 + r, k, z, bar);
-  } else {
-    tma_load_3d<PAIR>(dst, map, k, r0, z, bar);
-  }
-}
-
 // The whole warp waits; the same answer in every lane.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
                                           const ProductDev &p) {
@@ -168,9 +172,9 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
 struct Tile {
   int p0, q0, z;
 };
-// Tiles in groups of up to 16 along P, Q's tiles inside a group in order: what the resident
-// CTAs read at one time is a few slices of each operand.  Of a symmetric product those that
-// hold any output (m, n) with n <= m.
+// Tiles in groups of up to 16 along out's columns, inside a group row by row: the resident CTAs
+// read a few slices of a at a time, once, and a group of slices of b that stays in L2.  Of a
+// symmetric product those that hold any output (m, n) with n <= m.
 template <int WIDTH, bool SYMMETRIC>
 __device__ __forceinline__ Tile tile_at(const ProductDev &p, int tile) {
   Tile r{0, 0, 0};
@@ -188,14 +192,39 @@ __device__ __forceinline__ Tile tile_at(const ProductDev &p, int tile) {
     }
     tp = t;
   } else {
-    const uint32_t per = 16u * p.tiles_q, g = t / per, in = t - g * per;
-    const uint32_t wide = min(16u, p.tiles_p - g * 16u);
-    tq = in / wide;
-    tp = g * 16 + in - tq * wide;
+    const uint32_t columns = p.rows ? p.tiles_q : p.tiles_p, rows = p.rows ? p.tiles_p : p.tiles_q;
+    const uint32_t per = 16u * rows, g = t / per, in = t - g * per;
+    const uint32_t wide = min(16u, columns - g * 16u), row = in / wide, column = g * 16 + in - row * wide;
+    tp = p.rows ? row : column, tq = p.rows ? column : row;
   }
   r.p0 = (int)tp * WIDTH, r.q0 = (int)tq * p.q_tile;
   return r;
 }
+
+// The tiles of worker w of `workers` (CTAs or pairs).  One after the other in steps of `workers`;
+// but of a second product the workers from `shift` on, which had a tile less of the first, take
+// `extra` more each before that, and the others come last.
+struct Walk {
+  int tile, left, step, rest, lights;
+
+  __device__ __forceinline__ Walk(const ProductDev &p, int w, int workers) {
+    lights = workers - p.shift;
+    step = workers;
+    const int turn = w >= p.shift ? w - p.shift : w + lights;
+    rest = p.extra * lights + turn;
+    left = w >= p.shift ? p.extra : 0;
+    tile = left ? turn : rest;
+  }
+  __device__ __forceinline__ void next() {
+    if (left > 1)
+      tile += lights;
+    else if (left == 1)
+      tile = rest;
+    else
+      tile += step;
+    if (left) --left;
+  }
+};
 
 // ---- epilogue ---------------------------------------------------------------------------
 
@@ -207,7 +236,6 @@ __device__ __forceinline__ Tile tile_at(const ProductDev &p, int tile) {
 //   kSingles: the lanes of TMEM are columns of out.  A warp moves 32 neighbouring values of a row at
 //     a time: any strides, few rows, sums in segments.
 //   kSymmetric: as kSingles, for a symmetric product.
-// One of them to a kernel: code of all would not stay in the instruction cache.
 enum Epilogue { kTiles, kSingles, kSymmetric };
 
 // f(a null pointer of the C++ type of `type`).
@@ -367,54 +395,69 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&v)[32]) {
 
 // What a warp moves of its CTA's tiles, unit by unit (32 rows x 32 columns): units [first, end) of
 // each tile, `row0` rows into it.  Units that lie outside out are passed over.
+template <int WIDTH>
 struct Units {
-  int tile, step, unit, first, end, row0;
+  Walk walk;
+  int unit, first, end, row0;
   Tile at;
 
-  template <int WIDTH>
-  __device__ __forceinline__ void start(const ProductDev &p, int tile_, int step_, int first_, int end_, int row0_) {
-    tile = tile_, step = step_, first = unit = first_, end = end_, row0 = row0_;
-    if (first == end) tile = p.tiles;
-    if (tile < p.tiles) at = tile_at<WIDTH, false>(p, tile);
+  __device__ __forceinline__ Units(const ProductDev &p, const Walk &w, int first_, int end_, int row0_)
+      : walk(w), unit(first_), first(first_), end(end_), row0(row0_) {
+    if (walk.tile < p.tiles) at = tile_at<WIDTH, false>(p, walk.tile);
   }
-  __device__ __forceinline__ bool done(const ProductDev &p) const { return tile >= p.tiles; }
+  __device__ __forceinline__ bool done(const ProductDev &p) const { return walk.tile >= p.tiles; }
   __device__ __forceinline__ int n() const { return at.q0 + unit * kUnit; }
   __device__ __forceinline__ int m() const { return at.p0 + row0; }
   __device__ __forceinline__ bool inside(const ProductDev &p) const { return n() < p.N && m() < p.M; }
-  template <int WIDTH>
   __device__ __forceinline__ void next(const ProductDev &p) {
     if (++unit < end) return;
     unit = first;
-    tile += step;
-    if (tile < p.tiles) at = tile_at<WIDTH, false>(p, tile);
+    walk.next();
+    if (walk.tile < p.tiles) at = tile_at<WIDTH, false>(p, walk.tile);
   }
 };
 
-// A warp's share of the epilogue of all of its CTA's tiles.  `buffers`: its shared memory; `arrived`:
-// its barriers, one a residual buffer.
+// An epilogue warp's place in what it shares with the rest of its CTA.
+struct Shared {
+  uint32_t buffers;           // its shared memory
+  uint64_t *arrived;          // its barriers, one a residual buffer
+  uint64_t *acc_full;
+  uint32_t tmem;              // its quarter of the lanes
+  int lane, row0;             // row0: its first lane, of the tile
+  volatile int *abort_flag;
+  uint32_t unit, phases;      // accumulators drained so far; the parities of `arrived`
+};
+
+// A warp's share of the epilogue of all of its CTA's tiles: units [first, end) of each.
 template <bool PAIR, typename F>
-__device__ __forceinline__ void move_tiles(const ProductDev &p, const CUtensorMap *map_out, const CUtensorMap *map_pre,
-                                           const CUtensorMap *map_residual, uint32_t buffers, uint64_t *arrived,
-                                           uint64_t *acc_full, uint32_t quad_tmem, int first_tile, int tile_step,
-                                           int first, int end, int row0, int lane, volatile int *abort_flag,
-                                           F release) {
+__device__ __forceinline__ bool move_tiles(const Job &job, const Walk &walk, Shared &w, int first, int end, F release) {
   constexpr int kWidth = PAIR ? 2 * kP : kP, kAccCols = PAIR ? kPairQMax : kQMax;
-  const uint32_t slots = buffers + p.ahead * p.ahead_bytes;
-  Units ahead, now;
-  ahead.start<kWidth>(p, first_tile, tile_step, first, end, row0);
-  uint32_t asked = 0, used = 0, slot = 0;
+  const ProductDev &p = job.d;
+  const int lane = w.lane;
+  if (first == end) {  // a narrow tile has nothing for this part
+    for (Walk k = walk; k.tile < p.tiles; k.next()) {
+      const uint32_t acc = w.unit & 1;
+      if (!warp_wait(w.acc_full + acc, (w.unit >> 1) & 1, w.abort_flag, p)) return false;
+      release(acc);
+      ++w.unit;
+    }
+    return true;
+  }
+  const uint32_t slots = w.buffers + p.ahead * p.ahead_bytes;
+  Units<kWidth> ahead(p, walk, first, end, w.row0), now = ahead;
+  int asked = 0, used = 0, slot = 0, waiting = 0;
   // The residual of the next unit that has not been asked for.
   const auto ask = [&] {
-    while (!ahead.done(p) && !ahead.inside(p)) ahead.next<kWidth>(p);
+    while (!ahead.done(p) && !ahead.inside(p)) ahead.next(p);
     if (ahead.done(p)) return;
-    const uint32_t b = asked % (uint32_t)p.ahead;
     if (lane == 0) {
-      mbar_arrive_expect_tx(arrived + b, p.ahead_bytes);
-      tma_load_3d<false>(buffers + b * p.ahead_bytes, map_residual, ahead.n(), ahead.m(), ahead.at.z,
-                         smem_u32(arrived + b));
+      mbar_arrive_expect_tx(w.arrived + asked, p.ahead_bytes);
+      tma_load_3d<false>(w.buffers + asked * p.ahead_bytes, &job.residual, ahead.n(), ahead.m(), ahead.at.z,
+                         smem_u32(w.arrived + asked));
     }
-    ++asked;
-    ahead.next<kWidth>(p);
+    asked = asked + 1 == p.ahead ? 0 : asked + 1;
+    ++waiting;
+    ahead.next(p);
   };
   // A free buffer: of the stores before, all but slots - 1 have been read.
   const auto free_slot = [&] {
@@ -426,7 +469,7 @@ __device__ __forceinline__ void move_tiles(const ProductDev &p, const CUtensorMa
     }
     __syncwarp();
     const uint32_t at = slots + slot * p.slot_bytes;
-    slot = slot + 1 == (uint32_t)p.slots ? 0 : slot + 1;
+    slot = slot + 1 == p.slots ? 0 : slot + 1;
     return at;
   };
   const auto send = [&](const CUtensorMap *map, uint32_t from) {
@@ -434,23 +477,20 @@ __device__ __forceinline__ void move_tiles(const ProductDev &p, const CUtensorMa
     __syncwarp();
     if (lane == 0) tma_store_3d(map, from, now.n(), now.m(), now.at.z);
   };
-  if (p.ahead)
-    for (int i = 0; i < p.ahead; ++i) ask();
+  for (int i = 0; i < p.ahead; ++i) ask();
   bool ok = true;
-  uint32_t local = 0;
-  now.start<kWidth>(p, first_tile, tile_step, first, end, row0);
-  for (; ok && !now.done(p); now.next<kWidth>(p)) {
-    const uint32_t acc = local & 1;
+  for (; !now.done(p); now.next(p)) {
+    const uint32_t acc = w.unit & 1;
     if (now.unit == first) {
-      if (!(ok = warp_wait(acc_full + acc, (local >> 1) & 1, abort_flag, p))) break;
+      if (!(ok = warp_wait(w.acc_full + acc, (w.unit >> 1) & 1, w.abort_flag, p))) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     }
     uint32_t v[kUnit];
     __syncwarp();
-    tmem_ld32(quad_tmem + acc * kAccCols + now.unit * kUnit, v);
+    tmem_ld32(w.tmem + acc * kAccCols + now.unit * kUnit, v);
     if (now.unit == end - 1) {
       release(acc);
-      ++local;
+      ++w.unit;
     }
     if (!now.inside(p)) continue;
     float x[kUnit];
@@ -471,11 +511,11 @@ __device__ __forceinline__ void move_tiles(const ProductDev &p, const CUtensorMa
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint4 b = __ldg(at + j);
-            const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+            const uint32_t words[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              x[8 * j + 2 * i] += __uint_as_float(w[i] << 16);
-              x[8 * j + 2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
+              x[8 * j + 2 * i] += __uint_as_float(words[i] << 16);
+              x[8 * j + 2 * i + 1] += __uint_as_float(words[i] & 0xffff0000u);
             }
           }
         }
@@ -489,29 +529,33 @@ __device__ __forceinline__ void move_tiles(const ProductDev &p, const CUtensorMa
     if (p.pre.p) {
       const uint32_t at = free_slot();
       put_row(at, lane, p.pre.type, x);
-      send(map_pre, at);
+      send(&job.pre, at);
     }
     activate(x, p.act);
     if (p.ahead) {
-      const uint32_t b = used % (uint32_t)p.ahead;
-      if (!(ok = warp_wait(arrived + b, (used / (uint32_t)p.ahead) & 1, abort_flag, p))) break;
-      ++used;
-      add_row(buffers + b * p.ahead_bytes, lane, p.residual.type, p.residual_scale, x);
+      if (!(ok = warp_wait(w.arrived + used, (w.phases >> used) & 1, w.abort_flag, p))) break;
+      w.phases ^= 1u << used;
+      add_row(w.buffers + used * p.ahead_bytes, lane, p.residual.type, p.residual_scale, x);
+      used = used + 1 == p.ahead ? 0 : used + 1;
+      --waiting;
       __syncwarp();
       ask();
     }
     const uint32_t at = free_slot();
     put_row(at, lane, p.out.type, x);
-    send(map_out, at);
+    send(&job.out, at);
   }
   // What is on its way into shared memory has arrived, and what leaves it has been read, before
-  // the block exits.
+  // the buffers serve anything else and before the block exits.
   if (lane == 0) {
-    for (; used < asked; ++used)
-      drain_phase(arrived + used % (uint32_t)p.ahead, (used / (uint32_t)p.ahead) & 1, p.wait_limit_ns);
+    for (; waiting > 0; --waiting) {  // after a wait that gave up
+      drain_phase(w.arrived + used, (w.phases >> used) & 1, p.wait_limit_ns);
+      used = used + 1 == p.ahead ? 0 : used + 1;
+    }
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   }
   __syncwarp();
+  return ok;
 }
 
 // A warp's part of an accumulator: 32 lanes (columns n0, n0 + 1, .. of out), `chunks` times 16 of
@@ -696,17 +740,14 @@ __device__ __forceinline__ void finish_one(const ProductDev &p, int64_t z, int64
 // arrival that expects both CTAs' bytes; empty, acc_full and mma_done exist in both and take the
 // leader's multicast commits; acc_empty lives in the leader and takes an arrival from every
 // epilogue warp of the pair.
-template <bool PAIR, bool SPLIT, int KIND>
+template <bool PAIR, bool SPLIT, bool SYMMETRIC>
 __global__ void __launch_bounds__(PAIR ? kPairThreads : kThreads, SPLIT ? 2 : 1)
-    product_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
-                   const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_pre,
-                   const __grid_constant__ CUtensorMap map_residual, const __grid_constant__ ProductDev p) {
-  static_assert(!(PAIR && SPLIT) && !(SPLIT && KIND == kTiles));
+    product_kernel(const __grid_constant__ Jobs jobs) {
+  static_assert(!(PAIR && SPLIT));
   constexpr uint32_t kCols = SPLIT ? kSplitTmemCols : kTmemCols;
   constexpr int kAccCols = PAIR ? kPairQMax : kQMax;
   constexpr int kTileP = PAIR ? 2 * kP : kP;
   constexpr int kPartsHere = PAIR ? kPairParts : kParts;
-  constexpr bool kSym = KIND == kSymmetric;
   extern __shared__ uint8_t sm_raw[];
   // Barriers, stages, the epilogue's buffers.
   uint8_t *base = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023), *sm = base + kBarBytes;
@@ -720,14 +761,20 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : kThreads, SPLIT ? 2 : 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int stages = p.stages, qt = p.q_tile;
-  const uint32_t stage_bytes = kPBytes + (uint32_t)p.q_rows * 128;
+  const int stages = jobs.stages, splits = jobs.splits;
+  const uint32_t stage_bytes = jobs.stage_bytes;
   const uint32_t rank = PAIR || SPLIT ? cluster_rank() : 0;
-  // This CTA's blocks of K (from kb_first on) and its tiles.
-  const int kb_first = SPLIT ? (int)((int64_t)p.kblocks * rank / p.splits) : 0;
-  const int kblocks = SPLIT ? (int)((int64_t)p.kblocks * (rank + 1) / p.splits) - kb_first : p.kblocks;
-  const int share = PAIR ? 2 : SPLIT ? p.splits : 1;  // CTAs a tile
-  const int first_tile = blockIdx.x / share, tile_step = gridDim.x / share;
+  const int share = PAIR ? 2 : SPLIT ? splits : 1;  // CTAs a tile
+  const int worker = blockIdx.x / share, workers = gridDim.x / share;
+  // Two products have their code each: what they read of their parameters stays constant operands.
+  constexpr bool kTwo = !SPLIT && !SYMMETRIC;
+  // This CTA's blocks of K of a product.
+  const auto first_block = [&](const ProductDev &p) {
+    return SPLIT ? (int)((int64_t)p.kblocks * rank / splits) : 0;
+  };
+  const auto blocks = [&](const ProductDev &p) {
+    return SPLIT ? (int)((int64_t)p.kblocks * (rank + 1) / splits) - first_block(p) : p.kblocks;
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
@@ -739,20 +786,18 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : kThreads, SPLIT ? 2 : 1)
       mbar_init(acc_empty + a, (PAIR ? 2 : 1) * 4 * kPartsHere);
     }
     mbar_init(mma_done, 1);
-    if (KIND == kTiles)
-      for (int i = 0; i < 4 * kPartsHere * kMaxAhead; ++i) mbar_init(arrived + i, 1);
-    if (p.withhold) mbar_expect_tx(full, 16);
+    for (int i = 0; i < 4 * kPartsHere * kMaxAhead; ++i) mbar_init(arrived + i, 1);
+    if (jobs.job[0].d.withhold) mbar_expect_tx(full, 16);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (threadIdx.x == 64) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_p)) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_q)) : "memory");
-    if (KIND == kTiles) {
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_out)) : "memory");
-      if (p.ahead)
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_residual)) : "memory");
-    }
+  if (threadIdx.x >= 96 && threadIdx.x < 96 + jobs.count) {
+    const Job &job = jobs.job[threadIdx.x - 96];
+    const CUtensorMap *maps[4] = {&job.p, &job.q, job.d.rows ? &job.out : nullptr,
+                                  job.d.rows && job.d.ahead ? &job.residual : nullptr};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (maps[i]) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(maps[i])) : "memory");
   }
   if (warp == 1) {
     if constexpr (PAIR) {
@@ -778,32 +823,51 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : kThreads, SPLIT ? 2 : 1)
   const uint32_t tmem = *tmem_slot;
   dependency_wait();
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 2) {
     if (lane == 0) {
-      // -------------------------------------------------------- TMA producer
+      // ----------------------------- TMA producers: warp 0 of P, warp 2 of Q
+      // Two threads, as one could not issue the four copies that a stage of rows along K takes, a
+      // pair's stage of 256 x 256 being worked off in 270 ns.
+      const bool of_p = warp == 0;
       const uint32_t full_at = PAIR ? map_to_rank(smem_u32(full), 0) : smem_u32(full);
+      const int64_t limit = jobs.job[0].d.wait_limit_ns;
+      const uint32_t begin = smem_u32(sm) + (of_p ? 0 : kPBytes);
       uint32_t it = 0;
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int tile = first_tile; ok && tile < p.tiles; tile += tile_step) {
-        Tile t = tile_at<kTileP, kSym>(p, tile);
-        if constexpr (PAIR) t.p0 += rank * kP, t.q0 += rank * (qt / 2);
-        for (int kb = 0; kb < kblocks; ++kb, ++it) {
-          if (!(ok = wait_phase(empty + s, ph ^ 1, abort_flag, p.wait_limit_ns, p.status))) break;
-          const uint32_t st = smem_u32(sm) + s * stage_bytes, bar = full_at + 8u * s;
-          if (rank == 0 || !PAIR) mbar_arrive_expect_tx(full + s, (PAIR ? 2 : 1) * stage_bytes);
-          const int k = (kb_first + kb) * kBK;
-          load_operand<PAIR>(st, &map_p, p.p_t, t.p0, kP, k, t.z, bar);
-          load_operand<PAIR>(st + kPBytes, &map_q, p.q_t, t.q0, p.q_rows, k, t.z, bar);
-          if (++s == stages) s = 0, ph ^= 1;
+      const auto produce = [&](const Job &job) {
+        const ProductDev &p = job.d;
+        const int kb_first = first_block(p), kblocks = blocks(p);
+        const CUtensorMap *map = of_p ? &job.p : &job.q;
+        const bool t = of_p ? p.p_t : p.q_t, wide = (of_p ? kP : p.q_rows) > 64;
+        const uint32_t bytes = (PAIR ? 2 : 1) * (kPBytes + (uint32_t)p.q_rows * 128);
+        const bool counts = of_p && (rank == 0 || !PAIR);
+        for (Walk walk(p, worker, workers); ok && walk.tile < p.tiles; walk.next()) {
+          const Tile at = tile_at<kTileP, SYMMETRIC>(p, walk.tile);
+          int r0 = of_p ? at.p0 : at.q0, k = kb_first * kBK;
+          if constexpr (PAIR) r0 += rank * (of_p ? kP : p.q_tile / 2);
+          for (int kb = 0; kb < kblocks; ++kb, ++it, k += kBK) {
+            if (!(ok = wait_phase(empty + s, ph ^ 1, abort_flag, limit, p.status))) break;
+            const uint32_t st = begin + s * stage_bytes, bar = full_at + 8u * s;
+            if (counts) mbar_arrive_expect_tx(full + s, bytes);
+            if (t) {
+              tma_load_3d<PAIR>(st, map, r0, k, at.z, bar);
+              if (wide) tma_load_3d<PAIR>(st + 64 * 128, map, r0 + 64, k, at.z, bar);
+            } else {
+              tma_load_3d<PAIR>(st, map, k, r0, at.z, bar);
+            }
+            if (++s == stages) s = 0, ph ^= 1;
+          }
         }
-      }
+      };
+      produce(jobs.job[0]);
+      if (kTwo && jobs.count > 1) produce(jobs.job[1]);
       // Loads issued into shared memory land before the block can exit (a pair's leader counts
       // both CTAs' bytes).
       if (rank == 0 || !PAIR)
         for (uint32_t j = it > (uint32_t)stages ? it - stages : 0; j < it; ++j)
-          drain_phase(full + j % stages, (j / stages) & 1, p.wait_limit_ns);
+          drain_phase(full + j % stages, (j / stages) & 1, limit);
     }
   } else if (warp == 1) {
     if (rank == 0 || !PAIR) {
@@ -815,32 +879,37 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : kThreads, SPLIT ? 2 : 1)
       uint32_t ph = 0;
       bool ok = true;
       const bool one = elect_one();
-      const uint32_t p_step = desc_step(p.p_t), q_step = desc_step(p.q_t);
-      for (int tile = first_tile; ok && tile < p.tiles; tile += tile_step) {
-        for (int kb0 = 0; ok && kb0 < kblocks; kb0 += p.seg_blocks, ++unit) {
-          const int kb1 = min(kb0 + p.seg_blocks, kblocks);
-          const uint32_t acc = SPLIT ? 0 : unit & 1, use = unit >> 1;
-          if (!(ok = warp_wait(acc_empty + acc, (use & 1) ^ 1, abort_flag, p))) break;
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t d = tmem + acc * kAccCols;
-          for (int kb = kb0; kb < kb1; ++kb) {
-            if (!(ok = warp_wait(full + s, ph, abort_flag, p))) break;
+      const auto multiply = [&](const ProductDev &p) {
+        const int kblocks = blocks(p);
+        const uint32_t p_step = desc_step(p.p_t), q_step = desc_step(p.q_t);
+        for (Walk walk(p, worker, workers); ok && walk.tile < p.tiles; walk.next()) {
+          for (int kb0 = 0; ok && kb0 < kblocks; kb0 += p.seg_blocks, ++unit) {
+            const int kb1 = min(kb0 + p.seg_blocks, kblocks);
+            const uint32_t acc = SPLIT ? 0 : unit & 1, use = unit >> 1;
+            if (!(ok = warp_wait(acc_empty + acc, (use & 1) ^ 1, abort_flag, p))) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint32_t st = smem_u32(sm) + s * stage_bytes;
-            const uint64_t pd = operand_desc(st, p.p_t), qd = operand_desc(st + kPBytes, p.q_t);
-            if (one) {
+            const uint32_t d = tmem + acc * kAccCols;
+            for (int kb = kb0; kb < kb1; ++kb) {
+              if (!(ok = warp_wait(full + s, ph, abort_flag, p))) break;
+              asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+              const uint32_t st = smem_u32(sm) + s * stage_bytes;
+              const uint64_t pd = operand_desc(st, p.p_t), qd = operand_desc(st + kPBytes, p.q_t);
+              if (one) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                umma_f16<PAIR>(d, pd + k * p_step, qd + k * q_step, p.idesc, kb != kb0 || k != 0 ? 1u : 0u);
-              commit<PAIR>(empty + s);
+                for (int k = 0; k < 4; ++k)
+                  umma_f16<PAIR>(d, pd + k * p_step, qd + k * q_step, p.idesc, kb != kb0 || k != 0 ? 1u : 0u);
+                commit<PAIR>(empty + s);
+              }
+              __syncwarp();
+              if (++s == stages) s = 0, ph ^= 1;
             }
+            if (ok && one) commit<PAIR>(acc_full + acc);
             __syncwarp();
-            if (++s == stages) s = 0, ph ^= 1;
           }
-          if (ok && one) commit<PAIR>(acc_full + acc);
-          __syncwarp();
         }
-      }
+      };
+      multiply(jobs.job[0].d);
+      if (kTwo && jobs.count > 1) multiply(jobs.job[1].d);
       if (one) commit<PAIR>(mma_done);
       __syncwarp();
     }
@@ -848,9 +917,14 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : kThreads, SPLIT ? 2 : 1)
     // ------------------------------------------------------------- epilogue
     const int quad = warp & 3, part = (warp - 4) >> 2;
     const uint32_t acc_empty_at = PAIR ? map_to_rank(smem_u32(acc_empty), 0) : smem_u32(acc_empty);
-    const uint32_t quad_tmem = tmem + ((uint32_t)(quad * 32) << 16);
-    const int lanes0 = (PAIR ? rank * kP : 0) + quad * 32;  // of P, of the tile
-    uint8_t *buffers = sm + stages * stage_bytes;
+    Shared w;
+    w.arrived = arrived + (warp - 4) * kMaxAhead;
+    w.acc_full = acc_full;
+    w.tmem = tmem + ((uint32_t)(quad * 32) << 16);
+    w.lane = lane;
+    w.row0 = (PAIR ? rank * kP : 0) + quad * 32;
+    w.abort_flag = abort_flag;
+    w.unit = w.phases = 0;
     const auto release = [&](uint32_t acc) {
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
@@ -861,38 +935,34 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : kThreads, SPLIT ? 2 : 1)
           mbar_arrive(acc_empty + acc);
       }
     };
-    if constexpr (KIND == kTiles) {
-      const int units = qt / kUnit, u0 = units * part / kPartsHere, u1 = units * (part + 1) / kPartsHere;
-      if (u0 == u1) {  // a narrow tile has nothing for this part
-        uint32_t local = 0;
-        for (int tile = first_tile; tile < p.tiles; tile += tile_step, ++local) {
-          if (!warp_wait(acc_full + (local & 1), (local >> 1) & 1, abort_flag, p)) break;
-          release(local & 1);
+    bool ok = true;
+    const auto drain_all = [&](const Job &job) {
+      const ProductDev &p = job.d;
+      const int qt = p.q_tile;
+      if constexpr (!SPLIT && !SYMMETRIC) {
+        if (p.rows) {
+          const int units = qt / kUnit;
+          w.buffers = smem_u32(sm) + stages * stage_bytes + (warp - 4) * (p.ahead * p.ahead_bytes + p.slots * p.slot_bytes);
+          ok = move_tiles<PAIR>(job, Walk(p, worker, workers), w, units * part / kPartsHere,
+                                units * (part + 1) / kPartsHere, release);
+          return;
         }
-      } else {
-        move_tiles<PAIR>(p, &map_out, &map_pre, &map_residual,
-                         smem_u32(buffers) + (warp - 4) * (p.ahead * p.ahead_bytes + p.slots * p.slot_bytes),
-                         arrived + (warp - 4) * kMaxAhead, acc_full, quad_tmem, first_tile, tile_step, u0, u1, lanes0,
-                         lane, abort_flag, release);
       }
-    } else {
       // This warp's 16-column chunks: a part of the tile's.
       const int c0 = qt / 16 * part / kPartsHere, chunks = qt / 16 * (part + 1) / kPartsHere - c0;
-      float *buffer = reinterpret_cast<float *>(buffers + (warp - 4) * kBufferBytes);
-      uint32_t unit = 0;
-      bool ok = true;
-      for (int tile = first_tile; ok && tile < p.tiles; tile += tile_step) {
-        const Tile t = tile_at<kTileP, kSym>(p, tile);
-        const int n0 = t.p0 + lanes0, m0 = t.q0 + c0 * 16;
-        for (int seg = 0; seg < p.segments; ++seg, ++unit) {
-          const uint32_t acc = SPLIT ? 0 : unit & 1, use = unit >> 1;
+      float *buffer = reinterpret_cast<float *>(sm + stages * stage_bytes + (warp - 4) * kBufferBytes);
+      for (Walk walk(p, worker, workers); ok && walk.tile < p.tiles; walk.next()) {
+        const Tile t = tile_at<kTileP, SYMMETRIC>(p, walk.tile);
+        const int n0 = t.p0 + w.row0, m0 = t.q0 + c0 * 16;
+        for (int seg = 0; seg < p.segments; ++seg, ++w.unit) {
+          const uint32_t acc = SPLIT ? 0 : w.unit & 1, use = w.unit >> 1;
           const bool first = seg == 0, last = seg == p.segments - 1;
-          Drain<KIND> drain;
+          Drain<SYMMETRIC ? kSymmetric : kSingles> drain;
           if constexpr (!SPLIT) drain.begin(p, t.z, m0, chunks, n0, lane, first, last);
           ok = warp_wait(acc_full + acc, use & 1, abort_flag, p);
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t taddr = quad_tmem + acc * kAccCols + c0 * 16;
+          const uint32_t taddr = w.tmem + acc * kAccCols + c0 * 16;
           if constexpr (SPLIT) {
             // The partial tile into shared memory (the stages: every MMA has read them).
             float *mine = reinterpret_cast<float *>(sm) + c0 * 16 * kP + quad * 32 + lane;
@@ -910,22 +980,26 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : kThreads, SPLIT ? 2 : 1)
             drain.run(p, taddr, chunks, buffer, lane, first, last, [&] { release(acc); });
         }
       }
-    }
+    };
+    drain_all(jobs.job[0]);
+    if (kTwo && ok && jobs.count > 1) drain_all(jobs.job[1]);
   }
 
   if constexpr (SPLIT) {
+    const ProductDev &p = jobs.job[0].d;
+    const int qt = p.q_tile;
     // Each CTA adds a share of the tile's columns over the cluster, in rank order.
     __syncwarp();
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     cluster_sync();
     bool ok = true;
-    for (int r = 0; r < p.splits; ++r)  // a CTA that gave up has no partial tile
+    for (int r = 0; r < splits; ++r)  // a CTA that gave up has no partial tile
       ok &= load_cluster(map_to_rank(smem_u32(const_cast<int *>(abort_flag)), r)) == 0;
-    const Tile t = tile_at<kTileP, kSym>(p, first_tile);
+    const Tile t = tile_at<kTileP, SYMMETRIC>(p, worker);
     // A warp a column (128 outputs of one row of out), four outputs a lane.
     const int n = t.p0 + lane * 4;
-    const int q_end = qt * (rank + 1) / p.splits;
-    for (int q = qt * rank / p.splits + warp; q < q_end; q += kThreads / 32) {
+    const int q_end = qt * (rank + 1) / splits;
+    for (int q = qt * rank / splits + warp; q < q_end; q += kThreads / 32) {
       const int m = t.q0 + q;
       if (!ok || m >= p.M) break;
       const uint32_t at = smem_u32(sm) + (q * kP + lane * 4) * 4;
@@ -938,14 +1012,14 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : kThreads, SPLIT ? 2 : 1)
       float4 v[8];
 #pragma unroll
       for (int r = 0; r < 8; ++r)
-        v[r] = r < p.splits ? load4_cluster(map_to_rank(at, r)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[r] = r < splits ? load4_cluster(map_to_rank(at, r)) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int r = 1; r < 8; ++r)
         v[0].x += v[r].x, v[0].y += v[r].y, v[0].z += v[r].z, v[0].w += v[r].w;
       const float x[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (n + i < p.N) finish_one<kSym>(p, t.z, m, n + i, p.scale * x[i], bias[i], residual[i]);
+        if (n + i < p.N) finish_one<SYMMETRIC>(p, t.z, m, n + i, p.scale * x[i], bias[i], residual[i]);
     }
     cluster_sync();  // no CTA leaves while another may still read its part
   }
@@ -954,7 +1028,7 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : kThreads, SPLIT ? 2 : 1)
   __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  if (warp == 1 && lane == 0) drain_phase(mma_done, 0, p.wait_limit_ns);  // the MMAs ran
+  if (warp == 1 && lane == 0) drain_phase(mma_done, 0, jobs.job[0].d.wait_limit_ns);  // the MMAs ran
   __syncwarp();
   if constexpr (PAIR) cluster_sync();  // no CTA leaves while the other may still signal it
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -1008,18 +1082,14 @@ struct DeviceInfo {
 DeviceInfo g_info[64];
 std::mutex g_info_mu;
 
-using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, ProductDev);
+using Kernel = void (*)(Jobs);
 enum Form { kSingle, kSplit, kPair, kForms };
-Kernel kernel_of(int form, int kind) {
-  static constexpr Kernel all[kForms][3] = {
-      {product_kernel<false, false, kTiles>, product_kernel<false, false, kSingles>,
-       product_kernel<false, false, kSymmetric>},
-      // the join moves values one by one in any case
-      {product_kernel<false, true, kSingles>, product_kernel<false, true, kSingles>,
-       product_kernel<false, true, kSymmetric>},
-      {product_kernel<true, false, kTiles>, product_kernel<true, false, kSingles>,
-       product_kernel<true, false, kSymmetric>}};
-  return all[form][kind];
+Kernel kernel_of(int form, bool symmetric) {
+  static constexpr Kernel all[kForms][2] = {
+      {product_kernel<false, false, false>, product_kernel<false, false, true>},
+      {product_kernel<false, true, false>, product_kernel<false, true, true>},
+      {product_kernel<true, false, false>, product_kernel<true, false, true>}};
+  return all[form][symmetric];
 }
 
 cudaError_t device_info(DeviceInfo &out) {
@@ -1030,9 +1100,9 @@ cudaError_t device_info(DeviceInfo &out) {
   DeviceInfo &d = g_info[dev & 63];
   if (!d.ready) {
     e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-    for (int i = 0; i < 3 * kForms && e == cudaSuccess; ++i)
-      e = cudaFuncSetAttribute(kernel_of(i / 3, i % 3), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)(i / 3 == kSplit ? kSplitSmemBytes : kSmemBytes));
+    for (int i = 0; i < 2 * kForms && e == cudaSuccess; ++i)
+      e = cudaFuncSetAttribute(kernel_of(i / 2, i & 1), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)(i / 2 == kSplit ? kSplitSmemBytes : kSmemBytes));
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -1045,7 +1115,7 @@ cudaError_t device_info(DeviceInfo &out) {
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if ((e = cudaOccupancyMaxActiveClusters(&d.pairs, kernel_of(kPair, kTiles), &cfg)) != cudaSuccess) return e;
+    if ((e = cudaOccupancyMaxActiveClusters(&d.pairs, kernel_of(kPair, false), &cfg)) != cudaSuccess) return e;
     d.ready = true;
   }
   out = d;
@@ -1084,80 +1154,23 @@ bool overlaps(const Plane &a, const Plane &b, int64_t M, int64_t N) {
 // Bytes of a tiles' epilogue unit.
 uint32_t unit_bytes(const PlaneDev &d) { return d.p ? 32 * kUnit * (d.type == ENGRAM_DTYPE_F32 ? 4 : 2) : 0; }
 
-// Fills in what a form needs and launches it: rows of a (`rows`) or of b in the lanes.
-cudaError_t launch_form(const ProductParams &p, ProductDev &d, int form, bool rows, int q_tile, const DeviceInfo &info,
-                        cudaStream_t stream) {
-  const Operand &op = rows ? p.a : p.b, &oq = rows ? p.b : p.a;
-  const int64_t P = rows ? p.M : p.N, Q = rows ? p.N : p.M;
-  const int kind = p.symmetric ? kSymmetric : rows ? kTiles : kSingles;
-  d.p_t = op.t;
-  d.q_t = oq.t;
-  d.q_tile = q_tile;
-  const int q_staged = form == kPair ? q_tile / 2 : q_tile;
-  d.q_rows = d.q_t ? (q_staged + 63) / 64 * 64 : q_staged;
-  const int64_t stage = kPBytes + d.q_rows * 128;
-  uint32_t budget = form == kSplit ? kSplitBudget : kBudget;
-  const int warps = 4 * (form == kPair ? kPairParts : kParts);
-  if (kind == kTiles) {
-    // One buffer of each sort beside the stages; more of them, and fewer stages, where K is short
-    // and moving out's values is the work.
-    d.ahead_bytes = unit_bytes(d.residual);
-    d.slot_bytes = unit_bytes(d.out) > unit_bytes(d.pre) ? unit_bytes(d.out) : unit_bytes(d.pre);
-    d.ahead = d.ahead_bytes ? 1 : 0;
-    d.slots = 1;
-    const auto stages = [&](int ahead, int slots) {
-      const int64_t left = (int64_t)budget - (int64_t)warps * (ahead * d.ahead_bytes + slots * d.slot_bytes);
-      return (int)(left / stage);
-    };
-    const int least = d.kblocks <= 16 ? 2 : 5;
-    if (stages(d.ahead, 2) >= least) d.slots = 2;
-    while (d.ahead && d.ahead < kMaxAhead && stages(d.ahead + 1, d.slots) >= least) ++d.ahead;
-    budget -= warps * (d.ahead * d.ahead_bytes + d.slots * d.slot_bytes);
-  } else if (kind == kSymmetric && form != kSplit) {
-    budget -= warps * kBufferBytes;
-  }
-  d.stages = (int32_t)(budget / stage);
-  if (d.stages > kMaxStages) d.stages = kMaxStages;
-  if (form == kSplit) {  // a CTA's part of K is one segment
-    d.segments = 1;
-    d.seg_blocks = d.kblocks;
-    d.fold = false;
-  }
-  const int width = form == kPair ? 2 * kP : kP;
-  const int64_t matrix_tiles = tiles_of(P, Q, width, q_tile, p.symmetric), tiles = matrix_tiles * p.count;
-  if (tiles > INT32_MAX / 16) return cudaErrorInvalidConfiguration;
-  d.tiles_p = (int32_t)ceil_div(P, width);
-  d.tiles_q = (int32_t)ceil_div(Q, q_tile);
-  d.matrix_tiles = (int32_t)matrix_tiles;
-  d.tiles = (int32_t)tiles;
-  // kind::f16: fp32 accumulator, the operands' type (0: f16, 1: bf16), which of them are MN-major.
-  d.idesc = 1u << 4 | (p.f16 ? 0u : 1u << 7 | 1u << 10) | (uint32_t)d.p_t << 15 | (uint32_t)d.q_t << 16 |
-            (uint32_t)(q_tile >> 3) << 17 | (uint32_t)(width >> 4) << 24;
-  CUtensorMap map_p, map_q, map_out{}, map_pre{}, map_residual{};
-  if (!make_map(&map_p, op, P, p.K, p.count, kP) || !make_map(&map_q, oq, Q, p.K, p.count, (uint32_t)q_staged))
-    return cudaErrorInvalidValue;
-  if (kind == kTiles && (!make_plane_map(&map_out, d.out, p.M, p.N, p.count) ||
-                         (d.pre.p && !make_plane_map(&map_pre, d.pre, p.M, p.N, p.count)) ||
-                         (d.residual.p && !make_plane_map(&map_residual, d.residual, p.M, p.N, p.count))))
-    return cudaErrorInvalidValue;
-  const Kernel kernel = kernel_of(form, kind);
-  if (form == kPair)
-    return launch(kernel, 2 * (tiles < info.pairs ? tiles : info.pairs), kPairThreads, kSmemBytes, stream, 2, map_p,
-                  map_q, map_out, map_pre, map_residual, d);
-  if (form == kSplit)
-    return launch(kernel, tiles * d.splits, kThreads, kSplitSmemBytes, stream, d.splits, map_p, map_q, map_out, map_pre,
-                  map_residual, d);
-  return launch(kernel, tiles < info.sms ? tiles : info.sms, kThreads, kSmemBytes, stream, 1, map_p, map_q, map_out,
-                map_pre, map_residual, d);
-}
+// A way to compute one product: its form, rows of out in the lanes or columns, the tile's width
+// along Q, and what it is estimated to take in microseconds, less the launch's.
+struct Plan {
+  int form = kSingle, q_tile = 0, splits = 1;
+  bool rows = false;
+  double tile_us = 0, us = HUGE_VAL;  // tile_us: of one tile among others
+  int64_t tiles = 0;
+};
 
-}  // namespace
-
-cudaError_t launch_product(const ProductParams &p, cudaStream_t stream) {
-  DeviceInfo info;
-  cudaError_t e = device_info(info);
-  if (e != cudaSuccess) return e;
-  ProductDev d{};
+// What the choice goes by of a product.
+struct Facts {
+  ProductDev d;  // all but what a plan decides
+  bool tiles_epilogue;
+};
+Facts facts_of(const ProductParams &p) {
+  Facts f{};
+  ProductDev &d = f.d;
   d.out = plane_of(p, p.out);
   d.residual = plane_of(p, p.residual);
   d.pre = plane_of(p, p.pre);
@@ -1167,7 +1180,6 @@ cudaError_t launch_product(const ProductParams &p, cudaStream_t stream) {
   d.residual_scale = p.residual_scale;
   d.status = p.status;
   d.wait_limit_ns = wait_limit_ns();
-  d.withhold = take_withheld_launch();
   d.M = (int32_t)p.M;
   d.N = (int32_t)p.N;
   d.many = p.count > 1;
@@ -1183,32 +1195,205 @@ cudaError_t launch_product(const ProductParams &p, cudaStream_t stream) {
   }
   // The tiles' epilogue wants rows on 16-byte boundaries (a row that repeats has none apart).
   const auto moves = [&](const PlaneDev &x) { return !x.p || (x.vec && (p.M == 1 || x.stride >= p.N)); };
-  const bool rows = !p.symmetric && d.segments == 1 && p.M > 64 && moves(d.out) && moves(d.pre) && moves(d.residual);
+  f.tiles_epilogue = !p.symmetric && d.segments == 1 && moves(d.out) && moves(d.pre) && moves(d.residual);
+  return f;
+}
+
+// The best tile width of a form without splits.
+Plan plan_form(const ProductParams &p, const Facts &f, int form, bool rows, const DeviceInfo &info) {
   const int64_t P = rows ? p.M : p.N, Q = rows ? p.N : p.M;
-  const int step = rows ? kUnit : 16;
-  const double kb = d.kblocks;
-  const int q_single = (int)(Q < kQMax ? ceil_div(Q, step) * step : kQMax);
-  const int64_t single_tiles = p.count * tiles_of(P, Q, kP, q_single, p.symmetric);
-  const double single_us = ceil_div(single_tiles, info.sms) * (1.3 + 0.23 * kb);
-  double pair_us = HUGE_VAL;
-  if (info.pairs > 0 && P > 128) {
-    for (int qt = kPairQMax; qt >= 32; qt -= 32) {
-      const int64_t waves = ceil_div(p.count * tiles_of(P, Q, 2 * kP, qt, p.symmetric), info.pairs);
-      const double us = 1.5 + waves * fmax(4.6 * qt / kPairQMax, 2.1 + fmax(0.2, 0.0013 * qt) * kb);
-      if (us < pair_us) pair_us = us, d.q_tile = qt;
-    }
+  const bool pair = form == kPair;
+  const int step = rows || pair ? kUnit : 16, workers = pair ? info.pairs : info.sms;
+  Plan best;
+  if (workers <= 0 || (pair && P <= kP)) return best;
+  const double kb = f.d.kblocks;
+  for (int qt = pair ? kPairQMax : kQMax; qt >= step; qt -= step) {
+    if (qt - step >= Q) continue;  // wider than Q
+    Plan n;
+    n.form = form;
+    n.rows = rows;
+    n.q_tile = qt;
+    n.tiles = p.count * tiles_of(P, Q, pair ? 2 * kP : kP, qt, p.symmetric);
+    n.tile_us = pair ? fmax(4.6 * qt / kPairQMax, 2.1 + fmax(0.2, 0.0013 * qt) * kb) : 1.3 + 0.23 * kb;
+    n.us = (pair ? 1.5 : 0.) + ceil_div(n.tiles, workers) * n.tile_us;
+    if (n.us < best.us) best = n;
   }
-  double split_us = HUGE_VAL;
-  const int q_split = (int)(p.M < kQMax ? ceil_div(p.M, 16) * 16 : kQMax);
-  const int64_t split_tiles = p.count * tiles_of(p.N, p.M, kP, q_split, p.symmetric);
+  return best;
+}
+
+Plan plan_split(const ProductParams &p, const Facts &f, const DeviceInfo &info) {
+  Plan best;
+  const int qt = (int)(p.M < kQMax ? ceil_div(p.M, 16) * 16 : kQMax);
+  const int64_t tiles = p.count * tiles_of(p.N, p.M, kP, qt, p.symmetric);
+  const double kb = f.d.kblocks;
   for (int n = 4; n <= 8; n *= 2) {
-    if (n * split_tiles > 2 * info.sms || d.kblocks < n || ceil_div(d.kblocks, n) > kSegmentBlocks) continue;
-    const double us = 0.25 * kb / n + 2.4 + 0.02 * q_split + 0.00014 * q_split * n * split_tiles;
-    if (us < split_us) split_us = us, d.splits = n;
+    if (n * tiles > 2 * info.sms || kb < n || ceil_div(f.d.kblocks, n) > kSegmentBlocks) continue;
+    Plan s;
+    s.form = kSplit;
+    s.q_tile = qt;
+    s.splits = n;
+    s.tiles = tiles;
+    s.us = 0.25 * kb / n + 2.4 + 0.02 * qt + 0.00014 * qt * n * tiles;
+    if (s.us < best.us) best = s;
   }
-  const int form = split_us < single_us && split_us < pair_us ? kSplit : pair_us < single_us ? kPair : kSingle;
-  return launch_form(p, d, form, form != kSplit && rows, form == kSplit ? q_split : form == kPair ? d.q_tile : q_single,
-                     info, stream);
+  return best;
+}
+
+// Rows of out in the lanes where the tiles' epilogue can move it, and there are rows to fill them.
+bool rows_of(const ProductParams &p, const Facts &f) { return f.tiles_epilogue && p.M > 64; }
+
+Plan plan_of(const ProductParams &p, const Facts &f, const DeviceInfo &info) {
+  const bool rows = rows_of(p, f);
+  Plan best = plan_form(p, f, kSingle, rows, info);
+  for (const Plan &n : {plan_form(p, f, kPair, rows, info), plan_split(p, f, info)})
+    if (n.us < best.us) best = n;
+  return best;
+}
+
+// Bytes of a stage, and those that the stages of a plan should have at least: where K is short,
+// moving out's values is the work, and buffers for them come first.
+int64_t stage_bytes_of(const ProductParams &p, const Plan &plan) {
+  const int staged = plan.form == kPair ? plan.q_tile / 2 : plan.q_tile;
+  return kPBytes + ((plan.rows ? p.b : p.a).t ? (staged + 63) / 64 * 64 : staged) * 128;
+}
+int64_t reserve_of(const ProductParams &p, int64_t stage) { return (p.K <= 16 * kBK ? 2 : 5) * stage; }
+
+// A job of a plan; its share of the shared memory (the epilogue's buffers) in `buffers`, which leave
+// `reserve` bytes for stages.
+cudaError_t job_of(const ProductParams &p, const Facts &f, const Plan &plan, int64_t reserve, Job &job,
+                   int64_t &buffers) {
+  const Operand &op = plan.rows ? p.a : p.b, &oq = plan.rows ? p.b : p.a;
+  const int64_t P = plan.rows ? p.M : p.N, Q = plan.rows ? p.N : p.M;
+  ProductDev &d = job.d;
+  d = f.d;
+  d.rows = plan.rows;
+  d.p_t = op.t;
+  d.q_t = oq.t;
+  d.q_tile = plan.q_tile;
+  const int q_staged = plan.form == kPair ? plan.q_tile / 2 : plan.q_tile;
+  d.q_rows = (int32_t)((stage_bytes_of(p, plan) - kPBytes) / 128);
+  const int warps = 4 * (plan.form == kPair ? kPairParts : kParts);
+  buffers = p.symmetric ? warps * (int64_t)kBufferBytes : 0;
+  if (plan.rows) {
+    // One buffer of each sort at least.
+    d.ahead_bytes = unit_bytes(d.residual);
+    d.slot_bytes = unit_bytes(d.out) > unit_bytes(d.pre) ? unit_bytes(d.out) : unit_bytes(d.pre);
+    d.ahead = d.ahead_bytes ? 1 : 0;
+    d.slots = 1;
+    const auto bytes = [&](int ahead, int slots) {
+      return (int64_t)warps * (ahead * d.ahead_bytes + slots * d.slot_bytes);
+    };
+    const int64_t most = kBudget - reserve;
+    if (bytes(d.ahead, 2) <= most) d.slots = 2;
+    while (d.ahead && d.ahead < kMaxAhead && bytes(d.ahead + 1, d.slots) <= most) ++d.ahead;
+    buffers = bytes(d.ahead, d.slots);
+  }
+  if (plan.form == kSplit) {  // a CTA's part of K is one segment
+    d.segments = 1;
+    d.seg_blocks = d.kblocks;
+    d.fold = false;
+  }
+  const int width = plan.form == kPair ? 2 * kP : kP;
+  const int64_t matrix_tiles = tiles_of(P, Q, width, plan.q_tile, p.symmetric), tiles = matrix_tiles * p.count;
+  if (tiles > INT32_MAX / 16) return cudaErrorInvalidConfiguration;
+  d.tiles_p = (int32_t)ceil_div(P, width);
+  d.tiles_q = (int32_t)ceil_div(Q, plan.q_tile);
+  d.matrix_tiles = (int32_t)matrix_tiles;
+  d.tiles = (int32_t)tiles;
+  // kind::f16: fp32 accumulator, the operands' type (0: f16, 1: bf16), which of them are MN-major.
+  d.idesc = 1u << 4 | (p.f16 ? 0u : 1u << 7 | 1u << 10) | (uint32_t)d.p_t << 15 | (uint32_t)d.q_t << 16 |
+            (uint32_t)(plan.q_tile >> 3) << 17 | (uint32_t)(width >> 4) << 24;
+  const bool ok = make_map(&job.p, op, P, p.K, p.count, kP) &&
+                  make_map(&job.q, oq, Q, p.K, p.count, (uint32_t)q_staged) &&
+                  (!plan.rows || (make_plane_map(&job.out, d.out, p.M, p.N, p.count) &&
+                                  (!d.pre.p || make_plane_map(&job.pre, d.pre, p.M, p.N, p.count)) &&
+                                  (!d.residual.p || make_plane_map(&job.residual, d.residual, p.M, p.N, p.count))));
+  return ok ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Launches the jobs of plans of one form.
+cudaError_t launch_jobs(Jobs &jobs, const Plan &plan, int64_t buffers, bool symmetric, const DeviceInfo &info,
+                        cudaStream_t stream) {
+  jobs.job[0].d.withhold = take_withheld_launch();
+  jobs.splits = plan.splits;
+  int64_t tiles = 0;
+  for (int i = 0; i < jobs.count; ++i) {
+    const uint32_t bytes = kPBytes + jobs.job[i].d.q_rows * 128;
+    if (bytes > jobs.stage_bytes) jobs.stage_bytes = bytes;
+    tiles += jobs.job[i].d.tiles;
+  }
+  jobs.stages = (int32_t)(((plan.form == kSplit ? kSplitBudget : kBudget) - (plan.form == kSplit ? 0 : buffers)) /
+                          jobs.stage_bytes);
+  if (jobs.stages > kMaxStages) jobs.stages = kMaxStages;
+  const Kernel kernel = kernel_of(plan.form, symmetric);
+  if (plan.form == kPair)
+    return launch(kernel, 2 * (tiles < info.pairs ? tiles : info.pairs), kPairThreads, kSmemBytes, stream, 2, jobs);
+  if (plan.form == kSplit)
+    return launch(kernel, tiles * plan.splits, kThreads, kSplitSmemBytes, stream, plan.splits, jobs);
+  return launch(kernel, tiles < info.sms ? tiles : info.sms, kThreads, kSmemBytes, stream, 1, jobs);
+}
+
+}  // namespace
+
+cudaError_t launch_product(const ProductParams &p, cudaStream_t stream) {
+  DeviceInfo info;
+  cudaError_t e = device_info(info);
+  if (e != cudaSuccess) return e;
+  const Facts f = facts_of(p);
+  const Plan plan = plan_of(p, f, info);
+  Jobs jobs{};
+  jobs.count = 1;
+  int64_t buffers;
+  const int64_t reserve = reserve_of(p, stage_bytes_of(p, plan));
+  if ((e = job_of(p, f, plan, reserve, jobs.job[0], buffers)) != cudaSuccess) return e;
+  return launch_jobs(jobs, plan, buffers, p.symmetric, info, stream);
+}
+
+cudaError_t launch_products(const ProductParams &p0, const ProductParams &p1, cudaStream_t stream) {
+  DeviceInfo info;
+  cudaError_t e = device_info(info);
+  if (e != cudaSuccess) return e;
+  const ProductParams *p[2] = {&p0, &p1};
+  const Facts f[2] = {facts_of(p0), facts_of(p1)};
+  Plan alone[2], best[2];
+  for (int i = 0; i < 2; ++i) alone[i] = plan_of(*p[i], f[i], info);
+  // Together in one launch, both in one form, the one of the longer tiles first: its last wave is
+  // filled by the other's tiles.  Another launch takes 2.5 us.
+  double us = alone[0].us + alone[1].us + 2.5;
+  bool together = false;
+  for (int form : {kSingle, kPair}) {
+    Plan n[2];
+    for (int i = 0; i < 2; ++i) n[i] = plan_form(*p[i], f[i], form, rows_of(*p[i], f[i]), info);
+    if (n[0].us == HUGE_VAL || n[1].us == HUGE_VAL) continue;
+    const int workers = form == kPair ? info.pairs : info.sms;
+    const double work = (n[0].tiles * n[0].tile_us + n[1].tiles * n[1].tile_us) / workers;
+    const double longest = fmax(n[0].tile_us, n[1].tile_us), shorter = fmin(n[0].tile_us, n[1].tile_us);
+    const double both = (form == kPair ? 1.5 : 0.) + fmax(longest, work + 0.5 * shorter);
+    if (both < us) us = both, best[0] = n[0], best[1] = n[1], together = true;
+  }
+  if (!together) {
+    if ((e = launch_product(p0, stream)) != cudaSuccess) return e;
+    return launch_product(p1, stream);
+  }
+  const int a = best[0].tile_us >= best[1].tile_us ? 0 : 1, b = 1 - a;
+  Jobs jobs{};
+  jobs.count = 2;
+  int64_t buffers[2], stage = 0, reserve = 0;
+  for (int i = 0; i < 2; ++i)
+    if (stage_bytes_of(*p[i], best[i]) > stage) stage = stage_bytes_of(*p[i], best[i]);
+  for (int i = 0; i < 2; ++i)
+    if (reserve_of(*p[i], stage) > reserve) reserve = reserve_of(*p[i], stage);
+  if ((e = job_of(*p[a], f[a], best[a], reserve, jobs.job[0], buffers[0])) != cudaSuccess) return e;
+  if ((e = job_of(*p[b], f[b], best[b], reserve, jobs.job[1], buffers[1])) != cudaSuccess) return e;
+  const int64_t most = best[0].form == kPair ? info.pairs : info.sms, tiles = best[0].tiles + best[1].tiles;
+  const int64_t workers = tiles < most ? tiles : most;
+  ProductDev &second = jobs.job[1].d;
+  second.shift = (int32_t)(best[a].tiles % workers);
+  const int64_t lights = workers - second.shift;
+  int64_t extra = second.shift ? (int64_t)(best[a].tile_us / best[b].tile_us) : 0;
+  if (extra > best[b].tiles / lights) extra = best[b].tiles / lights;
+  second.extra = (int32_t)extra;
+  return launch_jobs(jobs, best[0], buffers[0] > buffers[1] ? buffers[0] : buffers[1], false, info, stream);
 }
 
 }  // namespace engram

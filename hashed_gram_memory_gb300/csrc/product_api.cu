@@ -282,30 +282,33 @@ ENGRAM_API engram_status engram_matmul_grad(const void *dy, int32_t dy_dtype, in
   Operand oa{}, ob{};
   if (db && (e = operand_of(ga, scratch, oa, s)) != cudaSuccess) return launched(fn, e);
   if (da && (e = operand_of(gb, scratch, ob, s)) != cudaSuccess) return launched(fn, e);
-  engram::ProductParams p{};
-  p.count = 1;
-  p.scale = scale;
-  p.residual_scale = 1.f;
-  p.status = status;
+  engram::ProductParams pa{}, pb{};
+  pa.count = 1;
+  pa.scale = scale;
+  pa.residual_scale = 1.f;
+  pa.status = status;
+  pb = pa;
   if (da) {  // rows of dz by the columns of b, over N
-    p.a = Operand{gy.p, gy.stride, 0, false};
-    p.b = Operand{ob.p, ob.stride, 0, !ob.t};
-    p.M = M;
-    p.N = K;
-    p.K = N;
-    p.out = Plane{da, da_stride, 0, da_dtype};
-    if ((e = engram::launch_product(p, s)) != cudaSuccess) return launched(fn, e);
+    pa.a = Operand{gy.p, gy.stride, 0, false};
+    pa.b = Operand{ob.p, ob.stride, 0, !ob.t};
+    pa.M = M;
+    pa.N = K;
+    pa.K = N;
+    pa.out = Plane{da, da_stride, 0, da_dtype};
   }
   if (db) {  // columns of dz by the columns of a, over M
-    p.a = Operand{gy.p, gy.stride, 0, true};
-    p.b = Operand{oa.p, oa.stride, 0, !oa.t};
-    p.M = N;
-    p.N = K;
-    p.K = M;
-    p.out = Plane{db, db_stride, 0, db_dtype};
-    if (accumulate) p.residual = p.out;
-    e = engram::launch_product(p, s);
+    pb.a = Operand{gy.p, gy.stride, 0, true};
+    pb.b = Operand{oa.p, oa.stride, 0, !oa.t};
+    pb.M = N;
+    pb.N = K;
+    pb.K = M;
+    pb.out = Plane{db, db_stride, 0, db_dtype};
+    if (accumulate) pb.residual = pb.out;
   }
+  if (da && db)
+    e = engram::launch_products(pa, pb, s);
+  else if (da || db)
+    e = engram::launch_product(da ? pa : pb, s);
   return launched(fn, e);
 }
 
