@@ -48,8 +48,9 @@ constexpr int kQMax = 128;      // most rows of the Q operand a tile of one CTA
 constexpr int kPairQMax = 256;  // and of a pair
 // Epilogue warps: one of each quarter of the lanes for each part of a tile's columns; warp 3 idles,
 // as the epilogue's start at a multiple of 4.
-constexpr int kParts = 2, kPairParts = 3;
+constexpr int kParts = 4, kPairParts = 4;
 constexpr int kThreads = 128 * (1 + kParts), kPairThreads = 128 * (1 + kPairParts);
+constexpr int kSplitParts = 2, kSplitThreads = 128 * (1 + kSplitParts);
 constexpr int kSegmentBlocks = 128;
 constexpr int kMaxStages = 12, kMaxAhead = 4;
 constexpr uint32_t kPBytes = kP * kBK * 2;
@@ -64,7 +65,7 @@ constexpr uint32_t kTmemCols = 512, kSplitTmemCols = 128;
 constexpr size_t kSmemBytes = 1024 + kBarBytes + kBudget;
 constexpr size_t kSplitSmemBytes = 1024 + kBarBytes + kSplitBudget;
 static_assert(2 * (kSplitSmemBytes + 1024) <= 228 * 1024 && kSmemBytes <= 227 * 1024);
-static_assert((2 * kMaxStages + 6 + 4 * kPairParts * kMaxAhead) * 8 + 8 <= kBarBytes);
+static_assert(kParts <= kPairParts && (2 * kMaxStages + 6 + 4 * kPairParts * kMaxAhead) * 8 + 8 <= kBarBytes);
 
 struct PlaneDev {
   void *p;
@@ -83,6 +84,9 @@ struct ProductDev {
   int32_t kblocks, q_tile, q_rows, stages;  // q_rows: rows of Q that a CTA stages
   int32_t segments, seg_blocks;
   int32_t tiles_p, tiles_q, tiles, matrix_tiles;
+  // tiles of a group of out's columns; how many columns of tiles it has, and the last one
+  int32_t group_columns, group_tiles, last_columns;
+  FastDiv by_matrix, by_group, by_columns, by_last;
   uint32_t idesc;
   // the tiles' epilogue: of each warp, buffers for units of the residual ahead (ahead of them,
   // ahead_bytes each) and for units on their way out (slots of them, slot_bytes each)
@@ -172,7 +176,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
 struct Tile {
   int p0, q0, z;
 };
-// Tiles in groups of up to 16 along out's columns, inside a group row by row: the resident CTAs
+// Tiles in groups of up to group_columns along out's columns, inside a group row by row: the resident CTAs
 // read a few slices of a at a time, once, and a group of slices of b that stays in L2.  Of a
 // symmetric product those that hold any output (m, n) with n <= m.
 template <int WIDTH, bool SYMMETRIC>
@@ -180,7 +184,7 @@ __device__ __forceinline__ Tile tile_at(const ProductDev &p, int tile) {
   Tile r{0, 0, 0};
   uint32_t t = tile;
   if (p.many) {
-    r.z = t / (uint32_t)p.matrix_tiles;
+    r.z = fast_div(t, p.by_matrix);
     t -= r.z * (uint32_t)p.matrix_tiles;
   }
   uint32_t tp, tq;
@@ -192,9 +196,10 @@ __device__ __forceinline__ Tile tile_at(const ProductDev &p, int tile) {
     }
     tp = t;
   } else {
-    const uint32_t columns = p.rows ? p.tiles_q : p.tiles_p, rows = p.rows ? p.tiles_p : p.tiles_q;
-    const uint32_t per = 16u * rows, g = t / per, in = t - g * per;
-    const uint32_t wide = min(16u, columns - g * 16u), row = in / wide, column = g * 16 + in - row * wide;
+    const uint32_t g = fast_div(t, p.by_group), in = t - g * p.group_tiles, before = g * p.group_columns;
+    const bool last = before + p.group_columns > (uint32_t)(p.rows ? p.tiles_q : p.tiles_p);
+    const uint32_t row = fast_div(in, last ? p.by_last : p.by_columns);
+    const uint32_t column = before + in - row * (last ? p.last_columns : p.group_columns);
     tp = p.rows ? row : column, tq = p.rows ? column : row;
   }
   r.p0 = (int)tp * WIDTH, r.q0 = (int)tq * p.q_tile;
@@ -741,13 +746,14 @@ __device__ __forceinline__ void finish_one(const ProductDev &p, int64_t z, int64
 // leader's multicast commits; acc_empty lives in the leader and takes an arrival from every
 // epilogue warp of the pair.
 template <bool PAIR, bool SPLIT, bool SYMMETRIC>
-__global__ void __launch_bounds__(PAIR ? kPairThreads : kThreads, SPLIT ? 2 : 1)
+__global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : kThreads, SPLIT ? 2 : 1)
     product_kernel(const __grid_constant__ Jobs jobs) {
   static_assert(!(PAIR && SPLIT));
   constexpr uint32_t kCols = SPLIT ? kSplitTmemCols : kTmemCols;
   constexpr int kAccCols = PAIR ? kPairQMax : kQMax;
   constexpr int kTileP = PAIR ? 2 * kP : kP;
-  constexpr int kPartsHere = PAIR ? kPairParts : kParts;
+  constexpr int kPartsHere = PAIR ? kPairParts : SPLIT ? kSplitParts : kParts;
+  constexpr int kThreadsHere = 128 * (1 + kPartsHere);
   extern __shared__ uint8_t sm_raw[];
   // Barriers, stages, the epilogue's buffers.
   uint8_t *base = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023), *sm = base + kBarBytes;
@@ -999,7 +1005,7 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : kThreads, SPLIT ? 2 : 1)
     // A warp a column (128 outputs of one row of out), four outputs a lane.
     const int n = t.p0 + lane * 4;
     const int q_end = qt * (rank + 1) / splits;
-    for (int q = qt * rank / splits + warp; q < q_end; q += kThreads / 32) {
+    for (int q = qt * rank / splits + warp; q < q_end; q += kThreadsHere / 32) {
       const int m = t.q0 + q;
       if (!ok || m >= p.M) break;
       const uint32_t at = smem_u32(sm) + (q * kP + lane * 4) * 4;
@@ -1295,11 +1301,29 @@ cudaError_t job_of(const ProductParams &p, const Facts &f, const Plan &plan, int
   }
   const int width = plan.form == kPair ? 2 * kP : kP;
   const int64_t matrix_tiles = tiles_of(P, Q, width, plan.q_tile, p.symmetric), tiles = matrix_tiles * p.count;
-  if (tiles > INT32_MAX / 16) return cudaErrorInvalidConfiguration;
+  if (tiles > INT32_MAX / 16) return cudaErrorInvalidConfiguration;  // group_tiles stay in 31 bits too
   d.tiles_p = (int32_t)ceil_div(P, width);
   d.tiles_q = (int32_t)ceil_div(Q, plan.q_tile);
   d.matrix_tiles = (int32_t)matrix_tiles;
   d.tiles = (int32_t)tiles;
+  if (!p.symmetric) {
+    // b's slices of a group, about 32 MB, stay in L2 while a's pass by (65,536 x 4096 x 6144 in groups
+    // of 8 columns of tiles 1925 us, of 16 1979; 16,384 x 6144 x 4096 493 and 476).
+    const int64_t columns = plan.rows ? d.tiles_q : d.tiles_p, rows = plan.rows ? d.tiles_p : d.tiles_q;
+    const int64_t slice = (plan.rows ? plan.q_tile : width) * p.K * 2;
+    int64_t most = (32 << 20) / slice;
+    most = most < 4 ? 4 : most > 16 ? 16 : most;
+    const int64_t groups = ceil_div(columns, most), per = ceil_div(columns, groups);
+    d.group_columns = (int32_t)per;
+    d.group_tiles = (int32_t)(per * rows);
+    d.last_columns = (int32_t)(columns - columns / per * per);
+    d.by_matrix = fast_div_of((uint32_t)matrix_tiles);
+    d.by_group = fast_div_of((uint32_t)d.group_tiles);
+    d.by_columns = fast_div_of((uint32_t)per);
+    d.by_last = fast_div_of(d.last_columns ? (uint32_t)d.last_columns : 1);
+  } else {
+    d.by_matrix = fast_div_of((uint32_t)matrix_tiles);
+  }
   // kind::f16: fp32 accumulator, the operands' type (0: f16, 1: bf16), which of them are MN-major.
   d.idesc = 1u << 4 | (p.f16 ? 0u : 1u << 7 | 1u << 10) | (uint32_t)d.p_t << 15 | (uint32_t)d.q_t << 16 |
             (uint32_t)(plan.q_tile >> 3) << 17 | (uint32_t)(width >> 4) << 24;
@@ -1329,7 +1353,7 @@ cudaError_t launch_jobs(Jobs &jobs, const Plan &plan, int64_t buffers, bool symm
   if (plan.form == kPair)
     return launch(kernel, 2 * (tiles < info.pairs ? tiles : info.pairs), kPairThreads, kSmemBytes, stream, 2, jobs);
   if (plan.form == kSplit)
-    return launch(kernel, tiles * plan.splits, kThreads, kSplitSmemBytes, stream, plan.splits, jobs);
+    return launch(kernel, tiles * plan.splits, kSplitThreads, kSplitSmemBytes, stream, plan.splits, jobs);
   return launch(kernel, tiles < info.sms ? tiles : info.sms, kThreads, kSmemBytes, stream, 1, jobs);
 }
 
