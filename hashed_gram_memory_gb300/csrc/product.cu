@@ -15,9 +15,8 @@
 //     those leave SMs idle (a few rows of a: reading b is the work), 4 or 8 CTAs of a cluster
 //     share a tile, each with a part of K, and add their parts through distributed shared memory
 //     in rank order, two such CTAs an SM.
-// Warps: 0 and 2 TMA producers, of P and of Q (a ring of stages of 64 of K, 128-byte swizzle); 1
-// allocates TMEM, one thread (of the pair's even CTA) issues the MMAs into one of two accumulators;
-// 4.. epilogue.
+// Warps: 0, 2 and 3 TMA producers (a ring of stages of 64 of K, 128-byte swizzle); 1 allocates TMEM,
+// one thread (of the pair's even CTA) issues the MMAs into one of two accumulators; 4.. epilogue.
 //
 // The fp32 accumulator of the tensor cores does not round to nearest: its error grows with the
 // number of additions.  For fp32 outputs K is cut into segments of at most 8192 that each start
@@ -46,13 +45,12 @@ constexpr int kP = 128;         // rows of the P operand a CTA stages
 constexpr int kBK = 64;         // of K a stage: 128 bytes
 constexpr int kQMax = 128;      // most rows of the Q operand a tile of one CTA
 constexpr int kPairQMax = 256;  // and of a pair
-// Epilogue warps: one of each quarter of the lanes for each part of a tile's columns; warp 3 idles,
-// as the epilogue's start at a multiple of 4.
+// Epilogue warps: one of each quarter of the lanes for each part of a tile's columns.
 constexpr int kParts = 4, kPairParts = 4;
 constexpr int kThreads = 128 * (1 + kParts), kPairThreads = 128 * (1 + kPairParts);
 constexpr int kSplitParts = 2, kSplitThreads = 128 * (1 + kSplitParts);
 constexpr int kSegmentBlocks = 128;
-constexpr int kMaxStages = 12, kMaxAhead = 4;
+constexpr int kMaxStages = 12, kMaxAhead = 4, kProducers = 3;
 constexpr uint32_t kPBytes = kP * kBK * 2;
 constexpr uint32_t kBarBytes = 1024;
 constexpr int kUnit = 32;   // columns a warp of the tiles' epilogue moves at a time
@@ -65,6 +63,8 @@ constexpr uint32_t kTmemCols = 512, kSplitTmemCols = 128;
 constexpr size_t kSmemBytes = 1024 + kBarBytes + kBudget;
 constexpr size_t kSplitSmemBytes = 1024 + kBarBytes + kSplitBudget;
 static_assert(2 * (kSplitSmemBytes + 1024) <= 228 * 1024 && kSmemBytes <= 227 * 1024);
+static_assert(kSplitBudget >= kProducers * 2 * kPBytes &&
+              kBudget >= kProducers * 2 * kPBytes + 4 * kPairParts * 2 * 32 * kUnit * 4);
 static_assert(kParts <= kPairParts && (2 * kMaxStages + 6 + 4 * kPairParts * kMaxAhead) * 8 + 8 <= kBarBytes);
 
 struct PlaneDev {
@@ -113,30 +113,33 @@ struct Jobs {
 
 // Shared-memory descriptor of an operand tile, 128-byte swizzle.  K-major: rows of 64 of K,
 // 8-row groups 1024 bytes apart.  MN-major: boxes of 64 rows (128 bytes) by 64 of K, 8192 bytes
-// apart along the rows, groups of 8 along K 1024 bytes apart.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool t) {
-  return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(t ? 8192 >> 4 : 1) << 16 |
-         (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// apart along the rows, groups of 8 along K 1024 bytes apart.  The halves: address and the stride
+// between boxes; the stride between groups, descriptor version 1, SWIZZLE_128B (2).
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, bool t) {
+  return ((addr >> 4) & 0x3FFF) | (uint32_t)(t ? 8192 >> 4 : 1) << 16;
 }
+constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
 // What 16 of K add to it, in its units of 16 bytes.
 __device__ __forceinline__ uint32_t desc_step(bool t) { return t ? 2048 >> 4 : 32 >> 4; }
 
 template <bool PAIR>
-__device__ __forceinline__ void umma_f16(uint32_t d, uint64_t p_desc, uint64_t q_desc, uint32_t idesc,
+__device__ __forceinline__ void umma_f16(uint32_t d, uint32_t p_low, uint32_t q_low, uint32_t idesc,
                                          uint32_t accumulate) {
   if constexpr (PAIR)
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(p_desc), "l"(q_desc), "r"(idesc), "r"(accumulate)
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(p_low), "r"(q_low), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(p_desc), "l"(q_desc), "r"(idesc), "r"(accumulate)
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(p_low), "r"(q_low), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
         : "memory");
 }
 
@@ -829,40 +832,48 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : 
   const uint32_t tmem = *tmem_slot;
   dependency_wait();
 
-  if (warp == 0 || warp == 2) {
+  if (warp < 4 && warp != 1) {
     if (lane == 0) {
-      // ----------------------------- TMA producers: warp 0 of P, warp 2 of Q
-      // Two threads, as one could not issue the four copies that a stage of rows along K takes, a
-      // pair's stage of 256 x 256 being worked off in 270 ns.
-      const bool of_p = warp == 0;
+      // ------------------------------------------------------- TMA producers
+      // kProducers threads, a stage each in turn: one alone takes 180 ns a stage (waiting, expecting
+      // its bytes, issuing its copies), whatever the stage holds.  The ring has at least as many
+      // stages: a thread that waits for a stage to be free has seen the one kProducers before it
+      // freed, so the phase two before the one it waits for, of the same parity, is over.
       const uint32_t full_at = PAIR ? map_to_rank(smem_u32(full), 0) : smem_u32(full);
       const int64_t limit = jobs.job[0].d.wait_limit_ns;
-      const uint32_t begin = smem_u32(sm) + (of_p ? 0 : kPBytes);
       uint32_t it = 0;
-      int s = 0;
+      int s = 0, turn = warp == 0 ? 0 : warp - 1;  // stages to go to the next one of this thread
       uint32_t ph = 0;
       bool ok = true;
       const auto produce = [&](const Job &job) {
         const ProductDev &p = job.d;
-        const int kb_first = first_block(p), kblocks = blocks(p);
-        const CUtensorMap *map = of_p ? &job.p : &job.q;
-        const bool t = of_p ? p.p_t : p.q_t, wide = (of_p ? kP : p.q_rows) > 64;
-        const uint32_t bytes = (PAIR ? 2 : 1) * (kPBytes + (uint32_t)p.q_rows * 128);
-        const bool counts = of_p && (rank == 0 || !PAIR);
+        const int kb_first = first_block(p), kblocks = blocks(p), q_rows = p.q_rows;
+        const uint32_t bytes = (PAIR ? 2 : 1) * (kPBytes + (uint32_t)q_rows * 128);
+        const bool p_t = p.p_t, q_t = p.q_t;
         for (Walk walk(p, worker, workers); ok && walk.tile < p.tiles; walk.next()) {
-          const Tile at = tile_at<kTileP, SYMMETRIC>(p, walk.tile);
-          int r0 = of_p ? at.p0 : at.q0, k = kb_first * kBK;
-          if constexpr (PAIR) r0 += rank * (of_p ? kP : p.q_tile / 2);
+          Tile at = tile_at<kTileP, SYMMETRIC>(p, walk.tile);
+          if constexpr (PAIR) at.p0 += rank * kP, at.q0 += rank * (p.q_tile / 2);
+          int k = kb_first * kBK;
           for (int kb = 0; kb < kblocks; ++kb, ++it, k += kBK) {
-            if (!(ok = wait_phase(empty + s, ph ^ 1, abort_flag, limit, p.status))) break;
-            const uint32_t st = begin + s * stage_bytes, bar = full_at + 8u * s;
-            if (counts) mbar_arrive_expect_tx(full + s, bytes);
-            if (t) {
-              tma_load_3d<PAIR>(st, map, r0, k, at.z, bar);
-              if (wide) tma_load_3d<PAIR>(st + 64 * 128, map, r0 + 64, k, at.z, bar);
-            } else {
-              tma_load_3d<PAIR>(st, map, k, r0, at.z, bar);
+            if (turn == 0) {
+              if (!(ok = wait_phase(empty + s, ph ^ 1, abort_flag, limit, p.status))) break;
+              const uint32_t st = smem_u32(sm) + s * stage_bytes, bar = full_at + 8u * s;
+              if (rank == 0 || !PAIR) mbar_arrive_expect_tx(full + s, bytes);
+              if (p_t) {
+                tma_load_3d<PAIR>(st, &job.p, at.p0, k, at.z, bar);
+                tma_load_3d<PAIR>(st + 64 * 128, &job.p, at.p0 + 64, k, at.z, bar);
+              } else {
+                tma_load_3d<PAIR>(st, &job.p, k, at.p0, at.z, bar);
+              }
+              if (q_t) {
+                tma_load_3d<PAIR>(st + kPBytes, &job.q, at.q0, k, at.z, bar);
+                if (q_rows > 64) tma_load_3d<PAIR>(st + kPBytes + 64 * 128, &job.q, at.q0 + 64, k, at.z, bar);
+              } else {
+                tma_load_3d<PAIR>(st + kPBytes, &job.q, k, at.q0, at.z, bar);
+              }
+              turn = kProducers;
             }
+            --turn;
             if (++s == stages) s = 0, ph ^= 1;
           }
         }
@@ -885,37 +896,36 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : 
       uint32_t ph = 0;
       bool ok = true;
       const bool one = elect_one();
+      const int64_t limit = jobs.job[0].d.wait_limit_ns;
       const auto multiply = [&](const ProductDev &p) {
         const int kblocks = blocks(p);
-        const uint32_t p_step = desc_step(p.p_t), q_step = desc_step(p.q_t);
+        const uint32_t p_step = desc_step(p.p_t), q_step = desc_step(p.q_t), idesc = p.idesc;
+        const uint32_t p_first = desc_low(smem_u32(sm), p.p_t), q_first = desc_low(smem_u32(sm) + kPBytes, p.q_t);
         for (Walk walk(p, worker, workers); ok && walk.tile < p.tiles; walk.next()) {
           for (int kb0 = 0; ok && kb0 < kblocks; kb0 += p.seg_blocks, ++unit) {
             const int kb1 = min(kb0 + p.seg_blocks, kblocks);
             const uint32_t acc = SPLIT ? 0 : unit & 1, use = unit >> 1;
-            if (!(ok = warp_wait(acc_empty + acc, (use & 1) ^ 1, abort_flag, p))) break;
+            if (!(ok = wait_phase(acc_empty + acc, (use & 1) ^ 1, abort_flag, limit, p.status))) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t d = tmem + acc * kAccCols;
             for (int kb = kb0; kb < kb1; ++kb) {
-              if (!(ok = warp_wait(full + s, ph, abort_flag, p))) break;
+              if (!(ok = wait_phase(full + s, ph, abort_flag, limit, p.status))) break;
               asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-              const uint32_t st = smem_u32(sm) + s * stage_bytes;
-              const uint64_t pd = operand_desc(st, p.p_t), qd = operand_desc(st + kPBytes, p.q_t);
-              if (one) {
+              const uint32_t pd = p_first + s * (stage_bytes >> 4), qd = q_first + s * (stage_bytes >> 4);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  umma_f16<PAIR>(d, pd + k * p_step, qd + k * q_step, p.idesc, kb != kb0 || k != 0 ? 1u : 0u);
-                commit<PAIR>(empty + s);
-              }
-              __syncwarp();
+              for (int k = 0; k < 4; ++k)
+                umma_f16<PAIR>(d, pd + k * p_step, qd + k * q_step, idesc, kb != kb0 || k != 0 ? 1u : 0u);
+              commit<PAIR>(empty + s);
               if (++s == stages) s = 0, ph ^= 1;
             }
-            if (ok && one) commit<PAIR>(acc_full + acc);
-            __syncwarp();
+            if (ok) commit<PAIR>(acc_full + acc);
           }
         }
       };
-      multiply(jobs.job[0].d);
-      if (kTwo && jobs.count > 1) multiply(jobs.job[1].d);
+      if (one) {
+        multiply(jobs.job[0].d);
+        if (kTwo && jobs.count > 1) multiply(jobs.job[1].d);
+      }
       if (one) commit<PAIR>(mma_done);
       __syncwarp();
     }
@@ -1262,7 +1272,9 @@ int64_t stage_bytes_of(const ProductParams &p, const Plan &plan) {
   const int staged = plan.form == kPair ? plan.q_tile / 2 : plan.q_tile;
   return kPBytes + ((plan.rows ? p.b : p.a).t ? (staged + 63) / 64 * 64 : staged) * 128;
 }
-int64_t reserve_of(const ProductParams &p, int64_t stage) { return (p.K <= 16 * kBK ? 2 : 5) * stage; }
+int64_t reserve_of(const ProductParams &p, int64_t stage) {
+  return (p.K <= 16 * kBK ? kProducers : 5) * stage;
+}
 
 // A job of a plan; its share of the shared memory (the epilogue's buffers) in `buffers`, which leave
 // `reserve` bytes for stages.
@@ -1349,6 +1361,7 @@ cudaError_t launch_jobs(Jobs &jobs, const Plan &plan, int64_t buffers, bool symm
   jobs.stages = (int32_t)(((plan.form == kSplit ? kSplitBudget : kBudget) - (plan.form == kSplit ? 0 : buffers)) /
                           jobs.stage_bytes);
   if (jobs.stages > kMaxStages) jobs.stages = kMaxStages;
+  if (jobs.stages < kProducers) return cudaErrorInvalidConfiguration;
   const Kernel kernel = kernel_of(plan.form, symmetric);
   if (plan.form == kPair)
     return launch(kernel, 2 * (tiles < info.pairs ? tiles : info.pairs), kPairThreads, kSmemBytes, stream, 2, jobs);
