@@ -301,13 +301,13 @@ template <int N>
 __device__ __forceinline__ void activate(float (&x)[N], int act) {
   if (act == ENGRAM_ACT_RELU) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = x[i] < 0.f ? 0.f : x[i];  // a NaN stays
+    for (int i = 0; i < N; ++i) x[i] = activated(x[i], ENGRAM_ACT_RELU);
   } else if (act == ENGRAM_ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = __fdividef(x[i], 1.f + __expf(-x[i]));
+    for (int i = 0; i < N; ++i) x[i] = activated(x[i], ENGRAM_ACT_SILU);
   } else if (act == ENGRAM_ACT_GELU) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = 0.5f * x[i] * (1.f + erff(x[i] * 0.70710678f));
+    for (int i = 0; i < N; ++i) x[i] = activated(x[i], ENGRAM_ACT_GELU);
   }
 }
 
@@ -724,6 +724,8 @@ struct Drain<kSymmetric> {
   }
 };
 
+__device__ __noinline__ float activated_apart(float x, int act) { return activated(x, act); }
+
 // One sum of products of a tile that several CTAs share becomes outputs; of a symmetric product,
 // on the side n <= m, both images.
 template <bool SYMMETRIC>
@@ -736,10 +738,10 @@ __device__ __forceinline__ void finish_one(const ProductDev &p, int64_t z, int64
     if (n < m) store_one(p.out, z, n, m, x);
     return;
   }
-  float v[1] = {x + bias};
-  if (p.pre.p) store_one(p.pre, z, m, n, v[0]);
-  activate(v, p.act);
-  store_one(p.out, z, m, n, v[0] + residual);
+  x += bias;
+  if (p.pre.p) store_one(p.pre, z, m, n, x);
+  if (p.act != ENGRAM_ACT_NONE) x = activated_apart(x, p.act);
+  store_one(p.out, z, m, n, x + residual);
 }
 
 // ---- the kernels ------------------------------------------------------------------------
@@ -1012,30 +1014,23 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : 
     for (int r = 0; r < splits; ++r)  // a CTA that gave up has no partial tile
       ok &= load_cluster(map_to_rank(smem_u32(const_cast<int *>(abort_flag)), r)) == 0;
     const Tile t = tile_at<kTileP, SYMMETRIC>(p, worker);
-    // A warp a column (128 outputs of one row of out), four outputs a lane.
-    const int n = t.p0 + lane * 4;
-    const int q_end = qt * (rank + 1) / splits;
-    for (int q = qt * rank / splits + warp; q < q_end; q += kThreadsHere / 32) {
-      const int m = t.q0 + q;
-      if (!ok || m >= p.M) break;
-      const uint32_t at = smem_u32(sm) + (q * kP + lane * 4) * 4;
-      float residual[4], bias[4];
+    // A warp 32 neighbouring outputs of one row of out at a time.  Little code, as most launches run
+    // through it once or twice and fetch it from far away.
+    const int q_end = qt * (rank + 1) / splits, q_begin = qt * rank / splits;
+    const uint32_t at0 = smem_u32(sm) + lane * 4;
+#pragma unroll 1
+    for (int i = warp; i < 4 * (q_end - q_begin); i += kThreadsHere / 32) {
+      const int q = q_begin + (i >> 2), m = t.q0 + q, n = t.p0 + (i & 3) * 32 + lane;
+      if (!ok || m >= p.M || n >= p.N) continue;
+      const uint32_t at = at0 + (q * kP + (i & 3) * 32) * 4;
+      float v[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        residual[i] = p.residual.p && n + i < p.N ? p.residual_scale * load_one(p.residual, t.z, m, n + i) : 0.f;
-        bias[i] = p.bias.p && n + i < p.N ? load_one(p.bias, 0, 0, n + i) : 0.f;
-      }
-      float4 v[8];
+      for (int r = 0; r < 8; ++r) v[r] = r < splits ? __uint_as_float(load_cluster(map_to_rank(at, r))) : 0.f;
+      const float bias = p.bias.p ? load_one(p.bias, 0, 0, n) : 0.f;
+      const float residual = p.residual.p ? p.residual_scale * load_one(p.residual, t.z, m, n) : 0.f;
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
-        v[r] = r < splits ? load4_cluster(map_to_rank(at, r)) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int r = 1; r < 8; ++r)
-        v[0].x += v[r].x, v[0].y += v[r].y, v[0].z += v[r].z, v[0].w += v[r].w;
-      const float x[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n + i < p.N) finish_one<SYMMETRIC>(p, t.z, m, n + i, p.scale * x[i], bias[i], residual[i]);
+      for (int r = 1; r < 8; ++r) v[0] += v[r];
+      finish_one<SYMMETRIC>(p, t.z, m, n, p.scale * v[0], bias, residual);
     }
     cluster_sync();  // no CTA leaves while another may still read its part
   }
@@ -1215,14 +1210,22 @@ Facts facts_of(const ProductParams &p) {
   return f;
 }
 
+// The estimates are fitted to every form at M 16 .. 32,768, N 64 .. 8192, K 64 .. 8192 (within 13 %
+// on average; the form that they choose takes 2 % longer than the fastest).  A tile takes the
+// longer of its products (by the stages of K, which single CTAs cannot take in faster than 0.17 us
+// and pairs than 0.15) and of its epilogue (by the bytes that a value of out moves); the other of
+// the two counts once, where nothing hides it.
+
 // The best tile width of a form without splits.
 Plan plan_form(const ProductParams &p, const Facts &f, int form, bool rows, const DeviceInfo &info) {
   const int64_t P = rows ? p.M : p.N, Q = rows ? p.N : p.M;
-  const bool pair = form == kPair;
+  const bool pair = form == kPair, q_t = (rows ? p.b : p.a).t;
   const int step = rows || pair ? kUnit : 16, workers = pair ? info.pairs : info.sms;
   Plan best;
   if (workers <= 0 || (pair && P <= kP)) return best;
   const double kb = f.d.kblocks;
+  const auto bytes = [](const PlaneDev &x) { return !x.p ? 0 : x.type == ENGRAM_DTYPE_F32 ? 4 : 2; };
+  const double moved = (1 + bytes(f.d.out) + bytes(f.d.residual) + bytes(f.d.pre)) / 3.;
   for (int qt = pair ? kPairQMax : kQMax; qt >= step; qt -= step) {
     if (qt - step >= Q) continue;  // wider than Q
     Plan n;
@@ -1230,26 +1233,38 @@ Plan plan_form(const ProductParams &p, const Facts &f, int form, bool rows, cons
     n.rows = rows;
     n.q_tile = qt;
     n.tiles = p.count * tiles_of(P, Q, pair ? 2 * kP : kP, qt, p.symmetric);
-    n.tile_us = pair ? fmax(4.6 * qt / kPairQMax, 2.1 + fmax(0.2, 0.0013 * qt) * kb) : 1.3 + 0.23 * kb;
-    n.us = (pair ? 1.5 : 0.) + ceil_div(n.tiles, workers) * n.tile_us;
+    const int staged = q_t ? (int)ceil_div(qt, pair ? 128 : 64) * (pair ? 128 : 64) : qt;
+    double products, epilogue;
+    if (pair) {
+      products = kb * (rows ? 0.144 + 0.0005 * staged : fmax(0.157, 0.00106 * staged));
+      epilogue = rows ? 1.3 + 0.0066 * qt * moved : 1.5 + 0.0104 * qt * moved;
+    } else {
+      products = kb * (rows ? 0.173 + 0.0004 * staged : 0.177);
+      epilogue = rows ? 0.65 + 0.0058 * qt * moved : 0.9 + 0.0071 * qt * moved;
+    }
+    n.tile_us = fmax(products, epilogue);
+    n.us = (pair ? 3.0 : 2.8) + ceil_div(n.tiles, workers) * n.tile_us + fmin(products, epilogue);
     if (n.us < best.us) best = n;
   }
   return best;
 }
 
+// K shared by 2, 4 or 8 CTAs, two an SM: what a CTA takes of K, and the joining, by the rounds that
+// its warps need for their share of the tile.
 Plan plan_split(const ProductParams &p, const Facts &f, const DeviceInfo &info) {
   Plan best;
   const int qt = (int)(p.M < kQMax ? ceil_div(p.M, 16) * 16 : kQMax);
   const int64_t tiles = p.count * tiles_of(p.N, p.M, kP, qt, p.symmetric);
   const double kb = f.d.kblocks;
-  for (int n = 4; n <= 8; n *= 2) {
+  for (int n = 2; n <= 8; n *= 2) {
     if (n * tiles > 2 * info.sms || kb < n || ceil_div(f.d.kblocks, n) > kSegmentBlocks) continue;
     Plan s;
     s.form = kSplit;
     s.q_tile = qt;
     s.splits = n;
     s.tiles = tiles;
-    s.us = 0.25 * kb / n + 2.4 + 0.02 * qt + 0.00014 * qt * n * tiles;
+    s.us = 5.6 + 0.2 * kb / n * (n * tiles > info.sms ? 2 : 1) +
+           0.45 * ceil_div(4 * ceil_div(qt, n), kSplitThreads / 32);
     if (s.us < best.us) best = s;
   }
   return best;
@@ -1373,11 +1388,17 @@ cudaError_t launch_jobs(Jobs &jobs, const Plan &plan, int64_t buffers, bool symm
 }  // namespace
 
 cudaError_t launch_product(const ProductParams &p, cudaStream_t stream) {
+  if (few_rows_supported(p)) return launch_few_rows(p, stream);
   DeviceInfo info;
   cudaError_t e = device_info(info);
   if (e != cudaSuccess) return e;
   const Facts f = facts_of(p);
   const Plan plan = plan_of(p, f, info);
+  if (p.symmetric) {  // half of the tiles, unless that many run side by side in any case
+    ProductParams whole = p;
+    whole.symmetric = false;
+    if (plan_of(whole, facts_of(whole), info).us <= plan.us) return launch_product(whole, stream);
+  }
   Jobs jobs{};
   jobs.count = 1;
   int64_t buffers;
@@ -1394,6 +1415,10 @@ cudaError_t launch_products(const ProductParams &p0, const ProductParams &p1, cu
   const Facts f[2] = {facts_of(p0), facts_of(p1)};
   Plan alone[2], best[2];
   for (int i = 0; i < 2; ++i) alone[i] = plan_of(*p[i], f[i], info);
+  if (few_rows_supported(p0) || few_rows_supported(p1)) {
+    if ((e = launch_product(p0, stream)) != cudaSuccess) return e;
+    return launch_product(p1, stream);
+  }
   // Together in one launch, both in one form, the one of the longer tiles first: its last wave is
   // filled by the other's tiles.  Another launch takes 2.5 us.
   double us = alone[0].us + alone[1].us + 2.5;
@@ -1405,7 +1430,8 @@ cudaError_t launch_products(const ProductParams &p0, const ProductParams &p1, cu
     const int workers = form == kPair ? info.pairs : info.sms;
     const double work = (n[0].tiles * n[0].tile_us + n[1].tiles * n[1].tile_us) / workers;
     const double longest = fmax(n[0].tile_us, n[1].tile_us), shorter = fmin(n[0].tile_us, n[1].tile_us);
-    const double both = (form == kPair ? 1.5 : 0.) + fmax(longest, work + 0.5 * shorter);
+    const double rest = fmin(n[0].us - n[0].tile_us, n[1].us - n[1].tile_us);  // what counts once
+    const double both = fmin(rest, 5.) + fmax(longest, work + 0.5 * shorter);
     if (both < us) us = both, best[0] = n[0], best[1] = n[1], together = true;
   }
   if (!together) {

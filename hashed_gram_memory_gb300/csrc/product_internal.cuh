@@ -44,6 +44,10 @@ cudaError_t launch_product(const ProductParams &p, cudaStream_t stream);
 // Two products that do not depend on one another, in one launch where that is faster.
 cudaError_t launch_products(const ProductParams &p0, const ProductParams &p1, cudaStream_t stream);
 
+// The product for up to 16 rows of a (product_few.cu), which launch_product takes where it can.
+bool few_rows_supported(const ProductParams &p);
+cudaError_t launch_few_rows(const ProductParams &p, cudaStream_t stream);
+
 // [rows, cols] 16-bit values from rows src_stride apart to rows dst_stride apart (a multiple of
 // 8, dst 16-byte aligned).
 cudaError_t launch_pack(const void *src, int64_t src_stride, void *dst, int64_t dst_stride, int64_t rows,
