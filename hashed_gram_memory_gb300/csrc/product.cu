@@ -54,8 +54,6 @@ constexpr int kMaxStages = 12, kMaxAhead = 4, kProducers = 3;
 constexpr uint32_t kPBytes = kP * kBK * 2;
 constexpr uint32_t kBarBytes = 1024;
 constexpr int kUnit = 32;   // columns a warp of the tiles' epilogue moves at a time
-constexpr int kPitch = 36;  // floats between the rows of a warp's transposing buffer: no bank conflicts
-constexpr uint32_t kBufferBytes = 16 * kPitch * 4;
 // Shared memory for stages and epilogue buffers.
 constexpr uint32_t kBudget = 224 * 1024;
 constexpr uint32_t kSplitBudget = 104 * 1024;
@@ -95,7 +93,7 @@ struct ProductDev {
   // which CTAs (or pairs) take which tiles: see Walk
   int32_t shift, extra;
   bool p_t, q_t, many;
-  bool rows;      // rows of out in the lanes (kTiles); else its columns
+  bool rows;      // rows of out in the lanes; else its columns
   bool fold;      // the residual goes into the first segment's sum (it lies where out does)
   bool withhold;  // test hook: the first stage waits for bytes that never come
 };
@@ -192,12 +190,12 @@ __device__ __forceinline__ Tile tile_at(const ProductDev &p, int tile) {
   }
   uint32_t tp, tq;
   if constexpr (SYMMETRIC) {
-    for (tq = 0;; ++tq) {
-      const uint32_t wide = min(p.tiles_p, (min(p.M, (int)(tq + 1) * p.q_tile) - 1) / WIDTH + 1);
+    for (tp = 0;; ++tp) {
+      const uint32_t wide = min(p.tiles_q, (min(p.M, (int)(tp + 1) * WIDTH) - 1) / p.q_tile + 1);
       if (t < wide) break;
       t -= wide;
     }
-    tp = t;
+    tq = t;
   } else {
     const uint32_t g = fast_div(t, p.by_group), in = t - g * p.group_tiles, before = g * p.group_columns;
     const bool last = before + p.group_columns > (uint32_t)(p.rows ? p.tiles_q : p.tiles_p);
@@ -237,14 +235,13 @@ struct Walk {
 // ---- epilogue ---------------------------------------------------------------------------
 
 // How a kernel's epilogue moves its values.
-//   kTiles: the lanes of TMEM are rows of out.  A lane turns 32 values of its row into words that it
+//   tiles: the lanes of TMEM are rows of out.  A lane turns 32 values of its row into words that it
 //     puts into shared memory, from where tensor copies take 32 x 32 values at a time to out (and
 //     pre); the residual comes in the same way, asked for ahead.  Where out, pre and residual have
 //     rows on 16-byte boundaries.
-//   kSingles: the lanes of TMEM are columns of out.  A warp moves 32 neighbouring values of a row at
-//     a time: any strides, few rows, sums in segments.
-//   kSymmetric: as kSingles, for a symmetric product.
-enum Epilogue { kTiles, kSingles, kSymmetric };
+//   singles: the lanes of TMEM are columns of out.  A warp moves 32 neighbouring values of a row at a
+//     time: any strides, few rows, sums in segments.
+// A symmetric product takes the first, with a second store of each unit below the diagonal.
 
 // f(a null pointer of the C++ type of `type`).
 template <typename F>
@@ -286,17 +283,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, int type) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&v);
 }
-__device__ __forceinline__ void store8(const PlaneDev &d, int64_t z, int64_t m, int64_t n, const float (&x)[8]) {
-  uint4 *at = reinterpret_cast<uint4 *>(element(d, z, m, n));
-  if (d.type == ENGRAM_DTYPE_F32) {
-    reinterpret_cast<float4 *>(at)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4 *>(at)[1] = make_float4(x[4], x[5], x[6], x[7]);
-  } else {
-    at[0] = make_uint4(pack2(x[0], x[1], d.type), pack2(x[2], x[3], d.type), pack2(x[4], x[5], d.type),
-                       pack2(x[6], x[7], d.type));
-  }
-}
-
 template <int N>
 __device__ __forceinline__ void activate(float (&x)[N], int act) {
   if (act == ENGRAM_ACT_RELU) {
@@ -311,14 +297,7 @@ __device__ __forceinline__ void activate(float (&x)[N], int act) {
   }
 }
 
-// 8 values (four columns of each of two chunks' rows, say) of the buffer from `at` on.
-__device__ __forceinline__ void load8(const float *at, float (&x)[8]) {
-  const float4 a = reinterpret_cast<const float4 *>(at)[0], b = reinterpret_cast<const float4 *>(at)[1];
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-
-// ---- kTiles
+// ---- tiles
 
 // Where 16-byte piece j of row r of a unit lies: rows of 64 or 128 bytes (F32), swizzled as the
 // tensor copies do.
@@ -350,6 +329,15 @@ __device__ __forceinline__ void put_row(uint32_t unit, int r, int type, const fl
       st_shared(piece<false>(unit, r, j), pack2(x[8 * j], x[8 * j + 1], type), pack2(x[8 * j + 2], x[8 * j + 3], type),
                 pack2(x[8 * j + 4], x[8 * j + 5], type), pack2(x[8 * j + 6], x[8 * j + 7], type));
   }
+}
+// The same as column r of a unit, rounded to fp16: in every row a lane's value lies beside its
+// neighbours'.
+__device__ __forceinline__ void put_column(uint32_t unit, int r, const float (&x)[kUnit]) {
+#pragma unroll
+  for (int i = 0; i < kUnit; ++i)
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(piece<false>(unit, i, r >> 3) + (r & 7) * 2),
+                 "h"(__half_as_ushort(__float2half_rn(x[i])))
+                 : "memory");
 }
 // x += by * the row's values.
 __device__ __forceinline__ void add_row(uint32_t unit, int r, int type, float by, float (&x)[kUnit]) {
@@ -402,8 +390,9 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&v)[32]) {
 }
 
 // What a warp moves of its CTA's tiles, unit by unit (32 rows x 32 columns): units [first, end) of
-// each tile, `row0` rows into it.  Units that lie outside out are passed over.
-template <int WIDTH>
+// each tile, `row0` rows into it.  Units that lie outside out are passed over, of a symmetric product
+// those above the diagonal.
+template <int WIDTH, bool SYMMETRIC>
 struct Units {
   Walk walk;
   int unit, first, end, row0;
@@ -411,17 +400,19 @@ struct Units {
 
   __device__ __forceinline__ Units(const ProductDev &p, const Walk &w, int first_, int end_, int row0_)
       : walk(w), unit(first_), first(first_), end(end_), row0(row0_) {
-    if (walk.tile < p.tiles) at = tile_at<WIDTH, false>(p, walk.tile);
+    if (walk.tile < p.tiles) at = tile_at<WIDTH, SYMMETRIC>(p, walk.tile);
   }
   __device__ __forceinline__ bool done(const ProductDev &p) const { return walk.tile >= p.tiles; }
   __device__ __forceinline__ int n() const { return at.q0 + unit * kUnit; }
   __device__ __forceinline__ int m() const { return at.p0 + row0; }
-  __device__ __forceinline__ bool inside(const ProductDev &p) const { return n() < p.N && m() < p.M; }
+  __device__ __forceinline__ bool inside(const ProductDev &p) const {
+    return n() < p.N && m() < p.M && (!SYMMETRIC || n() <= m());
+  }
   __device__ __forceinline__ void next(const ProductDev &p) {
     if (++unit < end) return;
     unit = first;
     walk.next();
-    if (walk.tile < p.tiles) at = tile_at<WIDTH, false>(p, walk.tile);
+    if (walk.tile < p.tiles) at = tile_at<WIDTH, SYMMETRIC>(p, walk.tile);
   }
 };
 
@@ -437,7 +428,7 @@ struct Shared {
 };
 
 // A warp's share of the epilogue of all of its CTA's tiles: units [first, end) of each.
-template <bool PAIR, typename F>
+template <bool PAIR, bool SYMMETRIC, typename F>
 __device__ __forceinline__ bool move_tiles(const Job &job, const Walk &walk, Shared &w, int first, int end, F release) {
   constexpr int kWidth = PAIR ? 2 * kP : kP, kAccCols = PAIR ? kPairQMax : kQMax;
   const ProductDev &p = job.d;
@@ -452,7 +443,7 @@ __device__ __forceinline__ bool move_tiles(const Job &job, const Walk &walk, Sha
     return true;
   }
   const uint32_t slots = w.buffers + p.ahead * p.ahead_bytes;
-  Units<kWidth> ahead(p, walk, first, end, w.row0), now = ahead;
+  Units<kWidth, SYMMETRIC> ahead(p, walk, first, end, w.row0), now = ahead;
   int asked = 0, used = 0, slot = 0, waiting = 0;
   // The residual of the next unit that has not been asked for.
   const auto ask = [&] {
@@ -552,6 +543,13 @@ __device__ __forceinline__ bool move_tiles(const Job &job, const Walk &walk, Sha
     const uint32_t at = free_slot();
     put_row(at, lane, p.out.type, x);
     send(&job.out, at);
+    if (SYMMETRIC && now.n() < now.m()) {  // and its mirror image
+      const uint32_t turned = free_slot();
+      put_column(turned, lane, x);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) tma_store_3d(&job.out, turned, now.m(), now.n(), now.at.z);
+    }
   }
   // What is on its way into shared memory has arrived, and what leaves it has been read, before
   // the buffers serve anything else and before the block exits.
@@ -569,16 +567,12 @@ __device__ __forceinline__ bool move_tiles(const Job &job, const Walk &walk, Sha
 // A warp's part of an accumulator: 32 lanes (columns n0, n0 + 1, .. of out), `chunks` times 16 of
 // its rows from m0 on.  begin() asks for what the first rows need, before the accumulator is
 // waited for; run() drains it, and calls `release` once the last column is in registers.
-template <int KIND>
-struct Drain;
-
 // A lane a column: a warp moves 32 neighbouring values of a row at a time.
-template <>
-struct Drain<kSingles> {
+struct Drain {
   int z, m0, n;
   float bias;
 
-  __device__ __forceinline__ void begin(const ProductDev &p, int z_, int m0_, int, int n0, int lane, bool, bool last) {
+  __device__ __forceinline__ void begin(const ProductDev &p, int z_, int m0_, int n0, int lane, bool last) {
     z = z_, m0 = m0_, n = n0 + lane;
     bias = last && p.bias.p && n < p.N ? load_one(p.bias, 0, 0, n) : 0.f;
   }
@@ -606,7 +600,7 @@ struct Drain<kSingles> {
   }
 
   template <typename F>
-  __device__ __forceinline__ void run(const ProductDev &p, uint32_t taddr, int chunks, float *, int, bool first,
+  __device__ __forceinline__ void run(const ProductDev &p, uint32_t taddr, int chunks, bool first,
                                       bool last, F release) {
     const bool add = p.residual.p && (p.fold ? first : last);
 #pragma unroll 1
@@ -642,102 +636,11 @@ struct Drain<kSingles> {
   }
 };
 
-// A lane's 16 values of a chunk are neighbours in the mirror image's row n, where the residual
-// (fp16 and symmetric itself) is read and one image is stored; the other one is turned around.
-// Both are fp16 with rows on 16-byte boundaries.
-template <>
-struct Drain<kSymmetric> {
-  uint4 next[2];
-  int z, m0, row;  // row: this lane's n
-
-  __device__ __forceinline__ bool needs(const ProductDev &p, int m) const {
-    return p.residual.p && row < p.N && row < m + 16 && m < p.M;
-  }
-  // Rows are padded to multiples of 64, so a whole chunk can be read.
-  __device__ __forceinline__ void load_residual(const ProductDev &p, int m) {
-    const uint4 *at = reinterpret_cast<const uint4 *>(element(p.residual, z, row, m));
-    next[0] = at[0], next[1] = at[1];
-  }
-  __device__ __forceinline__ void begin(const ProductDev &p, int z_, int m0_, int, int n0, int lane, bool, bool) {
-    z = z_, m0 = m0_;
-    row = n0 + lane;
-    if (needs(p, m0)) load_residual(p, m0);
-  }
-
-  template <typename F>
-  __device__ __forceinline__ void run(const ProductDev &p, uint32_t taddr, int chunks, float *buffer, int lane, bool,
-                                      bool, F release) {
-#pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
-      const int m = m0 + c * 16;
-      uint32_t v[16];
-      __syncwarp();
-      tmem_ld16(taddr + c * 16, v);
-      if (c == chunks - 1) release();
-      float x[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = p.scale * __uint_as_float(v[i]);
-      if (needs(p, m)) {
-        const uint32_t w[8] = {next[0].x, next[0].y, next[0].z, next[0].w, next[1].x, next[1].y, next[1].z, next[1].w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float lo, hi;
-          decode2(w[i], kTypeF16, lo, hi);
-          x[2 * i] = fmaf(p.residual_scale, lo, x[2 * i]);
-          x[2 * i + 1] = fmaf(p.residual_scale, hi, x[2 * i + 1]);
-        }
-      }
-      if (c + 1 < chunks && needs(p, m + 16)) load_residual(p, m + 16);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) buffer[i * kPitch + lane] = x[i];
-      if (row < p.N && m < p.M) {
-        __half *dst = reinterpret_cast<__half *>(element(p.out, z, row, m));
-        if (row < m && m + 16 <= p.M) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            reinterpret_cast<uint4 *>(dst)[i] =
-                make_uint4(pack2(x[8 * i], x[8 * i + 1], kTypeF16), pack2(x[8 * i + 2], x[8 * i + 3], kTypeF16),
-                           pack2(x[8 * i + 4], x[8 * i + 5], kTypeF16), pack2(x[8 * i + 6], x[8 * i + 7], kTypeF16));
-        } else {  // on the diagonal the values after it, at the edge those before it
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (row < m + i && m + i < p.M) dst[i] = __float2half_rn(x[i]);
-        }
-      }
-      __syncwarp();
-      const int n = row - lane + (lane & 3) * 8;
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        const int q = 8 * h + (lane >> 2), side = min(p.N - 1, m + q) - n + 1;  // values up to the diagonal
-        if (m + q >= p.M || side <= 0) continue;
-        float y[8];
-        load8(buffer + q * kPitch + (lane & 3) * 8, y);
-        if (side >= 8) {
-          store8(p.out, z, m + q, n, y);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (i < side) store_one(p.out, z, m + q, n + i, y[i]);
-        }
-      }
-    }
-  }
-};
-
 __device__ __noinline__ float activated_apart(float x, int act) { return activated(x, act); }
 
-// One sum of products of a tile that several CTAs share becomes outputs; of a symmetric product,
-// on the side n <= m, both images.
-template <bool SYMMETRIC>
+// One sum of products of a tile that several CTAs share becomes an output.
 __device__ __forceinline__ void finish_one(const ProductDev &p, int64_t z, int64_t m, int64_t n, float x, float bias,
                                            float residual) {
-  if constexpr (SYMMETRIC) {
-    if (n > m) return;
-    x += residual;
-    store_one(p.out, z, m, n, x);
-    if (n < m) store_one(p.out, z, n, m, x);
-    return;
-  }
   x += bias;
   if (p.pre.p) store_one(p.pre, z, m, n, x);
   if (p.act != ENGRAM_ACT_NONE) x = activated_apart(x, p.act);
@@ -753,7 +656,7 @@ __device__ __forceinline__ void finish_one(const ProductDev &p, int64_t z, int64
 template <bool PAIR, bool SPLIT, bool SYMMETRIC>
 __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : kThreads, SPLIT ? 2 : 1)
     product_kernel(const __grid_constant__ Jobs jobs) {
-  static_assert(!(PAIR && SPLIT));
+  static_assert(!(PAIR && SPLIT) && !(SYMMETRIC && SPLIT));
   constexpr uint32_t kCols = SPLIT ? kSplitTmemCols : kTmemCols;
   constexpr int kAccCols = PAIR ? kPairQMax : kQMax;
   constexpr int kTileP = PAIR ? 2 * kP : kP;
@@ -957,45 +860,46 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : 
     const auto drain_all = [&](const Job &job) {
       const ProductDev &p = job.d;
       const int qt = p.q_tile;
-      if constexpr (!SPLIT && !SYMMETRIC) {
-        if (p.rows) {
+      if constexpr (!SPLIT) {
+        if (SYMMETRIC || p.rows) {
           const int units = qt / kUnit;
           w.buffers = smem_u32(sm) + stages * stage_bytes + (warp - 4) * (p.ahead * p.ahead_bytes + p.slots * p.slot_bytes);
-          ok = move_tiles<PAIR>(job, Walk(p, worker, workers), w, units * part / kPartsHere,
+          ok = move_tiles<PAIR, SYMMETRIC>(job, Walk(p, worker, workers), w, units * part / kPartsHere,
                                 units * (part + 1) / kPartsHere, release);
           return;
         }
       }
-      // This warp's 16-column chunks: a part of the tile's.
-      const int c0 = qt / 16 * part / kPartsHere, chunks = qt / 16 * (part + 1) / kPartsHere - c0;
-      float *buffer = reinterpret_cast<float *>(sm + stages * stage_bytes + (warp - 4) * kBufferBytes);
-      for (Walk walk(p, worker, workers); ok && walk.tile < p.tiles; walk.next()) {
-        const Tile t = tile_at<kTileP, SYMMETRIC>(p, walk.tile);
-        const int n0 = t.p0 + w.row0, m0 = t.q0 + c0 * 16;
-        for (int seg = 0; seg < p.segments; ++seg, ++w.unit) {
-          const uint32_t acc = SPLIT ? 0 : w.unit & 1, use = w.unit >> 1;
-          const bool first = seg == 0, last = seg == p.segments - 1;
-          Drain<SYMMETRIC ? kSymmetric : kSingles> drain;
-          if constexpr (!SPLIT) drain.begin(p, t.z, m0, chunks, n0, lane, first, last);
-          ok = warp_wait(acc_full + acc, use & 1, abort_flag, p);
-          if (!ok) break;
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t taddr = w.tmem + acc * kAccCols + c0 * 16;
-          if constexpr (SPLIT) {
-            // The partial tile into shared memory (the stages: every MMA has read them).
-            float *mine = reinterpret_cast<float *>(sm) + c0 * 16 * kP + quad * 32 + lane;
-            for (int c = 0; c < chunks; ++c) {
-              uint32_t v[16];
-              tmem_ld16(taddr + c * 16, v);
+      if constexpr (!SYMMETRIC) {
+        // This warp's 16-column chunks: a part of the tile's.
+        const int c0 = qt / 16 * part / kPartsHere, chunks = qt / 16 * (part + 1) / kPartsHere - c0;
+          for (Walk walk(p, worker, workers); ok && walk.tile < p.tiles; walk.next()) {
+          const Tile t = tile_at<kTileP, SYMMETRIC>(p, walk.tile);
+          const int n0 = t.p0 + w.row0, m0 = t.q0 + c0 * 16;
+          for (int seg = 0; seg < p.segments; ++seg, ++w.unit) {
+            const uint32_t acc = SPLIT ? 0 : w.unit & 1, use = w.unit >> 1;
+            const bool first = seg == 0, last = seg == p.segments - 1;
+            Drain drain;
+            if constexpr (!SPLIT) drain.begin(p, t.z, m0, n0, lane, last);
+            ok = warp_wait(acc_full + acc, use & 1, abort_flag, p);
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t taddr = w.tmem + acc * kAccCols + c0 * 16;
+            if constexpr (SPLIT) {
+              // The partial tile into shared memory (the stages: every MMA has read them).
+              float *mine = reinterpret_cast<float *>(sm) + c0 * 16 * kP + quad * 32 + lane;
+              for (int c = 0; c < chunks; ++c) {
+                uint32_t v[16];
+                tmem_ld16(taddr + c * 16, v);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) mine[(c * 16 + i) * kP] = __uint_as_float(v[i]);
+                for (int i = 0; i < 16; ++i) mine[(c * 16 + i) * kP] = __uint_as_float(v[i]);
+              }
+              break;
             }
-            break;
+            if (chunks == 0)  // a tile of 16 columns has nothing for the second part
+              release(acc);
+            else
+              drain.run(p, taddr, chunks, first, last, [&] { release(acc); });
           }
-          if (chunks == 0)  // a tile of 16 columns has nothing for the second part
-            release(acc);
-          else
-            drain.run(p, taddr, chunks, buffer, lane, first, last, [&] { release(acc); });
         }
       }
     };
@@ -1030,7 +934,7 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : 
       const float residual = p.residual.p ? p.residual_scale * load_one(p.residual, t.z, m, n) : 0.f;
 #pragma unroll
       for (int r = 1; r < 8; ++r) v[0] += v[r];
-      finish_one<SYMMETRIC>(p, t.z, m, n, p.scale * v[0], bias, residual);
+      finish_one(p, t.z, m, n, p.scale * v[0], bias, residual);
     }
     cluster_sync();  // no CTA leaves while another may still read its part
   }
@@ -1098,7 +1002,7 @@ enum Form { kSingle, kSplit, kPair, kForms };
 Kernel kernel_of(int form, bool symmetric) {
   static constexpr Kernel all[kForms][2] = {
       {product_kernel<false, false, false>, product_kernel<false, false, true>},
-      {product_kernel<false, true, false>, product_kernel<false, true, true>},
+      {product_kernel<false, true, false>, nullptr},
       {product_kernel<true, false, false>, product_kernel<true, false, true>}};
   return all[form][symmetric];
 }
@@ -1112,7 +1016,7 @@ cudaError_t device_info(DeviceInfo &out) {
   if (!d.ready) {
     e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
     for (int i = 0; i < 2 * kForms && e == cudaSuccess; ++i)
-      e = cudaFuncSetAttribute(kernel_of(i / 2, i & 1), cudaFuncAttributeMaxDynamicSharedMemorySize,
+      if (kernel_of(i / 2, i & 1)) e = cudaFuncSetAttribute(kernel_of(i / 2, i & 1), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)(i / 2 == kSplit ? kSplitSmemBytes : kSmemBytes));
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
@@ -1140,9 +1044,9 @@ int64_t tiles_of(int64_t P, int64_t Q, int width, int qt, bool symmetric) {
   const int64_t tp = ceil_div(P, width), tq = ceil_div(Q, qt);
   if (!symmetric) return tp * tq;
   int64_t n = 0;
-  for (int64_t q = 0; q < tq; ++q) {
-    const int64_t end = Q < (q + 1) * qt ? Q : (q + 1) * qt, wide = (end - 1) / width + 1;
-    n += tp < wide ? tp : wide;
+  for (int64_t i = 0; i < tp; ++i) {
+    const int64_t end = P < (i + 1) * width ? P : (i + 1) * width, wide = (end - 1) / qt + 1;
+    n += tq < wide ? tq : wide;
   }
   return n;
 }
@@ -1206,7 +1110,7 @@ Facts facts_of(const ProductParams &p) {
   }
   // The tiles' epilogue wants rows on 16-byte boundaries (a row that repeats has none apart).
   const auto moves = [&](const PlaneDev &x) { return !x.p || (x.vec && (p.M == 1 || x.stride >= p.N)); };
-  f.tiles_epilogue = !p.symmetric && d.segments == 1 && moves(d.out) && moves(d.pre) && moves(d.residual);
+  f.tiles_epilogue = d.segments == 1 && moves(d.out) && moves(d.pre) && moves(d.residual);
   return f;
 }
 
@@ -1225,7 +1129,7 @@ Plan plan_form(const ProductParams &p, const Facts &f, int form, bool rows, cons
   if (workers <= 0 || (pair && P <= kP)) return best;
   const double kb = f.d.kblocks;
   const auto bytes = [](const PlaneDev &x) { return !x.p ? 0 : x.type == ENGRAM_DTYPE_F32 ? 4 : 2; };
-  const double moved = (1 + bytes(f.d.out) + bytes(f.d.residual) + bytes(f.d.pre)) / 3.;
+  const double moved = (1 + bytes(f.d.out) * (p.symmetric ? 2 : 1) + bytes(f.d.residual) + bytes(f.d.pre)) / 3.;
   for (int qt = pair ? kPairQMax : kQMax; qt >= step; qt -= step) {
     if (qt - step >= Q) continue;  // wider than Q
     Plan n;
@@ -1271,12 +1175,12 @@ Plan plan_split(const ProductParams &p, const Facts &f, const DeviceInfo &info) 
 }
 
 // Rows of out in the lanes where the tiles' epilogue can move it, and there are rows to fill them.
-bool rows_of(const ProductParams &p, const Facts &f) { return f.tiles_epilogue && p.M > 64; }
+bool rows_of(const ProductParams &p, const Facts &f) { return f.tiles_epilogue && (p.symmetric || p.M > 64); }
 
 Plan plan_of(const ProductParams &p, const Facts &f, const DeviceInfo &info) {
   const bool rows = rows_of(p, f);
   Plan best = plan_form(p, f, kSingle, rows, info);
-  for (const Plan &n : {plan_form(p, f, kPair, rows, info), plan_split(p, f, info)})
+  for (const Plan &n : {plan_form(p, f, kPair, rows, info), p.symmetric ? Plan() : plan_split(p, f, info)})
     if (n.us < best.us) best = n;
   return best;
 }
@@ -1288,7 +1192,7 @@ int64_t stage_bytes_of(const ProductParams &p, const Plan &plan) {
   return kPBytes + ((plan.rows ? p.b : p.a).t ? (staged + 63) / 64 * 64 : staged) * 128;
 }
 int64_t reserve_of(const ProductParams &p, int64_t stage) {
-  return (p.K <= 16 * kBK ? kProducers : 5) * stage;
+  return (p.K <= 4 * kBK ? kProducers : 5) * stage;
 }
 
 // A job of a plan; its share of the shared memory (the epilogue's buffers) in `buffers`, which leave
@@ -1306,7 +1210,7 @@ cudaError_t job_of(const ProductParams &p, const Facts &f, const Plan &plan, int
   const int q_staged = plan.form == kPair ? plan.q_tile / 2 : plan.q_tile;
   d.q_rows = (int32_t)((stage_bytes_of(p, plan) - kPBytes) / 128);
   const int warps = 4 * (plan.form == kPair ? kPairParts : kParts);
-  buffers = p.symmetric ? warps * (int64_t)kBufferBytes : 0;
+  buffers = 0;
   if (plan.rows) {
     // One buffer of each sort at least.
     d.ahead_bytes = unit_bytes(d.residual);

@@ -3,10 +3,12 @@
 // start on 16 bytes.
 //
 // act_grad_kernel walks slabs of rows, 8 (or 1, where rows are not aligned) neighbouring columns
-// a lane: dz = dy act'(z) is stored as bf16, the operand of the products (rounded once, at most
-// 2^-9 of the value), and summed in fp32 before that rounding; a block adds its warps' sums in
-// order, a second kernel the slabs', so the result does not depend on timing.  Bound by HBM.
+// a thread: dz = dy act'(z) is stored as bf16, the operand of the products (rounded once, at most
+// 2^-9 of the value), and summed in fp32 before that rounding; a block adds its rows' sums in
+// order, of more than 1024 rows a second kernel the slabs', so the result does not depend on timing.  Bound by HBM.
 #include <math.h>
+
+#include <type_traits>
 
 #include "launch.cuh"
 #include "values.cuh"
@@ -14,23 +16,23 @@
 namespace engram {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kThreads = 256, kMostThreads = 1024;
 
 template <int VEC, typename T>
 __device__ __forceinline__ void load_vec(const T *src, int count, float (&x)[VEC]) {
   if constexpr (VEC == 8) {
     alignas(16) T v[8];
     if constexpr (sizeof(T) == 2) {
-      *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(src);
+      *reinterpret_cast<uint4 *>(v) = __ldg(reinterpret_cast<const uint4 *>(src));
     } else {
-      reinterpret_cast<uint4 *>(v)[0] = reinterpret_cast<const uint4 *>(src)[0];
-      reinterpret_cast<uint4 *>(v)[1] = reinterpret_cast<const uint4 *>(src)[1];
+      reinterpret_cast<uint4 *>(v)[0] = __ldg(reinterpret_cast<const uint4 *>(src));
+      reinterpret_cast<uint4 *>(v)[1] = __ldg(reinterpret_cast<const uint4 *>(src) + 1);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = to_float(v[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) x[i] = i < count ? to_float(src[i]) : 0.f;
+    for (int i = 0; i < VEC; ++i) x[i] = i < count ? to_float(__ldg(src + i)) : 0.f;
   }
 }
 
@@ -45,58 +47,88 @@ __device__ __forceinline__ float through(float dy, float z, int act) {
   return dy * (0.5f * (1.f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z));
 }
 
-template <int VEC, typename TY, typename TZ>
-__global__ void __launch_bounds__(kWarps * 32) act_grad_kernel(const ActGradParams p) {
+// DEEP rows, `step` apart, of a thread's VEC columns: all loads, then the rest.
+template <int VEC, int DEEP, typename TY, typename TZ>
+__device__ __forceinline__ void some_rows(const ActGradParams &p, const TY *dy, const TZ *pre, __nv_bfloat16 *dz,
+                                          int64_t step, int count, float (&sum)[VEC]) {
+  constexpr bool kAct = !std::is_same_v<TZ, void>;
+  float x[DEEP][VEC], z[DEEP][VEC];
+#pragma unroll
+  for (int d = 0; d < DEEP; ++d) {
+    load_vec<VEC>(dy + d * step * p.dy_stride, count, x[d]);
+    if constexpr (kAct) load_vec<VEC>(pre + d * step * p.pre_stride, count, z[d]);
+  }
+#pragma unroll
+  for (int d = 0; d < DEEP; ++d) {
+    if constexpr (kAct) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) x[d][i] = through(x[d][i], z[d][i], p.act);
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) sum[i] += x[d][i];
+    if (p.dz) {
+      __nv_bfloat16 *to = dz + d * step * p.dz_stride;
+      if constexpr (VEC == 8) {
+        alignas(16) __nv_bfloat16 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) from_float(v[i], x[d][i]);
+        *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(v);
+      } else {
+        from_float(*to, x[d][0]);
+      }
+    }
+  }
+}
+
+// A block has `lanes` threads a row, VEC columns each.  TZ void: no activation.
+template <int VEC, int THREADS, typename TY, typename TZ>
+__global__ void __launch_bounds__(THREADS) act_grad_kernel(const ActGradParams p) {
   dependency_wait();
-  __shared__ float sums[kWarps][32 * VEC + 1];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t col = (int64_t)(blockIdx.x % p.col_blocks) * 32 * VEC + lane * VEC;
+  __shared__ float sums[THREADS * VEC];
+  const int lanes = p.lanes, rows = THREADS / lanes, row = threadIdx.x / lanes, at = threadIdx.x & (lanes - 1);
+  const int64_t col0 = (int64_t)(blockIdx.x % p.col_blocks) * lanes * VEC, col = col0 + at * VEC;
   const int64_t slab = blockIdx.x / p.col_blocks;
   const int count = (int)min((int64_t)VEC, p.N - col);
-  const int64_t end = min(p.M, (slab + 1) * p.slab_rows);
   float sum[VEC];
 #pragma unroll
   for (int i = 0; i < VEC; ++i) sum[i] = 0.f;
   if (count > 0) {
-    const TY *dy = static_cast<const TY *>(p.dy) + col;
-    const TZ *pre = static_cast<const TZ *>(p.pre) + col;
-    __nv_bfloat16 *dz = static_cast<__nv_bfloat16 *>(p.dz) + col;
-#pragma unroll 2
-    for (int64_t m = slab * p.slab_rows + warp; m < end; m += kWarps) {
-      float x[VEC];
-      load_vec<VEC>(dy + m * p.dy_stride, count, x);
-      if (p.pre) {
-        float z[VEC];
-        load_vec<VEC>(pre + m * p.pre_stride, count, z);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) x[i] = through(x[i], z[i], p.act);
-      }
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) sum[i] += x[i];
-      if (p.dz) {
-        if constexpr (VEC == 8) {
-          alignas(16) __nv_bfloat16 v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) from_float(v[i], x[i]);
-          *reinterpret_cast<uint4 *>(dz + m * p.dz_stride) = *reinterpret_cast<const uint4 *>(v);
-        } else {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i)
-            if (i < count) from_float(dz[m * p.dz_stride + i], x[i]);
-        }
-      }
-    }
+    constexpr int kDeep = VEC == 1 ? 4 : 2;
+    const int64_t m = slab * p.slab_rows + row, end = min(p.M, (slab + 1) * p.slab_rows);
+    int left = m < end ? (int)((end - 1 - m) / rows + 1) : 0;
+    const TY *dy = static_cast<const TY *>(p.dy) + m * p.dy_stride + col;
+    const TZ *pre = nullptr;
+    if constexpr (!std::is_same_v<TZ, void>) pre = static_cast<const TZ *>(p.pre) + m * p.pre_stride + col;
+    __nv_bfloat16 *dz = static_cast<__nv_bfloat16 *>(p.dz) + m * p.dz_stride + col;
+    const auto move = [&](int n) {
+      dy += n * rows * p.dy_stride;
+      if constexpr (!std::is_same_v<TZ, void>) pre += n * rows * p.pre_stride;
+      dz += n * rows * p.dz_stride;
+      left -= n;
+    };
+    for (; left >= kDeep; move(kDeep)) some_rows<VEC, kDeep, TY, TZ>(p, dy, pre, dz, rows, count, sum);
+#pragma unroll 1
+    for (; left > 0; move(1)) some_rows<VEC, 1, TY, TZ>(p, dy, pre, dz, rows, count, sum);
   }
   if (!p.dbias) return;
+  // sums[row][column of the block]
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) sums[warp][lane * VEC + i] = sum[i];
+  for (int i = 0; i < VEC; ++i) sums[(row * lanes + at) * VEC + i] = sum[i];
   __syncthreads();
-  for (int i = threadIdx.x; i < 32 * VEC; i += kWarps * 32) {
-    const int64_t n = (int64_t)(blockIdx.x % p.col_blocks) * 32 * VEC + i;
-    if (n >= p.N) break;
-    float s = sums[0][i];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) s += sums[w][i];
+  // First the rows in a few groups, then those.
+  const int columns = lanes * VEC, groups = columns < THREADS ? THREADS / columns : 1;
+  if (groups > 1) {
+    const int i = threadIdx.x % columns, share = rows / groups, r0 = threadIdx.x / columns * share;
+    float s = sums[r0 * columns + i];
+    for (int r = 1; r < share; ++r) s += sums[(r0 + r) * columns + i];
+    sums[r0 * columns + i] = s;
+    __syncthreads();
+  }
+  const int step = rows / groups;
+  for (int i = threadIdx.x; i < columns && col0 + i < p.N; i += THREADS) {
+    float s = sums[i];
+    for (int r = groups > 1 ? step : 1; r < rows; r += groups > 1 ? step : 1) s += sums[r * columns + i];
+    const int64_t n = col0 + i;
     if (p.slabs == 1)
       p.dbias[n] = p.accumulate ? p.dbias[n] + s : s;
     else
@@ -129,33 +161,51 @@ __global__ void __launch_bounds__(256) pack_kernel(const uint16_t *src, int64_t 
 }
 
 constexpr int kMaxSlabs = 64;
+constexpr int64_t kOneSlab = 1024;  // up to so many rows a block takes them all, and nothing is joined
 
 bool vectors(const void *p, int64_t stride, int type) {
   const int64_t step = type == ENGRAM_DTYPE_F32 ? 4 : 8;
   return !p || (((uintptr_t)p & 15) == 0 && stride % step == 0);
 }
 
+template <int VEC, typename TY, typename TZ>
+cudaError_t launch_threads(const ActGradParams &p, int64_t grid, cudaStream_t stream) {
+  if (p.threads == kThreads) return launch(act_grad_kernel<VEC, kThreads, TY, TZ>, grid, kThreads, 0, stream, 1, p);
+  return launch(act_grad_kernel<VEC, kMostThreads, TY, TZ>, grid, kMostThreads, 0, stream, 1, p);
+}
 template <int VEC, typename TY>
 cudaError_t launch_typed(const ActGradParams &p, int64_t grid, cudaStream_t stream) {
-  if (p.pre_type == ENGRAM_DTYPE_F32)
-    return launch(act_grad_kernel<VEC, TY, float>, grid, kWarps * 32, 0, stream, 1, p);
-  return launch(act_grad_kernel<VEC, TY, __nv_bfloat16>, grid, kWarps * 32, 0, stream, 1, p);
+  if (!p.pre) return launch_threads<VEC, TY, void>(p, grid, stream);
+  if (p.pre_type == ENGRAM_DTYPE_F32) return launch_threads<VEC, TY, float>(p, grid, stream);
+  return launch_threads<VEC, TY, __nv_bfloat16>(p, grid, stream);
 }
 
 }  // namespace
 
-size_t act_grad_partial_bytes(int64_t M, int64_t N) { return M > 32 ? (size_t)kMaxSlabs * N * sizeof(float) : 0; }
+size_t act_grad_partial_bytes(int64_t M, int64_t N) {
+  return M > kOneSlab ? (size_t)kMaxSlabs * N * sizeof(float) : 0;
+}
 
 cudaError_t launch_act_grad(ActGradParams p, cudaStream_t stream) {
   const bool wide = p.N % 8 == 0 && vectors(p.dy, p.dy_stride, p.dy_type) && vectors(p.pre, p.pre_stride, p.pre_type) &&
                     vectors(p.dz, p.dz_stride, ENGRAM_DTYPE_BF16);
   const int vec = wide ? 8 : 1;
-  p.col_blocks = (int32_t)((p.N + 32 * vec - 1) / (32 * vec));
-  // About eight blocks an SM, each of 32 rows at least.
-  int64_t slabs = 8 * kSms / p.col_blocks;
-  if (slabs > (p.M + 31) / 32) slabs = (p.M + 31) / 32;
-  if (slabs > kMaxSlabs) slabs = kMaxSlabs;
-  if (slabs < 1) slabs = 1;
+  // As many blocks as run at once, each of 32 rows at least; of few rows, blocks of fewer columns.
+  int64_t slabs = 1;
+  p.lanes = 32;
+  p.threads = kThreads;
+  const auto blocks = [&] { return (p.N + p.lanes * vec - 1) / (p.lanes * vec); };
+  if (p.M > kOneSlab) {
+    slabs = (vec == 8 ? 4 : 5) * kSms / blocks();
+    if (slabs > (p.M + 31) / 32) slabs = (p.M + 31) / 32;
+    if (slabs > kMaxSlabs) slabs = kMaxSlabs;
+    if (slabs < 1) slabs = 1;
+  } else {
+    const int least = vec == 8 ? 4 : 16;
+    if (p.M > kThreads / 8) p.threads = kMostThreads;
+    while (p.lanes > least && p.threads / p.lanes < p.M && blocks() < kSms) p.lanes /= 2;
+  }
+  p.col_blocks = (int32_t)blocks();
   p.slab_rows = (p.M + slabs - 1) / slabs;
   p.slabs = (int32_t)((p.M + p.slab_rows - 1) / p.slab_rows);
   const int64_t grid = (int64_t)p.col_blocks * p.slabs;

@@ -63,7 +63,7 @@ struct ActGradParams {
   int32_t dy_type, pre_type, act;
   bool accumulate;  // dbias is added to
   // set by the launcher
-  int32_t slabs, col_blocks;
+  int32_t slabs, col_blocks, lanes, threads;
   int64_t slab_rows;
 };
 size_t act_grad_partial_bytes(int64_t M, int64_t N);
