@@ -19,9 +19,9 @@
 // one thread (of the pair's even CTA) issues the MMAs into one of two accumulators; 4.. epilogue.
 //
 // The fp32 accumulator of the tensor cores does not round to nearest: its error grows with the
-// number of additions.  For fp32 outputs K is cut into segments of at most 8192 that each start
-// a new accumulator, and the epilogue adds them to the sum so far, which it keeps in out,
-// rounding to nearest.
+// number of additions (1e-9 of the result for each value of K, against 1e-6 of an fp32 sum of
+// 8192).  So where out or pre is fp32, K is cut into segments of at most 512 that each start a new
+// accumulator, and the epilogue adds them in registers, rounding to nearest.
 //
 // A symmetric product (both operands one matrix) computes the tiles on one side of the diagonal
 // and stores every value twice, the second time transposed: a lane's 16 values of a chunk are
@@ -49,7 +49,7 @@ constexpr int kPairQMax = 256;  // and of a pair
 constexpr int kParts = 4, kPairParts = 4;
 constexpr int kThreads = 128 * (1 + kParts), kPairThreads = 128 * (1 + kPairParts);
 constexpr int kSplitParts = 2, kSplitThreads = 128 * (1 + kSplitParts);
-constexpr int kSegmentBlocks = 128;
+constexpr int kSegmentBlocks = 8;
 constexpr int kMaxStages = 12, kMaxAhead = 4, kProducers = 3;
 constexpr uint32_t kPBytes = kP * kBK * 2;
 constexpr uint32_t kBarBytes = 1024;
@@ -94,7 +94,6 @@ struct ProductDev {
   int32_t shift, extra;
   bool p_t, q_t, many;
   bool rows;      // rows of out in the lanes; else its columns
-  bool fold;      // the residual goes into the first segment's sum (it lies where out does)
   bool withhold;  // test hook: the first stage waits for bytes that never come
 };
 
@@ -427,12 +426,127 @@ struct Shared {
   uint32_t unit, phases;      // accumulators drained so far; the parities of `arrived`
 };
 
+// How a warp moves units: its buffers for what comes in (`ahead` of them) and goes out.
+template <bool SYMMETRIC>
+struct Mover {
+  const Job &job;
+  const ProductDev &p;
+  Shared &w;
+  int asked = 0, used = 0, slot = 0, waiting = 0;
+
+  __device__ __forceinline__ Mover(const Job &j, Shared &shared) : job(j), p(j.d), w(shared) {}
+
+  // Asks for the residual of a unit.
+  __device__ __forceinline__ void ask(int n, int m, int z) {
+    if (w.lane == 0) {
+      if (p.slots == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      mbar_arrive_expect_tx(w.arrived + asked, p.ahead_bytes);
+      tma_load_3d<false>(w.buffers + asked * p.ahead_bytes, &job.residual, n, m, z, smem_u32(w.arrived + asked));
+    }
+    asked = asked + 1 == p.ahead ? 0 : asked + 1;
+    ++waiting;
+  }
+
+  // A free buffer: of the stores before, all but slots - 1 have been read.
+  __device__ __forceinline__ uint32_t free_slot() {
+    if (w.lane == 0) {
+      if (p.slots == 1)
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      else
+        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    }
+    __syncwarp();
+    const uint32_t at = w.buffers + p.ahead * p.ahead_bytes + slot * p.slot_bytes;
+    slot = slot + 1 == p.slots ? 0 : slot + 1;
+    return at;
+  }
+  __device__ __forceinline__ void send(const CUtensorMap *map, uint32_t from, int n, int m, int z) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (w.lane == 0) tma_store_3d(map, from, n, m, z);
+  }
+
+  __device__ __forceinline__ void add_bias(int n, float (&x)[kUnit]) {
+    if (n + kUnit <= p.N && p.bias.vec) {  // the same 32 values in every lane
+      if (p.bias.type == ENGRAM_DTYPE_F32) {
+        const float4 *at = reinterpret_cast<const float4 *>(static_cast<const float *>(p.bias.p) + n);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float4 b = __ldg(at + j);
+          x[4 * j] += b.x, x[4 * j + 1] += b.y, x[4 * j + 2] += b.z, x[4 * j + 3] += b.w;
+        }
+      } else {
+        const uint4 *at = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias.p) + n);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 b = __ldg(at + j);
+          const uint32_t words[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[8 * j + 2 * i] += __uint_as_float(words[i] << 16);
+            x[8 * j + 2 * i + 1] += __uint_as_float(words[i] & 0xffff0000u);
+          }
+        }
+      }
+    } else {
+      // A lane a value; past the edge nothing is kept.
+      const float mine = n + w.lane < p.N ? load_one(p.bias, 0, 0, n + w.lane) : 0.f;
+#pragma unroll
+      for (int i = 0; i < kUnit; ++i) x[i] += __shfl_sync(0xffffffffu, mine, i);
+    }
+  }
+
+  // Sums of products of the unit at (m, n) become outputs; false if its residual did not arrive.
+  __device__ __forceinline__ bool finish(int n, int m, int z, float (&x)[kUnit]) {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) x[i] *= p.scale;
+    if (p.bias.p) add_bias(n, x);
+    if (p.pre.p) {
+      const uint32_t at = free_slot();
+      put_row(at, w.lane, p.pre.type, x);
+      send(&job.pre, at, n, m, z);
+    }
+    activate(x, p.act);
+    uint32_t at = 0;
+    if (p.ahead) {
+      if (!warp_wait(w.arrived + used, (w.phases >> used) & 1, w.abort_flag, p)) return false;
+      w.phases ^= 1u << used;
+      at = w.buffers + used * p.ahead_bytes;
+      add_row(at, w.lane, p.residual.type, p.residual_scale, x);
+      used = used + 1 == p.ahead ? 0 : used + 1;
+      --waiting;
+      __syncwarp();
+    }
+    if (p.slots) at = free_slot();  // else out goes where the residual came
+    put_row(at, w.lane, p.out.type, x);
+    send(&job.out, at, n, m, z);
+    if (SYMMETRIC && n < m) {  // and its mirror image
+      const uint32_t turned = free_slot();
+      put_column(turned, w.lane, x);
+      send(&job.out, turned, m, n, z);
+    }
+    return true;
+  }
+
+  // What is on its way into shared memory has arrived, and what leaves it has been read, before
+  // the buffers serve anything else and before the block exits.
+  __device__ __forceinline__ void end() {
+    if (w.lane == 0) {
+      for (; waiting > 0; --waiting) {  // after a wait that gave up
+        drain_phase(w.arrived + used, (w.phases >> used) & 1, p.wait_limit_ns);
+        used = used + 1 == p.ahead ? 0 : used + 1;
+      }
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    }
+    __syncwarp();
+  }
+};
+
 // A warp's share of the epilogue of all of its CTA's tiles: units [first, end) of each.
 template <bool PAIR, bool SYMMETRIC, typename F>
 __device__ __forceinline__ bool move_tiles(const Job &job, const Walk &walk, Shared &w, int first, int end, F release) {
   constexpr int kWidth = PAIR ? 2 * kP : kP, kAccCols = PAIR ? kPairQMax : kQMax;
   const ProductDev &p = job.d;
-  const int lane = w.lane;
   if (first == end) {  // a narrow tile has nothing for this part
     for (Walk k = walk; k.tile < p.tiles; k.next()) {
       const uint32_t acc = w.unit & 1;
@@ -442,39 +556,14 @@ __device__ __forceinline__ bool move_tiles(const Job &job, const Walk &walk, Sha
     }
     return true;
   }
-  const uint32_t slots = w.buffers + p.ahead * p.ahead_bytes;
+  Mover<SYMMETRIC> mover(job, w);
   Units<kWidth, SYMMETRIC> ahead(p, walk, first, end, w.row0), now = ahead;
-  int asked = 0, used = 0, slot = 0, waiting = 0;
   // The residual of the next unit that has not been asked for.
   const auto ask = [&] {
     while (!ahead.done(p) && !ahead.inside(p)) ahead.next(p);
     if (ahead.done(p)) return;
-    if (lane == 0) {
-      mbar_arrive_expect_tx(w.arrived + asked, p.ahead_bytes);
-      tma_load_3d<false>(w.buffers + asked * p.ahead_bytes, &job.residual, ahead.n(), ahead.m(), ahead.at.z,
-                         smem_u32(w.arrived + asked));
-    }
-    asked = asked + 1 == p.ahead ? 0 : asked + 1;
-    ++waiting;
+    mover.ask(ahead.n(), ahead.m(), ahead.at.z);
     ahead.next(p);
-  };
-  // A free buffer: of the stores before, all but slots - 1 have been read.
-  const auto free_slot = [&] {
-    if (lane == 0) {
-      if (p.slots == 1)
-        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-      else
-        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-    }
-    __syncwarp();
-    const uint32_t at = slots + slot * p.slot_bytes;
-    slot = slot + 1 == p.slots ? 0 : slot + 1;
-    return at;
-  };
-  const auto send = [&](const CUtensorMap *map, uint32_t from) {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncwarp();
-    if (lane == 0) tma_store_3d(map, from, now.n(), now.m(), now.at.z);
   };
   for (int i = 0; i < p.ahead; ++i) ask();
   bool ok = true;
@@ -494,147 +583,150 @@ __device__ __forceinline__ bool move_tiles(const Job &job, const Walk &walk, Sha
     if (!now.inside(p)) continue;
     float x[kUnit];
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i) x[i] = p.scale * __uint_as_float(v[i]);
-    if (p.bias.p) {
-      const int n = now.n();
-      if (n + kUnit <= p.N && p.bias.vec) {  // the same 32 values in every lane
-        if (p.bias.type == ENGRAM_DTYPE_F32) {
-          const float4 *at = reinterpret_cast<const float4 *>(static_cast<const float *>(p.bias.p) + n);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 b = __ldg(at + j);
-            x[4 * j] += b.x, x[4 * j + 1] += b.y, x[4 * j + 2] += b.z, x[4 * j + 3] += b.w;
-          }
-        } else {
-          const uint4 *at = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias.p) + n);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 b = __ldg(at + j);
-            const uint32_t words[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              x[8 * j + 2 * i] += __uint_as_float(words[i] << 16);
-              x[8 * j + 2 * i + 1] += __uint_as_float(words[i] & 0xffff0000u);
-            }
-          }
-        }
-      } else {
-        // A lane a value; past the edge nothing is kept.
-        const float mine = n + lane < p.N ? load_one(p.bias, 0, 0, n + lane) : 0.f;
-#pragma unroll
-        for (int i = 0; i < kUnit; ++i) x[i] += __shfl_sync(0xffffffffu, mine, i);
-      }
-    }
-    if (p.pre.p) {
-      const uint32_t at = free_slot();
-      put_row(at, lane, p.pre.type, x);
-      send(&job.pre, at);
-    }
-    activate(x, p.act);
-    if (p.ahead) {
-      if (!(ok = warp_wait(w.arrived + used, (w.phases >> used) & 1, w.abort_flag, p))) break;
-      w.phases ^= 1u << used;
-      add_row(w.buffers + used * p.ahead_bytes, lane, p.residual.type, p.residual_scale, x);
-      used = used + 1 == p.ahead ? 0 : used + 1;
-      --waiting;
-      __syncwarp();
-      ask();
-    }
-    const uint32_t at = free_slot();
-    put_row(at, lane, p.out.type, x);
-    send(&job.out, at);
-    if (SYMMETRIC && now.n() < now.m()) {  // and its mirror image
-      const uint32_t turned = free_slot();
-      put_column(turned, lane, x);
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) tma_store_3d(&job.out, turned, now.m(), now.n(), now.at.z);
-    }
+    for (int i = 0; i < kUnit; ++i) x[i] = __uint_as_float(v[i]);
+    if (!(ok = mover.finish(now.n(), now.m(), now.at.z, x))) break;
+    if (p.ahead) ask();
   }
-  // What is on its way into shared memory has arrived, and what leaves it has been read, before
-  // the buffers serve anything else and before the block exits.
-  if (lane == 0) {
-    for (; waiting > 0; --waiting) {  // after a wait that gave up
-      drain_phase(w.arrived + used, (w.phases >> used) & 1, p.wait_limit_ns);
-      used = used + 1 == p.ahead ? 0 : used + 1;
-    }
-    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-  }
-  __syncwarp();
+  mover.end();
   return ok;
 }
 
-// A warp's part of an accumulator: 32 lanes (columns n0, n0 + 1, .. of out), `chunks` times 16 of
-// its rows from m0 on.  begin() asks for what the first rows need, before the accumulator is
-// waited for; run() drains it, and calls `release` once the last column is in registers.
-// A lane a column: a warp moves 32 neighbouring values of a row at a time.
-struct Drain {
-  int z, m0, n;
-  float bias;
-
-  __device__ __forceinline__ void begin(const ProductDev &p, int z_, int m0_, int n0, int lane, bool last) {
-    z = z_, m0 = m0_, n = n0 + lane;
-    bias = last && p.bias.p && n < p.N ? load_one(p.bias, 0, 0, n) : 0.f;
-  }
-
-  static __device__ __forceinline__ void load(const PlaneDev &s, int z, int m, int n, int count, float (&x)[16]) {
-    by_type(s.type, [&](auto *type) {
-      auto *src = reinterpret_cast<decltype(type)>(element(s, z, m, n));
+// Adds a tile's segments: `chunks` times 16 columns of the accumulators from `column` on.
+template <int KACC, int COLUMNS, typename F>
+__device__ __forceinline__ bool add_segments(const ProductDev &p, Shared &w, int column, int chunks,
+                                             float (&sums)[COLUMNS], F release) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        x[i] = i < count ? to_float(*src) : 0.f;
-        src += s.stride;
-      }
-    });
-  }
-  static __device__ __forceinline__ void store(const PlaneDev &d, int z, int m, int n, int count,
-                                               const float (&x)[16]) {
-    by_type(d.type, [&](auto *type) {
-      auto *dst = reinterpret_cast<decltype(type)>(element(d, z, m, n));
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        if (i < count) from_float(*dst, x[i]);
-        dst += d.stride;
-      }
-    });
-  }
-
-  template <typename F>
-  __device__ __forceinline__ void run(const ProductDev &p, uint32_t taddr, int chunks, bool first,
-                                      bool last, F release) {
-    const bool add = p.residual.p && (p.fold ? first : last);
+  for (int i = 0; i < COLUMNS; ++i) sums[i] = 0.f;
 #pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
-      const int m = m0 + c * 16, count = n < p.N ? min(16, p.M - m) : 0;
-      float y[16];
-      if (add) load(p.residual, z, m, n, count, y);
-      uint32_t v[16];
-      __syncwarp();
-      tmem_ld16(taddr + c * 16, v);
-      if (c == chunks - 1) release();
-      float x[16];
+  for (int seg = 0; seg < p.segments; ++seg, ++w.unit) {
+    const uint32_t acc = w.unit & 1;
+    if (!warp_wait(w.acc_full + acc, (w.unit >> 1) & 1, w.abort_flag, p)) return false;
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = p.scale * __uint_as_float(v[i]);
-      if (!first) {
-        float sum[16];
-        load(p.out, z, m, n, count, sum);
+    for (int c = 0; c < COLUMNS / 16; ++c)
+      if (c < chunks) {
+        uint32_t v[16];
+        tmem_ld16(w.tmem + acc * KACC + column + c * 16, v);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] += sum[i];
+        for (int i = 0; i < 16; ++i) sums[c * 16 + i] += __uint_as_float(v[i]);
       }
-      if (last) {
+    release(acc);
+  }
+  return true;
+}
+
+// move_tiles for products in segments, whose sums stay in registers.
+template <bool PAIR, typename F>
+__device__ __forceinline__ bool move_tiles_of_segments(const Job &job, Walk walk, Shared &w, int first, int end,
+                                                       F release) {
+  constexpr int kWidth = PAIR ? 2 * kP : kP, kAccCols = PAIR ? kPairQMax : kQMax;
+  constexpr int kMost = kAccCols / kUnit / (PAIR ? kPairParts : kParts);  // units a warp
+  const ProductDev &p = job.d;
+  Mover<false> mover(job, w);
+  bool ok = true;
+  for (; ok && walk.tile < p.tiles; walk.next()) {
+    const Tile t = tile_at<kWidth, false>(p, walk.tile);
+    const int m = t.p0 + w.row0, n0 = t.q0 + first * kUnit;
+    const int units = m < p.M ? min(end - first, (p.N - n0 + kUnit - 1) / kUnit) : 0;  // inside
+    if (p.ahead && units > 0) mover.ask(n0, m, t.z);
+    float sums[kMost * kUnit];
+    ok = add_segments<kAccCols>(p, w, first * kUnit, 2 * (end - first), sums, release);
+#pragma unroll 1
+    for (int u = 0; ok && u < units; ++u) {
+      float x[kUnit];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] += bias;
-        if (p.pre.p) store(p.pre, z, m, n, count, x);
-        activate(x, p.act);
-      }
-      if (add) {
+      for (int i = 0; i < kUnit; ++i) x[i] = sums[i];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = fmaf(p.residual_scale, y[i], x[i]);
-      }
-      store(p.out, z, m, n, count, x);
+      for (int i = kUnit; i < kMost * kUnit; ++i) sums[i - kUnit] = sums[i];  // the next unit's
+      ok = mover.finish(n0 + u * kUnit, m, t.z, x);
+      if (p.ahead && u + 1 < units) mover.ask(n0 + (u + 1) * kUnit, m, t.z);
     }
   }
-};
+  mover.end();
+  return ok;
+}
+
+// ---- singles
+
+// 16 values of one column of out, from row m on, of which `count` are there.
+__device__ __forceinline__ void load_column(const PlaneDev &s, int z, int m, int n, int count, float (&x)[16]) {
+  by_type(s.type, [&](auto *type) {
+    auto *src = reinterpret_cast<decltype(type)>(element(s, z, m, n));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      x[i] = i < count ? to_float(*src) : 0.f;
+      src += s.stride;
+    }
+  });
+}
+__device__ __forceinline__ void store_column(const PlaneDev &d, int z, int m, int n, int count,
+                                             const float (&x)[16]) {
+  by_type(d.type, [&](auto *type) {
+    auto *dst = reinterpret_cast<decltype(type)>(element(d, z, m, n));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (i < count) from_float(*dst, x[i]);
+      dst += d.stride;
+    }
+  });
+}
+// Sums of products (m .., n) become outputs; y: the residual.
+__device__ __forceinline__ void finish_column(const ProductDev &p, int z, int m, int n, int count, float bias,
+                                              float (&x)[16], const float (&y)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = fmaf(p.scale, x[i], bias);
+  if (p.pre.p) store_column(p.pre, z, m, n, count, x);
+  activate(x, p.act);
+  if (p.residual.p) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = fmaf(p.residual_scale, y[i], x[i]);
+  }
+  store_column(p.out, z, m, n, count, x);
+}
+
+// A warp's share of a tile: column n of each lane, `chunks` times 16 rows from m0 on.  SEGMENTS: adds
+// up the accumulators of a tile first.
+template <int KACC, int MOST, bool SEGMENTS, typename F>
+__device__ __forceinline__ bool drain_columns(const ProductDev &p, Shared &w, int z, int m0, int n, int column,
+                                              int chunks, F release) {
+  const bool there = n < p.N;
+  const float bias = p.bias.p && there ? load_one(p.bias, 0, 0, n) : 0.f;
+  if constexpr (SEGMENTS) {
+    float sums[MOST * 16];
+    if (!add_segments<KACC>(p, w, column, chunks, sums, release)) return false;
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+      const int m = m0 + c * 16, count = there ? min(16, p.M - m) : 0;
+      float x[16], y[16];
+      if (p.residual.p) load_column(p.residual, z, m, n, count, y);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = sums[i];
+#pragma unroll
+      for (int i = 16; i < MOST * 16; ++i) sums[i - 16] = sums[i];
+      finish_column(p, z, m, n, count, bias, x, y);
+    }
+  } else {
+    const uint32_t acc = w.unit & 1;
+    if (!warp_wait(w.acc_full + acc, (w.unit >> 1) & 1, w.abort_flag, p)) return false;
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+      const int m = m0 + c * 16, count = there ? min(16, p.M - m) : 0;
+      float x[16], y[16];
+      if (p.residual.p) load_column(p.residual, z, m, n, count, y);
+      uint32_t v[16];
+      __syncwarp();  // together again after the stores, as tcgen05.ld wants the warp
+      tmem_ld16(w.tmem + acc * KACC + column + c * 16, v);
+      if (c == chunks - 1) release(acc);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[i]);
+      finish_column(p, z, m, n, count, bias, x, y);
+    }
+    if (chunks == 0) release(acc);  // a narrow tile has nothing for this part
+    ++w.unit;
+  }
+  return true;
+}
 
 __device__ __noinline__ float activated_apart(float x, int act) { return activated(x, act); }
 
@@ -653,12 +745,15 @@ __device__ __forceinline__ void finish_one(const ProductDev &p, int64_t z, int64
 // arrival that expects both CTAs' bytes; empty, acc_full and mma_done exist in both and take the
 // leader's multicast commits; acc_empty lives in the leader and takes an arrival from every
 // epilogue warp of the pair.
-template <bool PAIR, bool SPLIT, bool SYMMETRIC>
+enum Variant { kPlain, kSegments, kSymmetric };  // of the products that a kernel is for
+
+template <bool PAIR, bool SPLIT, int VARIANT>
 __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : kThreads, SPLIT ? 2 : 1)
     product_kernel(const __grid_constant__ Jobs jobs) {
-  static_assert(!(PAIR && SPLIT) && !(SYMMETRIC && SPLIT));
+  constexpr bool SYMMETRIC = VARIANT == kSymmetric, SEGMENTS = VARIANT == kSegments;
+  static_assert(!(PAIR && SPLIT) && !(SPLIT && VARIANT != kPlain));
   constexpr uint32_t kCols = SPLIT ? kSplitTmemCols : kTmemCols;
-  constexpr int kAccCols = PAIR ? kPairQMax : kQMax;
+  [[maybe_unused]] constexpr int kAccCols = PAIR ? kPairQMax : kQMax;
   constexpr int kTileP = PAIR ? 2 * kP : kP;
   constexpr int kPartsHere = PAIR ? kPairParts : SPLIT ? kSplitParts : kParts;
   constexpr int kThreadsHere = 128 * (1 + kPartsHere);
@@ -860,45 +955,39 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : 
     const auto drain_all = [&](const Job &job) {
       const ProductDev &p = job.d;
       const int qt = p.q_tile;
+      const Walk start(p, worker, workers);
       if constexpr (!SPLIT) {
         if (SYMMETRIC || p.rows) {
-          const int units = qt / kUnit;
+          const int units = qt / kUnit, u0 = units * part / kPartsHere, u1 = units * (part + 1) / kPartsHere;
           w.buffers = smem_u32(sm) + stages * stage_bytes + (warp - 4) * (p.ahead * p.ahead_bytes + p.slots * p.slot_bytes);
-          ok = move_tiles<PAIR, SYMMETRIC>(job, Walk(p, worker, workers), w, units * part / kPartsHere,
-                                units * (part + 1) / kPartsHere, release);
+          if constexpr (SEGMENTS)
+            ok = move_tiles_of_segments<PAIR>(job, start, w, u0, u1, release);
+          else
+            ok = move_tiles<PAIR, SYMMETRIC>(job, start, w, u0, u1, release);
           return;
         }
       }
       if constexpr (!SYMMETRIC) {
         // This warp's 16-column chunks: a part of the tile's.
         const int c0 = qt / 16 * part / kPartsHere, chunks = qt / 16 * (part + 1) / kPartsHere - c0;
-          for (Walk walk(p, worker, workers); ok && walk.tile < p.tiles; walk.next()) {
-          const Tile t = tile_at<kTileP, SYMMETRIC>(p, walk.tile);
-          const int n0 = t.p0 + w.row0, m0 = t.q0 + c0 * 16;
-          for (int seg = 0; seg < p.segments; ++seg, ++w.unit) {
-            const uint32_t acc = SPLIT ? 0 : w.unit & 1, use = w.unit >> 1;
-            const bool first = seg == 0, last = seg == p.segments - 1;
-            Drain drain;
-            if constexpr (!SPLIT) drain.begin(p, t.z, m0, n0, lane, last);
-            ok = warp_wait(acc_full + acc, use & 1, abort_flag, p);
-            if (!ok) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint32_t taddr = w.tmem + acc * kAccCols + c0 * 16;
-            if constexpr (SPLIT) {
-              // The partial tile into shared memory (the stages: every MMA has read them).
-              float *mine = reinterpret_cast<float *>(sm) + c0 * 16 * kP + quad * 32 + lane;
-              for (int c = 0; c < chunks; ++c) {
-                uint32_t v[16];
-                tmem_ld16(taddr + c * 16, v);
+        if constexpr (SPLIT) {
+          // The partial tile into shared memory (the stages: every MMA has read them).
+          ok = warp_wait(acc_full, 0, abort_flag, p);
+          if (!ok) return;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          float *mine = reinterpret_cast<float *>(sm) + c0 * 16 * kP + quad * 32 + lane;
+          for (int c = 0; c < chunks; ++c) {
+            uint32_t v[16];
+            tmem_ld16(w.tmem + (c0 + c) * 16, v);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) mine[(c * 16 + i) * kP] = __uint_as_float(v[i]);
-              }
-              break;
-            }
-            if (chunks == 0)  // a tile of 16 columns has nothing for the second part
-              release(acc);
-            else
-              drain.run(p, taddr, chunks, first, last, [&] { release(acc); });
+            for (int i = 0; i < 16; ++i) mine[(c * 16 + i) * kP] = __uint_as_float(v[i]);
+          }
+        } else {
+          constexpr int kMost = kAccCols / 16 / kPartsHere;
+          for (Walk walk = start; ok && walk.tile < p.tiles; walk.next()) {
+            const Tile t = tile_at<kTileP, false>(p, walk.tile);
+            ok = drain_columns<kAccCols, kMost, SEGMENTS>(p, w, t.z, t.q0 + c0 * 16, t.p0 + w.row0 + lane, c0 * 16,
+                                                          chunks, release);
           }
         }
       }
@@ -999,12 +1088,14 @@ std::mutex g_info_mu;
 
 using Kernel = void (*)(Jobs);
 enum Form { kSingle, kSplit, kPair, kForms };
-Kernel kernel_of(int form, bool symmetric) {
-  static constexpr Kernel all[kForms][2] = {
-      {product_kernel<false, false, false>, product_kernel<false, false, true>},
-      {product_kernel<false, true, false>, nullptr},
-      {product_kernel<true, false, false>, product_kernel<true, false, true>}};
-  return all[form][symmetric];
+Kernel kernel_of(int form, int variant) {
+  static constexpr Kernel all[kForms][3] = {
+      {product_kernel<false, false, kPlain>, product_kernel<false, false, kSegments>,
+       product_kernel<false, false, kSymmetric>},
+      {product_kernel<false, true, kPlain>, nullptr, nullptr},
+      {product_kernel<true, false, kPlain>, product_kernel<true, false, kSegments>,
+       product_kernel<true, false, kSymmetric>}};
+  return all[form][variant];
 }
 
 cudaError_t device_info(DeviceInfo &out) {
@@ -1015,9 +1106,10 @@ cudaError_t device_info(DeviceInfo &out) {
   DeviceInfo &d = g_info[dev & 63];
   if (!d.ready) {
     e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-    for (int i = 0; i < 2 * kForms && e == cudaSuccess; ++i)
-      if (kernel_of(i / 2, i & 1)) e = cudaFuncSetAttribute(kernel_of(i / 2, i & 1), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)(i / 2 == kSplit ? kSplitSmemBytes : kSmemBytes));
+    for (int i = 0; i < 3 * kForms && e == cudaSuccess; ++i)
+      if (kernel_of(i / 3, i % 3))
+        e = cudaFuncSetAttribute(kernel_of(i / 3, i % 3), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)(i / 3 == kSplit ? kSplitSmemBytes : kSmemBytes));
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -1030,7 +1122,7 @@ cudaError_t device_info(DeviceInfo &out) {
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if ((e = cudaOccupancyMaxActiveClusters(&d.pairs, kernel_of(kPair, false), &cfg)) != cudaSuccess) return e;
+    if ((e = cudaOccupancyMaxActiveClusters(&d.pairs, kernel_of(kPair, kPlain), &cfg)) != cudaSuccess) return e;
     d.ready = true;
   }
   out = d;
@@ -1056,14 +1148,6 @@ PlaneDev plane_of(const ProductParams &p, const Plane &x) {
   PlaneDev d{x.p, p.M > 1 ? x.stride : 0, p.count > 1 ? x.batch : 0, x.type, false};
   d.vec = ((uintptr_t)x.p & 15) == 0 && d.stride % step == 0 && d.batch % step == 0;
   return d;
-}
-
-bool overlaps(const Plane &a, const Plane &b, int64_t M, int64_t N) {
-  const auto bytes = [&](const Plane &x) {
-    return ((M - 1) * x.stride + N) * (x.type == ENGRAM_DTYPE_F32 ? 4 : 2);
-  };
-  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-  return x && y && x < y + bytes(b) && y < x + bytes(a);
 }
 
 // Bytes of a tiles' epilogue unit.
@@ -1099,18 +1183,16 @@ Facts facts_of(const ProductParams &p) {
   d.N = (int32_t)p.N;
   d.many = p.count > 1;
   d.kblocks = (int32_t)ceil_div(p.K, kBK);
-  // Segments only where the output has the bits to show them, and nothing of it is needed later.
-  const bool in_place = p.count == 1 && overlaps(p.out, p.residual, p.M, p.N);
+  // Segments only where the output has the bits to show them.
   d.segments = 1;
   d.seg_blocks = d.kblocks;
-  if (p.out.type == ENGRAM_DTYPE_F32 && !(in_place && (p.act != ENGRAM_ACT_NONE || p.pre.p))) {
+  if (p.out.type == ENGRAM_DTYPE_F32 || p.pre.type == ENGRAM_DTYPE_F32) {
     d.seg_blocks = (int32_t)ceil_div(d.kblocks, ceil_div(d.kblocks, kSegmentBlocks));
     d.segments = (int32_t)ceil_div(d.kblocks, d.seg_blocks);
-    d.fold = in_place && d.segments > 1;
   }
   // The tiles' epilogue wants rows on 16-byte boundaries (a row that repeats has none apart).
   const auto moves = [&](const PlaneDev &x) { return !x.p || (x.vec && (p.M == 1 || x.stride >= p.N)); };
-  f.tiles_epilogue = d.segments == 1 && moves(d.out) && moves(d.pre) && moves(d.residual);
+  f.tiles_epilogue = moves(d.out) && moves(d.pre) && moves(d.residual);
   return f;
 }
 
@@ -1161,7 +1243,9 @@ Plan plan_split(const ProductParams &p, const Facts &f, const DeviceInfo &info) 
   const int64_t tiles = p.count * tiles_of(p.N, p.M, kP, qt, p.symmetric);
   const double kb = f.d.kblocks;
   for (int n = 2; n <= 8; n *= 2) {
-    if (n * tiles > 2 * info.sms || kb < n || ceil_div(f.d.kblocks, n) > kSegmentBlocks) continue;
+    if (n * tiles > 2 * info.sms || kb < n) continue;
+    // A part is one segment: of fp32 outputs not much longer than the others'.
+    if (f.d.segments > 1 && ceil_div(f.d.kblocks, n) > (n == 8 ? 2 * kSegmentBlocks : kSegmentBlocks * 3 / 2)) continue;
     Plan s;
     s.form = kSplit;
     s.q_tile = qt;
@@ -1197,7 +1281,7 @@ int64_t reserve_of(const ProductParams &p, int64_t stage) {
 
 // A job of a plan; its share of the shared memory (the epilogue's buffers) in `buffers`, which leave
 // `reserve` bytes for stages.
-cudaError_t job_of(const ProductParams &p, const Facts &f, const Plan &plan, int64_t reserve, Job &job,
+cudaError_t job_of(const ProductParams &p, const Facts &f, const Plan &plan, int64_t reserve, bool segments, Job &job,
                    int64_t &buffers) {
   const Operand &op = plan.rows ? p.a : p.b, &oq = plan.rows ? p.b : p.a;
   const int64_t P = plan.rows ? p.M : p.N, Q = plan.rows ? p.N : p.M;
@@ -1220,7 +1304,9 @@ cudaError_t job_of(const ProductParams &p, const Facts &f, const Plan &plan, int
     const auto bytes = [&](int ahead, int slots) {
       return (int64_t)warps * (ahead * d.ahead_bytes + slots * d.slot_bytes);
     };
-    const int64_t most = kBudget - reserve;
+    // With sums in segments one buffer serves both where it can.
+    if (segments && d.ahead && !d.pre.p && d.ahead_bytes == d.slot_bytes) d.slots = 0;
+    const int64_t most = segments ? 0 : kBudget - reserve;
     if (bytes(d.ahead, 2) <= most) d.slots = 2;
     while (d.ahead && d.ahead < kMaxAhead && bytes(d.ahead + 1, d.slots) <= most) ++d.ahead;
     buffers = bytes(d.ahead, d.slots);
@@ -1228,7 +1314,6 @@ cudaError_t job_of(const ProductParams &p, const Facts &f, const Plan &plan, int
   if (plan.form == kSplit) {  // a CTA's part of K is one segment
     d.segments = 1;
     d.seg_blocks = d.kblocks;
-    d.fold = false;
   }
   const int width = plan.form == kPair ? 2 * kP : kP;
   const int64_t matrix_tiles = tiles_of(P, Q, width, plan.q_tile, p.symmetric), tiles = matrix_tiles * p.count;
@@ -1267,7 +1352,7 @@ cudaError_t job_of(const ProductParams &p, const Facts &f, const Plan &plan, int
 }
 
 // Launches the jobs of plans of one form.
-cudaError_t launch_jobs(Jobs &jobs, const Plan &plan, int64_t buffers, bool symmetric, const DeviceInfo &info,
+cudaError_t launch_jobs(Jobs &jobs, const Plan &plan, int64_t buffers, int variant, const DeviceInfo &info,
                         cudaStream_t stream) {
   jobs.job[0].d.withhold = take_withheld_launch();
   jobs.splits = plan.splits;
@@ -1281,7 +1366,7 @@ cudaError_t launch_jobs(Jobs &jobs, const Plan &plan, int64_t buffers, bool symm
                           jobs.stage_bytes);
   if (jobs.stages > kMaxStages) jobs.stages = kMaxStages;
   if (jobs.stages < kProducers) return cudaErrorInvalidConfiguration;
-  const Kernel kernel = kernel_of(plan.form, symmetric);
+  const Kernel kernel = kernel_of(plan.form, plan.form == kSplit ? kPlain : variant);
   if (plan.form == kPair)
     return launch(kernel, 2 * (tiles < info.pairs ? tiles : info.pairs), kPairThreads, kSmemBytes, stream, 2, jobs);
   if (plan.form == kSplit)
@@ -1307,8 +1392,8 @@ cudaError_t launch_product(const ProductParams &p, cudaStream_t stream) {
   jobs.count = 1;
   int64_t buffers;
   const int64_t reserve = reserve_of(p, stage_bytes_of(p, plan));
-  if ((e = job_of(p, f, plan, reserve, jobs.job[0], buffers)) != cudaSuccess) return e;
-  return launch_jobs(jobs, plan, buffers, p.symmetric, info, stream);
+  if ((e = job_of(p, f, plan, reserve, f.d.segments > 1, jobs.job[0], buffers)) != cudaSuccess) return e;
+  return launch_jobs(jobs, plan, buffers, p.symmetric ? kSymmetric : f.d.segments > 1 ? kSegments : kPlain, info, stream);
 }
 
 cudaError_t launch_products(const ProductParams &p0, const ProductParams &p1, cudaStream_t stream) {
@@ -1345,13 +1430,14 @@ cudaError_t launch_products(const ProductParams &p0, const ProductParams &p1, cu
   const int a = best[0].tile_us >= best[1].tile_us ? 0 : 1, b = 1 - a;
   Jobs jobs{};
   jobs.count = 2;
+  const bool segments = f[0].d.segments > 1 || f[1].d.segments > 1;
   int64_t buffers[2], stage = 0, reserve = 0;
   for (int i = 0; i < 2; ++i)
     if (stage_bytes_of(*p[i], best[i]) > stage) stage = stage_bytes_of(*p[i], best[i]);
   for (int i = 0; i < 2; ++i)
     if (reserve_of(*p[i], stage) > reserve) reserve = reserve_of(*p[i], stage);
-  if ((e = job_of(*p[a], f[a], best[a], reserve, jobs.job[0], buffers[0])) != cudaSuccess) return e;
-  if ((e = job_of(*p[b], f[b], best[b], reserve, jobs.job[1], buffers[1])) != cudaSuccess) return e;
+  if ((e = job_of(*p[a], f[a], best[a], reserve, segments, jobs.job[0], buffers[0])) != cudaSuccess) return e;
+  if ((e = job_of(*p[b], f[b], best[b], reserve, segments, jobs.job[1], buffers[1])) != cudaSuccess) return e;
   const int64_t most = best[0].form == kPair ? info.pairs : info.sms, tiles = best[0].tiles + best[1].tiles;
   const int64_t workers = tiles < most ? tiles : most;
   ProductDev &second = jobs.job[1].d;
@@ -1360,7 +1446,8 @@ cudaError_t launch_products(const ProductParams &p0, const ProductParams &p1, cu
   int64_t extra = second.shift ? (int64_t)(best[a].tile_us / best[b].tile_us) : 0;
   if (extra > best[b].tiles / lights) extra = best[b].tiles / lights;
   second.extra = (int32_t)extra;
-  return launch_jobs(jobs, best[0], buffers[0] > buffers[1] ? buffers[0] : buffers[1], false, info, stream);
+  return launch_jobs(jobs, best[0], buffers[0] > buffers[1] ? buffers[0] : buffers[1],
+                     segments ? kSegments : kPlain, info, stream);
 }
 
 }  // namespace engram
