@@ -20,8 +20,9 @@
 //
 // The fp32 accumulator of the tensor cores does not round to nearest: its error grows with the
 // number of additions (1e-9 of the result for each value of K, against 1e-6 of an fp32 sum of
-// 8192).  So where out or pre is fp32, K is cut into segments of at most 512 that each start a new
-// accumulator, and the epilogue adds them in registers, rounding to nearest.
+// 8192).  So where out or pre is fp32, K is cut into segments of at most 768 that each start a new
+// accumulator, and the epilogue adds them in registers, rounding to nearest (7e-7 of the result; segments
+// of 512 would be 5e-7 and take 4 % longer, of 1024 1e-6).
 //
 // A symmetric product (both operands one matrix) computes the tiles on one side of the diagonal
 // and stores every value twice, the second time transposed: a lane's 16 values of a chunk are
@@ -49,7 +50,7 @@ constexpr int kPairQMax = 256;  // and of a pair
 constexpr int kParts = 4, kPairParts = 4;
 constexpr int kThreads = 128 * (1 + kParts), kPairThreads = 128 * (1 + kPairParts);
 constexpr int kSplitParts = 2, kSplitThreads = 128 * (1 + kSplitParts);
-constexpr int kSegmentBlocks = 8;
+constexpr int kSegmentBlocks = 12;
 constexpr int kMaxStages = 12, kMaxAhead = 4, kProducers = 3;
 constexpr uint32_t kPBytes = kP * kBK * 2;
 constexpr uint32_t kBarBytes = 1024;
@@ -57,7 +58,7 @@ constexpr int kUnit = 32;   // columns a warp of the tiles' epilogue moves at a 
 // Shared memory for stages and epilogue buffers.
 constexpr uint32_t kBudget = 224 * 1024;
 constexpr uint32_t kSplitBudget = 104 * 1024;
-constexpr uint32_t kTmemCols = 512, kSplitTmemCols = 128;
+constexpr uint32_t kTmemCols = 512, kSplitTmemCols = 256;
 constexpr size_t kSmemBytes = 1024 + kBarBytes + kBudget;
 constexpr size_t kSplitSmemBytes = 1024 + kBarBytes + kSplitBudget;
 static_assert(2 * (kSplitSmemBytes + 1024) <= 228 * 1024 && kSmemBytes <= 227 * 1024);
@@ -902,9 +903,11 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : 
         const uint32_t p_step = desc_step(p.p_t), q_step = desc_step(p.q_t), idesc = p.idesc;
         const uint32_t p_first = desc_low(smem_u32(sm), p.p_t), q_first = desc_low(smem_u32(sm) + kPBytes, p.q_t);
         for (Walk walk(p, worker, workers); ok && walk.tile < p.tiles; walk.next()) {
-          for (int kb0 = 0; ok && kb0 < kblocks; kb0 += p.seg_blocks, ++unit) {
-            const int kb1 = min(kb0 + p.seg_blocks, kblocks);
-            const uint32_t acc = SPLIT ? 0 : unit & 1, use = unit >> 1;
+          // A part of K shared by CTAs goes half into each accumulator.
+          const int seg_blocks = SPLIT ? (kblocks + 1) / 2 : p.seg_blocks;
+          for (int kb0 = 0; ok && kb0 < kblocks; kb0 += seg_blocks, ++unit) {
+            const int kb1 = min(kb0 + seg_blocks, kblocks);
+            const uint32_t acc = unit & 1, use = unit >> 1;
             if (!(ok = wait_phase(acc_empty + acc, (use & 1) ^ 1, abort_flag, limit, p.status))) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t d = tmem + acc * kAccCols;
@@ -972,15 +975,18 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : 
         const int c0 = qt / 16 * part / kPartsHere, chunks = qt / 16 * (part + 1) / kPartsHere - c0;
         if constexpr (SPLIT) {
           // The partial tile into shared memory (the stages: every MMA has read them).
-          ok = warp_wait(acc_full, 0, abort_flag, p);
+          const bool two = blocks(p) > 1;
+          ok = warp_wait(acc_full, 0, abort_flag, p) && (!two || warp_wait(acc_full + 1, 0, abort_flag, p));
           if (!ok) return;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           float *mine = reinterpret_cast<float *>(sm) + c0 * 16 * kP + quad * 32 + lane;
           for (int c = 0; c < chunks; ++c) {
-            uint32_t v[16];
+            uint32_t v[16], u[16];
             tmem_ld16(w.tmem + (c0 + c) * 16, v);
+            if (two) tmem_ld16(w.tmem + kAccCols + (c0 + c) * 16, u);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) mine[(c * 16 + i) * kP] = __uint_as_float(v[i]);
+            for (int i = 0; i < 16; ++i)
+              mine[(c * 16 + i) * kP] = __uint_as_float(v[i]) + (two ? __uint_as_float(u[i]) : 0.f);
           }
         } else {
           constexpr int kMost = kAccCols / 16 / kPartsHere;
@@ -1244,8 +1250,8 @@ Plan plan_split(const ProductParams &p, const Facts &f, const DeviceInfo &info) 
   const double kb = f.d.kblocks;
   for (int n = 2; n <= 8; n *= 2) {
     if (n * tiles > 2 * info.sms || kb < n) continue;
-    // A part is one segment: of fp32 outputs not much longer than the others'.
-    if (f.d.segments > 1 && ceil_div(f.d.kblocks, n) > (n == 8 ? 2 * kSegmentBlocks : kSegmentBlocks * 3 / 2)) continue;
+    // A part is two segments: of fp32 outputs not much longer than the others'.
+    if (f.d.segments > 1 && ceil_div(f.d.kblocks, n) > 2 * kSegmentBlocks) continue;
     Plan s;
     s.form = kSplit;
     s.q_tile = qt;

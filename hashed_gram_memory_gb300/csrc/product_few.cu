@@ -102,9 +102,12 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(const __grid_cons
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  float acc[EIGHTS][4];
+  // Two sums each, as the instruction's own do not round to nearest: 8192 long 1e-6 off in one.
+  float acc[EIGHTS][2][4];
 #pragma unroll
-  for (int e = 0; e < EIGHTS; ++e) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.f;
+  for (int e = 0; e < EIGHTS; ++e)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[e][i / 4][i % 4] = 0.f;
   for (int i = 0; i < R::kDeep - 1; ++i) copy(i);
   for (int i = 0; i < steps; ++i) {
     asm volatile("cp.async.wait_group %0;" ::"n"(R::kDeep - 2) : "memory");
@@ -116,16 +119,16 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(const __grid_cons
     copy(i + R::kDeep - 1);
 #pragma unroll
     for (int e = 0; e < EIGHTS; ++e) {
-      mma(acc[e], w0.x, w1.x, w0.y, w1.y, v[e].x, v[e].y);
-      mma(acc[e], w0.z, w1.z, w0.w, w1.w, v[e].z, v[e].w);
+      mma(acc[e][0], w0.x, w1.x, w0.y, w1.y, v[e].x, v[e].y);
+      mma(acc[e][1], w0.z, w1.z, w0.w, w1.w, v[e].z, v[e].w);
     }
   }
 #pragma unroll
   for (int e = 0; e < EIGHTS; ++e) {
-    sums[warp][g][e * 8 + 2 * t] = acc[e][0];
-    sums[warp][g][e * 8 + 2 * t + 1] = acc[e][1];
-    sums[warp][g + 8][e * 8 + 2 * t] = acc[e][2];
-    sums[warp][g + 8][e * 8 + 2 * t + 1] = acc[e][3];
+    sums[warp][g][e * 8 + 2 * t] = acc[e][0][0] + acc[e][1][0];
+    sums[warp][g][e * 8 + 2 * t + 1] = acc[e][0][1] + acc[e][1][1];
+    sums[warp][g + 8][e * 8 + 2 * t] = acc[e][0][2] + acc[e][1][2];
+    sums[warp][g + 8][e * 8 + 2 * t + 1] = acc[e][0][3] + acc[e][1][3];
   }
   __syncthreads();
   for (int i = threadIdx.x; i < kRows * kColumns; i += warps * 32) {
