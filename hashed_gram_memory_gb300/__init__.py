@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes as C
 import dataclasses
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libengram.so")
@@ -170,17 +171,12 @@ def _load():
     L.engram_gate_add_grad.argtypes = [vp, vp, i64, i32, vp, vp, C.c_float, vp, vp, vp, i32, vp,
                                        vp, sz, vp]
     L.engram_gate_add_grad.restype = i32
-    f32, operands = C.c_float, [vp, i64, i32, vp, i64, i32, i64, i64, i64]
-    L.engram_matmul_workspace_bytes.argtypes = operands
-    L.engram_matmul_workspace_bytes.restype = sz
-    L.engram_matmul.argtypes = operands + [f32, vp, i32, i32, vp, i32, i64, vp, i32, i64, vp, i32,
-                                           i64, vp, sz, vp, vp]
-    L.engram_matmul.restype = i32
-    L.engram_matmul_grad_workspace_bytes.argtypes = [vp, i32, i64] + operands + [i32, i32, i32, i32]
-    L.engram_matmul_grad_workspace_bytes.restype = sz
-    L.engram_matmul_grad.argtypes = [vp, i32, i64] + operands + [
-        f32, vp, i32, i64, i32, i32, vp, i32, i64, vp, i32, i64, vp, vp, sz, vp, vp]
-    L.engram_matmul_grad.restype = i32
+    f32 = C.c_float
+    for f in ("engram_matmul", "engram_matmul_grad"):  # their arguments are packed structs
+        getattr(L, f + "_workspace_bytes").argtypes = [C.c_char_p]
+        getattr(L, f + "_workspace_bytes").restype = sz
+        getattr(L, f).argtypes = [C.c_char_p, vp, sz, vp, vp]
+        getattr(L, f).restype = i32
     L.engram_orthogonalise_workspace_bytes.argtypes = [i64, i64, i64]
     L.engram_orthogonalise_workspace_bytes.restype = sz
     L.engram_orthogonalise.argtypes = [vp, i32, i64, i64, i64, i64, i64, vp, i64, i64, f32, i32, i32,
@@ -975,16 +971,22 @@ def engram_gate_add_grad(k, state, streams_in, alpha, dy, eps: float = 1e-6, dx=
     return dx, dk, dalpha
 
 
+# engram_matmul_args and engram_matmul_grad_args of include/engram.h: pointers and 64-bit numbers,
+# then 32-bit ones and the scale.
+_MATMUL_ARGS = struct.Struct("QqQqqqqQQqQqQq7if")
+_MATMUL_GRAD_ARGS = struct.Struct("QqQqQqqqqQqQqQqQ8if4x")
+
+
 def _bf16_operand(t, name):
     """(rows, columns, pointer, stride, transposed) of a bf16 matrix of which either dimension
     is dense."""
     if _dtype(t, name) != DTYPE_BF16:
         import torch
         _need(t, (torch.bfloat16, torch.int16), name, contiguous=False)
-    if t.dim() != 2:
+    st = t.stride()
+    if len(st) != 2:
         raise EngramError(ERR_INVALID_ARG, f"{name} must be two-dimensional")
     rows, cols = t.shape
-    st = t.stride()
     if st[1] == 1 or cols == 1:
         return rows, cols, t.data_ptr(), st[0] if rows > 1 else cols, 0
     if st[0] == 1 or rows == 1:
@@ -993,12 +995,12 @@ def _bf16_operand(t, name):
 
 
 def _plane(t, shape, name):
-    """(pointer, dtype, row stride) of a bf16 or fp32 [M, N] tensor, (None, 0, 0) for none."""
+    """(pointer, row stride, dtype) of a bf16 or fp32 [M, N] tensor, zeros for none."""
     if t is None:
-        return None, 0, 0
+        return 0, 0, 0
     if t.shape != shape:
         raise EngramError(ERR_INVALID_ARG, f"{name} must be {list(shape)}")
-    return t.data_ptr(), _dtype(t, name), _strides(t, name)[0]
+    return t.data_ptr(), _strides(t, name)[0], _dtype(t, name)
 
 
 def _one_device(stream, first, *others):
@@ -1013,12 +1015,6 @@ def _one_device(stream, first, *others):
             raise EngramError(ERR_INVALID_ARG, "the tensors must be on the current device")
 
 
-def _activation(activation):
-    if activation.__class__ is not int:
-        raise EngramError(ERR_INVALID_ARG, "activation must be one of the ACT_* numbers")
-    return activation
-
-
 def _scratch(workspace, need, like, stream):
     """(pointer, bytes) of the caller's workspace, or of one that the call makes, and its tensor."""
     if workspace is None:
@@ -1027,15 +1023,42 @@ def _scratch(workspace, need, like, stream):
         import torch
         workspace = _made(stream, torch.empty, need, dtype=torch.uint8, device=like.device,
                           scratch=True)
-    _need(workspace, (workspace.dtype,), "workspace")
+    else:
+        _need(workspace, (workspace.dtype,), "workspace")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _packed(fmt, *values):
+    """The bytes of an argument struct."""
+    try:
+        return fmt.pack(*values)
+    except struct.error as e:
+        raise EngramError(ERR_INVALID_ARG, f"an argument is no number of its range: {e}") from None
+
+
+def _matmul_args(a, b, bias, activation, residual, scale, pre, out):
+    M, K, pa, sa, ta = _bf16_operand(a, "a")
+    N, kb, pb, sb, tb = _bf16_operand(b, "b")
+    if kb != K:
+        raise EngramError(ERR_INVALID_ARG, "a and b disagree on K")
+    bias_ptr = bias_dtype = 0
+    if bias is not None:
+        bias_ptr, bias_dtype = bias.data_ptr(), _dtype(bias, "bias")
+        if bias.shape != (N,) or not bias.is_contiguous():
+            raise EngramError(ERR_INVALID_ARG, f"bias must be contiguous {[N]}")
+    shape = (M, N)
+    pr, sr, dr = _plane(residual, shape, "residual")
+    pp, sp, dp = _plane(pre, shape, "pre")
+    po, so, do = _plane(out, shape, "out")
+    # whether the operands start on 16-byte boundaries throughout: then there is no workspace
+    return _packed(_MATMUL_ARGS, pa, sa, pb, sb, M, N, K, bias_ptr, pr, sr, pp, sp, po, so, ta, tb,
+                   activation, bias_dtype, dr, dp, do, scale), not ((pa | pb) & 15 or (sa | sb) & 7)
 
 
 def engram_matmul_workspace_bytes(a, b) -> int:
     """0 unless the rows of a or b are off 16-byte boundaries."""
-    M, K, *a = _bf16_operand(a, "a")
-    N, _, *b = _bf16_operand(b, "b")
-    return int(lib.engram_matmul_workspace_bytes(*a, *b, M, N, K))
+    return int(lib.engram_matmul_workspace_bytes(
+        _matmul_args(a, b, None, ACT_NONE, None, 1.0, None, None)[0]))
 
 
 def engram_matmul(a, b, bias=None, activation: int = ACT_NONE, residual=None, scale: float = 1.0,
@@ -1044,28 +1067,16 @@ def engram_matmul(a, b, bias=None, activation: int = ACT_NONE, residual=None, sc
     [M, K] and b bf16 [N, K], each row-major or a transposed view.  bias [N], residual [M, N] (it
     may be out itself) and out (fp32 by default) are bf16 or fp32; pre, a [M, N] buffer, receives z
     for engram_matmul_grad."""
-    M, K, *pa = _bf16_operand(a, "a")
-    N, kb, *pb = _bf16_operand(b, "b")
-    if kb != K:
-        raise EngramError(ERR_INVALID_ARG, "a and b disagree on K")
-    shape = (M, N)
     if out is None:
         import torch
-        out = _made(stream, torch.empty, shape, dtype=out_dtype or torch.float32, device=a.device)
-    bias_ptr, bias_dtype = None, 0
-    if bias is not None:
-        bias_ptr, bias_dtype = bias.data_ptr(), _dtype(bias, "bias")
-        if bias.shape != (N,) or not bias.is_contiguous():
-            raise EngramError(ERR_INVALID_ARG, f"bias must be contiguous {[N]}")
+        out = _made(stream, torch.empty, (a.shape[0], b.shape[0]), dtype=out_dtype or torch.float32,
+                    device=a.device)
+    args, direct = _matmul_args(a, b, bias, activation, residual, scale, pre, out)
     _one_device(stream, a, b, out, bias, residual, pre, workspace, status)
     ws, ws_bytes = None, 0
-    if workspace is not None or (pa[0] | pb[0]) & 15 or (pa[1] | pb[1]) & 7:  # else it needs none
-        ws, ws_bytes, workspace = _scratch(
-            workspace, lib.engram_matmul_workspace_bytes(*pa, *pb, M, N, K), a, stream)
-    code = lib.engram_matmul(*pa, *pb, M, N, K, scale, bias_ptr, bias_dtype, _activation(activation),
-                             *_plane(residual, shape, "residual"), *_plane(pre, shape, "pre"),
-                             *_plane(out, shape, "out"), ws, ws_bytes, _ptr(status),
-                             _stream(stream))
+    if not direct or workspace is not None:
+        ws, ws_bytes, workspace = _scratch(workspace, lib.engram_matmul_workspace_bytes(args), a, stream)
+    code = lib.engram_matmul(args, ws, ws_bytes, _ptr(status), _stream(stream))
     if code:
         _check(code, "engram_matmul")
     return out
@@ -1079,43 +1090,46 @@ def engram_matmul_grad(dy, a, b, pre=None, activation: int = ACT_NONE, scale: fl
     output gradient dy (bf16 or fp32 [M, N]; rows may repeat): (da [M, K], db [N, K], dbias fp32
     [N]), None for those not asked for.  da and db are bf16 by default; accumulate adds to the db
     and dbias given.  What the two products read of dy act'(pre) has been rounded to bf16."""
-    import torch
-    dd = _dtype(dy, "dy")
-    if dy.dim() != 2:
-        raise EngramError(ERR_INVALID_ARG, "dy must be [M, N]")
-    M, N = shape = dy.shape
-    rows, K, *pa = _bf16_operand(a, "a")
-    cols, kb, *pb = _bf16_operand(b, "b")
-    if rows != M or cols != N or kb != K:
+    M, K, pa, sa, ta = _bf16_operand(a, "a")
+    N, kb, pb, sb, tb = _bf16_operand(b, "b")
+    shape = (M, N)
+    if kb != K or dy.shape != shape:
         raise EngramError(ERR_INVALID_ARG, "a must be [M, K] and b [N, K] for dy [M, N]")
     if accumulate and ((grad_b and db is None) or (grad_bias and dbias is None)):
         raise EngramError(ERR_INVALID_ARG, "accumulate needs gradients to add to")
     if activation != ACT_NONE and pre is None:
         raise EngramError(ERR_INVALID_ARG, "the gradient of an activation needs pre")
-    dev = dy.device
     if not grad_a:
         da = None
     elif da is None:
-        da = _made(stream, torch.empty, (M, K), dtype=da_dtype or torch.bfloat16, device=dev)
+        import torch
+        da = _made(stream, torch.empty, (M, K), dtype=da_dtype or torch.bfloat16, device=dy.device)
     if not grad_b:
         db = None
     elif db is None:
-        db = _made(stream, torch.empty, (N, K), dtype=db_dtype or torch.bfloat16, device=dev)
+        import torch
+        db = _made(stream, torch.empty, (N, K), dtype=db_dtype or torch.bfloat16, device=dy.device)
     if not grad_bias:
         dbias = None
     elif dbias is None:
-        dbias = _made(stream, torch.empty, N, dtype=torch.float32, device=dev)
-    _need(dbias, (torch.float32,), "dbias")
-    if dbias is not None and dbias.shape != (N,):
-        raise EngramError(ERR_INVALID_ARG, f"dbias must be {[N]}")
+        import torch
+        dbias = _made(stream, torch.empty, N, dtype=torch.float32, device=dy.device)
+    if dbias is not None:
+        if dbias.shape != (N,) or _dtype(dbias, "dbias") != DTYPE_F32 or not dbias.is_contiguous():
+            raise EngramError(ERR_INVALID_ARG, f"dbias must be contiguous fp32 {[N]}")
     _one_device(stream, dy, a, b, pre, da, db, dbias, workspace, status)
-    args = (dy.data_ptr(), dd, _strides(dy, "dy")[0], *pa, *pb, M, N, K)
-    ws, ws_bytes, workspace = _scratch(
-        workspace, lib.engram_matmul_grad_workspace_bytes(*args, _activation(activation), grad_a, grad_b, grad_bias),
-        dy, stream)
-    _check(lib.engram_matmul_grad(*args, scale, *_plane(pre, shape, "pre"), _activation(activation), accumulate,
-                                  *_plane(da, (M, K), "da"), *_plane(db, (N, K), "db"), _ptr(dbias),
-                                  ws, ws_bytes, _ptr(status), _stream(stream)), "engram_matmul_grad")
+    py, sy, dd = _plane(dy, shape, "dy")
+    pp, sp, dp = _plane(pre, shape, "pre")
+    qa, ua, ea = _plane(da, (M, K), "da")
+    qb, ub, eb = _plane(db, (N, K), "db")
+    args = _packed(_MATMUL_GRAD_ARGS, py, sy, pa, sa, pb, sb, M, N, K, pp, sp, qa, ua, qb, ub,
+                   0 if dbias is None else dbias.data_ptr(), ta, tb, activation, dd, dp, ea, eb,
+                   bool(accumulate), scale)
+    ws, ws_bytes, workspace = _scratch(workspace, lib.engram_matmul_grad_workspace_bytes(args), dy,
+                                       stream)
+    code = lib.engram_matmul_grad(args, ws, ws_bytes, _ptr(status), _stream(stream))
+    if code:
+        _check(code, "engram_matmul_grad")
     return da, db, dbias
 
 

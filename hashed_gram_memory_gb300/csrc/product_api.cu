@@ -61,14 +61,25 @@ struct Given {
   }
 };
 
-// The operand for the product: as it is, or its copy at *scratch, which moves on.
-cudaError_t operand_of(const Given &g, uint8_t *&scratch, Operand &out, cudaStream_t stream) {
-  out = Operand{g.p, g.stride, 0, g.t};
-  if (g.direct()) return cudaSuccess;
-  out.p = scratch;
-  out.stride = g.packed_stride();
-  scratch += g.packed_bytes();
-  return engram::launch_pack(g.p, g.stride, const_cast<void *>(out.p), out.stride, g.outer(), g.inner(), stream);
+// The operands for the products, as they are or their copies in the workspace (one launch for both).
+cudaError_t operands_of(const Given *g[2], uint8_t *&scratch, Operand out[2], cudaStream_t stream) {
+  engram::PackParams pack{};
+  for (int i = 0; i < 2; ++i) {
+    if (!g[i]) continue;
+    out[i] = Operand{g[i]->p, g[i]->stride, 0, g[i]->t};
+    if (g[i]->direct()) continue;
+    engram::Packed &k = pack.part[pack.count++];
+    k.src = g[i]->p;
+    k.src_stride = g[i]->outer() > 1 ? g[i]->stride : 0;
+    k.dst = reinterpret_cast<uint16_t *>(scratch);
+    k.dst_stride = g[i]->packed_stride();
+    k.rows = g[i]->outer();
+    k.cols = g[i]->inner();
+    out[i].p = scratch;
+    out[i].stride = k.dst_stride;
+    scratch += g[i]->packed_bytes();
+  }
+  return pack.count ? engram::launch_pack(pack, stream) : cudaSuccess;
 }
 
 bool sizes_ok(int64_t M, int64_t N, int64_t K) {
@@ -93,23 +104,19 @@ size_t dz_bytes(int64_t M, int64_t N) { return (size_t)(M * dz_stride_of(N) * 2 
 
 extern "C" {
 
-ENGRAM_API size_t engram_matmul_workspace_bytes(const uint16_t *a, int64_t a_stride, int32_t a_trans,
-                                                const uint16_t *b, int64_t b_stride, int32_t b_trans,
-                                                int64_t M, int64_t N, int64_t K) {
-  if (!sizes_ok(M, N, K)) return 0;
-  return Given{a, a_stride, a_trans != 0, M, K}.packed_bytes() +
-         Given{b, b_stride, b_trans != 0, N, K}.packed_bytes();
+ENGRAM_API size_t engram_matmul_workspace_bytes(const engram_matmul_args *args) {
+  if (!args || !sizes_ok(args->M, args->N, args->K)) return 0;
+  return Given{args->a, args->a_stride, args->a_trans != 0, args->M, args->K}.packed_bytes() +
+         Given{args->b, args->b_stride, args->b_trans != 0, args->N, args->K}.packed_bytes();
 }
 
-ENGRAM_API engram_status engram_matmul(const uint16_t *a, int64_t a_stride, int32_t a_trans, const uint16_t *b,
-                                       int64_t b_stride, int32_t b_trans, int64_t M, int64_t N, int64_t K,
-                                       float scale, const void *bias, int32_t bias_dtype, int32_t activation,
-                                       const void *residual, int32_t residual_dtype, int64_t residual_stride,
-                                       void *pre, int32_t pre_dtype, int64_t pre_stride, void *out,
-                                       int32_t out_dtype, int64_t out_stride, void *workspace,
-                                       size_t workspace_bytes, int32_t *status, void *stream) {
+ENGRAM_API engram_status engram_matmul(const engram_matmul_args *args, void *workspace, size_t workspace_bytes,
+                                       int32_t *status, void *stream) {
   ENGRAM_NVTX_RANGE("engram_matmul");
   const char *fn = "engram_matmul";
+  if (!args) return set_error(ENGRAM_ERR_INVALID_ARG, "%s: args is NULL", fn);
+  const auto [a, a_stride, b, b_stride, M, N, K, bias, residual, residual_stride, pre, pre_stride, out, out_stride,
+              a_trans, b_trans, activation, bias_dtype, residual_dtype, pre_dtype, out_dtype, scale] = *args;
   if (!sizes_ok(M, N, K))
     return set_error(ENGRAM_ERR_INVALID_ARG, "%s: M >= 0, N >= 1 and K >= 1, all under 2^31 - 256", fn);
   if (!act_ok(activation)) return set_error(ENGRAM_ERR_INVALID_ARG, "%s: unknown activation", fn);
@@ -155,9 +162,12 @@ ENGRAM_API engram_status engram_matmul(const uint16_t *a, int64_t a_stride, int3
   if (st != ENGRAM_OK) return st;
   engram::ProductParams p{};
   uint8_t *scratch = static_cast<uint8_t *>(workspace);
-  cudaError_t e = operand_of(ga, scratch, p.a, (cudaStream_t)stream);
-  if (e == cudaSuccess) e = operand_of(gb, scratch, p.b, (cudaStream_t)stream);
+  const Given *given[2] = {&ga, &gb};
+  Operand operands[2];
+  const cudaError_t e = operands_of(given, scratch, operands, (cudaStream_t)stream);
   if (e != cudaSuccess) return launched("engram_matmul launch", e);
+  p.a = operands[0];
+  p.b = operands[1];
   p.M = M;
   p.N = N;
   p.K = K;
@@ -174,36 +184,31 @@ ENGRAM_API engram_status engram_matmul(const uint16_t *a, int64_t a_stride, int3
   return launched("engram_matmul launch", engram::launch_product(p, (cudaStream_t)stream));
 }
 
-ENGRAM_API size_t engram_matmul_grad_workspace_bytes(const void *dy, int32_t dy_dtype, int64_t dy_stride,
-                                                     const uint16_t *a, int64_t a_stride, int32_t a_trans,
-                                                     const uint16_t *b, int64_t b_stride, int32_t b_trans,
-                                                     int64_t M, int64_t N, int64_t K, int32_t activation,
-                                                     int32_t grad_a, int32_t grad_b, int32_t grad_bias) {
-  if (!sizes_ok(M, N, K) || M == 0) return 0;
+ENGRAM_API size_t engram_matmul_grad_workspace_bytes(const engram_matmul_grad_args *args) {
+  if (!args) return 0;
+  const engram_matmul_grad_args &g = *args;
+  if (!sizes_ok(g.M, g.N, g.K) || g.M == 0) return 0;
   size_t bytes = 0;
-  const Given gy{static_cast<const uint16_t *>(dy), dy_stride, false, M, N};
-  if ((grad_a || grad_b) && makes_dz(gy, dy_dtype, activation)) bytes += dz_bytes(M, N);
-  if (grad_bias) bytes += (engram::act_grad_partial_bytes(M, N) + 255) / 256 * 256;
-  if (grad_b) bytes += Given{a, a_stride, a_trans != 0, M, K}.packed_bytes();
-  if (grad_a) bytes += Given{b, b_stride, b_trans != 0, N, K}.packed_bytes();
+  const Given gy{static_cast<const uint16_t *>(g.dy), g.dy_stride, false, g.M, g.N};
+  if ((g.da || g.db) && makes_dz(gy, g.dy_dtype, g.activation)) bytes += dz_bytes(g.M, g.N);
+  if (g.dbias) bytes += (engram::act_grad_partial_bytes(g.M, g.N) + 255) / 256 * 256;
+  if (g.db) bytes += Given{g.a, g.a_stride, g.a_trans != 0, g.M, g.K}.packed_bytes();
+  if (g.da) bytes += Given{g.b, g.b_stride, g.b_trans != 0, g.N, g.K}.packed_bytes();
   return bytes;
 }
 
-ENGRAM_API engram_status engram_matmul_grad(const void *dy, int32_t dy_dtype, int64_t dy_stride, const uint16_t *a,
-                                            int64_t a_stride, int32_t a_trans, const uint16_t *b,
-                                            int64_t b_stride, int32_t b_trans, int64_t M, int64_t N, int64_t K,
-                                            float scale, const void *pre, int32_t pre_dtype, int64_t pre_stride,
-                                            int32_t activation, int32_t accumulate, void *da, int32_t da_dtype,
-                                            int64_t da_stride, void *db, int32_t db_dtype, int64_t db_stride,
-                                            float *dbias, void *workspace, size_t workspace_bytes,
-                                            int32_t *status, void *stream) {
+ENGRAM_API engram_status engram_matmul_grad(const engram_matmul_grad_args *args, void *workspace,
+                                            size_t workspace_bytes, int32_t *status, void *stream) {
   ENGRAM_NVTX_RANGE("engram_matmul_grad");
   const char *fn = "engram_matmul_grad";
   const cudaStream_t s = (cudaStream_t)stream;
+  if (!args) return set_error(ENGRAM_ERR_INVALID_ARG, "%s: args is NULL", fn);
+  const auto [dy, dy_stride, a, a_stride, b, b_stride, M, N, K, given_pre, pre_stride, da, da_stride, db, db_stride,
+              dbias, a_trans, b_trans, activation, dy_dtype, pre_dtype, da_dtype, db_dtype, accumulate, scale] = *args;
   if (!sizes_ok(M, N, K))
     return set_error(ENGRAM_ERR_INVALID_ARG, "%s: M >= 0, N >= 1 and K >= 1, all under 2^31 - 256", fn);
   if (!act_ok(activation)) return set_error(ENGRAM_ERR_INVALID_ARG, "%s: unknown activation", fn);
-  if (activation == ENGRAM_ACT_NONE) pre = nullptr;
+  const void *pre = activation == ENGRAM_ACT_NONE ? nullptr : given_pre;
   if (!da && !db && !dbias && M > 0) return set_error(ENGRAM_ERR_INVALID_ARG, "%s: no gradient is asked for", fn);
   if (!dtype_ok(dy_dtype) || (pre && !dtype_ok(pre_dtype)) || (da && !dtype_ok(da_dtype)) ||
       (db && !dtype_ok(db_dtype)))
@@ -226,9 +231,7 @@ ENGRAM_API engram_status engram_matmul_grad(const void *dy, int32_t dy_dtype, in
                      "%s: a or b NULL or misaligned, or its stride under a row's width or over 2^38", fn);
   Given gy{static_cast<const uint16_t *>(dy), dy_stride, false, M, N};
   const bool dz = (da || db) && M > 0 && makes_dz(gy, dy_dtype, activation);
-  const size_t need = engram_matmul_grad_workspace_bytes(dy, dy_dtype, dy_stride, a, a_stride, a_trans, b,
-                                                         b_stride, b_trans, M, N, K, activation, da != nullptr,
-                                                         db != nullptr, dbias != nullptr);
+  const size_t need = engram_matmul_grad_workspace_bytes(args);
   if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
     return set_error(ENGRAM_ERR_INVALID_ARG, "%s: workspace NULL, not 16-byte aligned or under %zu bytes", fn, need);
   const Span outs[4] = {span_of(da, M, da_stride, K, da ? dtype_bytes(da_dtype) : 0),
@@ -279,9 +282,10 @@ ENGRAM_API engram_status engram_matmul_grad(const void *dy, int32_t dy_dtype, in
     }
     if ((e = engram::launch_act_grad(g, s)) != cudaSuccess) return launched(fn, e);
   }
-  Operand oa{}, ob{};
-  if (db && (e = operand_of(ga, scratch, oa, s)) != cudaSuccess) return launched(fn, e);
-  if (da && (e = operand_of(gb, scratch, ob, s)) != cudaSuccess) return launched(fn, e);
+  const Given *given[2] = {db ? &ga : nullptr, da ? &gb : nullptr};
+  Operand operands[2] = {};
+  if ((e = operands_of(given, scratch, operands, s)) != cudaSuccess) return launched(fn, e);
+  const Operand &oa = operands[0], &ob = operands[1];
   engram::ProductParams pa{}, pb{};
   pa.count = 1;
   pa.scale = scale;

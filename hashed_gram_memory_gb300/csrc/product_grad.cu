@@ -147,16 +147,23 @@ __global__ void __launch_bounds__(256) join_slabs_kernel(const ActGradParams p) 
   p.dbias[n] = p.accumulate ? p.dbias[n] + s : s;
 }
 
-__global__ void __launch_bounds__(256) pack_kernel(const uint16_t *src, int64_t src_stride, uint16_t *dst,
-                                                   int64_t dst_stride, int64_t rows, int64_t cols, int64_t chunks) {
+__global__ void __launch_bounds__(256) pack_kernel(const PackParams p) {
   dependency_wait();
-  const int64_t total = rows * chunks;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / chunks, c = (i - r * chunks) * 8;
-    alignas(16) uint16_t v[8];
+  for (int k = 0; k < p.count; ++k) {
+    const Packed &part = p.part[k];
+    const int64_t chunks = (part.cols + 7) / 8, total = part.rows * chunks;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+      int64_t r;  // a 64-bit division takes longer than the copy
+      if (total <= UINT32_MAX)
+        r = (uint32_t)i / (uint32_t)chunks;
+      else
+        r = i / chunks;
+      const int64_t c = (i - r * chunks) * 8;
+      alignas(16) uint16_t v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? src[r * src_stride + c + j] : 0;
-    *reinterpret_cast<uint4 *>(dst + r * dst_stride + c) = *reinterpret_cast<const uint4 *>(v);
+      for (int j = 0; j < 8; ++j) v[j] = c + j < part.cols ? __ldg(part.src + r * part.src_stride + c + j) : 0;
+      *reinterpret_cast<uint4 *>(part.dst + r * part.dst_stride + c) = *reinterpret_cast<const uint4 *>(v);
+    }
   }
 }
 
@@ -218,12 +225,13 @@ cudaError_t launch_act_grad(ActGradParams p, cudaStream_t stream) {
   return launch(join_slabs_kernel, (p.N + 255) / 256, 256, 0, stream, 1, p);
 }
 
-cudaError_t launch_pack(const void *src, int64_t src_stride, void *dst, int64_t dst_stride, int64_t rows,
-                        int64_t cols, cudaStream_t stream) {
-  const int64_t chunks = (cols + 7) / 8, blocks = (rows * chunks + 255) / 256;
-  return launch(pack_kernel, blocks < 16 * kSms ? blocks : 16 * kSms, 256, 0, stream, 1,
-                static_cast<const uint16_t *>(src), src_stride, static_cast<uint16_t *>(dst), dst_stride, rows, cols,
-                chunks);
+cudaError_t launch_pack(const PackParams &p, cudaStream_t stream) {
+  int64_t blocks = 1;
+  for (int i = 0; i < p.count; ++i) {
+    const int64_t n = (p.part[i].rows * ((p.part[i].cols + 7) / 8) + 255) / 256;
+    if (n > blocks) blocks = n;
+  }
+  return launch(pack_kernel, blocks < 8 * kSms ? blocks : 8 * kSms, 256, 0, stream, 1, p);
 }
 
 }  // namespace engram

@@ -48,10 +48,18 @@ cudaError_t launch_products(const ProductParams &p0, const ProductParams &p1, cu
 bool few_rows_supported(const ProductParams &p);
 cudaError_t launch_few_rows(const ProductParams &p, cudaStream_t stream);
 
-// [rows, cols] 16-bit values from rows src_stride apart to rows dst_stride apart (a multiple of
-// 8, dst 16-byte aligned).
-cudaError_t launch_pack(const void *src, int64_t src_stride, void *dst, int64_t dst_stride, int64_t rows,
-                        int64_t cols, cudaStream_t stream);
+// Copies of [rows, cols] 16-bit values from rows src_stride apart to rows dst_stride apart (a
+// multiple of 8, dst 16-byte aligned).
+struct Packed {
+  const uint16_t *src;
+  uint16_t *dst;
+  int64_t src_stride, dst_stride, rows, cols;
+};
+struct PackParams {
+  Packed part[2];
+  int32_t count;
+};
+cudaError_t launch_pack(const PackParams &p, cudaStream_t stream);
 
 // dz = dy * act'(pre), rounded to bf16, and its column sums before the rounding.
 struct ActGradParams {

@@ -705,25 +705,30 @@ ENGRAM_API engram_status engram_gate_add_grad(const float *k, const uint8_t *sta
  *   out   ENGRAM_DTYPE_* [M, N], out_stride elements between rows
  * Any sizes, strides of a row's width or more, and element alignment.  An operand whose rows
  * do not all start on 16-byte boundaries is copied first, into the workspace:
- *   workspace  device, 16-byte aligned, engram_matmul_workspace_bytes(...) bytes for these
- *         operands; 0 (and workspace unused) when both start on 16-byte boundaries with
- *         strides that are multiples of 8 elements
- * The fp32 sums of long products (fp32 out, K > 8192) are added up in parts of at most 8192,
- * except with an activation or pre and out as its own residual.  A wait that runs out
- * sets ENGRAM_FLAG_TIMEOUT and leaves outputs unwritten.  M == 0 launches nothing.
+ *   workspace  device, 16-byte aligned, engram_matmul_workspace_bytes(args) bytes; 0 (and
+ *         workspace unused) when both operands start on 16-byte boundaries with strides that
+ *         are multiples of 8 elements
+ * Where out or pre is fp32, long sums are added up in parts of at most 768, rounding to
+ * nearest between them (the tensor cores do not inside).  A wait that runs out sets
+ * ENGRAM_FLAG_TIMEOUT and leaves outputs unwritten.  M == 0 launches nothing.
  */
-ENGRAM_API size_t engram_matmul_workspace_bytes(const uint16_t *a, int64_t a_stride, int32_t a_trans,
-                                                const uint16_t *b, int64_t b_stride, int32_t b_trans,
-                                                int64_t M, int64_t N, int64_t K);
-ENGRAM_API engram_status engram_matmul(const uint16_t *a, int64_t a_stride, int32_t a_trans,
-                                       const uint16_t *b, int64_t b_stride, int32_t b_trans,
-                                       int64_t M, int64_t N, int64_t K, float scale,
-                                       const void *bias, int32_t bias_dtype, int32_t activation,
-                                       const void *residual, int32_t residual_dtype,
-                                       int64_t residual_stride, void *pre, int32_t pre_dtype,
-                                       int64_t pre_stride, void *out, int32_t out_dtype,
-                                       int64_t out_stride, void *workspace, size_t workspace_bytes,
-                                       int32_t *status, void *stream);
+typedef struct engram_matmul_args {
+  const uint16_t *a;
+  int64_t a_stride;
+  const uint16_t *b;
+  int64_t b_stride, M, N, K;
+  const void *bias, *residual;
+  int64_t residual_stride;
+  void *pre;
+  int64_t pre_stride;
+  void *out;
+  int64_t out_stride;
+  int32_t a_trans, b_trans, activation, bias_dtype, residual_dtype, pre_dtype, out_dtype;
+  float scale;
+} engram_matmul_args;
+ENGRAM_API size_t engram_matmul_workspace_bytes(const engram_matmul_args *args);
+ENGRAM_API engram_status engram_matmul(const engram_matmul_args *args, void *workspace,
+                                       size_t workspace_bytes, int32_t *status, void *stream);
 
 /*
  * engram_matmul_grad -- the backward pass of engram_matmul for the output gradient dy (the
@@ -738,27 +743,29 @@ ENGRAM_API engram_status engram_matmul(const uint16_t *a, int64_t a_stride, int3
  *   da    ENGRAM_DTYPE_* [M, K], db ENGRAM_DTYPE_* [N, K] with strides between their rows,
  *         dbias fp32 [N]; NULL: not made
  *   accumulate  != 0: db and dbias are added to what is there
- *   workspace  device, 16-byte aligned, engram_matmul_grad_workspace_bytes(...) bytes for
- *         these operands and for the gradients that are asked for
+ *   workspace  device, 16-byte aligned, engram_matmul_grad_workspace_bytes(args) bytes
  * M == 0 zeroes db and dbias (unless they accumulate).
  */
-ENGRAM_API size_t engram_matmul_grad_workspace_bytes(const void *dy, int32_t dy_dtype,
-                                                     int64_t dy_stride, const uint16_t *a,
-                                                     int64_t a_stride, int32_t a_trans,
-                                                     const uint16_t *b, int64_t b_stride,
-                                                     int32_t b_trans, int64_t M, int64_t N,
-                                                     int64_t K, int32_t activation, int32_t grad_a,
-                                                     int32_t grad_b, int32_t grad_bias);
-ENGRAM_API engram_status engram_matmul_grad(const void *dy, int32_t dy_dtype, int64_t dy_stride,
-                                            const uint16_t *a, int64_t a_stride, int32_t a_trans,
-                                            const uint16_t *b, int64_t b_stride, int32_t b_trans,
-                                            int64_t M, int64_t N, int64_t K, float scale,
-                                            const void *pre, int32_t pre_dtype, int64_t pre_stride,
-                                            int32_t activation, int32_t accumulate, void *da,
-                                            int32_t da_dtype, int64_t da_stride, void *db,
-                                            int32_t db_dtype, int64_t db_stride, float *dbias,
-                                            void *workspace, size_t workspace_bytes,
-                                            int32_t *status, void *stream);
+typedef struct engram_matmul_grad_args {
+  const void *dy;
+  int64_t dy_stride;
+  const uint16_t *a;
+  int64_t a_stride;
+  const uint16_t *b;
+  int64_t b_stride, M, N, K;
+  const void *pre;
+  int64_t pre_stride;
+  void *da;
+  int64_t da_stride;
+  void *db;
+  int64_t db_stride;
+  float *dbias;
+  int32_t a_trans, b_trans, activation, dy_dtype, pre_dtype, da_dtype, db_dtype, accumulate;
+  float scale;
+} engram_matmul_grad_args;
+ENGRAM_API size_t engram_matmul_grad_workspace_bytes(const engram_matmul_grad_args *args);
+ENGRAM_API engram_status engram_matmul_grad(const engram_matmul_grad_args *args, void *workspace,
+                                            size_t workspace_bytes, int32_t *status, void *stream);
 
 /*
  * engram_orthogonalise -- the update of a weight matrix from its gradient by momentum and the
