@@ -50,7 +50,7 @@
 
 #include "launch.cuh"
 #include "lookup_common.cuh"
-#include "tensor_core.cuh"
+#include "tensor_pieces.cuh"
 #include "train_internal.cuh"
 
 namespace engram {

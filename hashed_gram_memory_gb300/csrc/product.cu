@@ -36,7 +36,7 @@
 
 #include "launch.cuh"
 #include "product_internal.cuh"
-#include "tensor_core.cuh"
+#include "tensor_pieces.cuh"
 #include "values.cuh"
 
 namespace engram {
