@@ -1245,21 +1245,25 @@ Plan plan_form(const ProductParams &p, const Facts &f, int form, bool rows, cons
 // its warps need for their share of the tile.
 Plan plan_split(const ProductParams &p, const Facts &f, const DeviceInfo &info) {
   Plan best;
-  const int qt = (int)(p.M < kQMax ? ceil_div(p.M, 16) * 16 : kQMax);
-  const int64_t tiles = p.count * tiles_of(p.N, p.M, kP, qt, p.symmetric);
   const double kb = f.d.kblocks;
-  for (int n = 2; n <= 8; n *= 2) {
-    if (n * tiles > 2 * info.sms || kb < n) continue;
-    // A part is two segments: of fp32 outputs not much longer than the others'.
-    if (f.d.segments > 1 && ceil_div(f.d.kblocks, n) > 2 * kSegmentBlocks) continue;
-    Plan s;
-    s.form = kSplit;
-    s.q_tile = qt;
-    s.splits = n;
-    s.tiles = tiles;
-    s.us = 5.6 + 0.2 * kb / n * (n * tiles > info.sms ? 2 : 1) +
-           0.45 * ceil_div(4 * ceil_div(qt, n), kSplitThreads / 32);
-    if (s.us < best.us) best = s;
+  for (int qt = kQMax; qt >= 16; qt /= 2) {
+    if (p.M <= qt / 2 && qt > 16) continue;
+    const int width = p.M < qt ? (int)ceil_div(p.M, 16) * 16 : qt;
+    const int64_t tiles = p.count * tiles_of(p.N, p.M, kP, width, p.symmetric);
+    for (int n = 2; n <= 8; n *= 2) {
+      if (n * tiles > 2 * info.sms || kb < n) continue;
+      // A part is two segments: of fp32 outputs not much longer than the others'.
+      if (f.d.segments > 1 && ceil_div(f.d.kblocks, n) > (n == 2 ? 24 : 32)) continue;
+      Plan s;
+      s.form = kSplit;
+      s.q_tile = width;
+      s.splits = n;
+      s.tiles = tiles;
+      const double stage = fmax(0.2, n * tiles * (kPBytes + 128. * width) / 16e6);  // 16 TB/s out of L2
+      s.us = 5.0 + 0.1 * n + 0.005 * width + stage * kb / n +
+             0.45 * ceil_div(4 * ceil_div(width, n), kSplitThreads / 32);
+      if (s.us < best.us) best = s;
+    }
   }
   return best;
 }
