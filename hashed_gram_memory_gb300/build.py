@@ -24,7 +24,8 @@ SOURCES = ["engram_api.cu", "compress_hash.cu", "lookup_fused.cu", "lookup_bulk.
            "decode_step.cu", "forward.cu", "forward_static.cu", "wkv_gemm.cu", "connection.cu",
            "table_pack.cu", "train_api.cu", "embed.cu", "embed_grad.cu", "gate_grad.cu",
            "fp8_quantise.cu", "fp8_matmul.cu", "product_api.cu", "product.cu",
-           "product_few.cu", "product_grad.cu", "orthogonalise.cu"]
+           "product_few.cu", "product_grad.cu", "orthogonalise.cu",
+           "orthogonalise_small.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -165,6 +165,7 @@ Layout layout_of(int64_t M, int64_t N, int64_t count) {
 size_t orthogonalise_workspace_bytes(int64_t M, int64_t N, int64_t count) { return layout_of(M, N, count).bytes; }
 
 cudaError_t launch_orthogonalise(const OrthogonaliseParams &p, void *workspace, cudaStream_t stream) {
+  if (orthogonalise_small_supported(p)) return launch_orthogonalise_small(p, stream);
   const Layout l = layout_of(p.M, p.N, p.count);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   StartDev s{};

@@ -88,5 +88,9 @@ struct OrthogonaliseParams {
 };
 size_t orthogonalise_workspace_bytes(int64_t M, int64_t N, int64_t count);
 cudaError_t launch_orthogonalise(const OrthogonaliseParams &p, void *workspace, cudaStream_t stream);
+// The same in one launch without a workspace (orthogonalise_small.cu), which launch_orthogonalise
+// takes where it can.
+bool orthogonalise_small_supported(const OrthogonaliseParams &p);
+cudaError_t launch_orthogonalise_small(const OrthogonaliseParams &p, cudaStream_t stream);
 
 }  // namespace engram

@@ -74,7 +74,7 @@ def test_gradient(eg, withheld, M, N, K):
     assert all(torch.equal(x, y) for x, y in zip(got, want))
 
 
-@pytest.mark.parametrize("L,M,N", [(1, 256, 1536), (8, 1024, 1100)])
+@pytest.mark.parametrize("L,M,N", [(1, 256, 1536), (8, 1024, 1100), (2, 90, 100), (1, 60, 2000)])
 def test_orthogonalise(eg, withheld, L, M, N):
     import torch
     g = torch.randn(L, M, N, device="cuda")

@@ -70,6 +70,7 @@ def gradients(g, L, M, N, dtype):
 # Wide, tall and square; odd sides; sides of one; every form of the products.
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("M,N", [(1, 1), (1, 37), (37, 1), (2, 3), (16, 16), (17, 130), (130, 17), (64, 257),
+                                 (128, 64), (128, 3584), (3584, 128), (100, 3585), (90, 700), (1000, 129), (128, 449),
                                  (256, 1536), (475, 300), (300, 475), (513, 1030), (1030, 513), (1100, 1100),
                                  (2100, 700), (700, 2100)])
 def test_sizes(eg, M, N, dtype):
@@ -82,7 +83,7 @@ def test_sizes(eg, M, N, dtype):
 
 
 @pytest.mark.parametrize("nesterov", [False, True])
-@pytest.mark.parametrize("L,M,N", [(1, 65, 200), (3, 200, 65), (12, 130, 260), (40, 16, 24)])
+@pytest.mark.parametrize("L,M,N", [(1, 65, 200), (3, 200, 65), (12, 130, 260), (40, 16, 24), (200, 40, 300), (40, 20, 1800)])
 def test_momentum_and_batches(eg, L, M, N, nesterov):
     """Several steps of several matrices at once: the momentum is beta m + g in fp32, one rounding
     of the sum (fma); every matrix has its own update."""
