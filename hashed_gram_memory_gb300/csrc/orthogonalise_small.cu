@@ -37,6 +37,10 @@ constexpr float kHeld = 256.f;               // what fp16 values are held times
 static_assert(kPart >= kSquare);
 constexpr size_t smem_bytes(int blocks) { return 1024 + (size_t)blocks * kBlock + kSquare + kPart; }
 static_assert(smem_bytes(kMostBlocks) + 1024 <= 227 * 1024);
+// A CTA takes all of an SM's TMEM.  One of a cluster (4 blocks and more) leaves no shared memory for
+// a CTA of another launch that holds TMEM, a split product's with 100 KB and more: two clusters on
+// two SMs, each with the TMEM that the other wants, would wait for ever.
+static_assert(smem_bytes(kMostBlocks / 2 + 1) + 100 * 1024 > 228 * 1024);
 
 struct SmallDev {
   Plane g, momentum, out;
