@@ -1,32 +1,37 @@
 // product.cu -- out = act(scale * a b^T + bias) + residual for 16-bit operands, on the sm_103a
 // tensor cores (tcgen05.mma kind::f16, fp32 accumulators in TMEM).
 //
-// The roles are turned around: the rows of b (the output's columns) are the instruction's M
-// rows, the rows of a its N columns, so that a warp of the epilogue holds 32 neighbouring
-// outputs of one row of out in its lanes and reads and stores whole lines for any stride and
-// size.  Either operand may run along K in memory (K-major) or along its rows (MN-major: boxes
-// of 64 rows x 64 of K, told to the instruction by its descriptors), so the gradient's products
-// and those of the symmetric iteration need no transposed copies.
+// Where out, pre and residual have rows on 16-byte boundaries and there are more than 64 rows, out's
+// rows are the instruction's M rows and lie in the lanes of TMEM: tensor copies move 32 x 32 values
+// at a time through shared memory.  Elsewhere the roles are turned around: out's columns lie in the
+// lanes, and a warp of the epilogue holds 32 neighbouring outputs of one row, which it reads and
+// stores as whole lines for any stride and size.  Either operand may run along K in memory (K-major)
+// or along its rows (MN-major: boxes of 64 rows x 64 of K, told to the instruction by its
+// descriptors), so the gradient's products and those of the symmetric iteration need no transposed
+// copies.
 //
-// Two persistent kernels walk tiles of out:
-//   pairs: CTA pairs (tcgen05.mma.cta_group::2), tiles of 256 (b) x up to 256 (a) values -- each
-//     CTA stages its 128 rows of b and half of the rows of a;
+// Two persistent kernels walk tiles of out; P stands for the operand whose rows are the lanes, Q for
+// the other:
+//   pairs: CTA pairs (tcgen05.mma.cta_group::2), tiles of 256 (P) x up to 256 (Q) values -- each CTA
+//     stages its 128 rows of P and half of the rows of Q;
 //   single: one CTA, 128 x up to 128 tiles, for products too small to fill the pairs; where even
-//     those leave SMs idle (a few rows of a: reading b is the work), 4 or 8 CTAs of a cluster
-//     share a tile, each with a part of K, and add their parts through distributed shared memory
-//     in rank order, two such CTAs an SM.
+//     those leave SMs idle (a few rows of a: reading b is the work), 2 to 8 CTAs of a cluster share a
+//     tile, each with a part of K, and add their parts through distributed shared memory in rank
+//     order, two such CTAs an SM.
+// 65,536 x 4096 x 6144 takes 2035 us in pairs, 1.62 PFLOP/s (the power limit's, as the library's);
+// 37 x 4096 x 6144 15.0 us, K shared by 8: 50 MB, 7.5 us at the measured bandwidth, behind the launch,
+// the first bytes and the joining.
 // Warps: 0, 2 and 3 TMA producers (a ring of stages of 64 of K, 128-byte swizzle); 1 allocates TMEM,
 // one thread (of the pair's even CTA) issues the MMAs into one of two accumulators; 4.. epilogue.
 //
 // The fp32 accumulator of the tensor cores does not round to nearest: its error grows with the
 // number of additions (1e-9 of the result for each value of K, against 1e-6 of an fp32 sum of
 // 8192).  So where out or pre is fp32, K is cut into segments of at most 768 that each start a new
-// accumulator, and the epilogue adds them in registers, rounding to nearest (7e-7 of the result; segments
-// of 512 would be 5e-7 and take 4 % longer, of 1024 1e-6).
+// accumulator, and the epilogue adds them in registers, rounding to nearest (7e-7 of the result;
+// segments of 512 would be 5e-7 and take 4 % longer, of 1024 1e-6).
 //
 // A symmetric product (both operands one matrix) computes the tiles on one side of the diagonal
-// and stores every value twice, the second time transposed: a lane's 16 values of a chunk are
-// neighbours there.
+// and stores every unit of 32 x 32 values twice, the second time turned in shared memory.
 //
 // Every wait is bounded as in wkv_gemm.cu: one that gives up sets ENGRAM_FLAG_TIMEOUT and leaves
 // the tiles not yet stored unwritten.
@@ -1088,9 +1093,14 @@ bool make_plane_map(CUtensorMap *map, const PlaneDev &d, int64_t M, int64_t N, i
 struct DeviceInfo {
   bool ready = false;
   int sms = 0, pairs = 0;  // pairs: CTA pairs that fit at once
+  int clusters[9] = {};    // clusters of 2 .. 8 CTAs, two an SM, that do
 };
 DeviceInfo g_info[64];
 std::mutex g_info_mu;
+
+// Has the threads and the shared memory of a CTA that shares K.  Of a kernel with tensor memory the
+// occupancy calls count one CTA an SM, whatever it takes; of this one the two that there are.
+__global__ void __launch_bounds__(kSplitThreads, 2) two_an_sm_kernel() {}
 
 using Kernel = void (*)(Jobs);
 enum Form { kSingle, kSplit, kPair, kForms };
@@ -1129,6 +1139,15 @@ cudaError_t device_info(DeviceInfo &out) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     if ((e = cudaOccupancyMaxActiveClusters(&d.pairs, kernel_of(kPair, kPlain), &cfg)) != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(two_an_sm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSplitSmemBytes);
+    cfg.blockDim = dim3(kSplitThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSplitSmemBytes;
+    for (int n = 2; n <= 8 && e == cudaSuccess; ++n) {
+      attr.val.clusterDim.x = n;
+      cfg.gridDim = dim3(2 * d.sms / n * n, 1, 1);
+      e = cudaOccupancyMaxActiveClusters(d.clusters + n, two_an_sm_kernel, &cfg);
+    }
+    if (e != cudaSuccess) return e;
     d.ready = true;
   }
   out = d;
@@ -1206,7 +1225,11 @@ Facts facts_of(const ProductParams &p) {
 // on average; the form that they choose takes 2 % longer than the fastest).  A tile takes the
 // longer of its products (by the stages of K, which single CTAs cannot take in faster than 0.17 us
 // and pairs than 0.15) and of its epilogue (by the bytes that a value of out moves); the other of
-// the two counts once, where nothing hides it.
+// the two counts once, where nothing hides it.  No form reads the operands faster than memory gives
+// them.
+double read_us(const ProductParams &p, double of_b = 1) {
+  return p.count * ((p.symmetric ? 0 : p.M) + of_b * p.N) * p.K * 2 / 6.5e6;
+}
 
 // The best tile width of a form without splits.
 Plan plan_form(const ProductParams &p, const Facts &f, int form, bool rows, const DeviceInfo &info) {
@@ -1215,7 +1238,7 @@ Plan plan_form(const ProductParams &p, const Facts &f, int form, bool rows, cons
   const int step = rows || pair ? kUnit : 16, workers = pair ? info.pairs : info.sms;
   Plan best;
   if (workers <= 0 || (pair && P <= kP)) return best;
-  const double kb = f.d.kblocks;
+  const double kb = f.d.kblocks, read = read_us(p);
   const auto bytes = [](const PlaneDev &x) { return !x.p ? 0 : x.type == ENGRAM_DTYPE_F32 ? 4 : 2; };
   const double moved = (1 + bytes(f.d.out) * (p.symmetric ? 2 : 1) + bytes(f.d.residual) + bytes(f.d.pre)) / 3.;
   for (int qt = pair ? kPairQMax : kQMax; qt >= step; qt -= step) {
@@ -1235,14 +1258,15 @@ Plan plan_form(const ProductParams &p, const Facts &f, int form, bool rows, cons
       epilogue = rows ? 0.65 + 0.0058 * qt * moved : 0.9 + 0.0071 * qt * moved;
     }
     n.tile_us = fmax(products, epilogue);
-    n.us = (pair ? 3.0 : 2.8) + ceil_div(n.tiles, workers) * n.tile_us + fmin(products, epilogue);
+    n.us = (pair ? 3.0 : 2.8) + fmax(ceil_div(n.tiles, workers) * n.tile_us, read) + fmin(products, epilogue);
     if (n.us < best.us) best = n;
   }
   return best;
 }
 
-// K shared by 2, 4 or 8 CTAs, two an SM: what a CTA takes of K, and the joining, by the rounds that
-// its warps need for their share of the tile.
+// K shared by 2 to 8 CTAs, two an SM: what a CTA takes of K, and the joining, by the rounds that its
+// warps need for their share of the tile.  Only as many clusters as run at once: 36 of 8 take 12.7 us
+// of 37 x 4608 x 4096, 37 of them 20.6 of 37 x 4736 x 4096.
 Plan plan_split(const ProductParams &p, const Facts &f, const DeviceInfo &info) {
   Plan best;
   const double kb = f.d.kblocks;
@@ -1250,8 +1274,8 @@ Plan plan_split(const ProductParams &p, const Facts &f, const DeviceInfo &info) 
     if (p.M <= qt / 2 && qt > 16) continue;
     const int width = p.M < qt ? (int)ceil_div(p.M, 16) * 16 : qt;
     const int64_t tiles = p.count * tiles_of(p.N, p.M, kP, width, p.symmetric);
-    for (int n = 2; n <= 8; n *= 2) {
-      if (n * tiles > 2 * info.sms || kb < n) continue;
+    for (int n = 2; n <= 8; ++n) {
+      if (tiles > info.clusters[n] || kb < n) continue;
       // A part is two segments: of fp32 outputs not much longer than the others'.
       if (f.d.segments > 1 && ceil_div(f.d.kblocks, n) > (n == 2 ? 24 : 32)) continue;
       Plan s;
@@ -1259,8 +1283,13 @@ Plan plan_split(const ProductParams &p, const Facts &f, const DeviceInfo &info) 
       s.q_tile = width;
       s.splits = n;
       s.tiles = tiles;
-      const double stage = fmax(0.2, n * tiles * (kPBytes + 128. * width) / 16e6);  // 16 TB/s out of L2
-      s.us = 5.0 + 0.1 * n + 0.005 * width + stage * kb / n +
+      // Stages at 0.2 us, of which reading b (a part again for each further tile of a) hides a part; or L2
+      // gives no more than 16 TB/s.  Clusters of 3, 5, 6 and 7 lie less well on the SMs (20 x 4096 x
+      // 4096: 4 11.1 us, 6 12.3, 8 10.9).
+      const double stages = 0.2 * kb / n, read = read_us(p, 0.85 + 0.15 * ceil_div(p.M, width));
+      const double taken = fmax(fmax(stages, read) + 0.4 * fmin(stages, read),
+                                tiles * (kPBytes + 128. * width) / 16e6 * kb);
+      s.us = 5.0 + 0.1 * n + 0.005 * width + taken + (n & (n - 1) ? 1.0 : 0.0) +
              0.45 * ceil_div(4 * ceil_div(width, n), kSplitThreads / 32);
       if (s.us < best.us) best = s;
     }

@@ -108,7 +108,7 @@ def product(eg, a, b, out="f32", act="none", bias=None, residual=None, scale=1.0
     return got
 
 
-# One CTA to a tile, K shared by 4 or 8 CTAs, pairs; odd sizes; lengths of one; several segments.
+# One CTA to a tile, K shared by 2 to 8 CTAs, pairs; odd sizes; lengths of one; several segments.
 SIZES = [(1, 1, 1), (1, 16, 8), (3, 1, 70), (1, 4096, 512), (16, 130, 2048), (37, 4096, 640), (128, 128, 64),
          (129, 131, 129), (300, 257, 1000), (1000, 500, 72), (513, 1030, 520), (2050, 700, 1100), (700, 2100, 300),
          (1, 300, 20000), (40, 140, 70000), (1300, 1100, 8300)]
@@ -119,6 +119,15 @@ SIZES = [(1, 1, 1), (1, 16, 8), (3, 1, 70), (1, 4096, 512), (16, 130, 2048), (37
 def test_matmul_sizes(eg, M, N, K, out):
     g = gen(M + N + K)
     product(eg, matrix(g, M, K), matrix(g, N, K), out)
+
+
+# K shared by 2 to 8 CTAs: as many of a tile as run at once.
+@pytest.mark.parametrize("M,N,K", [(24, 4097, 2100), (37, 4864, 3500), (33, 5500, 2900), (64, 7296, 6144), (20, 9300, 4500),
+                                   (60, 5000, 5000), (128, 128, 700), (65, 260, 1290)])
+def test_matmul_few_rows_of_many_columns(eg, M, N, K):
+    g = gen(M + N + K)
+    for out in ("f32", "bf16"):
+        product(eg, matrix(g, M, K), matrix(g, N, K), out, act="silu", residual=matrix(g, M, N))
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 40, 24), (130, 140, 150), (70, 4100, 1030), (523, 1031, 777), (1024, 1536, 512)])
