@@ -18,7 +18,7 @@ namespace engram {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxParts = 8 * kSms;  // blocks a matrix
+constexpr int kMostParts = 8 * kSms;  // blocks a matrix
 constexpr float kHeld = 256.f;  // what fp16 values are held times
 
 struct StartDev {
@@ -53,29 +53,43 @@ __device__ __forceinline__ void store_values(float *at, const float (&x)[VEC]) {
     *reinterpret_cast<float4 *>(at) = make_float4(x[0], x[1], x[2], x[3]);
 }
 
-// u of VEC elements; with FIRST the momentum moves.
-template <int VEC, typename T, bool FIRST>
-__device__ __forceinline__ void update_of(const StartDev &p, int64_t z, int64_t m, int64_t n, float (&u)[VEC]) {
-  load_values<VEC>(static_cast<const T *>(p.g.p) + z * p.g.batch + m * p.g.stride + n, u);
-  if (!p.momentum.p) return;
-  float *at = static_cast<float *>(p.momentum.p) + z * p.momentum.batch + m * p.momentum.stride + n;
-  float v[VEC];
-  load_values<VEC>(at, v);
-  if (FIRST) {
+// f(row, column, u) for a block's share of a matrix in steps of VEC columns, `lanes` threads a row;
+// with FIRST the momentum moves.  A thread asks for kAhead steps, then has them.
+constexpr int kAhead = 4;
+template <int VEC, typename T, bool FIRST, typename F>
+__device__ __forceinline__ void over_share(const StartDev &p, int64_t z, int part, F f) {
+  const uint32_t lanes = p.lanes, rows = kThreads / lanes, n0 = (threadIdx.x & (lanes - 1)) * VEC;
+  const uint32_t M = p.M, N = p.N;
+  const T *g = static_cast<const T *>(p.g.p) + z * p.g.batch;
+  float *momentum = static_cast<float *>(p.momentum.p) + z * p.momentum.batch;
+  uint32_t m = part * rows + threadIdx.x / lanes, n = n0;
+  if (n0 >= N) return;
+  while (m < M) {
+    uint32_t mm[kAhead], nn[kAhead];
+    float u[kAhead][VEC], v[kAhead][VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = fmaf(p.beta, v[i], u[i]);
-    store_values<VEC>(at, v);
+    for (int k = 0; k < kAhead; ++k) {
+      mm[k] = m, nn[k] = n;
+      if (m >= M) continue;
+      load_values<VEC>(g + m * p.g.stride + n, u[k]);
+      if (p.momentum.p) load_values<VEC>(momentum + m * p.momentum.stride + n, v[k]);
+      if ((n += lanes * VEC) >= N) n = n0, m += p.parts * rows;
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (mm[k] >= M) continue;
+      if (p.momentum.p) {
+        if (FIRST) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) v[k][i] = fmaf(p.beta, v[k][i], u[k][i]);
+          store_values<VEC>(momentum + mm[k] * p.momentum.stride + nn[k], v[k]);
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) u[k][i] = p.nesterov ? fmaf(p.beta, v[k][i], u[k][i]) : v[k][i];
+      }
+      f(mm[k], nn[k], u[k]);
+    }
   }
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) u[i] = p.nesterov ? fmaf(p.beta, v[i], u[i]) : v[i];
-}
-
-// f(row, column) for a block's share of a matrix in steps of VEC columns: `lanes` threads a row.
-template <int VEC, typename F>
-__device__ __forceinline__ void over_share(const StartDev &p, int part, F f) {
-  const int lanes = p.lanes, rows = kThreads / lanes;
-  for (int m = part * rows + threadIdx.x / lanes; m < p.M; m += p.parts * rows)
-    for (int n = (threadIdx.x & (lanes - 1)) * VEC; n < p.N; n += lanes * VEC) f(m, n);
 }
 
 __device__ __forceinline__ float block_sum(float v) {
@@ -96,9 +110,7 @@ __global__ void __launch_bounds__(kThreads) momentum_kernel(const StartDev p) {
   const int64_t z = blockIdx.x / p.parts;
   const int part = blockIdx.x - (int)z * p.parts;
   float sum = 0.f;
-  over_share<VEC>(p, part, [&](int m, int n) {
-    float u[VEC];
-    update_of<VEC, T, true>(p, z, m, n, u);
+  over_share<VEC, T, true>(p, z, part, [&](int64_t, int64_t, const float (&u)[VEC]) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) sum = fmaf(u[i], u[i], sum);
   });
@@ -115,10 +127,8 @@ __global__ void __launch_bounds__(kThreads) normalise_kernel(const StartDev p) {
   float sum = 0.f;
   for (int i = threadIdx.x; i < p.parts; i += kThreads) sum += p.partial[z * p.parts + i];
   const float by = kHeld / (sqrtf(block_sum(sum)) + p.eps);
-  over_share<VEC>(p, part, [&](int m, int n) {
-    float u[VEC];
-    update_of<VEC, T, false>(p, z, m, n, u);
-    __half *at = p.x + z * p.x_batch + (int64_t)m * p.x_stride + n;
+  over_share<VEC, T, false>(p, z, part, [&](int64_t m, int64_t n, const float (&u)[VEC]) {
+    __half *at = p.x + z * p.x_batch + m * p.x_stride + n;
     if constexpr (VEC == 1) {
       *at = __float2half_rn(u[0] * by);
     } else {
@@ -155,7 +165,7 @@ Layout layout_of(int64_t M, int64_t N, int64_t count) {
   l.x[1] = take(l.x_batch * count * 2);
   l.a = take(l.a_batch * count * 2);
   l.b = take(l.a_batch * count * 2);
-  l.partial = take((size_t)kMaxParts * count * sizeof(float));
+  l.partial = take((size_t)kMostParts * count * sizeof(float));
   l.bytes = at;
   return l;
 }
@@ -181,13 +191,16 @@ cudaError_t launch_orthogonalise(const OrthogonaliseParams &p, void *workspace, 
   s.eps = p.eps;
   s.nesterov = p.nesterov;
   const bool wide = p.N % 4 == 0 && words(p.g, p.count) && words(p.momentum, p.count);
+  // As many lanes as a row has values for; of words those of which a row leaves the fewest idle.
+  const int64_t vectors = wide ? (p.N + 3) / 4 : p.N;
+  const auto taken = [&](int lanes) { return (vectors + lanes - 1) / lanes * lanes; };
   s.lanes = 1;
-  while (s.lanes < kThreads && s.lanes * (wide ? 4 : 1) < p.N) s.lanes *= 2;
-  // About eight blocks an SM.
+  for (int lanes = 1; lanes <= kThreads && lanes / 2 < vectors; lanes *= 2)
+    if (!wide || lanes <= 32 || taken(lanes) <= taken(s.lanes)) s.lanes = lanes;
   const int64_t rows = kThreads / s.lanes, most = (p.M + rows - 1) / rows;
-  int64_t parts = (8 * kSms + p.count - 1) / p.count;
+  const int blocks = (wide ? 4 : 8) * kSms;  // as many as run at once
+  int64_t parts = p.count < blocks ? blocks / p.count : 1;
   if (parts > most) parts = most;
-  if (parts > kMaxParts) parts = kMaxParts;
   s.parts = (int32_t)parts;
   using Start = void (*)(StartDev);
   static constexpr Start first[4] = {momentum_kernel<1, __nv_bfloat16>, momentum_kernel<1, float>,
