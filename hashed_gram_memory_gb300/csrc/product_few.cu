@@ -8,7 +8,8 @@
 // values of a row, one 16-byte word, for every two instructions.  Those words come through shared
 // memory, copied asynchronously kDeep steps ahead, and each lane reads back what it copied itself:
 // nothing to wait for but its own copies.  A block has 16 rows of b, its warps take 32 of K in turn
-// and add their sums in shared memory, always in the same order.
+// and add their sums in shared memory, always in the same order.  1 x 4096 x 6144 takes 11.3 us, 50 MB
+// of b at 4.4 TB/s, 3.9 us of them before the first and after the last bytes.
 #include <atomic>
 
 #include "launch.cuh"
@@ -168,8 +169,8 @@ cudaError_t launch_eights(const FewDev &d, int64_t grid, cudaStream_t stream) {
 bool few_rows_supported(const ProductParams &p) {
   // Every block reads all rows of a: from 9 rows on that costs more than it saves where b is large
   // (16 x 4096 x 6144 14.0 us and 15.5 by clusters, 16 x 8192 x 8192 32.5 and 26.7).
-  return (p.M <= 8 || (p.M <= 16 && p.N * p.K <= 28 << 20)) && p.count == 1 && !p.symmetric && !p.f16 && !p.a.t && !p.b.t &&
-         p.out.type != kTypeF16;
+  return (p.M <= 8 || (p.M <= 16 && p.N * p.K <= 28 << 20)) && p.count == 1 && !p.symmetric && !p.f16 && !p.a.t &&
+         !p.b.t && p.out.type != kTypeF16;
 }
 
 cudaError_t launch_few_rows(const ProductParams &p, cudaStream_t stream) {

@@ -36,7 +36,7 @@ struct ProductParams {
   int32_t bias_type, act;
   // a and b are one matrix and so out is symmetric (as must be residual): the products on one
   // side of the diagonal are computed, and written on both; out and residual are fp16, their
-  // rows on 16-byte boundaries and readable up to the next multiple of 16
+  // rows on 16-byte boundaries
   bool symmetric;
   int32_t *status;
 };
