@@ -130,6 +130,32 @@ def test_matmul_few_rows_of_many_columns(eg, M, N, K):
         product(eg, matrix(g, M, K), matrix(g, N, K), out, act="silu", residual=matrix(g, M, N))
 
 
+@pytest.mark.parametrize("N,stride", [(5, 8), (9, 16), (33, 64), (191, 192), (185, 192), (252, 256), (1001, 1024)])
+@pytest.mark.parametrize("M,K", [(3, 40), (30, 600), (200, 64), (640, 1700)])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_matmul_leaves_what_lies_beside(eg, M, N, K, stride, out):
+    """Rows on 16 bytes that end inside 16 bytes: the values behind them stay, of out, pre and the
+    gradients."""
+    import torch
+    g = gen(M + N)
+    mine = {name: torch.full((rows + 1, width), 7.0, dtype=dt(out), device="cuda")
+            for name, rows, width in (("out", M, stride), ("pre", M, stride), ("da", M, stride), ("db", K, stride))}
+    a, b, r = matrix(g, M, K), matrix(g, N, K), matrix(g, M, N)
+    dst = mine["out"][:M, :N]
+    product(eg, a, b, out, dst=dst)
+    product(eg, a, b, out, act="silu", residual=r, dst=dst)
+    dst.copy_(r)
+    eg.engram_matmul(a, b, residual=dst, pre=mine["pre"][:M, :N], out=dst)
+    close(mine["pre"][:M, :N], a.double() @ b.double().t(), (K / 16 + 16) * 2.0 ** -22 * (a.double().abs() @ b.double().abs().t()), out)
+    dy, c = matrix(g, M, K), matrix(g, K, N)
+    eg.engram_matmul_grad(dy, r, c, da=mine["da"][:M, :N], db=mine["db"][:K, :N])
+    for name, rows in (("out", M), ("pre", M), ("da", M), ("db", K)):
+        buf = mine[name].clone()
+        assert not (buf[:rows, :N] == 7.0).all()
+        buf[:rows, :N] = 7.0
+        assert (buf == 7.0).all(), name
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 40, 24), (130, 140, 150), (70, 4100, 1030), (523, 1031, 777), (1024, 1536, 512)])
 @pytest.mark.parametrize("a", ["rows", "columns"])
 @pytest.mark.parametrize("b", ["rows", "columns"])

@@ -149,6 +149,17 @@ def test_strides(eg):
             check(one, x[1].double() * 1.95)
 
 
+@pytest.mark.parametrize("L,M,N,stride", [(2, 60, 91, 96), (2, 129, 191, 192), (1, 333, 210, 216), (3, 130, 1001, 1024)])
+def test_leaves_what_lies_beside(eg, L, M, N, stride):
+    import torch
+    x = gradients(gen(3), L, M, N, torch.float32)
+    out = torch.full((L, M + 1, stride), 7.0, dtype=torch.bfloat16, device="cuda")
+    eg.engram_orthogonalise(x, out=out[:, :M, :N])
+    assert torch.equal(out[:, :M, :N], eg.engram_orthogonalise(x))
+    out[:, :M, :N] = 7.0
+    assert (out == 7.0).all()
+
+
 def test_special_matrices(eg):
     """Zeros stay zero, one entry alone stays one, a NaN is its own matrix's; tiny and huge
     gradients come out as others do."""
