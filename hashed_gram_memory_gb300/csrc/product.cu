@@ -242,8 +242,8 @@ struct Walk {
 // How a kernel's epilogue moves its values.
 //   tiles: the lanes of TMEM are rows of out.  A lane turns 32 values of its row into words that it
 //     puts into shared memory, from where tensor copies take 32 x 32 values at a time to out (and
-//     pre); the residual comes in the same way, asked for ahead.  Where out, pre and residual have
-//     rows on 16-byte boundaries.
+//     pre); the residual comes in the same way, asked for ahead.  Where their rows lie on 16-byte
+//     boundaries.
 //   singles: the lanes of TMEM are columns of out.  A warp moves 32 neighbouring values of a row at a
 //     time: any strides, few rows, sums in segments.
 // A symmetric product takes the first, with a second store of each unit below the diagonal.

@@ -156,6 +156,27 @@ def test_matmul_leaves_what_lies_beside(eg, M, N, K, stride, out):
         assert (buf == 7.0).all(), name
 
 
+@pytest.mark.parametrize("N", [33000, 33001])
+def test_offsets_past_32_bits(eg, N):
+    """Outputs and gradients of more than 2^31 elements, on 16-byte boundaries and off them."""
+    import torch
+    M, K = 66000, 40
+    g = gen(N)
+    a, b = matrix(g, M, K), matrix(g, N, K)
+    y = eg.engram_matmul(a, b, out_dtype=torch.bfloat16)
+    rows = torch.tensor([0, 1, M // 2, 65074, 65080, M - 2, M - 1], device="cuda")
+    want = a[rows].double() @ b.double().t()
+    close(y[rows], want, (K / 16 + 16) * 2.0 ** -22 * (a[rows].double().abs() @ b.double().abs().t()), "bf16")
+    da, db, dbias = eg.engram_matmul_grad(y, a, b, grad_bias=True, da_dtype=torch.float32, db_dtype=torch.float32)
+    z = y[rows].double()
+    close(da[rows], z @ b.double(), (N / 16 + 16) * 2.0 ** -22 * (z.abs() @ b.double().abs()), "f32")
+    cols = slice(N - 300, N)
+    z = y[:, cols].double()
+    t = (M / 16 + 16) * 2.0 ** -22
+    close(db[cols], z.t() @ a.double(), t * (z.abs().t() @ a.double().abs()), "f32")
+    close(dbias[cols], z.sum(0), (M + 4) * 2.0 ** -24 * z.abs().sum(0), "f32")
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 40, 24), (130, 140, 150), (70, 4100, 1030), (523, 1031, 777), (1024, 1536, 512)])
 @pytest.mark.parametrize("a", ["rows", "columns"])
 @pytest.mark.parametrize("b", ["rows", "columns"])
