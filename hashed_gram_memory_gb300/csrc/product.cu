@@ -981,6 +981,15 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : 
         if constexpr (SPLIT) {
           // The partial tile into shared memory (the stages: every MMA has read them).
           const bool two = blocks(p) > 1;
+          if (p.residual.p) {  // what is added in the end is on its way to L2 meanwhile
+            const Tile t = tile_at<kTileP, SYMMETRIC>(p, worker);
+            const int q_begin = qt * rank / splits, rows = qt * (rank + 1) / splits - q_begin;
+            for (int i = warp - 4; i < 4 * rows; i += 4 * kPartsHere) {
+              const int m = t.q0 + q_begin + (i >> 2), n = t.p0 + (i & 3) * 32 + lane;
+              if ((lane & 7) == 0 && m < p.M && n < p.N)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(element(p.residual, t.z, m, n)));
+            }
+          }
           ok = warp_wait(acc_full, 0, abort_flag, p) && (!two || warp_wait(acc_full + 1, 0, abort_flag, p));
           if (!ok) return;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -1014,9 +1023,10 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : 
     __syncwarp();
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     cluster_sync();
-    bool ok = true;
-    for (int r = 0; r < splits; ++r)  // a CTA that gave up has no partial tile
-      ok &= load_cluster(map_to_rank(smem_u32(const_cast<int *>(abort_flag)), r)) == 0;
+    // A CTA that gave up has no partial tile.  A lane asks one of them: one after the other took 0.8 us.
+    const bool gave_up =
+        lane < splits && load_cluster(map_to_rank(smem_u32(const_cast<int *>(abort_flag)), lane)) != 0;
+    const bool ok = !__any_sync(0xffffffffu, gave_up);
     const Tile t = tile_at<kTileP, SYMMETRIC>(p, worker);
     // A warp 32 neighbouring outputs of one row of out at a time.  Little code, as most launches run
     // through it once or twice and fetch it from far away.
