@@ -19,7 +19,7 @@
 //     tile, each with a part of K, and add their parts through distributed shared memory in rank
 //     order, two such CTAs an SM.
 // 65,536 x 4096 x 6144 takes 2035 us in pairs, 1.62 PFLOP/s (the power limit's, as the library's);
-// 37 x 4096 x 6144 15.0 us, K shared by 8: 50 MB, 7.5 us at the measured bandwidth, behind the launch,
+// 37 x 4096 x 6144 13.5 us, K shared by 8: 50 MB, 7.5 us at the measured bandwidth, behind the launch,
 // the first bytes and the joining.
 // Warps: 0, 2 and 3 TMA producers (a ring of stages of 64 of K, 128-byte swizzle); 1 allocates TMEM,
 // one thread (of the pair's even CTA) issues the MMAs into one of two accumulators; 4.. epilogue.
@@ -981,7 +981,7 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : 
         if constexpr (SPLIT) {
           // The partial tile into shared memory (the stages: every MMA has read them).
           const bool two = blocks(p) > 1;
-          if (p.residual.p) {  // what is added in the end is on its way to L2 meanwhile
+          if (p.residual.p) {  // what is added in the end comes to L2 meanwhile: 0.7 us less
             const Tile t = tile_at<kTileP, SYMMETRIC>(p, worker);
             const int q_begin = qt * rank / splits, rows = qt * (rank + 1) / splits - q_begin;
             for (int i = warp - 4; i < 4 * rows; i += 4 * kPartsHere) {
@@ -1280,8 +1280,8 @@ Plan plan_form(const ProductParams &p, const Facts &f, int form, bool rows, cons
 }
 
 // K shared by 2 to 8 CTAs, two an SM: what a CTA takes of K, and the joining, by the rounds that its
-// warps need for their share of the tile.  Only as many clusters as run at once: 36 of 8 take 12.7 us
-// of 37 x 4608 x 4096, 37 of them 20.6 of 37 x 4736 x 4096.
+// warps need for their share of the tile.  Only as many clusters as run at once: 36 of 8 take 11.8 us
+// of 37 x 4608 x 4096, 37 of them 17.1 of 37 x 4736 x 4096.
 Plan plan_split(const ProductParams &p, const Facts &f, const DeviceInfo &info) {
   Plan best;
   const double kb = f.d.kblocks;
@@ -1300,11 +1300,11 @@ Plan plan_split(const ProductParams &p, const Facts &f, const DeviceInfo &info) 
       s.tiles = tiles;
       // Stages at 0.2 us, of which reading b (a part again for each further tile of a) hides a part; or L2
       // gives no more than 16 TB/s.  Clusters of 3, 5, 6 and 7 lie less well on the SMs (20 x 4096 x
-      // 4096: 4 11.1 us, 6 12.3, 8 10.9).
+      // 4096: 4 9.3 us, 6 10.4, 8 9.3).
       const double stages = 0.2 * kb / n, read = read_us(p, 0.85 + 0.15 * ceil_div(p.M, width));
       const double taken = fmax(fmax(stages, read) + 0.4 * fmin(stages, read),
                                 tiles * (kPBytes + 128. * width) / 16e6 * kb);
-      s.us = 5.0 + 0.1 * n + 0.005 * width + taken + (n & (n - 1) ? 1.0 : 0.0) +
+      s.us = 4.4 + 0.005 * width + taken + (n & (n - 1) ? 1.0 : 0.0) +
              0.45 * ceil_div(4 * ceil_div(width, n), kSplitThreads / 32);
       if (s.us < best.us) best = s;
     }
