@@ -138,56 +138,84 @@ __global__ void __launch_bounds__(THREADS) act_grad_kernel(const ActGradParams p
   }
 }
 
-// dbias = the slabs' sums, in order.
-__global__ void __launch_bounds__(256) join_slabs_kernel(const ActGradParams p) {
+// dbias = the slabs' sums: a block has 32 columns, its warps some slabs each, in order.
+constexpr int kJoinWarps = 8;
+__global__ void __launch_bounds__(32 * kJoinWarps) join_slabs_kernel(const ActGradParams p) {
   dependency_wait();
-  const int64_t n = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (n >= p.N) return;
+  __shared__ float sums[kJoinWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t n = (int64_t)blockIdx.x * 32 + lane;
+  const int begin = p.slabs * warp / kJoinWarps, end = p.slabs * (warp + 1) / kJoinWarps;
   float s = 0.f;
+  if (n < p.N) {
 #pragma unroll 8
-  for (int i = 0; i < p.slabs; ++i) s += p.partial[i * p.N + n];
+    for (int i = begin; i < end; ++i) s += p.partial[i * p.N + n];
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0 || n >= p.N) return;
+  for (int i = 1; i < kJoinWarps; ++i) s += sums[i][lane];
   p.dbias[n] = p.accumulate ? p.dbias[n] + s : s;
 }
 
 // Copies rows of 16-bit values to rows on 16 bytes, zeros up to the next 8.  A lane two neighbouring
 // columns, so that a warp reads and stores whole lines; kPackRows rows of them at a time: all loads,
-// then the stores.  16,411 x 1278 and 2573 x 1278 together: 25 us, 3.9 TB/s (37 with
-// a lane's 8 neighbouring columns read one by one).
+// then the stores.  A row that does not start on 4 bytes is read in words all the same, of which a lane
+// shifts its two values together; at the first and last rows, where such words would reach beyond
+// the matrix, values are read one by one.  16,411 x 1278 and 2573 x 1278 together: 23 us; 37,056 x 576
+// with odd strides 21 us, 4.1 TB/s (52 with values one by one: the instructions are what counts).
 constexpr int kPackRows = 8;
 __global__ void __launch_bounds__(256) pack_kernel(const PackParams p) {
   dependency_wait();
   const int lane = threadIdx.x & 31;
   for (int k = 0; k < p.count; ++k) {
     const Packed &part = p.part[k];
-    const int64_t pieces = ((part.cols + 7) / 8 * 4 + 31) / 32, total = (part.rows + kPackRows - 1) / kPackRows * pieces;
+    const int cols = (int)part.cols, padded = (cols + 7) / 8 * 8, pieces = (padded / 2 + 31) / 32;
+    const int64_t total = (part.rows + kPackRows - 1) / kPackRows * pieces;
+    const int64_t end = (part.rows - 1) * part.src_stride + cols;
     for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += (int64_t)gridDim.x * 8) {
       int64_t group;  // a 64-bit division takes longer than the copy
       if (total <= UINT32_MAX)
         group = (uint32_t)i / (uint32_t)pieces;
       else
         group = i / pieces;
-      const int64_t c = (i - group * pieces) * 64 + lane * 2, r0 = group * kPackRows;
-      if (c >= (part.cols + 7) / 8 * 8) continue;
-      const int rows = (int)min((int64_t)kPackRows, part.rows - r0);
+      const int c0 = (int)(i - group * pieces) * 64, c = c0 + lane * 2;
+      const int64_t r0 = group * kPackRows;
       const uint16_t *src = part.src + r0 * part.src_stride + c;
-      uint32_t v[kPackRows];
-      if (part.even && c + 1 < part.cols) {  // every row's pairs on 4 bytes
+      uint16_t *dst = part.dst + r0 * part.dst_stride + c;
+      // A lane's words end at most 66 columns on from c0: inside the row, or in those behind it.
+      if ((r0 > 0 || c0 > 0) && r0 + kPackRows <= part.rows &&
+          (r0 + kPackRows - 1) * part.src_stride + c0 + 66 <= end) {
+        uint32_t low[kPackRows], high[kPackRows];
 #pragma unroll
-        for (int j = 0; j < kPackRows; ++j)
-          if (j < rows) v[j] = __ldg(reinterpret_cast<const uint32_t *>(src + j * part.src_stride));
-      } else {
+        for (int j = 0; j < kPackRows; ++j) {
+          const uintptr_t at = reinterpret_cast<uintptr_t>(src + j * part.src_stride);
+          const uint32_t *word = reinterpret_cast<const uint32_t *>(at & ~(uintptr_t)3);
+          low[j] = __ldg(word);
+          high[j] = at & 2 ? __ldg(word + 1) : 0;
+        }
+        const uint32_t keep = c + 1 < cols ? ~0u : c < cols ? 0xffffu : 0u;
+        if (c < padded) {
+#pragma unroll
+          for (int j = 0; j < kPackRows; ++j) {
+            const uint32_t shift = reinterpret_cast<uintptr_t>(src + j * part.src_stride) & 2 ? 16 : 0;
+            *reinterpret_cast<uint32_t *>(dst + j * part.dst_stride) = __funnelshift_r(low[j], high[j], shift) & keep;
+          }
+        }
+      } else if (c < padded) {
+        const int rows = (int)min((int64_t)kPackRows, part.rows - r0);
+        uint32_t v[kPackRows];
 #pragma unroll
         for (int j = 0; j < kPackRows; ++j)
           if (j < rows) {
-            const uint32_t lo = c < part.cols ? __ldg(src + j * part.src_stride) : 0;
-            const uint32_t hi = c + 1 < part.cols ? __ldg(src + j * part.src_stride + 1) : 0;
+            const uint32_t lo = c < cols ? __ldg(src + j * part.src_stride) : 0;
+            const uint32_t hi = c + 1 < cols ? __ldg(src + j * part.src_stride + 1) : 0;
             v[j] = lo | hi << 16;
           }
-      }
-      uint16_t *dst = part.dst + r0 * part.dst_stride + c;
 #pragma unroll
-      for (int j = 0; j < kPackRows; ++j)
-        if (j < rows) *reinterpret_cast<uint32_t *>(dst + j * part.dst_stride) = v[j];
+        for (int j = 0; j < kPackRows; ++j)
+          if (j < rows) *reinterpret_cast<uint32_t *>(dst + j * part.dst_stride) = v[j];
+      }
     }
   }
 }
@@ -247,14 +275,13 @@ cudaError_t launch_act_grad(ActGradParams p, cudaStream_t stream) {
   else
     e = wide ? launch_typed<8, __nv_bfloat16>(p, grid, stream) : launch_typed<1, __nv_bfloat16>(p, grid, stream);
   if (e != cudaSuccess || !p.dbias || p.slabs == 1) return e;
-  return launch(join_slabs_kernel, (p.N + 255) / 256, 256, 0, stream, 1, p);
+  return launch(join_slabs_kernel, (p.N + 31) / 32, 32 * kJoinWarps, 0, stream, 1, p);
 }
 
-cudaError_t launch_pack(PackParams p, cudaStream_t stream) {
+cudaError_t launch_pack(const PackParams &p, cudaStream_t stream) {
   int64_t blocks = 1;
   for (int i = 0; i < p.count; ++i) {
-    Packed &part = p.part[i];
-    part.even = (uintptr_t)part.src % 4 == 0 && part.src_stride % 2 == 0;
+    const Packed &part = p.part[i];
     const int64_t warps = (part.rows + kPackRows - 1) / kPackRows * (((part.cols + 7) / 8 * 4 + 31) / 32);
     if ((warps + 7) / 8 > blocks) blocks = (warps + 7) / 8;
   }

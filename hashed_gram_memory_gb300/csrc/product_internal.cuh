@@ -54,13 +54,12 @@ struct Packed {
   const uint16_t *src;
   uint16_t *dst;
   int64_t src_stride, dst_stride, rows, cols;
-  bool even;  // set by launch_pack
 };
 struct PackParams {
   Packed part[2];
   int32_t count;
 };
-cudaError_t launch_pack(PackParams p, cudaStream_t stream);
+cudaError_t launch_pack(const PackParams &p, cudaStream_t stream);
 
 // dz = dy * act'(pre), rounded to bf16, and its column sums before the rounding.
 struct ActGradParams {
