@@ -18,7 +18,7 @@
 //     those leave SMs idle (a few rows of a: reading b is the work), 2 to 8 CTAs of a cluster share a
 //     tile, each with a part of K, and add their parts through distributed shared memory in rank
 //     order, two such CTAs an SM.
-// 65,536 x 4096 x 6144 takes 2035 us in pairs, 1.62 PFLOP/s (the power limit's, as the library's);
+// 65,536 x 4096 x 6144 takes 1947 us in pairs, 1.69 PFLOP/s (the power limit's, as the library's);
 // 37 x 4096 x 6144 13.5 us, K shared by 8: 50 MB, 7.5 us at the measured bandwidth, behind the launch,
 // the first bytes and the joining.
 // Warps: 0, 2 and 3 TMA producers (a ring of stages of 64 of K, 128-byte swizzle); 1 allocates TMEM,
