@@ -111,7 +111,9 @@ struct Job {
 struct Jobs {
   Job job[2];
   int32_t count, stages, splits;
-  uint32_t stage_bytes;
+  // warp_bytes: buffers of an epilogue warp, the larger of both jobs'.  A warp keeps its own from one
+  // job to the next: nothing orders it against the others there, whose copies may be on their way.
+  uint32_t stage_bytes, warp_bytes;
 };
 
 // Shared-memory descriptor of an operand tile, 128-byte swizzle.  K-major: rows of 64 of K,
@@ -967,7 +969,7 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : 
       if constexpr (!SPLIT) {
         if (SYMMETRIC || p.rows) {
           const int units = qt / kUnit, u0 = units * part / kPartsHere, u1 = units * (part + 1) / kPartsHere;
-          w.buffers = smem_u32(sm) + stages * stage_bytes + (warp - 4) * (p.ahead * p.ahead_bytes + p.slots * p.slot_bytes);
+          w.buffers = smem_u32(sm) + stages * stage_bytes + (warp - 4) * jobs.warp_bytes;
           if constexpr (SEGMENTS)
             ok = move_tiles_of_segments<PAIR>(job, start, w, u0, u1, release);
           else
@@ -1405,11 +1407,12 @@ cudaError_t job_of(const ProductParams &p, const Facts &f, const Plan &plan, int
   return ok ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Launches the jobs of plans of one form.
+// Launches the jobs of plans of one form; buffers: the most that one of them has for its epilogue.
 cudaError_t launch_jobs(Jobs &jobs, const Plan &plan, int64_t buffers, int variant, const DeviceInfo &info,
                         cudaStream_t stream) {
   jobs.job[0].d.withhold = take_withheld_launch();
   jobs.splits = plan.splits;
+  jobs.warp_bytes = (uint32_t)(buffers / (4 * (plan.form == kPair ? kPairParts : kParts)));
   int64_t tiles = 0;
   for (int i = 0; i < jobs.count; ++i) {
     const uint32_t bytes = kPBytes + jobs.job[i].d.q_rows * 128;
