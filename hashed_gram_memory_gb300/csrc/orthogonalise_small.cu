@@ -49,7 +49,7 @@ struct SmallDev {
   int32_t r, w, blocks, cluster, steps;  // the sides; 64-column blocks a CTA
   float beta, eps, scale, a, b, c;
   bool tall, nesterov, wide_out;  // wide_out: rows of out on 16 bytes
-  bool withhold;  // test hook: the first wait is for an arrival that never comes
+  bool withhold;  // test hook: a cluster's first CTA waits for an arrival that never comes
 };
 
 constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;  // groups of 8 rows, version 1, SWIZZLE_128B
@@ -153,9 +153,9 @@ __device__ __forceinline__ void over_elements(const SmallDev &p, int64_t z, int 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1) orthogonalise_small_kernel(const __grid_constant__ SmallDev p) {
   extern __shared__ uint8_t sm_raw[];
-  __shared__ uint64_t done;  // the instructions issued have completed
+  __shared__ uint64_t done, drained;  // the instructions issued have completed
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_flag;
+  __shared__ int abort_flag, gave_up;
   __shared__ float warp_sums[kWarps], cta_sum;
   uint8_t *sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
   const uint32_t X = smem_u32(sm), A = X + p.blocks * kBlock, B = A + kSquare, part = B;
@@ -167,7 +167,8 @@ __global__ void __launch_bounds__(kThreads, 1) orthogonalise_small_kernel(const 
   const int col0 = rank * p.blocks * 64, columns = max(0, min(p.blocks * 64, p.w - col0));
 
   if (threadIdx.x == 0) {
-    mbar_init(&done, p.withhold ? 2 : 1);
+    mbar_init(&done, p.withhold && rank == 0 ? 2 : 1);
+    mbar_init(&drained, 1);
     abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -218,21 +219,24 @@ __global__ void __launch_bounds__(kThreads, 1) orthogonalise_small_kernel(const 
   });
 
   uint32_t phase = 0;
+  // The same in every lane of a warp, and after run's barrier in every warp.  Once it is false a CTA
+  // issues nothing more and touches neither its matrices nor tensor memory, which instructions may
+  // still be reading and writing; it only meets the others of its cluster.
   bool ok = true;
   // What the generic proxy has written is there for the tensor cores; then one thread issues.
   const auto run = [&](auto issue) {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-    __syncthreads();
+    ok = __syncthreads_and(ok);
+    if (!ok) return;
     if (threadIdx.x == 0) {
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       issue();
       umma_commit(&done);
     }
-    // Every thread goes on, whether the wait ends or gives up: the CTAs of a cluster meet again.
-    ok &= wait_phase(&done, phase, &abort_flag, p.wait_limit_ns, p.status);
-    phase ^= 1;
     __syncwarp();
+    ok = __all_sync(0xffffffffu, wait_phase(&done, phase, &abort_flag, p.wait_limit_ns, p.status));
+    phase ^= 1;
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   };
   const int c0 = share * 32;  // of 128 columns of A and B
@@ -247,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) orthogonalise_small_kernel(const 
         for (int i = 0; i < 4; ++i)
           umma(tmem, x + k * (kBlock >> 4) + 2 * i, x + k * (kBlock >> 4) + 2 * i, idesc, k + i > 0);
     });
-    {
+    if (ok) {
       uint32_t v[16];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -275,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) orthogonalise_small_kernel(const 
       cluster_sync();
       // A share of the rows each, added in rank order and written to all.
       const int rows = kR / p.cluster, r0 = rank * rows;
-      for (int i = threadIdx.x; i < rows * 32; i += kThreads) {
+      for (int i = threadIdx.x; ok && i < rows * 32; i += kThreads) {
         const int r = r0 + (i >> 5), c = (i & 31) * 4;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         float4 v[8];
@@ -302,6 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) orthogonalise_small_kernel(const 
     });
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      if (!ok) break;
       uint32_t v[16];
       __syncwarp();
       tmem_ld16(quad_tmem + kR + c0 + 16 * h, v);
@@ -333,7 +338,16 @@ __global__ void __launch_bounds__(kThreads, 1) orthogonalise_small_kernel(const 
       }
     });
     const bool last = step == p.steps - 1;
-    for (int c = share * 16; c < p.blocks * 64; c += kWarps / 4 * 16) {
+    if (last) {  // out is written by all of a matrix's CTAs or by none
+      ok = __syncthreads_and(ok);
+      if (p.cluster > 1) {
+        if (threadIdx.x == 0) gave_up = !ok;
+        cluster_sync();
+        const uint32_t flag = smem_u32(&gave_up);
+        ok = !__any_sync(0xffffffffu, lane < p.cluster && load_cluster(map_to_rank(flag, lane)) != 0);
+      }
+    }
+    for (int c = share * 16; ok && c < p.blocks * 64; c += kWarps / 4 * 16) {
       uint32_t v[16];
       __syncwarp();
       tmem_ld16(quad_tmem + c, v);
@@ -359,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) orthogonalise_small_kernel(const 
                               halves(x[8 * q + 4], x[8 * q + 5]), halves(x[8 * q + 6], x[8 * q + 7])));
         }
       }
-      if (last && p.tall && ok && row < p.r)  // a warp's lanes are neighbours in memory
+      if (last && p.tall && row < p.r)  // a warp's lanes are neighbours in memory
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           if (c + i < columns) from_float(out[(col0 + c + i) * p.out.stride + row], x[i] * (p.scale / kHeld));
@@ -398,6 +412,11 @@ __global__ void __launch_bounds__(kThreads, 1) orthogonalise_small_kernel(const 
   }
 
   // ---- teardown
+  // After a wait that gave up: the instructions issued end before the memory that they use goes.
+  if (threadIdx.x == 0 && abort_flag) {
+    umma_commit(&drained);
+    drain_phase(&drained, 0, p.wait_limit_ns);
+  }
   __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   together();  // no CTA leaves while another may still read or write its memory
