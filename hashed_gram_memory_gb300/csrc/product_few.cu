@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kRows = 16;  // of b a block
 constexpr int kWarps = 8;  // of a block at most
+constexpr int kSegment = 48;  // steps that the instructions' sums run on: 768 values in each
 
 struct FewDev {
   const uint16_t *a, *b;
@@ -74,7 +75,8 @@ struct Ring {
   static constexpr uint32_t kStep = (2 + EIGHTS) * 512, kBytes = kDeep * kStep;  // of a warp
 };
 
-template <int EIGHTS>
+// SEGMENTS: the instructions' sums are added up in fp32 registers every kSegment steps.
+template <int EIGHTS, bool SEGMENTS>
 __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(const __grid_constant__ FewDev p) {
   using R = Ring<EIGHTS>;
   constexpr int kColumns = 8 * EIGHTS;
@@ -109,6 +111,8 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(const __grid_cons
   for (int e = 0; e < EIGHTS; ++e)
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[e][i / 4][i % 4] = 0.f;
+  [[maybe_unused]] float total[EIGHTS][4] = {};
+  [[maybe_unused]] int left = kSegment;
   for (int i = 0; i < R::kDeep - 1; ++i) copy(i);
   for (int i = 0; i < steps; ++i) {
     asm volatile("cp.async.wait_group %0;" ::"n"(R::kDeep - 2) : "memory");
@@ -123,13 +127,30 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(const __grid_cons
       mma(acc[e][0], w0.x, w1.x, w0.y, w1.y, v[e].x, v[e].y);
       mma(acc[e][1], w0.z, w1.z, w0.w, w1.w, v[e].z, v[e].w);
     }
+    if constexpr (SEGMENTS) {
+      if (--left == 0) {
+        left = kSegment;
+#pragma unroll
+        for (int e = 0; e < EIGHTS; ++e)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            total[e][j] += acc[e][0][j] + acc[e][1][j];
+            acc[e][0][j] = acc[e][1][j] = 0.f;
+          }
+      }
+    }
   }
 #pragma unroll
   for (int e = 0; e < EIGHTS; ++e) {
-    sums[warp][g][e * 8 + 2 * t] = acc[e][0][0] + acc[e][1][0];
-    sums[warp][g][e * 8 + 2 * t + 1] = acc[e][0][1] + acc[e][1][1];
-    sums[warp][g + 8][e * 8 + 2 * t] = acc[e][0][2] + acc[e][1][2];
-    sums[warp][g + 8][e * 8 + 2 * t + 1] = acc[e][0][3] + acc[e][1][3];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      acc[e][0][j] += acc[e][1][j];
+      if constexpr (SEGMENTS) acc[e][0][j] += total[e][j];
+    }
+    sums[warp][g][e * 8 + 2 * t] = acc[e][0][0];
+    sums[warp][g][e * 8 + 2 * t + 1] = acc[e][0][1];
+    sums[warp][g + 8][e * 8 + 2 * t] = acc[e][0][2];
+    sums[warp][g + 8][e * 8 + 2 * t + 1] = acc[e][0][3];
   }
   __syncthreads();
   for (int i = threadIdx.x; i < kRows * kColumns; i += warps * 32) {
@@ -148,7 +169,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(const __grid_cons
 }
 
 // More than 48 KB of shared memory have to be allowed, once a device.
-template <int EIGHTS>
+template <int EIGHTS, bool SEGMENTS>
 cudaError_t launch_eights(const FewDev &d, int64_t grid, cudaStream_t stream) {
   static std::atomic<uint64_t> configured{0};
   int dev = 0;
@@ -156,12 +177,12 @@ cudaError_t launch_eights(const FewDev &d, int64_t grid, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(configured.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(few_rows_kernel<EIGHTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(few_rows_kernel<EIGHTS, SEGMENTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kWarps * Ring<EIGHTS>::kBytes);
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_release);
   }
-  return launch(few_rows_kernel<EIGHTS>, grid, d.warps * 32, d.warps * Ring<EIGHTS>::kBytes, stream, 1, d);
+  return launch(few_rows_kernel<EIGHTS, SEGMENTS>, grid, d.warps * 32, d.warps * Ring<EIGHTS>::kBytes, stream, 1, d);
 }
 
 }  // namespace
@@ -195,7 +216,12 @@ cudaError_t launch_few_rows(const ProductParams &p, cudaStream_t stream) {
   // Four steps of K a warp at least, where there are that many.
   d.warps = 1;
   while (d.warps < kWarps && d.warps * 128 < p.K) d.warps *= 2;
-  return p.M <= 8 ? launch_eights<1>(d, grid, stream) : launch_eights<2>(d, grid, stream);
+  // Where outputs have the bits to show it and K is that long.  In segments 1 x 4096 x 6144 would take
+  // 12.2 us, not 12.0, and 16 x 2048 x 4096 6.6, not 6.2.
+  const bool segments = (p.out.type == ENGRAM_DTYPE_F32 || (p.pre.p && p.pre.type == ENGRAM_DTYPE_F32)) &&
+                        p.K > (int64_t)d.warps * 2 * kSegment * 16;
+  if (p.M <= 8) return segments ? launch_eights<1, true>(d, grid, stream) : launch_eights<1, false>(d, grid, stream);
+  return segments ? launch_eights<2, true>(d, grid, stream) : launch_eights<2, false>(d, grid, stream);
 }
 
 }  // namespace engram
