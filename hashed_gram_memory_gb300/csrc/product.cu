@@ -51,6 +51,7 @@ constexpr int kP = 128;         // rows of the P operand a CTA stages
 constexpr int kBK = 64;         // of K a stage: 128 bytes
 constexpr int kQMax = 128;      // most rows of the Q operand a tile of one CTA
 constexpr int kPairQMax = 256;  // and of a pair
+constexpr int kApartQMax = 64;  // and of CTAs that share K and have more than two accumulators
 // Epilogue warps: one of each quarter of the lanes for each part of a tile's columns.
 constexpr int kParts = 4, kPairParts = 4;
 constexpr int kThreads = 128 * (1 + kParts), kPairThreads = 128 * (1 + kPairParts);
@@ -86,7 +87,7 @@ struct ProductDev {
   float scale, residual_scale;
   int32_t act;
   int32_t kblocks, q_tile, q_rows, stages;  // q_rows: rows of Q that a CTA stages
-  int32_t segments, seg_blocks;
+  int32_t segments, seg_blocks;  // of a split product: the accumulators that a CTA's part of K goes into
   int32_t tiles_p, tiles_q, tiles, matrix_tiles;
   // tiles of a group of out's columns; how many columns of tiles it has, and the last one
   int32_t group_columns, group_tiles, last_columns;
@@ -759,9 +760,10 @@ template <bool PAIR, bool SPLIT, int VARIANT>
 __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : kThreads, SPLIT ? 2 : 1)
     product_kernel(const __grid_constant__ Jobs jobs) {
   constexpr bool SYMMETRIC = VARIANT == kSymmetric, SEGMENTS = VARIANT == kSegments;
-  static_assert(!(PAIR && SPLIT) && !(SPLIT && VARIANT != kPlain));
+  static_assert(!(PAIR && SPLIT) && !(SPLIT && SYMMETRIC));
+  constexpr bool kApart = SPLIT && SEGMENTS;  // more accumulators than two for a part of K
   constexpr uint32_t kCols = SPLIT ? kSplitTmemCols : kTmemCols;
-  [[maybe_unused]] constexpr int kAccCols = PAIR ? kPairQMax : kQMax;
+  [[maybe_unused]] constexpr int kAccCols = PAIR ? kPairQMax : SPLIT && SEGMENTS ? kApartQMax : kQMax;
   constexpr int kTileP = PAIR ? 2 * kP : kP;
   constexpr int kPartsHere = PAIR ? kPairParts : SPLIT ? kSplitParts : kParts;
   constexpr int kThreadsHere = 128 * (1 + kPartsHere);
@@ -910,12 +912,14 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : 
         const uint32_t p_step = desc_step(p.p_t), q_step = desc_step(p.q_t), idesc = p.idesc;
         const uint32_t p_first = desc_low(smem_u32(sm), p.p_t), q_first = desc_low(smem_u32(sm) + kPBytes, p.q_t);
         for (Walk walk(p, worker, workers); ok && walk.tile < p.tiles; walk.next()) {
-          // A part of K shared by CTAs goes half into each accumulator.
-          const int seg_blocks = SPLIT ? (kblocks + 1) / 2 : p.seg_blocks;
+          // A part of K shared by CTAs goes half into each accumulator, or evenly into several of 64
+          // columns that are used once.
+          const int seg_blocks = kApart ? (kblocks + p.segments - 1) / p.segments
+                                 : SPLIT ? (kblocks + 1) / 2 : p.seg_blocks;
           for (int kb0 = 0; ok && kb0 < kblocks; kb0 += seg_blocks, ++unit) {
             const int kb1 = min(kb0 + seg_blocks, kblocks);
-            const uint32_t acc = unit & 1, use = unit >> 1;
-            if (!(ok = wait_phase(acc_empty + acc, (use & 1) ^ 1, abort_flag, limit, p.status))) break;
+            const uint32_t acc = kApart ? unit : unit & 1, use = unit >> 1;
+            if (!kApart && !(ok = wait_phase(acc_empty + acc, (use & 1) ^ 1, abort_flag, limit, p.status))) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t d = tmem + acc * kAccCols;
             for (int kb = kb0; kb < kb1; ++kb) {
@@ -928,7 +932,7 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : 
               commit<PAIR>(empty + s);
               if (++s == stages) s = 0, ph ^= 1;
             }
-            if (ok) commit<PAIR>(acc_full + acc);
+            if (ok && (!kApart || kb1 == kblocks)) commit<PAIR>(acc_full + (kApart ? 0 : acc));
           }
         }
       };
@@ -982,7 +986,7 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : 
         const int c0 = qt / 16 * part / kPartsHere, chunks = qt / 16 * (part + 1) / kPartsHere - c0;
         if constexpr (SPLIT) {
           // The partial tile into shared memory (the stages: every MMA has read them).
-          const bool two = blocks(p) > 1;
+          const bool two = !kApart && blocks(p) > 1;
           if (p.residual.p) {  // what is added in the end comes to L2 meanwhile: 0.7 us less
             const Tile t = tile_at<kTileP, SYMMETRIC>(p, worker);
             const int q_begin = qt * rank / splits, rows = qt * (rank + 1) / splits - q_begin;
@@ -999,7 +1003,16 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : 
           for (int c = 0; c < chunks; ++c) {
             uint32_t v[16], u[16];
             tmem_ld16(w.tmem + (c0 + c) * 16, v);
-            if (two) tmem_ld16(w.tmem + kAccCols + (c0 + c) * 16, u);
+            if constexpr (kApart) {
+              const int each = (blocks(p) + p.segments - 1) / p.segments;
+              for (int k = 1; k * each < blocks(p); ++k) {
+                tmem_ld16(w.tmem + k * kAccCols + (c0 + c) * 16, u);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(u[i]));
+              }
+            } else if (two) {
+              tmem_ld16(w.tmem + kAccCols + (c0 + c) * 16, u);
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               mine[(c * 16 + i) * kP] = __uint_as_float(v[i]) + (two ? __uint_as_float(u[i]) : 0.f);
@@ -1120,7 +1133,7 @@ Kernel kernel_of(int form, int variant) {
   static constexpr Kernel all[kForms][3] = {
       {product_kernel<false, false, kPlain>, product_kernel<false, false, kSegments>,
        product_kernel<false, false, kSymmetric>},
-      {product_kernel<false, true, kPlain>, nullptr, nullptr},
+      {product_kernel<false, true, kPlain>, product_kernel<false, true, kSegments>, nullptr},
       {product_kernel<true, false, kPlain>, product_kernel<true, false, kSegments>,
        product_kernel<true, false, kSymmetric>}};
   return all[form][variant];
@@ -1281,6 +1294,12 @@ Plan plan_form(const ProductParams &p, const Facts &f, int form, bool rows, cons
   return best;
 }
 
+// Accumulators of a CTA where n share K: two, or where K goes in segments one for each of its own.
+int split_segments(const Facts &f, int n) {
+  const int64_t own = ceil_div(ceil_div(f.d.kblocks, n), kSegmentBlocks);
+  return f.d.segments > 1 && own > 2 ? (int)own : 2;
+}
+
 // K shared by 2 to 8 CTAs, two an SM: what a CTA takes of K, and the joining, by the rounds that its
 // warps need for their share of the tile.  Only as many clusters as run at once: 36 of 8 take 11.8 us
 // of 37 x 4608 x 4096, 37 of them 17.1 of 37 x 4736 x 4096.
@@ -1293,7 +1312,9 @@ Plan plan_split(const ProductParams &p, const Facts &f, const DeviceInfo &info) 
     const int64_t tiles = p.count * tiles_of(p.N, p.M, kP, width, p.symmetric);
     for (int n = 2; n <= 8; ++n) {
       if (tiles > info.clusters[n] || kb < n) continue;
-      // A part is two segments: of fp32 outputs not much longer than the others'.
+      // Of fp32 outputs the accumulators of a part have to fit, and parts are not much longer than the
+      // others' segments.
+      if (split_segments(f, n) > (width <= kApartQMax ? (int)kSplitTmemCols / kApartQMax : 2)) continue;
       if (f.d.segments > 1 && ceil_div(f.d.kblocks, n) > (n == 2 ? 24 : 32)) continue;
       Plan s;
       s.form = kSplit;
@@ -1367,10 +1388,7 @@ cudaError_t job_of(const ProductParams &p, const Facts &f, const Plan &plan, int
     while (d.ahead && d.ahead < kMaxAhead && bytes(d.ahead + 1, d.slots) <= most) ++d.ahead;
     buffers = bytes(d.ahead, d.slots);
   }
-  if (plan.form == kSplit) {  // a CTA's part of K is one segment
-    d.segments = 1;
-    d.seg_blocks = d.kblocks;
-  }
+  if (plan.form == kSplit) d.segments = split_segments(f, plan.splits);
   const int width = plan.form == kPair ? 2 * kP : kP;
   const int64_t matrix_tiles = tiles_of(P, Q, width, plan.q_tile, p.symmetric), tiles = matrix_tiles * p.count;
   if (tiles > INT32_MAX / 16) return cudaErrorInvalidConfiguration;  // group_tiles stay in 31 bits too
@@ -1423,7 +1441,8 @@ cudaError_t launch_jobs(Jobs &jobs, const Plan &plan, int64_t buffers, int varia
                           jobs.stage_bytes);
   if (jobs.stages > kMaxStages) jobs.stages = kMaxStages;
   if (jobs.stages < kProducers) return cudaErrorInvalidConfiguration;
-  const Kernel kernel = kernel_of(plan.form, plan.form == kSplit ? kPlain : variant);
+  if (plan.form == kSplit) variant = jobs.job[0].d.segments > 2 ? kSegments : kPlain;
+  const Kernel kernel = kernel_of(plan.form, variant);
   if (plan.form == kPair)
     return launch(kernel, 2 * (tiles < info.pairs ? tiles : info.pairs), kPairThreads, kSmemBytes, stream, 2, jobs);
   if (plan.form == kSplit)

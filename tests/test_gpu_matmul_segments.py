@@ -26,13 +26,15 @@ def eg():
     return eg
 
 
-def missing(eg, M, N, K, at):
-    """What the sums lack at most; row m has its 1 at at + 8 m."""
+def missing(eg, M, N, K, at, values=None):
+    """What the sums lack at most; row m has its 1 at at + 8 m.  values: that many of t from the
+    beginning on, the rest zeros."""
     import torch
     a = torch.full((M, K), T, dtype=torch.bfloat16, device="cuda")
-    a[torch.arange(M, device="cuda"), (at + 8 * torch.arange(M, device="cuda")) % K] = 1.0
+    a[:, values or K:] = 0
+    a[torch.arange(M, device="cuda"), (at + 8 * torch.arange(M, device="cuda")) % (values or K)] = 1.0
     out = eg.engram_matmul(a, torch.ones(N, K, dtype=torch.bfloat16, device="cuda"))
-    return float((1 + (K - 1) * T - out.double()).abs().max()) / T
+    return float((1 + ((values or K) - 1) * T - out.double()).abs().max()) / T
 
 
 def bound(additions):
@@ -51,3 +53,11 @@ def test_few_rows(eg, M, N, K, at):
                                    (300, 1023, 40000), (1300, 1100, 30000), (4096, 4096, 20000), (4096, 4095, 20000)])
 def test_tiles(eg, M, N, K):
     assert missing(eg, M, N, K, 64) <= bound(-(-K // 768) + 16)
+
+
+@pytest.mark.parametrize("M,N,K", [(37, 4608, 16000), (20, 4608, 16384), (64, 4096, 15000), (100, 4096, 6144),
+                                   (100, 4096, 16384)])
+def test_shared_by_clusters(eg, M, N, K):
+    """1024 values of K, those that the first of 4 CTAs once put into one accumulator: two parts of
+    them at least, and only additions of those round."""
+    assert missing(eg, M, N, K, 0, values=1024) <= bound(2)
