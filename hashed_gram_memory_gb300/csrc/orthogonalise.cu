@@ -28,7 +28,7 @@ struct StartDev {
   Plane g, momentum;
   __half *x;
   int64_t x_stride, x_batch;
-  float *partial;  // [count][parts]: sums of squares
+  Squares *partial;  // [count][parts]
   int32_t M, N, parts, lanes;  // lanes: threads a row, a power of two
   float beta, eps;
   bool nesterov;
@@ -95,14 +95,14 @@ __device__ __forceinline__ void over_share(const StartDev &p, int64_t z, int par
   }
 }
 
-__device__ __forceinline__ float block_sum(float v) {
-  __shared__ float sums[kThreads / 32];
-  for (int i = 16; i > 0; i >>= 1) v += __shfl_xor_sync(0xffffffffu, v, i);
+__device__ __forceinline__ Squares block_sum(Squares v) {
+  __shared__ Squares sums[kThreads / 32];
+  for (int i = 16; i > 0; i >>= 1) v.add(v.across_lane(i));
   if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = 0.f;
+  v = Squares{};
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) v += sums[i];
+  for (int i = 0; i < kThreads / 32; ++i) v.add(sums[i]);
   return v;
 }
 
@@ -112,10 +112,10 @@ __global__ void __launch_bounds__(kThreads) momentum_kernel(const StartDev p) {
   dependency_wait();
   const int64_t z = blockIdx.x / p.parts;
   const int part = blockIdx.x - (int)z * p.parts;
-  float sum = 0.f;
+  Squares sum{};
   over_share<VEC, T, true>(p, z, part, [&](int64_t, int64_t, const float (&u)[VEC]) {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) sum = fmaf(u[i], u[i], sum);
+    for (int i = 0; i < VEC; ++i) sum.add(u[i]);
   });
   sum = block_sum(sum);
   if (threadIdx.x == 0) p.partial[blockIdx.x] = sum;
@@ -127,15 +127,17 @@ __global__ void __launch_bounds__(kThreads) normalise_kernel(const StartDev p) {
   dependency_wait();
   const int64_t z = blockIdx.x / p.parts;
   const int part = blockIdx.x - (int)z * p.parts;
-  float sum = 0.f;
-  for (int i = threadIdx.x; i < p.parts; i += kThreads) sum += p.partial[z * p.parts + i];
-  const float by = kHeld / (sqrtf(block_sum(sum)) + p.eps);
+  Squares sum{};
+  for (int i = threadIdx.x; i < p.parts; i += kThreads) sum.add(p.partial[z * p.parts + i]);
+  const Norm norm(block_sum(sum), p.eps, kHeld);
+  const auto normal = [&](float v) { return v * norm.first * norm.second; };
   over_share<VEC, T, false>(p, z, part, [&](int64_t m, int64_t n, const float (&u)[VEC]) {
     __half *at = p.x + z * p.x_batch + m * p.x_stride + n;
     if constexpr (VEC == 1) {
-      *at = __float2half_rn(u[0] * by);
+      *at = __float2half_rn(normal(u[0]));
     } else {
-      __half2 v[2] = {__floats2half2_rn(u[0] * by, u[1] * by), __floats2half2_rn(u[2] * by, u[3] * by)};
+      __half2 v[2] = {__floats2half2_rn(normal(u[0]), normal(u[1])),
+                      __floats2half2_rn(normal(u[2]), normal(u[3]))};
       *reinterpret_cast<uint2 *>(at) = make_uint2(*reinterpret_cast<uint32_t *>(v), *reinterpret_cast<uint32_t *>(v + 1));
     }
   });
@@ -168,7 +170,7 @@ Layout layout_of(int64_t M, int64_t N, int64_t count) {
   l.x[1] = take(l.x_batch * count * 2);
   l.a = take(l.a_batch * count * 2);
   l.b = take(l.a_batch * count * 2);
-  l.partial = take((size_t)kMostParts * count * sizeof(float));
+  l.partial = take((size_t)kMostParts * count * sizeof(Squares));
   l.bytes = at;
   return l;
 }
@@ -187,7 +189,7 @@ cudaError_t launch_orthogonalise(const OrthogonaliseParams &p, void *workspace, 
   s.x = reinterpret_cast<__half *>(ws + l.x[0]);
   s.x_stride = padded(p.N);
   s.x_batch = l.x_batch;
-  s.partial = reinterpret_cast<float *>(ws + l.partial);
+  s.partial = reinterpret_cast<Squares *>(ws + l.partial);
   s.M = (int32_t)p.M;
   s.N = (int32_t)p.N;
   s.beta = p.beta;

@@ -16,6 +16,8 @@
 //   1 of 128 x  128   22 and 67        16 of 128 x 1024    50 and  98
 //   1 of 128 x  512   45 and 73      1000 of 128 x  128   169 and 316
 //   1 of 100 x 3500   76 and 97       300 of 128 x  896   301 and 419
+#include <stddef.h>
+
 #include <mutex>
 
 #include "launch.cuh"
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) orthogonalise_small_kernel(const 
   __shared__ uint64_t done, drained;  // the instructions issued have completed
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag, gave_up;
-  __shared__ float warp_sums[kWarps], cta_sum;
+  __shared__ Squares warp_sums[kWarps], cta_sum;
   uint8_t *sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
   const uint32_t X = smem_u32(sm), A = X + p.blocks * kBlock, B = A + kSquare, part = B;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -194,25 +196,32 @@ __global__ void __launch_bounds__(kThreads, 1) orthogonalise_small_kernel(const 
   };
 
   // The momentum step, the norm, X.
-  float sum = 0.f;
-  over_elements<true, T>(p, z, col0, columns, [&](int, int, float u) { sum = fmaf(u, u, sum); });
-  for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+  Squares sum{};
+  over_elements<true, T>(p, z, col0, columns, [&](int, int, float u) { sum.add(u); });
+  for (int i = 16; i > 0; i >>= 1) sum.add(sum.across_lane(i));
   if (lane == 0) warp_sums[warp] = sum;
   __syncthreads();
   if (threadIdx.x == 0) {
-    float s = 0.f;
-    for (int i = 0; i < kWarps; ++i) s += warp_sums[i];
+    Squares s{};
+    for (int i = 0; i < kWarps; ++i) s.add(warp_sums[i]);
     cta_sum = s;
   }
   together();
-  sum = 0.f;
-  if (p.cluster > 1)
-    for (int r = 0; r < p.cluster; ++r) sum += __uint_as_float(load_cluster(map_to_rank(smem_u32(&cta_sum), r)));
-  else
-    sum = cta_sum;
-  const float by = kHeld / (sqrtf(sum) + p.eps);
+  sum = cta_sum;
+  if (p.cluster > 1) {
+    sum = Squares{};
+    for (int r = 0; r < p.cluster; ++r) {
+      const uint32_t from = map_to_rank(smem_u32(&cta_sum), r);
+      Squares s{};
+      s.plain = __uint_as_float(load_cluster(from + offsetof(Squares, plain)));
+      s.small = __uint_as_float(load_cluster(from + offsetof(Squares, small)));
+      s.large = __uint_as_float(load_cluster(from + offsetof(Squares, large)));
+      sum.add(s);
+    }
+  }
+  const Norm norm(sum, p.eps, kHeld);
   over_elements<false, T>(p, z, col0, columns, [&](int i, int j, float u) {
-    const __half v = __float2half_rn(u * by);
+    const __half v = __float2half_rn(u * norm.first * norm.second);
     asm volatile("st.shared.u16 [%0], %1;" ::"r"(at(X + (j >> 6) * kBlock, i, (j & 63) >> 3) + (j & 7) * 2),
                  "h"(__half_as_ushort(v))
                  : "memory");

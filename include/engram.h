@@ -782,9 +782,9 @@ ENGRAM_API engram_status engram_matmul_grad(const engram_matmul_grad_args *args,
  * fp32 momentum, norm and sums; the iterate and the square matrices are held in fp16 times
  * 2^8 between the products: the result is about 4e-3 off at most (of its Frobenius norm;
  * its own rounding to bf16 is 1.7e-3) with the usual coefficients 3.4445, -4.7750, 2.0315
- * and 5 steps.  Singular values over 255 on the way overflow.  The squares of the norm are
- * fp32: values of u under 1e-19 count as zero in it.  A matrix of zeros stays zero; a NaN or
- * an infinity makes its matrix NaN.  steps in [1, 64], coefficients in [-16, 16].  A wait
+ * and 5 steps.  Singular values over 255 on the way overflow.  The norm is that of finite u
+ * of any size.  A matrix of zeros stays zero, with eps == 0 too; a NaN or an infinity in u
+ * makes all of its matrix NaN.  steps in [1, 64], coefficients in [-16, 16].  A wait
  * that runs out sets ENGRAM_FLAG_TIMEOUT: then the outputs are not valid.  count == 0
  * launches nothing.
  */
