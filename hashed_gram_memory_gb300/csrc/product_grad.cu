@@ -46,7 +46,9 @@ __device__ __forceinline__ float through(float dy, float z, int act) {
     return dy * (s * (1.f + z * (1.f - s)));
   }
   // gelu: Phi(z) + z phi(z)
-  return dy * (0.5f * (1.f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z));
+  float bell;
+  const float below = normal_below(z, bell);
+  return dy * fmaf(z * 0.39894228f, bell, below);
 }
 
 // DEEP rows, `step` apart, of a thread's VEC columns: all loads, then the rest.

@@ -17,11 +17,31 @@ __device__ __forceinline__ void from_float(float &d, float v) { d = v; }
 __device__ __forceinline__ void from_float(__nv_bfloat16 &d, float v) { d = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void from_float(__half &d, float v) { d = __float2half_rn(v); }
 
+// The normal distribution function, with e^(-z^2/2) in `bell`: below zero e^(-w^2/2) G(w), w = -z,
+// above it one less that, so that far values keep their bits (1 + erf cancels: 10 % of the value off
+// at -5).  G(w) = e^(w^2/2) erfc(w / sqrt 2) / 2 is a polynomial in t = 1 / (1 + 0.31 w) times t, fitted
+// for the least relative error on [0, 15]: 1.7e-7, 4.4e-7 with fp32's roundings.
+__device__ __forceinline__ float normal_below(float z, float &bell) {
+  bell = __expf(-0.5f * z * z);
+  const float t = __fdividef(1.f, fmaf(0.31f, fabsf(z), 1.f));
+  float g = fmaf(0.0358902439f, t, -0.141817674f);
+  g = fmaf(g, t, 0.155456692f);
+  g = fmaf(g, t, -0.0152842198f);
+  g = fmaf(g, t, 0.110325493f);
+  g = fmaf(g, t, 0.107701071f);
+  g = fmaf(g, t, 0.12407241f);
+  g = fmaf(g, t, 0.123656064f) * t * bell;
+  return z < 0.f ? g : 1.f - g;
+}
+
 // ENGRAM_ACT_* of one value.
 __device__ __forceinline__ float activated(float z, int act) {
   if (act == ENGRAM_ACT_RELU) return z < 0.f ? 0.f : z;  // a NaN stays
   if (act == ENGRAM_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
-  if (act == ENGRAM_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678f));
+  if (act == ENGRAM_ACT_GELU) {
+    float bell;
+    return z * normal_below(z, bell);
+  }
   return z;
 }
 
