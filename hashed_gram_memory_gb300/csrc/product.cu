@@ -87,6 +87,9 @@ struct ProductDev {
   float scale, residual_scale;
   int32_t act;
   int32_t kblocks, q_tile, q_rows, stages;  // q_rows: rows of Q that a CTA stages
+  // Blocks of K of one matrix.  Where an operand is the sum of two, K goes on from the first to the
+  // second (p_next, q_next: 1), and begins anew in the other.
+  int32_t pass_blocks, p_next, q_next;
   int32_t segments, seg_blocks;  // of a split product: the accumulators that a CTA's part of K goes into
   int32_t tiles_p, tiles_q, tiles, matrix_tiles;
   // tiles of a group of out's columns; how many columns of tiles it has, and the last one
@@ -860,26 +863,29 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : 
         const int kb_first = first_block(p), kblocks = blocks(p), q_rows = p.q_rows;
         const uint32_t bytes = (PAIR ? 2 : 1) * (kPBytes + (uint32_t)q_rows * 128);
         const bool p_t = p.p_t, q_t = p.q_t;
+        const int pass = kb_first >= p.pass_blocks, k_end = p.pass_blocks * kBK;
         for (Walk walk(p, worker, workers); ok && walk.tile < p.tiles; walk.next()) {
           Tile at = tile_at<kTileP, SYMMETRIC>(p, walk.tile);
           if constexpr (PAIR) at.p0 += rank * kP, at.q0 += rank * (p.q_tile / 2);
-          int k = kb_first * kBK;
+          int k = (kb_first - pass * p.pass_blocks) * kBK;
+          int pz = at.z + pass * p.p_next, qz = at.z + pass * p.q_next;
           for (int kb = 0; kb < kblocks; ++kb, ++it, k += kBK) {
+            if (k == k_end) k = 0, pz += p.p_next, qz += p.q_next;
             if (turn == 0) {
               if (!(ok = wait_phase(empty + s, ph ^ 1, abort_flag, limit, p.status))) break;
               const uint32_t st = smem_u32(sm) + s * stage_bytes, bar = full_at + 8u * s;
               if (rank == 0 || !PAIR) mbar_arrive_expect_tx(full + s, bytes);
               if (p_t) {
-                tma_load_3d<PAIR>(st, &job.p, at.p0, k, at.z, bar);
-                tma_load_3d<PAIR>(st + 64 * 128, &job.p, at.p0 + 64, k, at.z, bar);
+                tma_load_3d<PAIR>(st, &job.p, at.p0, k, pz, bar);
+                tma_load_3d<PAIR>(st + 64 * 128, &job.p, at.p0 + 64, k, pz, bar);
               } else {
-                tma_load_3d<PAIR>(st, &job.p, k, at.p0, at.z, bar);
+                tma_load_3d<PAIR>(st, &job.p, k, at.p0, pz, bar);
               }
               if (q_t) {
-                tma_load_3d<PAIR>(st + kPBytes, &job.q, at.q0, k, at.z, bar);
-                if (q_rows > 64) tma_load_3d<PAIR>(st + kPBytes + 64 * 128, &job.q, at.q0 + 64, k, at.z, bar);
+                tma_load_3d<PAIR>(st + kPBytes, &job.q, at.q0, k, qz, bar);
+                if (q_rows > 64) tma_load_3d<PAIR>(st + kPBytes + 64 * 128, &job.q, at.q0 + 64, k, qz, bar);
               } else {
-                tma_load_3d<PAIR>(st + kPBytes, &job.q, k, at.q0, at.z, bar);
+                tma_load_3d<PAIR>(st + kPBytes, &job.q, k, at.q0, qz, bar);
               }
               turn = kProducers;
             }
@@ -1232,7 +1238,8 @@ Facts facts_of(const ProductParams &p) {
   d.M = (int32_t)p.M;
   d.N = (int32_t)p.N;
   d.many = p.count > 1;
-  d.kblocks = (int32_t)ceil_div(p.K, kBK);
+  d.pass_blocks = (int32_t)ceil_div(p.K, kBK);
+  d.kblocks = p.a_two ? 2 * d.pass_blocks : d.pass_blocks;
   // Segments only where the output has the bits to show them.
   d.segments = 1;
   d.seg_blocks = d.kblocks;
@@ -1258,7 +1265,7 @@ Facts facts_of(const ProductParams &p) {
 // the two counts once, where nothing hides it.  No form reads the operands faster than memory gives
 // them.
 double read_us(const ProductParams &p, double of_b = 1) {
-  return p.count * ((p.symmetric ? 0 : p.M) + of_b * p.N) * p.K * 2 / 6.5e6;
+  return p.count * ((p.symmetric ? 0 : p.a_two ? 2 * p.M : p.M) + of_b * p.N) * p.K * 2 / 6.5e6;
 }
 
 // The best tile width of a form without splits.
@@ -1365,6 +1372,8 @@ cudaError_t job_of(const ProductParams &p, const Facts &f, const Plan &plan, int
   ProductDev &d = job.d;
   d = f.d;
   d.rows = plan.rows;
+  d.p_next = p.a_two && plan.rows;
+  d.q_next = p.a_two && !plan.rows;
   d.p_t = op.t;
   d.q_t = oq.t;
   d.q_tile = plan.q_tile;
@@ -1417,8 +1426,8 @@ cudaError_t job_of(const ProductParams &p, const Facts &f, const Plan &plan, int
   // kind::f16: fp32 accumulator, the operands' type (0: f16, 1: bf16), which of them are MN-major.
   d.idesc = 1u << 4 | (p.f16 ? 0u : 1u << 7 | 1u << 10) | (uint32_t)d.p_t << 15 | (uint32_t)d.q_t << 16 |
             (uint32_t)(plan.q_tile >> 3) << 17 | (uint32_t)(width >> 4) << 24;
-  const bool ok = make_map(&job.p, op, P, p.K, p.count, kP) &&
-                  make_map(&job.q, oq, Q, p.K, p.count, (uint32_t)q_staged) &&
+  const bool ok = make_map(&job.p, op, P, p.K, p.count + d.p_next, kP) &&
+                  make_map(&job.q, oq, Q, p.K, p.count + d.q_next, (uint32_t)q_staged) &&
                   (!plan.rows || (make_plane_map(&job.out, d.out, p.M, p.N, p.count) &&
                                   (!d.pre.p || make_plane_map(&job.pre, d.pre, p.M, p.N, p.count)) &&
                                   (!d.residual.p || make_plane_map(&job.residual, d.residual, p.M, p.N, p.count))));

@@ -97,6 +97,11 @@ bool makes_dz(const Given &dy, int32_t dy_dtype, int32_t act) {
   return act != ENGRAM_ACT_NONE || dy_dtype != ENGRAM_DTYPE_BF16 || !dy.direct() ||
          (dy.rows > 1 && dy.stride < dy.K);
 }
+// dz has to be two matrices: of fp32 outputs, where it is not bf16 to begin with.
+bool two_of_dz(const void *da, int32_t da_dtype, const void *db, int32_t db_dtype, int32_t dy_dtype, int32_t act) {
+  return ((da && da_dtype == ENGRAM_DTYPE_F32) || (db && db_dtype == ENGRAM_DTYPE_F32)) &&
+         (act != ENGRAM_ACT_NONE || dy_dtype != ENGRAM_DTYPE_BF16);
+}
 int64_t dz_stride_of(int64_t N) { return N > 512 ? (N + 63) / 64 * 64 : (N + 7) / 8 * 8; }
 size_t dz_bytes(int64_t M, int64_t N) { return (size_t)(M * dz_stride_of(N) * 2 + 255) / 256 * 256; }
 
@@ -190,7 +195,8 @@ ENGRAM_API size_t engram_matmul_grad_workspace_bytes(const engram_matmul_grad_ar
   if (!sizes_ok(g.M, g.N, g.K) || g.M == 0) return 0;
   size_t bytes = 0;
   const Given gy{static_cast<const uint16_t *>(g.dy), g.dy_stride, false, g.M, g.N};
-  if ((g.da || g.db) && makes_dz(gy, g.dy_dtype, g.activation)) bytes += dz_bytes(g.M, g.N);
+  if ((g.da || g.db) && makes_dz(gy, g.dy_dtype, g.activation))
+    bytes += dz_bytes(g.M, g.N) << two_of_dz(g.da, g.da_dtype, g.db, g.db_dtype, g.dy_dtype, g.activation);
   if (g.dbias) bytes += (engram::act_grad_partial_bytes(g.M, g.N) + 255) / 256 * 256;
   if (g.db) bytes += Given{g.a, g.a_stride, g.a_trans != 0, g.M, g.K}.packed_bytes();
   if (g.da) bytes += Given{g.b, g.b_stride, g.b_trans != 0, g.N, g.K}.packed_bytes();
@@ -231,6 +237,8 @@ ENGRAM_API engram_status engram_matmul_grad(const engram_matmul_grad_args *args,
                      "%s: a or b NULL or misaligned, or its stride under a row's width or over 2^38", fn);
   Given gy{static_cast<const uint16_t *>(dy), dy_stride, false, M, N};
   const bool dz = (da || db) && M > 0 && makes_dz(gy, dy_dtype, activation);
+  const bool two = dz && two_of_dz(da, da_dtype, db, db_dtype, dy_dtype, activation);
+  const int64_t between = (int64_t)dz_bytes(M, N) / 2;  // elements from dz to what its rounding left
   const size_t need = engram_matmul_grad_workspace_bytes(args);
   if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
     return set_error(ENGRAM_ERR_INVALID_ARG, "%s: workspace NULL, not 16-byte aligned or under %zu bytes", fn, need);
@@ -275,6 +283,10 @@ ENGRAM_API engram_status engram_matmul_grad(const engram_matmul_grad_args *args,
       g.dz_stride = dz_stride_of(N);
       gy = Given{reinterpret_cast<uint16_t *>(scratch), g.dz_stride, false, M, N};
       scratch += dz_bytes(M, N);
+      if (two) {
+        g.dz_rest = scratch;
+        scratch += dz_bytes(M, N);
+      }
     }
     if (dbias) {
       g.partial = reinterpret_cast<float *>(scratch);
@@ -293,7 +305,8 @@ ENGRAM_API engram_status engram_matmul_grad(const engram_matmul_grad_args *args,
   pa.status = status;
   pb = pa;
   if (da) {  // rows of dz by the columns of b, over N
-    pa.a = Operand{gy.p, gy.stride, 0, false};
+    pa.a = Operand{gy.p, gy.stride, between, false};
+    pa.a_two = two && da_dtype == ENGRAM_DTYPE_F32;
     pa.b = Operand{ob.p, ob.stride, 0, !ob.t};
     pa.M = M;
     pa.N = K;
@@ -301,7 +314,8 @@ ENGRAM_API engram_status engram_matmul_grad(const engram_matmul_grad_args *args,
     pa.out = Plane{da, da_stride, 0, da_dtype};
   }
   if (db) {  // columns of dz by the columns of a, over M
-    pb.a = Operand{gy.p, gy.stride, 0, true};
+    pb.a = Operand{gy.p, gy.stride, between, true};
+    pb.a_two = two && db_dtype == ENGRAM_DTYPE_F32;
     pb.b = Operand{oa.p, oa.stride, 0, !oa.t};
     pb.M = N;
     pb.N = K;

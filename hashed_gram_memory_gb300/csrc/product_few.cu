@@ -191,7 +191,7 @@ bool few_rows_supported(const ProductParams &p) {
   // Every block reads all rows of a: from 9 rows on that costs more than it saves where b is large
   // (16 x 4096 x 4096 9.5 us and 9.0 by clusters, 16 x 2048 x 4096 5.8 and 6.5; 8 x 4096 x 6144 11.8 and
   // 12.7).
-  return (p.M <= 8 || (p.M <= 16 && p.N * p.K <= 12 << 20)) && p.count == 1 && !p.symmetric && !p.f16 && !p.a.t &&
+  return (p.M <= 8 || (p.M <= 16 && p.N * p.K <= 12 << 20)) && p.count == 1 && !p.symmetric && !p.f16 && !p.a_two && !p.a.t &&
          !p.b.t && p.out.type != kTypeF16;
 }
 

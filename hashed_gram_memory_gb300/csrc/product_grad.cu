@@ -3,8 +3,9 @@
 // start on 16 bytes.
 //
 // act_grad_kernel walks slabs of rows, 8 (or 1, where rows are not aligned) neighbouring columns
-// a thread: dz = dy act'(z) is stored as bf16, the operand of the products (rounded once, at most
-// 2^-9 of the value), and summed in fp32 before that rounding; a block adds its rows' sums in
+// a thread: dz = dy act'(z) is stored as bf16, the operand of the products (at most 2^-8 of the value
+// off), for fp32 outputs with a second matrix of what that rounding left (the two are at most 2^-16
+// off), and summed in fp32 before any rounding; a block adds its rows' sums in
 // order, of more than 1024 rows a second kernel the slabs', so the result does not depend on timing.
 // Bound by HBM: 16,411 x 2573 of fp32 dy and pre take 69 us, 6.1 TB/s, with 8 rows of single columns
 // ahead of a thread and 4 blocks an SM (4 rows and 5 blocks: 104).
@@ -51,10 +52,17 @@ __device__ __forceinline__ float through(float dy, float z, int act) {
   return dy * fmaf(z * 0.39894228f, bell, below);
 }
 
-// DEEP rows, `step` apart, of a thread's VEC columns: all loads, then the rest.
-template <int VEC, int DEEP, typename TY, typename TZ>
+// What a rounding left; nothing of a value that is not finite, or that only its rounding is not.
+__device__ __forceinline__ float left_over(float x, __nv_bfloat16 rounded) {
+  const float r = to_float(rounded);
+  return fabsf(r) < INFINITY ? x - r : 0.f;
+}
+
+// DEEP rows, `step` apart, of a thread's VEC columns: all loads, then the others.  REST: dz_rest is
+// written too, `rest` elements behind dz (asked at run time it took 512 x 4096 1.5 us longer).
+template <int VEC, int DEEP, bool REST, typename TY, typename TZ>
 __device__ __forceinline__ void some_rows(const ActGradParams &p, const TY *dy, const TZ *pre, __nv_bfloat16 *dz,
-                                          int64_t step, int count, float (&sum)[VEC]) {
+                                          int64_t rest, int64_t step, int count, float (&sum)[VEC]) {
   constexpr bool kAct = !std::is_same_v<TZ, void>;
   float x[DEEP][VEC], z[DEEP][VEC];
 #pragma unroll
@@ -77,15 +85,25 @@ __device__ __forceinline__ void some_rows(const ActGradParams &p, const TY *dy, 
 #pragma unroll
         for (int i = 0; i < 8; ++i) from_float(v[i], x[d][i]);
         *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(v);
+        if constexpr (REST) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) from_float(v[i], left_over(x[d][i], v[i]));
+          *reinterpret_cast<uint4 *>(to + rest) = *reinterpret_cast<const uint4 *>(v);
+        }
       } else {
         from_float(*to, x[d][0]);
+        if constexpr (REST) {
+          __nv_bfloat16 v;
+          from_float(v, x[d][0]);
+          from_float(to[rest], left_over(x[d][0], v));
+        }
       }
     }
   }
 }
 
 // A block has `lanes` threads a row, VEC columns each.  TZ void: no activation.
-template <int VEC, int THREADS, typename TY, typename TZ>
+template <int VEC, int THREADS, bool REST, typename TY, typename TZ>
 __global__ void __launch_bounds__(THREADS) act_grad_kernel(const ActGradParams p) {
   dependency_wait();
   __shared__ float sums[THREADS * VEC];
@@ -104,15 +122,16 @@ __global__ void __launch_bounds__(THREADS) act_grad_kernel(const ActGradParams p
     const TZ *pre = nullptr;
     if constexpr (!std::is_same_v<TZ, void>) pre = static_cast<const TZ *>(p.pre) + m * p.pre_stride + col;
     __nv_bfloat16 *dz = static_cast<__nv_bfloat16 *>(p.dz) + m * p.dz_stride + col;
+    const int64_t rest = REST ? static_cast<__nv_bfloat16 *>(p.dz_rest) - static_cast<__nv_bfloat16 *>(p.dz) : 0;
     const auto move = [&](int n) {
       dy += n * rows * p.dy_stride;
       if constexpr (!std::is_same_v<TZ, void>) pre += n * rows * p.pre_stride;
       dz += n * rows * p.dz_stride;
       left -= n;
     };
-    for (; left >= kDeep; move(kDeep)) some_rows<VEC, kDeep, TY, TZ>(p, dy, pre, dz, rows, count, sum);
+    for (; left >= kDeep; move(kDeep)) some_rows<VEC, kDeep, REST, TY, TZ>(p, dy, pre, dz, rest, rows, count, sum);
 #pragma unroll 1
-    for (; left > 0; move(1)) some_rows<VEC, 1, TY, TZ>(p, dy, pre, dz, rows, count, sum);
+    for (; left > 0; move(1)) some_rows<VEC, 1, REST, TY, TZ>(p, dy, pre, dz, rest, rows, count, sum);
   }
   if (!p.dbias) return;
   // sums[row][column of the block]
@@ -230,16 +249,27 @@ bool vectors(const void *p, int64_t stride, int type) {
   return !p || (((uintptr_t)p & 15) == 0 && stride % step == 0);
 }
 
-template <int VEC, typename TY, typename TZ>
+template <int VEC, bool REST, typename TY, typename TZ>
 cudaError_t launch_threads(const ActGradParams &p, int64_t grid, cudaStream_t stream) {
-  if (p.threads == kThreads) return launch(act_grad_kernel<VEC, kThreads, TY, TZ>, grid, kThreads, 0, stream, 1, p);
-  return launch(act_grad_kernel<VEC, kMostThreads, TY, TZ>, grid, kMostThreads, 0, stream, 1, p);
+  if (p.threads == kThreads)
+    return launch(act_grad_kernel<VEC, kThreads, REST, TY, TZ>, grid, kThreads, 0, stream, 1, p);
+  return launch(act_grad_kernel<VEC, kMostThreads, REST, TY, TZ>, grid, kMostThreads, 0, stream, 1, p);
+}
+template <int VEC, bool REST, typename TY>
+cudaError_t launch_typed(const ActGradParams &p, int64_t grid, cudaStream_t stream) {
+  if (!p.pre) {
+    // A bf16 dy by itself leaves nothing to a second matrix.
+    if constexpr (REST && std::is_same_v<TY, __nv_bfloat16>)
+      return cudaErrorInvalidValue;
+    else
+      return launch_threads<VEC, REST, TY, void>(p, grid, stream);
+  }
+  if (p.pre_type == ENGRAM_DTYPE_F32) return launch_threads<VEC, REST, TY, float>(p, grid, stream);
+  return launch_threads<VEC, REST, TY, __nv_bfloat16>(p, grid, stream);
 }
 template <int VEC, typename TY>
-cudaError_t launch_typed(const ActGradParams &p, int64_t grid, cudaStream_t stream) {
-  if (!p.pre) return launch_threads<VEC, TY, void>(p, grid, stream);
-  if (p.pre_type == ENGRAM_DTYPE_F32) return launch_threads<VEC, TY, float>(p, grid, stream);
-  return launch_threads<VEC, TY, __nv_bfloat16>(p, grid, stream);
+cudaError_t launch_rest(const ActGradParams &p, int64_t grid, cudaStream_t stream) {
+  return p.dz_rest ? launch_typed<VEC, true, TY>(p, grid, stream) : launch_typed<VEC, false, TY>(p, grid, stream);
 }
 
 }  // namespace
@@ -273,9 +303,9 @@ cudaError_t launch_act_grad(ActGradParams p, cudaStream_t stream) {
   const int64_t grid = (int64_t)p.col_blocks * p.slabs;
   cudaError_t e;
   if (p.dy_type == ENGRAM_DTYPE_F32)
-    e = wide ? launch_typed<8, float>(p, grid, stream) : launch_typed<1, float>(p, grid, stream);
+    e = wide ? launch_rest<8, float>(p, grid, stream) : launch_rest<1, float>(p, grid, stream);
   else
-    e = wide ? launch_typed<8, __nv_bfloat16>(p, grid, stream) : launch_typed<1, __nv_bfloat16>(p, grid, stream);
+    e = wide ? launch_rest<8, __nv_bfloat16>(p, grid, stream) : launch_rest<1, __nv_bfloat16>(p, grid, stream);
   if (e != cudaSuccess || !p.dbias || p.slabs == 1) return e;
   return launch(join_slabs_kernel, (p.N + 31) / 32, 32 * kJoinWarps, 0, stream, 1, p);
 }

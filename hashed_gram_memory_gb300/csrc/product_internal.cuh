@@ -29,6 +29,7 @@ struct Plane {
 struct ProductParams {
   Operand a, b;
   bool f16;  // operands: f16, else bf16
+  bool a_two;  // a is the sum of two matrices, a.batch elements apart (count is 1)
   int64_t M, N, K, count;
   float scale, residual_scale;
   Plane out, residual, pre;
@@ -61,10 +62,12 @@ struct PackParams {
 };
 cudaError_t launch_pack(const PackParams &p, cudaStream_t stream);
 
-// dz = dy * act'(pre), rounded to bf16, and its column sums before the rounding.
+// dz = dy * act'(pre), rounded to bf16, what that rounding left, rounded again, and dz's column sums
+// before any rounding.
 struct ActGradParams {
   const void *dy, *pre;  // pre NULL without an activation
   void *dz;              // bf16 [M, N], dz_stride a multiple of 8, or NULL
+  void *dz_rest;         // the same, or NULL
   float *dbias;          // [N] or NULL
   float *partial;        // act_grad_partial_bytes()
   int64_t M, N, dy_stride, pre_stride, dz_stride;

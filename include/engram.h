@@ -734,8 +734,10 @@ ENGRAM_API engram_status engram_matmul(const engram_matmul_args *args, void *wor
  * engram_matmul_grad -- the backward pass of engram_matmul for the output gradient dy (the
  * residual's gradient is dy itself):
  *   dz = dy act'(pre);  da = scale dz b;  db = scale dz^T a;  dbias = sum over m of dz
- * dz is rounded once to bf16 as the operand of the two products (nothing is rounded where dy
- * is bf16 and there is no activation) and summed for dbias before that, in fp32 in an order
+ * As the operand of the two products dz is rounded to bf16, once for a bf16 da or db; for an
+ * fp32 one what that rounding left is rounded to bf16 too and goes into the product beside it
+ * (2^-16 of a value off at most, and twice the operations).  Nothing is rounded where dy is
+ * bf16 and there is no activation.  For dbias dz is summed before that, in fp32 in an order
  * that M and N fix.
  *   dy    ENGRAM_DTYPE_* [M, N], dy_stride elements between rows (0: one row for all)
  *   a, b  as engram_matmul (a is read for db, b for da; the other may be NULL)
