@@ -975,6 +975,8 @@ def engram_gate_add_grad(k, state, streams_in, alpha, dy, eps: float = 1e-6, dx=
 # then 32-bit ones and the scale.
 _MATMUL_ARGS = struct.Struct("QqQqqqqQQqQqQq7if")
 _MATMUL_GRAD_ARGS = struct.Struct("QqQqQqqqqQqQqQqQ8if4x")
+# The numbers of engram_orthogonalise, of which ctypes would keep the low bits.
+_ORTHOGONALISE_NUMBERS = struct.Struct("ii6f")
 
 
 def _bf16_operand(t, name):
@@ -1032,7 +1034,7 @@ def _packed(fmt, *values):
     """The bytes of an argument struct."""
     try:
         return fmt.pack(*values)
-    except struct.error as e:
+    except (struct.error, OverflowError) as e:  # the latter for a float that fp32 does not hold
         raise EngramError(ERR_INVALID_ARG, f"an argument is no number of its range: {e}") from None
 
 
@@ -1161,6 +1163,7 @@ def engram_orthogonalise(g, momentum=None, beta: float = 0.95, nesterov: bool = 
     L, M, N = shape if len(shape) == 3 else (1, *shape)
     if len(coefficients) != 3:
         raise EngramError(ERR_INVALID_ARG, "coefficients must be three numbers")
+    _packed(_ORTHOGONALISE_NUMBERS, bool(nesterov), steps, beta, *coefficients, scale, eps)
     if momentum is not None:
         _need(momentum, (torch.float32,), "momentum", contiguous=False)
     if out is None:
