@@ -1034,7 +1034,7 @@ def _packed(fmt, *values):
     """The bytes of an argument struct."""
     try:
         return fmt.pack(*values)
-    except (struct.error, OverflowError) as e:  # the latter for a float that fp32 does not hold
+    except struct.error as e:
         raise EngramError(ERR_INVALID_ARG, f"an argument is no number of its range: {e}") from None
 
 
