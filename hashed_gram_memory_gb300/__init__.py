@@ -1091,7 +1091,8 @@ def engram_matmul_grad(dy, a, b, pre=None, activation: int = ACT_NONE, scale: fl
     """The backward pass of engram_matmul(a, b, bias, activation, scale=scale, pre=pre) for the
     output gradient dy (bf16 or fp32 [M, N]; rows may repeat): (da [M, K], db [N, K], dbias fp32
     [N]), None for those not asked for.  da and db are bf16 by default; accumulate adds to the db
-    and dbias given.  What the two products read of dy act'(pre) has been rounded to bf16."""
+    and dbias given.  What a bf16 da or db's product reads of dy act'(pre) has been rounded to bf16;
+    an fp32 one's keeps 16 bits of it, for twice the operations."""
     M, K, pa, sa, ta = _bf16_operand(a, "a")
     N, kb, pb, sb, tb = _bf16_operand(b, "b")
     shape = (M, N)

@@ -12,10 +12,10 @@
 // All threads but the one that issues the instructions serve the epilogues, lanes being rows.  What
 // is rounded, and where, is as in orthogonalise.cu.  Bound by the latency of a step, 2.5 us in a CTA
 // by itself and 6 where two join A; fp32 with momentum, in us, beside the chain of launches:
-//   1 of  64 x   64   16 and 67        32 of  64 x  256    26 and  84
-//   1 of 128 x  128   22 and 67        16 of 128 x 1024    50 and  98
-//   1 of 128 x  512   45 and 73      1000 of 128 x  128   169 and 316
-//   1 of 100 x 3500   76 and 97       300 of 128 x  896   301 and 419
+//   1 of  64 x   64   17 and 63        32 of  64 x  256    28 and  76
+//   1 of 128 x  128   24 and 60        16 of 128 x 1024    55 and  92
+//   1 of 128 x  512   48 and 68      1000 of 128 x  128   180 and 303
+//   1 of 100 x 3500   80 and 80       300 of 128 x  896   316 and 428
 #include <stddef.h>
 
 #include <mutex>

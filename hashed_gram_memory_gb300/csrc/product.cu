@@ -18,8 +18,8 @@
 //     those leave SMs idle (a few rows of a: reading b is the work), 2 to 8 CTAs of a cluster share a
 //     tile, each with a part of K, and add their parts through distributed shared memory in rank
 //     order, two such CTAs an SM.
-// 65,536 x 4096 x 6144 takes 1947 us in pairs, 1.69 PFLOP/s (the power limit's, as the library's);
-// 37 x 4096 x 6144 13.5 us, K shared by 8: 50 MB, 7.5 us at the measured bandwidth, behind the launch,
+// 65,536 x 4096 x 6144 takes 1790 to 1930 us in pairs, 1.7 to 1.8 PFLOP/s as the power limit lets it;
+// 37 x 4096 x 6144 14.1 us, K shared by 8: 50 MB, 7.5 us at the measured bandwidth, behind the launch,
 // the first bytes and the joining.
 // Warps: 0, 2 and 3 TMA producers (a ring of stages of 64 of K, 128-byte swizzle); 1 allocates TMEM,
 // one thread (of the pair's even CTA) issues the MMAs into one of two accumulators; 4.. epilogue.
@@ -28,7 +28,11 @@
 // number of additions (1e-9 of the result for each value of K, against 1e-6 of an fp32 sum of
 // 8192).  So where out or pre is fp32, K is cut into segments of at most 768 that each start a new
 // accumulator, and the epilogue adds them in registers, rounding to nearest (7e-7 of the result;
-// segments of 512 would be 5e-7 and take 4 % longer, of 1024 1e-6).
+// segments of 512 would be 5e-7 and take 4 % longer, of 1024 1e-6).  CTAs that share K put their part
+// of it into two accumulators, or where it is longer than two segments into three or four.
+//
+// An operand may be the sum of two matrices (a gradient of which bf16 holds a half each): K goes
+// through one and then the other, in the same accumulators.
 //
 // A symmetric product (both operands one matrix) computes the tiles on one side of the diagonal
 // and stores every unit of 32 x 32 values twice, the second time turned in shared memory.

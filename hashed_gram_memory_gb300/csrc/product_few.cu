@@ -8,8 +8,8 @@
 // values of a row, one 16-byte word, for every two instructions.  Those words come through shared
 // memory, copied asynchronously kDeep steps ahead, and each lane reads back what it copied itself:
 // nothing to wait for but its own copies.  A block has 16 rows of b, its warps take 32 of K in turn
-// and add their sums in shared memory, always in the same order.  1 x 4096 x 6144 takes 11.3 us, 50 MB
-// of b at 4.4 TB/s, 3.9 us of them before the first and after the last bytes.
+// and add their sums in shared memory, always in the same order.  1 x 4096 x 6144 takes 12.0 us, 50 MB
+// of b at 4.2 TB/s, about 4 us of them before the first and after the last bytes.
 #include <atomic>
 
 #include "launch.cuh"
@@ -188,9 +188,10 @@ cudaError_t launch_eights(const FewDev &d, int64_t grid, cudaStream_t stream) {
 }  // namespace
 
 bool few_rows_supported(const ProductParams &p) {
-  // Every block reads all rows of a: from 9 rows on that costs more than it saves where b is large
-  // (16 x 4096 x 4096 9.5 us and 9.0 by clusters, 16 x 2048 x 4096 5.8 and 6.5; 8 x 4096 x 6144 11.8 and
-  // 12.7).
+  // Up to 8 rows always: 8 x 4096 x 6144 12.4 us and 13.4 by clusters, 1 x 4096 x 6144 12.0 and 13.1,
+  // 8 x 8192 x 8192 27.5 and 28.9.  From 9 rows on that every block reads all rows of a costs more than it
+  // saves where b is large, with the shape: 16 x 2048 x 4096 6.2 and 8.0; 16 x 4096 x 6144 14.4 and 13.4,
+  // 16 x 4096 x 5120 12.4 and 11.9, 16 x 1024 x 16,384 19.0 and 12.8, but 16 x 4096 x 4096 9.8 and 10.8.
   return (p.M <= 8 || (p.M <= 16 && p.N * p.K <= 12 << 20)) && p.count == 1 && !p.symmetric && !p.f16 && !p.a_two && !p.a.t &&
          !p.b.t && p.out.type != kTypeF16;
 }
