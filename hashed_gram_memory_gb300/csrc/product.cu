@@ -29,7 +29,9 @@
 // 8192).  So where out or pre is fp32, K is cut into segments of at most 768 that each start a new
 // accumulator, and the epilogue adds them in registers, rounding to nearest (7e-7 of the result;
 // segments of 512 would be 5e-7 and take 4 % longer, of 1024 1e-6).  CTAs that share K put their part
-// of it into two accumulators, or where it is longer than two segments into three or four.
+// of it into two accumulators, or where it is longer than two segments into three or four.  bf16
+// outputs take segments of 262,144, about 8e-4 of a sum of like signs, a fifth of their rounding: one
+// accumulator of 2^25 values is 1e-2 off.
 //
 // An operand may be the sum of two matrices (a gradient of which bf16 holds a half each): K goes
 // through one and then the other, in the same accumulators.
@@ -60,7 +62,7 @@ constexpr int kApartQMax = 64;  // and of CTAs that share K and have more than t
 constexpr int kParts = 4, kPairParts = 4;
 constexpr int kThreads = 128 * (1 + kParts), kPairThreads = 128 * (1 + kPairParts);
 constexpr int kSplitParts = 2, kSplitThreads = 128 * (1 + kSplitParts);
-constexpr int kSegmentBlocks = 12;
+constexpr int kSegmentBlocks = 12, kBf16SegmentBlocks = 4096;
 constexpr int kMaxStages = 12, kMaxAhead = 4, kProducers = 3;
 constexpr uint32_t kPBytes = kP * kBK * 2;
 constexpr uint32_t kBarBytes = 1024;
@@ -1225,6 +1227,7 @@ struct Plan {
 // What the choice goes by of a product.
 struct Facts {
   ProductDev d;  // all but what a plan decides
+  int64_t segment;  // most blocks of K in one accumulator
   bool tiles_epilogue;
 };
 Facts facts_of(const ProductParams &p) {
@@ -1244,13 +1247,12 @@ Facts facts_of(const ProductParams &p) {
   d.many = p.count > 1;
   d.pass_blocks = (int32_t)ceil_div(p.K, kBK);
   d.kblocks = p.a_two ? 2 * d.pass_blocks : d.pass_blocks;
-  // Segments only where the output has the bits to show them.
-  d.segments = 1;
-  d.seg_blocks = d.kblocks;
-  if (p.out.type == ENGRAM_DTYPE_F32 || p.pre.type == ENGRAM_DTYPE_F32) {
-    d.seg_blocks = (int32_t)ceil_div(d.kblocks, ceil_div(d.kblocks, kSegmentBlocks));
-    d.segments = (int32_t)ceil_div(d.kblocks, d.seg_blocks);
-  }
+  // Segments as short as the output has the bits to show them; none of fp16, the library's own.
+  f.segment = p.out.type == ENGRAM_DTYPE_F32 || (p.pre.p && p.pre.type == ENGRAM_DTYPE_F32) ? kSegmentBlocks
+              : p.out.type == kTypeF16                                                      ? d.kblocks
+                                                                                            : kBf16SegmentBlocks;
+  d.seg_blocks = (int32_t)ceil_div(d.kblocks, ceil_div(d.kblocks, f.segment));
+  d.segments = (int32_t)ceil_div(d.kblocks, d.seg_blocks);
   // The tiles' epilogue wants rows on 16-byte boundaries (a row that repeats has none apart).  Its
   // copies write whole 16 bytes, also where a row ends inside them: only the library's own planes,
   // which are fp16, have nothing there.  Storing such ends apart took the others 2 to 7 % longer.
@@ -1307,8 +1309,8 @@ Plan plan_form(const ProductParams &p, const Facts &f, int form, bool rows, cons
 
 // Accumulators of a CTA where n share K: two, or where K goes in segments one for each of its own.
 int split_segments(const Facts &f, int n) {
-  const int64_t own = ceil_div(ceil_div(f.d.kblocks, n), kSegmentBlocks);
-  return f.d.segments > 1 && own > 2 ? (int)own : 2;
+  const int64_t own = ceil_div(ceil_div(f.d.kblocks, n), f.segment);
+  return own > 2 ? (int)own : 2;
 }
 
 // K shared by 2 to 8 CTAs, two an SM: what a CTA takes of K, and the joining, by the rounds that its
@@ -1326,7 +1328,7 @@ Plan plan_split(const ProductParams &p, const Facts &f, const DeviceInfo &info) 
       // Of fp32 outputs the accumulators of a part have to fit, and parts are not much longer than the
       // others' segments.
       if (split_segments(f, n) > (width <= kApartQMax ? (int)kSplitTmemCols / kApartQMax : 2)) continue;
-      if (f.d.segments > 1 && ceil_div(f.d.kblocks, n) > (n == 2 ? 24 : 32)) continue;
+      if (f.segment == kSegmentBlocks && f.d.segments > 1 && ceil_div(f.d.kblocks, n) > (n == 2 ? 24 : 32)) continue;
       Plan s;
       s.form = kSplit;
       s.q_tile = width;

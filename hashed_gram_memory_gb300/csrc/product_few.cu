@@ -217,10 +217,10 @@ cudaError_t launch_few_rows(const ProductParams &p, cudaStream_t stream) {
   // Four steps of K a warp at least, where there are that many.
   d.warps = 1;
   while (d.warps < kWarps && d.warps * 128 < p.K) d.warps *= 2;
-  // Where outputs have the bits to show it and K is that long.  In segments 1 x 4096 x 6144 would take
-  // 12.2 us, not 12.0, and 16 x 2048 x 4096 6.6, not 6.2.
-  const bool segments = (p.out.type == ENGRAM_DTYPE_F32 || (p.pre.p && p.pre.type == ENGRAM_DTYPE_F32)) &&
-                        p.K > (int64_t)d.warps * 2 * kSegment * 16;
+  // Where K is so long that outputs have the bits to show it: sums of 768 in fp32, of 262,144 in bf16.  In
+  // segments 1 x 4096 x 6144 would take 12.2 us, not 12.0, and 16 x 2048 x 4096 6.6, not 6.2.
+  const bool f32 = p.out.type == ENGRAM_DTYPE_F32 || (p.pre.p && p.pre.type == ENGRAM_DTYPE_F32);
+  const bool segments = p.K > (int64_t)d.warps * 2 * (f32 ? kSegment * 16 : 262144);
   if (p.M <= 8) return segments ? launch_eights<1, true>(d, grid, stream) : launch_eights<1, false>(d, grid, stream);
   return segments ? launch_eights<2, true>(d, grid, stream) : launch_eights<2, false>(d, grid, stream);
 }

@@ -713,7 +713,7 @@ ENGRAM_API engram_status engram_gate_add_grad(const float *k, const uint8_t *sta
  *         workspace unused) when both operands start on 16-byte boundaries with strides that
  *         are multiples of 8 elements
  * Where out or pre is fp32, long sums are added up in parts of at most 768, rounding to
- * nearest between them (the tensor cores do not inside).  A wait that runs out sets
+ * nearest between them (the tensor cores do not inside); elsewhere of 262,144.  A wait that runs out sets
  * ENGRAM_FLAG_TIMEOUT and leaves outputs unwritten.  M == 0 launches nothing.
  */
 typedef struct engram_matmul_args {
