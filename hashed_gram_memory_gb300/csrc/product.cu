@@ -29,7 +29,7 @@
 // 8192).  So where out or pre is fp32, K is cut into segments of at most 768 that each start a new
 // accumulator, and the epilogue adds them in registers, rounding to nearest (7e-7 of the result;
 // segments of 512 would be 5e-7 and take 4 % longer, of 1024 1e-6).  CTAs that share K put their part
-// of it into two accumulators, or where it is longer than two segments into three or four.  bf16
+// of it into two accumulators, or where it is longer than two segments into three or four.  16-bit
 // outputs take segments of 262,144, about 8e-4 of a sum of like signs, a fifth of their rounding: one
 // accumulator of 2^25 values is 1e-2 off.
 //
@@ -62,7 +62,7 @@ constexpr int kApartQMax = 64;  // and of CTAs that share K and have more than t
 constexpr int kParts = 4, kPairParts = 4;
 constexpr int kThreads = 128 * (1 + kParts), kPairThreads = 128 * (1 + kPairParts);
 constexpr int kSplitParts = 2, kSplitThreads = 128 * (1 + kSplitParts);
-constexpr int kSegmentBlocks = 12, kBf16SegmentBlocks = 4096;
+constexpr int kSegmentBlocks = 12, kHalfSegmentBlocks = 4096;
 constexpr int kMaxStages = 12, kMaxAhead = 4, kProducers = 3;
 constexpr uint32_t kPBytes = kP * kBK * 2;
 constexpr uint32_t kBarBytes = 1024;
@@ -1247,10 +1247,10 @@ Facts facts_of(const ProductParams &p) {
   d.many = p.count > 1;
   d.pass_blocks = (int32_t)ceil_div(p.K, kBK);
   d.kblocks = p.a_two ? 2 * d.pass_blocks : d.pass_blocks;
-  // Segments as short as the output has the bits to show them; none of fp16, the library's own.
+  // Segments as short as the output has the bits to show them; none of symmetric products.
   f.segment = p.out.type == ENGRAM_DTYPE_F32 || (p.pre.p && p.pre.type == ENGRAM_DTYPE_F32) ? kSegmentBlocks
-              : p.out.type == kTypeF16                                                      ? d.kblocks
-                                                                                            : kBf16SegmentBlocks;
+              : p.symmetric                                                                 ? d.kblocks
+                                                                                            : kHalfSegmentBlocks;
   d.seg_blocks = (int32_t)ceil_div(d.kblocks, ceil_div(d.kblocks, f.segment));
   d.segments = (int32_t)ceil_div(d.kblocks, d.seg_blocks);
   // The tiles' epilogue wants rows on 16-byte boundaries (a row that repeats has none apart).  Its
@@ -1474,10 +1474,10 @@ cudaError_t launch_product(const ProductParams &p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const Facts f = facts_of(p);
   const Plan plan = plan_of(p, f, info);
-  if (p.symmetric) {  // half of the tiles, unless that many run side by side in any case
+  if (p.symmetric) {  // half of the tiles, unless that many run side by side in any case, or K is long
     ProductParams whole = p;
     whole.symmetric = false;
-    if (plan_of(whole, facts_of(whole), info).us <= plan.us) return launch_product(whole, stream);
+    if (f.d.kblocks > kHalfSegmentBlocks || plan_of(whole, facts_of(whole), info).us <= plan.us) return launch_product(whole, stream);
   }
   Jobs jobs{};
   jobs.count = 1;
