@@ -9,13 +9,19 @@
 //          shared memory in rank order, the fp16 result written to every CTA;
 //   B    = b A + c A^2: every CTA by itself;
 //   X_c  = a X_c + B X_c: every CTA its columns, in place.
-// All threads but the one that issues the instructions serve the epilogues, lanes being rows.  What
-// is rounded, and where, is as in orthogonalise.cu.  Bound by the latency of a step, 2.5 us in a CTA
+// All threads but the one that issues the instructions serve the epilogues, lanes being rows.
+//
+// X, A and B are held in fp16 as in orthogonalise.cu, but for the diagonals d of A and e of B, which stay
+// fp32: with A' and B' the others,
+//   B' = (b + c (d_i + d_j)) A' + c A'^2,   e = b d + c (d^2 + A'^2's diagonal),   X = (a + e_i) X + B' X.
+// Where few rows share the norm the square matrices are nearly diagonal, and a + e_i a difference four
+// times as small as e: rounding e to fp16 as the rest was most of the error (16 x 700 2.4e-3 off, its own
+// rounding to bf16 included, now 1.9e-3).  Bound by the latency of a step, 2.5 us in a CTA
 // by itself and 6 where two join A; fp32 with momentum, in us, beside the chain of launches:
-//   1 of  64 x   64   17 and 63        32 of  64 x  256    28 and  76
-//   1 of 128 x  128   24 and 60        16 of 128 x 1024    55 and  92
-//   1 of 128 x  512   48 and 68      1000 of 128 x  128   180 and 303
-//   1 of 100 x 3500   80 and 80       300 of 128 x  896   316 and 428
+//   1 of  64 x   64   18 and 63        32 of  64 x  256    29 and  76
+//   1 of 128 x  128   25 and 60        16 of 128 x 1024    57 and  92
+//   1 of 128 x  512   51 and 68      1000 of 128 x  128   189 and 303
+//   1 of 100 x 3500   80 and 80       300 of 128 x  896   329 and 428
 #include <stddef.h>
 
 #include <mutex>
@@ -99,6 +105,23 @@ __device__ __forceinline__ uint32_t bfloats(float lo, float hi) {
 }
 __device__ __forceinline__ float2 floats(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
 
+// Value i of 16 (a chain of 16 selections takes 0.1 us longer a time).
+__device__ __forceinline__ float pick(const uint32_t (&v)[16], int i) {
+  uint32_t a[8], b[4];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) a[k] = i & 1 ? v[2 * k + 1] : v[2 * k];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) b[k] = i & 2 ? a[2 * k + 1] : a[2 * k];
+  const uint32_t lo = i & 4 ? b[1] : b[0], hi = i & 4 ? b[3] : b[2];
+  return __uint_as_float(i & 8 ? hi : lo);
+}
+// Zero at row i, column i of a square matrix, after the row was stored.
+__device__ __forceinline__ void clear_diagonal(uint32_t square, int i) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(at(square + (i >> 6) * kBlock, i, (i & 63) >> 3) + (i & 7) * 2),
+               "h"((uint16_t)0)
+               : "memory");
+}
+
 // f(row of X, column of X of this CTA, u) over the CTA's elements; with FIRST the momentum moves.
 // Neighbouring threads take neighbouring elements of a matrix row in memory; a warp 128 of each of
 // kRows rows at a time: all of their loads, then the rest.
@@ -159,6 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1) orthogonalise_small_kernel(const 
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag, gave_up;
   __shared__ Squares warp_sums[kWarps], cta_sum;
+  __shared__ __align__(16) float diag_a[kR], diag_b[kR];
   uint8_t *sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
   const uint32_t X = smem_u32(sm), A = X + p.blocks * kBlock, B = A + kSquare, part = B;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -276,6 +300,13 @@ __global__ void __launch_bounds__(kThreads, 1) orthogonalise_small_kernel(const 
             const int c = c0 + 16 * h + 8 * q;
             st16(at(A + (c >> 6) * kBlock, row, (c & 63) >> 3), make_uint4(w[0], w[1], w[2], w[3]));
           }
+          if (quad == share) {
+            const float d = pick(v, lane & 15) / (kHeld * kHeld);
+            if (lane >> 4 == h) {
+              diag_a[row] = d;
+              clear_diagonal(A, row);
+            }
+          }
         } else {
 #pragma unroll
           for (int q = 0; q < 4; ++q)
@@ -297,6 +328,16 @@ __global__ void __launch_bounds__(kThreads, 1) orthogonalise_small_kernel(const 
           v[q] = q < p.cluster ? load4_cluster(map_to_rank(part + (r * kPitch + c) * 4, q)) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int q = 0; q < 8; ++q) s.x += v[q].x, s.y += v[q].y, s.z += v[q].z, s.w += v[q].w;
+        // A warp has a row: the lane of its diagonal takes it out, a lane for each CTA hands it on.
+        const int k = r & 3;
+        const bool here = r >> 2 == c >> 2;
+        const float d = __shfl_sync(0xffffffffu, k == 0 ? s.x : k == 1 ? s.y : k == 2 ? s.z : s.w, r >> 2);
+        s = make_float4(here && k == 0 ? 0.f : s.x, here && k == 1 ? 0.f : s.y, here && k == 2 ? 0.f : s.z,
+                        here && k == 3 ? 0.f : s.w);
+        if (lane < p.cluster)
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(map_to_rank(smem_u32(diag_a + r), lane)),
+                       "f"(d / (kHeld * kHeld))
+                       : "memory");
         const uint32_t lo = halves(s.x / kHeld, s.y / kHeld), hi = halves(s.z / kHeld, s.w / kHeld);
         const uint32_t to = at(A + (c >> 6) * kBlock, r, (c & 63) >> 3) + (c & 4) * 2;
         for (int q = 0; q < p.cluster; ++q)
@@ -313,6 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) orthogonalise_small_kernel(const 
         for (int i = 0; i < 4; ++i)
           umma(tmem + kR, x + k * (kBlock >> 4) + 2 * i, x + k * (kBlock >> 4) + 2 * i, idesc, k + i > 0);
     });
+    const float d = diag_a[row], mine = fmaf(p.c, d, p.b);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (!ok) break;
@@ -324,15 +366,24 @@ __global__ void __launch_bounds__(kThreads, 1) orthogonalise_small_kernel(const 
         const int c = c0 + 16 * h + 8 * q;
         const uint32_t to = at((c >> 6) * kBlock, row, (c & 63) >> 3);
         const uint4 have = ld16(A + to);
+        const float4 e0 = *reinterpret_cast<const float4 *>(diag_a + c), e1 = *reinterpret_cast<const float4 *>(diag_a + c + 4);
         const uint32_t w[4] = {have.x, have.y, have.z, have.w};
+        const float e[8] = {e0.x, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w};
         uint32_t y[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 f = floats(w[i]);
-          y[i] = halves(fmaf(p.b, f.x, p.c / kHeld * __uint_as_float(v[8 * q + 2 * i])),
-                        fmaf(p.b, f.y, p.c / kHeld * __uint_as_float(v[8 * q + 2 * i + 1])));
+          y[i] = halves(fmaf(fmaf(p.c, e[2 * i], mine), f.x, p.c / kHeld * __uint_as_float(v[8 * q + 2 * i])),
+                        fmaf(fmaf(p.c, e[2 * i + 1], mine), f.y, p.c / kHeld * __uint_as_float(v[8 * q + 2 * i + 1])));
         }
         st16(B + to, make_uint4(y[0], y[1], y[2], y[3]));
+      }
+      if (quad == share) {
+        const float e = fmaf(mine, d, p.c / (kHeld * kHeld) * pick(v, lane & 15));
+        if (lane >> 4 == h) {
+          diag_b[row] = e;
+          clear_diagonal(B, row);
+        }
       }
     }
     // ---- X
@@ -346,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) orthogonalise_small_kernel(const 
           umma(tmem + n * 64, b + (k >> 2) * (kBlock >> 4) + 2 * (k & 3), x + k * (2048 >> 4), idesc, k > 0);
       }
     });
+    const float own = p.a + diag_b[row];
     const bool last = step == p.steps - 1;
     if (last) {  // out is written by all of a matrix's CTAs or by none
       ok = __syncthreads_and(ok);
@@ -369,8 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1) orthogonalise_small_kernel(const 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 f = floats(w[i]);
-          x[8 * q + 2 * i] = fmaf(p.a, f.x, __uint_as_float(v[8 * q + 2 * i]) / kHeld);
-          x[8 * q + 2 * i + 1] = fmaf(p.a, f.y, __uint_as_float(v[8 * q + 2 * i + 1]) / kHeld);
+          x[8 * q + 2 * i] = fmaf(own, f.x, __uint_as_float(v[8 * q + 2 * i]) / kHeld);
+          x[8 * q + 2 * i + 1] = fmaf(own, f.y, __uint_as_float(v[8 * q + 2 * i + 1]) / kHeld);
         }
         if (last && !p.tall) {
 #pragma unroll
