@@ -155,7 +155,7 @@ int64_t padded(int64_t n) { return (n + 63) / 64 * 64; }
 
 struct Layout {
   int64_t x_batch, a_batch;  // elements a matrix
-  size_t a, b, x[2], partial, bytes;
+  size_t a, b, x[2], diagonals, partial, bytes;
 };
 Layout layout_of(int64_t M, int64_t N, int64_t count) {
   const int64_t r = M < N ? M : N;
@@ -172,6 +172,7 @@ Layout layout_of(int64_t M, int64_t N, int64_t count) {
   l.x[1] = take(l.x_batch * count * 2);
   l.a = take(l.a_batch * count * 2);
   l.b = take(l.a_batch * count * 2);
+  l.diagonals = take(padded(r) * count * 2 * sizeof(float));
   l.partial = take((size_t)kMostParts * count * sizeof(Squares));
   l.bytes = at;
   return l;
@@ -221,12 +222,15 @@ cudaError_t launch_orthogonalise(const OrthogonaliseParams &p, void *workspace, 
   const int64_t r = tall ? p.N : p.M, w = tall ? p.M : p.N;
   const Plane none{nullptr, 0, 0, ENGRAM_DTYPE_BF16};
   const Plane A{ws + l.a, padded(r), l.a_batch, kTypeF16}, B{ws + l.b, padded(r), l.a_batch, kTypeF16};
+  float *const of_a = reinterpret_cast<float *>(ws + l.diagonals), *const of_b = of_a + padded(r) * p.count;
   const auto operand = [](const Plane &x, bool t) { return Operand{x.p, x.stride, x.batch, t}; };
   for (int i = 0; i < p.steps && e == cudaSuccess; ++i) {
     const Plane X{ws + l.x[i & 1], padded(p.N), l.x_batch, kTypeF16};
     const bool last = i == p.steps - 1;
     ProductParams q{};
-    q.f16 = true;
+    q.f16 = q.newton = true;
+    q.diag_batch = padded(r);
+    q.diag_scale = 1.f / kHeld;
     q.count = p.count;
     q.status = p.status;
     q.residual = q.pre = none;
@@ -236,6 +240,7 @@ cudaError_t launch_orthogonalise(const OrthogonaliseParams &p, void *workspace, 
     q.K = w;
     q.scale = 1.f / kHeld;
     q.out = A;
+    q.diag_out = of_a;
     q.symmetric = true;
     if ((e = launch_product(q, stream)) != cudaSuccess) break;
     // B
@@ -245,6 +250,10 @@ cudaError_t launch_orthogonalise(const OrthogonaliseParams &p, void *workspace, 
     q.residual = A;
     q.residual_scale = p.b;
     q.out = B;
+    q.diag_in = of_a;
+    q.diag_out = of_b;
+    q.diag_rows = q.diag_columns = true;
+    q.diag_by = p.c;
     if ((e = launch_product(q, stream)) != cudaSuccess) break;
     // X
     q.symmetric = false;
@@ -256,6 +265,11 @@ cudaError_t launch_orthogonalise(const OrthogonaliseParams &p, void *workspace, 
     q.scale = by / kHeld;
     q.residual = X;
     q.residual_scale = p.a * by;
+    q.diag_in = of_b;
+    q.diag_out = nullptr;
+    q.diag_rows = !tall;
+    q.diag_columns = tall;
+    q.diag_by = by;
     q.out = last ? p.out : Plane{ws + l.x[(i + 1) & 1], padded(p.N), l.x_batch, kTypeF16};
     e = launch_product(q, stream);
   }

@@ -109,6 +109,11 @@ struct ProductDev {
   // which CTAs (or pairs) take which tiles: see Walk
   int32_t shift, extra;
   bool p_t, q_t, many;
+  const float *diag_in;  // as in ProductParams
+  float *diag_out;
+  int64_t diag_batch;
+  float diag_by, diag_scale;
+  bool diag_rows, diag_columns;
   bool rows;      // rows of out in the lanes; else its columns
   bool withhold;  // test hook: the first stage waits for bytes that never come
 };
@@ -356,6 +361,35 @@ __device__ __forceinline__ void put_column(uint32_t unit, int r, const float (&x
                  "h"(__half_as_ushort(__float2half_rn(x[i])))
                  : "memory");
 }
+// x += by(m, n) * the row's fp16 values: base and, where there is d, `column` times a column's value of d.
+__device__ __forceinline__ void add_row_by(uint32_t unit, int r, float base, float column, const float *d,
+                                           float (&x)[kUnit]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint4 v = ld_shared(piece<false>(unit, r, j));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float by[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) by[i] = base;
+    if (d) {
+      const float4 d0 = reinterpret_cast<const float4 *>(d)[2 * j], d1 = reinterpret_cast<const float4 *>(d)[2 * j + 1];
+      const float all[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) by[i] = fmaf(column, all[i], base);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      decode2(w[i], kTypeF16, lo, hi);
+      x[8 * j + 2 * i] = fmaf(by[2 * i], lo, x[8 * j + 2 * i]);
+      x[8 * j + 2 * i + 1] = fmaf(by[2 * i + 1], hi, x[8 * j + 2 * i + 1]);
+    }
+  }
+}
+// What diag_out receives of an element (m, m) and its value d of diag_in.
+__device__ __forceinline__ float on_diagonal(const ProductDev &p, float x, float d) {
+  return fmaf(fmaf(p.diag_by, d, p.residual_scale), d, x * p.diag_scale);
+}
 // x += by * the row's values.
 __device__ __forceinline__ void add_row(uint32_t unit, int r, int type, float by, float (&x)[kUnit]) {
   if (type == ENGRAM_DTYPE_F32) {
@@ -445,7 +479,7 @@ struct Shared {
 };
 
 // How a warp moves units: its buffers for what comes in (`ahead` of them) and goes out.
-template <bool SYMMETRIC>
+template <bool SYMMETRIC, bool NEWTON>
 struct Mover {
   const Job &job;
   const ProductDev &p;
@@ -525,15 +559,28 @@ struct Mover {
       send(&job.pre, at, n, m, z);
     }
     activate(x, p.act);
+    [[maybe_unused]] float d = 0.f;  // of the lane's row
+    if (NEWTON && p.diag_rows) d = p.diag_in[z * p.diag_batch + m + w.lane];
     uint32_t at = 0;
     if (p.ahead) {
       if (!warp_wait(w.arrived + used, (w.phases >> used) & 1, w.abort_flag, p)) return false;
       w.phases ^= 1u << used;
       at = w.buffers + used * p.ahead_bytes;
-      add_row(at, w.lane, p.residual.type, p.residual_scale, x);
+      if constexpr (NEWTON)
+        add_row_by(at, w.lane, fmaf(p.diag_by, d, p.residual_scale), p.diag_by,
+                   p.diag_columns ? p.diag_in + z * p.diag_batch + n : nullptr, x);
+      else
+        add_row(at, w.lane, p.residual.type, p.residual_scale, x);
       used = used + 1 == p.ahead ? 0 : used + 1;
       --waiting;
       __syncwarp();
+    }
+    if (NEWTON && p.diag_out && n == m) {  // units lie on multiples of 32
+      float own = 0.f;
+#pragma unroll
+      for (int i = 0; i < kUnit; ++i)
+        if (i == w.lane) own = x[i], x[i] = 0.f;
+      if (m + w.lane < p.M) p.diag_out[z * p.diag_batch + m + w.lane] = on_diagonal(p, own, d);
     }
     if (p.slots) at = free_slot();  // else out goes where the residual came
     put_row(at, w.lane, p.out.type, x);
@@ -561,7 +608,7 @@ struct Mover {
 };
 
 // A warp's share of the epilogue of all of its CTA's tiles: units [first, end) of each.
-template <bool PAIR, bool SYMMETRIC, typename F>
+template <bool PAIR, bool SYMMETRIC, bool NEWTON, typename F>
 __device__ __forceinline__ bool move_tiles(const Job &job, const Walk &walk, Shared &w, int first, int end, F release) {
   constexpr int kWidth = PAIR ? 2 * kP : kP, kAccCols = PAIR ? kPairQMax : kQMax;
   const ProductDev &p = job.d;
@@ -574,7 +621,7 @@ __device__ __forceinline__ bool move_tiles(const Job &job, const Walk &walk, Sha
     }
     return true;
   }
-  Mover<SYMMETRIC> mover(job, w);
+  Mover<SYMMETRIC, NEWTON> mover(job, w);
   Units<kWidth, SYMMETRIC> ahead(p, walk, first, end, w.row0), now = ahead;
   // The residual of the next unit that has not been asked for.
   const auto ask = [&] {
@@ -634,13 +681,13 @@ __device__ __forceinline__ bool add_segments(const ProductDev &p, Shared &w, int
 }
 
 // move_tiles for products in segments, whose sums stay in registers.
-template <bool PAIR, typename F>
+template <bool PAIR, bool NEWTON, typename F>
 __device__ __forceinline__ bool move_tiles_of_segments(const Job &job, Walk walk, Shared &w, int first, int end,
                                                        F release) {
   constexpr int kWidth = PAIR ? 2 * kP : kP, kAccCols = PAIR ? kPairQMax : kQMax;
   constexpr int kMost = kAccCols / kUnit / (PAIR ? kPairParts : kParts);  // units a warp
   const ProductDev &p = job.d;
-  Mover<false> mover(job, w);
+  Mover<false, NEWTON> mover(job, w);
   bool ok = true;
   for (; ok && walk.tile < p.tiles; walk.next()) {
     const Tile t = tile_at<kWidth, false>(p, walk.tile);
@@ -688,23 +735,57 @@ __device__ __forceinline__ void store_column(const PlaneDev &d, int z, int m, in
     }
   });
 }
+// How many times the residual's 16 values count: NEWTON by diagonals, `own` the column's.
+template <bool NEWTON>
+struct Counts {
+  float by[NEWTON ? 16 : 1], own;
+  __device__ __forceinline__ Counts(const ProductDev &p, int z, int m, int n, int count) {
+    if constexpr (NEWTON) {
+      const float *d = p.diag_in + z * p.diag_batch;
+      own = p.diag_columns && count > 0 ? d[n] : 0.f;
+      const float base = fmaf(p.diag_by, own, p.residual_scale);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) by[i] = base;
+      if (p.diag_rows && count > 0) {  // m is a multiple of 16, and d's length one of 64
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 v = *reinterpret_cast<const float4 *>(d + m + 4 * i);
+          by[4 * i] = fmaf(p.diag_by, v.x, base), by[4 * i + 1] = fmaf(p.diag_by, v.y, base);
+          by[4 * i + 2] = fmaf(p.diag_by, v.z, base), by[4 * i + 3] = fmaf(p.diag_by, v.w, base);
+        }
+      }
+    }
+  }
+};
+
 // Sums of products (m .., n) become outputs; y: the residual.
+template <bool NEWTON>
 __device__ __forceinline__ void finish_column(const ProductDev &p, int z, int m, int n, int count, float bias,
-                                              float (&x)[16], const float (&y)[16]) {
+                                              float (&x)[16], const float (&y)[16], const Counts<NEWTON> &counts) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = fmaf(p.scale, x[i], bias);
   if (p.pre.p) store_column(p.pre, z, m, n, count, x);
   activate(x, p.act);
   if (p.residual.p) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = fmaf(p.residual_scale, y[i], x[i]);
+    for (int i = 0; i < 16; ++i) x[i] = fmaf(NEWTON ? counts.by[NEWTON ? i : 0] : p.residual_scale, y[i], x[i]);
+  }
+  if constexpr (NEWTON) {
+    if (p.diag_out && n >= m && n < m + count) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (m + i == n) {
+          p.diag_out[z * p.diag_batch + n] = on_diagonal(p, x[i], counts.own);
+          x[i] = 0.f;
+        }
+    }
   }
   store_column(p.out, z, m, n, count, x);
 }
 
 // A warp's share of a tile: column n of each lane, `chunks` times 16 rows from m0 on.  SEGMENTS: adds
 // up the accumulators of a tile first.
-template <int KACC, int MOST, bool SEGMENTS, typename F>
+template <int KACC, int MOST, bool SEGMENTS, bool NEWTON, typename F>
 __device__ __forceinline__ bool drain_columns(const ProductDev &p, Shared &w, int z, int m0, int n, int column,
                                               int chunks, F release) {
   const bool there = n < p.N;
@@ -717,11 +798,12 @@ __device__ __forceinline__ bool drain_columns(const ProductDev &p, Shared &w, in
       const int m = m0 + c * 16, count = there ? min(16, p.M - m) : 0;
       float x[16], y[16];
       if (p.residual.p) load_column(p.residual, z, m, n, count, y);
+      const Counts<NEWTON> counts(p, z, m, n, count);
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = sums[i];
 #pragma unroll
       for (int i = 16; i < MOST * 16; ++i) sums[i - 16] = sums[i];
-      finish_column(p, z, m, n, count, bias, x, y);
+      finish_column<NEWTON>(p, z, m, n, count, bias, x, y, counts);
     }
   } else {
     const uint32_t acc = w.unit & 1;
@@ -732,13 +814,14 @@ __device__ __forceinline__ bool drain_columns(const ProductDev &p, Shared &w, in
       const int m = m0 + c * 16, count = there ? min(16, p.M - m) : 0;
       float x[16], y[16];
       if (p.residual.p) load_column(p.residual, z, m, n, count, y);
+      const Counts<NEWTON> counts(p, z, m, n, count);
       uint32_t v[16];
       __syncwarp();  // together again after the stores, as tcgen05.ld wants the warp
       tmem_ld16(w.tmem + acc * KACC + column + c * 16, v);
       if (c == chunks - 1) release(acc);
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[i]);
-      finish_column(p, z, m, n, count, bias, x, y);
+      finish_column<NEWTON>(p, z, m, n, count, bias, x, y, counts);
     }
     if (chunks == 0) release(acc);  // a narrow tile has nothing for this part
     ++w.unit;
@@ -749,8 +832,20 @@ __device__ __forceinline__ bool drain_columns(const ProductDev &p, Shared &w, in
 __device__ __noinline__ float activated_apart(float x, int act) { return activated(x, act); }
 
 // One sum of products of a tile that several CTAs share becomes an output.
+template <bool NEWTON>
 __device__ __forceinline__ void finish_one(const ProductDev &p, int64_t z, int64_t m, int64_t n, float x, float bias,
                                            float residual) {
+  if constexpr (NEWTON) {  // nothing but a residual comes to it
+    const float *d = p.diag_in + z * p.diag_batch;
+    const float own = p.diag_rows ? d[m] : 0.f;
+    x = fmaf(fmaf(p.diag_by, own + (p.diag_columns ? d[n] : 0.f), p.residual_scale), residual, x);
+    if (p.diag_out && m == n) {
+      p.diag_out[z * p.diag_batch + m] = on_diagonal(p, x, own);
+      x = 0.f;
+    }
+    store_one(p.out, z, m, n, x);
+    return;
+  }
   x += bias;
   if (p.pre.p) store_one(p.pre, z, m, n, x);
   if (p.act != ENGRAM_ACT_NONE) x = activated_apart(x, p.act);
@@ -763,13 +858,16 @@ __device__ __forceinline__ void finish_one(const ProductDev &p, int64_t z, int64
 // arrival that expects both CTAs' bytes; empty, acc_full and mma_done exist in both and take the
 // leader's multicast commits; acc_empty lives in the leader and takes an arrival from every
 // epilogue warp of the pair.
-enum Variant { kPlain, kSegments, kSymmetric };  // of the products that a kernel is for
+// Of the products that a kernel is for: sums of segments of K; the iteration's (ProductParams::newton),
+// symmetric ones among them.
+enum Variant { kPlain, kSegments, kSymmetric, kNewton, kNewtonSegments, kVariants };
 
 template <bool PAIR, bool SPLIT, int VARIANT>
 __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : kThreads, SPLIT ? 2 : 1)
     product_kernel(const __grid_constant__ Jobs jobs) {
-  constexpr bool SYMMETRIC = VARIANT == kSymmetric, SEGMENTS = VARIANT == kSegments;
-  static_assert(!(PAIR && SPLIT) && !(SPLIT && SYMMETRIC));
+  constexpr bool SYMMETRIC = VARIANT == kSymmetric, SEGMENTS = VARIANT == kSegments || VARIANT == kNewtonSegments;
+  constexpr bool NEWTON = VARIANT >= kSymmetric;
+  static_assert(!(PAIR && SPLIT) && !(SPLIT && (SYMMETRIC || VARIANT == kNewtonSegments)));
   constexpr bool kApart = SPLIT && SEGMENTS;  // more accumulators than two for a part of K
   constexpr uint32_t kCols = SPLIT ? kSplitTmemCols : kTmemCols;
   [[maybe_unused]] constexpr int kAccCols = PAIR ? kPairQMax : SPLIT && SEGMENTS ? kApartQMax : kQMax;
@@ -795,7 +893,7 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : 
   const int share = PAIR ? 2 : SPLIT ? splits : 1;  // CTAs a tile
   const int worker = blockIdx.x / share, workers = gridDim.x / share;
   // Two products have their code each: what they read of their parameters stays constant operands.
-  constexpr bool kTwo = !SPLIT && !SYMMETRIC;
+  constexpr bool kTwo = !SPLIT && !NEWTON;
   // This CTA's blocks of K of a product.
   const auto first_block = [&](const ProductDev &p) {
     return SPLIT ? (int)((int64_t)p.kblocks * rank / splits) : 0;
@@ -987,9 +1085,9 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : 
           const int units = qt / kUnit, u0 = units * part / kPartsHere, u1 = units * (part + 1) / kPartsHere;
           w.buffers = smem_u32(sm) + stages * stage_bytes + (warp - 4) * jobs.warp_bytes;
           if constexpr (SEGMENTS)
-            ok = move_tiles_of_segments<PAIR>(job, start, w, u0, u1, release);
+            ok = move_tiles_of_segments<PAIR, NEWTON>(job, start, w, u0, u1, release);
           else
-            ok = move_tiles<PAIR, SYMMETRIC>(job, start, w, u0, u1, release);
+            ok = move_tiles<PAIR, SYMMETRIC, NEWTON>(job, start, w, u0, u1, release);
           return;
         }
       }
@@ -1033,8 +1131,8 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : 
           constexpr int kMost = kAccCols / 16 / kPartsHere;
           for (Walk walk = start; ok && walk.tile < p.tiles; walk.next()) {
             const Tile t = tile_at<kTileP, false>(p, walk.tile);
-            ok = drain_columns<kAccCols, kMost, SEGMENTS>(p, w, t.z, t.q0 + c0 * 16, t.p0 + w.row0 + lane, c0 * 16,
-                                                          chunks, release);
+            ok = drain_columns<kAccCols, kMost, SEGMENTS, NEWTON>(p, w, t.z, t.q0 + c0 * 16, t.p0 + w.row0 + lane,
+                                                                  c0 * 16, chunks, release);
           }
         }
       }
@@ -1068,10 +1166,11 @@ __global__ void __launch_bounds__(PAIR ? kPairThreads : SPLIT ? kSplitThreads : 
 #pragma unroll
       for (int r = 0; r < 8; ++r) v[r] = r < splits ? __uint_as_float(load_cluster(map_to_rank(at, r))) : 0.f;
       const float bias = p.bias.p ? load_one(p.bias, 0, 0, n) : 0.f;
-      const float residual = p.residual.p ? p.residual_scale * load_one(p.residual, t.z, m, n) : 0.f;
+      const float residual =
+          p.residual.p ? (NEWTON ? 1.f : p.residual_scale) * load_one(p.residual, t.z, m, n) : 0.f;
 #pragma unroll
       for (int r = 1; r < 8; ++r) v[0] += v[r];
-      finish_one(p, t.z, m, n, p.scale * v[0], bias, residual);
+      finish_one<NEWTON>(p, t.z, m, n, p.scale * v[0], bias, residual);
     }
     cluster_sync();  // no CTA leaves while another may still read its part
   }
@@ -1142,12 +1241,15 @@ __global__ void __launch_bounds__(kSplitThreads, 2) two_an_sm_kernel() {}
 using Kernel = void (*)(Jobs);
 enum Form { kSingle, kSplit, kPair, kForms };
 Kernel kernel_of(int form, int variant) {
-  static constexpr Kernel all[kForms][3] = {
+  static constexpr Kernel all[kForms][kVariants] = {
       {product_kernel<false, false, kPlain>, product_kernel<false, false, kSegments>,
-       product_kernel<false, false, kSymmetric>},
-      {product_kernel<false, true, kPlain>, product_kernel<false, true, kSegments>, nullptr},
+       product_kernel<false, false, kSymmetric>, product_kernel<false, false, kNewton>,
+       product_kernel<false, false, kNewtonSegments>},
+      {product_kernel<false, true, kPlain>, product_kernel<false, true, kSegments>, nullptr,
+       product_kernel<false, true, kNewton>, nullptr},
       {product_kernel<true, false, kPlain>, product_kernel<true, false, kSegments>,
-       product_kernel<true, false, kSymmetric>}};
+       product_kernel<true, false, kSymmetric>, product_kernel<true, false, kNewton>,
+       product_kernel<true, false, kNewtonSegments>}};
   return all[form][variant];
 }
 
@@ -1159,10 +1261,10 @@ cudaError_t device_info(DeviceInfo &out) {
   DeviceInfo &d = g_info[dev & 63];
   if (!d.ready) {
     e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-    for (int i = 0; i < 3 * kForms && e == cudaSuccess; ++i)
-      if (kernel_of(i / 3, i % 3))
-        e = cudaFuncSetAttribute(kernel_of(i / 3, i % 3), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)(i / 3 == kSplit ? kSplitSmemBytes : kSmemBytes));
+    for (int i = 0; i < kVariants * kForms && e == cudaSuccess; ++i)
+      if (kernel_of(i / kVariants, i % kVariants))
+        e = cudaFuncSetAttribute(kernel_of(i / kVariants, i % kVariants), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)(i / kVariants == kSplit ? kSplitSmemBytes : kSmemBytes));
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -1241,6 +1343,13 @@ Facts facts_of(const ProductParams &p) {
   d.scale = p.scale;
   d.residual_scale = p.residual_scale;
   d.status = p.status;
+  d.diag_in = p.diag_in;
+  d.diag_out = p.diag_out;
+  d.diag_batch = p.diag_batch;
+  d.diag_rows = p.diag_rows;
+  d.diag_columns = p.diag_columns;
+  d.diag_by = p.diag_by;
+  d.diag_scale = p.diag_scale;
   d.wait_limit_ns = wait_limit_ns();
   d.M = (int32_t)p.M;
   d.N = (int32_t)p.N;
@@ -1327,7 +1436,7 @@ Plan plan_split(const ProductParams &p, const Facts &f, const DeviceInfo &info) 
       if (tiles > info.clusters[n] || kb < n) continue;
       // Of fp32 outputs the accumulators of a part have to fit, and parts are not much longer than the
       // others' segments.
-      if (split_segments(f, n) > (width <= kApartQMax ? (int)kSplitTmemCols / kApartQMax : 2)) continue;
+      if (split_segments(f, n) > (width <= kApartQMax && !p.newton ? (int)kSplitTmemCols / kApartQMax : 2)) continue;
       if (f.segment == kSegmentBlocks && f.d.segments > 1 && ceil_div(f.d.kblocks, n) > (n == 2 ? 24 : 32)) continue;
       Plan s;
       s.form = kSplit;
@@ -1456,7 +1565,7 @@ cudaError_t launch_jobs(Jobs &jobs, const Plan &plan, int64_t buffers, int varia
                           jobs.stage_bytes);
   if (jobs.stages > kMaxStages) jobs.stages = kMaxStages;
   if (jobs.stages < kProducers) return cudaErrorInvalidConfiguration;
-  if (plan.form == kSplit) variant = jobs.job[0].d.segments > 2 ? kSegments : kPlain;
+  if (plan.form == kSplit && variant != kNewton) variant = jobs.job[0].d.segments > 2 ? kSegments : kPlain;
   const Kernel kernel = kernel_of(plan.form, variant);
   if (plan.form == kPair)
     return launch(kernel, 2 * (tiles < info.pairs ? tiles : info.pairs), kPairThreads, kSmemBytes, stream, 2, jobs);
@@ -1484,7 +1593,11 @@ cudaError_t launch_product(const ProductParams &p, cudaStream_t stream) {
   int64_t buffers;
   const int64_t reserve = reserve_of(p, stage_bytes_of(p, plan));
   if ((e = job_of(p, f, plan, reserve, f.d.segments > 1, jobs.job[0], buffers)) != cudaSuccess) return e;
-  return launch_jobs(jobs, plan, buffers, p.symmetric ? kSymmetric : f.d.segments > 1 ? kSegments : kPlain, info, stream);
+  const bool segments = f.d.segments > 1 && plan.form != kSplit;
+  const int variant = p.symmetric ? kSymmetric
+                      : p.newton  ? segments ? kNewtonSegments : kNewton
+                                  : segments ? kSegments : kPlain;
+  return launch_jobs(jobs, plan, buffers, variant, info, stream);
 }
 
 cudaError_t launch_products(const ProductParams &p0, const ProductParams &p1, cudaStream_t stream) {

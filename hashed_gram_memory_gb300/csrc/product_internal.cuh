@@ -39,6 +39,16 @@ struct ProductParams {
   // side of the diagonal are computed, and written on both; out and residual are fp16, their
   // rows on 16-byte boundaries
   bool symmetric;
+  // The iteration's products (fp16 operands and residual): the diagonals of the square matrices stay
+  // fp32, [count][diag_batch] each, diag_batch a multiple of 64.  With D = diag_in residual (m, n) counts
+  // residual_scale + diag_by (D[m] + D[n]) times, of which D has the rows' or the columns' or both;
+  // diag_out (NULL: none) receives what out has at (m, m), times diag_scale, and (residual_scale + diag_by
+  // D[m]) D[m], and there out becomes zero.
+  bool newton, diag_rows, diag_columns;
+  const float *diag_in;
+  float *diag_out;
+  int64_t diag_batch;
+  float diag_by, diag_scale;
   int32_t *status;
 };
 cudaError_t launch_product(const ProductParams &p, cudaStream_t stream);
