@@ -6,15 +6,20 @@
 // Three products a step on the tensor cores (product.cu), two of them symmetric: half of their
 // tiles are computed.  The iterate and the two square matrices are held in fp16, times 2^8: all
 // their values are bounded (singular values stay under 1.3 with the usual coefficients), so the
-// 11 bits of fp16 serve where bf16's 8 cost precision -- against 64 bits the result is 1e-3 to
-// 4e-3 off, with bf16 1e-2 to 3e-2 -- at the same rate of the tensor cores.  Times 2^8, values
-// down to 2^-22 keep all their bits and singular values up to 255 have room.  The sums of the
-// products, the norm and the momentum are fp32.  Square matrices whose least singular values nearly
+// 11 bits of fp16 serve where bf16's 8 cost precision -- against 64 bits the result is 5e-4 to
+// 1e-3 off before its own rounding, with bf16 1e-2 to 3e-2 -- at the same rate of the tensor
+// cores.  The square matrices' diagonals, d of A and e of B, stay fp32, and their places in A and B
+// are zero:
+//   B = (b + c (d_i + d_j)) A + c A^2,   e = b d + c (d^2 + A^2's diagonal),   X = (a + e) X + B X
+// (e by X's rows, or its columns where A is X^T X).  Beside many columns A and B are nearly diagonal,
+// and a + e is four times as small as e: with e rounded 40 x 3000 is 2.9e-3 off, not 5e-4.  Times
+// 2^8, values down to 2^-22 keep all their bits and singular values up to 255 have room.  The sums of
+// the products, the norm and the momentum are fp32.  Square matrices whose least singular values nearly
 // vanish lose more: their parts of X lie under the roundings of the others, and the iteration brings
 // both up; it shows where few singular values make the norm (sides under 16, see the header).  Bound by
 // the tensor cores for large matrices (4096 x 6144 of fp32 in 1290 to 1440 us, 1.3 to 1.5 PFLOP/s of the
 // products that symmetry leaves, as the power limit lets it), by the launches for small ones (256 x 1536
-// in 85 us, 17 launches); 12 of 1024 x 1536 take 447 us, of which the momentum and the norm are 57 (5.2
+// in 85 us, 17 launches); 12 of 1024 x 1536 take 450 us, of which the momentum and the norm are 57 (5.2
 // TB/s).  A shorter side of at most 128 goes to orthogonalise_small.cu.
 #include "launch.cuh"
 #include "values.cuh"

@@ -11,17 +11,14 @@
 //   X_c  = a X_c + B X_c: every CTA its columns, in place.
 // All threads but the one that issues the instructions serve the epilogues, lanes being rows.
 //
-// X, A and B are held in fp16 as in orthogonalise.cu, but for the diagonals d of A and e of B, which stay
-// fp32: with A' and B' the others,
-//   B' = (b + c (d_i + d_j)) A' + c A'^2,   e = b d + c (d^2 + A'^2's diagonal),   X = (a + e_i) X + B' X.
-// Where few rows share the norm the square matrices are nearly diagonal, and a + e_i a difference four
-// times as small as e: rounding e to fp16 as the rest was most of the error (16 x 700 2.4e-3 off, its own
-// rounding to bf16 included, now 1.9e-3).  Bound by the latency of a step, 2.5 us in a CTA
-// by itself and 6 where two join A; fp32 with momentum, in us, beside the chain of launches:
-//   1 of  64 x   64   18 and 63        32 of  64 x  256    29 and  76
-//   1 of 128 x  128   25 and 60        16 of 128 x 1024    57 and  92
-//   1 of 128 x  512   51 and 68      1000 of 128 x  128   189 and 303
-//   1 of 100 x 3500   80 and 80       300 of 128 x  896   329 and 428
+// What is rounded, and where, and the diagonals that stay fp32 are as in orthogonalise.cu (16 x 700: 1.9e-3
+// off with its own rounding to bf16, 2.4e-3 with the diagonals rounded, which takes 128 x 128 1.2 us
+// less).  Bound by the latency of a step, 2.5 us in a CTA by itself and 6 where two join A; fp32 with
+// momentum, in us, beside the chain of launches:
+//   1 of  64 x   64   19 and 63        32 of  64 x  256    29 and  76
+//   1 of 128 x  128   25 and 60        16 of 128 x 1024    56 and  92
+//   1 of 128 x  512   51 and 68      1000 of 128 x  128   188 and 303
+//   1 of 100 x 3500   80 and 80       300 of 128 x  896   328 and 428
 #include <stddef.h>
 
 #include <mutex>
@@ -502,7 +499,7 @@ int cluster_of(int64_t w) {
 
 // Clusters of 4 and 8 spend more on joining A than on products.  They win while every matrix has its
 // CTAs at once; where there are more the chain, whose products share no A, is ahead: 300 of
-// 100 x 1800 1171 us here and 762 there, 500 of 16 x 2000 1667 and 696.
+// 100 x 1800 1259 us here and 755 there, 500 of 16 x 2000 1813 and 807.
 bool orthogonalise_small_supported(const OrthogonaliseParams &p) {
   const int64_t r = p.M < p.N ? p.M : p.N, w = p.M < p.N ? p.N : p.M;
   if (r > kR || w > 8 * kMostBlocks * 64) return false;

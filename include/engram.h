@@ -785,11 +785,12 @@ ENGRAM_API engram_status engram_matmul_grad(const engram_matmul_grad_args *args,
  *   momentum  fp32 [count, M, N], updated in place, or NULL
  *   out       bf16 bits [count, M, N]
  *   workspace device, 16-byte aligned, engram_orthogonalise_workspace_bytes(...) bytes
- * fp32 momentum, norm and sums; the iterate and the square matrices are held in fp16 times
- * 2^8 between the products: with the usual coefficients 3.4445, -4.7750, 2.0315 and 5 steps
- * the result is about 4e-3 off at most (of its Frobenius norm; its own rounding to bf16 is
- * 1.7e-3) where both sides are 16 or more; shorter ones of random values are within 8e-3 in
- * 99 of 100, and 6e-2 was met for a square of 2 that nearly had no inverse.  Singular values over 255 on the way overflow.  The norm is that of finite u
+ * fp32 momentum, norm, sums and diagonals of the square matrices; the iterate and the rest
+ * of those are held in fp16 times 2^8 between the products: with the usual coefficients
+ * 3.4445, -4.7750, 2.0315 and 5 steps the result is about 2e-3 off (of its Frobenius norm;
+ * its own rounding to bf16 is 1.7e-3).  Small square matrices that nearly have no inverse
+ * lose more: of random ones with sides up to 16 99 in 100 are within 7e-3, and 7e-2 was met
+ * for one of 2 x 2.  Singular values over 255 on the way overflow.  The norm is that of finite u
  * of any size.  A matrix of zeros stays zero, with eps == 0 too; a NaN or an infinity in u
  * makes all of its matrix NaN.  steps in [1, 64], coefficients in [-16, 16].  A wait
  * that runs out sets ENGRAM_FLAG_TIMEOUT: then the outputs are not valid.  count == 0
