@@ -1586,7 +1586,8 @@ cudaError_t launch_product(const ProductParams &p, cudaStream_t stream) {
   if (p.symmetric) {  // half of the tiles, unless that many run side by side in any case, or K is long
     ProductParams whole = p;
     whole.symmetric = false;
-    if (f.d.kblocks > kHalfSegmentBlocks || plan_of(whole, facts_of(whole), info).us <= plan.us) return launch_product(whole, stream);
+    if (f.d.kblocks > kHalfSegmentBlocks || plan_of(whole, facts_of(whole), info).us <= plan.us)
+      return launch_product(whole, stream);
   }
   Jobs jobs{};
   jobs.count = 1;
